@@ -212,7 +212,7 @@ def prepare(case, seed):
         c["dweights"] = 0.01 * _randn(g, t, c["k"])
         c["dloss"] = torch.ones((), device=DEV)
     if c["dir"] == "bwd":
-        c["indices"], c["weights"], c["counts"], _, _, c["lse"] = _route(
+        c["indices"], c["weights"], c["counts"], _, _, c["kept"] = _route(
             c["logits"], c["k"], c["keep"], c["renormalise"])
     return c
 
@@ -220,7 +220,7 @@ def prepare(case, seed):
 # ------------------------------------------------------------ the plain form
 
 def _route(logits, k, keep, renormalise):
-    """Indices, weights, counts, offsets, loss and log of the softmax's sum."""
+    """Indices, weights, counts, offsets, loss and the number of tokens kept."""
     z = logits.float()
     t, experts = z.shape
     top = z.amax(-1, keepdim=True)
@@ -242,7 +242,7 @@ def _route(logits, k, keep, renormalise):
     mean_p = torch.where(keep[:, None], p, 0.0).sum(0) / n
     loss = COEF * experts / (k * n) * (counts.float() * mean_p).sum()
     return (idx.to(torch.int32), w, counts.to(torch.int32), offsets, loss,
-            (top + torch.log(s))[:, 0])
+            keep.sum(dtype=torch.int32))
 
 
 def _route_grad(logits, idx, w, counts, keep, dloss, dw, k, renormalise):
@@ -345,7 +345,7 @@ def _own(s):
     if s["op"] == "route":
         first = ()
         if s["dir"] == "bwd":
-            r = ns.Routing(s["indices"], s["weights"], s["counts"], lse=s["lse"], mask=s["keep"],
+            r = ns.Routing(s["indices"], s["weights"], s["counts"], s["kept"],
                            coef=COEF, renormalise=s["renormalise"])
         else:
             r = ns.route(s["logits"], s["k"], mask=s["keep"], coef=COEF, renormalise=s["renormalise"])
