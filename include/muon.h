@@ -1,5 +1,7 @@
 /*
- * libmuon — the Muon optimizer step on one NVIDIA GB300 GPU (sm_103a).
+ * libmuon — the Muon optimizer step on one NVIDIA GB300 GPU (sm_103a), and
+ * operators that bring a block's activations to the gradients it reads (last
+ * section).
  *
  * One call, muon_step(), updates every registered 2-D weight matrix:
  *
@@ -353,6 +355,195 @@ MUON_API int muon_step_noalloc(const muon_param* param, float lr, float beta,
                                int nesterov, int ns_steps, float a, float b,
                                float c, void* cuda_stream, char* err,
                                size_t err_len);
+
+/* ---- operators of a block's training step ------------------------------ */
+
+/* What a block of a model runs between its activations and the gradients
+ * that muon_step reads: layer norm, activation checkpoints in 8 bits, the
+ * weight gradient taken from a checkpoint, and the router of a
+ * mixture-of-experts block with its balance loss.  These entry points need
+ * no handle.  Conventions, beside those at the top of this file:
+ *   - The work is queued on cuda_stream (NULL = the legacy default stream)
+ *     of the caller's current device.  Every device pointer, the workspace's
+ *     included, must stay valid until that work is done.
+ *   - err, err_len: optional buffer that receives a message on error.
+ *   - Argument checks run before any CUDA call.
+ *   - A workspace is device memory, 256-byte aligned, of the size that the
+ *     operator's _workspace call gives for the same arguments (that call
+ *     makes no CUDA call and looks at no pointer but for being NULL).  Its
+ *     contents before and after the call mean nothing.
+ *   - Leading dimensions are in elements.  One of a tensor that is only read
+ *     may be 0 (one row for all); every other is at least the row's length
+ *     (rows <= 1: anything).  No alignment is asked for beyond the element's
+ *     own unless stated; rows that start on 16 bytes are faster.
+ *   - Sums are held in fp32 and in a fixed order: the same call gives the
+ *     same bits again. */
+
+/* An activation checkpoint: rows x cols values in 8 bits, in blocks of 32
+ * consecutive values of a row that share a power of two.  A value stands for
+ *     q[r * ld_q + c] * 2^(e[r * ld_e + c / 32] - 133),
+ * q in -127 .. 127; e = 127 + floor(log2(largest magnitude of the block)),
+ * 0 for a block whose magnitudes are all below 2^-126, 255 for a block that
+ * held an infinity or a NaN (all of its values read as NaN).  Values are
+ * rounded to nearest, ties to even, and limited to 127; each is exact in
+ * bf16.  Device pointers: q 16-byte aligned with ld_q a multiple of 32 and
+ * at least cols rounded up to 32 (the values past cols are written as zero),
+ * ld_e at least ceil(cols / 32).  q = NULL where a checkpoint is optional
+ * means none. */
+typedef struct {
+    int8_t*  q;
+    uint8_t* e;
+    int64_t  ld_q, ld_e;
+} muon_ckpt8;
+
+/* Writes the checkpoint of x (rows x cols, x_dtype), and the values of a
+ * checkpoint to x.  0 <= rows < 2^31, 1 <= cols <= 1048576. */
+MUON_API int muon_ckpt8_pack(const void* x, int x_dtype, int64_t rows, int64_t cols,
+                             int64_t ld_x, const muon_ckpt8* saved, void* cuda_stream,
+                             char* err, size_t err_len);
+MUON_API int muon_ckpt8_unpack(const muon_ckpt8* saved, int64_t rows, int64_t cols, void* x,
+                               int x_dtype, int64_t ld_x, void* cuda_stream, char* err,
+                               size_t err_len);
+
+/* Layer norm over the rows of x:
+ *     h = (x - mean) * rstd,  rstd = 1 / sqrt(mean((x - mean)^2) + eps),
+ *     y = h * weight + bias.
+ * x and y: rows x cols of x_dtype (y may be x); weight, bias: cols values of
+ * w_dtype, NULL for ones and zeros; mean, rstd: rows fp32 values, either may
+ * be NULL.  saved (optional): receives the checkpoint of h.
+ * 0 <= rows < 2^31, 1 <= cols <= 1048576, eps >= 0. */
+typedef struct {
+    const void* x;
+    const void* weight;
+    const void* bias;
+    void*       y;
+    float*      mean;
+    float*      rstd;
+    muon_ckpt8  saved;
+    int64_t     rows, cols;
+    int64_t     ld_x, ld_y;
+    int32_t     x_dtype, w_dtype;
+    float       eps;
+} muon_layer_norm_args;
+MUON_API int muon_layer_norm(const muon_layer_norm_args* args, void* cuda_stream, char* err,
+                             size_t err_len);
+
+/* Its gradient.  With g = dy * weight:
+ *     dx = rstd * (g - mean(g) - h * mean(g * h)),
+ *     dweight = sum over rows of dy * h,  dbias = sum over rows of dy.
+ * h comes from saved (the checkpoint the forward pass wrote; x and mean are
+ * then NULL), or from x and mean.  dy, x and dx: rows x cols of x_dtype (dx
+ * may be dy); weight: w_dtype or NULL; dweight, dbias: cols values of
+ * w_dtype, either may be NULL.  rows = 0 gives zero dweight and dbias. */
+typedef struct {
+    const void*  dy;
+    const void*  x;
+    const float* mean;
+    const float* rstd;
+    const void*  weight;
+    void*        dx;
+    void*        dweight;
+    void*        dbias;
+    muon_ckpt8   saved;
+    int64_t      rows, cols;
+    int64_t      ld_dy, ld_x, ld_dx;
+    int32_t      x_dtype, w_dtype;
+} muon_layer_norm_grad_args;
+MUON_API int muon_layer_norm_grad_workspace(const muon_layer_norm_grad_args* args,
+                                            size_t* bytes);
+MUON_API int muon_layer_norm_grad(const muon_layer_norm_grad_args* args, void* workspace,
+                                  size_t bytes, void* cuda_stream, char* err, size_t err_len);
+
+/* The gradient of a matrix W (n x k) of a product Y = X W^T, from the
+ * checkpoint of X (or of the h that a norm made X from):
+ *     G[i][j] = sum over t of dy[t][i] * (h[t][j] * weight[j] + bias[j])  (+ C[i][j])
+ * dy: rows x n, bf16; saved: rows x k; weight, bias: k fp32 values, NULL for
+ * ones and zeros; g: n x k of g_dtype; c (optional): n x k of g_dtype, may
+ * be g itself (gradient accumulation).  The products run on the tensor cores
+ * from exact bf16 operands with fp32 sums; weight and bias are applied to
+ * the sums.
+ * offsets (optional): experts + 1 int32 values in device memory, rising from
+ * 0 to at most rows: matrix e takes rows offsets[e] .. offsets[e + 1] of dy
+ * and saved (none: G = 0, or C), and g and c are `experts` matrices, stride_g
+ * and stride_c elements apart.  Values outside that rule are limited to it.
+ * offsets = NULL: experts = 1, all rows.  0 <= rows < 2^31, 1 <= n, k <=
+ * 1048576, 1 <= experts <= 65536. */
+typedef struct {
+    const void*    dy;
+    const float*   weight;
+    const float*   bias;
+    const void*    c;
+    void*          g;
+    const int32_t* offsets;
+    muon_ckpt8     saved;
+    int64_t        rows, n, k, experts;
+    int64_t        ld_dy, ld_c, ld_g, stride_c, stride_g;
+    int32_t        g_dtype;
+} muon_weight_grad_args;
+MUON_API int muon_weight_grad_workspace(const muon_weight_grad_args* args, size_t* bytes);
+MUON_API int muon_weight_grad(const muon_weight_grad_args* args, void* workspace, size_t bytes,
+                              void* cuda_stream, char* err, size_t err_len);
+
+/* The router of a mixture-of-experts block.  p = softmax(logits) over the
+ * experts of every token; the k experts with the largest logits are taken
+ * (equal ones: the lower index first; one at -infinity never):
+ *     weights = p of those taken, divided by their sum if renormalise,
+ *     counts[e] = tokens that took expert e, offsets = their running sum,
+ *     loss = coef * experts / (k * kept^2) * sum over e of counts[e] * sum over t of p[t][e],
+ * where kept is the number of tokens that take part: those with mask != 0
+ * (mask NULL: all) and a logit above -infinity.  The others get indices -1
+ * and weights 0 and count nowhere; so do a token's places past its last
+ * logit above -infinity.  No token left: loss 0.  A NaN counts as the largest
+ * logit and makes its token's weights, and the loss, NaN.
+ * logits: tokens x experts of z_dtype; mask: one byte a token; indices,
+ * weights: tokens x k, dense; counts: experts; offsets: experts + 1; loss,
+ * kept: one value.  0 <= tokens, tokens * k < 2^31, 1 <= experts <= 1024,
+ * 1 <= k <= min(experts, 32). */
+typedef struct {
+    const void*    logits;
+    const uint8_t* mask;
+    int32_t*       indices;
+    float*         weights;
+    int32_t*       counts;
+    int32_t*       offsets;
+    float*         loss;
+    int32_t*       kept;
+    int64_t        tokens, experts, k;
+    int64_t        ld_z;
+    int32_t        z_dtype, renormalise;
+    float          coef;
+} muon_route_args;
+MUON_API int muon_route_workspace(const muon_route_args* args, size_t* bytes);
+MUON_API int muon_route(const muon_route_args* args, void* workspace, size_t bytes,
+                        void* cuda_stream, char* err, size_t err_len);
+
+/* Its gradient with respect to the logits, from the indices, weights, counts
+ * and kept that muon_route wrote (counts are constants of the loss), dloss
+ * (one fp32 value, NULL for 0) and dweights (tokens x k fp32, NULL for 0).
+ * dlogits: tokens x experts of z_dtype (may be logits); zero where a token
+ * takes no part. */
+typedef struct {
+    const void*    logits;
+    const int32_t* indices;
+    const float*   weights;
+    const int32_t* counts;
+    const int32_t* kept;
+    const float*   dloss;
+    const float*   dweights;
+    void*          dlogits;
+    int64_t        tokens, experts, k;
+    int64_t        ld_z, ld_dw, ld_dz;
+    int32_t        z_dtype, renormalise;
+    float          coef;
+} muon_route_grad_args;
+MUON_API int muon_route_grad(const muon_route_grad_args* args, void* cuda_stream, char* err,
+                             size_t err_len);
+
+/* Waits for the stream and reports what the operators above met on the GPU
+ * of the caller's current device: MUON_ERR_TIMEOUT if a bounded wait of
+ * muon_weight_grad ran out since the last call (its output is then not
+ * whole), MUON_ERR_CUDA for a CUDA error, else MUON_OK. */
+MUON_API int muon_ops_sync(void* cuda_stream, char* err, size_t err_len);
 
 #ifdef __cplusplus
 }

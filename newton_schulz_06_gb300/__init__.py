@@ -11,3 +11,6 @@ from ._lib import (MUON_BF16, MUON_BLOCKWISE, MUON_DISTRIBUTED,  # noqa
 from .flops import gemm_equiv_flops, useful_flops  # noqa: F401
 from .muon import DEFAULT_COEFFS, HostPlanner, Muon, mode_code  # noqa: F401
 from .layerwise import LayerwiseMuon, lpt_partition  # noqa: F401
+from .ops import (Checkpoint8, Routing, checkpoint8, layer_norm,  # noqa: F401
+                  layer_norm_backward, layer_norm_checkpoint, ops_sync, route,
+                  route_backward, weight_grad)

@@ -38,7 +38,12 @@ EXPORTS = ("muon_create", "muon_set_stream", "muon_register_params",
            "muon_step_noalloc", "muon_debug_wait_timeout", "muon_step_host",
            "muon_debug_check_chain_schedule", "muon_debug_set_chain_test",
            "muon_dist_configure", "muon_dist_momentum", "muon_dist_gram",
-           "muon_dist_update")
+           "muon_dist_update",
+           "muon_ckpt8_pack", "muon_ckpt8_unpack", "muon_layer_norm",
+           "muon_layer_norm_grad_workspace", "muon_layer_norm_grad",
+           "muon_weight_grad_workspace", "muon_weight_grad",
+           "muon_route_workspace", "muon_route", "muon_route_grad",
+           "muon_ops_sync")
 
 
 class MuonParam(ctypes.Structure):
@@ -56,6 +61,32 @@ class MuonPlanInfo(ctypes.Structure):
                 ("useful_flops", ctypes.c_int64),
                 ("executed_flops", ctypes.c_int64),
                 ("chained_groups", ctypes.c_int64)]
+
+
+def _struct(name, *groups):
+    """A ctypes structure from (C type, "field names") groups in order."""
+    return type(name, (ctypes.Structure,),
+                {"_fields_": [(f, t) for t, names in groups for f in names.split()]})
+
+
+_vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+Ckpt8 = _struct("Ckpt8", (_vp, "q e"), (_i64, "ld_q ld_e"))
+LayerNormArgs = _struct("LayerNormArgs", (_vp, "x weight bias y mean rstd"), (Ckpt8, "saved"),
+                        (_i64, "rows cols ld_x ld_y"), (_i32, "x_dtype w_dtype"), (_f32, "eps"))
+LayerNormGradArgs = _struct("LayerNormGradArgs",
+                            (_vp, "dy x mean rstd weight dx dweight dbias"), (Ckpt8, "saved"),
+                            (_i64, "rows cols ld_dy ld_x ld_dx"), (_i32, "x_dtype w_dtype"))
+WeightGradArgs = _struct("WeightGradArgs", (_vp, "dy weight bias c g offsets"), (Ckpt8, "saved"),
+                         (_i64, "rows n k experts ld_dy ld_c ld_g stride_c stride_g"),
+                         (_i32, "g_dtype"))
+RouteArgs = _struct("RouteArgs",
+                    (_vp, "logits mask indices weights counts offsets loss kept"),
+                    (_i64, "tokens experts k ld_z"), (_i32, "z_dtype renormalise"),
+                    (_f32, "coef"))
+RouteGradArgs = _struct("RouteGradArgs",
+                        (_vp, "logits indices weights counts kept dloss dweights dlogits"),
+                        (_i64, "tokens experts k ld_z ld_dw ld_dz"),
+                        (_i32, "z_dtype renormalise"), (_f32, "coef"))
 
 
 class MuonError(RuntimeError):
@@ -113,6 +144,18 @@ def lib() -> ctypes.CDLL:
         "muon_dist_gram": [H, vp, ctypes.c_int64, i32, i32],
         "muon_dist_update": [H, vp, ctypes.c_int64, i32, i32, vp, f32, f32, f32,
                              f32],
+        # the operators' argument structures go by address (ctypes.byref)
+        "muon_ckpt8_pack": [vp, i32, _i64, _i64, _i64, vp, vp, vp, sz],
+        "muon_ckpt8_unpack": [vp, _i64, _i64, vp, i32, _i64, vp, vp, sz],
+        "muon_layer_norm": [vp, vp, vp, sz],
+        "muon_layer_norm_grad_workspace": [vp, ctypes.POINTER(sz)],
+        "muon_layer_norm_grad": [vp, vp, sz, vp, vp, sz],
+        "muon_weight_grad_workspace": [vp, ctypes.POINTER(sz)],
+        "muon_weight_grad": [vp, vp, sz, vp, vp, sz],
+        "muon_route_workspace": [vp, ctypes.POINTER(sz)],
+        "muon_route": [vp, vp, sz, vp, vp, sz],
+        "muon_route_grad": [vp, vp, vp, sz],
+        "muon_ops_sync": [vp, vp, sz],
     }
     for name, args in sig.items():
         fn = getattr(L, name)

@@ -22,8 +22,10 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmuon.so")
 SOURCES = ["ew_kernels.cu", "ns_kernels.cu", "ns2_kernels.cu", "muon_api.cpp",
-           "muon_noalloc.cu"]
+           "muon_noalloc.cu", "ops_api.cpp", "checkpoint8.cu", "layer_norm.cu",
+           "weight_grad.cu", "route.cu"]
 HEADERS = [os.path.join(CSRC, "muon_internal.h"), os.path.join(CSRC, "tc_ptx.cuh"),
+           os.path.join(CSRC, "ops_internal.h"),
            os.path.join(ROOT, "include", "muon.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
