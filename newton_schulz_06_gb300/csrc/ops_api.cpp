@@ -110,6 +110,8 @@ int check_weight_grad(const Err& err, const muon_weight_grad_args* a) {
     if (!dtype_ok(a->g_dtype)) return err.bad("unknown element type");
     if (a->experts < 1 || a->experts > 65536) return err.bad("experts out of range");
     if (!a->offsets && a->experts != 1) return err.bad("experts without offsets");
+    if (a->experts * ops::ceil_div(a->n, 256) * ops::ceil_div(a->k, 256) > (int64_t(1) << 30))
+        return err.fail(MUON_ERR_UNSUPPORTED, "more than 2^30 tiles of 256 x 256");
     return MUON_OK;
 }
 
@@ -289,7 +291,12 @@ MUON_API int muon_route_grad(const muon_route_grad_args* a, void* cuda_stream, c
 
 MUON_API int muon_ops_sync(void* cuda_stream, char* err_buf, size_t err_len) {
     const Err err{err_buf, err_len};
-    return err.done(cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream)));
+    int code = 0;
+    const cudaError_t e = ops::ops_status(static_cast<cudaStream_t>(cuda_stream), &code);
+    if (e != cudaSuccess) return err.done(e);
+    if (code)
+        return err.fail(MUON_ERR_TIMEOUT, "a bounded wait of muon_weight_grad ran out on the GPU");
+    return MUON_OK;
 }
 
 }  // extern "C"

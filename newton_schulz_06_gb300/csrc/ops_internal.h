@@ -26,6 +26,8 @@ cudaError_t launch_weight_grad(const muon_weight_grad_args& a, void* ws, cudaStr
 size_t route_workspace(const muon_route_args& a);
 cudaError_t launch_route(const muon_route_args& a, void* ws, cudaStream_t s);
 cudaError_t launch_route_grad(const muon_route_grad_args& a, cudaStream_t s);
+// Waits for the stream; *code: the device error word (DEV_ERR_*), cleared.
+cudaError_t ops_status(cudaStream_t s, int* code);
 
 #ifdef __CUDACC__
 
