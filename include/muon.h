@@ -370,8 +370,8 @@ MUON_API int muon_step_noalloc(const muon_param* param, float lr, float beta,
  *   - Argument checks run before any CUDA call.
  *   - A workspace is device memory, 256-byte aligned, of the size that the
  *     operator's _workspace call gives for the same arguments (that call
- *     makes no CUDA call and looks at no pointer but for being NULL).  Its
- *     contents before and after the call mean nothing.
+ *     makes no CUDA call and looks behind no pointer).  Its contents before
+ *     and after the call mean nothing.
  *   - Leading dimensions are in elements.  One of a tensor that is only read
  *     may be 0 (one row for all); every other is at least the row's length
  *     (rows <= 1: anything).  No alignment is asked for beyond the element's
@@ -541,7 +541,7 @@ MUON_API int muon_route_grad(const muon_route_grad_args* args, void* cuda_stream
 
 /* Waits for the stream and reports what the operators above met on the GPU
  * of the caller's current device: MUON_ERR_TIMEOUT if a bounded wait of
- * muon_weight_grad ran out since the last call (its output is then not
+ * one of their kernels ran out since the last call (its output is then not
  * whole), MUON_ERR_CUDA for a CUDA error, else MUON_OK. */
 MUON_API int muon_ops_sync(void* cuda_stream, char* err, size_t err_len);
 

@@ -12,42 +12,66 @@ namespace {
 
 constexpr int THREADS = 256;
 
-// One thread per block of 32.
+// Vector i of rows of `per` vectors: its row and first column.
+__device__ __forceinline__ void place(int64_t i, int64_t total, uint32_t per, int ve, int64_t* r, int* c) {
+    *r = total <= 0xffffffffll ? static_cast<uint32_t>(i) / per : i / per;
+    *c = static_cast<int>(i - *r * per) * ve;
+}
+
+// One thread per vector, UNROLL of them in flight.
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
     pack_kernel(const T* x, int64_t rows, int64_t cols, int64_t ld_x, muon_ckpt8 out) {
-    const int64_t nb = (cols + CKPT_BLOCK - 1) / CKPT_BLOCK;
-    const int64_t total = rows * nb;
-    for (int64_t i = blockIdx.x * int64_t(THREADS) + threadIdx.x; i < total;
-         i += int64_t(gridDim.x) * THREADS) {
-        const int64_t r = i / nb, b = i % nb;
-        const int64_t c0 = b * CKPT_BLOCK;
-        const T* src = x + r * ld_x + c0;
-        float v[CKPT_BLOCK];
-        uint32_t top = 0;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    constexpr int VE = Vec<T>::VE, UNROLL = 4;
+    const uint32_t per = static_cast<uint32_t>((cols + CKPT_BLOCK - 1) / CKPT_BLOCK * (CKPT_BLOCK / VE));
+    const int64_t total = rows * per;
+    const int64_t stride = int64_t(gridDim.x) * THREADS;
+    // whole warps walk on together: encode_vec asks every lane
+    const int64_t rounded = (total + 31) / 32 * 32;
+    for (int64_t i0 = blockIdx.x * int64_t(THREADS) + threadIdx.x; i0 < rounded; i0 += UNROLL * stride) {
+        Vec<T> v[UNROLL];
+        int64_t r[UNROLL];
+        int c[UNROLL];
 #pragma unroll
-        for (int j = 0; j < CKPT_BLOCK; ++j) {
-            v[j] = c0 + j < cols ? to_f32(src[j]) : 0.f;
-            top = max(top, mag_bits(v[j]));
+        for (int u = 0; u < UNROLL; ++u) {
+            const int64_t i = i0 + u * stride;
+            place(i, total, per, VE, &r[u], &c[u]);
+            v[u].load(x + r[u] * ld_x + c[u], i < total ? static_cast<int>(cols) - c[u] : 0);
         }
-        const uint32_t e = scale_byte(top);
-        const float inv = scale_inv(e);
-        int8_t* q = out.q + r * out.ld_q + c0;
 #pragma unroll
-        for (int j = 0; j < CKPT_BLOCK; ++j) q[j] = static_cast<int8_t>(encode_q(v[j], e, inv));
-        out.e[r * out.ld_e + b] = static_cast<uint8_t>(e);
+        for (int u = 0; u < UNROLL; ++u) {
+            const int64_t i = i0 + u * stride;
+            if (i >= rounded) break;
+            float f[VE];
+            v[u].get(f);
+            encode_vec<VE>(out, r[u], c[u], i < total, f);
+        }
     }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
     unpack_kernel(muon_ckpt8 in, int64_t rows, int64_t cols, T* x, int64_t ld_x) {
-    const int64_t total = rows * cols;
-    for (int64_t i = blockIdx.x * int64_t(THREADS) + threadIdx.x; i < total;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    constexpr int VE = Vec<T>::VE;
+    const uint32_t per = static_cast<uint32_t>((cols + VE - 1) / VE);
+    const int64_t total = rows * per;
+    const int64_t rounded = (total + 31) / 32 * 32;
+    for (int64_t i = blockIdx.x * int64_t(THREADS) + threadIdx.x; i < rounded;
          i += int64_t(gridDim.x) * THREADS) {
-        const int64_t r = i / cols, c = i % cols;
-        const float p = scale_pow(in.e[r * in.ld_e + c / CKPT_BLOCK]);
-        from_f32(x + r * ld_x + c, static_cast<float>(in.q[r * in.ld_q + c]) * 0.015625f * p);
+        int64_t r = 0;
+        int c = 0;
+        Vec<T> v;
+        if (i < total) {
+            place(i, total, per, VE, &r, &c);
+            float f[VE];
+            decode_vec<VE>(in.q + r * in.ld_q + c, scale_pow(in.e[r * in.ld_e + c / CKPT_BLOCK]), f);
+            v.set(f);
+        }
+        v.store(x + r * ld_x + c, i < total ? static_cast<int>(cols) - c : 0, c == 0);
     }
 }
 
@@ -56,28 +80,33 @@ int grid_for(int64_t items) {
     return static_cast<int>(g < 1 ? 1 : g > 152 * 32 ? 152 * 32 : g);
 }
 
+template <typename T>
+cudaError_t pack(const T* x, int64_t rows, int64_t cols, int64_t ld_x, const muon_ckpt8& saved,
+                 cudaStream_t s) {
+    const int64_t vectors = rows * ceil_div(cols, CKPT_BLOCK) * (CKPT_BLOCK / Vec<T>::VE);
+    return launch_kernel(pack_kernel<T>, dim3(grid_for(vectors)), dim3(THREADS), 0, s, x, rows, cols,
+                         ld_x, saved);
+}
+
+template <typename T>
+cudaError_t unpack(const muon_ckpt8& saved, int64_t rows, int64_t cols, T* x, int64_t ld_x,
+                   cudaStream_t s) {
+    return launch_kernel(unpack_kernel<T>, dim3(grid_for(rows * ceil_div(cols, Vec<T>::VE))),
+                         dim3(THREADS), 0, s, saved, rows, cols, x, ld_x);
+}
+
 }  // namespace
 
 cudaError_t launch_ckpt8_pack(const void* x, int x_dtype, int64_t rows, int64_t cols,
                               int64_t ld_x, const muon_ckpt8& saved, cudaStream_t s) {
-    const int g = grid_for(rows * ceil_div(cols, CKPT_BLOCK));
-    if (x_dtype == MUON_F32)
-        pack_kernel<<<g, THREADS, 0, s>>>(static_cast<const float*>(x), rows, cols, ld_x, saved);
-    else
-        pack_kernel<<<g, THREADS, 0, s>>>(static_cast<const __nv_bfloat16*>(x), rows, cols, ld_x,
-                                          saved);
-    return cudaGetLastError();
+    return x_dtype == MUON_F32 ? pack(static_cast<const float*>(x), rows, cols, ld_x, saved, s)
+                               : pack(static_cast<const __nv_bfloat16*>(x), rows, cols, ld_x, saved, s);
 }
 
 cudaError_t launch_ckpt8_unpack(const muon_ckpt8& saved, int64_t rows, int64_t cols, void* x,
                                 int x_dtype, int64_t ld_x, cudaStream_t s) {
-    const int g = grid_for(rows * cols);
-    if (x_dtype == MUON_F32)
-        unpack_kernel<<<g, THREADS, 0, s>>>(saved, rows, cols, static_cast<float*>(x), ld_x);
-    else
-        unpack_kernel<<<g, THREADS, 0, s>>>(saved, rows, cols, static_cast<__nv_bfloat16*>(x),
-                                            ld_x);
-    return cudaGetLastError();
+    return x_dtype == MUON_F32 ? unpack(saved, rows, cols, static_cast<float*>(x), ld_x, s)
+                               : unpack(saved, rows, cols, static_cast<__nv_bfloat16*>(x), ld_x, s);
 }
 
 }  // namespace ops

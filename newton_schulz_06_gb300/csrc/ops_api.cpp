@@ -295,7 +295,7 @@ MUON_API int muon_ops_sync(void* cuda_stream, char* err_buf, size_t err_len) {
     const cudaError_t e = ops::ops_status(static_cast<cudaStream_t>(cuda_stream), &code);
     if (e != cudaSuccess) return err.done(e);
     if (code)
-        return err.fail(MUON_ERR_TIMEOUT, "a bounded wait of muon_weight_grad ran out on the GPU");
+        return err.fail(MUON_ERR_TIMEOUT, "a bounded wait of an operator ran out on the GPU");
     return MUON_OK;
 }
 

@@ -28,6 +28,15 @@ cudaError_t launch_route(const muon_route_args& a, void* ws, cudaStream_t s);
 cudaError_t launch_route_grad(const muon_route_grad_args& a, cudaStream_t s);
 // Waits for the stream; *code: the device error word (DEV_ERR_*), cleared.
 cudaError_t ops_status(cudaStream_t s, int* code);
+// Device address of the layer norm's error word.
+cudaError_t norm_error_word(void** word);
+// Limit of the kernels' waits (MUON_WAIT_LIMIT_MS, else two seconds).
+unsigned long long wait_limit_ns();
+
+// Whether every row of a tensor starts on 16 bytes.
+inline bool rows_on_16(const void* p, size_t size, int64_t rows, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld * size % 16 == 0);
+}
 
 #ifdef __CUDACC__
 
@@ -50,6 +59,203 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// Copies `bytes` (a multiple of 16, both addresses on 16) of global memory to
+// this CTA's shared memory; completion is counted on the barrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(__cvta_generic_to_global(src))), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+// ---- 16-byte vectors of VE elements at any alignment ----
+//
+// A row may start anywhere: a vector that does not lie on 16 bytes is put
+// together from the two aligned 16-byte pieces that hold it, so that odd
+// widths and odd addresses cost two loads instead of VE, and are added up in
+// the same order as aligned ones.  Every piece that is read holds at least
+// one byte of the row.
+
+// The 16 bytes that start m bytes into lo:hi (0 <= m < 16, a multiple of 2).
+__device__ __forceinline__ uint4 shift_bytes(uint4 lo, uint4 hi, uint32_t m) {
+    uint32_t w[6] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y};
+    if (m & 8) {
+        w[0] = w[2];
+        w[1] = w[3];
+        w[2] = w[4];
+        w[3] = w[5];
+        w[4] = hi.z;
+        w[5] = hi.w;
+    }
+    if (m & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t b = (m & 2) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], b), __funnelshift_r(w[1], w[2], b),
+                      __funnelshift_r(w[2], w[3], b), __funnelshift_r(w[3], w[4], b));
+}
+
+template <typename T>
+struct Vec {
+    static constexpr int VE = 16 / sizeof(T);
+    uint4 raw;
+    // The vector at p, of which the row holds `valid` elements (0 or less:
+    // none; those past it are 0).  Shared or global memory.
+    __device__ __forceinline__ void load(const T* p, int valid) {
+        raw = make_uint4(0u, 0u, 0u, 0u);
+        if (valid <= 0) return;
+        const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+        const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - m);
+        raw = q[0];
+        if (m) {
+            const uint4 hi = valid * int(sizeof(T)) > 16 - int(m) ? q[1] : make_uint4(0u, 0u, 0u, 0u);
+            raw = shift_bytes(raw, hi, m);
+        }
+        if (valid < VE) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&raw);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (sizeof(T) == 4) {
+                    if (i >= valid) w[i] = 0u;
+                } else {
+                    if (2 * i >= valid) w[i] = 0u;
+                    else if (2 * i + 1 >= valid) w[i] &= 0xffffu;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[VE]) const {
+        if constexpr (sizeof(T) == 4) {
+            f[0] = __uint_as_float(raw.x);
+            f[1] = __uint_as_float(raw.y);
+            f[2] = __uint_as_float(raw.z);
+            f[3] = __uint_as_float(raw.w);
+        } else {
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[VE]) {
+        if constexpr (sizeof(T) == 4) {
+            raw = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                             __float_as_uint(f[3]));
+        } else {
+            __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        }
+    }
+    // Element i of 16 bytes.
+    static __device__ __forceinline__ void put(T* p, const uint4& r, int i) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        if constexpr (sizeof(T) == 4)
+            *p = __uint_as_float(w[i & 3]);
+        else
+            *reinterpret_cast<unsigned short*>(p) =
+                static_cast<unsigned short>(w[(i >> 1) & 3] >> (16 * (i & 1)));
+    }
+    // Stores the vector at p (`valid` elements, as above).  All lanes of the
+    // warp call it, a lane's p one vector past the lane's before it unless it
+    // starts a row (row_start).  Off 16 bytes a lane stores the aligned piece
+    // that its vector begins in, whose first m bytes come from the lane
+    // before, and only the pieces at the ends of the warp or the row go out
+    // by elements.
+    __device__ __forceinline__ void store(T* p, int valid, bool row_start) const {
+        const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+        if (__all_sync(0xffffffffu, valid <= 0 || (m == 0 && valid >= VE))) {
+            if (valid > 0) *reinterpret_cast<uint4*>(p) = raw;
+            return;
+        }
+        const int lane = threadIdx.x & 31;
+        uint4 before;
+        before.x = __shfl_up_sync(0xffffffffu, raw.x, 1);
+        before.y = __shfl_up_sync(0xffffffffu, raw.y, 1);
+        before.z = __shfl_up_sync(0xffffffffu, raw.z, 1);
+        before.w = __shfl_up_sync(0xffffffffu, raw.w, 1);
+        if (valid <= 0) return;
+        const int head = (16 - static_cast<int>(m)) / int(sizeof(T));   // elements in the first piece
+        const bool alone = lane == 0 || row_start;
+        if (m == 0) {
+            if (valid >= VE) {
+                *reinterpret_cast<uint4*>(p) = raw;
+            } else {
+#pragma unroll
+                for (int i = 0; i < VE; ++i)
+                    if (i < valid) put(p + i, raw, i);
+            }
+            return;
+        }
+        if (!alone && valid >= head) {
+            *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p) - m) =
+                shift_bytes(before, raw, 16 - m);
+        } else {
+            if (!alone) {
+                // the lane before leaves its last elements to this piece
+#pragma unroll
+                for (int i = 0; i < VE; ++i)
+                    if (i >= head) put(p + i - VE, before, i);
+            }
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                if (i < head && i < valid) put(p + i, raw, i);
+        }
+        if (lane == 31 || valid <= VE) {
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                if (i >= head && i < valid) put(p + i, raw, i);
+        }
+    }
+};
+
+// VE elements from column c of a vector of either type (fill where p is
+// null), of which `valid` are there; vec: p lies on 16 bytes.
+template <int VE>
+__device__ __forceinline__ void load_row_vec(const void* p, int dtype, bool vec, int c, int valid,
+                                             float fill, float (&f)[VE]) {
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) f[i] = fill;
+    } else if (vec && valid >= VE) {
+        if (dtype == MUON_F32) {
+            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
+#pragma unroll
+            for (int i = 0; i < VE / 4; ++i) {
+                const float4 a = q[i];
+                f[4 * i] = a.x;
+                f[4 * i + 1] = a.y;
+                f[4 * i + 2] = a.z;
+                f[4 * i + 3] = a.w;
+            }
+        } else {
+            const uint2* q = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + c);
+            uint2 a[VE / 4];
+            if constexpr (VE == 8) {
+                const uint4 t = *reinterpret_cast<const uint4*>(q);
+                a[0] = make_uint2(t.x, t.y);
+                a[VE / 4 - 1] = make_uint2(t.z, t.w);
+            } else {
+                a[0] = q[0];
+            }
+#pragma unroll
+            for (int i = 0; i < VE / 4; ++i) {
+                f[4 * i] = __uint_as_float(a[i].x << 16);
+                f[4 * i + 1] = __uint_as_float(a[i].x & 0xffff0000u);
+                f[4 * i + 2] = __uint_as_float(a[i].y << 16);
+                f[4 * i + 3] = __uint_as_float(a[i].y & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) f[i] = i < valid ? load_any(p, dtype, c + i) : 0.f;
+    }
 }
 
 // ---- the 8-bit checkpoint's code (muon_ckpt8) ----
@@ -75,6 +281,64 @@ __device__ __forceinline__ int encode_q(float v, uint32_t e, float inv) {
     if (e == 255u) return 0;
     const int q = __float2int_rn(v * inv * 64.f);
     return max(-127, min(127, q));
+}
+
+// VE values from q, whose block's power of two is p (exact).
+template <int VE>
+__device__ __forceinline__ void decode_vec(const int8_t* q, float p, float (&f)[VE]) {
+    const float s = p * 0.015625f;
+    if constexpr (VE == 1) {
+        f[0] = static_cast<float>(*q) * s;
+    } else {
+        uint32_t w[VE / 4];
+        if constexpr (VE == 8) {
+            const uint2 t = *reinterpret_cast<const uint2*>(q);
+            w[0] = t.x;
+            w[VE / 4 - 1] = t.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(q);
+        }
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            // a byte b = q + 128 in the last byte of 2^23 is the float 2^23 + b
+            f[i] = (__uint_as_float(__byte_perm(w[i / 4] ^ 0x80808080u, 0x4B000000u, 0x7540u + i % 4)) -
+                    8388736.f) * s;
+    }
+}
+
+// Encodes VE consecutive values of a row whose block of 32 lies in 32 / VE
+// neighbouring lanes (values past the row's end given as 0), and writes q at
+// column c and the block's scale byte; every lane of the warp calls this, and
+// those with !write only take part in the maximum.
+template <int VE>
+__device__ __forceinline__ void encode_vec(const muon_ckpt8& s, int64_t r, int c, bool write,
+                                           const float (&f)[VE]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) top = max(top, mag_bits(f[i]));
+    if constexpr (VE == 1) {
+        top = __reduce_max_sync(0xffffffffu, top);
+    } else {
+#pragma unroll
+        for (int o = 1; o < CKPT_BLOCK / VE; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    if (!write) return;
+    const uint32_t e = scale_byte(top);
+    const float inv = scale_inv(e);
+    int8_t* q = s.q + r * s.ld_q + c;
+    if constexpr (VE == 1) {
+        *q = static_cast<int8_t>(encode_q(f[0], e, inv));
+    } else {
+        uint32_t w[VE / 4];
+#pragma unroll
+        for (int i = 0; i < VE / 4; ++i)
+            w[i] = (encode_q(f[4 * i], e, inv) & 0xff) | (encode_q(f[4 * i + 1], e, inv) & 0xff) << 8 |
+                   (encode_q(f[4 * i + 2], e, inv) & 0xff) << 16 |
+                   static_cast<uint32_t>(encode_q(f[4 * i + 3], e, inv)) << 24;
+        if constexpr (VE == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[VE / 4 - 1]);
+        else *reinterpret_cast<uint32_t*>(q) = w[0];
+    }
+    if ((c & (CKPT_BLOCK - 1)) == 0) s.e[r * s.ld_e + c / CKPT_BLOCK] = static_cast<uint8_t>(e);
 }
 
 #endif  // __CUDACC__

@@ -799,6 +799,8 @@ bool rows_aligned(const void* p, size_t size, const muon_weight_grad_args& a, in
            (a.experts <= 1 || stride * size % 16 == 0);
 }
 
+}  // namespace
+
 unsigned long long wait_limit_ns() {
     static const unsigned long long v = [] {
         const char* s = std::getenv("MUON_WAIT_LIMIT_MS");
@@ -807,8 +809,6 @@ unsigned long long wait_limit_ns() {
     }();
     return v;
 }
-
-}  // namespace
 
 size_t weight_grad_workspace(const muon_weight_grad_args& a) { return layout(a).bytes; }
 
@@ -887,13 +887,18 @@ cudaError_t launch_weight_grad(const muon_weight_grad_args& a, void* ws, cudaStr
 
 cudaError_t ops_status(cudaStream_t s, int* code) {
     *code = 0;
-    void* word = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&word, g_ops_err);
-    if (e == cudaSuccess) e = cudaMemcpyAsync(code, word, sizeof(int), cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess && *code) {
-        e = cudaMemsetAsync(word, 0, sizeof(int), s);
+    void* words[2];
+    cudaError_t e = cudaGetSymbolAddress(&words[0], g_ops_err);
+    if (e == cudaSuccess) e = norm_error_word(&words[1]);
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+        int c = 0;
+        e = cudaMemcpyAsync(&c, words[i], sizeof(int), cudaMemcpyDeviceToHost, s);
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        if (e == cudaSuccess && c) {
+            *code = c;
+            e = cudaMemsetAsync(words[i], 0, sizeof(int), s);
+            if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        }
     }
     return e;
 }
