@@ -207,6 +207,8 @@ struct GradLaunch {
     int32_t parts;           // blocks (rows of partial sums)
     int32_t stages;          // rows of the ring in shared memory (norm_grad_ring_kernel)
     uint32_t x_off, stage_bytes;   // of a ring's row: where x (or q) is, and its size
+    uint32_t w_bytes;        // the weight's room in shared memory, before the ring
+    int64_t ld_part;         // cols rounded up to 4
     unsigned long long wait_limit_ns;
 };
 
@@ -226,15 +228,17 @@ template <int VE, int NV>
 __device__ __forceinline__ void store_parts(const GradLaunch& p, int c0, int step,
                                             const float (&dw)[NV * VE], const float (&db)[NV * VE]) {
     const int cols = static_cast<int>(p.a.cols);
-    float* w = p.part + int64_t(blockIdx.x) * 2 * cols;
+    float* w = p.part + int64_t(blockIdx.x) * 2 * p.ld_part;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = c0 + i * step;
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            if (c + j >= cols) break;
-            w[c + j] = dw[i * VE + j];
-            w[cols + c + j] = db[i * VE + j];
+        for (int j = 0; j < VE; j += 4) {
+            const int c = c0 + i * step + j;
+            if (c >= cols) break;
+            const int u = i * VE + j;
+            *reinterpret_cast<float4*>(w + c) = make_float4(dw[u], dw[u + 1], dw[u + 2], dw[u + 3]);
+            *reinterpret_cast<float4*>(w + p.ld_part + c) =
+                make_float4(db[u], db[u + 1], db[u + 2], db[u + 3]);
         }
     }
 }
@@ -246,8 +250,8 @@ struct GradVec {
     static constexpr int VE = Vec<T>::VE;
     float dy[VE], h[VE], g[VE];
     __device__ __forceinline__ void make(const GradLaunch& p, const Vec<T>& dyv, const Vec<T>& xv,
-                                         const int8_t* q, uint32_t e, float mean, float rstd, int c,
-                                         int valid) {
+                                         const int8_t* q, uint32_t e, float mean, float rstd,
+                                         const void* weight, bool w_vec, int c, int valid) {
         dyv.get(dy);
         if constexpr (CKPT) {
             decode_vec<VE>(q, scale_pow(e), h);
@@ -256,7 +260,7 @@ struct GradVec {
 #pragma unroll
             for (int j = 0; j < VE; ++j) h[j] = (h[j] - mean) * rstd;
         }
-        load_row_vec<VE>(p.a.weight, p.a.w_dtype, p.w_vec, c, valid, 1.f, g);
+        load_row_vec<VE>(weight, p.a.w_dtype, w_vec, c, valid, 1.f, g);
 #pragma unroll
         for (int j = 0; j < VE; ++j) g[j] *= dy[j];
     }
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const __grid_constant__ 
             const int c = c0 + i * step;
             if (c >= cols) break;
             GradVec<T, CKPT> v;
-            v.make(p, dyv[i], xv[i], q + c, e[i], mean, rstd, c, cols - c);
+            v.make(p, dyv[i], xv[i], q + c, e[i], mean, rstd, a.weight, p.w_vec, c, cols - c);
 #pragma unroll
             for (int j = 0; j < VE; ++j) {
                 dw[i * VE + j] = fmaf(v.dy[j], v.h[j], dw[i * VE + j]);
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const __grid_constant__ 
             const int c = c0 + i * step;
             if (c < cols) {
                 GradVec<T, CKPT> v;
-                v.make(p, dyv[i], xv[i], q + c, e[i], mean, rstd, c, cols - c);
+                v.make(p, dyv[i], xv[i], q + c, e[i], mean, rstd, a.weight, p.w_vec, c, cols - c);
 #pragma unroll
                 for (int j = 0; j < VE; ++j) v.g[j] = (v.g[j] - m0 - v.h[j] * m1) * rstd;
                 dyv[i].set(v.g);
@@ -345,8 +349,11 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const __grid_constant__ 
         }
         __syncthreads();
     }
-    float* out = p.part + int64_t(blockIdx.x) * 2 * cols;
-    for (int c = threadIdx.y * 32 + threadIdx.x; c < 2 * cols; c += 256) out[c] = sums[c];
+    float* out = p.part + int64_t(blockIdx.x) * 2 * p.ld_part;
+    for (int c = threadIdx.y * 32 + threadIdx.x; c < cols; c += 256) {
+        out[c] = sums[c];
+        out[p.ld_part + c] = sums[cols + c];
+    }
 }
 
 // Longer rows, one at a time in a block: dy and x (or q) come through a ring
@@ -361,7 +368,8 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
     norm_grad_ring_kernel(const __grid_constant__ GradLaunch p) {
     constexpr int VE = Vec<T>::VE;
     constexpr bool KEEP = NV == 1;
-    extern __shared__ __align__(128) uint8_t ring[];
+    extern __shared__ __align__(128) uint8_t shared[];
+    uint8_t* const ring = shared + p.w_bytes;
     __shared__ float2 red[2][32];
     __shared__ uint64_t full[8];
     __shared__ int abort_flag;
@@ -378,6 +386,16 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    // the weight, which every row needs twice (the ring leaves L1 no room)
+    const void* w_row = a.weight ? shared : nullptr;
+    if (a.weight)
+        for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+            if (a.w_dtype == MUON_F32)
+                reinterpret_cast<float*>(shared)[c] = static_cast<const float*>(a.weight)[c];
+            else
+                reinterpret_cast<__nv_bfloat16*>(shared)[c] =
+                    static_cast<const __nv_bfloat16*>(a.weight)[c];
+        }
     __syncthreads();
     const T* dy0 = static_cast<const T*>(a.dy);
     const T* x0 = static_cast<const T*>(a.x);
@@ -433,7 +451,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
             Vec<T> dyv, xv;
             dyv.load(dy_row + c, cols - c);
             if constexpr (!CKPT) xv.load(x_row + c, cols - c);
-            v.make(p, dyv, xv, q_row + c, e[i], mean, rstd, c, cols - c);
+            v.make(p, dyv, xv, q_row + c, e[i], mean, rstd, w_row, true, c, VE);
         };
         GradVec<T, CKPT> kept;
         float s0 = 0.f, s1 = 0.f;
@@ -502,8 +520,8 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const __grid_constant__ G
     float w = 0.f, b = 0.f;
     if (c < cols)
         for (int i = threadIdx.y; i < p.parts; i += 32) {
-            w += p.part[int64_t(2 * i) * cols + c];
-            b += p.part[int64_t(2 * i + 1) * cols + c];
+            w += p.part[2 * i * p.ld_part + c];
+            b += p.part[(2 * i + 1) * p.ld_part + c];
         }
     red[0][threadIdx.y][threadIdx.x] = w;
     red[1][threadIdx.y][threadIdx.x] = b;
@@ -568,16 +586,16 @@ __global__ void __launch_bounds__(256) norm_long_dw_kernel(const __grid_constant
         b += dy;
         w = fmaf(dy, long_h<T>(a, r, c, a.saved.q ? 0.f : a.mean[r], a.rstd[r]), w);
     }
-    float* out = p.part + int64_t(blockIdx.y) * 2 * cols;
+    float* out = p.part + int64_t(blockIdx.y) * 2 * p.ld_part;
     out[c] = w;
-    out[cols + c] = b;
+    out[p.ld_part + c] = b;
 }
 
 // How a gradient is computed; the same for every alignment.
 struct GradPlan {
     RowShape shape;
     int stages = 0;          // > 0: through the ring; 0 and no warp: long rows
-    uint32_t x_off = 0, stage_bytes = 0;
+    uint32_t x_off = 0, stage_bytes = 0, w_bytes = 0;
     size_t smem = 0;
     int parts = 1;
 };
@@ -596,13 +614,17 @@ GradPlan grad_plan(const muon_layer_norm_grad_args& a) {
         const int64_t row = dy + (a.saved.q ? ceil_div(a.cols, 16) * 16 : dy);
         const int most = g.shape.nv < 4 || size == 2 ? 512 : 1024;
         const int per_sm = g.shape.nv < 4 ? 2 : 1;
-        int64_t stages = (per_sm == 2 ? 112 : 224) * 1024 / row;
+        // the vectors read whole: room to the end of the last one
+        const int64_t w = a.weight ? ceil_div(a.cols, 8) * 8 * (a.w_dtype == MUON_F32 ? 4 : 2) : 0;
+        const int64_t w_bytes = ceil_div(w, 128) * 128;
+        int64_t stages = ((per_sm == 2 ? 112 : 224) * 1024 - w_bytes) / row;
         if (stages > 8) stages = 8;
         if (g.shape.threads <= most && stages >= 1) {
             g.stages = static_cast<int>(stages);
             g.x_off = static_cast<uint32_t>(dy);
             g.stage_bytes = static_cast<uint32_t>(row);
-            g.smem = size_t(row) * stages;
+            g.w_bytes = static_cast<uint32_t>(w_bytes);
+            g.smem = size_t(w_bytes) + size_t(row) * stages;
             parts = SMS * per_sm;
         } else {
             parts = 64;
@@ -656,6 +678,8 @@ cudaError_t norm_backward(GradLaunch& p, cudaStream_t s) {
     p.stages = g.stages;
     p.x_off = g.x_off;
     p.stage_bytes = g.stage_bytes;
+    p.w_bytes = g.w_bytes;
+    p.ld_part = ceil_div(a.cols, 4) * 4;
     p.w_vec = rows_on_16(a.weight, 1, 1, 0);
     p.wait_limit_ns = wait_limit_ns();
     if (a.rows == 0) {
@@ -685,7 +709,7 @@ cudaError_t launch_layer_norm(const muon_layer_norm_args& a, cudaStream_t s) {
 
 size_t layer_norm_grad_workspace(const muon_layer_norm_grad_args& a) {
     if (!a.dweight && !a.dbias) return 0;
-    const size_t n = size_t(grad_plan(a).parts) * 2 * size_t(a.cols) * 4;
+    const size_t n = size_t(grad_plan(a).parts) * 2 * size_t(ceil_div(a.cols, 4) * 4) * 4;
     return n ? n : 4;        // never NULL: the launch tells by the pointer
 }
 

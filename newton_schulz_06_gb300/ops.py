@@ -20,7 +20,7 @@ include/muon.h has each operator's formula.
 from __future__ import annotations
 
 import ctypes
-from ctypes import byref
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -29,8 +29,27 @@ from . import _lib
 from ._lib import MuonError, lib
 from .muon import _DT
 
-_NO_CKPT = _lib.Ckpt8(None, None, 0, 0)
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+_NO_CKPT = (0, 0, 0, 0)
 _ERR_LEN = 256
+_norm_args = _lib.packer(_lib.LayerNormArgs).pack
+_norm_grad_args = _lib.packer(_lib.LayerNormGradArgs).pack
+_weight_grad_args = _lib.packer(_lib.WeightGradArgs).pack
+_route_args = _lib.packer(_lib.RouteArgs).pack
+_route_grad_args = _lib.packer(_lib.RouteGradArgs).pack
+_ckpt_arg = _lib.packer(_lib.Ckpt8).pack
+
+
+class _Local(threading.local):
+    """A thread's message buffer and workspace size."""
+
+    def __init__(self):
+        self.err = ctypes.create_string_buffer(_ERR_LEN)
+        self.size = ctypes.c_size_t()
+        self.size_ref = ctypes.byref(self.size)
+
+
+_local = _Local()
 
 
 def _need(ok: bool, message: str) -> None:
@@ -49,9 +68,9 @@ def _matrix(name: str, t: torch.Tensor, device=None, shape=None) -> int:
     """Checks a row-major 2-D CUDA tensor; its leading dimension."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
-    if t.device.type != "cuda" or (device is not None and t.device != device):
+    if not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name} must be a CUDA tensor of its operator's device, is on {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     ld, inner = t.stride()
     if inner != 1 and t.shape[1] > 1:
@@ -59,11 +78,11 @@ def _matrix(name: str, t: torch.Tensor, device=None, shape=None) -> int:
     return ld
 
 
-def _vector(name: str, t: Optional[torch.Tensor], device, n: int, dtype=None) -> Optional[int]:
+def _vector(name: str, t: Optional[torch.Tensor], device, n: int, dtype=None) -> int:
     """Checks a dense 1-D tensor of n values (or None); its address."""
     if t is None:
-        return None
-    if t.device != device or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        return 0
+    if t.device != device or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be {n} dense values on {device}, got {tuple(t.shape)} "
                          f"on {t.device}")
     if dtype is not None and t.dtype != dtype:
@@ -71,49 +90,31 @@ def _vector(name: str, t: Optional[torch.Tensor], device, n: int, dtype=None) ->
     return t.data_ptr()
 
 
-def _out(name: str, t: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-    return t
+def _call(device: torch.device, name: str, *args) -> None:
+    """Calls an entry point on the device's current stream, with the device
+    current."""
+    index = device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _call(device, name, *args)
+    err = _local.err
+    rc = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index), err, _ERR_LEN)
+    if rc < 0:
+        raise MuonError(rc, f"{name}: {err.value.decode(errors='replace')}")
 
 
-class _On:
-    """The device and stream of one call: makes the device current if it is
-    not, and calls an entry point on the device's current stream."""
-
-    __slots__ = ("device", "_guard")
-
-    def __init__(self, device: torch.device):
-        self.device = device
-        self._guard = None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.device.index:
-            self._guard = torch.cuda.device(self.device)
-            self._guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-
-    def call(self, name: str, *args) -> None:
-        buf = ctypes.create_string_buffer(_ERR_LEN)
-        rc = getattr(lib(), name)(*args, torch.cuda.current_stream(self.device).cuda_stream,
-                                  buf, _ERR_LEN)
-        if rc < 0:
-            raise MuonError(rc, f"{name}: {buf.value.decode(errors='replace')}")
-
-    def call_ws(self, name: str, args) -> None:
-        """Calls an entry point that takes a workspace, allocated here."""
-        n = ctypes.c_size_t()
-        rc = getattr(lib(), name + "_workspace")(byref(args), byref(n))
-        ws = None
-        if rc == 0 and n.value:
-            ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
-        # a query that refuses its arguments leaves the message to the call
-        self.call(name, byref(args), None if ws is None else ws.data_ptr(), n.value)
+def _call_ws(device: torch.device, name: str, query: str, args: bytes) -> None:
+    """Calls an entry point that takes a workspace, allocated here."""
+    size = _local.size
+    size.value = 0
+    # a query that refuses its arguments leaves the message to the call
+    getattr(lib(), query)(args, _local.size_ref)
+    n = size.value
+    if n:
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        _call(device, name, args, ws.data_ptr(), n)
+    else:
+        _call(device, name, args, None, 0)
 
 
 class Checkpoint8:
@@ -138,8 +139,11 @@ class Checkpoint8:
     @classmethod
     def empty(cls, rows: int, cols: int, device) -> "Checkpoint8":
         blocks = -(-cols // 32)
-        return cls(torch.empty((rows, 32 * blocks), dtype=torch.int8, device=device),
-                   torch.empty((rows, blocks), dtype=torch.uint8, device=device), cols)
+        c = cls.__new__(cls)
+        c.q = torch.empty((rows, 32 * blocks), dtype=torch.int8, device=device)
+        c.e = torch.empty((rows, blocks), dtype=torch.uint8, device=device)
+        c.cols = cols
+        return c
 
     @property
     def rows(self) -> int:
@@ -157,30 +161,49 @@ class Checkpoint8:
     def nbytes(self) -> int:
         return self.q.nbytes + self.e.nbytes
 
-    def _arg(self):
-        return _lib.Ckpt8(self.q.data_ptr(), self.e.data_ptr(), self.q.stride(0), self.e.stride(0))
+    def _fields(self):
+        return self.q.data_ptr(), self.e.data_ptr(), self.q.stride(0), self.e.stride(0)
 
     def values(self, dtype: torch.dtype = torch.bfloat16,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """What the checkpoint stands for (exact in bf16 and fp32)."""
-        out = _out("out", out, self.shape, out.dtype if out is not None else dtype, self.device)
-        ld = _matrix("out", out, self.device, self.shape)
-        with _On(self.device) as on:
-            on.call("muon_ckpt8_unpack", byref(self._arg()), self.rows, self.cols, out.data_ptr(),
-                    _dtype("out", out), ld)
+        q, cols = self.q, self.cols
+        rows, dev = q.shape[0], q.device
+        if out is None:
+            out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        ld = _matrix("out", out, dev, (rows, cols))
+        _call(dev, "muon_ckpt8_unpack", _ckpt_arg(*self._fields()), rows, cols, out.data_ptr(),
+              _dtype("out", out), ld)
         return out
 
 
 def checkpoint8(x: torch.Tensor, out: Optional[Checkpoint8] = None) -> Checkpoint8:
     """The 8-bit checkpoint of x (2-D, fp32 or bf16)."""
     ld = _matrix("x", x)
-    if out is None:
-        out = Checkpoint8.empty(*x.shape, x.device)
-    _need(out.shape == tuple(x.shape) and out.device == x.device,
-          f"out must be a checkpoint of {tuple(x.shape)} on {x.device}")
-    with _On(x.device) as on:
-        on.call("muon_ckpt8_pack", x.data_ptr(), _dtype("x", x), *x.shape, ld, byref(out._arg()))
+    rows, cols = x.shape
+    dev = x.device
+    out = _checkpoint("out", out, rows, cols, dev)
+    _call(dev, "muon_ckpt8_pack", x.data_ptr(), _dtype("x", x), rows, cols, ld,
+          _ckpt_arg(*out._fields()))
     return out
+
+
+def _checkpoint(name: str, c: Optional[Checkpoint8], rows: int, cols: int, device) -> Checkpoint8:
+    if c is None:
+        return Checkpoint8.empty(rows, cols, device)
+    _need(c.shape == (rows, cols) and c.device == device,
+          f"{name} must be a checkpoint of {(rows, cols)} on {device}")
+    return c
+
+
+def _output(name: str, t: Optional[torch.Tensor], like: torch.Tensor):
+    """The output of `like`'s shape, type and device (given or new): (it, its
+    leading dimension)."""
+    if t is None:
+        rows, cols = like.shape
+        return torch.empty((rows, cols), dtype=like.dtype, device=like.device), cols
+    _need(t.dtype == like.dtype, f"{name} must be {like.dtype}, got {t.dtype}")
+    return t, _matrix(name, t, like.device, like.shape)
 
 
 def _w_dtype(weight, bias) -> int:
@@ -190,21 +213,19 @@ def _w_dtype(weight, bias) -> int:
     return _lib.MUON_F32 if t is None else _dtype("weight and bias", t)
 
 
-def _norm_forward(x, weight, bias, eps, out, saved):
+def _norm_forward(x, weight, bias, eps, out, saved, mean):
     ld = _matrix("x", x)
     rows, cols = x.shape
     dev = x.device
-    y = _out("out", out, x.shape, x.dtype, dev)
-    ld_y = _matrix("out", y, dev, x.shape)
-    stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
-    p = stats.data_ptr()
-    args = _lib.LayerNormArgs(
+    y, ld_y = _output("out", out, x)
+    rstd = torch.empty(rows, dtype=_F32, device=dev)
+    args = _norm_args(
         x.data_ptr(), _vector("weight", weight, dev, cols), _vector("bias", bias, dev, cols),
-        y.data_ptr(), p, p + 4 * rows, _NO_CKPT if saved is None else saved._arg(),
+        y.data_ptr(), 0 if mean is None else mean.data_ptr(), rstd.data_ptr(),
+        *(_NO_CKPT if saved is None else saved._fields()),
         rows, cols, ld, ld_y, _dtype("x", x), _w_dtype(weight, bias), eps)
-    with _On(dev) as on:
-        on.call("muon_layer_norm", byref(args))
-    return y, stats[0], stats[1]
+    _call(dev, "muon_layer_norm", args)
+    return y, rstd
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -214,7 +235,10 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
 
     Returns (y, mean, rstd); y has x's type (out may be x), mean and rstd are
     fp32.  weight and bias: fp32 or bf16, of one type; None for ones, zeros."""
-    return _norm_forward(x, weight, bias, eps, out, None)
+    _matrix("x", x)
+    mean = torch.empty(x.shape[0], dtype=_F32, device=x.device)
+    y, rstd = _norm_forward(x, weight, bias, eps, out, None, mean)
+    return y, mean, rstd
 
 
 def layer_norm_checkpoint(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -228,11 +252,8 @@ def layer_norm_checkpoint(x: torch.Tensor, weight: Optional[torch.Tensor] = None
     with the norm's weight and bias, :func:`weight_grad` of every product that
     reads y, so that neither x nor y has to be kept."""
     _matrix("x", x)
-    if saved is None:
-        saved = Checkpoint8.empty(*x.shape, x.device)
-    _need(saved.shape == tuple(x.shape) and saved.device == x.device,
-          f"saved must be a checkpoint of {tuple(x.shape)} on {x.device}")
-    y, _, rstd = _norm_forward(x, weight, bias, eps, out, saved)
+    saved = _checkpoint("saved", saved, x.shape[0], x.shape[1], x.device)
+    y, rstd = _norm_forward(x, weight, bias, eps, out, saved, None)
     return y, rstd, saved
 
 
@@ -253,31 +274,28 @@ def layer_norm_backward(dy: torch.Tensor, x, mean: Optional[torch.Tensor], rstd:
         _need(x.shape == (rows, cols) and x.device == dev,
               f"x must be a checkpoint of {(rows, cols)} on {dev}, is of {x.shape}")
         _need(mean is None, "mean must be None beside a checkpoint (it holds h itself)")
-        saved, x_ptr, ld_x = x._arg(), None, 0
+        saved, x_ptr, ld_x = x._fields(), 0, 0
     else:
         ld_x = _matrix("x", x, dev, dy.shape)
         _need(x.dtype == dy.dtype, f"x and dy differ in type: {x.dtype}, {dy.dtype}")
         _need(mean is not None, "mean is needed beside x")
         saved, x_ptr = _NO_CKPT, x.data_ptr()
-    dx = _out("out", out, dy.shape, dy.dtype, dev)
-    ld_dx = _matrix("out", dx, dev, dy.shape)
-    dw = torch.empty_like(weight) if weight is not None else None
-    db = torch.empty_like(bias) if bias is not None else None
-    args = _lib.LayerNormGradArgs(
-        dy.data_ptr(), x_ptr, _vector("mean", mean, dev, rows, torch.float32),
-        _vector("rstd", rstd, dev, rows, torch.float32), _vector("weight", weight, dev, cols),
-        dx.data_ptr(), _vector("dweight", dw, dev, cols), _vector("dbias", db, dev, cols),
-        saved, rows, cols, ld_dy, ld_x, ld_dx, _dtype("dy", dy), _w_dtype(weight, bias))
-    if bias is not None:
-        _vector("bias", bias, dev, cols)
-    with _On(dev) as on:
-        on.call_ws("muon_layer_norm_grad", args)
+    dx, ld_dx = _output("out", out, dy)
+    dw = torch.empty(cols, dtype=weight.dtype, device=dev) if weight is not None else None
+    db = torch.empty(cols, dtype=bias.dtype, device=dev) if bias is not None else None
+    _vector("bias", bias, dev, cols)
+    args = _norm_grad_args(
+        dy.data_ptr(), x_ptr, _vector("mean", mean, dev, rows, _F32),
+        _vector("rstd", rstd, dev, rows, _F32), _vector("weight", weight, dev, cols),
+        dx.data_ptr(), 0 if dw is None else dw.data_ptr(), 0 if db is None else db.data_ptr(),
+        *saved, rows, cols, ld_dy, ld_x, ld_dx, _dtype("dy", dy), _w_dtype(weight, bias))
+    _call_ws(dev, "muon_layer_norm_grad", "muon_layer_norm_grad_workspace", args)
     return dx, dw, db
 
 
 def _gradient(name: str, t: torch.Tensor, shape, device):
     """Checks a row-major gradient (n x k, or experts x n x k): (ld, stride)."""
-    if tuple(t.shape) != shape or t.device != device:
+    if t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be {shape} on {device}, got {tuple(t.shape)} on {t.device}")
     if t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be row-major (stride(-1) == 1)")
@@ -314,13 +332,12 @@ def weight_grad(dy: torch.Tensor, x: Checkpoint8, *, weight: Optional[torch.Tens
     if add is not None:
         ld_c, stride_c = _gradient("add", add, shape, dev)
         _need(add.dtype == g.dtype, f"add and the result differ in type: {add.dtype}, {g.dtype}")
-    args = _lib.WeightGradArgs(
-        dy.data_ptr(), _vector("weight", weight, dev, k, torch.float32),
-        _vector("bias", bias, dev, k, torch.float32), None if add is None else add.data_ptr(),
-        g.data_ptr(), None if offsets is None else offsets.data_ptr(), x._arg(),
+    args = _weight_grad_args(
+        dy.data_ptr(), _vector("weight", weight, dev, k, _F32),
+        _vector("bias", bias, dev, k, _F32), 0 if add is None else add.data_ptr(),
+        g.data_ptr(), 0 if offsets is None else offsets.data_ptr(), *x._fields(),
         rows, n, k, experts, ld_dy, ld_c, ld_g, stride_c, stride_g, _dtype("out", g))
-    with _On(dev) as on:
-        on.call_ws("muon_weight_grad", args)
+    _call_ws(dev, "muon_weight_grad", "muon_weight_grad_workspace", args)
     return g
 
 
@@ -347,25 +364,24 @@ def route(logits: torch.Tensor, k: int, *, mask: Optional[torch.Tensor] = None,
     ld = _matrix("logits", logits)
     tokens, experts = logits.shape
     dev = logits.device
-    mask_ptr = None
+    mask_ptr = 0
     if mask is not None:
         _need(mask.dtype in (torch.bool, torch.uint8), f"mask must be bool or uint8, got {mask.dtype}")
         mask_ptr = _vector("mask", mask, dev, tokens)
     _need(1 <= k <= min(experts, 32), f"k must be 1 .. min(experts, 32), got {k}")
-    indices = torch.empty((tokens, k), dtype=torch.int32, device=dev)
-    weights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
-    # counts, kept and offsets in one allocation
-    ints = torch.empty(2 * experts + 2, dtype=torch.int32, device=dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    p = ints.data_ptr()
-    args = _lib.RouteArgs(
-        logits.data_ptr(), mask_ptr, indices.data_ptr(), weights.data_ptr(), p,
-        p + 4 * (experts + 1), loss.data_ptr(), p + 4 * experts, tokens, experts, k, ld,
-        _dtype("logits", logits), int(bool(renormalise)), coef)
-    with _On(dev) as on:
-        on.call_ws("muon_route", args)
-    return Routing(indices, weights, ints[:experts], ints[experts], offsets=ints[experts + 1:],
-                   loss=loss, coef=coef, renormalise=renormalise)
+    indices = torch.empty((tokens, k), dtype=_I32, device=dev)
+    weights = torch.empty((tokens, k), dtype=_F32, device=dev)
+    counts = torch.empty(experts, dtype=_I32, device=dev)
+    offsets = torch.empty(experts + 1, dtype=_I32, device=dev)
+    kept = torch.empty((), dtype=_I32, device=dev)
+    loss = torch.empty((), dtype=_F32, device=dev)
+    args = _route_args(
+        logits.data_ptr(), mask_ptr, indices.data_ptr(), weights.data_ptr(), counts.data_ptr(),
+        offsets.data_ptr(), loss.data_ptr(), kept.data_ptr(), tokens, experts, k, ld,
+        _dtype("logits", logits), bool(renormalise), coef)
+    _call_ws(dev, "muon_route", "muon_route_workspace", args)
+    return Routing(indices, weights, counts, kept, offsets=offsets, loss=loss, coef=coef,
+                   renormalise=renormalise)
 
 
 def route_backward(logits: torch.Tensor, routing: Routing, *,
@@ -381,29 +397,27 @@ def route_backward(logits: torch.Tensor, routing: Routing, *,
     r = routing
     _need(r.indices.dim() == 2, "routing.indices must be 2-D")
     k = r.indices.shape[1]
-    for name, t, dtype, shape in (("indices", r.indices, torch.int32, (tokens, k)),
-                                  ("weights", r.weights, torch.float32, (tokens, k)),
-                                  ("counts", r.counts, torch.int32, (experts,))):
-        _need(t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous()
-              and t.device == dev, f"routing.{name} must be {dtype} {shape}, dense, on {dev}")
-    _need(r.kept.dtype == torch.int32 and r.kept.numel() == 1 and r.kept.device == dev,
+    for name, t, dtype, shape in (("indices", r.indices, _I32, (tokens, k)),
+                                  ("weights", r.weights, _F32, (tokens, k)),
+                                  ("counts", r.counts, _I32, (experts,))):
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"routing.{name} must be {dtype} {shape}, dense, on {dev}")
+    _need(r.kept.dtype == _I32 and r.kept.numel() == 1 and r.kept.device == dev,
           "routing.kept must be one int32 value on the device")
     if dloss is not None:
-        _need(dloss.dtype == torch.float32 and dloss.numel() == 1 and dloss.device == dev,
+        _need(dloss.dtype == _F32 and dloss.numel() == 1 and dloss.device == dev,
               "dloss must be one float32 value on the device")
     ld_dw = 0
     if dweights is not None:
         ld_dw = _matrix("dweights", dweights, dev, (tokens, k))
         _need(dweights.dtype == torch.float32, f"dweights must be float32, got {dweights.dtype}")
-    dz = _out("out", out, logits.shape, logits.dtype, dev)
-    ld_dz = _matrix("out", dz, dev, logits.shape)
-    args = _lib.RouteGradArgs(
+    dz, ld_dz = _output("out", out, logits)
+    args = _route_grad_args(
         logits.data_ptr(), r.indices.data_ptr(), r.weights.data_ptr(), r.counts.data_ptr(),
-        r.kept.data_ptr(), None if dloss is None else dloss.data_ptr(),
-        None if dweights is None else dweights.data_ptr(), dz.data_ptr(), tokens, experts, k,
-        ld, ld_dw, ld_dz, _dtype("logits", logits), int(bool(r.renormalise)), r.coef)
-    with _On(dev) as on:
-        on.call("muon_route_grad", byref(args))
+        r.kept.data_ptr(), 0 if dloss is None else dloss.data_ptr(),
+        0 if dweights is None else dweights.data_ptr(), dz.data_ptr(), tokens, experts, k,
+        ld, ld_dw, ld_dz, _dtype("logits", logits), bool(r.renormalise), r.coef)
+    _call(dev, "muon_route_grad", args)
     return dz
 
 
@@ -411,5 +425,4 @@ def ops_sync(device: Optional[int] = None) -> None:
     """Waits for the current stream and raises what the operators met on the
     GPU (MuonError; a bounded wait that ran out is MUON_ERR_TIMEOUT)."""
     dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
-    with _On(dev) as on:
-        on.call("muon_ops_sync")
+    _call(dev, "muon_ops_sync")

@@ -215,3 +215,24 @@ def test_oracle_router_gradient_is_that_of_its_objective(renormalise):
     got = O.route_grad(z, idx, counts, kept, 0.3, renormalise, 0.9, dw)
     assert torch.allclose(torch.nan_to_num(zr.grad), got, rtol=1e-12, atol=1e-14)
     assert abs(O.route_objective(z, idx, counts, kept, 0.3, renormalise, 1.0, None).item() - loss) < 1e-14
+
+
+def test_packed_arguments_have_the_structures_layout(L):
+    for cls in (L.Ckpt8, L.LayerNormArgs, L.LayerNormGradArgs, L.WeightGradArgs, L.RouteArgs,
+                L.RouteGradArgs):
+        pack = L.packer(cls)
+        assert pack.size == ctypes.sizeof(cls)
+        n = len(pack.unpack(bytes(pack.size)))
+        a = cls.from_buffer_copy(pack.pack(*range(1, n + 1)))
+        flat = []
+
+        def walk(v):
+            for f, _ in v._fields_:
+                x = getattr(v, f)
+                if isinstance(x, ctypes.Structure):
+                    walk(x)
+                else:
+                    flat.append(x)
+
+        walk(a)
+        assert flat == list(range(1, n + 1))
