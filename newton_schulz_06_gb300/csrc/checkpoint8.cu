@@ -19,19 +19,19 @@ __device__ __forceinline__ void place(int64_t i, int64_t total, uint32_t per, in
 }
 
 // One thread per vector, UNROLL of them in flight.
-template <typename T>
+template <typename T, bool AL>
 __global__ void __launch_bounds__(THREADS)
     pack_kernel(const T* x, int64_t rows, int64_t cols, int64_t ld_x, muon_ckpt8 out) {
     grid_dependency_wait();
     allow_dependent_launch();
-    constexpr int VE = Vec<T>::VE, UNROLL = 4;
+    constexpr int VE = Vec<T, AL>::VE, UNROLL = 4;
     const uint32_t per = static_cast<uint32_t>((cols + CKPT_BLOCK - 1) / CKPT_BLOCK * (CKPT_BLOCK / VE));
     const int64_t total = rows * per;
     const int64_t stride = int64_t(gridDim.x) * THREADS;
     // whole warps walk on together: encode_vec asks every lane
     const int64_t rounded = (total + 31) / 32 * 32;
     for (int64_t i0 = blockIdx.x * int64_t(THREADS) + threadIdx.x; i0 < rounded; i0 += UNROLL * stride) {
-        Vec<T> v[UNROLL];
+        Vec<T, AL> v[UNROLL];
         int64_t r[UNROLL];
         int c[UNROLL];
 #pragma unroll
@@ -44,19 +44,19 @@ __global__ void __launch_bounds__(THREADS)
         for (int u = 0; u < UNROLL; ++u) {
             const int64_t i = i0 + u * stride;
             if (i >= rounded) break;
-            float f[VE];
+            float2 f[VE / 2];
             v[u].get(f);
             encode_vec<VE>(out, r[u], c[u], i < total, f);
         }
     }
 }
 
-template <typename T>
+template <typename T, bool AL>
 __global__ void __launch_bounds__(THREADS)
     unpack_kernel(muon_ckpt8 in, int64_t rows, int64_t cols, T* x, int64_t ld_x) {
     grid_dependency_wait();
     allow_dependent_launch();
-    constexpr int VE = Vec<T>::VE;
+    constexpr int VE = Vec<T, AL>::VE;
     const uint32_t per = static_cast<uint32_t>((cols + VE - 1) / VE);
     const int64_t total = rows * per;
     const int64_t rounded = (total + 31) / 32 * 32;
@@ -64,10 +64,10 @@ __global__ void __launch_bounds__(THREADS)
          i += int64_t(gridDim.x) * THREADS) {
         int64_t r = 0;
         int c = 0;
-        Vec<T> v;
+        Vec<T, AL> v;
         if (i < total) {
             place(i, total, per, VE, &r, &c);
-            float f[VE];
+            float2 f[VE / 2];
             decode_vec<VE>(in.q + r * in.ld_q + c, scale_pow(in.e[r * in.ld_e + c / CKPT_BLOCK]), f);
             v.set(f);
         }
@@ -81,18 +81,24 @@ int grid_for(int64_t items) {
 }
 
 template <typename T>
+bool whole(const T* x, int64_t rows, int64_t cols, int64_t ld) {
+    return cols % Vec<T, true>::VE == 0 && rows_on_16(x, sizeof(T), rows, ld);
+}
+
+template <typename T>
 cudaError_t pack(const T* x, int64_t rows, int64_t cols, int64_t ld_x, const muon_ckpt8& saved,
                  cudaStream_t s) {
-    const int64_t vectors = rows * ceil_div(cols, CKPT_BLOCK) * (CKPT_BLOCK / Vec<T>::VE);
-    return launch_kernel(pack_kernel<T>, dim3(grid_for(vectors)), dim3(THREADS), 0, s, x, rows, cols,
-                         ld_x, saved);
+    const int64_t vectors = rows * ceil_div(cols, CKPT_BLOCK) * (CKPT_BLOCK / Vec<T, true>::VE);
+    return launch_kernel(whole(x, rows, cols, ld_x) ? pack_kernel<T, true> : pack_kernel<T, false>,
+                         dim3(grid_for(vectors)), dim3(THREADS), 0, s, x, rows, cols, ld_x, saved);
 }
 
 template <typename T>
 cudaError_t unpack(const muon_ckpt8& saved, int64_t rows, int64_t cols, T* x, int64_t ld_x,
                    cudaStream_t s) {
-    return launch_kernel(unpack_kernel<T>, dim3(grid_for(rows * ceil_div(cols, Vec<T>::VE))),
-                         dim3(THREADS), 0, s, saved, rows, cols, x, ld_x);
+    return launch_kernel(whole(x, rows, cols, ld_x) ? unpack_kernel<T, true> : unpack_kernel<T, false>,
+                         dim3(grid_for(rows * ceil_div(cols, Vec<T, true>::VE))), dim3(THREADS), 0, s,
+                         saved, rows, cols, x, ld_x);
 }
 
 }  // namespace

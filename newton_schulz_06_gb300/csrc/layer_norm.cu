@@ -2,7 +2,7 @@
 // muon_layer_norm_grad).
 //
 // Forward.  A row is read once, in 16-byte vectors (at any alignment: see
-// Vec) that stay in registers, by a warp (up to 128 vectors) or a block.  The variance is taken around the
+// Vec) that stay in registers, by 8 to 32 lanes of a warp or by a block.  The variance is taken around the
 // mean in a second sum over the registers (sums of x^2 lose it when the mean
 // is large), with the first sum's rounding corrected by the sum of the
 // deviations.  The checkpoint of h is written from the same registers.
@@ -21,22 +21,31 @@ namespace {
 constexpr int SMS = 152;
 __device__ int g_norm_err;             // DEV_ERR_TIMEOUT once a bounded wait ran out
 
-// Sums of two values over a row's threads, in a fixed order, returned to all
-// of them: a warp, or a block (buf alternates between two, so that one
-// barrier a sum is enough).
-template <bool WARP>
-__device__ __forceinline__ float2 row_sum2(float a, float b, float2* buf) {
+// Sums of two values over a block, in a fixed order, returned to all threads;
+// buf alternates between two, so that one barrier a sum is enough.
+__device__ __forceinline__ float2 block_sum2(float a, float b, float2* buf) {
     a = warp_sum(a);
     b = warp_sum(b);
-    if constexpr (!WARP) {
-        const int lane = threadIdx.x & 31;
-        if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
-        const float2 t = lane < static_cast<int>(blockDim.x >> 5) ? buf[lane] : make_float2(0.f, 0.f);
-        a = warp_sum(t.x);
-        b = warp_sum(t.y);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    const float2 t = lane < static_cast<int>(blockDim.x >> 5) ? buf[lane] : make_float2(0.f, 0.f);
+    return make_float2(warp_sum(t.x), warp_sum(t.y));
+}
+// The same over the L threads of a row: neighbouring lanes (L = 8, 16, 32),
+// or the block (L = 0).
+template <int L>
+__device__ __forceinline__ float2 row_sum2(float a, float b, float2* buf) {
+    if constexpr (L == 0) {
+        return block_sum2(a, b, buf);
+    } else {
+#pragma unroll
+        for (int o = L / 2; o; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        return make_float2(a, b);
     }
-    return make_float2(a, b);
 }
 
 // ------------------------------------------------------------------ forward
@@ -46,54 +55,60 @@ struct NormLaunch {
     int32_t w_vec;           // weight and bias allow 16-byte loads
 };
 
-// A row in the registers of a warp (WARP; blockDim.y rows a block) or of a
-// block: NV vectors a thread.
-template <typename T, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 1024)
+// A row in the registers of L lanes (256 / L rows a block) or of a block
+// (L = 0): NV vectors a thread.
+template <typename T, bool AL, int NV, int L>
+__global__ void __launch_bounds__(L ? 256 : 1024)
     norm_kernel(const __grid_constant__ NormLaunch p) {
-    constexpr int VE = Vec<T>::VE;
+    constexpr int VE = Vec<T, AL>::VE, F2 = VE / 2;
     __shared__ float2 red[2][32];
     grid_dependency_wait();
     allow_dependent_launch();
     const muon_layer_norm_args& a = p.a;
-    const int64_t r = WARP ? blockIdx.x * int64_t(blockDim.y) + threadIdx.y : int64_t(blockIdx.x);
-    if (WARP && r >= a.rows) return;
-    const int cols = static_cast<int>(a.cols);
-    const float inv_n = 1.f / static_cast<float>(cols);
-    const int step = (WARP ? 32 : blockDim.x) * VE;
+    const int64_t r = L ? int64_t(blockIdx.x) * (256 / (L ? L : 1)) + threadIdx.x / (L ? L : 1)
+                        : int64_t(blockIdx.x);
+    // lanes whose row is not there walk along with nothing in it
+    const int cols = !L || r < a.rows ? static_cast<int>(a.cols) : 0;
+    const float inv_n = 1.f / static_cast<float>(a.cols);
+    const int step = (L ? L : blockDim.x) * VE;
+    const int c0 = (L ? threadIdx.x % (L ? L : 1) : threadIdx.x) * VE;
     const T* x = static_cast<const T*>(a.x) + r * a.ld_x;
-    Vec<T> v[NV];
-    const int c0 = threadIdx.x * VE;
+    Vec<T, AL> raw[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i].load(x + c0 + i * step, cols - c0 - i * step);
-    float s = 0.f;
+    for (int i = 0; i < NV; ++i) raw[i].load(x + c0 + i * step, cols - c0 - i * step);
+    float2 s = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        float f[VE];
-        v[i].get(f);
+        float2 v[F2];
+        raw[i].get(v);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) s += f[j];
+        for (int j = 0; j < F2; ++j) s = add2(s, v[j]);
     }
-    float mean = row_sum2<WARP>(s, 0.f, red[0]).x * inv_n;
-    float d1 = 0.f, d2 = 0.f;
+    float mean = row_sum2<L>(s.x + s.y, 0.f, red[0]).x * inv_n;
+    float2 d1 = both(0.f), d2 = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int valid = cols - c0 - i * step;
-        float f[VE];
-        v[i].get(f);
+        if (valid <= 0) break;
+        float2 v[F2];
+        raw[i].get(v);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-            const float d = j < valid ? f[j] - mean : 0.f;
-            d1 += d;
-            d2 = fmaf(d, d, d2);
+        for (int j = 0; j < F2; ++j) {
+            float2 d = add2(v[j], both(-mean));
+            if (!AL) {
+                if (2 * j >= valid) d.x = 0.f;
+                if (2 * j + 1 >= valid) d.y = 0.f;
+            }
+            d1 = add2(d1, d);
+            d2 = fma2(d, d, d2);
         }
     }
-    const float2 t = row_sum2<WARP>(d1, d2, red[1]);
+    const float2 t = row_sum2<L>(d1.x + d1.y, d2.x + d2.y, red[1]);
     const float off = t.x * inv_n;
     const float var = fmaxf(fmaf(-off, off, t.y * inv_n), 0.f) + (t.y != t.y ? t.y : 0.f);
     mean += off;
     const float rstd = 1.f / sqrtf(var + a.eps);
-    if (threadIdx.x == 0) {
+    if (c0 == 0 && cols) {
         if (a.mean) a.mean[r] = mean;
         if (a.rstd) a.rstd[r] = rstd;
     }
@@ -102,20 +117,28 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = c0 + i * step, valid = cols - c;
-        float h[VE];
-        v[i].get(h);
+        float2 h[F2];
+        raw[i].get(h);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) h[j] = j < valid ? (h[j] - mean) * rstd : 0.f;
-        if (a.saved.q) encode_vec<VE>(a.saved, r, c, c < padded, h);
-        if (valid > 0) {
-            float w[VE], b[VE];
-            load_row_vec<VE>(a.weight, a.w_dtype, p.w_vec, c, valid, 1.f, w);
-            load_row_vec<VE>(a.bias, a.w_dtype, p.w_vec, c, valid, 0.f, b);
+        for (int j = 0; j < F2; ++j) h[j] = mul2(add2(h[j], both(-mean)), both(rstd));
+        if (a.saved.q) {
+            // past the row's end the checkpoint holds zeros
 #pragma unroll
-            for (int j = 0; j < VE; ++j) h[j] = fmaf(h[j], w[j], b[j]);
-            v[i].set(h);
+            for (int j = 0; j < F2; ++j) {
+                if (AL ? valid <= 0 : 2 * j >= valid) h[j].x = 0.f;
+                if (AL ? valid <= 0 : 2 * j + 1 >= valid) h[j].y = 0.f;
+            }
+            encode_vec<VE>(a.saved, r, c, c < padded, h);
         }
-        v[i].store(y + c, valid, c == 0);
+        if (valid > 0) {
+            float2 w[F2], b[F2];
+            load_row_vec<VE>(a.weight, a.w_dtype, p.w_vec, c, AL ? VE : valid, 1.f, w);
+            load_row_vec<VE>(a.bias, a.w_dtype, p.w_vec, c, AL ? VE : valid, 0.f, b);
+#pragma unroll
+            for (int j = 0; j < F2; ++j) h[j] = fma2(h[j], w[j], b[j]);
+            raw[i].set(h);
+        }
+        raw[i].store(y + c, valid, c == 0);
     }
 }
 
@@ -133,14 +156,14 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
     T* y = static_cast<T*>(a.y) + r * a.ld_y;
     float s = 0.f;
     for (int c = threadIdx.x; c < cols; c += 1024) s += to_f32(x[c]);
-    float mean = row_sum2<false>(s, 0.f, red[0]).x * inv_n;
+    float mean = block_sum2(s, 0.f, red[0]).x * inv_n;
     float d1 = 0.f, d2 = 0.f;
     for (int c = threadIdx.x; c < cols; c += 1024) {
         const float d = to_f32(x[c]) - mean;
         d1 += d;
         d2 = fmaf(d, d, d2);
     }
-    const float2 t = row_sum2<false>(d1, d2, red[1]);
+    const float2 t = block_sum2(d1, d2, red[1]);
     const float off = t.x * inv_n;
     const float var = fmaxf(fmaf(-off, off, t.y * inv_n), 0.f) + (t.y != t.y ? t.y : 0.f);
     mean += off;
@@ -151,64 +174,80 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
     }
     const int padded = (cols + CKPT_BLOCK - 1) / CKPT_BLOCK * CKPT_BLOCK;
     for (int c = threadIdx.x; c < padded; c += 1024) {
-        float h[1] = {c < cols ? (to_f32(x[c]) - mean) * rstd : 0.f};
+        const float h = c < cols ? (to_f32(x[c]) - mean) * rstd : 0.f;
         if (c < cols) {
             const float w = a.weight ? load_any(a.weight, a.w_dtype, c) : 1.f;
             const float b = a.bias ? load_any(a.bias, a.w_dtype, c) : 0.f;
-            from_f32(y + c, fmaf(h[0], w, b));
+            from_f32(y + c, fmaf(h, w, b));
         }
-        if (a.saved.q) encode_vec<1>(a.saved, r, c, true, h);
+        if (a.saved.q) {
+            // a warp's 32 columns are one block
+            const uint32_t e = scale_byte(__reduce_max_sync(0xffffffffu, mag_bits(h)));
+            a.saved.q[r * a.saved.ld_q + c] = static_cast<int8_t>(encode_q(h, e, scale_inv(e)));
+            if ((c & 31) == 0) a.saved.e[r * a.saved.ld_e + c / CKPT_BLOCK] = static_cast<uint8_t>(e);
+        }
     }
 }
 
-// A row's vectors over threads: a warp up to 4 vectors a lane, then blocks
-// with as few vectors a thread as keep them at `best` threads.
+// A row's vectors over threads: lanes of a warp up to most_lanes vectors,
+// then blocks with as few vectors a thread as keep them at 512 threads.
 struct RowShape {
-    bool warp = false;
-    int nv = 1, threads = 32;
+    int lanes = 0;           // 8, 16 or 32; 0: the block
+    int nv = 1, threads = 256;
 };
-RowShape row_shape(int64_t vectors, int max_nv, int best) {
+RowShape row_shape(int64_t vectors, int most_lanes, int max_nv) {
     RowShape s;
-    if (vectors <= 32 * 4) {
-        s.warp = true;
+    if (vectors <= most_lanes) {
+        s.lanes = vectors <= 8 ? 8 : vectors <= 16 ? 16 : 32;
         s.nv = vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4;
         return s;
     }
-    while (s.nv < max_nv && ceil_div(vectors, s.nv) > best) s.nv *= 2;
+    while (s.nv < max_nv && ceil_div(vectors, s.nv) > 512) s.nv *= 2;
     s.threads = static_cast<int>(ceil_div(ceil_div(vectors, s.nv), 32) * 32);
     return s;
 }
 
-template <typename T>
-cudaError_t norm_forward(NormLaunch& p, cudaStream_t s) {
-    p.w_vec = rows_on_16(p.a.weight, 1, 1, 0) && rows_on_16(p.a.bias, 1, 1, 0);
+template <typename T, bool AL>
+cudaError_t norm_forward(const NormLaunch& p, cudaStream_t s) {
+    const RowShape sh = row_shape(ceil_div(p.a.cols, Vec<T, AL>::VE), 128, 8);
     const unsigned rows = static_cast<unsigned>(p.a.rows);
-    const RowShape sh = row_shape(ceil_div(p.a.cols, Vec<T>::VE), 8, 512);
-    if (sh.warp) {
-        const dim3 grid((rows + 7) / 8), block(32, 8);
-        if (sh.nv == 1) return launch_kernel(norm_kernel<T, 1, true>, grid, block, 0, s, p);
-        if (sh.nv == 2) return launch_kernel(norm_kernel<T, 2, true>, grid, block, 0, s, p);
-        return launch_kernel(norm_kernel<T, 4, true>, grid, block, 0, s, p);
+    const dim3 block(sh.threads);
+    if (sh.lanes) {
+        const dim3 grid((rows + 256 / sh.lanes - 1) / (256 / sh.lanes));
+        if (sh.lanes == 8) return launch_kernel(norm_kernel<T, AL, 1, 8>, grid, block, 0, s, p);
+        if (sh.lanes == 16) return launch_kernel(norm_kernel<T, AL, 1, 16>, grid, block, 0, s, p);
+        if (sh.nv == 1) return launch_kernel(norm_kernel<T, AL, 1, 32>, grid, block, 0, s, p);
+        if (sh.nv == 2) return launch_kernel(norm_kernel<T, AL, 2, 32>, grid, block, 0, s, p);
+        return launch_kernel(norm_kernel<T, AL, 4, 32>, grid, block, 0, s, p);
     }
-    if (sh.threads > 1024) return launch_kernel(norm_long_kernel<T>, dim3(rows), dim3(1024), 0, s, p);
-    const dim3 grid(rows), block(sh.threads);
-    if (sh.nv == 1) return launch_kernel(norm_kernel<T, 1, false>, grid, block, 0, s, p);
-    if (sh.nv == 2) return launch_kernel(norm_kernel<T, 2, false>, grid, block, 0, s, p);
-    if (sh.nv == 4) return launch_kernel(norm_kernel<T, 4, false>, grid, block, 0, s, p);
-    return launch_kernel(norm_kernel<T, 8, false>, grid, block, 0, s, p);
+    const dim3 grid(rows);
+    if (sh.threads > 1024) return launch_kernel(norm_long_kernel<T>, grid, dim3(1024), 0, s, p);
+    if (sh.nv == 1) return launch_kernel(norm_kernel<T, AL, 1, 0>, grid, block, 0, s, p);
+    if (sh.nv == 2) return launch_kernel(norm_kernel<T, AL, 2, 0>, grid, block, 0, s, p);
+    if (sh.nv == 4) return launch_kernel(norm_kernel<T, AL, 4, 0>, grid, block, 0, s, p);
+    return launch_kernel(norm_kernel<T, AL, 8, 0>, grid, block, 0, s, p);
+}
+
+template <typename T>
+cudaError_t norm_forward_t(NormLaunch& p, cudaStream_t s) {
+    const muon_layer_norm_args& a = p.a;
+    p.w_vec = rows_on_16(a.weight, 1, 1, 0) && rows_on_16(a.bias, 1, 1, 0);
+    const bool al = a.cols % Vec<T, true>::VE == 0 && rows_on_16(a.x, sizeof(T), a.rows, a.ld_x) &&
+                    rows_on_16(a.y, sizeof(T), a.rows, a.ld_y);
+    return al ? norm_forward<T, true>(p, s) : norm_forward<T, false>(p, s);
 }
 
 // ----------------------------------------------------------------- backward
 
 struct GradLaunch {
     muon_layer_norm_grad_args a;
-    float* part;             // parts x 2 x cols partial sums of dweight, dbias (or null)
+    float* part;             // parts x 2 x ld_part partial sums of dweight, dbias (or null)
+    int64_t ld_part;         // cols rounded up to 4
     int32_t w_vec;
     int32_t parts;           // blocks (rows of partial sums)
     int32_t stages;          // rows of the ring in shared memory (norm_grad_ring_kernel)
     uint32_t x_off, stage_bytes;   // of a ring's row: where x (or q) is, and its size
     uint32_t w_bytes;        // the weight's room in shared memory, before the ring
-    int64_t ld_part;         // cols rounded up to 4
     unsigned long long wait_limit_ns;
 };
 
@@ -223,136 +262,133 @@ struct Pieces {
         : first(static_cast<const char*>(p) - lead(p)), bytes((lead(p) + n + 15u) & ~15u) {}
 };
 
-// The partial sums of a block whose threads hold whole columns.
-template <int VE, int NV>
-__device__ __forceinline__ void store_parts(const GradLaunch& p, int c0, int step,
-                                            const float (&dw)[NV * VE], const float (&db)[NV * VE]) {
-    const int cols = static_cast<int>(p.a.cols);
-    float* w = p.part + int64_t(blockIdx.x) * 2 * p.ld_part;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-        for (int j = 0; j < VE; j += 4) {
-            const int c = c0 + i * step + j;
-            if (c >= cols) break;
-            const int u = i * VE + j;
-            *reinterpret_cast<float4*>(w + c) = make_float4(dw[u], dw[u + 1], dw[u + 2], dw[u + 3]);
-            *reinterpret_cast<float4*>(w + p.ld_part + c) =
-                make_float4(db[u], db[u + 1], db[u + 2], db[u + 3]);
-        }
-    }
-}
-
-// One vector: dy, h and g = dy * w, from the row's vectors of dy and x (or q
-// and its scale).  CKPT: x is the checkpoint's row.
-template <typename T, bool CKPT>
+// One vector of a row: dy, h and g = dy * weight.  CKPT: h comes from q and
+// its scale byte e, else from x as x * rstd + shift (shift = -mean * rstd).
+template <typename T, bool AL, bool CKPT>
 struct GradVec {
-    static constexpr int VE = Vec<T>::VE;
-    float dy[VE], h[VE], g[VE];
-    __device__ __forceinline__ void make(const GradLaunch& p, const Vec<T>& dyv, const Vec<T>& xv,
-                                         const int8_t* q, uint32_t e, float mean, float rstd,
-                                         const void* weight, bool w_vec, int c, int valid) {
+    static constexpr int VE = Vec<T, AL>::VE, F2 = VE / 2;
+    float2 dy[F2], h[F2], g[F2];
+    __device__ __forceinline__ void make(const Vec<T, AL>& dyv, const Vec<T, AL>& xv, const int8_t* q,
+                                         uint32_t e, float rstd, float shift, const void* weight,
+                                         int w_dtype, bool w_vec, int c, int valid) {
         dyv.get(dy);
         if constexpr (CKPT) {
             decode_vec<VE>(q, scale_pow(e), h);
         } else {
             xv.get(h);
 #pragma unroll
-            for (int j = 0; j < VE; ++j) h[j] = (h[j] - mean) * rstd;
+            for (int j = 0; j < F2; ++j) h[j] = fma2(h[j], both(rstd), both(shift));
         }
-        load_row_vec<VE>(weight, p.a.w_dtype, w_vec, c, valid, 1.f, g);
+        load_row_vec<VE>(weight, w_dtype, w_vec, c, valid, 1.f, g);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) g[j] *= dy[j];
+        for (int j = 0; j < F2; ++j) g[j] = mul2(g[j], dy[j]);
+    }
+    // The columns' and the row's sums.
+    __device__ __forceinline__ void add(float2* dw, float2* db, float2& s0, float2& s1) const {
+#pragma unroll
+        for (int j = 0; j < F2; ++j) {
+            dw[j] = fma2(dy[j], h[j], dw[j]);
+            db[j] = add2(db[j], dy[j]);
+            s0 = add2(s0, g[j]);
+            s1 = fma2(g[j], h[j], s1);
+        }
+    }
+    // rstd (g - m0 - h m1), with m0 and m1 times -rstd in n0 and n1.
+    __device__ __forceinline__ void finish(float rstd, float n0, float n1, Vec<T, AL>& out) const {
+        float2 d[F2];
+#pragma unroll
+        for (int j = 0; j < F2; ++j) d[j] = fma2(h[j], both(n1), fma2(g[j], both(rstd), both(n0)));
+        out.set(d);
     }
 };
 
-// Short rows: a warp has rows of its own (eight warps a block) and reads them
-// straight from memory.
-template <typename T, int NV, bool CKPT>
+// Short rows: L lanes have rows of their own (256 / L a block at a time) and
+// read them straight from memory, one row ahead.
+template <typename T, bool AL, int L, bool CKPT>
 __global__ void __launch_bounds__(256) norm_grad_kernel(const __grid_constant__ GradLaunch p) {
-    constexpr int VE = Vec<T>::VE;
-    extern __shared__ float sums[];               // 2 x cols
+    constexpr int VE = Vec<T, AL>::VE, F2 = VE / 2, ROWS = 256 / L;
+    __shared__ float sums[2][32 * VE];
     grid_dependency_wait();
     allow_dependent_launch();
     const muon_layer_norm_grad_args& a = p.a;
     const int cols = static_cast<int>(a.cols);
     const float inv_n = 1.f / static_cast<float>(cols);
-    constexpr int step = 32 * VE;
-    const int c0 = threadIdx.x * VE;
-    float dw[NV * VE], db[NV * VE];
+    const int c = (threadIdx.x % L) * VE;
+    float2 dw[F2], db[F2];
 #pragma unroll
-    for (int i = 0; i < NV * VE; ++i) dw[i] = db[i] = 0.f;
-    for (int64_t r = blockIdx.x * 8 + threadIdx.y; r < a.rows; r += gridDim.x * 8) {
-        const T* dyp = static_cast<const T*>(a.dy) + r * a.ld_dy;
-        Vec<T> dyv[NV], xv[NV];
-        uint32_t e[NV];
-        const int8_t* q = CKPT ? a.saved.q + r * a.saved.ld_q : nullptr;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = c0 + i * step;
-            dyv[i].load(dyp + c, cols - c);
-            if constexpr (CKPT) {
-                e[i] = c < cols ? a.saved.e[r * a.saved.ld_e + c / CKPT_BLOCK] : 0u;
-            } else {
-                xv[i].load(static_cast<const T*>(a.x) + r * a.ld_x + c, cols - c);
-                e[i] = 0u;
+    for (int j = 0; j < F2; ++j) dw[j] = db[j] = both(0.f);
+    Vec<T, AL> dyv, xv;
+    uint2 q8 = make_uint2(0u, 0u);
+    uint32_t e = 0;
+    float rstd = 0.f, shift = 0.f;
+    auto fetch = [&](int64_t r) {
+        const int valid = r < a.rows ? cols - c : 0;
+        dyv.load(static_cast<const T*>(a.dy) + r * a.ld_dy + c, valid);
+        if constexpr (CKPT) {
+            if (valid > 0) {
+                const int8_t* q = a.saved.q + r * a.saved.ld_q + c;
+                if (VE == 8) q8 = *reinterpret_cast<const uint2*>(q);
+                else q8.x = *reinterpret_cast<const uint32_t*>(q);
+                e = a.saved.e[r * a.saved.ld_e + c / CKPT_BLOCK];
             }
+        } else {
+            xv.load(static_cast<const T*>(a.x) + r * a.ld_x + c, valid);
         }
-        const float rstd = a.rstd[r];
-        const float mean = CKPT ? 0.f : a.mean[r];
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = c0 + i * step;
-            if (c >= cols) break;
-            GradVec<T, CKPT> v;
-            v.make(p, dyv[i], xv[i], q + c, e[i], mean, rstd, a.weight, p.w_vec, c, cols - c);
-#pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                dw[i * VE + j] = fmaf(v.dy[j], v.h[j], dw[i * VE + j]);
-                db[i * VE + j] += v.dy[j];
-                s0 += v.g[j];
-                s1 = fmaf(v.g[j], v.h[j], s1);
-            }
+        if (r < a.rows) {
+            rstd = a.rstd[r];
+            shift = CKPT ? 0.f : -a.mean[r] * rstd;
         }
-        const float2 t = row_sum2<true>(s0, s1, nullptr);
-        const float m0 = t.x * inv_n, m1 = t.y * inv_n;
-        T* dx = static_cast<T*>(a.dx) + r * a.ld_dx;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = c0 + i * step;
-            if (c < cols) {
-                GradVec<T, CKPT> v;
-                v.make(p, dyv[i], xv[i], q + c, e[i], mean, rstd, a.weight, p.w_vec, c, cols - c);
-#pragma unroll
-                for (int j = 0; j < VE; ++j) v.g[j] = (v.g[j] - m0 - v.h[j] * m1) * rstd;
-                dyv[i].set(v.g);
-            }
-            dyv[i].store(dx + c, cols - c, c == 0);
+    };
+    const int64_t stride = int64_t(gridDim.x) * ROWS;
+    // a block's lanes walk on together: shuffles ask every lane
+    const int64_t last = (a.rows + ROWS - 1) / ROWS * ROWS;
+    int64_t r = int64_t(blockIdx.x) * ROWS + threadIdx.x / L;
+    fetch(r);
+    for (; r < last; r += stride) {
+        const int valid = r < a.rows ? cols - c : 0;
+        const float rs = rstd;
+        GradVec<T, AL, CKPT> v;
+        float2 s0 = both(0.f), s1 = both(0.f);
+        if (valid > 0) {
+            v.make(dyv, xv, reinterpret_cast<const int8_t*>(&q8), e, rstd, shift, a.weight, a.w_dtype,
+                   p.w_vec, c, AL ? VE : valid);
+            v.add(dw, db, s0, s1);
         }
+        fetch(r + stride);
+        const float2 t = row_sum2<L>(s0.x + s0.y, s1.x + s1.y, nullptr);
+        Vec<T, AL> out;
+        if (valid > 0) v.finish(rs, -t.x * inv_n * rs, -t.y * inv_n * rs, out);
+        out.store(static_cast<T*>(a.dx) + r * a.ld_dx + c, valid, c == 0);
     }
     if (!p.part) return;
-    // the eight warps' sums, in order
+    // over the warp's rows, then the eight warps' sums, in order
+#pragma unroll
+    for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < F2; ++j) {
+            dw[j].x += __shfl_xor_sync(0xffffffffu, dw[j].x, o);
+            dw[j].y += __shfl_xor_sync(0xffffffffu, dw[j].y, o);
+            db[j].x += __shfl_xor_sync(0xffffffffu, db[j].x, o);
+            db[j].y += __shfl_xor_sync(0xffffffffu, db[j].y, o);
+        }
+    const int warp = threadIdx.x >> 5;
 #pragma unroll 1
     for (int w = 0; w < 8; ++w) {
-        if (w == static_cast<int>(threadIdx.y)) {
+        if (w == warp && (threadIdx.x & 31) < L) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = c0 + i * step;
-#pragma unroll
-                for (int j = 0; j < VE; ++j) {
-                    if (c + j >= cols) break;
-                    sums[c + j] = dw[i * VE + j] + (w ? sums[c + j] : 0.f);
-                    sums[cols + c + j] = db[i * VE + j] + (w ? sums[cols + c + j] : 0.f);
-                }
+            for (int j = 0; j < F2; ++j) {
+                sums[0][c + 2 * j] = dw[j].x + (w ? sums[0][c + 2 * j] : 0.f);
+                sums[0][c + 2 * j + 1] = dw[j].y + (w ? sums[0][c + 2 * j + 1] : 0.f);
+                sums[1][c + 2 * j] = db[j].x + (w ? sums[1][c + 2 * j] : 0.f);
+                sums[1][c + 2 * j + 1] = db[j].y + (w ? sums[1][c + 2 * j + 1] : 0.f);
             }
         }
         __syncthreads();
     }
     float* out = p.part + int64_t(blockIdx.x) * 2 * p.ld_part;
-    for (int c = threadIdx.y * 32 + threadIdx.x; c < cols; c += 256) {
-        out[c] = sums[c];
-        out[p.ld_part + c] = sums[cols + c];
+    if (static_cast<int>(threadIdx.x) < cols) {
+        out[threadIdx.x] = sums[0][threadIdx.x];
+        out[p.ld_part + threadIdx.x] = sums[1][threadIdx.x];
     }
 }
 
@@ -363,10 +399,10 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const __grid_constant__ 
 // a row from the ring again instead of keeping it in registers.
 template <typename T>
 constexpr int ring_threads(int nv) { return nv < 4 ? 512 : sizeof(T) == 4 ? 1024 : 512; }
-template <typename T, int NV, bool CKPT>
+template <typename T, bool AL, int NV, bool CKPT>
 __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
     norm_grad_ring_kernel(const __grid_constant__ GradLaunch p) {
-    constexpr int VE = Vec<T>::VE;
+    constexpr int VE = Vec<T, AL>::VE, F2 = VE / 2;
     constexpr bool KEEP = NV == 1;
     extern __shared__ __align__(128) uint8_t shared[];
     uint8_t* const ring = shared + p.w_bytes;
@@ -386,16 +422,12 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // the weight, which every row needs twice (the ring leaves L1 no room)
+    // the weight, which every row needs (the ring leaves L1 no room), with
+    // zeros to the end of its last vector
     const void* w_row = a.weight ? shared : nullptr;
     if (a.weight)
-        for (int c = threadIdx.x; c < cols; c += blockDim.x) {
-            if (a.w_dtype == MUON_F32)
-                reinterpret_cast<float*>(shared)[c] = static_cast<const float*>(a.weight)[c];
-            else
-                reinterpret_cast<__nv_bfloat16*>(shared)[c] =
-                    static_cast<const __nv_bfloat16*>(a.weight)[c];
-        }
+        for (int c = threadIdx.x; c < (cols + 7) / 8 * 8; c += blockDim.x)
+            store_any(shared, a.w_dtype, c, c < cols ? load_any(a.weight, a.w_dtype, c) : 0.f);
     __syncthreads();
     const T* dy0 = static_cast<const T*>(a.dy);
     const T* x0 = static_cast<const T*>(a.x);
@@ -412,9 +444,9 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
     };
     if (threadIdx.x == 0)
         for (int s = 0; s < stages; ++s) load(blockIdx.x + int64_t(s) * gridDim.x, s);
-    float dw[NV * VE], db[NV * VE];
+    float2 dw[NV * F2], db[NV * F2];
 #pragma unroll
-    for (int i = 0; i < NV * VE; ++i) dw[i] = db[i] = 0.f;
+    for (int i = 0; i < NV * F2; ++i) dw[i] = db[i] = both(0.f);
     int odd = 0, stage = 0;
     uint32_t phase = 0;
     uint32_t e_next[NV];
@@ -433,7 +465,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
     };
     fetch(blockIdx.x);
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, odd ^= 1) {
-        const float rstd = rstd_next, mean = mean_next;
+        const float rstd = rstd_next, shift = -mean_next * rstd_next;
         uint32_t e[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) e[i] = CKPT ? e_next[i] : 0u;
@@ -443,49 +475,45 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
         ptx::wait_bounded(ptx::smem_u32(&full[stage]), phase, &abort_flag, &g_norm_err,
                           p.wait_limit_ns);
         const uint8_t* at = ring + stage * p.stage_bytes;
-        const T* dy_row = reinterpret_cast<const T*>(at + Pieces::lead(dy0 + r * a.ld_dy));
-        const T* x_row = reinterpret_cast<const T*>(at + p.x_off + (CKPT ? 0 : Pieces::lead(x0 + r * a.ld_x)));
+        const T* dy_row = reinterpret_cast<const T*>(at + (AL ? 0 : Pieces::lead(dy0 + r * a.ld_dy)));
+        const T* x_row = reinterpret_cast<const T*>(
+            at + p.x_off + (AL || CKPT ? 0 : Pieces::lead(x0 + r * a.ld_x)));
         const int8_t* q_row = reinterpret_cast<const int8_t*>(at + p.x_off);
-        auto vec = [&](int i, GradVec<T, CKPT>& v) {
+        auto vec = [&](int i, GradVec<T, AL, CKPT>& v) {
             const int c = c0 + i * step;
-            Vec<T> dyv, xv;
+            Vec<T, AL> dyv, xv;
             dyv.load(dy_row + c, cols - c);
             if constexpr (!CKPT) xv.load(x_row + c, cols - c);
-            v.make(p, dyv, xv, q_row + c, e[i], mean, rstd, w_row, true, c, VE);
+            v.make(dyv, xv, q_row + c, e[i], rstd, shift, w_row, a.w_dtype, true, c, VE);
         };
-        GradVec<T, CKPT> kept;
-        float s0 = 0.f, s1 = 0.f;
+        GradVec<T, AL, CKPT> kept;
+        float2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (c0 + i * step >= cols) break;
-            GradVec<T, CKPT> v;
+            GradVec<T, AL, CKPT> v;
             vec(i, v);
-#pragma unroll
-            for (int j = 0; j < VE; ++j) {
-                dw[i * VE + j] = fmaf(v.dy[j], v.h[j], dw[i * VE + j]);
-                db[i * VE + j] += v.dy[j];
-                s0 += v.g[j];
-                s1 = fmaf(v.g[j], v.h[j], s1);
-            }
+            v.add(dw + i * F2, db + i * F2, s0, s1);
             if constexpr (KEEP) kept = v;
         }
-        const float2 t = row_sum2<false>(s0, s1, red[odd]);
+        const float2 t = block_sum2(s0.x + s0.y, s1.x + s1.y, red[odd]);
         // its barrier says that every thread has read the stage
         if (KEEP && threadIdx.x == 0) load(r + int64_t(stages) * gridDim.x, stage);
-        const float m0 = t.x * inv_n, m1 = t.y * inv_n;
+        const float n0 = -t.x * inv_n * rstd, n1 = -t.y * inv_n * rstd;
         T* dx = static_cast<T*>(a.dx) + r * a.ld_dx;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
-            Vec<T> out;
+            Vec<T, AL> out;
             out.raw = make_uint4(0u, 0u, 0u, 0u);
             if (c < cols) {
-                GradVec<T, CKPT> v;
-                if constexpr (KEEP) v = kept;
-                else vec(i, v);
-#pragma unroll
-                for (int j = 0; j < VE; ++j) v.g[j] = (v.g[j] - m0 - v.h[j] * m1) * rstd;
-                out.set(v.g);
+                if constexpr (KEEP) {
+                    kept.finish(rstd, n0, n1, out);
+                } else {
+                    GradVec<T, AL, CKPT> v;
+                    vec(i, v);
+                    v.finish(rstd, n0, n1, out);
+                }
             }
             out.store(dx + c, cols - c, c == 0);
         }
@@ -498,7 +526,19 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
             phase ^= 1;
         }
     }
-    if (p.part) store_parts<VE, NV>(p, c0, step, dw, db);
+    if (p.part) {
+        float* w = p.part + int64_t(blockIdx.x) * 2 * p.ld_part;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < F2; j += 2) {
+                const int c = c0 + i * step + 2 * j, u = i * F2 + j;
+                if (c >= cols) break;
+                *reinterpret_cast<float4*>(w + c) = make_float4(dw[u].x, dw[u].y, dw[u + 1].x, dw[u + 1].y);
+                *reinterpret_cast<float4*>(w + p.ld_part + c) =
+                    make_float4(db[u].x, db[u].y, db[u + 1].x, db[u + 1].y);
+            }
+    }
     __syncthreads();
     if (abort_flag && threadIdx.x == 0) {
         // copies still in flight must land before the block leaves
@@ -539,12 +579,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const __grid_constant__ G
 template <typename T>
 __device__ __forceinline__ float long_h(const muon_layer_norm_grad_args& a, int64_t r, int c,
                                         float mean, float rstd) {
-    if (a.saved.q) {
-        float h[1];
-        decode_vec<1>(a.saved.q + r * a.saved.ld_q + c,
-                      scale_pow(a.saved.e[r * a.saved.ld_e + c / CKPT_BLOCK]), h);
-        return h[0];
-    }
+    if (a.saved.q) return decode_one(a.saved, r, c);
     return (to_f32(static_cast<const T*>(a.x)[r * a.ld_x + c]) - mean) * rstd;
 }
 template <typename T>
@@ -565,7 +600,7 @@ __global__ void __launch_bounds__(1024) norm_long_dx_kernel(const __grid_constan
         s0 += g;
         s1 = fmaf(g, long_h<T>(a, r, c, mean, rstd), s1);
     }
-    const float2 t = row_sum2<false>(s0, s1, red);
+    const float2 t = block_sum2(s0, s1, red);
     const float m0 = t.x * inv_n, m1 = t.y * inv_n;
     for (int c = threadIdx.x; c < cols; c += 1024) {
         const float g = to_f32(dy[c]) * (a.weight ? load_any(a.weight, a.w_dtype, c) : 1.f);
@@ -594,7 +629,7 @@ __global__ void __launch_bounds__(256) norm_long_dw_kernel(const __grid_constant
 // How a gradient is computed; the same for every alignment.
 struct GradPlan {
     RowShape shape;
-    int stages = 0;          // > 0: through the ring; 0 and no warp: long rows
+    int stages = 0;          // > 0: through the ring; 0 and no lanes: long rows
     uint32_t x_off = 0, stage_bytes = 0, w_bytes = 0;
     size_t smem = 0;
     int parts = 1;
@@ -602,22 +637,23 @@ struct GradPlan {
 GradPlan grad_plan(const muon_layer_norm_grad_args& a) {
     GradPlan g;
     const int64_t size = a.x_dtype == MUON_F32 ? 4 : 2;
-    g.shape = row_shape(ceil_div(a.cols, 16 / size), 4, 512);
+    g.shape = row_shape(ceil_div(a.cols, 16 / size), 32, 4);
     int64_t parts;
-    if (g.shape.warp) {
-        g.smem = size_t(2) * a.cols * 4;
-        parts = ceil_div(a.rows, 8);
+    if (g.shape.lanes) {
+        parts = ceil_div(a.rows, 256 / g.shape.lanes);
         if (parts > SMS * 4) parts = SMS * 4;
     } else {
         // room for a row that starts 14 bytes into its first piece
         const int64_t dy = ceil_div(a.cols * size + 14, 16) * 16;
         const int64_t row = dy + (a.saved.q ? ceil_div(a.cols, 16) * 16 : dy);
-        const int most = g.shape.nv < 4 || size == 2 ? 512 : 1024;
-        const int per_sm = g.shape.nv < 4 ? 2 : 1;
-        // the vectors read whole: room to the end of the last one
+        // the weight's vectors are read whole: room to the end of the last one
         const int64_t w = a.weight ? ceil_div(a.cols, 8) * 8 * (a.w_dtype == MUON_F32 ? 4 : 2) : 0;
         const int64_t w_bytes = ceil_div(w, 128) * 128;
-        int64_t stages = ((per_sm == 2 ? 112 : 224) * 1024 - w_bytes) / row;
+        const int most = g.shape.nv < 4 || size == 2 ? 512 : 1024;
+        // blocks an SM: about 1024 threads, of the 64 registers that leaves
+        int64_t per_sm = g.shape.nv < 4 ? 1024 / g.shape.threads : 1;
+        if (per_sm > 8) per_sm = 8;
+        int64_t stages = (224 * 1024 / per_sm - 2048 - w_bytes) / row;
         if (stages > 8) stages = 8;
         if (g.shape.threads <= most && stages >= 1) {
             g.stages = static_cast<int>(stages);
@@ -652,19 +688,16 @@ cudaError_t launch_grad(const GradPlan& g, dim3 block, const GradLaunch& p, cuda
     return launch_kernel(KERN, dim3(g.parts), block, g.smem, s, p);
 }
 
-template <typename T, bool CKPT>
+template <typename T, bool AL, bool CKPT>
 cudaError_t grad_rows(const GradPlan& g, const GradLaunch& p, cudaStream_t s) {
     const RowShape& sh = g.shape;
-    if (sh.warp) {
-        const dim3 block(32, 8);
-        if (sh.nv == 1) return launch_grad<norm_grad_kernel<T, 1, CKPT>>(g, block, p, s);
-        if (sh.nv == 2) return launch_grad<norm_grad_kernel<T, 2, CKPT>>(g, block, p, s);
-        return launch_grad<norm_grad_kernel<T, 4, CKPT>>(g, block, p, s);
-    }
     const dim3 block(sh.threads);
-    if (sh.nv == 1) return launch_grad<norm_grad_ring_kernel<T, 1, CKPT>>(g, block, p, s);
-    if (sh.nv == 2) return launch_grad<norm_grad_ring_kernel<T, 2, CKPT>>(g, block, p, s);
-    return launch_grad<norm_grad_ring_kernel<T, 4, CKPT>>(g, block, p, s);
+    if (sh.lanes == 8) return launch_grad<norm_grad_kernel<T, AL, 8, CKPT>>(g, block, p, s);
+    if (sh.lanes == 16) return launch_grad<norm_grad_kernel<T, AL, 16, CKPT>>(g, block, p, s);
+    if (sh.lanes == 32) return launch_grad<norm_grad_kernel<T, AL, 32, CKPT>>(g, block, p, s);
+    if (sh.nv == 1) return launch_grad<norm_grad_ring_kernel<T, AL, 1, CKPT>>(g, block, p, s);
+    if (sh.nv == 2) return launch_grad<norm_grad_ring_kernel<T, AL, 2, CKPT>>(g, block, p, s);
+    return launch_grad<norm_grad_ring_kernel<T, AL, 4, CKPT>>(g, block, p, s);
 }
 
 template <typename T>
@@ -672,7 +705,10 @@ cudaError_t norm_backward(GradLaunch& p, cudaStream_t s) {
     const muon_layer_norm_grad_args& a = p.a;
     const GradPlan g = grad_plan(a);
     const unsigned cols = static_cast<unsigned>(a.cols);
-    const bool in_rows = g.shape.warp || g.stages;
+    const bool in_rows = g.shape.lanes || g.stages;
+    const bool al = a.cols % Vec<T, true>::VE == 0 && rows_on_16(a.dy, sizeof(T), a.rows, a.ld_dy) &&
+                    rows_on_16(a.dx, sizeof(T), a.rows, a.ld_dx) &&
+                    (a.saved.q || rows_on_16(a.x, sizeof(T), a.rows, a.ld_x));
     cudaError_t e = cudaSuccess;
     p.parts = g.parts;
     p.stages = g.stages;
@@ -685,7 +721,8 @@ cudaError_t norm_backward(GradLaunch& p, cudaStream_t s) {
     if (a.rows == 0) {
         p.parts = 0;
     } else if (in_rows) {
-        e = a.saved.q ? grad_rows<T, true>(g, p, s) : grad_rows<T, false>(g, p, s);
+        if (al) e = a.saved.q ? grad_rows<T, true, true>(g, p, s) : grad_rows<T, true, false>(g, p, s);
+        else e = a.saved.q ? grad_rows<T, false, true>(g, p, s) : grad_rows<T, false, false>(g, p, s);
     } else if (p.part) {
         e = launch_kernel(norm_long_dw_kernel<T>, dim3((cols + 255) / 256, g.parts), dim3(256), 0, s, p);
     }
@@ -704,7 +741,7 @@ cudaError_t norm_error_word(void** word) { return cudaGetSymbolAddress(word, g_n
 cudaError_t launch_layer_norm(const muon_layer_norm_args& a, cudaStream_t s) {
     NormLaunch p = {};
     p.a = a;
-    return a.x_dtype == MUON_F32 ? norm_forward<float>(p, s) : norm_forward<__nv_bfloat16>(p, s);
+    return a.x_dtype == MUON_F32 ? norm_forward_t<float>(p, s) : norm_forward_t<__nv_bfloat16>(p, s);
 }
 
 size_t layer_norm_grad_workspace(const muon_layer_norm_grad_args& a) {

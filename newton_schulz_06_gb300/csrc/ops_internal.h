@@ -71,6 +71,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
+// ---- two floats at a time (one instruction on sm_103a, each rounded as
+// its scalar form) ----
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+// Two bf16 numbers of a word.
+__device__ __forceinline__ float2 bf16x2_f32(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
 // ---- 16-byte vectors of VE elements at any alignment ----
 //
 // A row may start anywhere: a vector that does not lie on 16 bytes is put
@@ -99,7 +110,9 @@ __device__ __forceinline__ uint4 shift_bytes(uint4 lo, uint4 hi, uint32_t m) {
                       __funnelshift_r(w[2], w[3], b), __funnelshift_r(w[3], w[4], b));
 }
 
-template <typename T>
+//
+// AL: every row is known to start on 16 bytes and to hold whole vectors.
+template <typename T, bool AL>
 struct Vec {
     static constexpr int VE = 16 / sizeof(T);
     uint4 raw;
@@ -108,6 +121,10 @@ struct Vec {
     __device__ __forceinline__ void load(const T* p, int valid) {
         raw = make_uint4(0u, 0u, 0u, 0u);
         if (valid <= 0) return;
+        if (AL) {
+            raw = *reinterpret_cast<const uint4*>(p);
+            return;
+        }
         const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
         const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - m);
         raw = q[0];
@@ -128,29 +145,25 @@ struct Vec {
             }
         }
     }
-    __device__ __forceinline__ void get(float (&f)[VE]) const {
+    __device__ __forceinline__ void get(float2 (&f)[VE / 2]) const {
         if constexpr (sizeof(T) == 4) {
-            f[0] = __uint_as_float(raw.x);
-            f[1] = __uint_as_float(raw.y);
-            f[2] = __uint_as_float(raw.z);
-            f[3] = __uint_as_float(raw.w);
+            f[0] = make_float2(__uint_as_float(raw.x), __uint_as_float(raw.y));
+            f[1] = make_float2(__uint_as_float(raw.z), __uint_as_float(raw.w));
         } else {
-            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(w[i] << 16);
-                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
+            f[0] = bf16x2_f32(raw.x);
+            f[1] = bf16x2_f32(raw.y);
+            f[2] = bf16x2_f32(raw.z);
+            f[3] = bf16x2_f32(raw.w);
         }
     }
-    __device__ __forceinline__ void set(const float (&f)[VE]) {
+    __device__ __forceinline__ void set(const float2 (&f)[VE / 2]) {
         if constexpr (sizeof(T) == 4) {
-            raw = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                             __float_as_uint(f[3]));
+            raw = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y),
+                             __float_as_uint(f[1].x), __float_as_uint(f[1].y));
         } else {
             __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[i].x, f[i].y);
         }
     }
     // Element i of 16 bytes.
@@ -169,6 +182,10 @@ struct Vec {
     // before, and only the pieces at the ends of the warp or the row go out
     // by elements.
     __device__ __forceinline__ void store(T* p, int valid, bool row_start) const {
+        if (AL) {
+            if (valid > 0) *reinterpret_cast<uint4*>(p) = raw;
+            return;
+        }
         const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
         if (__all_sync(0xffffffffu, valid <= 0 || (m == 0 && valid >= VE))) {
             if (valid > 0) *reinterpret_cast<uint4*>(p) = raw;
@@ -219,42 +236,38 @@ struct Vec {
 // null), of which `valid` are there; vec: p lies on 16 bytes.
 template <int VE>
 __device__ __forceinline__ void load_row_vec(const void* p, int dtype, bool vec, int c, int valid,
-                                             float fill, float (&f)[VE]) {
+                                             float fill, float2 (&f)[VE / 2]) {
     if (!p) {
 #pragma unroll
-        for (int i = 0; i < VE; ++i) f[i] = fill;
+        for (int i = 0; i < VE / 2; ++i) f[i] = both(fill);
     } else if (vec && valid >= VE) {
         if (dtype == MUON_F32) {
             const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
 #pragma unroll
             for (int i = 0; i < VE / 4; ++i) {
                 const float4 a = q[i];
-                f[4 * i] = a.x;
-                f[4 * i + 1] = a.y;
-                f[4 * i + 2] = a.z;
-                f[4 * i + 3] = a.w;
+                f[2 * i] = make_float2(a.x, a.y);
+                f[2 * i + 1] = make_float2(a.z, a.w);
             }
         } else {
-            const uint2* q = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + c);
-            uint2 a[VE / 4];
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p) + c;
             if constexpr (VE == 8) {
                 const uint4 t = *reinterpret_cast<const uint4*>(q);
-                a[0] = make_uint2(t.x, t.y);
-                a[VE / 4 - 1] = make_uint2(t.z, t.w);
+                f[0] = bf16x2_f32(t.x);
+                f[1] = bf16x2_f32(t.y);
+                f[2 % (VE / 2)] = bf16x2_f32(t.z);
+                f[3 % (VE / 2)] = bf16x2_f32(t.w);
             } else {
-                a[0] = q[0];
-            }
-#pragma unroll
-            for (int i = 0; i < VE / 4; ++i) {
-                f[4 * i] = __uint_as_float(a[i].x << 16);
-                f[4 * i + 1] = __uint_as_float(a[i].x & 0xffff0000u);
-                f[4 * i + 2] = __uint_as_float(a[i].y << 16);
-                f[4 * i + 3] = __uint_as_float(a[i].y & 0xffff0000u);
+                const uint2 t = *reinterpret_cast<const uint2*>(q);
+                f[0] = bf16x2_f32(t.x);
+                f[1] = bf16x2_f32(t.y);
             }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < VE; ++i) f[i] = i < valid ? load_any(p, dtype, c + i) : 0.f;
+        for (int i = 0; i < VE / 2; ++i)
+            f[i] = make_float2(2 * i < valid ? load_any(p, dtype, c + 2 * i) : 0.f,
+                               2 * i + 1 < valid ? load_any(p, dtype, c + 2 * i + 1) : 0.f);
     }
 }
 
@@ -275,35 +288,40 @@ __device__ __forceinline__ float scale_inv(uint32_t e) {
 __device__ __forceinline__ float scale_pow(uint32_t e) {
     return __uint_as_float(e == 255u ? 0x7fc00000u : e == 0u ? 0x00400000u : e << 23);
 }
-// The multiplications by powers of two are exact (the first brings the block
-// into [-2, 2]), so this rounds once.
-__device__ __forceinline__ int encode_q(float v, uint32_t e, float inv) {
-    if (e == 255u) return 0;
-    const int q = __float2int_rn(v * inv * 64.f);
-    return max(-127, min(127, q));
+// v 2^(6 - E) rounded to nearest, ties to even, and limited; 0 where e is
+// 255 (inv is 0 then, and the limits' fminf and fmaxf pass a NaN by).  The
+// multiplications by powers of two are exact (the first brings the block into
+// [-2, 2]); adding 1.5 * 2^23 rounds to whole numbers, which the float's low
+// byte then holds.
+__device__ __forceinline__ uint32_t encode_q(float v, uint32_t e, float inv) {
+    const float x = fmaxf(fminf(v * inv * 64.f, 127.f), -127.f);
+    return e == 255u ? 0u : __float_as_uint(x + 12582912.f);
 }
 
 // VE values from q, whose block's power of two is p (exact).
 template <int VE>
-__device__ __forceinline__ void decode_vec(const int8_t* q, float p, float (&f)[VE]) {
-    const float s = p * 0.015625f;
-    if constexpr (VE == 1) {
-        f[0] = static_cast<float>(*q) * s;
+__device__ __forceinline__ void decode_vec(const int8_t* q, float p, float2 (&f)[VE / 2]) {
+    const float2 s = both(p * 0.015625f);
+    uint32_t w[VE / 4];
+    if constexpr (VE == 8) {
+        const uint2 t = *reinterpret_cast<const uint2*>(q);
+        w[0] = t.x ^ 0x80808080u;
+        w[VE / 4 - 1] = t.y ^ 0x80808080u;
     } else {
-        uint32_t w[VE / 4];
-        if constexpr (VE == 8) {
-            const uint2 t = *reinterpret_cast<const uint2*>(q);
-            w[0] = t.x;
-            w[VE / 4 - 1] = t.y;
-        } else {
-            w[0] = *reinterpret_cast<const uint32_t*>(q);
-        }
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-            // a byte b = q + 128 in the last byte of 2^23 is the float 2^23 + b
-            f[i] = (__uint_as_float(__byte_perm(w[i / 4] ^ 0x80808080u, 0x4B000000u, 0x7540u + i % 4)) -
-                    8388736.f) * s;
+        w[0] = *reinterpret_cast<const uint32_t*>(q) ^ 0x80808080u;
     }
+#pragma unroll
+    for (int i = 0; i < VE / 2; ++i) {
+        // a byte b = q + 128 in the last byte of 2^23 is the float 2^23 + b
+        const float2 v = make_float2(
+            __uint_as_float(__byte_perm(w[i / 2], 0x4B000000u, 0x7540u + 2 * i % 4)),
+            __uint_as_float(__byte_perm(w[i / 2], 0x4B000000u, 0x7541u + 2 * i % 4)));
+        f[i] = mul2(add2(v, both(-8388736.f)), s);
+    }
+}
+__device__ __forceinline__ float decode_one(const muon_ckpt8& s, int64_t r, int64_t c) {
+    return static_cast<float>(s.q[r * s.ld_q + c]) * 0.015625f *
+           scale_pow(s.e[r * s.ld_e + c / CKPT_BLOCK]);
 }
 
 // Encodes VE consecutive values of a row whose block of 32 lies in 32 / VE
@@ -312,32 +330,24 @@ __device__ __forceinline__ void decode_vec(const int8_t* q, float p, float (&f)[
 // those with !write only take part in the maximum.
 template <int VE>
 __device__ __forceinline__ void encode_vec(const muon_ckpt8& s, int64_t r, int c, bool write,
-                                           const float (&f)[VE]) {
+                                           const float2 (&f)[VE / 2]) {
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) top = max(top, mag_bits(f[i]));
-    if constexpr (VE == 1) {
-        top = __reduce_max_sync(0xffffffffu, top);
-    } else {
+    for (int i = 0; i < VE / 2; ++i) top = max(top, max(mag_bits(f[i].x), mag_bits(f[i].y)));
 #pragma unroll
-        for (int o = 1; o < CKPT_BLOCK / VE; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
+    for (int o = 1; o < CKPT_BLOCK / VE; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (!write) return;
     const uint32_t e = scale_byte(top);
     const float inv = scale_inv(e);
     int8_t* q = s.q + r * s.ld_q + c;
-    if constexpr (VE == 1) {
-        *q = static_cast<int8_t>(encode_q(f[0], e, inv));
-    } else {
-        uint32_t w[VE / 4];
+    uint32_t w[VE / 4];
 #pragma unroll
-        for (int i = 0; i < VE / 4; ++i)
-            w[i] = (encode_q(f[4 * i], e, inv) & 0xff) | (encode_q(f[4 * i + 1], e, inv) & 0xff) << 8 |
-                   (encode_q(f[4 * i + 2], e, inv) & 0xff) << 16 |
-                   static_cast<uint32_t>(encode_q(f[4 * i + 3], e, inv)) << 24;
-        if constexpr (VE == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[VE / 4 - 1]);
-        else *reinterpret_cast<uint32_t*>(q) = w[0];
-    }
+    for (int i = 0; i < VE / 4; ++i)
+        w[i] = __byte_perm(__byte_perm(encode_q(f[2 * i].x, e, inv), encode_q(f[2 * i].y, e, inv), 0x0040),
+                           __byte_perm(encode_q(f[2 * i + 1].x, e, inv),
+                                       encode_q(f[2 * i + 1].y, e, inv), 0x0040), 0x5410);
+    if constexpr (VE == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[VE / 4 - 1]);
+    else *reinterpret_cast<uint32_t*>(q) = w[0];
     if ((c & (CKPT_BLOCK - 1)) == 0) s.e[r * s.ld_e + c / CKPT_BLOCK] = static_cast<uint8_t>(e);
 }
 
