@@ -12,7 +12,7 @@
 // Each block leaves one row of partial sums, which a second kernel adds up in
 // order.
 #include "ops_internal.h"
-#include "tc_ptx.cuh"
+#include "tc_wait.cuh"
 
 namespace muon {
 namespace ops {
@@ -22,15 +22,35 @@ constexpr int SMS = 152;
 __device__ int g_norm_err;             // DEV_ERR_TIMEOUT once a bounded wait ran out
 
 // Sums of two values over a block, in a fixed order, returned to all threads;
-// buf alternates between two, so that one barrier a sum is enough.
+// buf alternates between two, so that one barrier a sum is enough.  Up to 16
+// warps, half the lanes add up one value and half the other, which halves the
+// shuffles (they were a quarter of the backward kernel's instructions).
 __device__ __forceinline__ float2 block_sum2(float a, float b, float2* buf) {
-    a = warp_sum(a);
-    b = warp_sum(b);
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const bool hi = lane & 16;
+    float v = hi ? b : a;
+    v += __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    float* flat = reinterpret_cast<float*>(buf);
+    if ((lane & 15) == 0) flat[2 * (threadIdx.x >> 5) + (lane >> 4)] = v;
     __syncthreads();
-    const float2 t = lane < static_cast<int>(blockDim.x >> 5) ? buf[lane] : make_float2(0.f, 0.f);
+    if (warps <= 16) {
+        float t = (lane & 15) < warps ? flat[2 * (lane & 15) + (lane >> 4)] : 0.f;
+#pragma unroll
+        for (int o = 8; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        return make_float2(__shfl_sync(0xffffffffu, t, 0), __shfl_sync(0xffffffffu, t, 16));
+    }
+    const float2 t = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
     return make_float2(warp_sum(t.x), warp_sum(t.y));
+}
+__device__ __forceinline__ float block_sum(float a, float2* buf) {
+    const int lane = threadIdx.x & 31;
+    a = warp_sum(a);
+    float* flat = reinterpret_cast<float*>(buf);
+    if (lane == 0) flat[threadIdx.x >> 5] = a;
+    __syncthreads();
+    return warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? flat[lane] : 0.f);
 }
 // The same over the L threads of a row: neighbouring lanes (L = 8, 16, 32),
 // or the block (L = 0).
@@ -53,7 +73,44 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* buf) {
 struct NormLaunch {
     muon_layer_norm_args a;
     int32_t w_vec;           // weight and bias allow 16-byte loads
+    int32_t stages;          // rows of the ring in shared memory (norm_ring_kernel)
+    uint32_t stage_bytes;
+    unsigned long long wait_limit_ns;
 };
+
+// The aligned 16-byte pieces that hold `n` bytes from p.
+struct Pieces {
+    const char* first;
+    uint32_t bytes;
+    static __device__ __forceinline__ uint32_t lead(const void* p) {
+        return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+    }
+    __device__ __forceinline__ Pieces(const void* p, uint32_t n)
+        : first(static_cast<const char*>(p) - lead(p)), bytes((lead(p) + n + 15u) & ~15u) {}
+};
+
+// Waits until the ring's stage is full.  A wait that runs out raises the
+// flag, which ends the later ones at once; the rows that follow hold nothing
+// of use then.
+__device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t phase, int* abort_flag,
+                                          unsigned long long limit_ns) {
+    wait_soon(ptx::smem_u32(bar), phase, abort_flag, &g_norm_err, limit_ns);
+}
+// After an abort: copies still in flight must land before the block leaves.
+__device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int64_t rows,
+                                           unsigned long long limit_ns) {
+    const int64_t mine = (rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+    for (int s = 0; s < stages && s < mine; ++s)
+        ptx::wait_quiet(ptx::smem_u32(&full[s]),
+                        static_cast<uint32_t>((mine - s + stages - 1) / stages - 1) & 1u, limit_ns);
+}
+constexpr int RING_MAX = 8;
+// Threads that a block of the ring kernels may have.
+template <typename T>
+constexpr int ring_threads(int nv) { return nv == 4 && sizeof(T) == 4 ? 1024 : 512; }
+// Blocks of that size an SM holds: 64 registers a thread, 128 with four
+// vectors of bf16.
+constexpr int ring_blocks(int nv) { return nv < 4 ? 2 : 1; }
 
 // A row in the registers of L lanes (256 / L rows a block) or of a block
 // (L = 0): NV vectors a thread.
@@ -84,7 +141,7 @@ __global__ void __launch_bounds__(L ? 256 : 1024)
 #pragma unroll
         for (int j = 0; j < F2; ++j) s = add2(s, v[j]);
     }
-    float mean = row_sum2<L>(s.x + s.y, 0.f, red[0]).x * inv_n;
+    float mean = (L ? row_sum2<L>(s.x + s.y, 0.f, nullptr).x : block_sum(s.x + s.y, red[0])) * inv_n;
     float2 d1 = both(0.f), d2 = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -140,6 +197,123 @@ __global__ void __launch_bounds__(L ? 256 : 1024)
         }
         raw[i].store(y + c, valid, c == 0);
     }
+}
+
+// Many longer rows: blocks that stay, with the weight and the bias of their
+// threads' columns in registers and a ring of rows in shared memory that bulk
+// copies fill ahead of them.
+template <typename T, bool AL, int NV, bool CKPT>
+__global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
+    norm_ring_kernel(const __grid_constant__ NormLaunch p) {
+    constexpr int VE = Vec<T, AL>::VE, F2 = VE / 2;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float2 red[2][32];
+    __shared__ uint64_t full[RING_MAX];
+    __shared__ int abort_flag;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const muon_layer_norm_args& a = p.a;
+    const int cols = static_cast<int>(a.cols);
+    const float inv_n = 1.f / static_cast<float>(cols);
+    const int step = blockDim.x * VE;
+    const int c0 = threadIdx.x * VE;
+    const int stages = p.stages;
+    const T* x0 = static_cast<const T*>(a.x);
+    auto load = [&](int64_t r, int s) {
+        if (r >= a.rows) return;
+        const Pieces x(x0 + r * a.ld_x, cols * sizeof(T));
+        ptx::mbar_expect_tx(ptx::smem_u32(&full[s]), x.bytes);
+        bulk_load(ptx::smem_u32(ring) + s * p.stage_bytes, x.first, x.bytes, ptx::smem_u32(&full[s]));
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int s = 0; s < stages; ++s) load(blockIdx.x + int64_t(s) * gridDim.x, s);
+    }
+    float2 w[NV][F2], b[NV][F2];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = c0 + i * step;
+        load_row_vec<VE>(a.weight, a.w_dtype, p.w_vec, c, cols - c, 1.f, w[i]);
+        load_row_vec<VE>(a.bias, a.w_dtype, p.w_vec, c, cols - c, 0.f, b[i]);
+    }
+    const int padded = (cols + CKPT_BLOCK - 1) / CKPT_BLOCK * CKPT_BLOCK;
+    __syncthreads();
+    int stage = 0;
+    uint32_t phase = 0;
+    T* y = static_cast<T*>(a.y) + blockIdx.x * a.ld_y + c0;
+    const int64_t y_step = gridDim.x * a.ld_y;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, y += y_step) {
+        ring_wait(&full[stage], phase, &abort_flag, p.wait_limit_ns);
+        const T* x = reinterpret_cast<const T*>(ring + stage * p.stage_bytes +
+                                                (AL ? 0 : Pieces::lead(x0 + r * a.ld_x)));
+        float2 v[NV][F2];
+        float2 s = both(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            Vec<T, AL> raw;
+            raw.load(x + c0 + i * step, cols - c0 - i * step);
+            raw.get(v[i]);
+#pragma unroll
+            for (int j = 0; j < F2; ++j) s = add2(s, v[i][j]);
+        }
+        float mean = block_sum(s.x + s.y, red[0]) * inv_n;
+        // its barrier says that every thread has read the stage
+        if (threadIdx.x == 0) load(r + int64_t(stages) * gridDim.x, stage);
+        float2 d1 = both(0.f), d2 = both(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int valid = cols - c0 - i * step;
+            if (valid <= 0) break;
+#pragma unroll
+            for (int j = 0; j < F2; ++j) {
+                float2 d = add2(v[i][j], both(-mean));
+                if (!AL) {
+                    if (2 * j >= valid) d.x = 0.f;
+                    if (2 * j + 1 >= valid) d.y = 0.f;
+                }
+                d1 = add2(d1, d);
+                d2 = fma2(d, d, d2);
+            }
+        }
+        const float2 t = block_sum2(d1.x + d1.y, d2.x + d2.y, red[1]);
+        const float off = t.x * inv_n;
+        const float var = fmaxf(fmaf(-off, off, t.y * inv_n), 0.f) + (t.y != t.y ? t.y : 0.f);
+        mean += off;
+        const float rstd = 1.f / sqrtf(var + a.eps);
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[r] = mean;
+            if (a.rstd) a.rstd[r] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = c0 + i * step, valid = cols - c;
+            float2 h[F2];
+#pragma unroll
+            for (int j = 0; j < F2; ++j) h[j] = mul2(add2(v[i][j], both(-mean)), both(rstd));
+            if constexpr (CKPT) {
+                // past the row's end the checkpoint holds zeros
+#pragma unroll
+                for (int j = 0; j < F2; ++j) {
+                    if (AL ? valid <= 0 : 2 * j >= valid) h[j].x = 0.f;
+                    if (AL ? valid <= 0 : 2 * j + 1 >= valid) h[j].y = 0.f;
+                }
+                encode_vec<VE>(a.saved, r, c, c < padded, h);
+            }
+#pragma unroll
+            for (int j = 0; j < F2; ++j) h[j] = fma2(h[j], w[i][j], b[i][j]);
+            Vec<T, AL> out;
+            out.set(h);
+            out.store(y + i * step, valid, c == 0);
+        }
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+    __syncthreads();
+    if (abort_flag && threadIdx.x == 0) ring_drain(full, stages, a.rows, p.wait_limit_ns);
 }
 
 // Rows that do not fit a block's registers: three sweeps over the row.
@@ -207,8 +381,58 @@ RowShape row_shape(int64_t vectors, int most_lanes, int max_nv) {
     return s;
 }
 
+// Lets a kernel have `bytes` of dynamic shared memory.
+template <auto KERN>
+cudaError_t allow_smem(size_t bytes) {
+    if (bytes <= 40 * 1024) return cudaSuccess;   // with the static arrays, below the default
+    static int set[64] = {0};          // the most asked for so far, by device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && set[dev] >= static_cast<int>(bytes)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(bytes));
+    if (e == cudaSuccess && dev >= 0 && dev < 64) set[dev] = static_cast<int>(bytes);
+    return e;
+}
+
+template <void (*KERN)(NormLaunch)>
+cudaError_t launch_norm_ring(int grid, int threads, size_t smem, const NormLaunch& p, cudaStream_t s) {
+    const cudaError_t e = allow_smem<KERN>(smem);
+    return e != cudaSuccess ? e : launch_kernel(KERN, dim3(grid), dim3(threads), smem, s, p);
+}
+
+// Rows for which blocks that stay pay: two a block and more.
 template <typename T, bool AL>
-cudaError_t norm_forward(const NormLaunch& p, cudaStream_t s) {
+cudaError_t norm_forward_ring(NormLaunch& p, cudaStream_t s, bool* done) {
+    const RowShape sh = row_shape(ceil_div(p.a.cols, Vec<T, AL>::VE), 128, 4);
+    *done = false;
+    if (sh.lanes || sh.threads > ring_threads<T>(sh.nv)) return cudaSuccess;
+    int per_sm = sh.nv < 4 ? 1024 / sh.threads : 1;
+    if (per_sm > 8) per_sm = 8;
+    if (p.a.rows < 2 * SMS * per_sm) return cudaSuccess;
+    p.stage_bytes = static_cast<uint32_t>(ceil_div(p.a.cols * int64_t(sizeof(T)) + 14, 16) * 16);
+    int64_t stages = (224 * 1024 / per_sm - 2048) / p.stage_bytes;
+    p.stages = static_cast<int32_t>(stages > RING_MAX ? RING_MAX : stages);
+    if (p.stages < 2) return cudaSuccess;
+    p.wait_limit_ns = wait_limit_ns();
+    *done = true;
+    const size_t smem = size_t(p.stage_bytes) * p.stages;
+    const int grid = SMS * per_sm;
+    if (p.a.saved.q) {
+        if (sh.nv == 1) return launch_norm_ring<norm_ring_kernel<T, AL, 1, true>>(grid, sh.threads, smem, p, s);
+        if (sh.nv == 2) return launch_norm_ring<norm_ring_kernel<T, AL, 2, true>>(grid, sh.threads, smem, p, s);
+        return launch_norm_ring<norm_ring_kernel<T, AL, 4, true>>(grid, sh.threads, smem, p, s);
+    }
+    if (sh.nv == 1) return launch_norm_ring<norm_ring_kernel<T, AL, 1, false>>(grid, sh.threads, smem, p, s);
+    if (sh.nv == 2) return launch_norm_ring<norm_ring_kernel<T, AL, 2, false>>(grid, sh.threads, smem, p, s);
+    return launch_norm_ring<norm_ring_kernel<T, AL, 4, false>>(grid, sh.threads, smem, p, s);
+}
+
+template <typename T, bool AL>
+cudaError_t norm_forward(NormLaunch& p, cudaStream_t s) {
+    bool done;
+    const cudaError_t e = norm_forward_ring<T, AL>(p, s, &done);
+    if (done || e != cudaSuccess) return e;
     const RowShape sh = row_shape(ceil_div(p.a.cols, Vec<T, AL>::VE), 128, 8);
     const unsigned rows = static_cast<unsigned>(p.a.rows);
     const dim3 block(sh.threads);
@@ -251,26 +475,15 @@ struct GradLaunch {
     unsigned long long wait_limit_ns;
 };
 
-// The aligned 16-byte pieces that hold `n` bytes from p.
-struct Pieces {
-    const char* first;
-    uint32_t bytes;
-    static __device__ __forceinline__ uint32_t lead(const void* p) {
-        return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
-    }
-    __device__ __forceinline__ Pieces(const void* p, uint32_t n)
-        : first(static_cast<const char*>(p) - lead(p)), bytes((lead(p) + n + 15u) & ~15u) {}
-};
-
-// One vector of a row: dy, h and g = dy * weight.  CKPT: h comes from q and
+// One vector of a row: dy, h and g = dy * weight (the caller puts the weight
+// into g).  CKPT: h comes from q and
 // its scale byte e, else from x as x * rstd + shift (shift = -mean * rstd).
 template <typename T, bool AL, bool CKPT>
 struct GradVec {
     static constexpr int VE = Vec<T, AL>::VE, F2 = VE / 2;
     float2 dy[F2], h[F2], g[F2];
     __device__ __forceinline__ void make(const Vec<T, AL>& dyv, const Vec<T, AL>& xv, const int8_t* q,
-                                         uint32_t e, float rstd, float shift, const void* weight,
-                                         int w_dtype, bool w_vec, int c, int valid) {
+                                         uint32_t e, float rstd, float shift) {
         dyv.get(dy);
         if constexpr (CKPT) {
             decode_vec<VE>(q, scale_pow(e), h);
@@ -279,7 +492,7 @@ struct GradVec {
 #pragma unroll
             for (int j = 0; j < F2; ++j) h[j] = fma2(h[j], both(rstd), both(shift));
         }
-        load_row_vec<VE>(weight, w_dtype, w_vec, c, valid, 1.f, g);
+        // g holds the weight's vector
 #pragma unroll
         for (int j = 0; j < F2; ++j) g[j] = mul2(g[j], dy[j]);
     }
@@ -350,8 +563,8 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const __grid_constant__ 
         GradVec<T, AL, CKPT> v;
         float2 s0 = both(0.f), s1 = both(0.f);
         if (valid > 0) {
-            v.make(dyv, xv, reinterpret_cast<const int8_t*>(&q8), e, rstd, shift, a.weight, a.w_dtype,
-                   p.w_vec, c, AL ? VE : valid);
+            load_row_vec<VE>(a.weight, a.w_dtype, p.w_vec, c, AL ? VE : valid, 1.f, v.g);
+            v.make(dyv, xv, reinterpret_cast<const int8_t*>(&q8), e, rstd, shift);
             v.add(dw, db, s0, s1);
         }
         fetch(r + stride);
@@ -397,17 +610,15 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const __grid_constant__ 
 // 16-byte pieces that hold a row, so that memory is kept busy whatever the
 // registers hold.  With more than one vector a thread, the second sweep takes
 // a row from the ring again instead of keeping it in registers.
-template <typename T>
-constexpr int ring_threads(int nv) { return nv < 4 ? 512 : sizeof(T) == 4 ? 1024 : 512; }
 template <typename T, bool AL, int NV, bool CKPT>
-__global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
+__global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     norm_grad_ring_kernel(const __grid_constant__ GradLaunch p) {
     constexpr int VE = Vec<T, AL>::VE, F2 = VE / 2;
     constexpr bool KEEP = NV == 1;
     extern __shared__ __align__(128) uint8_t shared[];
     uint8_t* const ring = shared + p.w_bytes;
     __shared__ float2 red[2][32];
-    __shared__ uint64_t full[8];
+    __shared__ uint64_t full[RING_MAX];
     __shared__ int abort_flag;
     grid_dependency_wait();
     allow_dependent_launch();
@@ -422,12 +633,26 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // the weight, which every row needs (the ring leaves L1 no room), with
-    // zeros to the end of its last vector
-    const void* w_row = a.weight ? shared : nullptr;
+    // the weight in fp32, which every row needs (the ring leaves L1 no room),
+    // with zeros to the end of its last vector; beside bf16 rows in two
+    // planes, the first and the last four values of the vectors, so that
+    // neighbouring threads read neighbouring 16 bytes
+    const int w_vecs = (cols + VE - 1) / VE;
     if (a.weight)
-        for (int c = threadIdx.x; c < (cols + 7) / 8 * 8; c += blockDim.x)
-            store_any(shared, a.w_dtype, c, c < cols ? load_any(a.weight, a.w_dtype, c) : 0.f);
+        for (int c = threadIdx.x; c < w_vecs * VE; c += blockDim.x) {
+            const int plane = VE == 8 ? c / 4 % 2 : 0;
+            reinterpret_cast<float*>(shared)[(plane * w_vecs + c / VE) * 4 + c % 4] =
+                c < cols ? load_any(a.weight, a.w_dtype, c) : 0.f;
+        }
+    auto w_vec = [&](int v, float2 (&w)[F2]) {
+#pragma unroll
+        for (int h = 0; h < VE / 4; ++h) {
+            const float4 f = a.weight ? reinterpret_cast<const float4*>(shared)[h * w_vecs + v]
+                                      : make_float4(1.f, 1.f, 1.f, 1.f);
+            w[2 * h] = make_float2(f.x, f.y);
+            w[2 * h + 1] = make_float2(f.z, f.w);
+        }
+    };
     __syncthreads();
     const T* dy0 = static_cast<const T*>(a.dy);
     const T* x0 = static_cast<const T*>(a.x);
@@ -451,29 +676,37 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
     uint32_t phase = 0;
     uint32_t e_next[NV];
     float rstd_next = 0.f, mean_next = 0.f;
-    auto fetch = [&](int64_t r) {
-        if (r >= a.rows) return;
-        rstd_next = a.rstd[r];
+    // pointers walk along with the rows (a 64-bit product a tensor and row
+    // costs as much as the row's arithmetic)
+    const float* rstd_at = a.rstd + blockIdx.x;
+    const float* mean_at = CKPT ? nullptr : a.mean + blockIdx.x;
+    const uint8_t* e_at = CKPT ? a.saved.e + blockIdx.x * a.saved.ld_e + c0 / CKPT_BLOCK : nullptr;
+    const int64_t e_step = CKPT ? gridDim.x * a.saved.ld_e : 0;
+    T* dx = static_cast<T*>(a.dx) + blockIdx.x * a.ld_dx + c0;
+    const int64_t dx_step = gridDim.x * a.ld_dx;
+    auto fetch = [&]() {
+        rstd_next = *rstd_at;
+        rstd_at += gridDim.x;
         if constexpr (CKPT) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (c0 + i * step < cols)
-                    e_next[i] = a.saved.e[r * a.saved.ld_e + (c0 + i * step) / CKPT_BLOCK];
+                if (c0 + i * step < cols) e_next[i] = e_at[i * (step / CKPT_BLOCK)];
+            e_at += e_step;
         } else {
-            mean_next = a.mean[r];
+            mean_next = *mean_at;
+            mean_at += gridDim.x;
         }
     };
-    fetch(blockIdx.x);
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, odd ^= 1) {
+    fetch();
+    int left = static_cast<int>((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
+    int64_t r = blockIdx.x;
+    for (; left > 0; --left, r += gridDim.x, dx += dx_step, odd ^= 1) {
         const float rstd = rstd_next, shift = -mean_next * rstd_next;
         uint32_t e[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) e[i] = CKPT ? e_next[i] : 0u;
-        fetch(r + gridDim.x);
-        // a wait that runs out raises the flag, which ends the later ones at
-        // once; the rows that follow hold nothing of use then
-        ptx::wait_bounded(ptx::smem_u32(&full[stage]), phase, &abort_flag, &g_norm_err,
-                          p.wait_limit_ns);
+        if (left > 1) fetch();
+        ring_wait(&full[stage], phase, &abort_flag, p.wait_limit_ns);
         const uint8_t* at = ring + stage * p.stage_bytes;
         const T* dy_row = reinterpret_cast<const T*>(at + (AL ? 0 : Pieces::lead(dy0 + r * a.ld_dy)));
         const T* x_row = reinterpret_cast<const T*>(
@@ -484,7 +717,8 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
             Vec<T, AL> dyv, xv;
             dyv.load(dy_row + c, cols - c);
             if constexpr (!CKPT) xv.load(x_row + c, cols - c);
-            v.make(dyv, xv, q_row + c, e[i], rstd, shift, w_row, a.w_dtype, true, c, VE);
+            w_vec(threadIdx.x + i * blockDim.x, v.g);
+            v.make(dyv, xv, q_row + c, e[i], rstd, shift);
         };
         GradVec<T, AL, CKPT> kept;
         float2 s0 = both(0.f), s1 = both(0.f);
@@ -500,7 +734,6 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
         // its barrier says that every thread has read the stage
         if (KEEP && threadIdx.x == 0) load(r + int64_t(stages) * gridDim.x, stage);
         const float n0 = -t.x * inv_n * rstd, n1 = -t.y * inv_n * rstd;
-        T* dx = static_cast<T*>(a.dx) + r * a.ld_dx;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
@@ -515,7 +748,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
                     v.finish(rstd, n0, n1, out);
                 }
             }
-            out.store(dx + c, cols - c, c == 0);
+            out.store(dx + i * step, cols - c, c == 0);
         }
         if (!KEEP) {
             __syncthreads();
@@ -540,14 +773,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), NV < 4 ? 2 : 1)
             }
     }
     __syncthreads();
-    if (abort_flag && threadIdx.x == 0) {
-        // copies still in flight must land before the block leaves
-        const int64_t mine = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
-        for (int s = 0; s < stages && s < mine; ++s)
-            ptx::wait_quiet(ptx::smem_u32(&full[s]),
-                            static_cast<uint32_t>((mine - s + stages - 1) / stages - 1) & 1u,
-                            p.wait_limit_ns);
-    }
+    if (abort_flag && threadIdx.x == 0) ring_drain(full, stages, a.rows, p.wait_limit_ns);
 }
 
 // The partial sums of 32 columns in a block, 32 of them at a time.
@@ -647,14 +873,13 @@ GradPlan grad_plan(const muon_layer_norm_grad_args& a) {
         const int64_t dy = ceil_div(a.cols * size + 14, 16) * 16;
         const int64_t row = dy + (a.saved.q ? ceil_div(a.cols, 16) * 16 : dy);
         // the weight's vectors are read whole: room to the end of the last one
-        const int64_t w = a.weight ? ceil_div(a.cols, 8) * 8 * (a.w_dtype == MUON_F32 ? 4 : 2) : 0;
-        const int64_t w_bytes = ceil_div(w, 128) * 128;
-        const int most = g.shape.nv < 4 || size == 2 ? 512 : 1024;
+        const int64_t w_bytes = a.weight ? ceil_div(a.cols, 32) * 32 * 4 : 0;
+        const int most = size == 4 ? ring_threads<float>(g.shape.nv) : ring_threads<__nv_bfloat16>(g.shape.nv);
         // blocks an SM: about 1024 threads, of the 64 registers that leaves
         int64_t per_sm = g.shape.nv < 4 ? 1024 / g.shape.threads : 1;
         if (per_sm > 8) per_sm = 8;
         int64_t stages = (224 * 1024 / per_sm - 2048 - w_bytes) / row;
-        if (stages > 8) stages = 8;
+        if (stages > RING_MAX) stages = RING_MAX;
         if (g.shape.threads <= most && stages >= 1) {
             g.stages = static_cast<int>(stages);
             g.x_off = static_cast<uint32_t>(dy);
@@ -673,19 +898,8 @@ GradPlan grad_plan(const muon_layer_norm_grad_args& a) {
 
 template <void (*KERN)(GradLaunch)>
 cudaError_t launch_grad(const GradPlan& g, dim3 block, const GradLaunch& p, cudaStream_t s) {
-    if (g.smem > 40 * 1024) {          // with the static arrays, above the default
-        static int set[64] = {0};      // the most asked for so far, by device
-        int dev = 0;
-        cudaGetDevice(&dev);
-        const int bytes = static_cast<int>(g.smem);
-        if (dev < 0 || dev >= 64 || set[dev] < bytes) {
-            const cudaError_t e =
-                cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-            if (e != cudaSuccess) return e;
-            if (dev >= 0 && dev < 64) set[dev] = bytes;
-        }
-    }
-    return launch_kernel(KERN, dim3(g.parts), block, g.smem, s, p);
+    const cudaError_t e = allow_smem<KERN>(g.smem);
+    return e != cudaSuccess ? e : launch_kernel(KERN, dim3(g.parts), block, g.smem, s, p);
 }
 
 template <typename T, bool AL, bool CKPT>

@@ -24,7 +24,7 @@
 #include <cudaTypedefs.h>
 
 #include "ops_internal.h"
-#include "tc_ptx.cuh"
+#include "tc_wait.cuh"
 
 namespace muon {
 namespace ops {
@@ -313,9 +313,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                 const int a0 = x.n0 + static_cast<int>(rank) * 128;
                 const int b0 = x.k0 + static_cast<int>(rank) * 128;
                 for (int s = 0; s < x.steps; ++s) {
-                    if (!mbar_try_wait(smem_u32(&empty_bar[stage]), phase ^ 1) &&
-                        !wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1, abort_flag,
-                                      &g_ops_err, limit)) {
+                    if (!wait_soon(smem_u32(&empty_bar[stage]), phase ^ 1, abort_flag, &g_ops_err,
+                                   limit)) {
                         ok = false;
                         break;
                     }
@@ -358,8 +357,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                 for (int s0 = 0; ok && s0 < x.steps; s0 += chunk) {
                     const uint32_t acc = s0 ? first ^ 1 : first;
                     const uint32_t use = acc ? uses[1]++ : uses[0]++;
-                    if (!wait_bounded(smem_u32(&tempty_bar[acc]), (use & 1) ^ 1, abort_flag,
-                                      &g_ops_err, limit)) {
+                    if (!wait_soon(smem_u32(&tempty_bar[acc]), (use & 1) ^ 1, abort_flag, &g_ops_err,
+                                   limit)) {
                         ok = false;
                         break;
                     }
@@ -367,9 +366,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                     const uint32_t d_tmem = tmem_base + acc * 256;
                     const int s1 = min(s0 + chunk, x.steps);
                     for (int s = s0; s < s1; ++s) {
-                        if (!mbar_try_wait(smem_u32(&ready_bar[stage]), phase) &&
-                            !wait_bounded(smem_u32(&ready_bar[stage]), phase, abort_flag,
-                                          &g_ops_err, limit)) {
+                        if (!wait_soon(smem_u32(&ready_bar[stage]), phase, abort_flag, &g_ops_err,
+                                       limit)) {
                             ok = false;
                             break;
                         }
@@ -444,8 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                     const int su = s + u * W_DEC_GROUPS;
                     if (su >= x.steps) break;
                     const uint32_t fb = smem_u32(&full_bar[stage]);
-                    const bool got = mbar_try_wait(fb, phase) ||
-                                     wait_bounded(fb, phase, abort_flag, &g_ops_err, limit);
+                    const bool got = wait_soon(fb, phase, abort_flag, &g_ops_err, limit);
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
@@ -494,8 +491,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         bool ok = true;
         auto wait_full = [&](uint32_t acc) {
             const uint32_t use = acc ? uses[1]++ : uses[0]++;
-            const bool got = wait_bounded(smem_u32(&tfull_bar[acc]), use & 1, abort_flag,
-                                          &g_ops_err, limit);
+            const bool got = wait_soon(smem_u32(&tfull_bar[acc]), use & 1, abort_flag, &g_ops_err,
+                                       limit);
             if (!__all_sync(0xffffffffu, got)) return false;
             tc_fence_after();
             return true;
