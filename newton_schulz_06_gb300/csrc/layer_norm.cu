@@ -253,7 +253,13 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             Vec<T, AL> raw;
-            raw.load(x + c0 + i * step, cols - c0 - i * step);
+            const int valid = cols - c0 - i * step;
+            if (AL && !CKPT) {
+                if (valid <= 0) break;
+                raw.load_some(x + c0 + i * step, valid);
+            } else {
+                raw.load(x + c0 + i * step, valid);
+            }
             raw.get(v[i]);
 #pragma unroll
             for (int j = 0; j < F2; ++j) s = add2(s, v[i][j]);
@@ -289,6 +295,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step, valid = cols - c;
+            if (AL && !CKPT && valid <= 0) break;
             float2 h[F2];
 #pragma unroll
             for (int j = 0; j < F2; ++j) h[j] = mul2(add2(v[i][j], both(-mean)), both(rstd));
@@ -638,17 +645,15 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     // planes, the first and the last four values of the vectors, so that
     // neighbouring threads read neighbouring 16 bytes
     const int w_vecs = (cols + VE - 1) / VE;
-    if (a.weight)
-        for (int c = threadIdx.x; c < w_vecs * VE; c += blockDim.x) {
-            const int plane = VE == 8 ? c / 4 % 2 : 0;
-            reinterpret_cast<float*>(shared)[(plane * w_vecs + c / VE) * 4 + c % 4] =
-                c < cols ? load_any(a.weight, a.w_dtype, c) : 0.f;
-        }
+    for (int c = threadIdx.x; c < w_vecs * VE; c += blockDim.x) {
+        const int plane = VE == 8 ? c / 4 % 2 : 0;
+        reinterpret_cast<float*>(shared)[(plane * w_vecs + c / VE) * 4 + c % 4] =
+            c >= cols ? 0.f : a.weight ? load_any(a.weight, a.w_dtype, c) : 1.f;
+    }
     auto w_vec = [&](int v, float2 (&w)[F2]) {
 #pragma unroll
         for (int h = 0; h < VE / 4; ++h) {
-            const float4 f = a.weight ? reinterpret_cast<const float4*>(shared)[h * w_vecs + v]
-                                      : make_float4(1.f, 1.f, 1.f, 1.f);
+            const float4 f = reinterpret_cast<const float4*>(shared)[h * w_vecs + v];
             w[2 * h] = make_float2(f.x, f.y);
             w[2 * h + 1] = make_float2(f.z, f.w);
         }
@@ -715,8 +720,8 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
         auto vec = [&](int i, GradVec<T, AL, CKPT>& v) {
             const int c = c0 + i * step;
             Vec<T, AL> dyv, xv;
-            dyv.load(dy_row + c, cols - c);
-            if constexpr (!CKPT) xv.load(x_row + c, cols - c);
+            dyv.load_some(dy_row + c, cols - c);
+            if constexpr (!CKPT) xv.load_some(x_row + c, cols - c);
             w_vec(threadIdx.x + i * blockDim.x, v.g);
             v.make(dyv, xv, q_row + c, e[i], rstd, shift);
         };
@@ -738,8 +743,8 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
             Vec<T, AL> out;
-            out.raw = make_uint4(0u, 0u, 0u, 0u);
-            if (c < cols) {
+            if (AL && c >= cols) break;
+            if (AL || c < cols) {
                 if constexpr (KEEP) {
                     kept.finish(rstd, n0, n1, out);
                 } else {
@@ -748,7 +753,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
                     v.finish(rstd, n0, n1, out);
                 }
             }
-            out.store(dx + i * step, cols - c, c == 0);
+            out.store(dx + i * step, AL ? VE : cols - c, c == 0);
         }
         if (!KEEP) {
             __syncthreads();
@@ -873,7 +878,7 @@ GradPlan grad_plan(const muon_layer_norm_grad_args& a) {
         const int64_t dy = ceil_div(a.cols * size + 14, 16) * 16;
         const int64_t row = dy + (a.saved.q ? ceil_div(a.cols, 16) * 16 : dy);
         // the weight's vectors are read whole: room to the end of the last one
-        const int64_t w_bytes = a.weight ? ceil_div(a.cols, 32) * 32 * 4 : 0;
+        const int64_t w_bytes = ceil_div(a.cols, 32) * 32 * 4;
         const int most = size == 4 ? ring_threads<float>(g.shape.nv) : ring_threads<__nv_bfloat16>(g.shape.nv);
         // blocks an SM: about 1024 threads, of the 64 registers that leaves
         int64_t per_sm = g.shape.nv < 4 ? 1024 / g.shape.threads : 1;

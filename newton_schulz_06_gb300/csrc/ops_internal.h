@@ -120,7 +120,10 @@ struct Vec {
     // none; those past it are 0).  Shared or global memory.
     __device__ __forceinline__ void load(const T* p, int valid) {
         raw = make_uint4(0u, 0u, 0u, 0u);
-        if (valid <= 0) return;
+        if (valid > 0) load_some(p, valid);
+    }
+    // The same where the row is known to hold some of it.
+    __device__ __forceinline__ void load_some(const T* p, int valid) {
         if (AL) {
             raw = *reinterpret_cast<const uint4*>(p);
             return;
