@@ -2,328 +2,555 @@
 // softmax over the experts, the k largest logits, counts, offsets and the
 // balance loss; its gradient.
 //
-// One warp holds a token's logits, expert e in lane e % 32.  The k largest
-// are taken from the logits themselves, one after another, so that which
-// experts are taken depends on no rounding; a tie goes to the lower index.
+// A token's logits lie in the registers of a warp (of eight lanes up to 32
+// experts), in pieces of four neighbouring experts: expert e is value e % 4
+// of piece e / 4, and lane l has the pieces l, l + L, ...  The k largest are
+// taken from the logits themselves, one after another, so that which experts
+// are taken depends on no rounding; a tie goes to the lower index.
+//
+// Sums of p over the tokens collect in registers, then in one row of partial
+// results a block; a cluster of blocks adds these up in order and computes
+// offsets and loss.
 #include "ops_internal.h"
 
 namespace muon {
 namespace ops {
 namespace {
 
-constexpr int WARPS = 8;
-constexpr int THREADS = 32 * WARPS;
-constexpr int MAX_PARTS = 304;       // blocks of the first kernel
+constexpr int SMS = 152;
+constexpr int JOIN_CTAS = 8;             // the cluster of the second kernel
+constexpr int JOIN_THREADS = 512;
 
-__device__ __forceinline__ float warp_max(float v) {
+template <int V>
+__host__ __device__ constexpr int route_threads() { return V <= 16 ? 512 : 256; }
+
+// Values of the L lanes of a token; all lanes of the warp take part.
+template <int L>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    if constexpr (L == 32) {
+        return __reduce_max_sync(0xffffffffu, v);
+    } else {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        for (int o = L / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+        return v;
+    }
+}
+template <int L>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+    return ~group_max<L>(~v);
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// A logit's place in the order of the reals as an unsigned number; 0 for
-// -infinity, which is never taken, and the largest for a NaN, whose token's
-// weights and gradients then show it.
+// A logit's place in the order of the reals as an unsigned number: never 0,
+// which stands for no logit; a NaN is the largest.  Adding 0 makes -0 a 0 and
+// every NaN the positive one.
 __device__ __forceinline__ uint32_t order_key(float v) {
-    if (v != v) return 0xffffffffu;
-    if (v == -INFINITY) return 0u;
-    const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);    // -0 and 0 are equal
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+    const uint32_t b = __float_as_uint(v + 0.f);
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// The V logits of a lane; those past the experts are -infinity.  AL: pieces
+// are whole and lie on their size.
+template <typename T, int V, int L, bool AL>
+struct Logits {
+    static constexpr int P = V / 4;
+    uint4 raw[P];
+    static __device__ __forceinline__ int expert(int i, int lane) { return (i / 4 * L + lane) * 4 + i % 4; }
+    __device__ __forceinline__ void load(const T* z, int lane, int experts, bool there) {
+        const uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * L + lane) * 4;
+            raw[p] = make_uint4(none, none, none, none);
+            if (!there || e >= experts) continue;
+            if constexpr (AL && sizeof(T) == 4) {
+                raw[p] = *reinterpret_cast<const uint4*>(z + e);
+            } else if constexpr (AL) {
+                const uint2 t = *reinterpret_cast<const uint2*>(z + e);
+                raw[p].x = t.x;
+                raw[p].y = t.y;
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    w[j] = sizeof(T) == 4 ? 0xff800000u : 0xff80u;
+                    if (e + j < experts) {
+                        if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(z[e + j]);
+                        else w[j] = __bfloat16_as_ushort(z[e + j]);
+                    }
+                }
+                if constexpr (sizeof(T) == 4) {
+                    raw[p] = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    raw[p].x = w[0] | w[1] << 16;
+                    raw[p].y = w[2] | w[3] << 16;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[V]) const {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            if constexpr (sizeof(T) == 4) {
+                v[4 * p] = __uint_as_float(raw[p].x);
+                v[4 * p + 1] = __uint_as_float(raw[p].y);
+                v[4 * p + 2] = __uint_as_float(raw[p].z);
+                v[4 * p + 3] = __uint_as_float(raw[p].w);
+            } else {
+                v[4 * p] = __uint_as_float(raw[p].x << 16);
+                v[4 * p + 1] = __uint_as_float(raw[p].x & 0xffff0000u);
+                v[4 * p + 2] = __uint_as_float(raw[p].y << 16);
+                v[4 * p + 3] = __uint_as_float(raw[p].y & 0xffff0000u);
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(T* z, const float (&v)[V], int lane, int experts) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * L + lane) * 4;
+            if (e >= experts) continue;
+            if constexpr (AL && sizeof(T) == 4) {
+                *reinterpret_cast<float4*>(z + e) =
+                    make_float4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+            } else if constexpr (AL) {
+                const __nv_bfloat162 a = __floats2bfloat162_rn(v[4 * p], v[4 * p + 1]);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[4 * p + 2], v[4 * p + 3]);
+                *reinterpret_cast<uint2*>(z + e) = make_uint2(reinterpret_cast<const uint32_t&>(a),
+                                                              reinterpret_cast<const uint32_t&>(b));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (e + j < experts) from_f32(z + e + j, v[4 * p + j]);
+            }
+        }
+    }
+};
+
+// The largest logits of a token, one a call.  bf16: a key has the logit's 16
+// bits and below them 65535 - expert, so that no two are equal and the next
+// one is the largest key below the last.
+template <typename T, int V, int L>
+struct Selection {
+    uint32_t key[V], best;               // best: this lane's largest left
+    __device__ __forceinline__ void start(const float (&v)[V], int lane, int experts) {
+        best = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = Logits<T, V, L, true>::expert(i, lane);
+            const uint32_t k = (order_key(v[i]) & 0xffff0000u) | (65535u - e);
+            key[i] = e < experts ? k : 0u;
+            best = max(best, key[i]);
+        }
+    }
+    __device__ __forceinline__ uint32_t next(int) {
+        const uint32_t top = group_max<L>(best);
+        // differences wrap: those of keys below top are the larger ones
+        uint32_t d = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) d = max(d, key[i] - top);
+        best = top + d < top ? top + d : 0u;
+        return top;
+    }
+    static __device__ __forceinline__ float value(uint32_t top) {
+        // the index's bits are no part of the logit
+        return __uint_as_float(__float_as_uint(key_value(top)) & 0xffff0000u);
+    }
+    __device__ __forceinline__ int expert(uint32_t top) const { return 65535 - (top & 0xffffu); }
+};
+// fp32: the key is the whole logit; the lane that holds the taken one looks
+// for its next.
+template <int V, int L>
+struct Selection<float, V, L> {
+    uint32_t key[V], best;
+    int at, taken;
+    __device__ __forceinline__ void look() {
+        best = 0;
+        at = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+    }
+    __device__ __forceinline__ void start(const float (&v)[V], int lane, int experts) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            key[i] = Logits<float, V, L, true>::expert(i, lane) < experts ? order_key(v[i]) : 0u;
+        look();
+    }
+    __device__ __forceinline__ uint32_t next(int lane) {
+        const uint32_t top = group_max<L>(best);
+        const uint32_t e = ((at >> 2) * L + lane) * 4 + (at & 3);
+        const uint32_t mine = best == top ? e : 0xffffffffu;
+        taken = static_cast<int>(group_min<L>(mine));
+        if (static_cast<int>(mine) == taken && top) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i == at) key[i] = 0u;
+            look();
+        }
+        return top;
+    }
+    static __device__ __forceinline__ float value(uint32_t top) { return key_value(top); }
+    __device__ __forceinline__ int expert(uint32_t) const { return taken; }
+};
 
 // Partial results of a block: sums of p, then counts, then tokens kept.
 __host__ __device__ __forceinline__ int64_t part_words(int64_t experts) { return 2 * experts + 1; }
 
-// V: logits a lane holds (experts <= 32 V).
-template <typename T, int V>
-__global__ void __launch_bounds__(THREADS)
+template <typename T, int V, int L, bool AL>
+__global__ void __launch_bounds__(route_threads<V>())
     route_kernel(const __grid_constant__ muon_route_args a, float* part) {
-    __shared__ float s_p[1024];
+    constexpr int THREADS = route_threads<V>(), WARPS = THREADS / 32, ROWS = THREADS / L;
+    extern __shared__ float s_p[];               // WARPS x experts
     __shared__ int s_c[1024];
     __shared__ int s_kept;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int lane = threadIdx.x % L, warp = threadIdx.x >> 5;
     const int E = static_cast<int>(a.experts), K = static_cast<int>(a.k);
-    for (int e = threadIdx.x; e < E; e += THREADS) {
-        s_p[e] = 0.f;
-        s_c[e] = 0;
-    }
+    for (int e = threadIdx.x; e < E; e += THREADS) s_c[e] = 0;
     if (threadIdx.x == 0) s_kept = 0;
     __syncthreads();
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (int64_t t = blockIdx.x * int64_t(WARPS) + warp; t < a.tokens;
-         t += int64_t(gridDim.x) * WARPS) {
-        const T* z = static_cast<const T*>(a.logits) + t * a.ld_z;
-        bool keep = !a.mask || a.mask[t];
+    int kept = 0;
+    const int64_t stride = int64_t(gridDim.x) * ROWS;
+    // a block's lanes walk on together: the reductions ask every lane
+    const int64_t last = (a.tokens + ROWS - 1) / ROWS * ROWS;
+    int64_t t = int64_t(blockIdx.x) * ROWS + threadIdx.x / L;
+    Logits<T, V, L, AL> z;
+    bool use = false;
+    auto fetch = [&](int64_t row) {
+        use = row < a.tokens && (!a.mask || a.mask[row]);
+        z.load(static_cast<const T*>(a.logits) + row * a.ld_z, lane, E, use);
+    };
+    fetch(t);
+    for (; t < last; t += stride) {
         float v[V];
-        float top = -INFINITY;
-        bool nan = false;
+        z.get(v);
+        const bool masked_out = !use;
+        fetch(t + stride);                       // ahead of this token's work
+        Selection<T, V, L> sel;
+        sel.start(v, lane, E);
+        uint32_t top = sel.next(lane);
+        const float shift = sel.value(top);
+        const bool keep = !masked_out && !(shift == -INFINITY);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[i] = __expf(v[i] - shift);
+            sum += v[i];
+        }
+        const float inv = 1.f / group_sum<L>(sum);
         if (keep) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = i * 32 + lane;
-                v[i] = e < E ? to_f32(z[e]) : -INFINITY;
-                nan |= v[i] != v[i];
-                top = fmaxf(top, v[i]);
-            }
-            top = warp_max(top);
-            nan = __any_sync(0xffffffffu, nan);
-            keep = nan || top > -INFINITY;
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+            if (lane == 0) ++kept;
         }
-        int32_t* idx = a.indices + t * K;
-        float* wt = a.weights + t * K;
-        if (!keep) {
-            if (lane < K) {
-                idx[lane] = -1;
-                wt[lane] = 0.f;
-            }
-            continue;
-        }
-        float p[V], sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            p[i] = expf(v[i] - top);
-            sum += p[i];
-        }
-        sum = warp_sum(sum);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            p[i] /= sum;
-            if (i * 32 + lane < E) acc[i] += p[i];
-        }
-        uint32_t key[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = order_key(v[i]);
-        int my_e = -1;
-        float my_w = 0.f, taken = 0.f;
-        for (int j = 0; j < K; ++j) {
-            uint32_t best = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i) best = max(best, key[i]);
-            best = __reduce_max_sync(0xffffffffu, best);
-            if (best == 0u) break;
-            // the lowest index among the equal ones
-            int at = 1 << 30;
-#pragma unroll
-            for (int i = V - 1; i >= 0; --i)
-                if (key[i] == best) at = i * 32 + lane;
-            at = __reduce_min_sync(0xffffffffu, at);
-            float pw = 0.f;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i * 32 + lane == at) {
-                    pw = p[i];
-                    key[i] = 0u;
-                }
-            pw = __shfl_sync(0xffffffffu, pw, at & 31);
-            taken += pw;
+        int my_e = 0;
+        uint32_t my_key = 0;
+        for (int j = 0;;) {
             if (lane == j) {
-                my_e = at;
-                my_w = pw;
+                my_key = top;
+                my_e = sel.expert(top);
             }
+            if (++j == K) break;
+            top = sel.next(lane);
         }
-        if (lane < K) {
-            idx[lane] = my_e;
-            wt[lane] = a.renormalise && my_e >= 0 ? my_w / taken : my_w;
-            if (my_e >= 0) atomicAdd(&s_c[my_e], 1);
+        const float my_v = sel.value(my_key);
+        const bool mine = keep && lane < K && my_key && !(my_v == -INFINITY);
+        float w = mine ? __expf(my_v - shift) * inv : 0.f;
+        if (a.renormalise) {
+            const float total = group_sum<L>(w);
+            if (mine) w /= total;
         }
-        if (lane == 0) atomicAdd(&s_kept, 1);
+        if (lane < K && t < a.tokens) {
+            a.indices[t * K + lane] = mine ? my_e : -1;
+            a.weights[t * K + lane] = w;
+            if (mine) atomicAdd(&s_c[my_e], 1);
+        }
     }
-    // sums of p in the order of the warps
-    for (int w = 0; w < WARPS; ++w) {
-        __syncthreads();
-        if (w == warp) {
+    if (kept) atomicAdd(&s_kept, kept);
+    // over a warp's tokens (eight lanes each), then the warps' sums in order
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i * 32 + lane < E) s_p[i * 32 + lane] += acc[i];
-        }
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+        const int e = Logits<T, V, L, AL>::expert(i, lane);
+        if (e < E && (threadIdx.x & 31) < L) s_p[warp * E + e] = acc[i];
     }
     __syncthreads();
     float* out = part + blockIdx.x * part_words(E);
     for (int e = threadIdx.x; e < E; e += THREADS) {
-        out[e] = s_p[e];
+        float p = 0.f;
+        for (int w = 0; w < WARPS; ++w) p += s_p[w * E + e];
+        out[e] = p;
         reinterpret_cast<int*>(out)[E + e] = s_c[e];
     }
     if (threadIdx.x == 0) reinterpret_cast<int*>(out)[2 * E] = s_kept;
 }
 
-// One block: the partial results in order, offsets, loss.
-__global__ void __launch_bounds__(1024)
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores a word to this variable of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_to_rank(void* at, uint32_t rank, uint32_t v) {
+    uint32_t addr;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(addr)
+                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(at))), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// One cluster: each CTA adds up the n partial results of its experts, with as
+// many threads an expert as there are (in order within a thread, then the
+// threads in order); CTA 0 makes offsets and loss of them.
+__global__ void __cluster_dims__(JOIN_CTAS, 1, 1) __launch_bounds__(JOIN_THREADS)
     route_join_kernel(const __grid_constant__ muon_route_args a, const float* part, int n) {
-    __shared__ int s_scan[1024];
-    __shared__ float s_sum[32];
-    __shared__ int s_kept;
-    const int e = threadIdx.x, E = static_cast<int>(a.experts);
+    __shared__ float s_p[JOIN_THREADS];
+    __shared__ int s_n[JOIN_THREADS];
+    __shared__ int s_count[1024];
+    __shared__ float s_term[1024];               // count times sum of p
+    __shared__ int s_warp[JOIN_THREADS / 32];
+    __shared__ float s_sum[JOIN_THREADS / 32];
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int E = static_cast<int>(a.experts);
     const int64_t words = part_words(E);
+    const int each = (E + JOIN_CTAS - 1) / JOIN_CTAS;        // at most 128
+    const int slices = JOIN_THREADS / each;
+    const int mine = threadIdx.x % each, slice = threadIdx.x / each;
+    const int e = blockIdx.x * each + mine;
+    const int* ints = reinterpret_cast<const int*>(part);
     float p = 0.f;
     int c = 0;
-    if (e < E)
-        for (int i = 0; i < n; ++i) {
+    if (e < E && slice < slices)
+#pragma unroll 4
+        for (int i = slice; i < n; i += slices) {
             p += part[i * words + e];
-            c += reinterpret_cast<const int*>(part)[i * words + E + e];
+            c += ints[i * words + E + e];
         }
-    if (e == 0) {
-        int kept = 0;
-        for (int i = 0; i < n; ++i) kept += reinterpret_cast<const int*>(part)[i * words + 2 * E];
-        s_kept = kept;
-        *a.kept = kept;
-    }
-    s_scan[e] = c;
-    for (int o = 1; o < 1024; o <<= 1) {
-        __syncthreads();
-        const int add = e >= o ? s_scan[e - o] : 0;
-        __syncthreads();
-        s_scan[e] += add;
-    }
-    if (e < E) {
+    s_p[threadIdx.x] = p;
+    s_n[threadIdx.x] = c;
+    cluster_sync();                              // every CTA runs: its memory can be written
+    if (slice == 0 && e < E) {
+        for (int s = 1; s < slices; ++s) {
+            p += s_p[s * each + mine];
+            c += s_n[s * each + mine];
+        }
         a.counts[e] = c;
-        a.offsets[e + 1] = s_scan[e];
-        if (e == 0) a.offsets[0] = 0;
+        store_to_rank(&s_count[e], 0, c);
+        store_to_rank(&s_term[e], 0, __float_as_uint(static_cast<float>(c) * p));
     }
-    const float part_sum = warp_sum(e < E ? static_cast<float>(c) * p : 0.f);
-    if ((e & 31) == 0) s_sum[e >> 5] = part_sum;
+    cluster_sync();
+    if (blockIdx.x != 0) return;
+    // two experts a thread: offsets by scanning, the loss's sum, tokens kept
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e0 = 2 * threadIdx.x;
+    const int c0 = e0 < E ? s_count[e0] : 0, c1 = e0 + 1 < E ? s_count[e0 + 1] : 0;
+    int scan = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += up;
+    }
+    const float term = warp_sum((e0 < E ? s_term[e0] : 0.f) + (e0 + 1 < E ? s_term[e0 + 1] : 0.f));
+    int kept = 0;
+    for (int i = threadIdx.x; i < n; i += JOIN_THREADS) kept += ints[i * words + 2 * E];
+    kept = __reduce_add_sync(0xffffffffu, kept);
+    if (lane == 31) s_warp[warp] = scan;
+    if (lane == 0) {
+        s_sum[warp] = term;
+        s_n[warp] = kept;
+    }
     __syncthreads();
-    if (e < 32) {
-        const float total = warp_sum(s_sum[e]);
-        const float kept = static_cast<float>(s_kept);
-        if (e == 0)
-            *a.loss = s_kept ? a.coef * static_cast<float>(E) / (static_cast<float>(a.k) * kept) *
-                                   (total / kept)
-                             : 0.f;
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += s_warp[w];
+    before += scan - c0 - c1;
+    if (e0 < E) a.offsets[e0 + 1] = before + c0;
+    if (e0 + 1 < E) a.offsets[e0 + 2] = before + c0 + c1;
+    if (threadIdx.x == 0) {
+        a.offsets[0] = 0;
+        float total = 0.f;
+        kept = 0;
+        for (int w = 0; w < JOIN_THREADS / 32; ++w) {
+            total += s_sum[w];
+            kept += s_n[w];
+        }
+        *a.kept = kept;
+        const float t = static_cast<float>(kept);
+        *a.loss = kept ? a.coef * static_cast<float>(E) / (static_cast<float>(a.k) * t) * (total / t) : 0.f;
     }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(THREADS)
+// dz = p (h - sum p h), where h is the loss's part, the same for all tokens
+// (count times a factor, in registers), and for the taken experts also that
+// of their weights: a lane computes theirs again and stores them over the
+// others'.
+template <typename T, int V, int L, bool AL>
+__global__ void __launch_bounds__(256)
     route_grad_kernel(const __grid_constant__ muon_route_grad_args a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int ROWS = 256 / L;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int lane = threadIdx.x % L, base = (threadIdx.x & 31) / L * L;
     const int E = static_cast<int>(a.experts), K = static_cast<int>(a.k);
     const float kept = static_cast<float>(max(1, *a.kept));
     const float factor = (a.dloss ? *a.dloss : 0.f) * a.coef * static_cast<float>(E) /
                          (static_cast<float>(K) * kept) / kept;
-    for (int64_t t = blockIdx.x * int64_t(WARPS) + warp; t < a.tokens;
-         t += int64_t(gridDim.x) * WARPS) {
-        const T* z = static_cast<const T*>(a.logits) + t * a.ld_z;
-        T* dz = static_cast<T*>(a.dlogits) + t * a.ld_dz;
-        int my_e = -1;
-        float my_w = 0.f, my_d = 0.f;
-        if (lane < K) {
-            my_e = a.indices[t * K + lane];
-            if (my_e >= E) my_e = -1;
-            if (my_e >= 0) {
-                my_w = a.weights[t * K + lane];
-                my_d = a.dweights ? a.dweights[t * a.ld_dw + lane] : 0.f;
-            }
-        }
-        // the first place is empty only if the token takes no part
-        if (__shfl_sync(0xffffffffu, my_e, 0) < 0) {
-            for (int e = lane; e < E; e += 32) from_f32(dz + e, 0.f);
-            continue;
-        }
-        float p[V], top = -INFINITY;
+    float f[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = i * 32 + lane;
-            p[i] = e < E ? to_f32(z[e]) : -INFINITY;
-            top = fmaxf(top, p[i]);
+    for (int i = 0; i < V; ++i) {
+        const int e = Logits<T, V, L, AL>::expert(i, lane);
+        f[i] = e < E ? factor * static_cast<float>(a.counts[e]) : 0.f;
+    }
+    const int64_t stride = int64_t(gridDim.x) * ROWS;
+    const int64_t last = (a.tokens + ROWS - 1) / ROWS * ROWS;
+    int64_t t = int64_t(blockIdx.x) * ROWS + threadIdx.x / L;
+    Logits<T, V, L, AL> z;
+    int my_e = -1;
+    auto fetch = [&](int64_t row) {
+        z.load(static_cast<const T*>(a.logits) + row * a.ld_z, lane, E, row < a.tokens);
+        my_e = -1;
+        if (lane < K && row < a.tokens) my_e = a.indices[row * K + lane];
+        if (my_e >= E) my_e = -1;
+    };
+    fetch(t);
+    for (; t < last; t += stride) {
+        const int e = my_e;
+        const bool row = t < a.tokens;
+        float v[V];
+        z.get(v);
+        float my_z = 0.f, my_w = 0.f, my_d = 0.f, my_f = 0.f;
+        if (e >= 0) {
+            my_z = to_f32(static_cast<const T*>(a.logits)[t * a.ld_z + e]);
+            my_w = a.weights[t * K + lane];
+            my_d = a.dweights ? a.dweights[t * a.ld_dw + lane] : 0.f;
+            my_f = factor * static_cast<float>(a.counts[e]);
         }
-        top = warp_max(top);
+        fetch(t + stride);
+        // the first place holds the largest logit, and is empty only if the
+        // token takes no part
+        const float top = __shfl_sync(0xffffffffu, my_z, base);
+        const bool keep = __shfl_sync(0xffffffffu, e, base) >= 0;
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            p[i] = expf(p[i] - top);
-            sum += p[i];
+            v[i] = __expf(v[i] - top);
+            sum += v[i];
         }
-        sum = warp_sum(sum);
-        float h[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = i * 32 + lane;
-            p[i] /= sum;
-            h[i] = e < E ? factor * static_cast<float>(a.counts[e]) : 0.f;
-        }
-        if (a.dweights) {
-            if (a.renormalise) {
-                float taken = 0.f;
-                for (int j = 0; j < K; ++j) {
-                    const int e = __shfl_sync(0xffffffffu, my_e, j);
-                    float pe = 0.f;
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (i * 32 + lane == e) pe = p[i];
-                    taken += e >= 0 ? __shfl_sync(0xffffffffu, pe, e & 31) : 0.f;
-                }
-                const float inner = warp_sum(my_w * my_d);
-                my_d = my_e >= 0 ? (my_d - inner) / taken : 0.f;
-            }
-            for (int j = 0; j < K; ++j) {
-                const int e = __shfl_sync(0xffffffffu, my_e, j);
-                const float d = __shfl_sync(0xffffffffu, my_d, j);
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (i * 32 + lane == e) h[i] += d;
-            }
+        const float inv = 1.f / group_sum<L>(sum);
+        float my_p = e >= 0 ? __expf(my_z - top) * inv : 0.f;
+        if (a.dweights && a.renormalise) {
+            const float taken = group_sum<L>(my_p), mean = group_sum<L>(my_w * my_d);
+            my_d = e >= 0 ? (my_d - mean) / taken : 0.f;
         }
         float inner = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) inner = fmaf(p[i], h[i], inner);
-        inner = warp_sum(inner);
-#pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = i * 32 + lane;
-            if (e < E) from_f32(dz + e, p[i] * (h[i] - inner));
+            v[i] *= inv;
+            inner = fmaf(v[i], f[i], inner);
         }
+        inner = group_sum<L>(fmaf(my_p, my_d, inner));
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = keep ? v[i] * (f[i] - inner) : 0.f;
+        T* dz = static_cast<T*>(a.dlogits) + t * a.ld_dz;
+        if (row) Logits<T, V, L, AL>::store(dz, v, lane, E);
+        __syncwarp();                            // the stores below come after those
+        if (row && e >= 0) from_f32(dz + e, my_p * (my_f + my_d - inner));
     }
 }
 
-int route_parts(int64_t tokens) {
-    const int64_t g = ceil_div(tokens, WARPS);
-    return static_cast<int>(g < 1 ? 1 : g > MAX_PARTS ? MAX_PARTS : g);
+// Rows of a block (of 512 or 256 threads) and how many blocks run.
+int route_v(int64_t experts) { return static_cast<int>(ceil_div(experts, 128) * 4); }
+bool eight_lanes(int64_t experts, int64_t k) { return experts <= 32 && k <= 8; }
+int route_rows(int64_t experts, int64_t k) {
+    return eight_lanes(experts, k) ? 64 : route_v(experts) <= 16 ? 16 : 8;
+}
+int route_parts(const muon_route_args& a) {
+    const int64_t g = ceil_div(a.tokens, route_rows(a.experts, a.k));
+    return static_cast<int>(g < 1 ? 1 : g > SMS * 2 ? SMS * 2 : g);
 }
 
-template <typename T, int V>
-cudaError_t route_v(const muon_route_args& a, float* part, cudaStream_t s) {
-    const int g = route_parts(a.tokens);
-    route_kernel<T, V><<<g, THREADS, 0, s>>>(a, part);
-    route_join_kernel<<<1, 1024, 0, s>>>(a, part, g);
-    return cudaGetLastError();
+template <typename T, int V, int L, bool AL>
+cudaError_t launch_route_v(const muon_route_args& a, float* part, cudaStream_t s) {
+    const size_t smem = size_t(route_threads<V>() / 32) * a.experts * 4;
+    return launch_kernel(route_kernel<T, V, L, AL>, dim3(route_parts(a)), dim3(route_threads<V>()), smem,
+                         s, a, part);
+}
+template <typename T, int V, int L, bool AL>
+cudaError_t launch_grad_v(const muon_route_grad_args& a, cudaStream_t s) {
+    const int64_t g = ceil_div(a.tokens, 256 / L);
+    return launch_kernel(route_grad_kernel<T, V, L, AL>,
+                         dim3(static_cast<unsigned>(g > SMS * 8 ? SMS * 8 : g)), dim3(256), 0, s, a);
 }
 
-template <typename T, int V>
-cudaError_t route_grad_v(const muon_route_grad_args& a, cudaStream_t s) {
-    const int64_t g = ceil_div(a.tokens, WARPS);
-    route_grad_kernel<T, V><<<static_cast<int>(g > 152 * 8 ? 152 * 8 : g), THREADS, 0, s>>>(a);
-    return cudaGetLastError();
-}
-
-template <typename T>
+template <typename T, bool AL>
 cudaError_t route_t(const muon_route_args& a, float* part, cudaStream_t s) {
-    if (a.experts <= 128) return route_v<T, 4>(a, part, s);
-    if (a.experts <= 512) return route_v<T, 16>(a, part, s);
-    return route_v<T, 32>(a, part, s);
+    if (eight_lanes(a.experts, a.k)) return launch_route_v<T, 4, 8, AL>(a, part, s);
+    switch (route_v(a.experts)) {
+        case 4: return launch_route_v<T, 4, 32, AL>(a, part, s);
+        case 8: return launch_route_v<T, 8, 32, AL>(a, part, s);
+        case 12: return launch_route_v<T, 12, 32, AL>(a, part, s);
+        case 16: return launch_route_v<T, 16, 32, AL>(a, part, s);
+        default: return launch_route_v<T, 32, 32, AL>(a, part, s);
+    }
 }
-template <typename T>
+template <typename T, bool AL>
 cudaError_t route_grad_t(const muon_route_grad_args& a, cudaStream_t s) {
-    if (a.experts <= 128) return route_grad_v<T, 4>(a, s);
-    if (a.experts <= 512) return route_grad_v<T, 16>(a, s);
-    return route_grad_v<T, 32>(a, s);
+    if (eight_lanes(a.experts, a.k)) return launch_grad_v<T, 4, 8, AL>(a, s);
+    switch (route_v(a.experts)) {
+        case 4: return launch_grad_v<T, 4, 32, AL>(a, s);
+        case 8: return launch_grad_v<T, 8, 32, AL>(a, s);
+        case 12: return launch_grad_v<T, 12, 32, AL>(a, s);
+        case 16: return launch_grad_v<T, 16, 32, AL>(a, s);
+        default: return launch_grad_v<T, 32, 32, AL>(a, s);
+    }
+}
+
+// Whole pieces of four that lie on their size.
+bool whole_pieces(const void* p, int dtype, int64_t rows, int64_t experts, int64_t ld) {
+    const int64_t size = dtype == MUON_F32 ? 16 : 8;
+    return experts % 4 == 0 && reinterpret_cast<uintptr_t>(p) % size == 0 && (rows <= 1 || ld % 4 == 0);
 }
 
 }  // namespace
 
 size_t route_workspace(const muon_route_args& a) {
-    return size_t(route_parts(a.tokens)) * part_words(a.experts) * 4;
+    return size_t(route_parts(a)) * part_words(a.experts) * 4;
 }
 
 cudaError_t launch_route(const muon_route_args& a, void* ws, cudaStream_t s) {
-    return a.z_dtype == MUON_F32 ? route_t<float>(a, static_cast<float*>(ws), s)
-                                 : route_t<__nv_bfloat16>(a, static_cast<float*>(ws), s);
+    float* part = static_cast<float*>(ws);
+    const bool al = whole_pieces(a.logits, a.z_dtype, a.tokens, a.experts, a.ld_z);
+    cudaError_t e;
+    if (a.z_dtype == MUON_F32)
+        e = al ? route_t<float, true>(a, part, s) : route_t<float, false>(a, part, s);
+    else
+        e = al ? route_t<__nv_bfloat16, true>(a, part, s) : route_t<__nv_bfloat16, false>(a, part, s);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(route_join_kernel, dim3(JOIN_CTAS), dim3(JOIN_THREADS), 0, s, a,
+                         static_cast<const float*>(part), route_parts(a));
 }
 
 cudaError_t launch_route_grad(const muon_route_grad_args& a, cudaStream_t s) {
     if (a.tokens == 0) return cudaSuccess;
-    return a.z_dtype == MUON_F32 ? route_grad_t<float>(a, s) : route_grad_t<__nv_bfloat16>(a, s);
+    const bool al = whole_pieces(a.logits, a.z_dtype, a.tokens, a.experts, a.ld_z) &&
+                    whole_pieces(a.dlogits, a.z_dtype, a.tokens, a.experts, a.ld_dz);
+    if (a.z_dtype == MUON_F32)
+        return al ? route_grad_t<float, true>(a, s) : route_grad_t<float, false>(a, s);
+    return al ? route_grad_t<__nv_bfloat16, true>(a, s) : route_grad_t<__nv_bfloat16, false>(a, s);
 }
 
 }  // namespace ops
