@@ -52,6 +52,17 @@ class _Local(threading.local):
 _local = _Local()
 
 
+_fns = {}
+
+
+def _fn(name: str):
+    """An entry point of the library (looked up once)."""
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(lib(), name)
+    return f
+
+
 def _need(ok: bool, message: str) -> None:
     if not ok:
         raise ValueError(message)
@@ -64,57 +75,60 @@ def _dtype(name: str, t: torch.Tensor) -> int:
     return d
 
 
-def _matrix(name: str, t: torch.Tensor, device=None, shape=None) -> int:
-    """Checks a row-major 2-D CUDA tensor; its leading dimension."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
-    if not t.is_cuda or (device is not None and t.device != device):
+def _matrix(name: str, t: torch.Tensor, index: int = -1, rows: int = -1, cols: int = -1):
+    """Checks a row-major 2-D CUDA tensor (of device `index` and rows x cols,
+    where given): (rows, cols, leading dimension, device index)."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(shape)}")
+    on = t.get_device()
+    if on < 0 or (index >= 0 and on != index):
         raise ValueError(f"{name} must be a CUDA tensor of its operator's device, is on {t.device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    r, c = shape
+    if rows >= 0 and (r != rows or c != cols):
+        raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(shape)}")
     ld, inner = t.stride()
-    if inner != 1 and t.shape[1] > 1:
+    if inner != 1 and c > 1:
         raise ValueError(f"{name} must be row-major (stride(1) == 1)")
-    return ld
+    return r, c, ld, on
 
 
-def _vector(name: str, t: Optional[torch.Tensor], device, n: int, dtype=None) -> int:
+def _vector(name: str, t: Optional[torch.Tensor], index: int, n: int, dtype=None) -> int:
     """Checks a dense 1-D tensor of n values (or None); its address."""
     if t is None:
         return 0
-    if t.device != device or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be {n} dense values on {device}, got {tuple(t.shape)} "
+    if t.dim() != 1 or t.numel() != n or t.get_device() != index or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be {n} dense values on cuda:{index}, got {tuple(t.shape)} "
                          f"on {t.device}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
 
 
-def _call(device: torch.device, name: str, *args) -> None:
+def _call(index: int, name: str, *args) -> None:
     """Calls an entry point on the device's current stream, with the device
     current."""
-    index = device.index
-    if torch.cuda.current_device() != index:
+    if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
-            return _call(device, name, *args)
+            return _call(index, name, *args)
     err = _local.err
-    rc = getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index), err, _ERR_LEN)
+    rc = _fn(name)(*args, torch._C._cuda_getCurrentRawStream(index), err, _ERR_LEN)
     if rc < 0:
         raise MuonError(rc, f"{name}: {err.value.decode(errors='replace')}")
 
 
-def _call_ws(device: torch.device, name: str, query: str, args: bytes) -> None:
+def _call_ws(index: int, name: str, query: str, args: bytes, device) -> None:
     """Calls an entry point that takes a workspace, allocated here."""
     size = _local.size
     size.value = 0
     # a query that refuses its arguments leaves the message to the call
-    getattr(lib(), query)(args, _local.size_ref)
+    _fn(query)(args, _local.size_ref)
     n = size.value
     if n:
         ws = torch.empty(n, dtype=torch.uint8, device=device)
-        _call(device, name, args, ws.data_ptr(), n)
+        _call(index, name, args, ws.data_ptr(), n)
     else:
-        _call(device, name, args, None, 0)
+        _call(index, name, args, None, 0)
 
 
 class Checkpoint8:
@@ -168,42 +182,39 @@ class Checkpoint8:
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """What the checkpoint stands for (exact in bf16 and fp32)."""
         q, cols = self.q, self.cols
-        rows, dev = q.shape[0], q.device
+        rows = q.shape[0]
         if out is None:
-            out = torch.empty((rows, cols), dtype=dtype, device=dev)
-        ld = _matrix("out", out, dev, (rows, cols))
-        _call(dev, "muon_ckpt8_unpack", _ckpt_arg(*self._fields()), rows, cols, out.data_ptr(),
+            out = torch.empty((rows, cols), dtype=dtype, device=q.device)
+        _, _, ld, index = _matrix("out", out, q.get_device(), rows, cols)
+        _call(index, "muon_ckpt8_unpack", _ckpt_arg(*self._fields()), rows, cols, out.data_ptr(),
               _dtype("out", out), ld)
         return out
 
 
 def checkpoint8(x: torch.Tensor, out: Optional[Checkpoint8] = None) -> Checkpoint8:
     """The 8-bit checkpoint of x (2-D, fp32 or bf16)."""
-    ld = _matrix("x", x)
-    rows, cols = x.shape
-    dev = x.device
-    out = _checkpoint("out", out, rows, cols, dev)
-    _call(dev, "muon_ckpt8_pack", x.data_ptr(), _dtype("x", x), rows, cols, ld,
+    rows, cols, ld, index = _matrix("x", x)
+    out = _checkpoint("out", out, rows, cols, x)
+    _call(index, "muon_ckpt8_pack", x.data_ptr(), _dtype("x", x), rows, cols, ld,
           _ckpt_arg(*out._fields()))
     return out
 
 
-def _checkpoint(name: str, c: Optional[Checkpoint8], rows: int, cols: int, device) -> Checkpoint8:
+def _checkpoint(name: str, c: Optional[Checkpoint8], rows: int, cols: int, like) -> Checkpoint8:
     if c is None:
-        return Checkpoint8.empty(rows, cols, device)
-    _need(c.shape == (rows, cols) and c.device == device,
-          f"{name} must be a checkpoint of {(rows, cols)} on {device}")
+        return Checkpoint8.empty(rows, cols, like.device)
+    _need(c.shape == (rows, cols) and c.device == like.device,
+          f"{name} must be a checkpoint of {(rows, cols)} on {like.device}")
     return c
 
 
-def _output(name: str, t: Optional[torch.Tensor], like: torch.Tensor):
+def _output(name: str, t: Optional[torch.Tensor], like: torch.Tensor, rows: int, cols: int):
     """The output of `like`'s shape, type and device (given or new): (it, its
     leading dimension)."""
     if t is None:
-        rows, cols = like.shape
         return torch.empty((rows, cols), dtype=like.dtype, device=like.device), cols
     _need(t.dtype == like.dtype, f"{name} must be {like.dtype}, got {t.dtype}")
-    return t, _matrix(name, t, like.device, like.shape)
+    return t, _matrix(name, t, like.get_device(), rows, cols)[2]
 
 
 def _w_dtype(weight, bias) -> int:
@@ -213,19 +224,24 @@ def _w_dtype(weight, bias) -> int:
     return _lib.MUON_F32 if t is None else _dtype("weight and bias", t)
 
 
-def _norm_forward(x, weight, bias, eps, out, saved, mean):
-    ld = _matrix("x", x)
-    rows, cols = x.shape
+def _norm_forward(x, weight, bias, eps, out, keep, saved):
+    """(y, mean, rstd, saved): with keep, h goes to a checkpoint and no mean
+    is written."""
+    rows, cols, ld, index = _matrix("x", x)
     dev = x.device
-    y, ld_y = _output("out", out, x)
+    y, ld_y = _output("out", out, x, rows, cols)
     rstd = torch.empty(rows, dtype=_F32, device=dev)
-    args = _norm_args(
-        x.data_ptr(), _vector("weight", weight, dev, cols), _vector("bias", bias, dev, cols),
-        y.data_ptr(), 0 if mean is None else mean.data_ptr(), rstd.data_ptr(),
-        *(_NO_CKPT if saved is None else saved._fields()),
-        rows, cols, ld, ld_y, _dtype("x", x), _w_dtype(weight, bias), eps)
-    _call(dev, "muon_layer_norm", args)
-    return y, rstd
+    if keep:
+        saved = _checkpoint("saved", saved, rows, cols, x)
+        mean, mean_at, fields = None, 0, saved._fields()
+    else:
+        mean = torch.empty(rows, dtype=_F32, device=dev)
+        mean_at, fields = mean.data_ptr(), _NO_CKPT
+    _call(index, "muon_layer_norm", _norm_args(
+        x.data_ptr(), _vector("weight", weight, index, cols), _vector("bias", bias, index, cols),
+        y.data_ptr(), mean_at, rstd.data_ptr(), *fields, rows, cols, ld, ld_y, _dtype("x", x),
+        _w_dtype(weight, bias), eps))
+    return y, mean, rstd, saved
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -235,10 +251,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
 
     Returns (y, mean, rstd); y has x's type (out may be x), mean and rstd are
     fp32.  weight and bias: fp32 or bf16, of one type; None for ones, zeros."""
-    _matrix("x", x)
-    mean = torch.empty(x.shape[0], dtype=_F32, device=x.device)
-    y, rstd = _norm_forward(x, weight, bias, eps, out, None, mean)
-    return y, mean, rstd
+    return _norm_forward(x, weight, bias, eps, out, False, None)[:3]
 
 
 def layer_norm_checkpoint(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -251,9 +264,7 @@ def layer_norm_checkpoint(x: torch.Tensor, weight: Optional[torch.Tensor] = None
     Returns (y, rstd, saved).  saved serves :func:`layer_norm_backward` and,
     with the norm's weight and bias, :func:`weight_grad` of every product that
     reads y, so that neither x nor y has to be kept."""
-    _matrix("x", x)
-    saved = _checkpoint("saved", saved, x.shape[0], x.shape[1], x.device)
-    y, rstd = _norm_forward(x, weight, bias, eps, out, saved, None)
+    y, _, rstd, saved = _norm_forward(x, weight, bias, eps, out, True, saved)
     return y, rstd, saved
 
 
@@ -267,8 +278,7 @@ def layer_norm_backward(dy: torch.Tensor, x, mean: Optional[torch.Tensor], rstd:
     layer_norm_checkpoint kept (mean is then None).  dweight and dbias have
     the types of weight and bias and are None where those are.  dx has dy's
     type (out may be dy)."""
-    ld_dy = _matrix("dy", dy)
-    rows, cols = dy.shape
+    rows, cols, ld_dy, index = _matrix("dy", dy)
     dev = dy.device
     if isinstance(x, Checkpoint8):
         _need(x.shape == (rows, cols) and x.device == dev,
@@ -276,27 +286,32 @@ def layer_norm_backward(dy: torch.Tensor, x, mean: Optional[torch.Tensor], rstd:
         _need(mean is None, "mean must be None beside a checkpoint (it holds h itself)")
         saved, x_ptr, ld_x = x._fields(), 0, 0
     else:
-        ld_x = _matrix("x", x, dev, dy.shape)
+        ld_x = _matrix("x", x, index, rows, cols)[2]
         _need(x.dtype == dy.dtype, f"x and dy differ in type: {x.dtype}, {dy.dtype}")
         _need(mean is not None, "mean is needed beside x")
         saved, x_ptr = _NO_CKPT, x.data_ptr()
-    dx, ld_dx = _output("out", out, dy)
-    dw = torch.empty(cols, dtype=weight.dtype, device=dev) if weight is not None else None
-    db = torch.empty(cols, dtype=bias.dtype, device=dev) if bias is not None else None
-    _vector("bias", bias, dev, cols)
-    args = _norm_grad_args(
-        dy.data_ptr(), x_ptr, _vector("mean", mean, dev, rows, _F32),
-        _vector("rstd", rstd, dev, rows, _F32), _vector("weight", weight, dev, cols),
-        dx.data_ptr(), 0 if dw is None else dw.data_ptr(), 0 if db is None else db.data_ptr(),
-        *saved, rows, cols, ld_dy, ld_x, ld_dx, _dtype("dy", dy), _w_dtype(weight, bias))
-    _call_ws(dev, "muon_layer_norm_grad", "muon_layer_norm_grad_workspace", args)
+    dx, ld_dx = _output("out", out, dy, rows, cols)
+    dw = db = None
+    w_at = dw_at = db_at = 0
+    if weight is not None:
+        w_at = _vector("weight", weight, index, cols)
+        dw = torch.empty(cols, dtype=weight.dtype, device=dev)
+        dw_at = dw.data_ptr()
+    if bias is not None:
+        _vector("bias", bias, index, cols)
+        db = torch.empty(cols, dtype=bias.dtype, device=dev)
+        db_at = db.data_ptr()
+    _call_ws(index, "muon_layer_norm_grad", "muon_layer_norm_grad_workspace", _norm_grad_args(
+        dy.data_ptr(), x_ptr, _vector("mean", mean, index, rows, _F32),
+        _vector("rstd", rstd, index, rows, _F32), w_at, dx.data_ptr(), dw_at, db_at,
+        *saved, rows, cols, ld_dy, ld_x, ld_dx, _dtype("dy", dy), _w_dtype(weight, bias)), dev)
     return dx, dw, db
 
 
-def _gradient(name: str, t: torch.Tensor, shape, device):
+def _gradient(name: str, t: torch.Tensor, shape, index: int):
     """Checks a row-major gradient (n x k, or experts x n x k): (ld, stride)."""
-    if t.shape != shape or t.device != device:
-        raise ValueError(f"{name} must be {shape} on {device}, got {tuple(t.shape)} on {t.device}")
+    if t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{name} must be {shape} on cuda:{index}, got {tuple(t.shape)} on {t.device}")
     if t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be row-major (stride(-1) == 1)")
     return t.stride(-2), t.stride(0) if len(shape) == 3 else 0
@@ -314,30 +329,32 @@ def weight_grad(dy: torch.Tensor, x: Checkpoint8, *, weight: Optional[torch.Tens
     experts x n x k, matrix e over the tokens offsets[e] .. offsets[e + 1].
     add may be out (gradient accumulation).  out (or a new tensor of dtype):
     fp32 or bf16; the matrices of a Muon set's gradients can be given."""
-    ld_dy = _matrix("dy", dy)
-    _need(dy.dtype == torch.bfloat16, f"dy must be bfloat16, got {dy.dtype}")
-    rows, n = dy.shape
+    rows, n, ld_dy, index = _matrix("dy", dy)
+    _need(dy.dtype == _BF16, f"dy must be bfloat16, got {dy.dtype}")
     k, dev = x.cols, dy.device
-    _need(x.rows == rows and x.device == dev,
+    _need(x.q.shape[0] == rows and x.q.get_device() == index,
           f"x must hold {rows} rows on {dev}, has {x.rows} on {x.device}")
-    experts = 1
+    experts, offsets_at, shape = 1, 0, (n, k)
     if offsets is not None:
         _need(offsets.dim() == 1 and offsets.shape[0] >= 2, "offsets must be experts + 1 values")
         experts = offsets.shape[0] - 1
-        _vector("offsets", offsets, dev, experts + 1, torch.int32)
-    shape = (n, k) if offsets is None else (experts, n, k)
-    g = torch.empty(shape, dtype=dtype, device=dev) if out is None else out
-    ld_g, stride_g = _gradient("out", g, shape, dev)
-    ld_c = stride_c = 0
+        offsets_at = _vector("offsets", offsets, index, experts + 1, _I32)
+        shape = (experts, n, k)
+    if out is None:
+        g = torch.empty(shape, dtype=dtype, device=dev)
+        ld_g, stride_g = k, n * k
+    else:
+        g = out
+        ld_g, stride_g = _gradient("out", g, shape, index)
+    ld_c = stride_c = add_at = 0
     if add is not None:
-        ld_c, stride_c = _gradient("add", add, shape, dev)
+        ld_c, stride_c = _gradient("add", add, shape, index)
         _need(add.dtype == g.dtype, f"add and the result differ in type: {add.dtype}, {g.dtype}")
-    args = _weight_grad_args(
-        dy.data_ptr(), _vector("weight", weight, dev, k, _F32),
-        _vector("bias", bias, dev, k, _F32), 0 if add is None else add.data_ptr(),
-        g.data_ptr(), 0 if offsets is None else offsets.data_ptr(), *x._fields(),
-        rows, n, k, experts, ld_dy, ld_c, ld_g, stride_c, stride_g, _dtype("out", g))
-    _call_ws(dev, "muon_weight_grad", "muon_weight_grad_workspace", args)
+        add_at = add.data_ptr()
+    _call_ws(index, "muon_weight_grad", "muon_weight_grad_workspace", _weight_grad_args(
+        dy.data_ptr(), _vector("weight", weight, index, k, _F32),
+        _vector("bias", bias, index, k, _F32), add_at, g.data_ptr(), offsets_at, *x._fields(),
+        rows, n, k, experts, ld_dy, ld_c, ld_g, stride_c, stride_g, _dtype("out", g)), dev)
     return g
 
 
@@ -361,25 +378,24 @@ def route(logits: torch.Tensor, k: int, *, mask: Optional[torch.Tensor] = None,
     experts, fp32 or bf16): the k largest of every token, their softmax
     weights, counts per expert and the balance loss times coef.
     mask (bool or uint8, one per token): tokens with 0 take no part."""
-    ld = _matrix("logits", logits)
-    tokens, experts = logits.shape
+    tokens, experts, ld, index = _matrix("logits", logits)
     dev = logits.device
-    mask_ptr = 0
+    mask_at = 0
     if mask is not None:
         _need(mask.dtype in (torch.bool, torch.uint8), f"mask must be bool or uint8, got {mask.dtype}")
-        mask_ptr = _vector("mask", mask, dev, tokens)
-    _need(1 <= k <= min(experts, 32), f"k must be 1 .. min(experts, 32), got {k}")
+        mask_at = _vector("mask", mask, index, tokens)
+    if not 1 <= k <= min(experts, 32):
+        raise ValueError(f"k must be 1 .. min(experts, 32), got {k}")
     indices = torch.empty((tokens, k), dtype=_I32, device=dev)
     weights = torch.empty((tokens, k), dtype=_F32, device=dev)
     counts = torch.empty(experts, dtype=_I32, device=dev)
     offsets = torch.empty(experts + 1, dtype=_I32, device=dev)
     kept = torch.empty((), dtype=_I32, device=dev)
     loss = torch.empty((), dtype=_F32, device=dev)
-    args = _route_args(
-        logits.data_ptr(), mask_ptr, indices.data_ptr(), weights.data_ptr(), counts.data_ptr(),
+    _call_ws(index, "muon_route", "muon_route_workspace", _route_args(
+        logits.data_ptr(), mask_at, indices.data_ptr(), weights.data_ptr(), counts.data_ptr(),
         offsets.data_ptr(), loss.data_ptr(), kept.data_ptr(), tokens, experts, k, ld,
-        _dtype("logits", logits), bool(renormalise), coef)
-    _call_ws(dev, "muon_route", "muon_route_workspace", args)
+        _dtype("logits", logits), bool(renormalise), coef), dev)
     return Routing(indices, weights, counts, kept, offsets=offsets, loss=loss, coef=coef,
                    renormalise=renormalise)
 
@@ -391,38 +407,38 @@ def route_backward(logits: torch.Tensor, routing: Routing, *,
     """The gradient with respect to the logits, from that of the loss (one
     fp32 value on the device) and of the weights (tokens x k, fp32).  Returns
     dlogits of the logits' type (out may be logits)."""
-    ld = _matrix("logits", logits)
-    tokens, experts = logits.shape
-    dev = logits.device
+    tokens, experts, ld, index = _matrix("logits", logits)
     r = routing
-    _need(r.indices.dim() == 2, "routing.indices must be 2-D")
-    k = r.indices.shape[1]
-    for name, t, dtype, shape in (("indices", r.indices, _I32, (tokens, k)),
-                                  ("weights", r.weights, _F32, (tokens, k)),
-                                  ("counts", r.counts, _I32, (experts,))):
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"routing.{name} must be {dtype} {shape}, dense, on {dev}")
-    _need(r.kept.dtype == _I32 and r.kept.numel() == 1 and r.kept.device == dev,
-          "routing.kept must be one int32 value on the device")
+    indices, weights, counts = r.indices, r.weights, r.counts
+    _need(indices.dim() == 2, "routing.indices must be 2-D")
+    k = indices.shape[1]
+    if (indices.dtype != _I32 or weights.dtype != _F32 or counts.dtype != _I32
+            or indices.shape[0] != tokens or weights.shape != (tokens, k)
+            or counts.shape != (experts,) or r.kept.dtype != _I32 or r.kept.numel() != 1
+            or not (indices.is_contiguous() and weights.is_contiguous() and counts.is_contiguous())
+            or not (indices.get_device() == weights.get_device() == counts.get_device()
+                    == r.kept.get_device() == index)):
+        raise ValueError(f"routing does not belong to logits of {(tokens, experts)} on "
+                         f"{logits.device} (dense int32 indices and fp32 weights of tokens x k, "
+                         "int32 counts of the experts and kept)")
+    dloss_at = dweights_at = ld_dw = 0
     if dloss is not None:
-        _need(dloss.dtype == _F32 and dloss.numel() == 1 and dloss.device == dev,
-              "dloss must be one float32 value on the device")
-    ld_dw = 0
+        if dloss.dtype != _F32 or dloss.numel() != 1 or dloss.get_device() != index:
+            raise ValueError("dloss must be one float32 value on the device")
+        dloss_at = dloss.data_ptr()
     if dweights is not None:
-        ld_dw = _matrix("dweights", dweights, dev, (tokens, k))
-        _need(dweights.dtype == torch.float32, f"dweights must be float32, got {dweights.dtype}")
-    dz, ld_dz = _output("out", out, logits)
-    args = _route_grad_args(
-        logits.data_ptr(), r.indices.data_ptr(), r.weights.data_ptr(), r.counts.data_ptr(),
-        r.kept.data_ptr(), 0 if dloss is None else dloss.data_ptr(),
-        0 if dweights is None else dweights.data_ptr(), dz.data_ptr(), tokens, experts, k,
-        ld, ld_dw, ld_dz, _dtype("logits", logits), bool(r.renormalise), r.coef)
-    _call(dev, "muon_route_grad", args)
+        ld_dw = _matrix("dweights", dweights, index, tokens, k)[2]
+        _need(dweights.dtype == _F32, f"dweights must be float32, got {dweights.dtype}")
+        dweights_at = dweights.data_ptr()
+    dz, ld_dz = _output("out", out, logits, tokens, experts)
+    _call(index, "muon_route_grad", _route_grad_args(
+        logits.data_ptr(), indices.data_ptr(), weights.data_ptr(), counts.data_ptr(),
+        r.kept.data_ptr(), dloss_at, dweights_at, dz.data_ptr(), tokens, experts, k, ld, ld_dw,
+        ld_dz, _dtype("logits", logits), bool(r.renormalise), r.coef))
     return dz
 
 
 def ops_sync(device: Optional[int] = None) -> None:
     """Waits for the current stream and raises what the operators met on the
     GPU (MuonError; a bounded wait that ran out is MUON_ERR_TIMEOUT)."""
-    dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
-    _call(dev, "muon_ops_sync")
+    _call(torch.cuda.current_device() if device is None else device, "muon_ops_sync")
