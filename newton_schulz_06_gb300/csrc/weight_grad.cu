@@ -45,14 +45,15 @@ constexpr int W_DEC_WARPS = 8;                     // that decode one step
 constexpr int W_DEC_GROUPS = 2;                    // steps in turn
 constexpr int W_DEC_WARP0 = 2 + W_EPI_WARPS;
 constexpr int W_THREADS = 32 * (W_DEC_WARP0 + W_DEC_GROUPS * W_DEC_WARPS);
-constexpr int W_BLK = 32 * 64;                     // a staged block: 32 rows of 64 bytes
-constexpr int W_EPI_BYTES = 2 * W_BLK;             // two of them a warp
+constexpr int W_EPI_BYTES = 32 * 32 * 4;           // a warp's staged block: 32 x 32 sums
+constexpr int W_ORDER = 512;                       // experts that are taken by their size
 constexpr int W_TMEM_COLS = 512;
 constexpr int W_PAIRS = 76;                        // a pair per two of the 152 SMs
 constexpr int W_EPI_OFF = W_STAGES * (W_A_BYTES + W_B_BYTES + W_R_BYTES) + 1024;
-constexpr int W_SMEM = W_EPI_OFF + W_EPI_WARPS * W_EPI_BYTES + 1024;
+constexpr int W_ORDER_OFF = W_EPI_OFF + W_EPI_WARPS * W_EPI_BYTES;
+constexpr int W_SMEM = W_ORDER_OFF + W_ORDER * 2 + 1024;
 static_assert(W_SMEM <= 232448, "shared memory per CTA");
-constexpr int COLSUM_PARTS = 16;
+constexpr int COLSUM_PARTS = 32;      // of one matrix's tokens
 constexpr int BAND = 8;
 // fp32 results: the tensor cores cut a running sum off at its last place, so
 // that it shrinks by about 7e-9 of itself a product of 16 tokens (measured);
@@ -64,11 +65,8 @@ __device__ int g_ops_err;
 struct WgLaunch {
     CUtensorMap tm_dy;       // dY: dims {n, rows}, box {64, 64}, 128-byte swizzle
     CUtensorMap tm_q;        // q: dims {k, rows}, box {64, 64}, 64-byte swizzle
-    // where tiles go, if TMA can store there (tma_out): G, or the partial
-    // sums of a split; boxes of 32 rows of 64 bytes, 64-byte swizzle
-    CUtensorMap tm_out;
-    int32_t tma_out;
-    int32_t c_vec;           // C's rows allow 16-byte loads
+    int32_t vec;             // G's and C's rows lie on 16 bytes
+    int32_t sorted;          // experts are taken by their size
     int32_t chunk;           // steps that one accumulator sums (0: all of a tile's)
     muon_weight_grad_args a;
     const float* colsum;     // parts x experts x n sums of dY's columns (bias), or null
@@ -99,7 +97,8 @@ struct Item {
     int32_t t0, steps;       // first token, steps of 64 tokens
     int32_t end;             // the matrix's tokens end here
 };
-__device__ __forceinline__ Item item_at(const WgLaunch& p, int32_t it) {
+// order: the experts by their size (or null: as they are).
+__device__ __forceinline__ Item item_at(const WgLaunch& p, const uint16_t* order, int32_t it) {
     const uint32_t per = static_cast<uint32_t>(p.tiles_n) * p.tiles_k;
     const uint32_t es = static_cast<uint32_t>(it) / per;
     const uint32_t w = it - es * per;
@@ -114,6 +113,7 @@ __device__ __forceinline__ Item item_at(const WgLaunch& p, int32_t it) {
     x.k0 = static_cast<int32_t>(in / high) * 256;
     x.n0 = static_cast<int32_t>(band * BAND + in % high) * 256;
     int64_t begin, end;
+    if (order) x.e = order[x.e];
     segment(p.a, x.e, &begin, &end);
     const int64_t steps = (end - begin + W_TOK - 1) / W_TOK;
     int64_t s0 = 0, s1 = steps;
@@ -158,46 +158,56 @@ __device__ __forceinline__ void arrive_leader(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
-// Four 8-bit values of a word as bf16 pairs, times s (a power of two in both
-// halves), all exact.  0x4300 | (q & 127) is the bf16 number 128 + (q & 127),
-// and 0x4300 | (q & 128) is 128 or, where q is negative, 256: their
-// difference is q.
-__device__ __forceinline__ uint2 decode4(uint32_t w, __nv_bfloat162 s) {
-    const uint32_t mag = w & 0x7f7f7f7fu, neg = w & 0x80808080u;
+// The decoding of a block's values.  With b = q + 128 as the last byte of a
+// float of exponent field e + 17, the float is 2^(e - 110) + b 2^(e - 133);
+// less the same with b = 128 it is q 2^(e - 133), exact, which bf16 holds
+// exactly too: a byte shuffle a value, and one addition and one conversion a
+// pair.  (In bf16 arithmetic the same took half as many instructions again,
+// and the decoding warps' arithmetic is what the tensor cores wait for.)
+struct BlockScale {
+    uint32_t base;           // the exponent field in its place
+    float up;                // 2^64 for the blocks that need it, else 1
+};
+// A token or column that is not there: its values become 0.
+constexpr uint32_t NO_SCALE = 256;
+// Blocks above 2^110 or so have no exponent field 17 further up: theirs are
+// 64 lower, and what comes out is multiplied (scale_is_high).
+__device__ __forceinline__ bool scale_is_high(uint32_t e) { return e >= 238u && e < 255u; }
+__device__ __forceinline__ BlockScale block_scale(uint32_t e) {
+    BlockScale s;
+    s.up = scale_is_high(e) ? 18446744073709551616.f : 1.f;
+    // NaN: an infinity's exponent, less a NaN; none: so small that bf16
+    // rounds it to 0
+    s.base = e == NO_SCALE ? 1u << 23 : e == 255u ? 255u << 23 : (e + 17u - (scale_is_high(e) ? 64u : 0u)) << 23;
+    return s;
+}
+template <bool HIGH>
+__device__ __forceinline__ uint2 decode4(uint32_t w, BlockScale s) {
+    const uint32_t x = w ^ 0x80808080u;
+    const float2 zero = both(-__uint_as_float(s.base | 128u));
     uint32_t r[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint32_t m = __byte_perm(mag, 0x43434343u, i ? 0x4342u : 0x4140u);
-        const uint32_t c = __byte_perm(neg, 0x43434343u, i ? 0x4342u : 0x4140u);
-        const __nv_bfloat162 v = __hmul2(__hsub2(reinterpret_cast<const __nv_bfloat162&>(m),
-                                                 reinterpret_cast<const __nv_bfloat162&>(c)), s);
+        float2 f = add2(make_float2(__uint_as_float(__byte_perm(x, s.base, 0x7650u + 2 * i)),
+                                    __uint_as_float(__byte_perm(x, s.base, 0x7651u + 2 * i))), zero);
+        if (HIGH) f = mul2(f, both(s.up));
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
         r[i] = reinterpret_cast<const uint32_t&>(v);
     }
     return make_uint2(r[0], r[1]);
 }
-// 2^(e - 133) in bf16 (subnormal below e = 7), NaN for e = 255; 0 for
-// NO_SCALE, the mark of a token or column that is not there.
-constexpr uint32_t NO_SCALE = 256;
-__device__ __forceinline__ __nv_bfloat162 scale_bf16x2(uint32_t e) {
-    const uint32_t b = e == NO_SCALE ? 0u
-                       : e == 255u   ? 0x7fc0u
-                       : e >= 7u     ? (e - 6u) << 7
-                                     : 1u << e;
-    const uint32_t both = b | b << 16;
-    return reinterpret_cast<const __nv_bfloat162&>(both);
-}
-
-__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-            reinterpret_cast<uint64_t>(tmap)),
-        "r"(x), "r"(y), "r"(z), "r"(src)
-        : "memory");
-}
-// Byte offset of 16-byte chunk q of row r in a staged block (TMA's 64-byte
-// swizzle).
-__device__ __forceinline__ uint32_t sw64(int r, int q) {
-    return static_cast<uint32_t>(r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+// 32 values of a block to their places in the tensor cores' layout.
+template <bool HIGH>
+__device__ __forceinline__ void decode_block(const uint4 (&q)[2], BlockScale s, uint8_t* to, int blk,
+                                             uint32_t sw) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint2 v0 = decode4<HIGH>(q[h].x, s), v1 = decode4<HIGH>(q[h].y, s);
+        const uint2 v2 = decode4<HIGH>(q[h].z, s), v3 = decode4<HIGH>(q[h].w, s);
+        *reinterpret_cast<uint4*>(to + (((blk * 4 + h * 2) ^ sw) << 4)) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+        *reinterpret_cast<uint4*>(to + (((blk * 4 + h * 2 + 1) ^ sw) << 4)) =
+            make_uint4(v2.x, v2.y, v3.x, v3.y);
+    }
 }
 
 // What becomes of a sum of row i and column j of matrix e: the norm's weight
@@ -216,34 +226,45 @@ __device__ __forceinline__ float column_sum(const WgLaunch& p, int64_t e, int64_
     return s;
 }
 
-// v += C[at .. at + 31], of which `left` are in the row.
-__device__ __forceinline__ void add_c(const WgLaunch& p, int64_t at, int left, float (&v)[32]) {
-    if (left >= 32 && p.c_vec) {
-        if (p.a.g_dtype == MUON_F32) {
-            const float4* c = reinterpret_cast<const float4*>(static_cast<const float*>(p.a.c) + at);
+// v += 32 neighbouring elements of a bf16 gradient that lie on 16 bytes.
+__device__ __forceinline__ void add32(const __nv_bfloat16* p, float (&v)[32]) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float4 f = c[q];
-                v[4 * q] += f.x;
-                v[4 * q + 1] += f.y;
-                v[4 * q + 2] += f.z;
-                v[4 * q + 3] += f.w;
-            }
-        } else {
-            const __nv_bfloat16* c = static_cast<const __nv_bfloat16*>(p.a.c) + at;
+    for (int q = 0; q < 4; ++q) {
+        float f[8];
+        load8_bf16(p + 8 * q, f);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float f[8];
-                load8_bf16(c + 8 * q, f);
-#pragma unroll
-                for (int u = 0; u < 8; ++u) v[8 * q + u] += f[u];
-            }
-        }
-        return;
+        for (int u = 0; u < 8; ++u) v[8 * q + u] += f[u];
     }
+}
+
+// 32 rows of 128 bytes that a warp staged (16-byte pieces, their places XORed
+// with the row) to a gradient, four whole rows a store; with add (fp32) the
+// same rows of C are added on the way.
+template <bool ADD>
+__device__ __forceinline__ void store_rows(const uint4* blk, char* to, int64_t pitch, const char* add,
+                                           int64_t add_pitch, int rows, int lane) {
+    const int piece = lane & 7, sub = lane >> 3;
+    to += sub * pitch + piece * 16;
+    if (ADD) add += sub * add_pitch + piece * 16;
+    pitch *= 4;
+    add_pitch *= 4;
 #pragma unroll
-    for (int u = 0; u < 32; ++u)
-        if (u < left) v[u] += load_any(p.a.c, p.a.g_dtype, at + u);
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + sub;
+        if (r < rows) {
+            uint4 v = blk[r * 8 + (piece ^ (r & 7))];
+            if (ADD) {
+                const float4 f = *reinterpret_cast<const float4*>(add);
+                v.x = __float_as_uint(__uint_as_float(v.x) + f.x);
+                v.y = __float_as_uint(__uint_as_float(v.y) + f.y);
+                v.z = __float_as_uint(__uint_as_float(v.z) + f.z);
+                v.w = __float_as_uint(__uint_as_float(v.w) + f.w);
+            }
+            *reinterpret_cast<uint4*>(to) = v;
+        }
+        to += pitch;
+        if (ADD) add += add_pitch;
+    }
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
@@ -292,11 +313,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    grid_dependency_wait();
+    allow_dependent_launch();
+    // Experts by their size, the largest first: with tiles dealt out in turn,
+    // no pair then has more than about one tile's steps above another (a
+    // quarter of the time, with sizes as a router gives them).
+    uint16_t* order = nullptr;
+    if (p.sorted) {
+        order = reinterpret_cast<uint16_t*>(smem + W_ORDER_OFF);
+        const int experts = static_cast<int>(p.a.experts);
+        int64_t* size = reinterpret_cast<int64_t*>(smem);    // the stages are not in use yet
+        for (int e = threadIdx.x; e < experts; e += W_THREADS) {
+            int64_t begin, end;
+            segment(p.a, e, &begin, &end);
+            size[e] = end - begin;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < experts; e += W_THREADS) {
+            const int64_t mine = size[e];
+            int rank_of = 0;
+            for (int o = 0; o < experts; ++o)
+                rank_of += size[o] > mine || (size[o] == mine && o < e);
+            order[rank_of] = static_cast<uint16_t>(e);
+        }
+        // before the stages' first loads (they are written by another proxy)
+        fence_proxy_async_smem();
+    }
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
-    grid_dependency_wait();
-    allow_dependent_launch();
     const uint32_t tmem_base = *tmem_slot;
     const uint64_t limit = p.wait_limit_ns;
 
@@ -309,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             for (int s = 0; s < W_STAGES; ++s) issued[s] = 0;
             bool ok = true;
             for (int32_t it = pair; ok && it < p.items; it += npairs) {
-                const Item x = item_at(p, it);
+                const Item x = item_at(p, order, it);
                 const int a0 = x.n0 + static_cast<int>(rank) * 128;
                 const int b0 = x.k0 + static_cast<int>(rank) * 128;
                 for (int s = 0; s < x.steps; ++s) {
@@ -351,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             const uint64_t b_desc = smem_desc(smem_u32(sB), W_BOX, 1024);
             const uint32_t idesc = instr_desc(256, 256, 1) | (1u << 15);
             for (int32_t it = pair; ok && it < p.items; it += npairs) {
-                const Item x = item_at(p, it);
+                const Item x = item_at(p, order, it);
                 if (x.steps == 0) continue;
                 const int chunk = p.chunk ? p.chunk : x.steps;
                 for (int s0 = 0; ok && s0 < x.steps; s0 += chunk) {
@@ -413,54 +458,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         int stage = group;
         uint32_t phase = 0;
         bool ok = true;
-        for (int32_t it = pair; ok && it < p.items; it += npairs) {
-            const Item x = item_at(p, it);
+        // the scale bytes come four of this group's steps at a time, one
+        // round ahead, also across tiles
+        uint32_t nxt[4];
+        auto fetch = [&](const Item& x, int s) {
             const int eb = (x.k0 + static_cast<int>(rank) * 128) / CKPT_BLOCK + box * 2 + blk;
             const uint8_t* ep = p.a.saved.e + eb;
-            const bool col_ok = eb < nblk;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int su = s + u * W_DEC_GROUPS;
+                const int64_t t = int64_t(x.t0) + su * W_TOK + row;
+                nxt[u] = (eb < nblk && su < x.steps && t < x.end) ? ep[t * p.a.saved.ld_e] : NO_SCALE;
+            }
+        };
+        Item x, y{};
+        int32_t it = pair;
+        if (it < p.items) {
+            x = item_at(p, order, it);
+            fetch(x, group);
+        }
+        for (; ok && it < p.items; it += npairs, x = y) {
             const int first = (group - static_cast<int>(before)) & (W_DEC_GROUPS - 1);
             before += x.steps;
-            // the scale bytes come four of this group's steps at a time, one
-            // round ahead
-            uint32_t nxt[4];
-            auto fetch = [&](int s) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int su = s + u * W_DEC_GROUPS;
-                    const int64_t t = int64_t(x.t0) + su * W_TOK + row;
-                    nxt[u] = (col_ok && su < x.steps && t < x.end) ? ep[t * p.a.saved.ld_e] : NO_SCALE;
-                }
-            };
-            fetch(first);
+            const int y_first = (group - static_cast<int>(before)) & (W_DEC_GROUPS - 1);
+            const bool more = it + npairs < p.items;
+            if (more) y = item_at(p, order, it + npairs);
+            if (first >= x.steps && more) fetch(y, y_first);
             for (int s = first; ok && s < x.steps; s += 4 * W_DEC_GROUPS) {
                 uint32_t cur[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) cur[u] = nxt[u];
-                fetch(s + 4 * W_DEC_GROUPS);
+                if (s + 4 * W_DEC_GROUPS < x.steps) fetch(x, s + 4 * W_DEC_GROUPS);
+                else if (more) fetch(y, y_first);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int su = s + u * W_DEC_GROUPS;
                     if (su >= x.steps) break;
-                    const uint32_t fb = smem_u32(&full_bar[stage]);
-                    const bool got = wait_soon(fb, phase, abort_flag, &g_ops_err, limit);
+                    const bool got = wait_soon(smem_u32(&full_bar[stage]), phase, abort_flag,
+                                               &g_ops_err, limit);
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
                     }
-                    const __nv_bfloat162 sc = scale_bf16x2(cur[u]);
                     const uint8_t* r = sR + stage * W_R_BYTES + src;
-                    uint8_t* b = sB + stage * W_B_BYTES + dst;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint4 q = *reinterpret_cast<const uint4*>(
-                            r + (((blk * 2 + h) ^ src_sw) << 4));
-                        const uint2 v0 = decode4(q.x, sc), v1 = decode4(q.y, sc);
-                        const uint2 v2 = decode4(q.z, sc), v3 = decode4(q.w, sc);
-                        *reinterpret_cast<uint4*>(b + (((blk * 4 + h * 2) ^ dst_sw) << 4)) =
-                            make_uint4(v0.x, v0.y, v1.x, v1.y);
-                        *reinterpret_cast<uint4*>(b + (((blk * 4 + h * 2 + 1) ^ dst_sw) << 4)) =
-                            make_uint4(v2.x, v2.y, v3.x, v3.y);
-                    }
+                    const uint4 q[2] = {
+                        *reinterpret_cast<const uint4*>(r + (((blk * 2) ^ src_sw) << 4)),
+                        *reinterpret_cast<const uint4*>(r + (((blk * 2 + 1) ^ src_sw) << 4))};
+                    const BlockScale sc = block_scale(cur[u]);
+                    uint8_t* const to = sB + stage * W_B_BYTES + dst;
+                    if (__any_sync(0xffffffffu, scale_is_high(cur[u])))
+                        decode_block<true>(q, sc, to, blk, dst_sw);
+                    else
+                        decode_block<false>(q, sc, to, blk, dst_sw);
                     const int left = x.end - (x.t0 + su * W_TOK);
                     if (left < W_TOK) {
                         // tokens of the next matrix in dY's stage: 0 times a
@@ -482,10 +531,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
     } else {
         // --------------------------------------------------------- write out
         const int lg = warp & 3;                    // this warp's 32 TMEM lanes
-        uint8_t* const stage0 = smem + W_EPI_OFF + (warp - 2) * W_EPI_BYTES;
+        uint4* const blk = reinterpret_cast<uint4*>(smem + W_EPI_OFF + (warp - 2) * W_EPI_BYTES);
         const uint32_t tempty_leader = map_to_rank(smem_u32(tempty_bar), 0);
-        const bool f32_out = p.splits > 1 || p.a.g_dtype == MUON_F32;
-        uint32_t stores = 0;
         uint32_t uses[2] = {0, 0};
         uint32_t first = 0;
         bool ok = true;
@@ -502,23 +549,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * acc);
         };
-        // the next of the warp's two staging blocks, once its last TMA store
-        // has read it
-        auto next_block = [&]() {
-            if (lane == 0) bulk_wait_read1();
-            __syncwarp();
-            return stage0 + (stores++ & 1u) * W_BLK;
-        };
-        auto store_block = [&](uint8_t* blk, int x, int y, int z) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                tma_store_3d(&p.tm_out, smem_u32(blk), x, y, z);
-                bulk_commit();
-            }
-        };
         for (int32_t it = pair; ok && it < p.items; it += npairs) {
-            const Item x = item_at(p, it);
+            const Item x = item_at(p, order, it);
             const uint32_t tlane = tmem_base + (static_cast<uint32_t>(lg * 32) << 16);
             const uint32_t taddr = tlane + first * 256;
             if (x.steps) {
@@ -550,8 +582,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             const int r0 = x.n0 + static_cast<int>(rank) * 128 + lg * 32;
             const int n = static_cast<int>(p.a.n), k = static_cast<int>(p.a.k);
             const int rows = min(32, n - r0);
+            // a part of a split leaves its sums as they are
             const bool apply = p.splits == 1;
             const float sum = (apply && p.colsum && lane < rows) ? column_sum(p, x.e, r0 + lane) : 0.f;
+            const int64_t ld = apply ? p.a.ld_g : p.ld_part;
+            const int64_t g0 = apply ? x.e * p.a.stride_g + r0 * ld
+                                     : ((int64_t(x.split) * p.a.experts + x.e) * n + r0) * ld;
+            const int64_t c0 = x.e * p.a.stride_c + r0 * p.a.ld_c;
+            void* const g = apply ? p.a.g : p.part;
+            const int g_type = apply ? p.a.g_dtype : MUON_F32;
+            const void* const add = apply ? p.a.c : nullptr;
+            const bool f32 = g_type == MUON_F32;
+            const int64_t size = f32 ? 4 : 2;
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
                 const int j0 = x.k0 + 32 * c;
@@ -571,63 +613,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                         v[u] = fmaf(__shfl_sync(0xffffffffu, bl, u), sum,
                                     v[u] * __shfl_sync(0xffffffffu, wl, u));
                 }
-                if (p.tma_out) {
-                    if (apply && p.a.c && lane < rows) {
-                        const int64_t at = x.e * p.a.stride_c + int64_t(r0 + lane) * p.a.ld_c + j0;
-                        add_c(p, at, k - j0, v);
-                    }
-                    const int z = apply ? x.e : static_cast<int>(x.split * p.a.experts + x.e);
-                    if (f32_out) {
+                // Staged, and stored as rows of 128 bytes: 32 columns of fp32,
+                // or 64 of bf16 from two rounds.  Lanes that store their own
+                // rows straight from registers touch 32 lines a store, which
+                // took three times as long.
+                const int odd = f32 ? 0 : c & 1;
+                const int row0 = f32 ? j0 : x.k0 + 64 * (c >> 1);
+                if (p.vec && row0 + (f32 ? 32 : 64) <= k) {
+                    if (!odd) __syncwarp();          // the last rows have been read
+                    if (f32) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (j0 + 16 * h >= k) break;
-                            uint8_t* blk = next_block();
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                *reinterpret_cast<float4*>(blk + sw64(lane, q)) =
-                                    make_float4(v[16 * h + 4 * q], v[16 * h + 4 * q + 1],
-                                                v[16 * h + 4 * q + 2], v[16 * h + 4 * q + 3]);
-                            store_block(blk, j0 + 16 * h, r0, z);
-                        }
+                        for (int q = 0; q < 8; ++q)
+                            blk[lane * 8 + (q ^ (lane & 7))] =
+                                make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                           __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
                     } else {
-                        uint8_t* blk = next_block();
+                        if (add && lane < rows)
+                            add32(static_cast<const __nv_bfloat16*>(add) + c0 + lane * p.a.ld_c + j0, v);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             float t[8];
 #pragma unroll
                             for (int u = 0; u < 8; ++u) t[u] = v[8 * q + u];
-                            store8_bf16(reinterpret_cast<__nv_bfloat16*>(blk + sw64(lane, q)), t);
+                            store8_bf16(reinterpret_cast<__nv_bfloat16*>(
+                                            &blk[lane * 8 + ((q + 4 * odd) ^ (lane & 7))]), t);
                         }
-                        store_block(blk, j0, r0, z);
+                        if (!odd) continue;
                     }
+                    __syncwarp();
+                    char* const to = static_cast<char*>(g) + (g0 + row0) * size;
+                    if (f32 && add)
+                        store_rows<true>(blk, to, ld * size, static_cast<const char*>(add) + (c0 + j0) * 4,
+                                         p.a.ld_c * 4, rows, lane);
+                    else
+                        store_rows<false>(blk, to, ld * size, nullptr, 0, rows, lane);
                     continue;
                 }
-                // rows that TMA cannot store to: turned in shared memory, then
                 // row by row
-                float* blk = reinterpret_cast<float*>(stage0);
+                float* const f = reinterpret_cast<float*>(blk);
+                __syncwarp();
 #pragma unroll
-                for (int u = 0; u < 32; ++u) blk[lane * 32 + (u ^ lane)] = v[u];
+                for (int u = 0; u < 32; ++u) f[lane * 32 + (u ^ lane)] = v[u];
                 __syncwarp();
                 if (j0 + lane < k) {
-                    int64_t g_at = x.e * p.a.stride_g + int64_t(r0) * p.a.ld_g + j0 + lane;
-                    int64_t c_at = x.e * p.a.stride_c + int64_t(r0) * p.a.ld_c + j0 + lane;
+                    int64_t at = g0 + j0 + lane, c_at = c0 + j0 + lane;
 #pragma unroll 4
                     for (int r = 0; r < rows; ++r) {
-                        float g = blk[r * 32 + (lane ^ r)];
-                        if (p.a.c) g += load_any(p.a.c, p.a.g_dtype, c_at);
-                        store_any(p.a.g, p.a.g_dtype, g_at, g);
-                        g_at += p.a.ld_g;
+                        float t = f[r * 32 + (lane ^ r)];
+                        if (add) t += load_any(add, g_type, c_at);
+                        store_any(g, g_type, at, t);
+                        at += ld;
                         c_at += p.a.ld_c;
                     }
                 }
-                __syncwarp();
             }
             if (x.steps) {
                 release(first);
                 first ^= 1;
             }
         }
-        if (lane == 0) bulk_wait_all0();
     }
 
     tc_fence_before();
@@ -656,30 +700,43 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
 }
 
 // Sums of dY's columns over each matrix's tokens (gridDim.z parts of them):
-// 64 columns and 4 rows at a time in a block.
+// 256 columns and 8 rows at a time in a block.
 __global__ void __launch_bounds__(256)
     colsum_kernel(const __grid_constant__ muon_weight_grad_args a, float* out) {
-    __shared__ float red[256];
+    __shared__ float red[8][256];
     grid_dependency_wait();
     allow_dependent_launch();
-    const int64_t i = blockIdx.x * int64_t(64) + (threadIdx.x & 63);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int i = blockIdx.x * 256 + lane * 8;
+    const int n = static_cast<int>(a.n);
+    const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(a.dy) + i;
     for (int64_t e = blockIdx.y; e < a.experts; e += gridDim.y) {
         int64_t begin, end;
         segment(a, e, &begin, &end);
         const int64_t len = end - begin;
         const int64_t t0 = begin + len * blockIdx.z / gridDim.z;
         const int64_t t1 = begin + len * (blockIdx.z + 1) / gridDim.z;
-        float s = 0.f;
-        if (i < a.n)
-            for (int64_t t = t0 + (threadIdx.x >> 6); t < t1; t += 4)
-                s += __bfloat162float(static_cast<const __nv_bfloat16*>(a.dy)[t * a.ld_dy + i]);
+        float2 s[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+#pragma unroll 4
+        for (int64_t t = t0 + warp; t < t1; t += 8) {
+            Vec<__nv_bfloat16, false> v;
+            float2 f[4];
+            v.load(dy + t * a.ld_dy, n - i);
+            v.get(f);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[u] = add2(s[u], f[u]);
+        }
         __syncthreads();
-        red[threadIdx.x] = s;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<float2*>(&red[warp][lane * 8 + 2 * u]) = s[u];
         __syncthreads();
-        if (threadIdx.x < 64 && i < a.n)
-            out[(blockIdx.z * a.experts + e) * a.n + i] =
-                (red[threadIdx.x] + red[threadIdx.x + 64]) +
-                (red[threadIdx.x + 128] + red[threadIdx.x + 192]);
+        const int col = blockIdx.x * 256 + threadIdx.x;
+        if (col < n) {
+            float sum = 0.f;
+            for (int w = 0; w < 8; ++w) sum += red[w][threadIdx.x];
+            out[(blockIdx.z * a.experts + e) * a.n + col] = sum;
+        }
     }
 }
 
@@ -743,7 +800,7 @@ Layout layout(const muon_weight_grad_args& a) {
     }
     if (l.splits > 1) {
         l.part = l.bytes;
-        l.ld_part = ceil_div(a.k, 4) * 4;
+        l.ld_part = ceil_div(a.k, 8) * 8;
         l.bytes += align256(size_t(l.splits) * a.experts * a.n * l.ld_part * 4);
     }
     return l;
@@ -774,26 +831,11 @@ bool encode_map(CUtensorMap* tm, CUtensorMapDataType type, size_t size, const vo
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A map to store tiles of `count` matrices of n x k with: boxes of 32 rows of
-// 64 bytes.
-bool encode_out(CUtensorMap* tm, bool f32, void* base, int64_t count, int64_t n, int64_t k,
-                int64_t ld, int64_t stride) {
-    if (!encoder()) return false;
-    const size_t size = f32 ? 4 : 2;
-    cuuint64_t dims[3] = {cuuint64_t(k), cuuint64_t(n), cuuint64_t(count)};
-    cuuint64_t strides[2] = {cuuint64_t(ld) * size, cuuint64_t(stride) * size};
-    cuuint32_t box[3] = {cuuint32_t(64 / size), 32, 1}, el[3] = {1, 1, 1};
-    return encoder()(tm, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                     base, dims, strides, box, el, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Whether 16-byte accesses and TMA suit a gradient's rows.
-bool rows_aligned(const void* p, size_t size, const muon_weight_grad_args& a, int64_t ld,
-                  int64_t stride) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.n <= 1 || ld * size % 16 == 0) &&
-           (a.experts <= 1 || stride * size % 16 == 0);
+// Whether a gradient's rows lie on `bytes`.
+bool rows_on(int64_t bytes, const void* p, int64_t size, const muon_weight_grad_args& a, int64_t ld,
+             int64_t stride) {
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (a.n <= 1 || ld * size % bytes == 0) &&
+           (a.experts <= 1 || stride * size % bytes == 0);
 }
 
 }  // namespace
@@ -819,29 +861,26 @@ cudaError_t launch_weight_grad(const muon_weight_grad_args& a, void* ws, cudaStr
     p.tiles_k = static_cast<int32_t>(ceil_div(a.k, 256));
     p.items = static_cast<int32_t>(tiles(a) * l.splits);
     p.wait_limit_ns = wait_limit_ns();
-    const size_t size = a.g_dtype == MUON_F32 ? 4 : 2;
+    const int64_t size = a.g_dtype == MUON_F32 ? 4 : 2;
     if (a.g_dtype == MUON_F32) p.chunk = CHUNK_STEPS;
-    if (a.c) p.c_vec = rows_aligned(a.c, size, a, a.ld_c, a.stride_c);
+    p.sorted = a.experts > 1 && a.experts <= W_ORDER;
     if (l.splits > 1) {
         p.part = reinterpret_cast<float*>(base + l.part);
         p.ld_part = l.ld_part;
-        p.tma_out = 1;
-        if (!encode_out(&p.tm_out, true, p.part, l.splits * a.experts, a.n, a.k, l.ld_part,
-                        a.n * l.ld_part))
-            return cudaErrorInvalidValue;
-    } else if (rows_aligned(a.g, size, a, a.ld_g, a.stride_g)) {
-        const int64_t ld = a.n > 1 ? a.ld_g : ceil_div(a.k, 8) * 8;
-        p.tma_out = 1;
-        if (!encode_out(&p.tm_out, size == 4, a.g, a.experts, a.n, a.k, ld,
-                        a.experts > 1 ? a.stride_g : a.n * ld))
-            return cudaErrorInvalidValue;
+        p.vec = 1;
+    } else {
+        auto on = [&](int64_t bytes) {
+            return rows_on(bytes, a.g, size, a, a.ld_g, a.stride_g) &&
+                   (!a.c || rows_on(bytes, a.c, size, a, a.ld_c, a.stride_c));
+        };
+        p.vec = on(16);
     }
     cudaError_t e;
     if (a.bias) {
         p.colsum = reinterpret_cast<float*>(base + l.colsum);
         p.colsum_parts = l.colsum_parts;
         e = launch_kernel(colsum_kernel,
-                          dim3(static_cast<unsigned>(ceil_div(a.n, 64)),
+                          dim3(static_cast<unsigned>(ceil_div(a.n, 256)),
                                static_cast<unsigned>(a.experts < 32768 ? a.experts : 32768),
                                static_cast<unsigned>(l.colsum_parts)),
                           dim3(256), 0, s, a, reinterpret_cast<float*>(base + l.colsum));
