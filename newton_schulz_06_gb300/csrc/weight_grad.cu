@@ -13,7 +13,7 @@
 //     sum_t dy[t][i] (h[t][j] w[j] + b[j]) = w[j] G0[i][j] + b[j] sum_t dy[t][i].
 //
 // Roles in a CTA: warp 0 loads, warp 1 issues the products (leader only),
-// warps 2-5 write tiles out, warps 6-13 decode.  Two accumulators in tensor
+// warps 2-9 write tiles out, warps 10-17 decode.  Two accumulators in tensor
 // memory, so a tile is written out while the next one's products run.  Pairs
 // walk the tiles in turn; how many tokens a tile has is read from the offsets
 // on the device, and every role finds the same number.
@@ -40,12 +40,13 @@ constexpr int W_A_BYTES = 2 * W_BOX;
 constexpr int W_B_BYTES = 2 * W_BOX;
 constexpr int W_R_BYTES = 2 * W_RBOX;
 constexpr int W_TX = W_A_BYTES + W_R_BYTES;
-constexpr int W_EPI_WARPS = 4;
-constexpr int W_DEC_WARPS = 8;                     // that decode one step
+constexpr int W_EPI_WARPS = 8;                     // two for 32 rows of the tile
+constexpr int W_DEC_WARPS = 4;                     // that decode one step
+constexpr int W_DEC_BLOCKS = 8 / W_DEC_WARPS;      // blocks of 32 values a thread decodes
 constexpr int W_DEC_GROUPS = 2;                    // steps in turn
 constexpr int W_DEC_WARP0 = 2 + W_EPI_WARPS;
 constexpr int W_THREADS = 32 * (W_DEC_WARP0 + W_DEC_GROUPS * W_DEC_WARPS);
-constexpr int W_EPI_BYTES = 32 * 32 * 4;           // a warp's staged block: 32 x 32 sums
+constexpr int W_EPI_BYTES = 32 * 64;               // a warp's staged block: 32 rows of 64 bytes
 constexpr int W_ORDER = 512;                       // experts that are taken by their size
 constexpr int W_TMEM_COLS = 512;
 constexpr int W_PAIRS = 76;                        // a pair per two of the 152 SMs
@@ -158,6 +159,37 @@ __device__ __forceinline__ void arrive_leader(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// 16 fp32 columns of this warp's TMEM lanes (asked for; there after
+// tmem_ld_wait).
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_wait() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Those at `to` plus those at `from`, to `to`; complete on return.
+__device__ __forceinline__ void tmem_add16(uint32_t to, uint32_t from) {
+    uint32_t a[16], b[16];
+    tmem_ld16(to, a);
+    tmem_ld16(from, b);
+    tmem_ld_wait();
+#pragma unroll
+    for (int u = 0; u < 16; ++u) a[u] = __float_as_uint(__uint_as_float(a[u]) + __uint_as_float(b[u]));
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(to),
+        "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7]), "r"(a[8]),
+        "r"(a[9]), "r"(a[10]), "r"(a[11]), "r"(a[12]), "r"(a[13]), "r"(a[14]), "r"(a[15])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // The decoding of a block's values.  With b = q + 128 as the last byte of a
 // float of exponent field e + 17, the float is 2^(e - 110) + b 2^(e - 133);
 // less the same with b = 128 it is q 2^(e - 133), exact, which bf16 holds
@@ -226,10 +258,10 @@ __device__ __forceinline__ float column_sum(const WgLaunch& p, int64_t e, int64_
     return s;
 }
 
-// v += 32 neighbouring elements of a bf16 gradient that lie on 16 bytes.
-__device__ __forceinline__ void add32(const __nv_bfloat16* p, float (&v)[32]) {
+// v += 16 neighbouring elements of a bf16 gradient that lie on 16 bytes.
+__device__ __forceinline__ void add16(const __nv_bfloat16* p, float (&v)[16]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
         float f[8];
         load8_bf16(p + 8 * q, f);
 #pragma unroll
@@ -237,22 +269,44 @@ __device__ __forceinline__ void add32(const __nv_bfloat16* p, float (&v)[32]) {
     }
 }
 
-// 32 rows of 128 bytes that a warp staged (16-byte pieces, their places XORed
-// with the row) to a gradient, four whole rows a store; with add (fp32) the
-// same rows of C are added on the way.
+// 16 columns of 32 sums, staged with the columns XORed with the row, to a
+// gradient element by element (rows off 16 bytes, a row's last columns): two
+// rows at a time.  `left`: the columns there are.
+__device__ __noinline__ void store_elements(const float* f, void* g, int g_type, int64_t at, int64_t ld,
+                                            const void* add, int64_t c_at, int64_t ld_c, int rows,
+                                            int left) {
+    const int lane = threadIdx.x & 31, col = lane & 15, two = lane >> 4;
+    if (col >= left) return;
+    at += two * ld + col;
+    c_at += two * ld_c + col;
+#pragma unroll 4
+    for (int r = two; r < rows; r += 2) {
+        float t = f[r * 16 + (col ^ (r & 15))];
+        if (add) t += load_any(add, g_type, c_at);
+        store_any(g, g_type, at, t);
+        at += 2 * ld;
+        c_at += 2 * ld_c;
+    }
+}
+
+// Place of 16-byte piece q of row r in a staged block of 32 rows of 64 bytes.
+__device__ __forceinline__ int staged(int r, int q) { return r * 4 + (q ^ ((r >> 1) & 3)); }
+
+// A staged block to a gradient, eight rows a store; with add (fp32) the same
+// rows of C are added on the way.
 template <bool ADD>
 __device__ __forceinline__ void store_rows(const uint4* blk, char* to, int64_t pitch, const char* add,
                                            int64_t add_pitch, int rows, int lane) {
-    const int piece = lane & 7, sub = lane >> 3;
+    const int piece = lane & 3, sub = lane >> 2;
     to += sub * pitch + piece * 16;
     if (ADD) add += sub * add_pitch + piece * 16;
-    pitch *= 4;
-    add_pitch *= 4;
+    pitch *= 8;
+    add_pitch *= 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + sub;
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + sub;
         if (r < rows) {
-            uint4 v = blk[r * 8 + (piece ^ (r & 7))];
+            uint4 v = blk[staged(r, piece)];
             if (ADD) {
                 const float4 f = *reinterpret_cast<const float4*>(add);
                 v.x = __float_as_uint(__uint_as_float(v.x) + f.x);
@@ -267,6 +321,8 @@ __device__ __forceinline__ void store_rows(const uint4* blk, char* to, int64_t p
     }
 }
 
+// F32: what is stored is fp32 (G, or the sums of a part of a split).
+template <bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
     weight_grad_kernel(const __grid_constant__ WgLaunch p) {
     extern __shared__ uint8_t smem_raw[];
@@ -439,14 +495,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         }
     } else if (warp >= W_DEC_WARP0) {
         // ----------------------------------------------------------- decode
-        // Two groups of warps take the steps in turn.  A thread turns one
-        // block of 32 values of one token: 16 tokens and the two blocks of a
-        // 64-wide box in a warp, so that eight lanes' 16-byte accesses fall
+        // Two groups of warps take the steps in turn.  A thread turns blocks of
+        // 32 values: 16 tokens and the two blocks of a 64-wide box in a warp at
+        // a time, so that eight lanes' 16-byte accesses fall
         // on all banks in both swizzles.
         const int group = (warp - W_DEC_WARP0) / W_DEC_WARPS;
         const int dw = (warp - W_DEC_WARP0) % W_DEC_WARPS;
         const int box = dw & 1;
-        const int row = (dw >> 1) * 16 + (lane >> 1);
+        const int row = (dw >> 1) * 16 * W_DEC_BLOCKS + (lane >> 1);   // and 16 rows on, ...
         const int blk = lane & 1;
         const uint32_t src = box * W_RBOX + row * 64;
         const uint32_t src_sw = (row >> 1) & 3;
@@ -460,15 +516,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         bool ok = true;
         // the scale bytes come four of this group's steps at a time, one
         // round ahead, also across tiles
-        uint32_t nxt[4];
+        uint32_t nxt[4][W_DEC_BLOCKS];
         auto fetch = [&](const Item& x, int s) {
             const int eb = (x.k0 + static_cast<int>(rank) * 128) / CKPT_BLOCK + box * 2 + blk;
             const uint8_t* ep = p.a.saved.e + eb;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int su = s + u * W_DEC_GROUPS;
-                const int64_t t = int64_t(x.t0) + su * W_TOK + row;
-                nxt[u] = (eb < nblk && su < x.steps && t < x.end) ? ep[t * p.a.saved.ld_e] : NO_SCALE;
+#pragma unroll
+                for (int i = 0; i < W_DEC_BLOCKS; ++i) {
+                    const int64_t t = int64_t(x.t0) + su * W_TOK + row + 16 * i;
+                    nxt[u][i] =
+                        (eb < nblk && su < x.steps && t < x.end) ? ep[t * p.a.saved.ld_e] : NO_SCALE;
+                }
             }
         };
         Item x, y{};
@@ -485,9 +545,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             if (more) y = item_at(p, order, it + npairs);
             if (first >= x.steps && more) fetch(y, y_first);
             for (int s = first; ok && s < x.steps; s += 4 * W_DEC_GROUPS) {
-                uint32_t cur[4];
+                uint32_t cur[4][W_DEC_BLOCKS];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) cur[u] = nxt[u];
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int i = 0; i < W_DEC_BLOCKS; ++i) cur[u][i] = nxt[u][i];
                 if (s + 4 * W_DEC_GROUPS < x.steps) fetch(x, s + 4 * W_DEC_GROUPS);
                 else if (more) fetch(y, y_first);
 #pragma unroll
@@ -500,16 +562,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                         ok = false;
                         break;
                     }
-                    const uint8_t* r = sR + stage * W_R_BYTES + src;
-                    const uint4 q[2] = {
-                        *reinterpret_cast<const uint4*>(r + (((blk * 2) ^ src_sw) << 4)),
-                        *reinterpret_cast<const uint4*>(r + (((blk * 2 + 1) ^ src_sw) << 4))};
-                    const BlockScale sc = block_scale(cur[u]);
-                    uint8_t* const to = sB + stage * W_B_BYTES + dst;
-                    if (__any_sync(0xffffffffu, scale_is_high(cur[u])))
-                        decode_block<true>(q, sc, to, blk, dst_sw);
-                    else
-                        decode_block<false>(q, sc, to, blk, dst_sw);
+                    bool high = false;
+                    uint4 q[W_DEC_BLOCKS][2];
+#pragma unroll
+                    for (int i = 0; i < W_DEC_BLOCKS; ++i) {
+                        // 16 rows on, the swizzles are the same
+                        const uint8_t* r = sR + stage * W_R_BYTES + src + i * 16 * 64;
+                        q[i][0] = *reinterpret_cast<const uint4*>(r + (((blk * 2) ^ src_sw) << 4));
+                        q[i][1] = *reinterpret_cast<const uint4*>(r + (((blk * 2 + 1) ^ src_sw) << 4));
+                        high |= scale_is_high(cur[u][i]);
+                    }
+                    high = __any_sync(0xffffffffu, high);
+#pragma unroll
+                    for (int i = 0; i < W_DEC_BLOCKS; ++i) {
+                        const BlockScale sc = block_scale(cur[u][i]);
+                        uint8_t* const to = sB + stage * W_B_BYTES + dst + i * 16 * 128;
+                        if (high) decode_block<true>(q[i], sc, to, blk, dst_sw);
+                        else decode_block<false>(q[i], sc, to, blk, dst_sw);
+                    }
                     const int left = x.end - (x.t0 + su * W_TOK);
                     if (left < W_TOK) {
                         // tokens of the next matrix in dY's stage: 0 times a
@@ -530,7 +600,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         }
     } else {
         // --------------------------------------------------------- write out
-        const int lg = warp & 3;                    // this warp's 32 TMEM lanes
+        const int lg = warp & 3;                    // this warp's 32 TMEM lanes,
+        const int c_first = (warp - 2) / 4 * 4;     // and four of its 32-column blocks
         uint4* const blk = reinterpret_cast<uint4*>(smem + W_EPI_OFF + (warp - 2) * W_EPI_BYTES);
         const uint32_t tempty_leader = map_to_rank(smem_u32(tempty_bar), 0);
         uint32_t uses[2] = {0, 0};
@@ -567,14 +638,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                         break;
                     }
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        float v[32], w[32];
-                        tmem_ld32(taddr + 32 * c, v);
-                        tmem_ld32(tlane + (first ^ 1) * 256 + 32 * c, w);
-#pragma unroll
-                        for (int u = 0; u < 32; ++u) v[u] += w[u];
-                        tmem_st32(taddr + 32 * c, v);
-                    }
+                    for (int c = 2 * c_first; c < 2 * (c_first + 4); ++c)
+                        tmem_add16(taddr + 16 * c, tlane + (first ^ 1) * 256 + 16 * c);
                     release(first ^ 1);
                 }
                 if (!ok) break;
@@ -590,81 +655,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                                      : ((int64_t(x.split) * p.a.experts + x.e) * n + r0) * ld;
             const int64_t c0 = x.e * p.a.stride_c + r0 * p.a.ld_c;
             void* const g = apply ? p.a.g : p.part;
-            const int g_type = apply ? p.a.g_dtype : MUON_F32;
             const void* const add = apply ? p.a.c : nullptr;
-            const bool f32 = g_type == MUON_F32;
-            const int64_t size = f32 ? 4 : 2;
+            constexpr int size = F32 ? 4 : 2;
+            if (rows > 0) {
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-                const int j0 = x.k0 + 32 * c;
-                if (rows <= 0 || j0 >= k) break;
-                float v[32];
-                if (x.steps) {
-                    tmem_ld32(taddr + 32 * c, v);
-                } else {
+                for (int c = 0; c < 8; ++c) {
+                    const int j0 = x.k0 + 32 * c_first + 16 * c;
+                    if (j0 >= k) break;
+                    uint32_t raw[16];
+                    float v[16];
+                    if (x.steps) {
+                        tmem_ld16(taddr + 32 * c_first + 16 * c, raw);
+                        tmem_ld_wait();
+                    }
 #pragma unroll
-                    for (int u = 0; u < 32; ++u) v[u] = 0.f;
-                }
-                if (apply && (p.a.weight || p.a.bias)) {
-                    const float wl = p.a.weight && j0 + lane < k ? p.a.weight[j0 + lane] : 1.f;
-                    const float bl = p.a.bias && j0 + lane < k ? p.a.bias[j0 + lane] : 0.f;
+                    for (int u = 0; u < 16; ++u) v[u] = x.steps ? __uint_as_float(raw[u]) : 0.f;
+                    if (apply && (p.a.weight || p.a.bias)) {
+                        const int j = j0 + (lane & 15);
+                        const float wl = p.a.weight && j < k ? p.a.weight[j] : 1.f;
+                        const float bl = p.a.bias && j < k ? p.a.bias[j] : 0.f;
 #pragma unroll
-                    for (int u = 0; u < 32; ++u)
-                        v[u] = fmaf(__shfl_sync(0xffffffffu, bl, u), sum,
-                                    v[u] * __shfl_sync(0xffffffffu, wl, u));
-                }
-                // Staged, and stored as rows of 128 bytes: 32 columns of fp32,
-                // or 64 of bf16 from two rounds.  Lanes that store their own
-                // rows straight from registers touch 32 lines a store, which
-                // took three times as long.
-                const int odd = f32 ? 0 : c & 1;
-                const int row0 = f32 ? j0 : x.k0 + 64 * (c >> 1);
-                if (p.vec && row0 + (f32 ? 32 : 64) <= k) {
-                    if (!odd) __syncwarp();          // the last rows have been read
-                    if (f32) {
+                        for (int u = 0; u < 16; ++u)
+                            v[u] = fmaf(__shfl_sync(0xffffffffu, bl, u), sum,
+                                        v[u] * __shfl_sync(0xffffffffu, wl, u));
+                    }
+                    // Staged, and stored as rows of 64 bytes (lanes that store
+                    // their own rows straight from registers touch 32 lines a
+                    // store, which took three times as long): 16 columns of
+                    // fp32, or 32 of bf16 from two rounds.
+                    const int odd = F32 ? 0 : c & 1;
+                    const int row0 = j0 - 16 * odd;
+                    if (p.vec && row0 + (F32 ? 16 : 32) <= k) {
+                        if (!odd) __syncwarp();      // the last rows have been read
+                        if constexpr (F32) {
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            blk[lane * 8 + (q ^ (lane & 7))] =
-                                make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                           __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
-                    } else {
-                        if (add && lane < rows)
-                            add32(static_cast<const __nv_bfloat16*>(add) + c0 + lane * p.a.ld_c + j0, v);
+                            for (int q = 0; q < 4; ++q)
+                                blk[staged(lane, q)] = make_uint4(
+                                    __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                    __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+                        } else {
+                            if (add && lane < rows)
+                                add16(static_cast<const __nv_bfloat16*>(add) + c0 + lane * p.a.ld_c + j0, v);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            float t[8];
+                            for (int q = 0; q < 2; ++q) {
+                                float t[8];
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) t[u] = v[8 * q + u];
-                            store8_bf16(reinterpret_cast<__nv_bfloat16*>(
-                                            &blk[lane * 8 + ((q + 4 * odd) ^ (lane & 7))]), t);
+                                for (int u = 0; u < 8; ++u) t[u] = v[8 * q + u];
+                                store8_bf16(reinterpret_cast<__nv_bfloat16*>(
+                                                &blk[staged(lane, q + 2 * odd)]), t);
+                            }
+                            if (!odd) continue;
                         }
-                        if (!odd) continue;
+                        __syncwarp();
+                        char* const to = static_cast<char*>(g) + (g0 + row0) * size;
+                        if (F32 && add)
+                            store_rows<true>(blk, to, ld * size,
+                                             static_cast<const char*>(add) + (c0 + j0) * 4, p.a.ld_c * 4,
+                                             rows, lane);
+                        else
+                            store_rows<false>(blk, to, ld * size, nullptr, 0, rows, lane);
+                        continue;
                     }
+                    float* const f = reinterpret_cast<float*>(blk);
                     __syncwarp();
-                    char* const to = static_cast<char*>(g) + (g0 + row0) * size;
-                    if (f32 && add)
-                        store_rows<true>(blk, to, ld * size, static_cast<const char*>(add) + (c0 + j0) * 4,
-                                         p.a.ld_c * 4, rows, lane);
-                    else
-                        store_rows<false>(blk, to, ld * size, nullptr, 0, rows, lane);
-                    continue;
-                }
-                // row by row
-                float* const f = reinterpret_cast<float*>(blk);
-                __syncwarp();
 #pragma unroll
-                for (int u = 0; u < 32; ++u) f[lane * 32 + (u ^ lane)] = v[u];
-                __syncwarp();
-                if (j0 + lane < k) {
-                    int64_t at = g0 + j0 + lane, c_at = c0 + j0 + lane;
-#pragma unroll 4
-                    for (int r = 0; r < rows; ++r) {
-                        float t = f[r * 32 + (lane ^ r)];
-                        if (add) t += load_any(add, g_type, c_at);
-                        store_any(g, g_type, at, t);
-                        at += ld;
-                        c_at += p.a.ld_c;
-                    }
+                    for (int u = 0; u < 16; ++u) f[lane * 16 + (u ^ (lane & 15))] = v[u];
+                    __syncwarp();
+                    store_elements(f, g, F32 ? MUON_F32 : MUON_BF16, g0 + j0, ld, add, c0 + j0, p.a.ld_c,
+                                   rows, k - j0);
+                    __syncwarp();
                 }
             }
             if (x.steps) {
@@ -909,13 +968,18 @@ cudaError_t launch_weight_grad(const muon_weight_grad_args& a, void* ws, cudaStr
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-        e = cudaFuncSetAttribute(weight_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 W_SMEM);
+        e = cudaFuncSetAttribute(weight_grad_kernel<false>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, W_SMEM);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(weight_grad_kernel<true>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, W_SMEM);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_done[dev] = 1;
     }
     const int pairs = p.items < W_PAIRS ? p.items : W_PAIRS;
-    e = launch_kernel(weight_grad_kernel, dim3(2 * pairs), dim3(W_THREADS), W_SMEM, s, p);
+    const bool f32 = l.splits > 1 || a.g_dtype == MUON_F32;
+    e = launch_kernel(f32 ? weight_grad_kernel<true> : weight_grad_kernel<false>, dim3(2 * pairs),
+                      dim3(W_THREADS), W_SMEM, s, p);
     if (e != cudaSuccess || l.splits == 1) return e;
     return launch_kernel(weight_grad_join_kernel, dim3(grid_for(a.experts * a.n * a.k)), dim3(256),
                          0, s, p);
