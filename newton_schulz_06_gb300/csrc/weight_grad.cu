@@ -572,13 +572,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                         q[i][1] = *reinterpret_cast<const uint4*>(r + (((blk * 2 + 1) ^ src_sw) << 4));
                         high |= scale_is_high(cur[u][i]);
                     }
-                    high = __any_sync(0xffffffffu, high);
+                    uint8_t* const to = sB + stage * W_B_BYTES + dst;
+                    if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
-                    for (int i = 0; i < W_DEC_BLOCKS; ++i) {
-                        const BlockScale sc = block_scale(cur[u][i]);
-                        uint8_t* const to = sB + stage * W_B_BYTES + dst + i * 16 * 128;
-                        if (high) decode_block<true>(q[i], sc, to, blk, dst_sw);
-                        else decode_block<false>(q[i], sc, to, blk, dst_sw);
+                        for (int i = 0; i < W_DEC_BLOCKS; ++i)
+                            decode_block<true>(q[i], block_scale(cur[u][i]), to + i * 16 * 128, blk, dst_sw);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < W_DEC_BLOCKS; ++i)
+                            decode_block<false>(q[i], block_scale(cur[u][i]), to + i * 16 * 128, blk, dst_sw);
                     }
                     const int left = x.end - (x.t0 + su * W_TOK);
                     if (left < W_TOK) {
