@@ -54,7 +54,7 @@ constexpr int W_EPI_OFF = W_STAGES * (W_A_BYTES + W_B_BYTES + W_R_BYTES) + 1024;
 constexpr int W_ORDER_OFF = W_EPI_OFF + W_EPI_WARPS * W_EPI_BYTES;
 constexpr int W_SMEM = W_ORDER_OFF + W_ORDER * 2 + 1024;
 static_assert(W_SMEM <= 232448, "shared memory per CTA");
-constexpr int COLSUM_PARTS = 32;      // of one matrix's tokens
+constexpr int COLSUM_PARTS = 16;      // of one matrix's tokens (experts: one part each)
 constexpr int BAND = 8;
 // fp32 results: the tensor cores cut a running sum off at its last place, so
 // that it shrinks by about 7e-9 of itself a product of 16 tokens (measured);
@@ -253,8 +253,9 @@ __device__ __forceinline__ void finish(const muon_weight_grad_args& a, int64_t e
 
 __device__ __forceinline__ float column_sum(const WgLaunch& p, int64_t e, int64_t i) {
     float s = 0.f;
-    for (int q = 0; q < p.colsum_parts; ++q)
-        s += p.colsum[(int64_t(q) * p.a.experts + e) * p.a.n + i];
+    if (p.colsum_parts == 1) return p.colsum[e * p.a.n + i];
+#pragma unroll
+    for (int q = 0; q < COLSUM_PARTS; ++q) s += p.colsum[q * p.a.n + i];
     return s;
 }
 
@@ -299,25 +300,29 @@ __device__ __forceinline__ void store_rows(const uint4* blk, char* to, int64_t p
                                            int64_t add_pitch, int rows, int lane) {
     const int piece = lane & 3, sub = lane >> 2;
     to += sub * pitch + piece * 16;
-    if (ADD) add += sub * add_pitch + piece * 16;
-    pitch *= 8;
-    add_pitch *= 8;
+    // C's rows before the first store: C may be G, so that the compiler must
+    // keep a load behind the stores before it
+    float4 f[4];
+    if (ADD) {
+        add += sub * add_pitch + piece * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (8 * i + sub < rows) f[i] = *reinterpret_cast<const float4*>(add + 8 * i * add_pitch);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 8 * i + sub;
         if (r < rows) {
             uint4 v = blk[staged(r, piece)];
             if (ADD) {
-                const float4 f = *reinterpret_cast<const float4*>(add);
-                v.x = __float_as_uint(__uint_as_float(v.x) + f.x);
-                v.y = __float_as_uint(__uint_as_float(v.y) + f.y);
-                v.z = __float_as_uint(__uint_as_float(v.z) + f.z);
-                v.w = __float_as_uint(__uint_as_float(v.w) + f.w);
+                v.x = __float_as_uint(__uint_as_float(v.x) + f[i].x);
+                v.y = __float_as_uint(__uint_as_float(v.y) + f[i].y);
+                v.z = __float_as_uint(__uint_as_float(v.z) + f[i].z);
+                v.w = __float_as_uint(__uint_as_float(v.w) + f[i].w);
             }
             *reinterpret_cast<uint4*>(to) = v;
         }
-        to += pitch;
-        if (ADD) add += add_pitch;
+        to += 8 * pitch;
     }
 }
 
@@ -745,18 +750,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
     }
 }
 
-// The splits' partial sums in order, then the epilogue.
+// The splits' partial sums in order, then the epilogue: a block has 1024
+// columns of a row, four neighbouring ones a thread.
 __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_constant__ WgLaunch p) {
     grid_dependency_wait();
     allow_dependent_launch();
-    const int64_t n = p.a.n, k = p.a.k, size = p.a.experts * n * k;
-    for (int64_t u = blockIdx.x * int64_t(256) + threadIdx.x; u < size; u += int64_t(gridDim.x) * 256) {
-        const int64_t j = u % k, i = u / k % n, e = u / (n * k);
-        float g = 0.f;
-        const int64_t at = (e * n + i) * p.ld_part + j;
-        for (int s = 0; s < p.splits; ++s) g += p.part[s * p.a.experts * n * p.ld_part + at];
-        finish(p.a, e, i, j, g, p.a.weight ? p.a.weight[j] : 1.f, p.a.bias ? p.a.bias[j] : 0.f,
-               p.colsum ? column_sum(p, e, i) : 0.f);
+    const int k = static_cast<int>(p.a.k), j = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (j >= k) return;
+    const int64_t rows = p.a.experts * p.a.n;
+    const int64_t size = rows * p.ld_part;
+    float w[4], b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        w[u] = p.a.weight && j + u < k ? p.a.weight[j + u] : 1.f;
+        b[u] = p.a.bias && j + u < k ? p.a.bias[j + u] : 0.f;
+    }
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+        const int64_t e = p.a.experts == 1 ? 0 : row / p.a.n, i = row - e * p.a.n;
+        const float* part = p.part + row * p.ld_part + j;
+        float g[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int s = 0; s < p.splits; ++s) {
+            const float4 f = *reinterpret_cast<const float4*>(part + s * size);
+            g[0] += f.x;
+            g[1] += f.y;
+            g[2] += f.z;
+            g[3] += f.w;
+        }
+        const float sum = p.colsum ? column_sum(p, e, i) : 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u < k) finish(p.a, e, i, j + u, g[u], w[u], b[u], sum);
     }
 }
 
@@ -778,7 +802,7 @@ __global__ void __launch_bounds__(256)
         const int64_t t0 = begin + len * blockIdx.z / gridDim.z;
         const int64_t t1 = begin + len * (blockIdx.z + 1) / gridDim.z;
         float2 s[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t t = t0 + warp; t < t1; t += 8) {
             Vec<__nv_bfloat16, false> v;
             float2 f[4];
@@ -983,8 +1007,12 @@ cudaError_t launch_weight_grad(const muon_weight_grad_args& a, void* ws, cudaStr
     e = launch_kernel(f32 ? weight_grad_kernel<true> : weight_grad_kernel<false>, dim3(2 * pairs),
                       dim3(W_THREADS), W_SMEM, s, p);
     if (e != cudaSuccess || l.splits == 1) return e;
-    return launch_kernel(weight_grad_join_kernel, dim3(grid_for(a.experts * a.n * a.k)), dim3(256),
-                         0, s, p);
+    const int64_t rows = a.experts * a.n, across = ceil_div(a.k, 1024);
+    const int64_t down = ceil_div(152 * 8, across);
+    return launch_kernel(weight_grad_join_kernel,
+                         dim3(static_cast<unsigned>(across),
+                              static_cast<unsigned>(rows < down ? rows : down)),
+                         dim3(256), 0, s, p);
 }
 
 cudaError_t ops_status(cudaStream_t s, int* code) {
