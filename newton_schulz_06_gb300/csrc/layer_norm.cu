@@ -300,11 +300,13 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
 #pragma unroll
             for (int j = 0; j < F2; ++j) h[j] = mul2(add2(v[i][j], both(-mean)), both(rstd));
             if constexpr (CKPT) {
-                // past the row's end the checkpoint holds zeros
+                if (padded != cols || valid <= 0) {
+                    // past the row's end the checkpoint holds zeros
 #pragma unroll
-                for (int j = 0; j < F2; ++j) {
-                    if (AL ? valid <= 0 : 2 * j >= valid) h[j].x = 0.f;
-                    if (AL ? valid <= 0 : 2 * j + 1 >= valid) h[j].y = 0.f;
+                    for (int j = 0; j < F2; ++j) {
+                        if (2 * j >= valid) h[j].x = 0.f;
+                        if (2 * j + 1 >= valid) h[j].y = 0.f;
+                    }
                 }
                 encode_vec<VE>(a.saved, r, c, c < padded, h);
             }
@@ -661,8 +663,8 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     __syncthreads();
     const T* dy0 = static_cast<const T*>(a.dy);
     const T* x0 = static_cast<const T*>(a.x);
-    auto load = [&](int64_t r, int s) {
-        if (r >= a.rows) return;
+    auto load = [&](uint32_t r, int s) {
+        if (r >= static_cast<uint32_t>(a.rows)) return;
         const uint32_t bar = ptx::smem_u32(&full[s]);
         const uint32_t dst = ptx::smem_u32(ring) + s * p.stage_bytes;
         const Pieces dy(dy0 + r * a.ld_dy, cols * sizeof(T));
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
         bulk_load(dst + p.x_off, x.first, x.bytes, bar);
     };
     if (threadIdx.x == 0)
-        for (int s = 0; s < stages; ++s) load(blockIdx.x + int64_t(s) * gridDim.x, s);
+        for (int s = 0; s < stages; ++s) load(blockIdx.x + s * gridDim.x, s);
     float2 dw[NV * F2], db[NV * F2];
 #pragma unroll
     for (int i = 0; i < NV * F2; ++i) dw[i] = db[i] = both(0.f);
@@ -681,36 +683,27 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     uint32_t phase = 0;
     uint32_t e_next[NV];
     float rstd_next = 0.f, mean_next = 0.f;
-    // pointers walk along with the rows (a 64-bit product a tensor and row
-    // costs as much as the row's arithmetic)
-    const float* rstd_at = a.rstd + blockIdx.x;
-    const float* mean_at = CKPT ? nullptr : a.mean + blockIdx.x;
-    const uint8_t* e_at = CKPT ? a.saved.e + blockIdx.x * a.saved.ld_e + c0 / CKPT_BLOCK : nullptr;
-    const int64_t e_step = CKPT ? gridDim.x * a.saved.ld_e : 0;
-    T* dx = static_cast<T*>(a.dx) + blockIdx.x * a.ld_dx + c0;
-    const int64_t dx_step = gridDim.x * a.ld_dx;
-    auto fetch = [&]() {
-        rstd_next = *rstd_at;
-        rstd_at += gridDim.x;
+    auto fetch = [&](uint32_t row) {
+        rstd_next = a.rstd[row];
         if constexpr (CKPT) {
+            const uint8_t* at = a.saved.e + row * a.saved.ld_e + c0 / CKPT_BLOCK;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (c0 + i * step < cols) e_next[i] = e_at[i * (step / CKPT_BLOCK)];
-            e_at += e_step;
+                if (c0 + i * step < cols) e_next[i] = at[i * (step / CKPT_BLOCK)];
         } else {
-            mean_next = *mean_at;
-            mean_at += gridDim.x;
+            mean_next = a.mean[row];
         }
     };
-    fetch();
-    int left = static_cast<int>((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
-    int64_t r = blockIdx.x;
-    for (; left > 0; --left, r += gridDim.x, dx += dx_step, odd ^= 1) {
+    // rows are below 2^31, and a block's stride is small
+    const uint32_t rows = static_cast<uint32_t>(a.rows);
+    uint32_t r = blockIdx.x;
+    fetch(r);
+    for (; r < rows; r += gridDim.x, odd ^= 1) {
         const float rstd = rstd_next, shift = -mean_next * rstd_next;
         uint32_t e[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) e[i] = CKPT ? e_next[i] : 0u;
-        if (left > 1) fetch();
+        if (r + gridDim.x < rows) fetch(r + gridDim.x);
         ring_wait(&full[stage], phase, &abort_flag, p.wait_limit_ns);
         const uint8_t* at = ring + stage * p.stage_bytes;
         const T* dy_row = reinterpret_cast<const T*>(at + (AL ? 0 : Pieces::lead(dy0 + r * a.ld_dy)));
@@ -737,8 +730,9 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
         }
         const float2 t = block_sum2(s0.x + s0.y, s1.x + s1.y, red[odd]);
         // its barrier says that every thread has read the stage
-        if (KEEP && threadIdx.x == 0) load(r + int64_t(stages) * gridDim.x, stage);
+        if (KEEP && threadIdx.x == 0) load(r + stages * gridDim.x, stage);
         const float n0 = -t.x * inv_n * rstd, n1 = -t.y * inv_n * rstd;
+        T* const dx = static_cast<T*>(a.dx) + r * a.ld_dx + c0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
@@ -757,7 +751,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
         }
         if (!KEEP) {
             __syncthreads();
-            if (threadIdx.x == 0) load(r + int64_t(stages) * gridDim.x, stage);
+            if (threadIdx.x == 0) load(r + stages * gridDim.x, stage);
         }
         if (++stage == stages) {
             stage = 0;

@@ -300,6 +300,12 @@ __device__ __forceinline__ uint32_t encode_q(float v, uint32_t e, float inv) {
     const float x = fmaxf(fminf(v * inv * 64.f, 127.f), -127.f);
     return e == 255u ? 0u : __float_as_uint(x + 12582912.f);
 }
+// The larger of m and |v|; a NaN wins.
+__device__ __forceinline__ float max_mag(float m, float v) {
+    float r;
+    asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(m), "f"(v));
+    return r;
+}
 
 // VE values from q, whose block's power of two is p (exact).
 template <int VE>
@@ -334,21 +340,37 @@ __device__ __forceinline__ float decode_one(const muon_ckpt8& s, int64_t r, int6
 template <int VE>
 __device__ __forceinline__ void encode_vec(const muon_ckpt8& s, int64_t r, int c, bool write,
                                            const float2 (&f)[VE / 2]) {
-    uint32_t top = 0;
+    float largest = 0.f;
 #pragma unroll
-    for (int i = 0; i < VE / 2; ++i) top = max(top, max(mag_bits(f[i].x), mag_bits(f[i].y)));
+    for (int i = 0; i < VE / 2; ++i) largest = max_mag(max_mag(largest, f[i].x), f[i].y);
+    uint32_t top = __float_as_uint(largest);
 #pragma unroll
     for (int o = 1; o < CKPT_BLOCK / VE; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (!write) return;
     const uint32_t e = scale_byte(top);
-    const float inv = scale_inv(e);
-    int8_t* q = s.q + r * s.ld_q + c;
+    // Blocks of ordinary size whose largest value does not round up to 128:
+    // one multiplication and addition rounds (see encode_q).  The others go
+    // the longer way.
+    const bool plain = e - 7u < 248u - 7u && (top & 0x7fffffu) < 0x7f0000u;
     uint32_t w[VE / 4];
+    if (__all_sync(0xffffffffu, plain)) {
+        const float2 scale = both(__uint_as_float((260u - e) << 23)), magic = both(12582912.f);
 #pragma unroll
-    for (int i = 0; i < VE / 4; ++i)
-        w[i] = __byte_perm(__byte_perm(encode_q(f[2 * i].x, e, inv), encode_q(f[2 * i].y, e, inv), 0x0040),
-                           __byte_perm(encode_q(f[2 * i + 1].x, e, inv),
-                                       encode_q(f[2 * i + 1].y, e, inv), 0x0040), 0x5410);
+        for (int i = 0; i < VE / 4; ++i) {
+            const float2 a = fma2(f[2 * i], scale, magic), b = fma2(f[2 * i + 1], scale, magic);
+            w[i] = __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                               __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+        }
+    } else {
+        const float inv = scale_inv(e);
+#pragma unroll
+        for (int i = 0; i < VE / 4; ++i)
+            w[i] = __byte_perm(
+                __byte_perm(encode_q(f[2 * i].x, e, inv), encode_q(f[2 * i].y, e, inv), 0x0040),
+                __byte_perm(encode_q(f[2 * i + 1].x, e, inv), encode_q(f[2 * i + 1].y, e, inv), 0x0040),
+                0x5410);
+    }
+    if (!write) return;
+    int8_t* q = s.q + r * s.ld_q + c;
     if constexpr (VE == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[VE / 4 - 1]);
     else *reinterpret_cast<uint32_t*>(q) = w[0];
     if ((c & (CKPT_BLOCK - 1)) == 0) s.e[r * s.ld_e + c / CKPT_BLOCK] = static_cast<uint8_t>(e);
