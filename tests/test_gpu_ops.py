@@ -622,3 +622,125 @@ def test_operators_in_a_captured_graph(ns):
         torch.cuda.synchronize()
         for a, c in zip(got, everything()):
             assert torch.equal(a, c)
+
+
+# ------------------------------------------------------ together, and far out
+
+def test_example_block_trains():
+    """The operators together, as a training step uses them: the block's
+    gradients are those of the same block with autograd in fp64, within what
+    bf16 and 8-bit activations cost, and its loss falls."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "train_moe_block.py")
+    spec = importlib.util.spec_from_file_location("train_moe_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    block = ex.Block(64, 32, 8, 2)
+    x = rand(80, 128, 64, dtype=BF)
+    out = block.forward(x)
+    dout = rand(81, 128, 64)
+    dx = block.backward(dout)
+    r = block.kept[3]
+    leaves = [t.to("cpu", D).requires_grad_() for t in (x, block.router, block.w1, block.w2, block.gain,
+                                                        block.shift)]
+    xr, router, w1, w2, gain, shift = leaves
+    y = torch.nn.functional.layer_norm(xr, (64,), gain, shift)
+    p = torch.softmax(y @ router.t(), -1)
+    idx = r.indices.cpu().long()
+    w = p.gather(1, idx)
+    w = w / w.sum(-1, keepdim=True)
+    # which units are active is the block's choice, as the experts taken are: a ReLU that
+    # switches by a rounding is no error of a gradient
+    order, active = block.kept[4].cpu(), block.kept[8].cpu()
+    on = torch.empty(128 * 2, 32, dtype=torch.bool)
+    on[order] = active
+    u = torch.einsum("tkih,th->tki", w1[idx], y) * on.view(128, 2, 32)
+    ref = xr + (w[..., None] * torch.einsum("tkhi,tki->tkh", w2[idx], u)).sum(1)
+    counts = torch.bincount(idx.flatten(), minlength=8).to(D)
+    balance = 0.01 * 8 / (2 * 128) * (counts * p.mean(0)).sum()
+    ((ref * to64(dout)).sum() + balance).backward()
+    # every value has passed about six roundings to bf16 (2^-9 each) and one to 8 bits (2^-7 of
+    # its block's largest, to nearest): a few percent of the norm
+    for got, want in ((out, ref), (dx, xr.grad), (block.g_router, router.grad), (block.g_w1, w1.grad),
+                      (block.g_w2, w2.grad), (block.d_gain, gain.grad), (block.d_shift, shift.grad)):
+        want = want.detach()
+        assert (to64(got) - want).norm() <= 0.06 * want.norm()
+    block.muon.close()
+    losses = ex.train(steps=25, tokens=512, hidden=128, inner=64, experts=8)
+    assert sum(losses[-5:]) < 0.8 * sum(losses[:5]), losses
+
+
+def _needs(gib):
+    free, _ = torch.cuda.mem_get_info()
+    if free < gib << 30:
+        pytest.skip(f"needs {gib} GiB of device memory")
+
+
+def test_layer_norm_past_32_bits(ns):
+    """Rows whose elements lie past 2^31, forward, checkpoint and backward: the
+    same bits as the same rows on their own."""
+    _needs(32)
+    rows, cols, n = 270000, 8192, 40
+    x = torch.empty(rows, cols, dtype=BF, device=DEV)
+    x.view(-1).view(torch.int16).random_(0x3c00, 0x4000)        # bf16 between 2^-7 and 2
+    w, b = rand(82, cols), rand(83, cols)
+    y, rstd, saved = ns.layer_norm_checkpoint(x, w, b)
+    tail = x[-n:].clone()
+    y1, rstd1, saved1 = ns.layer_norm_checkpoint(tail, w, b)
+    assert torch.equal(rstd[-n:], rstd1)
+    close(y[-n:], y1, 2.0 ** -7 * to64(y1).abs() + 1e-5, "y")
+    assert (saved.q[-n:].int() - saved1.q.int()).abs().max() <= 1
+    dx, dw, db = ns.layer_norm_backward(x, saved, None, rstd, w, b)
+    dx1, _, _ = ns.layer_norm_backward(tail, ns.Checkpoint8(saved.q[-n:], saved.e[-n:], cols), None,
+                                       rstd[-n:], w, b)
+    close(dx[-n:], dx1, 2.0 ** -7 * to64(dx1).abs() + 1e-4, "dx")
+    want = x[:, :8].sum(0, dtype=D)
+    close(db[:8], want, 1e-4 * to64(want).abs(), "dbias")       # rows of one part add up in chains of 900
+    del y, dx
+    v = saved.values()
+    assert torch.equal(v[-n:], ns.Checkpoint8(saved.q[-n:], saved.e[-n:], cols).values())
+    c = ns.checkpoint8(x)
+    assert torch.equal(c.q[-n:], ns.checkpoint8(tail).q)
+
+
+def test_weight_grad_past_32_bits(ns):
+    """Tokens whose elements lie past 2^31, and a result that passes it."""
+    _needs(32)
+    t, n, k = 560000, 4096, 256
+    dy = torch.empty(t, n, dtype=BF, device=DEV)
+    dy.view(-1).view(torch.int16).random_(0x3c00, 0x4000)
+    saved = ns.checkpoint8(rand(84, 200, k, dtype=BF))
+    q = torch.zeros(t, k, dtype=torch.int8, device=DEV)
+    e = torch.zeros(t, k // 32, dtype=torch.uint8, device=DEV)
+    q[-200:], e[-200:] = saved.q, saved.e
+    offsets = torch.tensor([0, 3, t - 200, t], dtype=torch.int32, device=DEV)
+    got = ns.weight_grad(dy, ns.Checkpoint8(q, e, k), offsets=offsets, dtype=F32)
+    check_weight_grad(got[2], dy[-200:], saved)
+    assert not got[:2].any()
+    del dy, q, e, got
+    torch.cuda.empty_cache()
+    dy = rand(85, 6, 300, dtype=BF)
+    saved = ns.checkpoint8(rand(86, 6, 512, dtype=BF))
+    big = torch.empty(15000, 300, 512, dtype=BF, device=DEV)
+    offsets = torch.zeros(15001, dtype=torch.int32, device=DEV)
+    offsets[14000:] = 6
+    ns.weight_grad(dy, saved, offsets=offsets, out=big)
+    check_weight_grad(big[13999], dy, saved)
+    assert not big[14000:].any() and not big[:13999:700].any()
+
+
+def test_route_past_32_bits(ns):
+    _needs(24)
+    t, experts, k = 2200000, 1024, 4
+    z = torch.empty(t, experts, dtype=BF, device=DEV)
+    z.view(-1).view(torch.int16).random_(0x3c00, 0x4080)
+    r = ns.route(z, k, coef=1.0)
+    n = 50
+    r1 = ns.route(z[-n:].clone(), k)
+    assert torch.equal(r.indices[-n:], r1.indices) and torch.equal(r.weights[-n:], r1.weights)
+    assert int(r.kept) == t and int(r.offsets[-1]) == t * k == int(r.counts.sum())
+    assert abs(float(r.loss) - 1.0) < 0.01                      # an even load: E * sum of f P is about 1
+    dz = ns.route_backward(z, r, dloss=torch.ones((), device=DEV), dweights=torch.ones_like(r.weights))
+    assert bool(torch.isfinite(dz[-n:].float()).all())
