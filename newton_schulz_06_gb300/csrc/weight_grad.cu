@@ -4,19 +4,29 @@
 // Both operands have their long axis, the tokens, as rows: dY is tokens x n
 // and the checkpoint tokens x k, so the tensor cores read both as MN-major
 // operands and no transpose is made.  A CTA pair (tcgen05 cta_group::2)
-// computes a 256 x 256 tile of G, 64 tokens a step: each CTA loads its 128
-// columns of dY (bf16) and of the checkpoint (8 bits) with TMA, eight warps
-// turn the latter into bf16 in the tensor cores' swizzled layout, and the
-// leader issues the products.  A checkpoint's value q 2^(e - 133) is exact in
-// bf16, so the operands are exact and the sums fp32; the norm's weight and
-// bias act on the sums, in the epilogue:
+// computes a 256 x 256 tile of G (or a 512 x 256 one: WIDE), 64 tokens a step:
+// each CTA loads its 128 columns of dY (bf16) and of the checkpoint (8 bits)
+// with TMA, four warps turn the latter into bf16 in the tensor cores' swizzled
+// layout, and the leader issues the products.  A checkpoint's value
+// q 2^(e - 133) is exact in bf16, so the operands are exact and the sums fp32;
+// the norm's weight and bias act on the sums, in the epilogue:
 //     sum_t dy[t][i] (h[t][j] w[j] + b[j]) = w[j] G0[i][j] + b[j] sum_t dy[t][i].
 //
 // Roles in a CTA: warp 0 loads, warp 1 issues the products (leader only),
-// warps 2-9 write tiles out, warps 10-17 decode.  Two accumulators in tensor
-// memory, so a tile is written out while the next one's products run.  Pairs
-// walk the tiles in turn; how many tokens a tile has is read from the offsets
-// on the device, and every role finds the same number.
+// warps 2-9 write tiles out, warps 10-17 decode, in two groups of four that
+// take the steps in turn.  Two accumulators in tensor memory, so that a tile
+// is written out while the next one's products run; a WIDE tile has both, one
+// for each of its halves.  Pairs walk the tiles in turn; how many tokens a
+// tile has is read from the offsets on the device, and every role finds the
+// same number.
+//
+// What bounds it is the tensor cores where the tiles are WIDE (16384 tokens,
+// 7168 x 8192, bf16: 1021 us, 1.88 PFLOP/s), and else the decoding warps: at
+// 4096 tokens and 256 x 256 tiles 345 us, 310 without the products and 274
+// without the decoding.  Four warps a group and two groups beat 2 x 8 warps
+// and 4 x 4 (69, 90 and 95 us with 512 tokens of 7168 x 8192), and eight warps
+// that write out beat four (their stores of 64-byte rows, 94 us with TMA
+// stores and 107 with 32-byte ones straight from registers).
 //
 // Every wait is bounded; one that runs out raises g_ops_err (muon_ops_sync).
 #include <cstdlib>
@@ -32,14 +42,11 @@ namespace {
 
 using namespace ptx;
 
-constexpr int W_STAGES = 5;
 constexpr int W_TOK = 64;                          // tokens a step
 constexpr int W_BOX = W_TOK * 64 * 2;              // 64 bf16 columns of a step
 constexpr int W_RBOX = W_TOK * 64;                 // 64 columns of a step in 8 bits
-constexpr int W_A_BYTES = 2 * W_BOX;
 constexpr int W_B_BYTES = 2 * W_BOX;
 constexpr int W_R_BYTES = 2 * W_RBOX;
-constexpr int W_TX = W_A_BYTES + W_R_BYTES;
 constexpr int W_EPI_WARPS = 8;                     // two for 32 rows of the tile
 constexpr int W_DEC_WARPS = 4;                     // that decode one step
 constexpr int W_DEC_BLOCKS = 8 / W_DEC_WARPS;      // blocks of 32 values a thread decodes
@@ -50,10 +57,24 @@ constexpr int W_EPI_BYTES = 32 * 64;               // a warp's staged block: 32 
 constexpr int W_ORDER = 512;                       // experts that are taken by their size
 constexpr int W_TMEM_COLS = 512;
 constexpr int W_PAIRS = 76;                        // a pair per two of the 152 SMs
-constexpr int W_EPI_OFF = W_STAGES * (W_A_BYTES + W_B_BYTES + W_R_BYTES) + 1024;
-constexpr int W_ORDER_OFF = W_EPI_OFF + W_EPI_WARPS * W_EPI_BYTES;
-constexpr int W_SMEM = W_ORDER_OFF + W_ORDER * 2 + 1024;
-static_assert(W_SMEM <= 232448, "shared memory per CTA");
+// A tile's 256-row halves and the rings of stages: of dY (A), of the decoded
+// values (B) and of the 8-bit ones (R).  The rings of WIDE are as long as the
+// shared memory allows, and each has its own barriers; in the other shape the
+// decoding warps have no time for them (345 -> 444 us with 4096 tokens of
+// 7168 x 8192).
+template <bool WIDE>
+struct Shape {
+    static constexpr int HALVES = WIDE ? 2 : 1;
+    static constexpr int A_STAGES = WIDE ? 4 : 5, B_STAGES = WIDE ? 3 : 5, R_STAGES = WIDE ? 4 : 5;
+    static constexpr int AHEAD = R_STAGES - 2;     // steps that R's loads run ahead of A's
+    static constexpr int A_BYTES = HALVES * 2 * W_BOX;
+    static constexpr int B_OFF = A_STAGES * A_BYTES, R_OFF = B_OFF + B_STAGES * W_B_BYTES;
+    static constexpr int BAR_OFF = R_OFF + R_STAGES * W_R_BYTES;
+    static constexpr int EPI_OFF = BAR_OFF + 1024;
+    static constexpr int ORDER_OFF = EPI_OFF + W_EPI_WARPS * W_EPI_BYTES;
+    static constexpr int SMEM = ORDER_OFF + W_ORDER * 2 + 1024;
+    static_assert(SMEM <= 232448, "shared memory per CTA");
+};
 constexpr int COLSUM_PARTS = 16;      // of one matrix's tokens (experts: one part each)
 constexpr int BAND = 8;
 // fp32 results: the tensor cores cut a running sum off at its last place, so
@@ -99,6 +120,7 @@ struct Item {
     int32_t end;             // the matrix's tokens end here
 };
 // order: the experts by their size (or null: as they are).
+template <bool WIDE>
 __device__ __forceinline__ Item item_at(const WgLaunch& p, const uint16_t* order, int32_t it) {
     const uint32_t per = static_cast<uint32_t>(p.tiles_n) * p.tiles_k;
     const uint32_t es = static_cast<uint32_t>(it) / per;
@@ -106,13 +128,14 @@ __device__ __forceinline__ Item item_at(const WgLaunch& p, const uint16_t* order
     Item x;
     x.e = static_cast<int32_t>(es / p.splits);
     x.split = static_cast<int32_t>(es - uint32_t(x.e) * p.splits);
-    // bands of 8 tiles of n, column by column: the tiles that run together
+    // bands of 2048 rows, column by column: the tiles that run together
     // share their rows of dY and of the checkpoint in L2
-    const uint32_t band = w / (BAND * p.tiles_k);
-    const uint32_t high = min(BAND, p.tiles_n - static_cast<int>(band) * BAND);
-    const uint32_t in = w - band * BAND * p.tiles_k;
+    constexpr int HIGH = BAND / Shape<WIDE>::HALVES;
+    const uint32_t band = w / (HIGH * p.tiles_k);
+    const uint32_t high = min(HIGH, p.tiles_n - static_cast<int>(band) * HIGH);
+    const uint32_t in = w - band * HIGH * p.tiles_k;
     x.k0 = static_cast<int32_t>(in / high) * 256;
-    x.n0 = static_cast<int32_t>(band * BAND + in % high) * 256;
+    x.n0 = static_cast<int32_t>(band * HIGH + in % high) * 256 * Shape<WIDE>::HALVES;
     int64_t begin, end;
     if (order) x.e = order[x.e];
     segment(p.a, x.e, &begin, &end);
@@ -326,21 +349,48 @@ __device__ __forceinline__ void store_rows(const uint4* blk, char* to, int64_t p
     }
 }
 
+// The steps of a pair's tiles, one after the other.
+template <bool WIDE>
+struct Steps {
+    const WgLaunch& p;
+    const uint16_t* order;
+    int32_t it, by;
+    Item x;
+    int s = -1;
+    bool more;
+    __device__ __forceinline__ Steps(const WgLaunch& l, const uint16_t* o, int first, int stride)
+        : p(l), order(o), it(first), by(stride), more(first < l.items) {
+        if (more) x = item_at<WIDE>(p, order, it);
+        next();
+    }
+    __device__ __forceinline__ void next() {
+        if (!more || ++s < x.steps) return;
+        s = 0;
+        do {
+            it += by;
+            more = it < p.items;
+            if (more) x = item_at<WIDE>(p, order, it);
+        } while (more && x.steps == 0);
+    }
+};
+
 // F32: what is stored is fp32 (G, or the sums of a part of a split).
-template <bool F32>
+template <bool F32, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
     weight_grad_kernel(const __grid_constant__ WgLaunch p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    using S = Shape<WIDE>;
     uint8_t* sA = smem;
-    uint8_t* sB = sA + W_STAGES * W_A_BYTES;
-    uint8_t* sR = sB + W_STAGES * W_B_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sR + W_STAGES * W_R_BYTES);
-    uint64_t* full_bar = bars;                      // this CTA's loads of a stage
-    uint64_t* ready_bar = bars + W_STAGES;          // both CTAs' decoded stage (leader's)
-    uint64_t* empty_bar = bars + 2 * W_STAGES;      // the products have read a stage
-    uint64_t* tfull_bar = bars + 3 * W_STAGES;
+    uint8_t* sB = smem + S::B_OFF;
+    uint8_t* sR = smem + S::R_OFF;
+    uint64_t* a_bar = reinterpret_cast<uint64_t*>(smem + S::BAR_OFF);   // this CTA's dY of a step
+    uint64_t* done_bar = a_bar + S::A_STAGES;       // the products of a step have run
+    uint64_t* r_bar = done_bar + S::A_STAGES;       // this CTA's 8-bit values
+    uint64_t* free_bar = r_bar + S::R_STAGES;       // and they have been read
+    uint64_t* ready_bar = free_bar + S::R_STAGES;   // both CTAs' operands (leader's)
+    uint64_t* tfull_bar = ready_bar + S::B_STAGES;
     uint64_t* tempty_bar = tfull_bar + 2;
     uint64_t* drain_bar = tempty_bar + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
@@ -353,11 +403,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
     const int npairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < W_STAGES; ++s) {
-            mbar_init(smem_u32(&full_bar[s]), 1);
-            mbar_init(smem_u32(&ready_bar[s]), 2 * W_DEC_WARPS);
-            mbar_init(smem_u32(&empty_bar[s]), 1);
+        for (int s = 0; s < S::A_STAGES; ++s) {
+            mbar_init(smem_u32(&a_bar[s]), 1);
+            mbar_init(smem_u32(&done_bar[s]), 1);
         }
+        for (int s = 0; s < S::R_STAGES; ++s) {
+            mbar_init(smem_u32(&r_bar[s]), 1);
+            mbar_init(smem_u32(&free_bar[s]), W_DEC_WARPS);
+        }
+        for (int s = 0; s < S::B_STAGES; ++s) mbar_init(smem_u32(&ready_bar[s]), 2 * W_DEC_WARPS);
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&tfull_bar[a]), 1);
             mbar_init(smem_u32(&tempty_bar[a]), 2 * W_EPI_WARPS);
@@ -381,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
     // quarter of the time, with sizes as a router gives them).
     uint16_t* order = nullptr;
     if (p.sorted) {
-        order = reinterpret_cast<uint16_t*>(smem + W_ORDER_OFF);
+        order = reinterpret_cast<uint16_t*>(smem + S::ORDER_OFF);
         const int experts = static_cast<int>(p.a.experts);
         int64_t* size = reinterpret_cast<int64_t*>(smem);    // the stages are not in use yet
         for (int e = threadIdx.x; e < experts; e += W_THREADS) {
@@ -408,46 +462,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ loads
+        // WIDE: the 8-bit values some steps ahead, as they are decoded
+        // meanwhile; else both operands of a step on one barrier.
         if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int issued[W_STAGES];
-            for (int s = 0; s < W_STAGES; ++s) issued[s] = 0;
+            Steps<WIDE> ra(p, order, pair, npairs), aa = ra;
+            uint32_t nr = 0, na = 0;      // steps issued
             bool ok = true;
-            for (int32_t it = pair; ok && it < p.items; it += npairs) {
-                const Item x = item_at(p, order, it);
-                const int a0 = x.n0 + static_cast<int>(rank) * 128;
-                const int b0 = x.k0 + static_cast<int>(rank) * 128;
-                for (int s = 0; s < x.steps; ++s) {
-                    if (!wait_soon(smem_u32(&empty_bar[stage]), phase ^ 1, abort_flag, &g_ops_err,
-                                   limit)) {
-                        ok = false;
-                        break;
+            auto load_r = [&](const Steps<WIDE>& at, uint32_t n, uint32_t bar) {
+                const uint32_t dst = smem_u32(sR + n % S::R_STAGES * W_R_BYTES);
+                const int b0 = at.x.k0 + static_cast<int>(rank) * 128, t = at.x.t0 + at.s * W_TOK;
+                tma_load_2d(dst, &p.tm_q, bar, b0, t);
+                tma_load_2d(dst + W_RBOX, &p.tm_q, bar, b0 + 64, t);
+            };
+            while (ok && aa.more) {
+                if constexpr (WIDE)
+                    for (; ra.more && nr <= na + S::AHEAD; ++nr, ra.next()) {
+                        const uint32_t slot = nr % S::R_STAGES, rb = smem_u32(&r_bar[slot]);
+                        ok = wait_soon(smem_u32(&free_bar[slot]), (nr / S::R_STAGES & 1) ^ 1, abort_flag,
+                                       &g_ops_err, limit);
+                        if (!ok) break;
+                        mbar_expect_tx(rb, W_R_BYTES);
+                        load_r(ra, nr, rb);
                     }
-                    const uint32_t fb = smem_u32(&full_bar[stage]);
-                    const int t = x.t0 + s * W_TOK;
-                    mbar_expect_tx(fb, W_TX);
-                    const uint32_t a_dst = smem_u32(sA + stage * W_A_BYTES);
-                    const uint32_t r_dst = smem_u32(sR + stage * W_R_BYTES);
-                    tma_load_2d(r_dst, &p.tm_q, fb, b0, t);
-                    tma_load_2d(r_dst + W_RBOX, &p.tm_q, fb, b0 + 64, t);
-                    tma_load_2d(a_dst, &p.tm_dy, fb, a0, t);
-                    tma_load_2d(a_dst + W_BOX, &p.tm_dy, fb, a0 + 64, t);
-                    issued[stage] = static_cast<int>(phase) + 1;
-                    if (++stage == W_STAGES) { stage = 0; phase ^= 1; }
+                const uint32_t slot = na % S::A_STAGES, ab = smem_u32(&a_bar[slot]);
+                ok = ok && wait_soon(smem_u32(&done_bar[slot]), (na / S::A_STAGES & 1) ^ 1, abort_flag,
+                                     &g_ops_err, limit);
+                if (!ok) break;
+                mbar_expect_tx(ab, S::A_BYTES + (WIDE ? 0 : W_R_BYTES));
+                if constexpr (!WIDE) load_r(aa, na, ab);
+                const uint32_t dst = smem_u32(sA + slot * S::A_BYTES);
+                const int a0 = aa.x.n0 + static_cast<int>(rank) * 128, t = aa.x.t0 + aa.s * W_TOK;
+#pragma unroll
+                for (int h = 0; h < S::HALVES; ++h) {
+                    tma_load_2d(dst + 2 * h * W_BOX, &p.tm_dy, ab, a0 + 256 * h, t);
+                    tma_load_2d(dst + (2 * h + 1) * W_BOX, &p.tm_dy, ab, a0 + 256 * h + 64, t);
                 }
+                ++na;
+                aa.next();
             }
-            if (!ok)
-                for (int s = 0; s < W_STAGES; ++s)
-                    if (issued[s])
-                        wait_quiet(smem_u32(&full_bar[s]), static_cast<uint32_t>(issued[s] - 1),
-                                   limit);
+            if (!ok) {
+                // the last load of each stage
+                for (uint32_t i = nr - min(nr, uint32_t(S::R_STAGES)); i < nr; ++i)
+                    wait_quiet(smem_u32(&r_bar[i % S::R_STAGES]), i / S::R_STAGES & 1, limit);
+                for (uint32_t i = na - min(na, uint32_t(S::A_STAGES)); i < na; ++i)
+                    wait_quiet(smem_u32(&a_bar[i % S::A_STAGES]), i / S::A_STAGES & 1, limit);
+            }
         }
     } else if (warp == 1) {
         // ------------------------------------------------- products (leader)
         if (lane == 0 && rank == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
+            uint32_t step = 0;
             uint32_t uses[2] = {0, 0};    // of each accumulator
             uint32_t first = 0;           // the one that the tile starts in
             bool ok = true, any = false;
@@ -456,38 +520,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             const uint64_t a_desc = smem_desc(smem_u32(sA), W_BOX, 1024);
             const uint64_t b_desc = smem_desc(smem_u32(sB), W_BOX, 1024);
             const uint32_t idesc = instr_desc(256, 256, 1) | (1u << 15);
+            // an accumulator that has been written out
+            auto take = [&](uint32_t acc) {
+                const uint32_t use = acc ? uses[1]++ : uses[0]++;
+                const bool got = wait_soon(smem_u32(&tempty_bar[acc]), (use & 1) ^ 1, abort_flag,
+                                           &g_ops_err, limit);
+                tc_fence_after();
+                return got;
+            };
+            // the products of a step and of the tile's half h
+            auto products = [&](uint32_t acc, int h, bool fresh) {
+                const uint64_t ad = a_desc + (step % S::A_STAGES * S::A_BYTES + h * 2 * W_BOX >> 4);
+                const uint64_t bd = b_desc + (step % S::B_STAGES * W_B_BYTES >> 4);
+#pragma unroll
+                for (int kk = 0; kk < W_TOK / 16; ++kk)
+                    mma_pair(tmem_base + acc * 256, ad + static_cast<uint64_t>(kk * (2048 >> 4)),
+                             bd + static_cast<uint64_t>(kk * (2048 >> 4)), idesc,
+                             (fresh && kk == 0) ? 0u : 1u);
+            };
             for (int32_t it = pair; ok && it < p.items; it += npairs) {
-                const Item x = item_at(p, order, it);
+                const Item x = item_at<WIDE>(p, order, it);
                 if (x.steps == 0) continue;
-                const int chunk = p.chunk ? p.chunk : x.steps;
+                const int chunk = !WIDE && p.chunk ? p.chunk : x.steps;
                 for (int s0 = 0; ok && s0 < x.steps; s0 += chunk) {
-                    const uint32_t acc = s0 ? first ^ 1 : first;
-                    const uint32_t use = acc ? uses[1]++ : uses[0]++;
-                    if (!wait_soon(smem_u32(&tempty_bar[acc]), (use & 1) ^ 1, abort_flag, &g_ops_err,
-                                   limit)) {
+                    const uint32_t acc = WIDE ? 0u : s0 ? first ^ 1 : first;
+                    if (!take(acc)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + acc * 256;
                     const int s1 = min(s0 + chunk, x.steps);
-                    for (int s = s0; s < s1; ++s) {
-                        if (!wait_soon(smem_u32(&ready_bar[stage]), phase, abort_flag, &g_ops_err,
-                                       limit)) {
+                    for (int s = s0; s < s1; ++s, ++step) {
+                        if (!wait_soon(smem_u32(&ready_bar[step % S::B_STAGES]),
+                                       step / S::B_STAGES & 1, abort_flag, &g_ops_err, limit)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t ad = a_desc + static_cast<uint64_t>(stage) * (W_A_BYTES >> 4);
-                        const uint64_t bd = b_desc + static_cast<uint64_t>(stage) * (W_B_BYTES >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < W_TOK / 16; ++kk)
-                            mma_pair(d_tmem, ad + static_cast<uint64_t>(kk * (2048 >> 4)),
-                                     bd + static_cast<uint64_t>(kk * (2048 >> 4)), idesc,
-                                     (s > s0 || kk > 0) ? 1u : 0u);
+                        products(acc, 0, s == s0);
                         any = true;
-                        commit_pair_multicast(smem_u32(&empty_bar[stage]));
-                        if (++stage == W_STAGES) { stage = 0; phase ^= 1; }
+                        if (WIDE) {
+                            if (s == 0 && !take(1)) {
+                                ok = false;
+                                break;
+                            }
+                            products(1, 1, s == 0);
+                        }
+                        commit_pair_multicast(smem_u32(&done_bar[step % S::A_STAGES]));
                     }
                     if (ok) commit_pair_multicast(smem_u32(&tfull_bar[acc]));
                 }
@@ -516,8 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         const int nblk = static_cast<int>((p.a.k + CKPT_BLOCK - 1) / CKPT_BLOCK);
         const uint32_t ready_leader = map_to_rank(smem_u32(ready_bar), 0);
         uint32_t before = 0;          // steps of the tiles before this one
-        int stage = group;
-        uint32_t phase = 0;
+        uint32_t step = group;
         bool ok = true;
         // the scale bytes come four of this group's steps at a time, one
         // round ahead, also across tiles
@@ -539,7 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         Item x, y{};
         int32_t it = pair;
         if (it < p.items) {
-            x = item_at(p, order, it);
+            x = item_at<WIDE>(p, order, it);
             fetch(x, group);
         }
         for (; ok && it < p.items; it += npairs, x = y) {
@@ -547,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             before += x.steps;
             const int y_first = (group - static_cast<int>(before)) & (W_DEC_GROUPS - 1);
             const bool more = it + npairs < p.items;
-            if (more) y = item_at(p, order, it + npairs);
+            if (more) y = item_at<WIDE>(p, order, it + npairs);
             if (first >= x.steps && more) fetch(y, y_first);
             for (int s = first; ok && s < x.steps; s += 4 * W_DEC_GROUPS) {
                 uint32_t cur[4][W_DEC_BLOCKS];
@@ -561,8 +638,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                 for (int u = 0; u < 4; ++u) {
                     const int su = s + u * W_DEC_GROUPS;
                     if (su >= x.steps) break;
-                    const bool got = wait_soon(smem_u32(&full_bar[stage]), phase, abort_flag,
-                                               &g_ops_err, limit);
+                    const uint32_t sa = step % S::A_STAGES, sb = step % S::B_STAGES,
+                                   sr = step % S::R_STAGES;
+                    bool got;
+                    if constexpr (WIDE) {
+                        const uint32_t last = step - S::B_STAGES;    // that used this stage of B
+                        got = wait_soon(smem_u32(&r_bar[sr]), step / S::R_STAGES & 1, abort_flag,
+                                        &g_ops_err, limit) &&
+                              (step < S::B_STAGES ||
+                               wait_soon(smem_u32(&done_bar[last % S::A_STAGES]),
+                                         last / S::A_STAGES & 1, abort_flag, &g_ops_err, limit));
+                    } else {
+                        got = wait_soon(smem_u32(&a_bar[sa]), step / S::A_STAGES & 1, abort_flag,
+                                        &g_ops_err, limit);
+                    }
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
@@ -572,12 +661,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < W_DEC_BLOCKS; ++i) {
                         // 16 rows on, the swizzles are the same
-                        const uint8_t* r = sR + stage * W_R_BYTES + src + i * 16 * 64;
+                        const uint8_t* r = sR + sr * W_R_BYTES + src + i * 16 * 64;
                         q[i][0] = *reinterpret_cast<const uint4*>(r + (((blk * 2) ^ src_sw) << 4));
                         q[i][1] = *reinterpret_cast<const uint4*>(r + (((blk * 2 + 1) ^ src_sw) << 4));
                         high |= scale_is_high(cur[u][i]);
                     }
-                    uint8_t* const to = sB + stage * W_B_BYTES + dst;
+                    uint8_t* const to = sB + sb * W_B_BYTES + dst;
                     if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
                         for (int i = 0; i < W_DEC_BLOCKS; ++i)
@@ -587,21 +676,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                         for (int i = 0; i < W_DEC_BLOCKS; ++i)
                             decode_block<false>(q[i], block_scale(cur[u][i]), to + i * 16 * 128, blk, dst_sw);
                     }
+                    if constexpr (WIDE) {
+                        // the values have been used, so their loads are done
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&free_bar[sr]));
+                        // dY has to be there too
+                        const bool in = wait_soon(smem_u32(&a_bar[sa]), step / S::A_STAGES & 1,
+                                                  abort_flag, &g_ops_err, limit);
+                        if (!__all_sync(0xffffffffu, in)) {
+                            ok = false;
+                            break;
+                        }
+                    }
                     const int left = x.end - (x.t0 + su * W_TOK);
                     if (left < W_TOK) {
                         // tokens of the next matrix in dY's stage: 0 times a
                         // NaN of theirs would be a NaN here
-                        uint8_t* a = sA + stage * W_A_BYTES;
-                        for (int c = dw * 32 + lane; c < (W_TOK - left) * 16; c += W_DEC_WARPS * 32)
-                            *reinterpret_cast<uint4*>(a + (c >> 3 & 1) * W_BOX +
-                                                      (left + (c >> 4)) * 128 + (c & 7) * 16) =
+                        uint8_t* a = sA + sa * S::A_BYTES;
+                        constexpr int BOXES = 2 * S::HALVES;
+                        for (int c = dw * 32 + lane; c < (W_TOK - left) * 8 * BOXES; c += W_DEC_WARPS * 32)
+                            *reinterpret_cast<uint4*>(a + (c >> 3) % BOXES * W_BOX +
+                                                      (left + (c >> 3) / BOXES) * 128 + (c & 7) * 16) =
                                 make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) arrive_leader(ready_leader + 8 * stage);
-                    stage += W_DEC_GROUPS;
-                    if (stage >= W_STAGES) { stage -= W_STAGES; phase ^= 1; }
+                    if (lane == 0) arrive_leader(ready_leader + 8 * sb);
+                    step += W_DEC_GROUPS;
                 }
             }
         }
@@ -609,7 +710,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         // --------------------------------------------------------- write out
         const int lg = warp & 3;                    // this warp's 32 TMEM lanes,
         const int c_first = (warp - 2) / 4 * 4;     // and four of its 32-column blocks
-        uint4* const blk = reinterpret_cast<uint4*>(smem + W_EPI_OFF + (warp - 2) * W_EPI_BYTES);
+        uint4* const blk = reinterpret_cast<uint4*>(smem + S::EPI_OFF + (warp - 2) * W_EPI_BYTES);
         const uint32_t tempty_leader = map_to_rank(smem_u32(tempty_bar), 0);
         uint32_t uses[2] = {0, 0};
         uint32_t first = 0;
@@ -628,9 +729,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * acc);
         };
         for (int32_t it = pair; ok && it < p.items; it += npairs) {
-            const Item x = item_at(p, order, it);
+            const Item x = item_at<WIDE>(p, order, it);
             const uint32_t tlane = tmem_base + (static_cast<uint32_t>(lg * 32) << 16);
-            const uint32_t taddr = tlane + first * 256;
             if (x.steps) {
                 if (!wait_full(first)) {
                     ok = false;
@@ -638,7 +738,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                 }
                 // later chunks of the tokens: added up in fp32, rounded to
                 // nearest
-                const int chunk = p.chunk ? p.chunk : x.steps;
+                const int chunk = !WIDE && p.chunk ? p.chunk : x.steps;
                 for (int s0 = chunk; s0 < x.steps; s0 += chunk) {
                     if (!wait_full(first ^ 1)) {
                         ok = false;
@@ -646,97 +746,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                     }
 #pragma unroll 1
                     for (int c = 2 * c_first; c < 2 * (c_first + 4); ++c)
-                        tmem_add16(taddr + 16 * c, tlane + (first ^ 1) * 256 + 16 * c);
+                        tmem_add16(tlane + first * 256 + 16 * c, tlane + (first ^ 1) * 256 + 16 * c);
                     release(first ^ 1);
                 }
                 if (!ok) break;
             }
-            const int r0 = x.n0 + static_cast<int>(rank) * 128 + lg * 32;
-            const int n = static_cast<int>(p.a.n), k = static_cast<int>(p.a.k);
-            const int rows = min(32, n - r0);
-            // a part of a split leaves its sums as they are
-            const bool apply = p.splits == 1;
-            const float sum = (apply && p.colsum && lane < rows) ? column_sum(p, x.e, r0 + lane) : 0.f;
-            const int64_t ld = apply ? p.a.ld_g : p.ld_part;
-            const int64_t g0 = apply ? x.e * p.a.stride_g + r0 * ld
-                                     : ((int64_t(x.split) * p.a.experts + x.e) * n + r0) * ld;
-            const int64_t c0 = x.e * p.a.stride_c + r0 * p.a.ld_c;
-            void* const g = apply ? p.a.g : p.part;
-            const void* const add = apply ? p.a.c : nullptr;
-            constexpr int size = F32 ? 4 : 2;
-            if (rows > 0) {
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    const int j0 = x.k0 + 32 * c_first + 16 * c;
-                    if (j0 >= k) break;
-                    uint32_t raw[16];
-                    float v[16];
-                    if (x.steps) {
-                        tmem_ld16(taddr + 32 * c_first + 16 * c, raw);
-                        tmem_ld_wait();
-                    }
-#pragma unroll
-                    for (int u = 0; u < 16; ++u) v[u] = x.steps ? __uint_as_float(raw[u]) : 0.f;
-                    if (apply && (p.a.weight || p.a.bias)) {
-                        const int j = j0 + (lane & 15);
-                        const float wl = p.a.weight && j < k ? p.a.weight[j] : 1.f;
-                        const float bl = p.a.bias && j < k ? p.a.bias[j] : 0.f;
-#pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            v[u] = fmaf(__shfl_sync(0xffffffffu, bl, u), sum,
-                                        v[u] * __shfl_sync(0xffffffffu, wl, u));
-                    }
-                    // Staged, and stored as rows of 64 bytes (lanes that store
-                    // their own rows straight from registers touch 32 lines a
-                    // store, which took three times as long): 16 columns of
-                    // fp32, or 32 of bf16 from two rounds.
-                    const int odd = F32 ? 0 : c & 1;
-                    const int row0 = j0 - 16 * odd;
-                    if (p.vec && row0 + (F32 ? 16 : 32) <= k) {
-                        if (!odd) __syncwarp();      // the last rows have been read
-                        if constexpr (F32) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                blk[staged(lane, q)] = make_uint4(
-                                    __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                    __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
-                        } else {
-                            if (add && lane < rows)
-                                add16(static_cast<const __nv_bfloat16*>(add) + c0 + lane * p.a.ld_c + j0, v);
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                float t[8];
-#pragma unroll
-                                for (int u = 0; u < 8; ++u) t[u] = v[8 * q + u];
-                                store8_bf16(reinterpret_cast<__nv_bfloat16*>(
-                                                &blk[staged(lane, q + 2 * odd)]), t);
-                            }
-                            if (!odd) continue;
+            for (int h = 0; h < S::HALVES; ++h) {
+                const uint32_t acc = WIDE ? h : first;
+                const uint32_t taddr = tlane + acc * 256;
+                const int r0 = x.n0 + 256 * h + static_cast<int>(rank) * 128 + lg * 32;
+                const int n = static_cast<int>(p.a.n), k = static_cast<int>(p.a.k);
+                const int rows = min(32, n - r0);
+                // a part of a split leaves its sums as they are
+                const bool apply = p.splits == 1;
+                const float sum = (apply && p.colsum && lane < rows) ? column_sum(p, x.e, r0 + lane) : 0.f;
+                const int64_t ld = apply ? p.a.ld_g : p.ld_part;
+                const int64_t g0 = apply ? x.e * p.a.stride_g + r0 * ld
+                                         : ((int64_t(x.split) * p.a.experts + x.e) * n + r0) * ld;
+                const int64_t c0 = x.e * p.a.stride_c + r0 * p.a.ld_c;
+                void* const g = apply ? p.a.g : p.part;
+                const void* const add = apply ? p.a.c : nullptr;
+                constexpr int size = F32 ? 4 : 2;
+                if (rows > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        const int j0 = x.k0 + 32 * c_first + 16 * c;
+                        if (j0 >= k) break;
+                        uint32_t raw[16];
+                        float v[16];
+                        if (x.steps) {
+                            tmem_ld16(taddr + 32 * c_first + 16 * c, raw);
+                            tmem_ld_wait();
                         }
-                        __syncwarp();
-                        char* const to = static_cast<char*>(g) + (g0 + row0) * size;
-                        if (F32 && add)
-                            store_rows<true>(blk, to, ld * size,
-                                             static_cast<const char*>(add) + (c0 + j0) * 4, p.a.ld_c * 4,
-                                             rows, lane);
-                        else
-                            store_rows<false>(blk, to, ld * size, nullptr, 0, rows, lane);
-                        continue;
-                    }
-                    float* const f = reinterpret_cast<float*>(blk);
-                    __syncwarp();
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) f[lane * 16 + (u ^ (lane & 15))] = v[u];
-                    __syncwarp();
-                    store_elements(f, g, F32 ? MUON_F32 : MUON_BF16, g0 + j0, ld, add, c0 + j0, p.a.ld_c,
-                                   rows, k - j0);
-                    __syncwarp();
+                        for (int u = 0; u < 16; ++u) v[u] = x.steps ? __uint_as_float(raw[u]) : 0.f;
+                        if (apply && (p.a.weight || p.a.bias)) {
+                            const int j = j0 + (lane & 15);
+                            const float wl = p.a.weight && j < k ? p.a.weight[j] : 1.f;
+                            const float bl = p.a.bias && j < k ? p.a.bias[j] : 0.f;
+#pragma unroll
+                            for (int u = 0; u < 16; ++u)
+                                v[u] = fmaf(__shfl_sync(0xffffffffu, bl, u), sum,
+                                            v[u] * __shfl_sync(0xffffffffu, wl, u));
+                        }
+                        // Staged, and stored as rows of 64 bytes (lanes that store
+                        // their own rows straight from registers touch 32 lines a
+                        // store, which took three times as long): 16 columns of
+                        // fp32, or 32 of bf16 from two rounds.
+                        const int odd = F32 ? 0 : c & 1;
+                        const int row0 = j0 - 16 * odd;
+                        if (p.vec && row0 + (F32 ? 16 : 32) <= k) {
+                            if (!odd) __syncwarp();      // the last rows have been read
+                            if constexpr (F32) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    blk[staged(lane, q)] = make_uint4(
+                                        __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                        __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+                            } else {
+                                if (add && lane < rows)
+                                    add16(static_cast<const __nv_bfloat16*>(add) + c0 + lane * p.a.ld_c + j0, v);
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    float t[8];
+#pragma unroll
+                                    for (int u = 0; u < 8; ++u) t[u] = v[8 * q + u];
+                                    store8_bf16(reinterpret_cast<__nv_bfloat16*>(
+                                                    &blk[staged(lane, q + 2 * odd)]), t);
+                                }
+                                if (!odd) continue;
+                            }
+                            __syncwarp();
+                            char* const to = static_cast<char*>(g) + (g0 + row0) * size;
+                            if (F32 && add)
+                                store_rows<true>(blk, to, ld * size,
+                                                 static_cast<const char*>(add) + (c0 + j0) * 4, p.a.ld_c * 4,
+                                                 rows, lane);
+                            else
+                                store_rows<false>(blk, to, ld * size, nullptr, 0, rows, lane);
+                            continue;
+                        }
+                        float* const f = reinterpret_cast<float*>(blk);
+                        __syncwarp();
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) f[lane * 16 + (u ^ (lane & 15))] = v[u];
+                        __syncwarp();
+                        store_elements(f, g, F32 ? MUON_F32 : MUON_BF16, g0 + j0, ld, add, c0 + j0, p.a.ld_c,
+                                       rows, k - j0);
+                        __syncwarp();
+                    }
                 }
+                if (x.steps) release(acc);
             }
-            if (x.steps) {
-                release(first);
-                first ^= 1;
-            }
+            if (!WIDE && x.steps) first ^= 1;
         }
     }
 
@@ -860,6 +963,20 @@ int split_count(const muon_weight_grad_args& a) {
     return static_cast<int>(s < 1 ? 1 : s);
 }
 
+// Tiles of 512 x 256 instead of 256 x 256.  A decoded value then serves twice
+// the products, but there is one accumulator, so that a tile's writing out is
+// not hidden, and the last round of tiles is coarser.  In units of 0.21 us a
+// pair takes 3 a step + 34 for a wide tile and 2 a step + 10 for another
+// (measured with 7168 x 8192 from 300 to 4096 tokens; us, wide and not: 512
+// tokens 78 and 68, 1024 108 and 106, 2048 165 and 182, 4096 286 and 345,
+// 16384 1021 and 1452).  fp32 sums are added up in both accumulators.
+bool is_wide(const muon_weight_grad_args& a, int splits) {
+    if (a.g_dtype != MUON_BF16 || splits > 1) return false;
+    const int64_t steps = ceil_div(ceil_div(a.rows, a.experts), W_TOK);
+    const int64_t tall = a.experts * ceil_div(a.n, 512) * ceil_div(a.k, 256);
+    return ceil_div(tall, W_PAIRS) * (3 * steps + 34) < ceil_div(tiles(a), W_PAIRS) * (2 * steps + 10);
+}
+
 int grid_for(int64_t items) {
     const int64_t g = ceil_div(items, 256);
     return static_cast<int>(g < 1 ? 1 : g > 152 * 8 ? 152 * 8 : g);
@@ -942,9 +1059,10 @@ cudaError_t launch_weight_grad(const muon_weight_grad_args& a, void* ws, cudaStr
     WgLaunch p = {};
     p.a = a;
     p.splits = l.splits;
-    p.tiles_n = static_cast<int32_t>(ceil_div(a.n, 256));
+    const bool wide = is_wide(a, l.splits);
+    p.tiles_n = static_cast<int32_t>(ceil_div(a.n, wide ? 512 : 256));
     p.tiles_k = static_cast<int32_t>(ceil_div(a.k, 256));
-    p.items = static_cast<int32_t>(tiles(a) * l.splits);
+    p.items = static_cast<int32_t>(a.experts * p.tiles_n * p.tiles_k * l.splits);
     p.wait_limit_ns = wait_limit_ns();
     const int64_t size = a.g_dtype == MUON_F32 ? 4 : 2;
     if (a.g_dtype == MUON_F32) p.chunk = CHUNK_STEPS;
@@ -990,22 +1108,23 @@ cudaError_t launch_weight_grad(const muon_weight_grad_args& a, void* ws, cudaStr
                         CU_TENSOR_MAP_SWIZZLE_64B))
             return cudaErrorInvalidValue;
     }
+    const int pairs = p.items < W_PAIRS ? p.items : W_PAIRS;
+    const bool f32 = l.splits > 1 || a.g_dtype == MUON_F32;
+    const int size_of[3] = {Shape<false>::SMEM, Shape<false>::SMEM, Shape<true>::SMEM};
+    void (*const kernel[3])(WgLaunch) = {weight_grad_kernel<false, false>, weight_grad_kernel<true, false>,
+                                         weight_grad_kernel<false, true>};
     static int attr_done[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-        e = cudaFuncSetAttribute(weight_grad_kernel<false>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, W_SMEM);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(weight_grad_kernel<true>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, W_SMEM);
-        if (e != cudaSuccess) return e;
+        for (int i = 0; i < 3; ++i) {
+            e = cudaFuncSetAttribute(kernel[i], cudaFuncAttributeMaxDynamicSharedMemorySize, size_of[i]);
+            if (e != cudaSuccess) return e;
+        }
         if (dev >= 0 && dev < 64) attr_done[dev] = 1;
     }
-    const int pairs = p.items < W_PAIRS ? p.items : W_PAIRS;
-    const bool f32 = l.splits > 1 || a.g_dtype == MUON_F32;
-    e = launch_kernel(f32 ? weight_grad_kernel<true> : weight_grad_kernel<false>, dim3(2 * pairs),
-                      dim3(W_THREADS), W_SMEM, s, p);
+    const int which = wide ? 2 : f32 ? 1 : 0;
+    e = launch_kernel(kernel[which], dim3(2 * pairs), dim3(W_THREADS), size_of[which], s, p);
     if (e != cudaSuccess || l.splits == 1) return e;
     const int64_t rows = a.experts * a.n, across = ceil_div(a.k, 1024);
     const int64_t down = ceil_div(152 * 8, across);

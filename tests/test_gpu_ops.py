@@ -400,6 +400,47 @@ def test_weight_grad_of_views(ns, dtype):
                        ns.weight_grad(dy, saved, offsets=offsets, dtype=dtype))
 
 
+@pytest.mark.parametrize("t,n,k", [(1000, 2300, 2100), (1100, 6000, 6400), (961, 2304, 2304),
+                                   (1025, 2049, 2305)])
+def test_weight_grad_of_many_tiles(ns, t, n, k):
+    """Long sums and enough tiles for several a pair: bf16 takes tiles of 512
+    rows there (sizes with whole ones, with half of one, with a ragged end)."""
+    dy, saved = rand(57, t, n, scale=0.1, dtype=BF), saved_of(ns, 58, t, k)
+    got = ns.weight_grad(dy, saved)
+    check_weight_grad(got, dy, saved)
+    for lead, pad in ((8, 8), (1, 3)):
+        out = strided(torch.zeros(n, k, dtype=BF, device=DEV), lead, pad)
+        base = out._base.clone()
+        assert torch.equal(ns.weight_grad(dy, saved, out=out), got)
+        rest = out._base.clone()
+        rest[lead:lead + n * (k + pad)].view(n, k + pad)[:, :k] = 0
+        assert torch.equal(rest, base)                      # nothing outside the view
+    w, b, c = rand(59, k), rand(60, k), rand(61, n, k, dtype=BF)
+    check_weight_grad(ns.weight_grad(dy, saved, weight=w, bias=b, add=c), dy, saved, w, b, c)
+
+
+def test_weight_grad_of_long_sums(ns):
+    """Hundreds of steps a tile with all stages in flight; the same every
+    time."""
+    dy, saved = rand(67, 16384, 4096, scale=0.1, dtype=BF), saved_of(ns, 68, 16384, 4096)
+    got = ns.weight_grad(dy, saved)
+    check_weight_grad(got, dy, saved)
+    for _ in range(5):
+        assert torch.equal(ns.weight_grad(dy, saved), got)
+
+
+@pytest.mark.parametrize("counts,n,k", [([3000, 0, 1, 4000, 63, 2900], 1024, 1500),
+                                        ([2000, 2111, 0, 1900], 1100, 2050)])
+def test_weight_grad_of_experts_with_many_tokens(ns, counts, n, k):
+    t = sum(counts)
+    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32).to(DEV)
+    dy, saved = rand(62, t, n, scale=0.1, dtype=BF), saved_of(ns, 63, t, k)
+    check_weight_grad(ns.weight_grad(dy, saved, offsets=offsets), dy, saved, offsets=offsets)
+    w, b, c = rand(64, k), rand(65, k), rand(66, len(counts), n, k, dtype=BF)
+    got = ns.weight_grad(dy, saved, weight=w, bias=b, add=c, offsets=offsets)
+    check_weight_grad(got, dy, saved, w, b, c, offsets)
+
+
 def test_weight_grad_scales_over_their_whole_range(ns):
     """Blocks from the smallest scale to the largest: powers of two pass
     through exactly; a block that held a NaN makes its columns NaN."""
