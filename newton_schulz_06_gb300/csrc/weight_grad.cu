@@ -295,57 +295,90 @@ __device__ __forceinline__ void add16(const __nv_bfloat16* p, float (&v)[16]) {
 
 // 16 columns of 32 sums, staged with the columns XORed with the row, to a
 // gradient element by element (rows off 16 bytes, a row's last columns): two
-// rows at a time.  `left`: the columns there are.
+// rows at a time.  `left`: the columns there are; sum: of dY's column `lane`.
 __device__ __noinline__ void store_elements(const float* f, void* g, int g_type, int64_t at, int64_t ld,
                                             const void* add, int64_t c_at, int64_t ld_c, int rows,
-                                            int left) {
+                                            int left, const float* weight, const float* bias, float sum) {
     const int lane = threadIdx.x & 31, col = lane & 15, two = lane >> 4;
-    if (col >= left) return;
+    const bool there = col < left;
+    const float w = weight && there ? weight[col] : 1.f, b = bias && there ? bias[col] : 0.f;
     at += two * ld + col;
     c_at += two * ld_c + col;
 #pragma unroll 4
-    for (int r = two; r < rows; r += 2) {
-        float t = f[r * 16 + (col ^ (r & 15))];
-        if (add) t += load_any(add, g_type, c_at);
-        store_any(g, g_type, at, t);
+    for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + two;
+        const float s = __shfl_sync(0xffffffffu, sum, r);
+        if (there && r < rows) {
+            float t = fmaf(b, s, f[r * 16 + (col ^ (r & 15))] * w);
+            if (add) t += load_any(add, g_type, c_at);
+            store_any(g, g_type, at, t);
+        }
         at += 2 * ld;
         c_at += 2 * ld_c;
     }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // Place of 16-byte piece q of row r in a staged block of 32 rows of 64 bytes.
 __device__ __forceinline__ int staged(int r, int q) { return r * 4 + (q ^ ((r >> 1) & 3)); }
 
-// A staged block to a gradient, eight rows a store; with add (fp32) the same
-// rows of C are added on the way.
-template <bool ADD>
-__device__ __forceinline__ void store_rows(const uint4* blk, char* to, int64_t pitch, const char* add,
-                                           int64_t add_pitch, int rows, int lane) {
+// A staged block to a gradient, eight rows a store.
+__device__ __forceinline__ void store_rows(const uint4* blk, char* to, int64_t pitch, int rows, int lane) {
     const int piece = lane & 3, sub = lane >> 2;
     to += sub * pitch + piece * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + sub;
+        if (r < rows) *reinterpret_cast<uint4*>(to) = blk[staged(r, piece)];
+        to += 8 * pitch;
+    }
+}
+
+// As store_rows, of fp32 and with the epilogue on the way: a thread has the
+// same four columns of all its rows, so that w and b are asked for once a
+// block; sum is the sum of dY's column `lane`.
+__device__ __forceinline__ void finish_rows(const uint4* blk, float* g, int64_t ld, const float* c, int64_t ld_c,
+                                            const float* weight, const float* bias, float sum, int rows,
+                                            int lane) {
+    const int piece = lane & 3, sub = lane >> 2;
+    float w[4], b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        w[u] = weight ? weight[piece * 4 + u] : 1.f;
+        b[u] = bias ? bias[piece * 4 + u] : 0.f;
+    }
+    g += sub * ld + piece * 4;
     // C's rows before the first store: C may be G, so that the compiler must
     // keep a load behind the stores before it
     float4 f[4];
-    if (ADD) {
-        add += sub * add_pitch + piece * 16;
+    if (c) {
+        c += sub * ld_c + piece * 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (8 * i + sub < rows) f[i] = *reinterpret_cast<const float4*>(add + 8 * i * add_pitch);
+            if (8 * i + sub < rows) f[i] = *reinterpret_cast<const float4*>(c + 8 * i * ld_c);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 8 * i + sub;
+        const float s = __shfl_sync(0xffffffffu, sum, r);
         if (r < rows) {
-            uint4 v = blk[staged(r, piece)];
-            if (ADD) {
-                v.x = __float_as_uint(__uint_as_float(v.x) + f[i].x);
-                v.y = __float_as_uint(__uint_as_float(v.y) + f[i].y);
-                v.z = __float_as_uint(__uint_as_float(v.z) + f[i].z);
-                v.w = __float_as_uint(__uint_as_float(v.w) + f[i].w);
+            const uint4 u = blk[staged(r, piece)];
+            float4 v = make_float4(fmaf(b[0], s, __uint_as_float(u.x) * w[0]),
+                                   fmaf(b[1], s, __uint_as_float(u.y) * w[1]),
+                                   fmaf(b[2], s, __uint_as_float(u.z) * w[2]),
+                                   fmaf(b[3], s, __uint_as_float(u.w) * w[3]));
+            if (c) {
+                v.x += f[i].x;
+                v.y += f[i].y;
+                v.z += f[i].z;
+                v.w += f[i].w;
             }
-            *reinterpret_cast<uint4*>(to) = v;
+            *reinterpret_cast<float4*>(g) = v;
         }
-        to += 8 * pitch;
+        g += 8 * ld;
     }
 }
 
@@ -731,6 +764,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         for (int32_t it = pair; ok && it < p.items; it += npairs) {
             const Item x = item_at<WIDE>(p, order, it);
             const uint32_t tlane = tmem_base + (static_cast<uint32_t>(lg * 32) << 16);
+            if (F32 && p.a.c && p.splits == 1) {
+                // C on its way to L2 while the products run
+                constexpr int size = F32 ? 4 : 2;
+#pragma unroll 1
+                for (int h = 0; h < S::HALVES; ++h) {
+                    const int64_t i = x.n0 + 256 * h + static_cast<int>(rank) * 128 + lg * 32 + lane;
+                    const int64_t j0 = x.k0 + 32 * c_first, j1 = min(p.a.k, j0 + 128);
+                    if (i < p.a.n)
+                        for (int64_t j = j0; j < j1; j += 128 / size)
+                            prefetch_l2(static_cast<const char*>(p.a.c) +
+                                        (x.e * p.a.stride_c + i * p.a.ld_c + j) * size);
+                }
+            }
             if (x.steps) {
                 if (!wait_full(first)) {
                     ok = false;
@@ -766,6 +812,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                                          : ((int64_t(x.split) * p.a.experts + x.e) * n + r0) * ld;
                 const int64_t c0 = x.e * p.a.stride_c + r0 * p.a.ld_c;
                 void* const g = apply ? p.a.g : p.part;
+                const bool affine = apply && (p.a.weight || p.a.bias);
                 const void* const add = apply ? p.a.c : nullptr;
                 constexpr int size = F32 ? 4 : 2;
                 if (rows > 0) {
@@ -773,67 +820,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                     for (int c = 0; c < 8; ++c) {
                         const int j0 = x.k0 + 32 * c_first + 16 * c;
                         if (j0 >= k) break;
+                        // Staged, and stored as rows of 64 bytes (lanes that
+                        // store their own rows straight from registers touch 32
+                        // lines a store): 16 columns of fp32, or 32 of bf16
+                        // from two rounds.  fp32 sums are finished on the way
+                        // out of the stage, bf16 ones before they are rounded
+                        // into it.
+                        const int odd = F32 ? 0 : c & 1;
+                        const int row0 = j0 - 16 * odd;
+                        const bool whole = p.vec && row0 + (F32 ? 16 : 32) <= k;
                         uint32_t raw[16];
-                        float v[16];
                         if (x.steps) {
                             tmem_ld16(taddr + 32 * c_first + 16 * c, raw);
                             tmem_ld_wait();
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) raw[u] = 0;
                         }
+                        const float* const weight = affine && p.a.weight ? p.a.weight + j0 : nullptr;
+                        const float* const bias = affine && p.a.bias ? p.a.bias + j0 : nullptr;
+                        if (F32 && whole) {
+                            __syncwarp();      // the last rows have been read
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) v[u] = x.steps ? __uint_as_float(raw[u]) : 0.f;
-                        if (apply && (p.a.weight || p.a.bias)) {
-                            const int j = j0 + (lane & 15);
-                            const float wl = p.a.weight && j < k ? p.a.weight[j] : 1.f;
-                            const float bl = p.a.bias && j < k ? p.a.bias[j] : 0.f;
-#pragma unroll
-                            for (int u = 0; u < 16; ++u)
-                                v[u] = fmaf(__shfl_sync(0xffffffffu, bl, u), sum,
-                                            v[u] * __shfl_sync(0xffffffffu, wl, u));
-                        }
-                        // Staged, and stored as rows of 64 bytes (lanes that store
-                        // their own rows straight from registers touch 32 lines a
-                        // store, which took three times as long): 16 columns of
-                        // fp32, or 32 of bf16 from two rounds.
-                        const int odd = F32 ? 0 : c & 1;
-                        const int row0 = j0 - 16 * odd;
-                        if (p.vec && row0 + (F32 ? 16 : 32) <= k) {
-                            if (!odd) __syncwarp();      // the last rows have been read
-                            if constexpr (F32) {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    blk[staged(lane, q)] = make_uint4(
-                                        __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                        __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
-                            } else {
-                                if (add && lane < rows)
-                                    add16(static_cast<const __nv_bfloat16*>(add) + c0 + lane * p.a.ld_c + j0, v);
-#pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    float t[8];
-#pragma unroll
-                                    for (int u = 0; u < 8; ++u) t[u] = v[8 * q + u];
-                                    store8_bf16(reinterpret_cast<__nv_bfloat16*>(
-                                                    &blk[staged(lane, q + 2 * odd)]), t);
-                                }
-                                if (!odd) continue;
-                            }
+                            for (int q = 0; q < 4; ++q)
+                                blk[staged(lane, q)] =
+                                    make_uint4(raw[4 * q], raw[4 * q + 1], raw[4 * q + 2], raw[4 * q + 3]);
                             __syncwarp();
-                            char* const to = static_cast<char*>(g) + (g0 + row0) * size;
-                            if (F32 && add)
-                                store_rows<true>(blk, to, ld * size,
-                                                 static_cast<const char*>(add) + (c0 + j0) * 4, p.a.ld_c * 4,
-                                                 rows, lane);
+                            float* const to = static_cast<float*>(g) + g0 + j0;
+                            if (affine || add)
+                                finish_rows(blk, to, ld,
+                                            add ? static_cast<const float*>(add) + c0 + j0 : nullptr,
+                                            p.a.ld_c, weight, bias, sum, rows, lane);
                             else
-                                store_rows<false>(blk, to, ld * size, nullptr, 0, rows, lane);
+                                store_rows(blk, reinterpret_cast<char*>(to), ld * size, rows, lane);
+                            continue;
+                        }
+                        if (whole) {
+                            float v[16];
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) v[u] = __uint_as_float(raw[u]);
+                            if (affine) {
+                                const float wl = weight ? weight[lane & 15] : 1.f;
+                                const float bl = bias ? bias[lane & 15] : 0.f;
+#pragma unroll
+                                for (int u = 0; u < 16; ++u)
+                                    v[u] = fmaf(__shfl_sync(0xffffffffu, bl, u), sum,
+                                                v[u] * __shfl_sync(0xffffffffu, wl, u));
+                            }
+                            if (!odd) __syncwarp();
+                            if (add && lane < rows)
+                                add16(static_cast<const __nv_bfloat16*>(add) + c0 + lane * p.a.ld_c + j0, v);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                float t[8];
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) t[u] = v[8 * q + u];
+                                store8_bf16(reinterpret_cast<__nv_bfloat16*>(&blk[staged(lane, q + 2 * odd)]),
+                                            t);
+                            }
+                            if (!odd) continue;
+                            __syncwarp();
+                            store_rows(blk, static_cast<char*>(g) + (g0 + row0) * size, ld * size, rows, lane);
                             continue;
                         }
                         float* const f = reinterpret_cast<float*>(blk);
                         __syncwarp();
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) f[lane * 16 + (u ^ (lane & 15))] = v[u];
+                        for (int u = 0; u < 16; ++u)
+                            f[lane * 16 + (u ^ (lane & 15))] = __uint_as_float(raw[u]);
                         __syncwarp();
-                        store_elements(f, g, F32 ? MUON_F32 : MUON_BF16, g0 + j0, ld, add, c0 + j0, p.a.ld_c,
-                                       rows, k - j0);
+                        store_elements(f, g, F32 ? MUON_F32 : MUON_BF16, g0 + j0, ld, add, c0 + j0,
+                                       p.a.ld_c, rows, k - j0, weight, bias, sum);
                         __syncwarp();
                     }
                 }
