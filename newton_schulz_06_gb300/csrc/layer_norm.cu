@@ -112,10 +112,17 @@ constexpr int ring_threads(int nv) { return nv == 4 && sizeof(T) == 4 ? 1024 : 5
 // vectors of bf16.
 constexpr int ring_blocks(int nv) { return nv < 4 ? 2 : 1; }
 
+// Blocks of 256 lanes that an SM is to hold: the rows in flight count for
+// more than a few spilled registers (65536 x 768 bf16: 44 us with 5, 50 with
+// 3; 65536 x 2048: 99 with 4, 103 with 3; 65536 x 512: 30 with 6, 34 where the
+// compiler takes the registers it likes, 41 with 8).
+template <typename T>
+constexpr int lane_blocks(int nv) { return nv < 4 ? 6 : nv == 4 ? 5 : sizeof(T) == 2 ? 4 : 2; }
+
 // A row in the registers of L lanes (256 / L rows a block) or of a block
 // (L = 0): NV vectors a thread.
 template <typename T, bool AL, int NV, int L>
-__global__ void __launch_bounds__(L ? 256 : 1024)
+__global__ void __launch_bounds__(L ? 256 : 1024, L ? lane_blocks<T>(NV) : 1)
     norm_kernel(const __grid_constant__ NormLaunch p) {
     constexpr int VE = Vec<T, AL>::VE, F2 = VE / 2;
     __shared__ float2 red[2][32];
@@ -382,12 +389,23 @@ RowShape row_shape(int64_t vectors, int most_lanes, int max_nv) {
     RowShape s;
     if (vectors <= most_lanes) {
         s.lanes = vectors <= 8 ? 8 : vectors <= 16 ? 16 : 32;
-        s.nv = vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4;
+        s.nv = vectors <= 32 ? 1 : vectors <= 64 ? 2 : vectors <= 128 ? 4 : vectors <= 256 ? 8 : 16;
         return s;
     }
     while (s.nv < max_nv && ceil_div(vectors, s.nv) > 512) s.nv *= 2;
     s.threads = static_cast<int>(ceil_div(ceil_div(vectors, s.nv), 32) * 32);
     return s;
+}
+
+// Vectors up to which a row's lanes of a warp are better than blocks.  Rows
+// off 16 bytes: 128 (16384 x 2047 bf16: 60 us by blocks, 91 by lanes).  Rows
+// on 16 bytes that fill the SMs: 256 of bf16 and 512 of fp32 (65536 x 2048
+// bf16: 102 us by lanes, 140 by blocks; 65536 x 4096: 268 and 270; 16384 x
+// 2048 fp32: 52 and 62), and 128 again for fewer rows, which blocks spread
+// over more SMs.
+template <typename T, bool AL>
+int most_lanes(int64_t rows) {
+    return !AL || rows < 8 * SMS ? 128 : sizeof(T) == 4 ? 512 : 256;
 }
 
 // Lets a kernel have `bytes` of dynamic shared memory.
@@ -413,7 +431,7 @@ cudaError_t launch_norm_ring(int grid, int threads, size_t smem, const NormLaunc
 // Rows for which blocks that stay pay: two a block and more.
 template <typename T, bool AL>
 cudaError_t norm_forward_ring(NormLaunch& p, cudaStream_t s, bool* done) {
-    const RowShape sh = row_shape(ceil_div(p.a.cols, Vec<T, AL>::VE), 128, 4);
+    const RowShape sh = row_shape(ceil_div(p.a.cols, Vec<T, AL>::VE), most_lanes<T, AL>(p.a.rows), 4);
     *done = false;
     if (sh.lanes || sh.threads > ring_threads<T>(sh.nv)) return cudaSuccess;
     int per_sm = sh.nv < 4 ? 1024 / sh.threads : 1;
@@ -442,7 +460,7 @@ cudaError_t norm_forward(NormLaunch& p, cudaStream_t s) {
     bool done;
     const cudaError_t e = norm_forward_ring<T, AL>(p, s, &done);
     if (done || e != cudaSuccess) return e;
-    const RowShape sh = row_shape(ceil_div(p.a.cols, Vec<T, AL>::VE), 128, 8);
+    const RowShape sh = row_shape(ceil_div(p.a.cols, Vec<T, AL>::VE), most_lanes<T, AL>(p.a.rows), 8);
     const unsigned rows = static_cast<unsigned>(p.a.rows);
     const dim3 block(sh.threads);
     if (sh.lanes) {
@@ -451,6 +469,11 @@ cudaError_t norm_forward(NormLaunch& p, cudaStream_t s) {
         if (sh.lanes == 16) return launch_kernel(norm_kernel<T, AL, 1, 16>, grid, block, 0, s, p);
         if (sh.nv == 1) return launch_kernel(norm_kernel<T, AL, 1, 32>, grid, block, 0, s, p);
         if (sh.nv == 2) return launch_kernel(norm_kernel<T, AL, 2, 32>, grid, block, 0, s, p);
+        if constexpr (AL) {
+            if (sh.nv == 8) return launch_kernel(norm_kernel<T, AL, 8, 32>, grid, block, 0, s, p);
+            if constexpr (sizeof(T) == 4)
+                if (sh.nv == 16) return launch_kernel(norm_kernel<T, AL, 16, 32>, grid, block, 0, s, p);
+        }
         return launch_kernel(norm_kernel<T, AL, 4, 32>, grid, block, 0, s, p);
     }
     const dim3 grid(rows);
@@ -525,9 +548,11 @@ struct GradVec {
 };
 
 // Short rows: L lanes have rows of their own (256 / L a block at a time) and
-// read them straight from memory, one row ahead.
+// read them straight from memory, one row ahead.  What bounds it is how many
+// rows are in flight: with the registers for four blocks an SM, which stay for
+// all rows, 262144 x 128 of bf16 take 47 us (4.2 TB/s), with three 67 us.
 template <typename T, bool AL, int L, bool CKPT>
-__global__ void __launch_bounds__(256) norm_grad_kernel(const __grid_constant__ GradLaunch p) {
+__global__ void __launch_bounds__(256, 4) norm_grad_kernel(const __grid_constant__ GradLaunch p) {
     constexpr int VE = Vec<T, AL>::VE, F2 = VE / 2, ROWS = 256 / L;
     __shared__ float sums[2][32 * VE];
     grid_dependency_wait();
