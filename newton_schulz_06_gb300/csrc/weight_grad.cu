@@ -75,7 +75,7 @@ struct Shape {
     static constexpr int SMEM = ORDER_OFF + W_ORDER * 2 + 1024;
     static_assert(SMEM <= 232448, "shared memory per CTA");
 };
-constexpr int COLSUM_PARTS = 16;      // of one matrix's tokens (experts: one part each)
+constexpr int COLSUM_PARTS = 32;      // of one matrix's tokens (experts: one part each)
 constexpr int BAND = 8;
 // fp32 results: the tensor cores cut a running sum off at its last place, so
 // that it shrinks by about 7e-9 of itself a product of 16 tokens (measured);
@@ -945,7 +945,10 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
 }
 
 // Sums of dY's columns over each matrix's tokens (gridDim.z parts of them):
-// 256 columns and 8 rows at a time in a block.
+// 256 columns and 8 rows at a time in a block.  It waits for its loads: 32
+// parts of one matrix's tokens keep more of them in flight than 16 (4097
+// tokens of 4096 columns, with the product behind it: 82 and 97 us; 64 parts
+// are no better).
 __global__ void __launch_bounds__(256)
     colsum_kernel(const __grid_constant__ muon_weight_grad_args a, float* out) {
     __shared__ float red[8][256];
