@@ -165,38 +165,52 @@ struct Selection {
     }
     __device__ __forceinline__ int expert(uint32_t top) const { return 65535 - (top & 0xffffu); }
 };
-// fp32: the key is the whole logit; the lane that holds the taken one looks
-// for its next.
+// fp32: the key is the whole logit.  A lane knows its largest two and where
+// they are; only where both are taken (once a token or so) it looks through
+// its keys again, for the largest one after the last in the order by key and
+// then by index (262144 tokens of 384 experts: 253 us, and 427 us looking
+// after each).
 template <int V, int L>
 struct Selection<float, V, L> {
-    uint32_t key[V], best;
-    int at, taken;
-    __device__ __forceinline__ void look() {
-        best = 0;
-        at = 0;
+    uint32_t key[V], best, second;       // 0: not known
+    int at, at2, taken;
+    __device__ __forceinline__ void start(const float (&v)[V], int lane, int experts) {
+        best = second = 0;
+        at = at2 = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+            key[i] = Logits<float, V, L, true>::expert(i, lane) < experts ? order_key(v[i]) : 0u;
             if (key[i] > best) {
+                second = best;
+                at2 = at;
                 best = key[i];
                 at = i;
+            } else if (key[i] > second) {
+                second = key[i];
+                at2 = i;
             }
-    }
-    __device__ __forceinline__ void start(const float (&v)[V], int lane, int experts) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            key[i] = Logits<float, V, L, true>::expert(i, lane) < experts ? order_key(v[i]) : 0u;
-        look();
+        }
     }
     __device__ __forceinline__ uint32_t next(int lane) {
         const uint32_t top = group_max<L>(best);
         const uint32_t e = ((at >> 2) * L + lane) * 4 + (at & 3);
-        const uint32_t mine = best == top ? e : 0xffffffffu;
-        taken = static_cast<int>(group_min<L>(mine));
-        if (static_cast<int>(mine) == taken && top) {
+        taken = static_cast<int>(group_min<L>(best == top ? e : 0xffffffffu));
+        const bool mine = top && best == top && static_cast<int>(e) == taken;
+        const int last = at;
+        if (mine) {
+            best = second;
+            at = at2;
+            second = 0;
+        }
+        if (__any_sync(0xffffffffu, mine && best == 0u)) {
+            if (mine && best == 0u) {
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i == at) key[i] = 0u;
-            look();
+                for (int i = 0; i < V; ++i)
+                    if (key[i] > best && (key[i] < top || (key[i] == top && i > last))) {
+                        best = key[i];
+                        at = i;
+                    }
+            }
         }
         return top;
     }
