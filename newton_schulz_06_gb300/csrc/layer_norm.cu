@@ -2,10 +2,11 @@
 // muon_layer_norm_grad).
 //
 // Forward.  A row is read once, in 16-byte vectors (at any alignment: see
-// Vec) that stay in registers, by 8 to 32 lanes of a warp or by a block.  The variance is taken around the
-// mean in a second sum over the registers (sums of x^2 lose it when the mean
-// is large), with the first sum's rounding corrected by the sum of the
-// deviations.  The checkpoint of h is written from the same registers.
+// Vec) that stay in registers, by 8 to 32 lanes of a warp or by a block.  The
+// variance is taken around the mean in a second sum over the registers (sums
+// of x^2 lose it when the mean is large), with the first sum's rounding
+// corrected by the sum of the deviations.  The checkpoint of h is written from
+// the same registers.
 //
 // Backward.  Blocks stay for many rows, so that the column sums of dweight
 // and dbias collect in registers: a thread has the same columns in every row.
@@ -120,7 +121,10 @@ template <typename T>
 constexpr int lane_blocks(int nv) { return nv < 4 ? 6 : nv == 4 ? 5 : sizeof(T) == 2 ? 4 : 2; }
 
 // A row in the registers of L lanes (256 / L rows a block) or of a block
-// (L = 0): NV vectors a thread.
+// (L = 0): NV vectors a thread.  Lanes need no barrier and few instructions a
+// row, and what bounds them is memory: 65536 x 2048 bf16 99 us (5.4 TB/s),
+// 65536 x 768 fp32 68 us (5.9 TB/s).  One block a row is for few rows: 64 x
+// 2048 4.4 us, which is the latency of the load and of two sums.
 template <typename T, bool AL, int NV, int L>
 __global__ void __launch_bounds__(L ? 256 : 1024, L ? lane_blocks<T>(NV) : 1)
     norm_kernel(const __grid_constant__ NormLaunch p) {
@@ -208,7 +212,12 @@ __global__ void __launch_bounds__(L ? 256 : 1024, L ? lane_blocks<T>(NV) : 1)
 
 // Many longer rows: blocks that stay, with the weight and the bias of their
 // threads' columns in registers and a ring of rows in shared memory that bulk
-// copies fill ahead of them.
+// copies fill ahead of them.  8192 x 7168 bf16: 55 us (4.2 TB/s), with the
+// checkpoint 70 us; 16384 x 4096 fp32 97 us (5.5 TB/s).  bf16 is bound by the
+// instructions of the two sums (59 % of the issue slots, and what waits for
+// their shuffles and barriers).  With one vector a thread instead of two, 8192
+// x 7168 takes 75 us; rows off 16 bytes take 97 us (8192 x 7167), for their
+// vectors are put together from two.
 template <typename T, bool AL, int NV, bool CKPT>
 __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     norm_ring_kernel(const __grid_constant__ NormLaunch p) {
@@ -332,7 +341,8 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     if (abort_flag && threadIdx.x == 0) ring_drain(full, stages, a.rows, p.wait_limit_ns);
 }
 
-// Rows that do not fit a block's registers: three sweeps over the row.
+// Rows that do not fit a block's registers: three sweeps over the row, of
+// which L2 serves two (1024 x 65536 bf16: 85 us, 3.1 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__ NormLaunch p) {
     __shared__ float2 red[2][32];
@@ -428,7 +438,9 @@ cudaError_t launch_norm_ring(int grid, int threads, size_t smem, const NormLaunc
     return e != cudaSuccess ? e : launch_kernel(KERN, dim3(grid), dim3(threads), smem, s, p);
 }
 
-// Rows for which blocks that stay pay: two a block and more.
+// Rows for which blocks that stay pay: two a block and more (8192 x 7168 bf16
+// 55 us, 74 with a block a row; 16384 x 4096 fp32 97 and 109 us; 2048 x 7168
+// 17 and 18 us; below that both are bound by the launch).
 template <typename T, bool AL>
 cudaError_t norm_forward_ring(NormLaunch& p, cudaStream_t s, bool* done) {
     const RowShape sh = row_shape(ceil_div(p.a.cols, Vec<T, AL>::VE), most_lanes<T, AL>(p.a.rows), 4);
@@ -643,7 +655,12 @@ __global__ void __launch_bounds__(256, 4) norm_grad_kernel(const __grid_constant
 // of `stages` rows in shared memory, filled by bulk copies of the aligned
 // 16-byte pieces that hold a row, so that memory is kept busy whatever the
 // registers hold.  With more than one vector a thread, the second sweep takes
-// a row from the ring again instead of keeping it in registers.
+// a row from the ring again instead of keeping it in registers.  8192 x 7168
+// bf16: 77 us (4.6 TB/s), from the checkpoint 79 us (3.7 TB/s); 16384 x 4096
+// fp32 135 us (5.9 TB/s).  bf16 is bound by instructions and their latency at
+// 64 registers a thread: 896 threads of one vector take 91 us, blocks of
+// several rows that share the weight 82, a bf16 weight in shared memory 89;
+// rows off 16 bytes 167 us (8192 x 7167).
 template <typename T, bool AL, int NV, bool CKPT>
 __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     norm_grad_ring_kernel(const __grid_constant__ GradLaunch p) {
@@ -800,7 +817,8 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     if (abort_flag && threadIdx.x == 0) ring_drain(full, stages, a.rows, p.wait_limit_ns);
 }
 
-// The partial sums of 32 columns in a block, 32 of them at a time.
+// The partial sums of 32 columns in a block, 32 of them at a time (304 of 7168
+// columns 7 us, 1216 of 768 columns 13 us).
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const __grid_constant__ GradLaunch p) {
     __shared__ float red[2][32][33];
     grid_dependency_wait();

@@ -11,6 +11,12 @@
 // Sums of p over the tokens collect in registers, then in one row of partial
 // results a block; a cluster of blocks adds these up in order and computes
 // offsets and loss.
+//
+// What bounds the forward pass is the arithmetic of the selection and of the
+// exponentials: 32769 tokens of 384 experts, bf16, k = 8: 26 us, 71 % of the
+// integer pipe's rate, and 11 us for the second kernel; 262144 tokens 178 us
+// (fp32 253 us).  The gradient: 19 us, and 118 us (3.6 TB/s).  200 tokens of
+// 128 experts take 5 us in each of the two kernels, a launch's latency.
 #include "ops_internal.h"
 
 namespace muon {
@@ -411,9 +417,11 @@ __global__ void __cluster_dims__(JOIN_CTAS, 1, 1) __launch_bounds__(JOIN_THREADS
 // dz = p (h - sum p h), where h is the loss's part, the same for all tokens
 // (count times a factor, in registers), and for the taken experts also that
 // of their weights: a lane computes theirs again and stores them over the
-// others'.
+// others'.  Registers for four blocks an SM: 262144 tokens of 384 experts
+// bf16 118 us, fp32 162 us (5.1 TB/s), and 126 and 181 us with what the
+// compiler takes (79 registers).
 template <typename T, int V, int L, bool AL>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, V <= 16 ? 4 : 2)
     route_grad_kernel(const __grid_constant__ muon_route_grad_args a) {
     constexpr int ROWS = 256 / L;
     grid_dependency_wait();
@@ -488,6 +496,9 @@ __global__ void __launch_bounds__(256)
 
 // Rows of a block (of 512 or 256 threads) and how many blocks run.
 int route_v(int64_t experts) { return static_cast<int>(ceil_div(experts, 128) * 4); }
+// Eight lanes a token, four tokens a warp, where they hold the experts and the
+// taken ones (2^20 tokens of 8 experts, k = 2, bf16: 91 us, with a warp a token
+// 325; 32 experts, k = 4: 100 and 358 us; the gradient of 8 experts 58 and 237).
 bool eight_lanes(int64_t experts, int64_t k) { return experts <= 32 && k <= 8; }
 int route_rows(int64_t experts, int64_t k) {
     return eight_lanes(experts, k) ? 64 : route_v(experts) <= 16 ? 16 : 8;

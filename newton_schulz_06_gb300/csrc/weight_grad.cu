@@ -79,7 +79,9 @@ constexpr int COLSUM_PARTS = 32;      // of one matrix's tokens (experts: one pa
 constexpr int BAND = 8;
 // fp32 results: the tensor cores cut a running sum off at its last place, so
 // that it shrinks by about 7e-9 of itself a product of 16 tokens (measured);
-// after this many steps it is added to a sum that is rounded to nearest.
+// after this many steps it is added to a sum that is rounded to nearest (4096
+// tokens of 7168 x 8192: 377 us, 363 with one sum, whose error is 1.8e-6
+// instead of 4e-7).
 constexpr int CHUNK_STEPS = 16;
 
 __device__ int g_ops_err;
@@ -176,8 +178,8 @@ __device__ __forceinline__ void commit_pair_local(uint32_t bar) {
 // Arrive on a barrier of the pair's leader.  What the waiter's products read
 // are this CTA's own writes to its shared memory, ordered before the arrival
 // by the fence to the async proxy; a release over the whole cluster would
-// wait for every load in flight (measured: the decoding warps' scale loads,
-// a third of the kernel's time).
+// wait for every load in flight (the decoding warps' scale loads: 4096 tokens
+// of 4096 x 2048 took 256 us instead of 116 at the time).
 __device__ __forceinline__ void arrive_leader(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
@@ -296,6 +298,7 @@ __device__ __forceinline__ void add16(const __nv_bfloat16* p, float (&v)[16]) {
 // 16 columns of 32 sums, staged with the columns XORed with the row, to a
 // gradient element by element (rows off 16 bytes, a row's last columns): two
 // rows at a time.  `left`: the columns there are; sum: of dY's column `lane`.
+// (4096 tokens of 7168 x 8191, bf16: 422 us; 8192 columns, by rows: 287 us.)
 __device__ __noinline__ void store_elements(const float* f, void* g, int g_type, int64_t at, int64_t ld,
                                             const void* add, int64_t c_at, int64_t ld_c, int rows,
                                             int left, const float* weight, const float* bias, float sum) {
@@ -464,8 +467,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
     grid_dependency_wait();
     allow_dependent_launch();
     // Experts by their size, the largest first: with tiles dealt out in turn,
-    // no pair then has more than about one tile's steps above another (a
-    // quarter of the time, with sizes as a router gives them).
+    // no pair then has more than about one tile's steps above another.  Sizes
+    // that fall as 1 / rank: 128 experts of 768 x 2048 302 us instead of 319,
+    // 16 of 2048 x 2048 147 instead of 166; even sizes: no difference.
     uint16_t* order = nullptr;
     if (p.sorted) {
         order = reinterpret_cast<uint16_t*>(smem + S::ORDER_OFF);
@@ -1015,7 +1019,8 @@ int64_t tiles(const muon_weight_grad_args& a) {
 }
 
 // Parts that the tokens are split into: as many as give every pair a tile,
-// each of eight steps or more on average.
+// each of eight steps or more on average (8192 tokens of 512 x 2048: 30 us in
+// four parts, 55 in one; 300 tokens: 16 and 15 us, not split).
 int split_count(const muon_weight_grad_args& a) {
     const int64_t steps = ceil_div(ceil_div(a.rows, a.experts), W_TOK);
     int64_t s = W_PAIRS / tiles(a);
