@@ -409,13 +409,14 @@ RowShape row_shape(int64_t vectors, int most_lanes, int max_nv) {
 
 // Vectors up to which a row's lanes of a warp are better than blocks.  Rows
 // off 16 bytes: 128 (16384 x 2047 bf16: 60 us by blocks, 91 by lanes).  Rows
-// on 16 bytes that fill the SMs: 256 of bf16 and 512 of fp32 (65536 x 2048
-// bf16: 102 us by lanes, 140 by blocks; 65536 x 4096: 268 and 270; 16384 x
-// 2048 fp32: 52 and 62), and 128 again for fewer rows, which blocks spread
-// over more SMs.
+// on 16 bytes, of which every SM has two rounds: 256 of bf16 and 512 of fp32
+// (65536 x 2048 bf16: 99 us by lanes, 140 by blocks; 16384 x 2048: 31 and 40;
+// 65536 x 4096: 268 and 270; 16384 x 2048 fp32: 52 and 62).  Fewer rows are
+// done sooner by blocks, which spread a row over more warps: 512 x 2048 bf16
+// 4.7 us and 12.3 by lanes, 2048 x 2048 9.5 and 13, 8192 x 2048 23 and 25.
 template <typename T, bool AL>
 int most_lanes(int64_t rows) {
-    return !AL || rows < 8 * SMS ? 128 : sizeof(T) == 4 ? 512 : 256;
+    return !AL || rows < 64 * SMS ? 128 : sizeof(T) == 4 ? 512 : 256;
 }
 
 // Lets a kernel have `bytes` of dynamic shared memory.

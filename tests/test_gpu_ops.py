@@ -171,6 +171,32 @@ def test_layer_norm_checkpoint(ns, shape, dtype):
     check_saved(saved, h, norm_bounds(to64(x), mean64, rstd64, h)[2])
 
 
+@pytest.mark.parametrize("rows,cols,dtype", [(9729, 1032, BF), (10000, 1536, BF), (9800, 2048, BF),
+                                             (9728, 2056, BF), (9731, 516, F32), (9728, 1024, F32),
+                                             (9729, 1028, F32), (9730, 2048, F32)])
+def test_layer_norm_of_many_rows(ns, rows, cols, dtype):
+    """Enough rows for a warp to have a long one, the last block partly
+    filled, up to the row's length where blocks take over again."""
+    x = rand(25, rows, cols, scale=2.0, shift=-0.4, dtype=dtype)
+    w, b = rand(26, cols), rand(27, cols)
+    y, mean, rstd = ns.layer_norm(x, w, b)
+    y64, mean64, rstd64, h = O.layer_norm(to64(x), to64(w), to64(b), 1e-5)
+    d_mean, d_rel, d_h = norm_bounds(to64(x), mean64, rstd64, h)
+    close(mean, mean64, d_mean, "mean")
+    close(rstd, rstd64, d_rel * rstd64, "rstd")
+    aw, ab = to64(w).abs(), to64(b).abs()
+    close(y, y64, aw * d_h + 2 * U32 * (h.abs() * aw + ab) + OUT_ROUND[dtype] * y64.abs() + 1e-38, "y")
+    out = strided(torch.zeros(rows, cols, dtype=dtype, device=DEV), 16, 16)
+    base = out._base.clone()
+    assert torch.equal(ns.layer_norm(x, w, b, out=out)[0], y)
+    rest = out._base.clone()
+    rest[16:16 + rows * (cols + 16)].view(rows, cols + 16)[:, :cols] = 0
+    assert torch.equal(rest, base)                          # nothing outside the view
+    y1, rstd1, saved = ns.layer_norm_checkpoint(x, w, b)
+    assert torch.equal(y1, y) and torch.equal(rstd1, rstd)
+    check_saved(saved, h, d_h)
+
+
 def check_norm_grads(got, dy, h, rstd, w, dtype, d_h):
     """got: (dx, dweight, dbias); h, rstd: 64-bit, d_h: how far off the fp32 h."""
     dx, dw, db = got
