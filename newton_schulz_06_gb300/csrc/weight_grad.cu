@@ -35,6 +35,7 @@
 
 #include "ops_internal.h"
 #include "tc_wait.cuh"
+#include "weight_grad_stages.h"
 
 namespace muon {
 namespace ops {
@@ -50,23 +51,18 @@ constexpr int W_R_BYTES = 2 * W_RBOX;
 constexpr int W_EPI_WARPS = 8;                     // two for 32 rows of the tile
 constexpr int W_DEC_WARPS = 4;                     // that decode one step
 constexpr int W_DEC_BLOCKS = 8 / W_DEC_WARPS;      // blocks of 32 values a thread decodes
-constexpr int W_DEC_GROUPS = 2;                    // steps in turn
 constexpr int W_DEC_WARP0 = 2 + W_EPI_WARPS;
 constexpr int W_THREADS = 32 * (W_DEC_WARP0 + W_DEC_GROUPS * W_DEC_WARPS);
 constexpr int W_EPI_BYTES = 32 * 64;               // a warp's staged block: 32 rows of 64 bytes
 constexpr int W_ORDER = 512;                       // experts that are taken by their size
 constexpr int W_TMEM_COLS = 512;
 constexpr int W_PAIRS = 76;                        // a pair per two of the 152 SMs
-// A tile's 256-row halves and the rings of stages: of dY (A), of the decoded
-// values (B) and of the 8-bit ones (R).  The rings of WIDE are as long as the
-// shared memory allows, and each has its own barriers; in the other shape the
-// decoding warps have no time for them (345 -> 444 us with 4096 tokens of
-// 7168 x 8192).
+// A tile's 256-row halves and the rings of stages in shared memory.
 template <bool WIDE>
 struct Shape {
     static constexpr int HALVES = WIDE ? 2 : 1;
-    static constexpr int A_STAGES = WIDE ? 4 : 5, B_STAGES = WIDE ? 3 : 5, R_STAGES = WIDE ? 4 : 5;
-    static constexpr int AHEAD = R_STAGES - 2;     // steps that R's loads run ahead of A's
+    static constexpr int A_STAGES = Stages<WIDE>::A, B_STAGES = Stages<WIDE>::B, R_STAGES = Stages<WIDE>::R;
+    static constexpr int AHEAD = Stages<WIDE>::AHEAD;
     static constexpr int A_BYTES = HALVES * 2 * W_BOX;
     static constexpr int B_OFF = A_STAGES * A_BYTES, R_OFF = B_OFF + B_STAGES * W_B_BYTES;
     static constexpr int BAR_OFF = R_OFF + R_STAGES * W_R_BYTES;
@@ -506,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             uint32_t nr = 0, na = 0;      // steps issued
             bool ok = true;
             auto load_r = [&](const Steps<WIDE>& at, uint32_t n, uint32_t bar) {
-                const uint32_t dst = smem_u32(sR + n % S::R_STAGES * W_R_BYTES);
+                const uint32_t dst = smem_u32(sR + stage_of(n, S::R_STAGES) * W_R_BYTES);
                 const int b0 = at.x.k0 + static_cast<int>(rank) * 128, t = at.x.t0 + at.s * W_TOK;
                 tma_load_2d(dst, &p.tm_q, bar, b0, t);
                 tma_load_2d(dst + W_RBOX, &p.tm_q, bar, b0 + 64, t);
@@ -514,15 +510,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             while (ok && aa.more) {
                 if constexpr (WIDE)
                     for (; ra.more && nr <= na + S::AHEAD; ++nr, ra.next()) {
-                        const uint32_t slot = nr % S::R_STAGES, rb = smem_u32(&r_bar[slot]);
-                        ok = wait_soon(smem_u32(&free_bar[slot]), (nr / S::R_STAGES & 1) ^ 1, abort_flag,
+                        const uint32_t slot = stage_of(nr, S::R_STAGES), rb = smem_u32(&r_bar[slot]);
+                        ok = wait_soon(smem_u32(&free_bar[slot]), parity_of(nr, S::R_STAGES) ^ 1, abort_flag,
                                        &g_ops_err, limit);
                         if (!ok) break;
                         mbar_expect_tx(rb, W_R_BYTES);
                         load_r(ra, nr, rb);
                     }
-                const uint32_t slot = na % S::A_STAGES, ab = smem_u32(&a_bar[slot]);
-                ok = ok && wait_soon(smem_u32(&done_bar[slot]), (na / S::A_STAGES & 1) ^ 1, abort_flag,
+                const uint32_t slot = stage_of(na, S::A_STAGES), ab = smem_u32(&a_bar[slot]);
+                ok = ok && wait_soon(smem_u32(&done_bar[slot]), parity_of(na, S::A_STAGES) ^ 1, abort_flag,
                                      &g_ops_err, limit);
                 if (!ok) break;
                 mbar_expect_tx(ab, S::A_BYTES + (WIDE ? 0 : W_R_BYTES));
@@ -540,9 +536,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             if (!ok) {
                 // the last load of each stage
                 for (uint32_t i = nr - min(nr, uint32_t(S::R_STAGES)); i < nr; ++i)
-                    wait_quiet(smem_u32(&r_bar[i % S::R_STAGES]), i / S::R_STAGES & 1, limit);
+                    wait_quiet(smem_u32(&r_bar[stage_of(i, S::R_STAGES)]), parity_of(i, S::R_STAGES), limit);
                 for (uint32_t i = na - min(na, uint32_t(S::A_STAGES)); i < na; ++i)
-                    wait_quiet(smem_u32(&a_bar[i % S::A_STAGES]), i / S::A_STAGES & 1, limit);
+                    wait_quiet(smem_u32(&a_bar[stage_of(i, S::A_STAGES)]), parity_of(i, S::A_STAGES), limit);
             }
         }
     } else if (warp == 1) {
@@ -567,8 +563,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             };
             // the products of a step and of the tile's half h
             auto products = [&](uint32_t acc, int h, bool fresh) {
-                const uint64_t ad = a_desc + (step % S::A_STAGES * S::A_BYTES + h * 2 * W_BOX >> 4);
-                const uint64_t bd = b_desc + (step % S::B_STAGES * W_B_BYTES >> 4);
+                const uint64_t ad = a_desc + (stage_of(step, S::A_STAGES) * S::A_BYTES + h * 2 * W_BOX >> 4);
+                const uint64_t bd = b_desc + (stage_of(step, S::B_STAGES) * W_B_BYTES >> 4);
 #pragma unroll
                 for (int kk = 0; kk < W_TOK / 16; ++kk)
                     mma_pair(tmem_base + acc * 256, ad + static_cast<uint64_t>(kk * (2048 >> 4)),
@@ -587,8 +583,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                     }
                     const int s1 = min(s0 + chunk, x.steps);
                     for (int s = s0; s < s1; ++s, ++step) {
-                        if (!wait_soon(smem_u32(&ready_bar[step % S::B_STAGES]),
-                                       step / S::B_STAGES & 1, abort_flag, &g_ops_err, limit)) {
+                        if (!wait_soon(smem_u32(&ready_bar[stage_of(step, S::B_STAGES)]),
+                                       parity_of(step, S::B_STAGES), abort_flag, &g_ops_err, limit)) {
                             ok = false;
                             break;
                         }
@@ -602,7 +598,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                             }
                             products(1, 1, s == 0);
                         }
-                        commit_pair_multicast(smem_u32(&done_bar[step % S::A_STAGES]));
+                        commit_pair_multicast(smem_u32(&done_bar[stage_of(step, S::A_STAGES)]));
                     }
                     if (ok) commit_pair_multicast(smem_u32(&tfull_bar[acc]));
                 }
@@ -675,20 +671,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                 for (int u = 0; u < 4; ++u) {
                     const int su = s + u * W_DEC_GROUPS;
                     if (su >= x.steps) break;
-                    const uint32_t sa = step % S::A_STAGES, sb = step % S::B_STAGES,
-                                   sr = step % S::R_STAGES;
-                    bool got;
-                    if constexpr (WIDE) {
-                        const uint32_t last = step - S::B_STAGES;    // that used this stage of B
-                        got = wait_soon(smem_u32(&r_bar[sr]), step / S::R_STAGES & 1, abort_flag,
-                                        &g_ops_err, limit) &&
-                              (step < S::B_STAGES ||
-                               wait_soon(smem_u32(&done_bar[last % S::A_STAGES]),
-                                         last / S::A_STAGES & 1, abort_flag, &g_ops_err, limit));
-                    } else {
-                        got = wait_soon(smem_u32(&a_bar[sa]), step / S::A_STAGES & 1, abort_flag,
-                                        &g_ops_err, limit);
-                    }
+                    const uint32_t sa = stage_of(step, S::A_STAGES), sb = stage_of(step, S::B_STAGES),
+                                   sr = stage_of(step, S::R_STAGES);
+                    // the step that had the stage of B before, which may have
+                    // been the other group's: without this wait, a load of
+                    // that step's that is slow to land makes the next one
+                    // return too soon (weight_grad_stages.h)
+                    const uint32_t last = last_user<WIDE>(step);
+                    bool got = !stage_was_used<WIDE>(step) ||
+                               wait_soon(smem_u32(&done_bar[stage_of(last, S::A_STAGES)]),
+                                         parity_of(last, S::A_STAGES), abort_flag, &g_ops_err, limit);
+                    // WIDE: the 8-bit values; else both operands
+                    uint64_t* const in = WIDE ? &r_bar[sr] : &a_bar[sa];
+                    got = got && wait_soon(smem_u32(in), parity_of(step, WIDE ? S::R_STAGES : S::A_STAGES),
+                                           abort_flag, &g_ops_err, limit);
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
@@ -718,7 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&free_bar[sr]));
                         // dY has to be there too
-                        const bool in = wait_soon(smem_u32(&a_bar[sa]), step / S::A_STAGES & 1,
+                        const bool in = wait_soon(smem_u32(&a_bar[sa]), parity_of(step, S::A_STAGES),
                                                   abort_flag, &g_ops_err, limit);
                         if (!__all_sync(0xffffffffu, in)) {
                             ok = false;
