@@ -675,16 +675,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                                    sr = stage_of(step, S::R_STAGES);
                     // the step that had the stage of B before, which may have
                     // been the other group's: without this wait, a load of
-                    // that step's that is slow to land makes the next one
-                    // return too soon (weight_grad_stages.h)
+                    // that step's that is slow to land makes a wait for both
+                    // operands return too soon (weight_grad_stages.h).  WIDE:
+                    // the 8-bit values have a stage whose users are all this
+                    // group's, and are asked for first (16384 tokens: 1038 us,
+                    // 1061 the other way round)
                     const uint32_t last = last_user<WIDE>(step);
-                    bool got = !stage_was_used<WIDE>(step) ||
+                    const auto used = [&] {
+                        return !stage_was_used<WIDE>(step) ||
                                wait_soon(smem_u32(&done_bar[stage_of(last, S::A_STAGES)]),
                                          parity_of(last, S::A_STAGES), abort_flag, &g_ops_err, limit);
-                    // WIDE: the 8-bit values; else both operands
-                    uint64_t* const in = WIDE ? &r_bar[sr] : &a_bar[sa];
-                    got = got && wait_soon(smem_u32(in), parity_of(step, WIDE ? S::R_STAGES : S::A_STAGES),
-                                           abort_flag, &g_ops_err, limit);
+                    };
+                    const auto there = [&] {
+                        return wait_soon(smem_u32(WIDE ? &r_bar[sr] : &a_bar[sa]),
+                                         parity_of(step, WIDE ? S::R_STAGES : S::A_STAGES), abort_flag,
+                                         &g_ops_err, limit);
+                    };
+                    const bool got = WIDE ? there() && used() : used() && there();
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;

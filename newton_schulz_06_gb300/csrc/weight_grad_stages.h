@@ -25,6 +25,7 @@ template <bool WIDE>
 struct Stages {
     static constexpr int A = WIDE ? 4 : 5, B = WIDE ? 3 : 5, R = WIDE ? 4 : 5;
     static constexpr int AHEAD = R - 2;      // steps that R's loads run ahead of A's (WIDE)
+    static_assert(!WIDE || R % W_DEC_GROUPS == 0, "a stage of R is one group's");
 };
 
 // The stage of a step in a ring of n, and the parity of the step's phase of
@@ -35,9 +36,10 @@ MUON_HD uint32_t parity_of(uint32_t step, uint32_t n) { return step / n & 1; }
 // A wait for a parity also returns while the phase before the one that is
 // meant has not completed: a group may only wait for a phase of a stage whose
 // earlier phases it knows to be over.  Of its own steps it knows; the stage's
-// last user may have been the other group's step.  So every step first waits
-// for the products of the step that last had its stage of B: they read all
-// that was loaded and decoded for that step, and those before it ran in order.
+// last user may have been the other group's step.  So every step waits for the
+// products of the step that last had its stage of B: they read all that was
+// loaded and decoded for that step, and those before it ran in order.  It does
+// so before anything else unless the stages of R are a group's own.
 template <bool WIDE>
 MUON_HD bool stage_was_used(uint32_t step) { return step >= uint32_t(Stages<WIDE>::B); }
 template <bool WIDE>

@@ -40,4 +40,4 @@ def test_the_kernel_waits_for_the_stages_last_user():
     wait = text[text.index("const uint32_t last = last_user<WIDE>(step);"):]
     wait = wait[:wait.index("uint4 q[")]
     assert "if constexpr" not in wait and "stage_was_used<WIDE>(step)" in wait
-    assert wait.index("done_bar[stage_of(last, S::A_STAGES)]") < wait.index("r_bar[sr] : &a_bar[sa]")
+    assert "WIDE ? there() && used() : used() && there()" in wait

@@ -100,16 +100,18 @@ bool plays(std::mt19937& rng, bool guard) {
             const uint32_t step = w.step, sa = stage_of(step, S::A), sb = stage_of(step, S::B),
                            sr = stage_of(step, S::R);
             const int me = int(i) % WARPS;
-            if (w.at == 0) {                              // the stage's last user
-                const uint32_t last = last_user<WIDE>(step);
-                if (guard && stage_was_used<WIDE>(step) &&
-                    !done[stage_of(last, S::A)].over(parity_of(last, S::A)))
-                    continue;
-                w.at = 1;
-            }
-            if (w.at == 1) {                              // the 8-bit values
-                const Bar& in = WIDE ? r[sr] : a[sa];
-                if (!in.over(WIDE ? parity_of(step, S::R) : parity_of(step, S::A))) continue;
+            const Bar& in = WIDE ? r[sr] : a[sa];
+            const uint32_t last = last_user<WIDE>(step);
+            auto used = [&] {                             // the stage's last user
+                return !guard || !stage_was_used<WIDE>(step) ||
+                       done[stage_of(last, S::A)].over(parity_of(last, S::A));
+            };
+            auto there = [&] {                            // the 8-bit values
+                return in.over(WIDE ? parity_of(step, S::R) : parity_of(step, S::A));
+            };
+            if (w.at == 0 && (WIDE ? there() : used())) w.at = 1;
+            if (w.at == 1) {
+                if (!(WIDE ? used() : there())) continue;
                 bad |= has_r[sr] != int(step);
                 // nothing that the products have not read may be written over
                 bad |= has_b[sb][me] >= 0 && uint32_t(has_b[sb][me]) >= products;
@@ -117,6 +119,7 @@ bool plays(std::mt19937& rng, bool guard) {
                 if (WIDE) free_r[sr].arrive();
                 w.at = 2;
             }
+            if (w.at == 0) continue;
             if (WIDE && !a[sa].over(parity_of(step, S::A))) continue;
             bad |= has_a[sa] != int(step);
             ready[sb].arrive();
