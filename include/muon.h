@@ -545,6 +545,12 @@ MUON_API int muon_route_grad(const muon_route_grad_args* args, void* cuda_stream
  * whole), MUON_ERR_CUDA for a CUDA error, else MUON_OK. */
 MUON_API int muon_ops_sync(void* cuda_stream, char* err, size_t err_len);
 
+/* Failure test only: queues a wait of the operators' kind that nothing
+ * satisfies.  It runs out after limit_ms (1 .. 10000) and raises what
+ * muon_ops_sync then reports as MUON_ERR_TIMEOUT. */
+MUON_API int muon_debug_ops_wait_timeout(int limit_ms, void* cuda_stream, char* err,
+                                         size_t err_len);
+
 #ifdef __cplusplus
 }
 #endif

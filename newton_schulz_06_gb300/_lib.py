@@ -44,7 +44,7 @@ EXPORTS = ("muon_create", "muon_set_stream", "muon_register_params",
            "muon_layer_norm_grad_workspace", "muon_layer_norm_grad",
            "muon_weight_grad_workspace", "muon_weight_grad",
            "muon_route_workspace", "muon_route", "muon_route_grad",
-           "muon_ops_sync")
+           "muon_ops_sync", "muon_debug_ops_wait_timeout")
 
 
 class MuonParam(ctypes.Structure):
@@ -180,6 +180,7 @@ def lib() -> ctypes.CDLL:
         "muon_route": [vp, vp, sz, vp, vp, sz],
         "muon_route_grad": [vp, vp, vp, sz],
         "muon_ops_sync": [vp, vp, sz],
+        "muon_debug_ops_wait_timeout": [i32, vp, vp, sz],
     }
     for name, args in sig.items():
         fn = getattr(L, name)

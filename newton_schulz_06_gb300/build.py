@@ -28,7 +28,7 @@ SOURCES = ["ew_kernels.cu", "ns_kernels.cu", "ns2_kernels.cu", "muon_api.cpp",
            "weight_grad.cu", "route.cu"]
 HEADERS = [os.path.join(CSRC, "muon_internal.h"), os.path.join(CSRC, "tc_ptx.cuh"),
            os.path.join(CSRC, "ops_internal.h"), os.path.join(CSRC, "tc_wait.cuh"),
-           os.path.join(CSRC, "weight_grad_stages.h"),
+           os.path.join(CSRC, "weight_grad_stages.h"), os.path.join(CSRC, "norm_ring.h"),
            os.path.join(ROOT, "include", "muon.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -12,6 +12,7 @@
 // and dbias collect in registers: a thread has the same columns in every row.
 // Each block leaves one row of partial sums, which a second kernel adds up in
 // order.
+#include "norm_ring.h"
 #include "ops_internal.h"
 #include "tc_wait.cuh"
 
@@ -91,19 +92,21 @@ struct Pieces {
 };
 
 // Waits until the ring's stage is full.  A wait that runs out raises the
-// flag, which ends the later ones at once; the rows that follow hold nothing
-// of use then.
-__device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t phase, int* abort_flag,
+// flag.  Every thread reads it behind the barrier that follows, where it can
+// no longer change, so that the whole block leaves the loop at the same row:
+// a stage whose copy has not landed is never asked for again.
+__device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t phase, volatile int* abort_flag,
                                           unsigned long long limit_ns) {
     wait_soon(ptx::smem_u32(bar), phase, abort_flag, &g_norm_err, limit_ns);
 }
-// After an abort: copies still in flight must land before the block leaves.
-__device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int64_t rows,
-                                           unsigned long long limit_ns) {
-    const int64_t mine = (rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
-    for (int s = 0; s < stages && s < mine; ++s)
-        ptx::wait_quiet(ptx::smem_u32(&full[s]),
-                        static_cast<uint32_t>((mine - s + stages - 1) / stages - 1) & 1u, limit_ns);
+// After an abort at the row that `at` stands for: the copies still in flight
+// must land before the block leaves.
+__device__ __forceinline__ void ring_drain(uint64_t* full, RingAt at, int stages, int64_t rows,
+                                           int64_t row, unsigned long long limit_ns) {
+    for (int d = 0; ring_in_flight(rows, row, gridDim.x, stages, d); ++d) {
+        const RingAt l = ring_ahead(at, stages, d);
+        ptx::wait_quiet(ptx::smem_u32(&full[l.stage]), l.phase, limit_ns);
+    }
 }
 constexpr int RING_MAX = 8;
 // Threads that a block of the ring kernels may have.
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float2 red[2][32];
     __shared__ uint64_t full[RING_MAX];
-    __shared__ int abort_flag;
+    __shared__ volatile int abort_flag;
     grid_dependency_wait();
     allow_dependent_launch();
     const muon_layer_norm_args& a = p.a;
@@ -256,13 +259,14 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     }
     const int padded = (cols + CKPT_BLOCK - 1) / CKPT_BLOCK * CKPT_BLOCK;
     __syncthreads();
-    int stage = 0;
-    uint32_t phase = 0;
+    RingAt at{0, 0};
+    bool aborted = false;
     T* y = static_cast<T*>(a.y) + blockIdx.x * a.ld_y + c0;
     const int64_t y_step = gridDim.x * a.ld_y;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, y += y_step) {
-        ring_wait(&full[stage], phase, &abort_flag, p.wait_limit_ns);
-        const T* x = reinterpret_cast<const T*>(ring + stage * p.stage_bytes +
+    int64_t r = blockIdx.x;
+    for (; r < a.rows; r += gridDim.x, y += y_step) {
+        ring_wait(&full[at.stage], at.phase, &abort_flag, p.wait_limit_ns);
+        const T* x = reinterpret_cast<const T*>(ring + at.stage * p.stage_bytes +
                                                 (AL ? 0 : Pieces::lead(x0 + r * a.ld_x)));
         float2 v[NV][F2];
         float2 s = both(0.f);
@@ -281,8 +285,10 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
             for (int j = 0; j < F2; ++j) s = add2(s, v[i][j]);
         }
         float mean = block_sum(s.x + s.y, red[0]) * inv_n;
-        // its barrier says that every thread has read the stage
-        if (threadIdx.x == 0) load(r + int64_t(stages) * gridDim.x, stage);
+        // its barrier says that every thread has read the stage; a later row's
+        // wait is behind the next barrier
+        if ((aborted = abort_flag)) break;
+        if (threadIdx.x == 0) load(r + int64_t(stages) * gridDim.x, at.stage);
         float2 d1 = both(0.f), d2 = both(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -332,13 +338,9 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
             out.set(h);
             out.store(y + i * step, valid, c == 0);
         }
-        if (++stage == stages) {
-            stage = 0;
-            phase ^= 1;
-        }
+        at = ring_ahead(at, stages, 1);
     }
-    __syncthreads();
-    if (abort_flag && threadIdx.x == 0) ring_drain(full, stages, a.rows, p.wait_limit_ns);
+    if (aborted && threadIdx.x == 0) ring_drain(full, at, stages, a.rows, r, p.wait_limit_ns);
 }
 
 // Rows that do not fit a block's registers: three sweeps over the row, of
@@ -671,7 +673,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     uint8_t* const ring = shared + p.w_bytes;
     __shared__ float2 red[2][32];
     __shared__ uint64_t full[RING_MAX];
-    __shared__ int abort_flag;
+    __shared__ volatile int abort_flag[2];   // of even and of odd rows
     grid_dependency_wait();
     allow_dependent_launch();
     const muon_layer_norm_grad_args& a = p.a;
@@ -682,7 +684,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     const int stages = p.stages;
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) ptx::mbar_init(ptx::smem_u32(&full[s]), 1);
-        abort_flag = 0;
+        abort_flag[0] = abort_flag[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // the weight in fp32, which every row needs (the ring leaves L1 no room),
@@ -722,8 +724,9 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     float2 dw[NV * F2], db[NV * F2];
 #pragma unroll
     for (int i = 0; i < NV * F2; ++i) dw[i] = db[i] = both(0.f);
-    int odd = 0, stage = 0;
-    uint32_t phase = 0;
+    int odd = 0;
+    RingAt at{0, 0};
+    bool aborted = false;
     uint32_t e_next[NV];
     float rstd_next = 0.f, mean_next = 0.f;
     auto fetch = [&](uint32_t row) {
@@ -747,12 +750,12 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
 #pragma unroll
         for (int i = 0; i < NV; ++i) e[i] = CKPT ? e_next[i] : 0u;
         if (r + gridDim.x < rows) fetch(r + gridDim.x);
-        ring_wait(&full[stage], phase, &abort_flag, p.wait_limit_ns);
-        const uint8_t* at = ring + stage * p.stage_bytes;
-        const T* dy_row = reinterpret_cast<const T*>(at + (AL ? 0 : Pieces::lead(dy0 + r * a.ld_dy)));
+        ring_wait(&full[at.stage], at.phase, &abort_flag[odd], p.wait_limit_ns);
+        const uint8_t* here = ring + at.stage * p.stage_bytes;
+        const T* dy_row = reinterpret_cast<const T*>(here + (AL ? 0 : Pieces::lead(dy0 + r * a.ld_dy)));
         const T* x_row = reinterpret_cast<const T*>(
-            at + p.x_off + (AL || CKPT ? 0 : Pieces::lead(x0 + r * a.ld_x)));
-        const int8_t* q_row = reinterpret_cast<const int8_t*>(at + p.x_off);
+            here + p.x_off + (AL || CKPT ? 0 : Pieces::lead(x0 + r * a.ld_x)));
+        const int8_t* q_row = reinterpret_cast<const int8_t*>(here + p.x_off);
         auto vec = [&](int i, GradVec<T, AL, CKPT>& v) {
             const int c = c0 + i * step;
             Vec<T, AL> dyv, xv;
@@ -772,8 +775,10 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
             if constexpr (KEEP) kept = v;
         }
         const float2 t = block_sum2(s0.x + s0.y, s1.x + s1.y, red[odd]);
-        // its barrier says that every thread has read the stage
-        if (KEEP && threadIdx.x == 0) load(r + stages * gridDim.x, stage);
+        // its barrier says that every thread has read the stage; a wait that
+        // raises this flag again is two barriers on
+        if ((aborted = abort_flag[odd])) break;
+        if (KEEP && threadIdx.x == 0) load(r + stages * gridDim.x, at.stage);
         const float n0 = -t.x * inv_n * rstd, n1 = -t.y * inv_n * rstd;
         T* const dx = static_cast<T*>(a.dx) + r * a.ld_dx + c0;
 #pragma unroll
@@ -794,12 +799,9 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
         }
         if (!KEEP) {
             __syncthreads();
-            if (threadIdx.x == 0) load(r + stages * gridDim.x, stage);
+            if (threadIdx.x == 0) load(r + stages * gridDim.x, at.stage);
         }
-        if (++stage == stages) {
-            stage = 0;
-            phase ^= 1;
-        }
+        at = ring_ahead(at, stages, 1);
     }
     if (p.part) {
         float* w = p.part + int64_t(blockIdx.x) * 2 * p.ld_part;
@@ -814,8 +816,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
                     make_float4(db[u].x, db[u].y, db[u + 1].x, db[u + 1].y);
             }
     }
-    __syncthreads();
-    if (abort_flag && threadIdx.x == 0) ring_drain(full, stages, a.rows, p.wait_limit_ns);
+    if (aborted && threadIdx.x == 0) ring_drain(full, at, stages, rows, r, p.wait_limit_ns);
 }
 
 // The partial sums of 32 columns in a block, 32 of them at a time (304 of 7168
@@ -991,7 +992,23 @@ cudaError_t norm_backward(GradLaunch& p, cudaStream_t s) {
     return e;
 }
 
+// A wait that nothing satisfies, as the rings wait.
+__global__ void __launch_bounds__(32) ring_timeout_kernel(unsigned long long limit_ns) {
+    __shared__ uint64_t bar;
+    __shared__ volatile int abort_flag;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(ptx::smem_u32(&bar), 1);
+        abort_flag = 0;
+    }
+    __syncthreads();
+    ring_wait(&bar, 0, &abort_flag, limit_ns);
+}
+
 }  // namespace
+
+cudaError_t launch_ring_timeout(unsigned long long limit_ns, cudaStream_t s) {
+    return launch_kernel(ring_timeout_kernel, dim3(1), dim3(32), 0, s, limit_ns);
+}
 
 cudaError_t norm_error_word(void** word) { return cudaGetSymbolAddress(word, g_norm_err); }
 

@@ -30,6 +30,8 @@ cudaError_t launch_route_grad(const muon_route_grad_args& a, cudaStream_t s);
 cudaError_t ops_status(cudaStream_t s, int* code);
 // Device address of the layer norm's error word.
 cudaError_t norm_error_word(void** word);
+// A kernel whose wait nothing satisfies: it runs out after the limit.
+cudaError_t launch_ring_timeout(unsigned long long limit_ns, cudaStream_t s);
 // Limit of the kernels' waits (MUON_WAIT_LIMIT_MS, else two seconds).
 unsigned long long wait_limit_ns();
 

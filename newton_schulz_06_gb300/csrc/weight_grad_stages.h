@@ -5,10 +5,12 @@
 
 #include <cstdint>
 
+#ifndef MUON_HD
 #ifdef __CUDACC__
 #define MUON_HD __host__ __device__ __forceinline__
 #else
 #define MUON_HD inline
+#endif
 #endif
 
 namespace muon {
