@@ -12,6 +12,8 @@
 // and dbias collect in registers: a thread has the same columns in every row.
 // Each block leaves one row of partial sums, which a second kernel adds up in
 // order.
+#include <atomic>
+
 #include "norm_ring.h"
 #include "ops_internal.h"
 #include "tc_wait.cuh"
@@ -421,17 +423,23 @@ int most_lanes(int64_t rows) {
     return !AL || rows < 64 * SMS ? 128 : sizeof(T) == 4 ? 512 : 256;
 }
 
-// Lets a kernel have `bytes` of dynamic shared memory.
+// The most dynamic shared memory that the ring kernels ask for, of all blocks
+// of an SM together.
+constexpr int64_t RING_SMEM = 224 * 1024;
+
+// Lets a kernel have its dynamic shared memory.  What is set is the same for
+// every size, so that calls from several threads cannot leave less than one
+// of them needs.
 template <auto KERN>
 cudaError_t allow_smem(size_t bytes) {
     if (bytes <= 40 * 1024) return cudaSuccess;   // with the static arrays, below the default
-    static int set[64] = {0};          // the most asked for so far, by device
+    static std::atomic<bool> done[64];           // by device
     int dev = 0;
     cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 64 && set[dev] >= static_cast<int>(bytes)) return cudaSuccess;
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
     const cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(bytes));
-    if (e == cudaSuccess && dev >= 0 && dev < 64) set[dev] = static_cast<int>(bytes);
+                                               static_cast<int>(RING_SMEM));
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
     return e;
 }
 
@@ -453,7 +461,7 @@ cudaError_t norm_forward_ring(NormLaunch& p, cudaStream_t s, bool* done) {
     if (per_sm > 8) per_sm = 8;
     if (p.a.rows < 2 * SMS * per_sm) return cudaSuccess;
     p.stage_bytes = static_cast<uint32_t>(ceil_div(p.a.cols * int64_t(sizeof(T)) + 14, 16) * 16);
-    int64_t stages = (224 * 1024 / per_sm - 2048) / p.stage_bytes;
+    int64_t stages = (RING_SMEM / per_sm - 2048) / p.stage_bytes;
     p.stages = static_cast<int32_t>(stages > RING_MAX ? RING_MAX : stages);
     if (p.stages < 2) return cudaSuccess;
     p.wait_limit_ns = wait_limit_ns();
@@ -922,7 +930,7 @@ GradPlan grad_plan(const muon_layer_norm_grad_args& a) {
         // blocks an SM: about 1024 threads, of the 64 registers that leaves
         int64_t per_sm = g.shape.nv < 4 ? 1024 / g.shape.threads : 1;
         if (per_sm > 8) per_sm = 8;
-        int64_t stages = (224 * 1024 / per_sm - 2048 - w_bytes) / row;
+        int64_t stages = (RING_SMEM / per_sm - 2048 - w_bytes) / row;
         if (stages > RING_MAX) stages = RING_MAX;
         if (g.shape.threads <= most && stages >= 1) {
             g.stages = static_cast<int>(stages);
