@@ -1,8 +1,9 @@
 """ctypes binding of libmuon's C ABI (include/muon.h): marshalling only.
 
 Every function here forwards to the library with the same name; there is no
-computation and no fallback.  If libmuon.so has not been built the first use
-raises, so a missing extension can never turn into a silent CPU path.
+computation and no fallback.  What is loaded is libmuon_torch.so: libmuon.so's
+code on the process's CUDA runtime (build.py).  If it has not been built the
+first use raises, so a missing extension can never turn into a silent CPU path.
 """
 from __future__ import annotations
 
@@ -11,7 +12,7 @@ import os
 import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
-LIB_PATH = os.path.join(PKG, "libmuon.so")
+LIB_PATH = os.path.join(PKG, "libmuon_torch.so")
 
 MUON_OK = 0
 MUON_ERR_INVALID_ARG = -1
@@ -123,7 +124,7 @@ _lib = None
 
 
 def lib() -> ctypes.CDLL:
-    """The loaded libmuon.so (raises if it has not been built)."""
+    """The loaded libmuon_torch.so (raises if it has not been built)."""
     global _lib
     if _lib is not None:
         return _lib
