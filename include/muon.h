@@ -461,7 +461,9 @@ MUON_API int muon_layer_norm_grad(const muon_layer_norm_grad_args* args, void* w
  * ones and zeros; g: n x k of g_dtype; c (optional): n x k of g_dtype, may
  * be g itself (gradient accumulation).  The products run on the tensor cores
  * from exact bf16 operands with fp32 sums; weight and bias are applied to
- * the sums.
+ * the sums.  The tensor cores cut their running sums off at the last place
+ * (sums of one sign lose 9e-7 in 1024 tokens and 4e-5 in 16384): fp32 results
+ * add them up to nearest every 1024 tokens, bf16 ones every 16384.
  * offsets (optional): experts + 1 int32 values in device memory, rising from
  * 0 to at most rows: matrix e takes rows offsets[e] .. offsets[e + 1] of dy
  * and saved (none: G = 0, or C), and g and c are `experts` matrices, stride_g

@@ -73,12 +73,16 @@ struct Shape {
 };
 constexpr int COLSUM_PARTS = 32;      // of one matrix's tokens (experts: one part each)
 constexpr int BAND = 8;
-// fp32 results: the tensor cores cut a running sum off at its last place, so
-// that it shrinks by about 7e-9 of itself a product of 16 tokens (measured);
-// after this many steps it is added to a sum that is rounded to nearest (4096
-// tokens of 7168 x 8192: 377 us, 363 with one sum, whose error is 1.8e-6
-// instead of 4e-7).
-constexpr int CHUNK_STEPS = 16;
+// The tensor cores cut a running sum off at its last place, twice a product of
+// 16 tokens, so that it shrinks: sums of one sign by 9e-7 of themselves after 64
+// products and by 4e-5 after 1024, sums of both signs by 1.7e-7 after 64
+// (measured).  After this many steps of four products a sum is added to one
+// that is rounded to nearest.  fp32 results: 16 (4096 tokens of 7168 x 8192: 380
+// us, 363 with one sum, whose error is 1.8e-6 instead of 4e-7).  bf16 results,
+// whose rounding is 2e-3: 256, or 16384 tokens, so that what is lost stays at a
+// fiftieth of that however many there are (65536 tokens of 7168 x 8192: 4257
+// us, and 3986 with one sum, which loses 1e-3 of 200000 tokens).
+constexpr int CHUNK_F32 = 16, CHUNK_BF16 = 256;
 
 __device__ int g_ops_err;
 
@@ -87,13 +91,14 @@ struct WgLaunch {
     CUtensorMap tm_q;        // q: dims {k, rows}, box {64, 64}, 64-byte swizzle
     int32_t vec;             // G's and C's rows lie on 16 bytes
     int32_t sorted;          // experts are taken by their size
-    int32_t chunk;           // steps that one accumulator sums (0: all of a tile's)
+    int32_t chunk;           // steps that one accumulator sums
     muon_weight_grad_args a;
     const float* colsum;     // parts x experts x n sums of dY's columns (bias), or null
     int32_t colsum_parts;
     float* part;             // splits > 1: splits x experts x n x ld_part partial sums
     int64_t ld_part;
     int32_t splits;
+    float4* held;            // WIDE: a tile's sums while its next chunk runs
     int32_t tiles_n, tiles_k;
     int32_t items;
     unsigned long long wait_limit_ns;
@@ -209,6 +214,29 @@ __device__ __forceinline__ void tmem_add16(uint32_t to, uint32_t from) {
         "r"(a[9]), "r"(a[10]), "r"(a[11]), "r"(a[12]), "r"(a[13]), "r"(a[14]), "r"(a[15])
         : "memory");
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Sums of 16 columns that wait in memory (this lane's pieces lie 32 apart):
+// added to raw, and those of an accumulator added to them (first: put there).
+__device__ __forceinline__ void add_held(const float4* held, uint32_t (&raw)[16]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float4 f = held[32 * q];
+        raw[4 * q] = __float_as_uint(__uint_as_float(raw[4 * q]) + f.x);
+        raw[4 * q + 1] = __float_as_uint(__uint_as_float(raw[4 * q + 1]) + f.y);
+        raw[4 * q + 2] = __float_as_uint(__uint_as_float(raw[4 * q + 2]) + f.z);
+        raw[4 * q + 3] = __float_as_uint(__uint_as_float(raw[4 * q + 3]) + f.w);
+    }
+}
+__device__ __forceinline__ void hold16(float4* held, uint32_t from, bool more) {
+    uint32_t raw[16];
+    tmem_ld16(from, raw);
+    tmem_ld_wait();
+    if (more) add_held(held, raw);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        held[32 * q] = make_float4(__uint_as_float(raw[4 * q]), __uint_as_float(raw[4 * q + 1]),
+                                   __uint_as_float(raw[4 * q + 2]), __uint_as_float(raw[4 * q + 3]));
 }
 
 // The decoding of a block's values.  With b = q + 128 as the last byte of a
@@ -574,14 +602,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             for (int32_t it = pair; ok && it < p.items; it += npairs) {
                 const Item x = item_at<WIDE>(p, order, it);
                 if (x.steps == 0) continue;
-                const int chunk = !WIDE && p.chunk ? p.chunk : x.steps;
-                for (int s0 = 0; ok && s0 < x.steps; s0 += chunk) {
+                for (int s0 = 0; ok && s0 < x.steps; s0 += p.chunk) {
                     const uint32_t acc = WIDE ? 0u : s0 ? first ^ 1 : first;
                     if (!take(acc)) {
                         ok = false;
                         break;
                     }
-                    const int s1 = min(s0 + chunk, x.steps);
+                    const int s1 = min(s0 + p.chunk, x.steps);
                     for (int s = s0; s < s1; ++s, ++step) {
                         if (!wait_soon(smem_u32(&ready_bar[stage_of(step, S::B_STAGES)]),
                                        parity_of(step, S::B_STAGES), abort_flag, &g_ops_err, limit)) {
@@ -592,11 +619,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                         products(acc, 0, s == s0);
                         any = true;
                         if (WIDE) {
-                            if (s == 0 && !take(1)) {
+                            if (s == s0 && !take(1)) {
                                 ok = false;
                                 break;
                             }
-                            products(1, 1, s == 0);
+                            products(1, 1, s == s0);
                         }
                         commit_pair_multicast(smem_u32(&done_bar[stage_of(step, S::A_STAGES)]));
                     }
@@ -752,6 +779,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         const int c_first = (warp - 2) / 4 * 4;     // and four of its 32-column blocks
         uint4* const blk = reinterpret_cast<uint4*>(smem + S::EPI_OFF + (warp - 2) * W_EPI_BYTES);
         const uint32_t tempty_leader = map_to_rank(smem_u32(tempty_bar), 0);
+        // WIDE: this lane's places, 16 columns in four pieces 32 apart
+        float4* const held = p.held + ((int64_t(blockIdx.x) * W_EPI_WARPS + warp - 2) * 16) * 128 + lane;
         uint32_t uses[2] = {0, 0};
         uint32_t first = 0;
         bool ok = true;
@@ -791,12 +820,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                 }
                 // later chunks of the tokens: added up in fp32, rounded to
                 // nearest
-                const int chunk = !WIDE && p.chunk ? p.chunk : x.steps;
-                for (int s0 = chunk; s0 < x.steps; s0 += chunk) {
-                    if (!wait_full(first ^ 1)) {
+                for (int s0 = p.chunk; s0 < x.steps; s0 += p.chunk) {
+                    if constexpr (WIDE) {
+                        // both accumulators are in use: the sums so far wait
+                        // in memory (L2 holds all pairs')
+#pragma unroll 1
+                        for (int c = 0; c < 16; ++c) {
+                            hold16(held + c * 128, tlane + c / 8 * 256 + 32 * c_first + 16 * (c & 7),
+                                   s0 > p.chunk);
+                            if (c == 7) release(0);
+                        }
+                        release(1);
+                    }
+                    if (!wait_full(WIDE ? 0 : first ^ 1)) {
                         ok = false;
                         break;
                     }
+                    if constexpr (WIDE) continue;
 #pragma unroll 1
                     for (int c = 2 * c_first; c < 2 * (c_first + 4); ++c)
                         tmem_add16(tlane + first * 256 + 16 * c, tlane + (first ^ 1) * 256 + 16 * c);
@@ -840,6 +880,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                         if (x.steps) {
                             tmem_ld16(taddr + 32 * c_first + 16 * c, raw);
                             tmem_ld_wait();
+                            if (WIDE && x.steps > p.chunk) add_held(held + (8 * h + c) * 128, raw);
                         } else {
 #pragma unroll
                             for (int u = 0; u < 16; ++u) raw[u] = 0;
@@ -1051,8 +1092,9 @@ int grid_for(int64_t items) {
 }
 
 struct Layout {
-    size_t colsum = 0, dy = 0, part = 0, bytes = 0;
+    size_t colsum = 0, dy = 0, part = 0, held = 0, bytes = 0;
     int colsum_parts = 0, splits = 1;
+    bool wide = false;
     int64_t ld_dy = 0, ld_part = 0;
 };
 Layout layout(const muon_weight_grad_args& a) {
@@ -1072,6 +1114,12 @@ Layout layout(const muon_weight_grad_args& a) {
         l.part = l.bytes;
         l.ld_part = ceil_div(a.k, 8) * 8;
         l.bytes += align256(size_t(l.splits) * a.experts * a.n * l.ld_part * 4);
+    }
+    l.wide = is_wide(a, l.splits);
+    if (l.wide && ceil_div(a.rows, W_TOK) > CHUNK_BF16) {
+        // a tile may have more than one chunk
+        l.held = l.bytes;
+        l.bytes += size_t(W_PAIRS) * 512 * 256 * 4;
     }
     return l;
 }
@@ -1127,13 +1175,14 @@ cudaError_t launch_weight_grad(const muon_weight_grad_args& a, void* ws, cudaStr
     WgLaunch p = {};
     p.a = a;
     p.splits = l.splits;
-    const bool wide = is_wide(a, l.splits);
+    const bool wide = l.wide;
     p.tiles_n = static_cast<int32_t>(ceil_div(a.n, wide ? 512 : 256));
     p.tiles_k = static_cast<int32_t>(ceil_div(a.k, 256));
     p.items = static_cast<int32_t>(a.experts * p.tiles_n * p.tiles_k * l.splits);
     p.wait_limit_ns = wait_limit_ns();
     const int64_t size = a.g_dtype == MUON_F32 ? 4 : 2;
-    if (a.g_dtype == MUON_F32) p.chunk = CHUNK_STEPS;
+    p.chunk = a.g_dtype == MUON_F32 ? CHUNK_F32 : CHUNK_BF16;
+    p.held = reinterpret_cast<float4*>(base + l.held);
     p.sorted = a.experts > 1 && a.experts <= W_ORDER;
     if (l.splits > 1) {
         p.part = reinterpret_cast<float*>(base + l.part);
