@@ -457,8 +457,8 @@ MUON_API int muon_layer_norm_grad(const muon_layer_norm_grad_args* args, void* w
 /* The gradient of a matrix W (n x k) of a product Y = X W^T, from the
  * checkpoint of X (or of the h that a norm made X from):
  *     G[i][j] = sum over t of dy[t][i] * (h[t][j] * weight[j] + bias[j])  (+ C[i][j])
- * dy: rows x n, bf16; saved: rows x k; weight, bias: k fp32 values, NULL for
- * ones and zeros; g: n x k of g_dtype; c (optional): n x k of g_dtype, may
+ * dy: rows x n, bf16; saved: rows x k; weight, bias: k values of w_dtype, NULL
+ * for ones and zeros; g: n x k of g_dtype; c (optional): n x k of g_dtype, may
  * be g itself (gradient accumulation).  The products run on the tensor cores
  * from exact bf16 operands with fp32 sums; weight and bias are applied to
  * the sums.  The tensor cores cut their running sums off at the last place
@@ -472,15 +472,15 @@ MUON_API int muon_layer_norm_grad(const muon_layer_norm_grad_args* args, void* w
  * 1048576, 1 <= experts <= 65536. */
 typedef struct {
     const void*    dy;
-    const float*   weight;
-    const float*   bias;
+    const void*    weight;
+    const void*    bias;
     const void*    c;
     void*          g;
     const int32_t* offsets;
     muon_ckpt8     saved;
     int64_t        rows, n, k, experts;
     int64_t        ld_dy, ld_c, ld_g, stride_c, stride_g;
-    int32_t        g_dtype;
+    int32_t        g_dtype, w_dtype;
 } muon_weight_grad_args;
 MUON_API int muon_weight_grad_workspace(const muon_weight_grad_args* args, size_t* bytes);
 MUON_API int muon_weight_grad(const muon_weight_grad_args* args, void* workspace, size_t bytes,

@@ -80,7 +80,7 @@ LayerNormGradArgs = _struct("LayerNormGradArgs",
                             (_i64, "rows cols ld_dy ld_x ld_dx"), (_i32, "x_dtype w_dtype"))
 WeightGradArgs = _struct("WeightGradArgs", (_vp, "dy weight bias c g offsets"), (Ckpt8, "saved"),
                          (_i64, "rows n k experts ld_dy ld_c ld_g stride_c stride_g"),
-                         (_i32, "g_dtype"))
+                         (_i32, "g_dtype w_dtype"))
 RouteArgs = _struct("RouteArgs",
                     (_vp, "logits mask indices weights counts offsets loss kept"),
                     (_i64, "tokens experts k ld_z"), (_i32, "z_dtype renormalise"),

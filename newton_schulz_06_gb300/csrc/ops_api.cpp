@@ -107,7 +107,7 @@ int check_weight_grad(const Err& err, const muon_weight_grad_args* a) {
     if (!a) return err.bad("args is NULL");
     RETURN_IF(check_shape(err, a->rows, a->n));
     RETURN_IF(check_shape(err, a->rows, a->k));
-    if (!dtype_ok(a->g_dtype)) return err.bad("unknown element type");
+    if (!dtype_ok(a->g_dtype) || !dtype_ok(a->w_dtype)) return err.bad("unknown element type");
     if (a->experts < 1 || a->experts > 65536) return err.bad("experts out of range");
     if (!a->offsets && a->experts != 1) return err.bad("experts without offsets");
     if (a->experts * ops::ceil_div(a->n, 256) * ops::ceil_div(a->k, 256) > (int64_t(1) << 30))
@@ -222,8 +222,8 @@ MUON_API int muon_weight_grad(const muon_weight_grad_args* a, void* ws, size_t b
     RETURN_IF(check_weight_grad(err, a));
     RETURN_IF(check_tensor(err, "dy", a->dy, MUON_BF16, a->rows, a->n, a->ld_dy, true));
     RETURN_IF(check_ckpt(err, a->saved, a->rows, a->k));
-    RETURN_IF(check_vector(err, "weight", a->weight, MUON_F32));
-    RETURN_IF(check_vector(err, "bias", a->bias, MUON_F32));
+    RETURN_IF(check_vector(err, "weight", a->weight, a->w_dtype));
+    RETURN_IF(check_vector(err, "bias", a->bias, a->w_dtype));
     RETURN_IF(check_vector(err, "offsets", a->offsets, MUON_F32));
     RETURN_IF(check_tensor(err, "g", a->g, a->g_dtype, a->n, a->k, a->ld_g, false));
     if (a->experts > 1) {

@@ -93,6 +93,7 @@ struct WgLaunch {
     int32_t sorted;          // experts are taken by their size
     int32_t chunk;           // steps that one accumulator sums
     muon_weight_grad_args a;
+    const float *weight, *bias;    // a's, or their fp32 copies
     const float* colsum;     // parts x experts x n sums of dY's columns (bias), or null
     int32_t colsum_parts;
     float* part;             // splits > 1: splits x experts x n x ld_part partial sums
@@ -859,7 +860,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                                          : ((int64_t(x.split) * p.a.experts + x.e) * n + r0) * ld;
                 const int64_t c0 = x.e * p.a.stride_c + r0 * p.a.ld_c;
                 void* const g = apply ? p.a.g : p.part;
-                const bool affine = apply && (p.a.weight || p.a.bias);
+                const bool affine = apply && (p.weight || p.bias);
                 const void* const add = apply ? p.a.c : nullptr;
                 constexpr int size = F32 ? 4 : 2;
                 if (rows > 0) {
@@ -885,8 +886,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
 #pragma unroll
                             for (int u = 0; u < 16; ++u) raw[u] = 0;
                         }
-                        const float* const weight = affine && p.a.weight ? p.a.weight + j0 : nullptr;
-                        const float* const bias = affine && p.a.bias ? p.a.bias + j0 : nullptr;
+                        const float* const weight = affine && p.weight ? p.weight + j0 : nullptr;
+                        const float* const bias = affine && p.bias ? p.bias + j0 : nullptr;
                         if (F32 && whole) {
                             __syncwarp();      // the last rows have been read
 #pragma unroll
@@ -970,8 +971,8 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
     float w[4], b[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-        w[u] = p.a.weight && j + u < k ? p.a.weight[j + u] : 1.f;
-        b[u] = p.a.bias && j + u < k ? p.a.bias[j + u] : 0.f;
+        w[u] = p.weight && j + u < k ? p.weight[j + u] : 1.f;
+        b[u] = p.bias && j + u < k ? p.bias[j + u] : 0.f;
     }
     for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
         const int64_t e = p.a.experts == 1 ? 0 : row / p.a.n, i = row - e * p.a.n;
@@ -1036,6 +1037,17 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// The norm's weight and bias, where they are bf16, as the write-out reads them.
+__global__ void __launch_bounds__(256)
+    widen_kernel(const __nv_bfloat16* weight, const __nv_bfloat16* bias, int k, float* w, float* b) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int j = blockIdx.x * 256 + threadIdx.x;
+    if (j >= k) return;
+    if (weight) w[j] = __bfloat162float(weight[j]);
+    if (bias) b[j] = __bfloat162float(bias[j]);
+}
+
 // dY with rows that TMA can read: dense rows of ld elements (a multiple of 8).
 __global__ void __launch_bounds__(256)
     align_kernel(const __nv_bfloat16* src, int64_t rows, int64_t n, int64_t ld_src,
@@ -1092,7 +1104,7 @@ int grid_for(int64_t items) {
 }
 
 struct Layout {
-    size_t colsum = 0, dy = 0, part = 0, held = 0, bytes = 0;
+    size_t colsum = 0, dy = 0, part = 0, held = 0, weight = 0, bias = 0, bytes = 0;
     int colsum_parts = 0, splits = 1;
     bool wide = false;
     int64_t ld_dy = 0, ld_part = 0;
@@ -1114,6 +1126,13 @@ Layout layout(const muon_weight_grad_args& a) {
         l.part = l.bytes;
         l.ld_part = ceil_div(a.k, 8) * 8;
         l.bytes += align256(size_t(l.splits) * a.experts * a.n * l.ld_part * 4);
+    }
+    if (a.w_dtype == MUON_BF16) {
+        const size_t each = align256(size_t(a.k) * 4);
+        l.weight = l.bytes;
+        if (a.weight) l.bytes += each;
+        l.bias = l.bytes;
+        if (a.bias) l.bytes += each;
     }
     l.wide = is_wide(a, l.splits);
     if (l.wide && ceil_div(a.rows, W_TOK) > CHUNK_BF16) {
@@ -1196,6 +1215,19 @@ cudaError_t launch_weight_grad(const muon_weight_grad_args& a, void* ws, cudaStr
         p.vec = on(16);
     }
     cudaError_t e;
+    if (a.w_dtype == MUON_BF16 && (a.weight || a.bias)) {
+        auto* w = reinterpret_cast<float*>(base + l.weight);
+        auto* b = reinterpret_cast<float*>(base + l.bias);
+        e = launch_kernel(widen_kernel, dim3(static_cast<unsigned>(ceil_div(a.k, 256))), dim3(256), 0, s,
+                          static_cast<const __nv_bfloat16*>(a.weight),
+                          static_cast<const __nv_bfloat16*>(a.bias), static_cast<int>(a.k), w, b);
+        if (e != cudaSuccess) return e;
+        p.weight = a.weight ? w : nullptr;
+        p.bias = a.bias ? b : nullptr;
+    } else {
+        p.weight = static_cast<const float*>(a.weight);
+        p.bias = static_cast<const float*>(a.bias);
+    }
     if (a.bias) {
         p.colsum = reinterpret_cast<float*>(base + l.colsum);
         p.colsum_parts = l.colsum_parts;

@@ -324,7 +324,8 @@ def weight_grad(dy: torch.Tensor, x: Checkpoint8, *, weight: Optional[torch.Tens
     """The gradient of W (n x k) of a product Y = X W^T: dY^T X (+ add).
 
     dy: tokens x n, bf16.  x: the checkpoint of X, or of the h of the norm
-    that X came from, with that norm's weight and bias (k fp32 values each).
+    that X came from, with that norm's weight and bias (k values each, fp32 or
+    bf16, of one type).
     offsets: experts + 1 int32 values on the device; the result is then
     experts x n x k, matrix e over the tokens offsets[e] .. offsets[e + 1].
     add may be out (gradient accumulation).  out (or a new tensor of dtype):
@@ -352,9 +353,9 @@ def weight_grad(dy: torch.Tensor, x: Checkpoint8, *, weight: Optional[torch.Tens
         _need(add.dtype == g.dtype, f"add and the result differ in type: {add.dtype}, {g.dtype}")
         add_at = add.data_ptr()
     _call_ws(index, "muon_weight_grad", "muon_weight_grad_workspace", _weight_grad_args(
-        dy.data_ptr(), _vector("weight", weight, index, k, _F32),
-        _vector("bias", bias, index, k, _F32), add_at, g.data_ptr(), offsets_at, *x._fields(),
-        rows, n, k, experts, ld_dy, ld_c, ld_g, stride_c, stride_g, _dtype("out", g)), dev)
+        dy.data_ptr(), _vector("weight", weight, index, k), _vector("bias", bias, index, k), add_at,
+        g.data_ptr(), offsets_at, *x._fields(), rows, n, k, experts, ld_dy, ld_c, ld_g, stride_c,
+        stride_g, _dtype("out", g), _w_dtype(weight, bias)), dev)
     return g
 
 
