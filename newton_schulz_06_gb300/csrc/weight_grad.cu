@@ -80,8 +80,8 @@ constexpr int BAND = 8;
 // that is rounded to nearest.  fp32 results: 16 (4096 tokens of 7168 x 8192: 380
 // us, 363 with one sum, whose error is 1.8e-6 instead of 4e-7).  bf16 results,
 // whose rounding is 2e-3: 256, or 16384 tokens, so that what is lost stays at a
-// fiftieth of that however many there are (65536 tokens of 7168 x 8192: 4257
-// us, and 3986 with one sum, which loses 1e-3 of 200000 tokens).
+// fiftieth of that however many there are (65536 tokens of 7168 x 8192: 4242
+// us, and 3980 with one sum, which loses 1e-3 of 200000 tokens).
 constexpr int CHUNK_F32 = 16, CHUNK_BF16 = 256;
 
 __device__ int g_ops_err;
@@ -200,14 +200,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
 __device__ __forceinline__ void tmem_ld_wait() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-// Those at `to` plus those at `from`, to `to`; complete on return.
-__device__ __forceinline__ void tmem_add16(uint32_t to, uint32_t from) {
-    uint32_t a[16], b[16];
-    tmem_ld16(to, a);
-    tmem_ld16(from, b);
-    tmem_ld_wait();
-#pragma unroll
-    for (int u = 0; u < 16; ++u) a[u] = __float_as_uint(__uint_as_float(a[u]) + __uint_as_float(b[u]));
+// The way back; complete on return.
+__device__ __forceinline__ void tmem_st16(uint32_t to, const uint32_t (&a)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
         "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(to),
@@ -216,28 +210,43 @@ __device__ __forceinline__ void tmem_add16(uint32_t to, uint32_t from) {
         : "memory");
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// Those at `to` plus those at `from`, to `to`.
+__device__ __forceinline__ void tmem_add16(uint32_t to, uint32_t from) {
+    uint32_t a[16], b[16];
+    tmem_ld16(to, a);
+    tmem_ld16(from, b);
+    tmem_ld_wait();
+#pragma unroll
+    for (int u = 0; u < 16; ++u) a[u] = __float_as_uint(__uint_as_float(a[u]) + __uint_as_float(b[u]));
+    tmem_st16(to, a);
+}
 
-// Sums of 16 columns that wait in memory (this lane's pieces lie 32 apart):
-// added to raw, and those of an accumulator added to them (first: put there).
-__device__ __forceinline__ void add_held(const float4* held, uint32_t (&raw)[16]) {
+// 16 columns of an accumulator, with the sums that wait in memory for them
+// (this lane's pieces lie 32 apart) added if `more`: to memory, or back.
+template <bool BACK>
+__device__ __forceinline__ void hold16(float4* held, uint32_t at, bool more) {
+    uint32_t raw[16];
+    tmem_ld16(at, raw);
+    tmem_ld_wait();
+    float4 f[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f[q] = more ? held[32 * q] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const float4 f = held[32 * q];
-        raw[4 * q] = __float_as_uint(__uint_as_float(raw[4 * q]) + f.x);
-        raw[4 * q + 1] = __float_as_uint(__uint_as_float(raw[4 * q + 1]) + f.y);
-        raw[4 * q + 2] = __float_as_uint(__uint_as_float(raw[4 * q + 2]) + f.z);
-        raw[4 * q + 3] = __float_as_uint(__uint_as_float(raw[4 * q + 3]) + f.w);
+        f[q].x += __uint_as_float(raw[4 * q]);
+        f[q].y += __uint_as_float(raw[4 * q + 1]);
+        f[q].z += __uint_as_float(raw[4 * q + 2]);
+        f[q].w += __uint_as_float(raw[4 * q + 3]);
+        if constexpr (BACK) {
+            raw[4 * q] = __float_as_uint(f[q].x);
+            raw[4 * q + 1] = __float_as_uint(f[q].y);
+            raw[4 * q + 2] = __float_as_uint(f[q].z);
+            raw[4 * q + 3] = __float_as_uint(f[q].w);
+        } else {
+            held[32 * q] = f[q];
+        }
     }
-}
-__device__ __forceinline__ void hold16(float4* held, uint32_t from, bool more) {
-    uint32_t raw[16];
-    tmem_ld16(from, raw);
-    tmem_ld_wait();
-    if (more) add_held(held, raw);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        held[32 * q] = make_float4(__uint_as_float(raw[4 * q]), __uint_as_float(raw[4 * q + 1]),
-                                   __uint_as_float(raw[4 * q + 2]), __uint_as_float(raw[4 * q + 3]));
+    if constexpr (BACK) tmem_st16(at, raw);
 }
 
 // The decoding of a block's values.  With b = q + 128 as the last byte of a
@@ -827,8 +836,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                         // in memory (L2 holds all pairs')
 #pragma unroll 1
                         for (int c = 0; c < 16; ++c) {
-                            hold16(held + c * 128, tlane + c / 8 * 256 + 32 * c_first + 16 * (c & 7),
-                                   s0 > p.chunk);
+                            hold16<false>(held + c * 128, tlane + c / 8 * 256 + 32 * c_first + 16 * (c & 7),
+                                          s0 > p.chunk);
                             if (c == 7) release(0);
                         }
                         release(1);
@@ -844,6 +853,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                     release(first ^ 1);
                 }
                 if (!ok) break;
+                if (WIDE && x.steps > p.chunk)
+#pragma unroll 1
+                    for (int c = 0; c < 16; ++c)
+                        hold16<true>(held + c * 128, tlane + c / 8 * 256 + 32 * c_first + 16 * (c & 7), true);
             }
 #pragma unroll 1
             for (int h = 0; h < S::HALVES; ++h) {
@@ -881,7 +894,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                         if (x.steps) {
                             tmem_ld16(taddr + 32 * c_first + 16 * c, raw);
                             tmem_ld_wait();
-                            if (WIDE && x.steps > p.chunk) add_held(held + (8 * h + c) * 128, raw);
                         } else {
 #pragma unroll
                             for (int u = 0; u < 16; ++u) raw[u] = 0;
