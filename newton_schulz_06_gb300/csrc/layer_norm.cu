@@ -532,20 +532,22 @@ struct GradLaunch {
 
 // One vector of a row: dy, h and g = dy * weight (the caller puts the weight
 // into g).  CKPT: h comes from q and
-// its scale byte e, else from x as x * rstd + shift (shift = -mean * rstd).
+// its scale byte e, else from x as the forward pass makes it, (x - mean) * rstd
+// (x * rstd - mean * rstd would save an instruction for two values, and loses
+// the digits that x and the mean share; minus = -mean).
 template <typename T, bool AL, bool CKPT>
 struct GradVec {
     static constexpr int VE = Vec<T, AL>::VE, F2 = VE / 2;
     float2 dy[F2], h[F2], g[F2];
     __device__ __forceinline__ void make(const Vec<T, AL>& dyv, const Vec<T, AL>& xv, const int8_t* q,
-                                         uint32_t e, float rstd, float shift) {
+                                         uint32_t e, float rstd, float minus) {
         dyv.get(dy);
         if constexpr (CKPT) {
             decode_vec<VE>(q, scale_pow(e), h);
         } else {
             xv.get(h);
 #pragma unroll
-            for (int j = 0; j < F2; ++j) h[j] = fma2(h[j], both(rstd), both(shift));
+            for (int j = 0; j < F2; ++j) h[j] = mul2(add2(h[j], both(minus)), both(rstd));
         }
         // g holds the weight's vector
 #pragma unroll
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(256, 4) norm_grad_kernel(const __grid_constant
     Vec<T, AL> dyv, xv;
     uint2 q8 = make_uint2(0u, 0u);
     uint32_t e = 0;
-    float rstd = 0.f, shift = 0.f;
+    float rstd = 0.f, minus = 0.f;
     auto fetch = [&](int64_t r) {
         const int valid = r < a.rows ? cols - c : 0;
         dyv.load(static_cast<const T*>(a.dy) + r * a.ld_dy + c, valid);
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(256, 4) norm_grad_kernel(const __grid_constant
         }
         if (r < a.rows) {
             rstd = a.rstd[r];
-            shift = CKPT ? 0.f : -a.mean[r] * rstd;
+            minus = CKPT ? 0.f : -a.mean[r];
         }
     };
     const int64_t stride = int64_t(gridDim.x) * ROWS;
@@ -621,7 +623,7 @@ __global__ void __launch_bounds__(256, 4) norm_grad_kernel(const __grid_constant
         float2 s0 = both(0.f), s1 = both(0.f);
         if (valid > 0) {
             load_row_vec<VE>(a.weight, a.w_dtype, p.w_vec, c, AL ? VE : valid, 1.f, v.g);
-            v.make(dyv, xv, reinterpret_cast<const int8_t*>(&q8), e, rstd, shift);
+            v.make(dyv, xv, reinterpret_cast<const int8_t*>(&q8), e, rstd, minus);
             v.add(dw, db, s0, s1);
         }
         fetch(r + stride);
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     uint32_t r = blockIdx.x;
     fetch(r);
     for (; r < rows; r += gridDim.x, odd ^= 1) {
-        const float rstd = rstd_next, shift = -mean_next * rstd_next;
+        const float rstd = rstd_next, minus = -mean_next;
         uint32_t e[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) e[i] = CKPT ? e_next[i] : 0u;
@@ -770,7 +772,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
             dyv.load_some(dy_row + c, cols - c);
             if constexpr (!CKPT) xv.load_some(x_row + c, cols - c);
             w_vec(threadIdx.x + i * blockDim.x, v.g);
-            v.make(dyv, xv, q_row + c, e[i], rstd, shift);
+            v.make(dyv, xv, q_row + c, e[i], rstd, minus);
         };
         GradVec<T, AL, CKPT> kept;
         float2 s0 = both(0.f), s1 = both(0.f);
