@@ -4,8 +4,8 @@
 // Forward.  A row is read once, in 16-byte vectors (at any alignment: see
 // Vec) that stay in registers, by 8 to 32 lanes of a warp or by a block.  The
 // variance is taken around the mean in a second sum over the registers (sums
-// of x^2 lose it when the mean is large), with the first sum's rounding
-// corrected by the sum of the deviations.  The checkpoint of h is written from
+// of x^2 lose it when the mean is large), which also corrects the rounding of a
+// large mean (settle).  The checkpoint of h is written from
 // the same registers.
 //
 // Backward.  Blocks stay for many rows, so that the column sums of dweight
@@ -70,6 +70,18 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* buf) {
         }
         return make_float2(a, b);
     }
+}
+
+// The variance of a row from the sums of d = x - mean and of d^2; the mean is
+// corrected by that of d where it helps.  That sum carries the rounding of every
+// d, about 2e-8 of the deviation, the first sum about 6e-8 of the mean: a mean
+// above the deviation gains two or three times its error, a smaller one would
+// lose (7168 columns of bf16 about 0: 6e-8 of itself became 1.5e-6).
+__device__ __forceinline__ float settle(float& mean, float2 sums, float inv_n) {
+    const float off = sums.x * inv_n;
+    const float var = fmaxf(fmaf(-off, off, sums.y * inv_n), 0.f) + (sums.y != sums.y ? sums.y : 0.f);
+    if (mean * mean > var) mean += off;
+    return var;
 }
 
 // ------------------------------------------------------------------ forward
@@ -177,10 +189,7 @@ __global__ void __launch_bounds__(L ? 256 : 1024, L ? lane_blocks<T>(NV) : 1)
         }
     }
     const float2 t = row_sum2<L>(d1.x + d1.y, d2.x + d2.y, red[1]);
-    const float off = t.x * inv_n;
-    const float var = fmaxf(fmaf(-off, off, t.y * inv_n), 0.f) + (t.y != t.y ? t.y : 0.f);
-    mean += off;
-    const float rstd = 1.f / sqrtf(var + a.eps);
+    const float rstd = 1.f / sqrtf(settle(mean, t, inv_n) + a.eps);
     if (c0 == 0 && cols) {
         if (a.mean) a.mean[r] = mean;
         if (a.rstd) a.rstd[r] = rstd;
@@ -308,10 +317,7 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
             }
         }
         const float2 t = block_sum2(d1.x + d1.y, d2.x + d2.y, red[1]);
-        const float off = t.x * inv_n;
-        const float var = fmaxf(fmaf(-off, off, t.y * inv_n), 0.f) + (t.y != t.y ? t.y : 0.f);
-        mean += off;
-        const float rstd = 1.f / sqrtf(var + a.eps);
+        const float rstd = 1.f / sqrtf(settle(mean, t, inv_n) + a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[r] = mean;
             if (a.rstd) a.rstd[r] = rstd;
@@ -368,10 +374,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
         d2 = fmaf(d, d, d2);
     }
     const float2 t = block_sum2(d1, d2, red[1]);
-    const float off = t.x * inv_n;
-    const float var = fmaxf(fmaf(-off, off, t.y * inv_n), 0.f) + (t.y != t.y ? t.y : 0.f);
-    mean += off;
-    const float rstd = 1.f / sqrtf(var + a.eps);
+    const float rstd = 1.f / sqrtf(settle(mean, t, inv_n) + a.eps);
     if (threadIdx.x == 0) {
         if (a.mean) a.mean[r] = mean;
         if (a.rstd) a.rstd[r] = rstd;
