@@ -873,7 +873,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                                          : ((int64_t(x.split) * p.a.experts + x.e) * n + r0) * ld;
                 const int64_t c0 = x.e * p.a.stride_c + r0 * p.a.ld_c;
                 void* const g = apply ? p.a.g : p.part;
-                const bool affine = apply && (p.weight || p.bias);
+                // a matrix without tokens is 0 whatever its weights are
+                const bool affine = apply && x.steps && (p.weight || p.bias);
                 const void* const add = apply ? p.a.c : nullptr;
                 constexpr int size = F32 ? 4 : 2;
                 if (rows > 0) {
@@ -999,9 +1000,12 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
             g[3] += f.w;
         }
         const float sum = p.colsum ? column_sum(p, e, i) : 0.f;
+        int64_t begin, end;
+        segment(p.a, e, &begin, &end);
+        const bool some = end > begin;           // else 0 whatever the weights are
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (j + u < k) finish(p.a, e, i, j + u, g[u], w[u], b[u], sum);
+            if (j + u < k) finish(p.a, e, i, j + u, g[u], some ? w[u] : 1.f, some ? b[u] : 0.f, sum);
     }
 }
 

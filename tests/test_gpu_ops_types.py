@@ -54,3 +54,26 @@ def test_weights_of_two_types_are_refused(ns):
         ns.weight_grad(dy, saved, weight=rand(11, 32), bias=rand(12, 32, dtype=F32))
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         ns.weight_grad(dy, saved, weight=rand(11, 32).half())
+
+
+@pytest.mark.parametrize("wdtype", [BF, F32])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("t,n,k", [(0, 40, 65), (300, 264, 520), (3000, 64, 64)])
+def test_a_matrix_without_tokens_is_zero_whatever_its_weights(ns, t, n, k, dtype, wdtype):
+    """An infinity or a NaN among the norm's weights shows where there are
+    tokens, and nowhere else; C passes through."""
+    dy = rand(13, t, n)
+    saved = ns.checkpoint8(rand(14, t, k)) if t else ns.Checkpoint8.empty(0, k, DEV)
+    w, b = rand(15, k, dtype=wdtype), rand(16, k, dtype=wdtype)
+    w[3], b[5] = float("inf"), float("nan")
+    offsets = torch.tensor([0, 0, t, t], dtype=torch.int32, device=DEV)
+    got = ns.weight_grad(dy, saved, weight=w, bias=b, offsets=offsets, dtype=dtype)
+    assert not got[[0, 2]].any()
+    if t:
+        assert torch.isnan(got[1, :, 5]).all() and not torch.isfinite(got[1, :, 3]).any()
+        assert torch.isfinite(got[1, :, 6:].float()).all()
+    c = rand(17, 3, n, k, dtype=dtype)
+    got = ns.weight_grad(dy, saved, weight=w, bias=b, offsets=offsets, add=c, dtype=dtype)
+    assert torch.equal(got[[0, 2]], c[[0, 2]])
+    if not t:
+        assert not ns.weight_grad(dy, saved, weight=w, bias=b, dtype=dtype).any()
