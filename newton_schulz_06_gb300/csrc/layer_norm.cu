@@ -226,11 +226,11 @@ __global__ void __launch_bounds__(L ? 256 : 1024, L ? lane_blocks<T>(NV) : 1)
 
 // Many longer rows: blocks that stay, with the weight and the bias of their
 // threads' columns in registers and a ring of rows in shared memory that bulk
-// copies fill ahead of them.  8192 x 7168 bf16: 55 us (4.2 TB/s), with the
-// checkpoint 70 us; 16384 x 4096 fp32 97 us (5.5 TB/s).  bf16 is bound by the
+// copies fill ahead of them.  8192 x 7168 bf16: 51 us (4.6 TB/s), with the
+// checkpoint 69 us; 16384 x 4096 fp32 92 us (5.8 TB/s), with it 110 us.  bf16 is bound by the
 // instructions of the two sums (59 % of the issue slots, and what waits for
 // their shuffles and barriers).  With one vector a thread instead of two, 8192
-// x 7168 takes 75 us; rows off 16 bytes take 97 us (8192 x 7167), for their
+// x 7168 takes 75 us; rows off 16 bytes take 95 us (8192 x 7167), for their
 // vectors are put together from two.
 template <typename T, bool AL, int NV, bool CKPT>
 __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
@@ -351,8 +351,10 @@ __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     if (aborted && threadIdx.x == 0) ring_drain(full, at, stages, a.rows, r, p.wait_limit_ns);
 }
 
-// Rows that do not fit a block's registers: three sweeps over the row, of
-// which L2 serves two (1024 x 65536 bf16: 85 us, 3.1 TB/s).
+// Rows that do not fit a block's registers (more than 65536 columns of bf16,
+// 32768 of fp32): three sweeps over the row, of which L2 serves two, element by
+// element (1024 x 70000 bf16: 269 us, 1.1 TB/s; 1024 x 40000 fp32 169 us; 1024 x
+// 65536 bf16 in registers 87 us).
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__ NormLaunch p) {
     __shared__ float2 red[2][32];
@@ -453,7 +455,7 @@ cudaError_t launch_norm_ring(int grid, int threads, size_t smem, const NormLaunc
 }
 
 // Rows for which blocks that stay pay: two a block and more (8192 x 7168 bf16
-// 55 us, 74 with a block a row; 16384 x 4096 fp32 97 and 109 us; 2048 x 7168
+// 51 us, 74 with a block a row; 16384 x 4096 fp32 92 and 109 us; 2048 x 7168
 // 17 and 18 us; below that both are bound by the launch).
 template <typename T, bool AL>
 cudaError_t norm_forward_ring(NormLaunch& p, cudaStream_t s, bool* done) {
@@ -672,11 +674,11 @@ __global__ void __launch_bounds__(256, 4) norm_grad_kernel(const __grid_constant
 // 16-byte pieces that hold a row, so that memory is kept busy whatever the
 // registers hold.  With more than one vector a thread, the second sweep takes
 // a row from the ring again instead of keeping it in registers.  8192 x 7168
-// bf16: 77 us (4.6 TB/s), from the checkpoint 79 us (3.7 TB/s); 16384 x 4096
-// fp32 135 us (5.9 TB/s).  bf16 is bound by instructions and their latency at
+// bf16: 80 us (4.4 TB/s), from the checkpoint 80 us (3.7 TB/s); 16384 x 4096
+// fp32 136 us (5.9 TB/s), from it 103 us.  bf16 is bound by instructions and their latency at
 // 64 registers a thread: 896 threads of one vector take 91 us, blocks of
 // several rows that share the weight 82, a bf16 weight in shared memory 89;
-// rows off 16 bytes 167 us (8192 x 7167).
+// rows off 16 bytes 169 us (8192 x 7167).
 template <typename T, bool AL, int NV, bool CKPT>
 __global__ void __launch_bounds__(ring_threads<T>(NV), ring_blocks(NV))
     norm_grad_ring_kernel(const __grid_constant__ GradLaunch p) {

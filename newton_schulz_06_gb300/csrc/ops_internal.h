@@ -88,8 +88,9 @@ __device__ __forceinline__ float2 bf16x2_f32(uint32_t w) {
 //
 // A row may start anywhere: a vector that does not lie on 16 bytes is put
 // together from the two aligned 16-byte pieces that hold it, so that odd
-// widths and odd addresses cost two loads instead of VE, and are added up in
-// the same order as aligned ones.  Every piece that is read holds at least
+// widths and odd addresses cost two loads instead of VE.  A kernel adds rows up
+// in the same order wherever they lie; which kernel takes them may go by the
+// alignment and the number of rows (norm_forward).  Every piece that is read holds at least
 // one byte of the row.
 
 // The 16 bytes that start m bytes into lo:hi (0 <= m < 16, a multiple of 2).

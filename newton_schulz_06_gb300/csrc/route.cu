@@ -15,9 +15,10 @@
 // What bounds the forward pass is the arithmetic of the selection and of the
 // exponentials: 32769 tokens of 384 experts, bf16, k = 8: 26 us, 71 % of the
 // integer pipe's rate, and 11 us for the second kernel; 262144 tokens 178 us
-// (fp32 253 us).  The gradient: 19 us, and 118 us (3.6 TB/s).  200 tokens of
+// (fp32 253 us).  The gradient: 19 us, and 114 us (3.7 TB/s).  200 tokens of
 // 128 experts take 5 us in each of the two kernels, a launch's latency.
 #include "ops_internal.h"
+#include "tc_ptx.cuh"
 
 namespace muon {
 namespace ops {
@@ -367,15 +368,9 @@ __global__ void __launch_bounds__(route_threads<V>())
     if (threadIdx.x == 0) reinterpret_cast<int*>(out)[2 * E] = s_kept;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // Stores a word to this variable of CTA `rank` of the cluster.
 __device__ __forceinline__ void store_to_rank(void* at, uint32_t rank, uint32_t v) {
-    uint32_t addr;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                 : "=r"(addr)
-                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(at))), "r"(rank));
+    const uint32_t addr = ptx::map_to_rank(ptx::smem_u32(at), rank);
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
@@ -409,7 +404,7 @@ __global__ void __cluster_dims__(JOIN_CTAS, 1, 1) __launch_bounds__(JOIN_THREADS
         }
     s_p[threadIdx.x] = p;
     s_n[threadIdx.x] = c;
-    cluster_sync();                              // every CTA runs: its memory can be written
+    ptx::cluster_sync_all();                              // every CTA runs: its memory can be written
     if (slice == 0 && e < E) {
         for (int s = 1; s < slices; ++s) {
             p += s_p[s * each + mine];
@@ -419,7 +414,7 @@ __global__ void __cluster_dims__(JOIN_CTAS, 1, 1) __launch_bounds__(JOIN_THREADS
         store_to_rank(&s_count[e], 0, c);
         store_to_rank(&s_term[e], 0, __float_as_uint(static_cast<float>(c) * p));
     }
-    cluster_sync();
+    ptx::cluster_sync_all();
     if (blockIdx.x != 0) return;
     // two experts a thread: offsets by scanning, the loss's sum, tokens kept
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -464,8 +459,8 @@ __global__ void __cluster_dims__(JOIN_CTAS, 1, 1) __launch_bounds__(JOIN_THREADS
 // (count times a factor, in registers), and for the taken experts also that
 // of their weights: a lane computes theirs again and stores them over the
 // others'.  Registers for four blocks an SM: 262144 tokens of 384 experts
-// bf16 118 us, fp32 162 us (5.1 TB/s), and 126 and 181 us with what the
-// compiler takes (79 registers).
+// bf16 114 us, fp32 163 us (5.1 TB/s); 126 and 181 us with what the compiler
+// takes (79 registers).
 template <typename T, int V, int L, bool AL>
 __global__ void __launch_bounds__(256, V <= 16 ? 4 : 2)
     route_grad_kernel(const __grid_constant__ muon_route_grad_args a) {
@@ -538,8 +533,8 @@ __global__ void __launch_bounds__(256, V <= 16 ? 4 : 2)
 // Rows of a block (of 512 or 256 threads) and how many blocks run.
 int route_v(int64_t experts) { return static_cast<int>(ceil_div(experts, 128) * 4); }
 // Eight lanes a token, four tokens a warp, where they hold the experts and the
-// taken ones (2^20 tokens of 8 experts, k = 2, bf16: 91 us, with a warp a token
-// 325; 32 experts, k = 4: 100 and 358 us; the gradient of 8 experts 58 and 237).
+// taken ones (2^20 tokens of 8 experts, k = 2, bf16: 94 us, with a warp a token
+// 325; 32 experts, k = 4: 100 and 358 us; the gradient of 8 experts 59 and 237).
 bool eight_lanes(int64_t experts, int64_t k) { return experts <= 32 && k <= 8; }
 int route_rows(int64_t experts, int64_t k) {
     return eight_lanes(experts, k) ? 64 : route_v(experts) <= 16 ? 16 : 8;

@@ -16,6 +16,12 @@ libmuon's kernels.  All calls queue their work on the current stream of their
 tensors' device and return; outputs that are not given are allocated.
 Tensors are CUDA tensors, row-major (stride(1) == 1), fp32 or bf16 as stated;
 include/muon.h has each operator's formula.
+
+Nothing here records for torch.autograd: an input's requires_grad has no
+effect, and the passes are joined by hand, as examples/train_moe_block.py does.
+The bits of a row of the layer norm may depend on the number of rows beside it
+and on its alignment (other kernels add in another order); the same call gives
+the same bits again.
 """
 from __future__ import annotations
 
