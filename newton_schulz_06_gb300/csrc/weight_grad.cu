@@ -21,7 +21,7 @@
 // same number.
 //
 // What bounds it is the tensor cores where the tiles are WIDE (16384 tokens,
-// 7168 x 8192, bf16: 1021 us, 1.88 PFLOP/s), and else the decoding warps: at
+// 7168 x 8192, bf16: 1040 us, 1.85 PFLOP/s), and else the decoding warps: at
 // 4096 tokens and 256 x 256 tiles 345 us, 310 without the products and 274
 // without the decoding.  Four warps a group and two groups beat 2 x 8 warps
 // and 4 x 4 (69, 90 and 95 us with 512 tokens of 7168 x 8192), and eight warps
@@ -1106,7 +1106,7 @@ int split_count(const muon_weight_grad_args& a) {
 // pair takes 3 a step + 34 for a wide tile and 2 a step + 10 for another
 // (measured with 7168 x 8192 from 300 to 4096 tokens; us, wide and not: 512
 // tokens 78 and 68, 1024 108 and 106, 2048 165 and 182, 4096 286 and 345,
-// 16384 1021 and 1452).  fp32 sums are added up in both accumulators.
+// 16384 1040 and 1452).  fp32 sums are added up in both accumulators.
 bool is_wide(const muon_weight_grad_args& a, int splits) {
     if (a.g_dtype != MUON_BF16 || splits > 1) return false;
     const int64_t steps = ceil_div(ceil_div(a.rows, a.experts), W_TOK);
