@@ -360,9 +360,10 @@ MUON_API int muon_step_noalloc(const muon_param* param, float lr, float beta,
 
 /* What a block of a model runs between its activations and the gradients
  * that muon_step reads: layer norm, activation checkpoints in 8 bits, the
- * weight gradient taken from a checkpoint, and the router of a
- * mixture-of-experts block with its balance loss.  These entry points need
- * no handle.  Conventions, beside those at the top of this file:
+ * weight gradient taken from a checkpoint, the router of a
+ * mixture-of-experts block with its balance loss, the gated feed-forward block
+ * (dense or per expert), rotary positions and dropout.  These entry points
+ * need no handle.  Conventions, beside those at the top of this file:
  *   - The work is queued on cuda_stream (NULL = the legacy default stream)
  *     of the caller's current device.  Every device pointer, the workspace's
  *     included, must stay valid until that work is done.
@@ -540,6 +541,163 @@ typedef struct {
 } muon_route_grad_args;
 MUON_API int muon_route_grad(const muon_route_grad_args* args, void* cuda_stream, char* err,
                              size_t err_len);
+
+/* A gated feed-forward block, dense or one per expert:
+ *     g = x w_gate^T,  u = x w_up^T,  h = act(g) * u,  y = h w_down^T.
+ * Both first products, act and their product are one kernel.  bf16 tensors:
+ * x, y: rows x hidden; w_gate, w_up: inner x hidden; w_down: hidden x inner;
+ * gate, up (both or neither, rows x inner, leading dimension ld_kept): receive
+ * g and u for the backward pass.  Sums are fp32 in the tensor cores; g, u, h
+ * and y are each rounded once, from fp32.
+ * act: MUON_ACT_SILU g / (1 + e^-g), MUON_ACT_GELU g Phi(g),
+ * MUON_ACT_GELU_TANH its approximation by tanh(sqrt(2/pi) (g + 0.044715 g^3)).
+ * offsets (optional): experts + 1 int32 values in device memory, rising from
+ * 0 to at most rows: expert e has rows offsets[e] .. offsets[e + 1] and the
+ * matrices e, stride_gate, stride_up and stride_down elements apart.  Values
+ * outside that rule are limited to it (one below another before it counts as
+ * that one); rows of no expert are not written.
+ * offsets = NULL: experts = 1, all rows.  y must not overlap x or a weight.
+ * A stride of matrices may be 0 (one for all).  0 <= rows < 2^31 - 256,
+ * 1 <= hidden, inner <= 262144, 1 <= experts <= 1024. */
+#define MUON_ACT_SILU 0
+#define MUON_ACT_GELU 1
+#define MUON_ACT_GELU_TANH 2
+typedef struct {
+    const void*    x;
+    const void*    w_gate;
+    const void*    w_up;
+    const void*    w_down;
+    void*          y;
+    void*          gate;
+    void*          up;
+    const int32_t* offsets;
+    int64_t        rows, hidden, inner, experts;
+    int64_t        ld_x, ld_gate, ld_up, ld_down, ld_y, ld_kept;
+    int64_t        stride_gate, stride_up, stride_down;
+    int32_t        activation;
+} muon_gated_ffn_args;
+MUON_API int muon_gated_ffn_workspace(const muon_gated_ffn_args* args, size_t* bytes);
+MUON_API int muon_gated_ffn(const muon_gated_ffn_args* args, void* workspace, size_t bytes,
+                            void* cuda_stream, char* err, size_t err_len);
+
+/* Its gradient.  From gate and up as the forward pass kept them:
+ *     dh = dy w_down,  dgate = dh * u * act'(g),  dup = dh * act(g),  h = act(g) * u
+ * (one kernel; rounded to bf16, as the next products read them),
+ *     dx = dgate w_gate + dup w_up   (one sum),
+ *     dw_gate = dgate^T x,  dw_up = dup^T x,  dw_down = dy^T h.
+ * dy, x, dx: rows x hidden; gate, up: rows x inner.  Every output may be NULL:
+ * dx; dw_gate and dw_up (then x may be, too); dw_down; dgate, dup and h (bf16,
+ * rows x inner, leading dimension ld_d), which muon_weight_grad takes with a
+ * checkpoint of x.  The weight gradients are g_dtype, dense matrices laid out
+ * as their weights (leading dimensions ld_dgate ..., strides stride_dgate ...);
+ * with accumulate they are added to what is there, in fp32, and rounded once.
+ * An expert without rows has zero gradients.  offsets as above. */
+typedef struct {
+    const void*    dy;
+    const void*    x;
+    const void*    gate;
+    const void*    up;
+    const void*    w_gate;
+    const void*    w_up;
+    const void*    w_down;
+    void*          dx;
+    void*          dw_gate;
+    void*          dw_up;
+    void*          dw_down;
+    void*          dgate;
+    void*          dup;
+    void*          h;
+    const int32_t* offsets;
+    int64_t        rows, hidden, inner, experts;
+    int64_t        ld_dy, ld_x, ld_kept, ld_gate, ld_up, ld_down, ld_dx, ld_d;
+    int64_t        ld_dw_gate, ld_dw_up, ld_dw_down;
+    int64_t        stride_gate, stride_up, stride_down;
+    int64_t        stride_dw_gate, stride_dw_up, stride_dw_down;
+    int32_t        activation, g_dtype, accumulate;
+} muon_gated_ffn_grad_args;
+MUON_API int muon_gated_ffn_grad_workspace(const muon_gated_ffn_grad_args* args, size_t* bytes);
+MUON_API int muon_gated_ffn_grad(const muon_gated_ffn_grad_args* args, void* workspace, size_t bytes,
+                                 void* cuda_stream, char* err, size_t err_len);
+
+/* Rotary positions of queries and keys.  Pair i of a head (values i and
+ * pairs + i with MUON_ROTARY_HALF, 2 i and 2 i + 1 with
+ * MUON_ROTARY_INTERLEAVED) turns by a = position * frequency[i]:
+ *     y1 = scale (x1 cos a - x2 sin a),  y2 = scale (x2 cos a + x1 sin a);
+ * with inverse by -a, which makes the gradient of x from that of y.  The
+ * values of a head past 2 * pairs are copied (they stay where y is x).
+ * q, k: tensors of batch x seq x heads x head values of x_dtype, each value
+ * 1 element and batches, positions and heads the given strides apart; a
+ * tensor of 0 heads is left out.  y may be x, with its strides.
+ * positions: batch rows (stride_positions apart, 0 for one row) of seq values, 32-
+ * or 64-bit (positions_64), in device memory; NULL: 0, 1, ... seq - 1.  offset
+ * is added to each.  turns: host memory, read during the call: every pair's
+ * frequency in turns per position times 2^64 (muon_rotary_frequencies), so
+ * that position * turns modulo 2^64 is the angle without whole turns: good to
+ * 2^-53 of itself, whole turns included, and to 2^-64 turns a position.
+ * 0 <= batch * seq < 2^31, 1 <= pairs <= 256, 2 * pairs <= head <= 65536, heads of
+ * both 1 .. 65536. */
+#define MUON_ROTARY_HALF 0
+#define MUON_ROTARY_INTERLEAVED 1
+typedef struct {
+    const void* x;
+    void*       y;
+    int64_t     heads;
+    int64_t     x_batch, x_seq, x_head;
+    int64_t     y_batch, y_seq, y_head;
+} muon_rotary_tensor;
+typedef struct {
+    muon_rotary_tensor q, k;
+    const void*     positions;
+    const uint64_t* turns;
+    int64_t         batch, seq, head, pairs;
+    int64_t         stride_positions, offset;
+    int32_t         x_dtype, layout, positions_64, inverse;
+    float           scale;
+} muon_rotary_args;
+MUON_API int muon_rotary(const muon_rotary_args* args, void* cuda_stream, char* err, size_t err_len);
+
+/* The frequencies of `pairs` pairs and the scale, for muon_rotary (host only).
+ * frequency[i] = base^(-i / pairs) radians a position, and
+ *   MUON_ROTARY_LINEAR: divided by factor;
+ *   MUON_ROTARY_NTK: base times factor^(pairs / (pairs - 1)) (pairs > 1);
+ *   MUON_ROTARY_YARN ("YaRN: Efficient Context Window Extension of Large
+ *     Language Models", Peng, Quesnelle, Fan and Shippole, 2023): divided by
+ *     factor for pairs that turn less than slow times in the `original`
+ *     positions, unchanged above fast times, a linear ramp over the pairs
+ *     between; scale = 0.1 ln(factor) + 1.
+ * base > 1, factor >= 1; for yarn original >= 1 and 0 < slow < fast. */
+#define MUON_ROTARY_PLAIN 0
+#define MUON_ROTARY_LINEAR 1
+#define MUON_ROTARY_NTK 2
+#define MUON_ROTARY_YARN 3
+MUON_API int muon_rotary_frequencies(int64_t pairs, double base, int scaling, double factor,
+                                     double original, double fast, double slow, uint64_t* turns,
+                                     float* scale, char* err, size_t err_len);
+
+/* Dropout:  y = keep * x / (1 - p)  (+ residual),  keep made again wherever it
+ * is needed: the backward pass is the same call on dy without the residual.
+ * Element i = row * cols + col is dropped where number i % 8 of block i / 8 is
+ * below round(65536 p), so that p is taken to the nearest 2^-16 and 1 / (1 - p)
+ * is that of this p.  Block b: Philox4x32-10 ("Parallel random numbers: as easy
+ * as 1, 2, 3", Salmon, Moraes, Dror and Shaw, 2011) of the counter words b, b >>
+ * 32, o, o >> 32 under the key words seed, seed >> 32, o = offset + *counter
+ * modulo 2^64; its four words are eight 16-bit numbers, low halves first.
+ * counter (optional): one value in device memory, read when the kernel runs,
+ * so that a captured graph drops others in every replay.  A dropped element
+ * is 0 whatever x holds.  x, residual, y: rows x cols of x_dtype; y may be x or
+ * the residual.  0 <= rows < 2^31, 1 <= cols <= 1048576, 0 <= p <= 1. */
+typedef struct {
+    const void*    x;
+    const void*    residual;
+    void*          y;
+    const int64_t* counter;
+    int64_t        rows, cols;
+    int64_t        ld_x, ld_r, ld_y;
+    uint64_t       seed, offset;
+    double         p;
+    int32_t        x_dtype;
+} muon_dropout_args;
+MUON_API int muon_dropout(const muon_dropout_args* args, void* cuda_stream, char* err, size_t err_len);
 
 /* Waits for the stream and reports what the operators above met on the GPU
  * of the caller's current device: MUON_ERR_TIMEOUT if a bounded wait of

@@ -14,3 +14,5 @@ from .layerwise import LayerwiseMuon, lpt_partition  # noqa: F401
 from .ops import (Checkpoint8, Routing, checkpoint8, layer_norm,  # noqa: F401
                   layer_norm_backward, layer_norm_checkpoint, ops_sync, route,
                   route_backward, weight_grad)
+from .block import (RotaryPlan, dropout, dropout_backward, gated_ffn,  # noqa: F401
+                    gated_ffn_backward, rotary, rotary_backward)

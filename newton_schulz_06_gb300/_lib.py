@@ -45,6 +45,9 @@ EXPORTS = ("muon_create", "muon_set_stream", "muon_register_params",
            "muon_layer_norm_grad_workspace", "muon_layer_norm_grad",
            "muon_weight_grad_workspace", "muon_weight_grad",
            "muon_route_workspace", "muon_route", "muon_route_grad",
+           "muon_gated_ffn_workspace", "muon_gated_ffn",
+           "muon_gated_ffn_grad_workspace", "muon_gated_ffn_grad",
+           "muon_rotary", "muon_rotary_frequencies", "muon_dropout",
            "muon_ops_sync", "muon_debug_ops_wait_timeout")
 
 
@@ -72,6 +75,7 @@ def _struct(name, *groups):
 
 
 _vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+_u64, _f64 = ctypes.c_uint64, ctypes.c_double
 Ckpt8 = _struct("Ckpt8", (_vp, "q e"), (_i64, "ld_q ld_e"))
 LayerNormArgs = _struct("LayerNormArgs", (_vp, "x weight bias y mean rstd"), (Ckpt8, "saved"),
                         (_i64, "rows cols ld_x ld_y"), (_i32, "x_dtype w_dtype"), (_f32, "eps"))
@@ -90,12 +94,29 @@ RouteGradArgs = _struct("RouteGradArgs",
                         (_i64, "tokens experts k ld_z ld_dw ld_dz"),
                         (_i32, "z_dtype renormalise"), (_f32, "coef"))
 
+GatedFfnArgs = _struct("GatedFfnArgs", (_vp, "x w_gate w_up w_down y gate up offsets"),
+                       (_i64, "rows hidden inner experts ld_x ld_gate ld_up ld_down ld_y ld_kept "
+                              "stride_gate stride_up stride_down"), (_i32, "activation"))
+GatedFfnGradArgs = _struct("GatedFfnGradArgs",
+                           (_vp, "dy x gate up w_gate w_up w_down dx dw_gate dw_up dw_down dgate dup h "
+                                 "offsets"),
+                           (_i64, "rows hidden inner experts ld_dy ld_x ld_kept ld_gate ld_up ld_down "
+                                  "ld_dx ld_d ld_dw_gate ld_dw_up ld_dw_down stride_gate stride_up "
+                                  "stride_down stride_dw_gate stride_dw_up stride_dw_down"),
+                           (_i32, "activation g_dtype accumulate"))
+RotaryTensor = _struct("RotaryTensor", (_vp, "x y"), (_i64, "heads x_batch x_seq x_head y_batch y_seq y_head"))
+RotaryArgs = _struct("RotaryArgs", (RotaryTensor, "q k"), (_vp, "positions turns"),
+                     (_i64, "batch seq head pairs stride_positions offset"),
+                     (_i32, "x_dtype layout positions_64 inverse"), (_f32, "scale"))
+DropoutArgs = _struct("DropoutArgs", (_vp, "x residual y counter"), (_i64, "rows cols ld_x ld_r ld_y"),
+                      (_u64, "seed offset"), (_f64, "p"), (_i32, "x_dtype"))
+
 
 def packer(cls):
     """struct.Struct that packs a structure's fields in order, nested ones in
     line (several times faster than filling the ctypes object): its bytes can
     be passed where a pointer to the structure is expected."""
-    code = {_vp: "Q", _i64: "q", _i32: "i", _f32: "f"}
+    code = {_vp: "Q", _i64: "q", _i32: "i", _f32: "f", _u64: "Q", _f64: "d"}
     flat = []
 
     def walk(c, base):
@@ -180,6 +201,13 @@ def lib() -> ctypes.CDLL:
         "muon_route_workspace": [vp, ctypes.POINTER(sz)],
         "muon_route": [vp, vp, sz, vp, vp, sz],
         "muon_route_grad": [vp, vp, vp, sz],
+        "muon_gated_ffn_workspace": [vp, ctypes.POINTER(sz)],
+        "muon_gated_ffn": [vp, vp, sz, vp, vp, sz],
+        "muon_gated_ffn_grad_workspace": [vp, ctypes.POINTER(sz)],
+        "muon_gated_ffn_grad": [vp, vp, sz, vp, vp, sz],
+        "muon_rotary": [vp, vp, vp, sz],
+        "muon_rotary_frequencies": [_i64, _f64, i32, _f64, _f64, _f64, _f64, vp, vp, vp, sz],
+        "muon_dropout": [vp, vp, vp, sz],
         "muon_ops_sync": [vp, vp, sz],
         "muon_debug_ops_wait_timeout": [i32, vp, vp, sz],
     }

@@ -1,0 +1,350 @@
+"""Python face of libmuon's operators inside a block: the gated feed-forward
+block (dense, or one per expert over a router's offsets), rotary positions of
+queries and keys, and dropout, each with its backward pass.
+
+    q, k = rotary(q, k, plan)                                 # plan = RotaryPlan(head_dim)
+    ...
+    x = dropout(attention, p, seed, step, residual=x)
+    y, saved = gated_ffn(rows, w_gate, w_up, w_down, offsets=r.offsets)
+    drows, dw_gate, dw_up, dw_down = gated_ffn_backward(dy, rows, saved, w_gate, w_up, w_down,
+                                                        offsets=r.offsets)
+
+They keep to :mod:`~newton_schulz_06_gb300.ops`: work is queued on the current
+stream of the tensors' device, outputs that are not given are allocated,
+nothing records for torch.autograd, and the same call gives the same bits
+again.  include/muon.h has the formulas.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Tuple, Union
+
+import torch
+
+from . import _lib
+from ._lib import MuonError
+from .ops import (_BF16, _ERR_LEN, _F32, _I32, _call, _call_ws, _dtype, _fn, _gradient, _local,
+                  _matrix, _need, _output, _vector, Checkpoint8, weight_grad)
+
+_ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+_ffn_args = _lib.packer(_lib.GatedFfnArgs).pack
+_ffn_grad_args = _lib.packer(_lib.GatedFfnGradArgs).pack
+_rotary_args = _lib.packer(_lib.RotaryArgs).pack
+_dropout_args = _lib.packer(_lib.DropoutArgs).pack
+_NO_TENSOR = (0, 0, 0, 0, 0, 0, 0, 0, 0)
+
+
+# ------------------------------------------------------- gated feed-forward
+
+def _bf16(name: str, t: torch.Tensor, index: int, rows: int, cols: int) -> int:
+    """Checks a bf16 matrix of rows x cols; its leading dimension."""
+    if t.dtype != _BF16:
+        raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+    return _matrix(name, t, index, rows, cols)[2]
+
+
+def _experts(offsets: Optional[torch.Tensor], index: int) -> Tuple[int, int]:
+    """(experts, or 0 for a dense block; address of the offsets)."""
+    if offsets is None:
+        return 0, 0
+    _need(offsets.dim() == 1 and offsets.shape[0] >= 2, "offsets must be experts + 1 values")
+    experts = offsets.shape[0] - 1
+    return experts, _vector("offsets", offsets, index, experts + 1, _I32)
+
+
+def _weights(index: int, experts: int, hidden: int, gate, up, down):
+    """Checks the three matrices (or experts x matrices); (inner, their leading
+    dimensions, their strides)."""
+    for name, w in (("w_gate", gate), ("w_up", up), ("w_down", down)):
+        if w.dtype != _BF16:
+            raise ValueError(f"{name} must be bfloat16, got {w.dtype}")
+    shape = gate.shape
+    if len(shape) != (3 if experts else 2):
+        raise ValueError(f"w_gate must be {'experts x inner x hidden' if experts else 'inner x hidden'}, "
+                         f"got {tuple(shape)}")
+    inner = shape[-2]
+    one, two = (inner, hidden), (hidden, inner)
+    if experts:
+        one, two = (experts, *one), (experts, *two)
+    lds = []
+    strides = []
+    for name, w, s in (("w_gate", gate, one), ("w_up", up, one), ("w_down", down, two)):
+        ld, stride = _gradient(name, w, s, index)
+        lds.append(ld)
+        strides.append(stride)
+    return inner, lds, strides
+
+
+def _activation(name: str) -> int:
+    code = _ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {name!r}")
+    return code
+
+
+def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, *,
+              offsets: Optional[torch.Tensor] = None, activation: str = "silu", keep: bool = True,
+              out: Optional[torch.Tensor] = None):
+    """y = (act(x w_gate^T) * (x w_up^T)) w_down^T, in bf16 with fp32 sums.
+
+    x: rows x hidden; w_gate, w_up: inner x hidden; w_down: hidden x inner.
+    offsets (experts + 1 int32 values on the device, e.g. Routing.offsets): x
+    holds the rows by expert, and the weights are experts x matrices; rows of
+    no expert are not written (a new y holds anything there).
+    activation: "silu", "gelu" (by erf) or "gelu_tanh".
+    Returns (y, saved): saved is (g, u), both rows x inner, for
+    :func:`gated_ffn_backward`, or None without keep."""
+    rows, hidden, ld_x, index = _matrix("x", x)
+    _need(x.dtype == _BF16, f"x must be bfloat16, got {x.dtype}")
+    act = _activation(activation)
+    experts, offsets_at = _experts(offsets, index)
+    inner, lds, strides = _weights(index, experts, hidden, w_gate, w_up, w_down)
+    y, ld_y = _output("out", out, x, rows, hidden)
+    saved, gate_at, up_at = None, 0, 0
+    if keep:
+        gate = torch.empty((rows, inner), dtype=_BF16, device=x.device)
+        up = torch.empty((rows, inner), dtype=_BF16, device=x.device)
+        saved, gate_at, up_at = (gate, up), gate.data_ptr(), up.data_ptr()
+    _call_ws(index, "muon_gated_ffn", "muon_gated_ffn_workspace", _ffn_args(
+        x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), y.data_ptr(), gate_at, up_at,
+        offsets_at, rows, hidden, inner, experts or 1, ld_x, *lds, ld_y, inner, *strides, act), x.device)
+    return y, saved
+
+
+def gated_ffn_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint8, None], saved,
+                       w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, *,
+                       offsets: Optional[torch.Tensor] = None, activation: str = "silu",
+                       weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, grads=None, accumulate: bool = False,
+                       dtype: torch.dtype = _BF16):
+    """The gradients of gated_ffn: (dx, dw_gate, dw_up, dw_down).
+
+    saved: what gated_ffn kept.  x: its input, or a Checkpoint8 of it, or of the
+    h of a norm that made it (weight, bias: that norm's); None leaves out the
+    gradients of w_gate and w_up.
+    grads: (dw_gate, dw_up, dw_down) to write, fp32 or bf16 tensors of the
+    weights' shapes, e.g. those that a Muon set steps with (new ones of dtype
+    otherwise); with accumulate the gradients are added to them.  Experts
+    without rows get zeros.  out: receives dx (it may not be dy)."""
+    rows, hidden, ld_dy, index = _matrix("dy", dy)
+    _need(dy.dtype == _BF16, f"dy must be bfloat16, got {dy.dtype}")
+    dev = dy.device
+    act = _activation(activation)
+    experts, offsets_at = _experts(offsets, index)
+    inner, lds, strides = _weights(index, experts, hidden, w_gate, w_up, w_down)
+    gate, up = saved
+    ld_kept = _bf16("gate", gate, index, rows, inner)
+    _need(_bf16("up", up, index, rows, inner) == ld_kept, "gate and up differ in their strides")
+    checkpoint = isinstance(x, Checkpoint8)
+    ld_x = x_at = 0
+    if checkpoint:
+        _need(x.shape == (rows, hidden) and x.device == dev,
+              f"x must be a checkpoint of {(rows, hidden)} on {dev}, is of {x.shape}")
+    else:
+        _need(weight is None and bias is None, "weight and bias go with a checkpoint of x")
+        if x is not None:
+            ld_x, x_at = _bf16("x", x, index, rows, hidden), x.data_ptr()
+    dx, ld_dx = _output("out", out, dy, rows, hidden)
+    if out is not None and rows and (dx.data_ptr() == dy.data_ptr() or dx.data_ptr() == x_at):
+        raise ValueError("out may not be dy or x: they are read after it is written")
+    need_x = x is not None
+    if grads is None:
+        _need(not accumulate, "accumulate needs grads to add to")
+        grads = [torch.empty(w.shape, dtype=dtype, device=dev) if need_x or i == 2 else None
+                 for i, w in enumerate((w_gate, w_up, w_down))]
+    else:
+        grads = list(grads)
+        _need(len(grads) == 3, "grads must be (dw_gate, dw_up, dw_down)")
+        if not need_x:
+            grads[:2] = None, None
+    lead = (experts,) if experts else ()
+    at, ld_g, stride_g, kind = [0, 0, 0], [0, 0, 0], [0, 0, 0], None
+    for i, (name, shape) in enumerate((("dw_gate", (inner, hidden)), ("dw_up", (inner, hidden)),
+                                       ("dw_down", (hidden, inner)))):
+        g = grads[i]
+        if g is None:
+            continue
+        ld_g[i], stride_g[i] = _gradient(name, g, (*lead, *shape), index)
+        _need(kind is None or g.dtype == kind, "grads differ in type")
+        kind = g.dtype
+        if not (checkpoint and i < 2):
+            at[i] = g.data_ptr()
+    made = [None, None]
+    made_at, ld_d = (0, 0), 0
+    if checkpoint:
+        made = [torch.empty((rows, inner), dtype=_BF16, device=dev) for _ in range(2)]
+        made_at, ld_d = (made[0].data_ptr(), made[1].data_ptr()), inner
+    code = _lib.MUON_BF16 if kind is None else _dtype("grads", next(g for g in grads if g is not None))
+    _call_ws(index, "muon_gated_ffn_grad", "muon_gated_ffn_grad_workspace", _ffn_grad_args(
+        dy.data_ptr(), x_at, gate.data_ptr(), up.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+        w_down.data_ptr(), dx.data_ptr(), *at, *made_at, 0, offsets_at, rows, hidden, inner, experts or 1,
+        ld_dy, ld_x, ld_kept, *lds, ld_dx, ld_d, *ld_g, *strides, *stride_g, act, code, bool(accumulate)), dev)
+    if checkpoint:
+        for d, g in zip(made, grads):
+            if g is not None:
+                weight_grad(d, x, weight=weight, bias=bias, offsets=offsets, add=g if accumulate else None, out=g)
+    return (dx, *grads)
+
+
+# --------------------------------------------------------- rotary positions
+
+class RotaryPlan:
+    """The frequencies of a rotary embedding of the first `dim` values of a
+    head (even, at most 512): pair i turns by base^(-2 i / dim) radians a
+    position.
+
+    layout: "half" (value i with i + dim / 2) or "interleaved" (2 i with 2 i + 1).
+    scaling, for contexts longer than the trained one: "none", "linear"
+    (frequencies divided by factor), "ntk" (a larger base) or "yarn" (divided
+    for the pairs that turn less than slow times in `original` positions, kept
+    for those that turn more than fast times, a ramp between, and the result
+    times 0.1 ln(factor) + 1).  A plan is host data and serves any device."""
+
+    __slots__ = ("dim", "layout", "scale", "_turns", "_at")
+
+    def __init__(self, dim: int, *, base: float = 10000.0, layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, original: float = 4096, fast: float = 32.0, slow: float = 1.0):
+        _need(dim % 2 == 0 and 2 <= dim <= 512, f"dim must be even and 2 .. 512, got {dim}")
+        if layout not in _LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+        if scaling not in _SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}, got {scaling!r}")
+        turns, scale = (ctypes.c_uint64 * (dim // 2))(), ctypes.c_float()
+        err = _local.err
+        rc = _fn("muon_rotary_frequencies")(dim // 2, base, _SCALINGS[scaling], factor, original, fast, slow,
+                                            turns, ctypes.byref(scale), err, _ERR_LEN)
+        if rc < 0:
+            raise MuonError(rc, f"muon_rotary_frequencies: {err.value.decode(errors='replace')}")
+        self.dim, self.layout, self.scale = dim, _LAYOUTS[layout], scale.value
+        self._turns, self._at = turns, ctypes.addressof(turns)
+
+    @property
+    def frequencies(self) -> Tuple[float, ...]:
+        """Radians a position of every pair."""
+        return tuple(t * (2.0 * math.pi) * 2.0 ** -64 for t in self._turns)
+
+
+def _heads(name: str, t: torch.Tensor, index: int):
+    """Checks a tensor of (batch x) seq x heads x head; (shape with a batch,
+    strides with one)."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be seq x heads x head, or batch x seq x heads x head, got "
+                         f"{tuple(t.shape)}")
+    on = t.get_device()
+    if on < 0 or (index >= 0 and on != index):
+        raise ValueError(f"{name} must be a CUDA tensor of its operator's device, is on {t.device}")
+    shape, strides = tuple(t.shape), t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}'s heads must be dense (stride(-1) == 1)")
+    if len(shape) == 3:
+        shape, strides = (1, *shape), (0, *strides)
+    return shape, strides
+
+
+def _turn(q, k, plan: RotaryPlan, positions, offset: int, out_q, out_k, inverse: bool):
+    index = q.get_device()
+    shape, _ = _heads("q", q, index)
+    batch, seq, _, head = shape
+    dtype = _dtype("q", q)
+    _need(plan.dim <= head, f"heads of {head} values are shorter than the plan's {plan.dim}")
+    tensors, outs = [], []
+    for name, x, out in (("q", q, out_q), ("k", k, out_k)):
+        if x is None:
+            _need(out is None, f"out_{name} without {name}")
+            tensors.append(_NO_TENSOR)
+            outs.append(None)
+            continue
+        s, strides = _heads(name, x, index)
+        _need(x.dim() == q.dim() and (s[0], s[1], s[3]) == (batch, seq, head) and x.dtype == q.dtype,
+              f"{name} must match q in all but its heads, got {tuple(x.shape)} of {x.dtype}")
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _need(out.dtype == x.dtype and out.shape == x.shape,
+              f"out_{name} must be {tuple(x.shape)} of {x.dtype}, got {tuple(out.shape)} of {out.dtype}")
+        o = _heads(f"out_{name}", out, index)[1]
+        for n, st in zip(s[:3], o[:3]):
+            _need(st > 0 or n <= 1, f"out_{name} has places that share memory")
+        tensors.append((x.data_ptr(), out.data_ptr(), s[2], *strides[:3], *o[:3]))
+        outs.append(out)
+    at = stride = wide = 0
+    if positions is not None:
+        if positions.dtype not in (_I32, torch.int64):
+            raise ValueError(f"positions must be int32 or int64, got {positions.dtype}")
+        _need(positions.get_device() == index, f"positions must be on {q.device}")
+        want = positions.shape
+        _need(tuple(want) in ((seq,), (1, seq), (batch, seq)),
+              f"positions must be {(seq,)} or {(batch, seq)}, got {tuple(want)}")
+        _need(positions.stride(-1) == 1 or seq <= 1, "positions must be dense along seq")
+        at, wide = positions.data_ptr(), positions.dtype == torch.int64
+        stride = positions.stride(0) if len(want) == 2 and want[0] > 1 else 0
+    _call(index, "muon_rotary", _rotary_args(
+        *tensors[0], *tensors[1], at, plan._at, batch, seq, head, plan.dim // 2, stride, offset, dtype,
+        plan.layout, wide, inverse, plan.scale))
+    return tuple(outs)
+
+
+def rotary(q: torch.Tensor, k: Optional[torch.Tensor], plan: RotaryPlan, *,
+           positions: Optional[torch.Tensor] = None, offset: int = 0,
+           out_q: Optional[torch.Tensor] = None, out_k: Optional[torch.Tensor] = None):
+    """Turns the first plan.dim values of every head of q and k (or of q alone)
+    by their positions; the others are copied.  Returns (q', k').
+
+    q, k: seq x heads x head, or batch x seq x heads x head, fp32 or bf16; any
+    strides but that a head is dense, so that views (a transposed batch, the
+    last values of longer heads) do.  out_q, out_k may be q and k themselves.
+    positions: int32 or int64, seq or batch x seq; None counts from 0.  offset
+    is added to each."""
+    return _turn(q, k, plan, positions, offset, out_q, out_k, False)
+
+
+def rotary_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], plan: RotaryPlan, *,
+                    positions: Optional[torch.Tensor] = None, offset: int = 0,
+                    out_q: Optional[torch.Tensor] = None, out_k: Optional[torch.Tensor] = None):
+    """The gradients of rotary's q and k from those of its results."""
+    return _turn(dq, dk, plan, positions, offset, out_q, out_k, True)
+
+
+# ----------------------------------------------------------------- dropout
+
+_U64 = (1 << 64) - 1
+
+
+def _drop(name, x, p, seed, offset, counter, residual, out):
+    rows, cols, ld, index = _matrix(name, x)
+    y, ld_y = _output("out", out, x, rows, cols)
+    r_at = ld_r = counter_at = 0
+    if residual is not None:
+        _need(residual.dtype == x.dtype, f"residual must be {x.dtype}, got {residual.dtype}")
+        ld_r, r_at = _matrix("residual", residual, index, rows, cols)[2], residual.data_ptr()
+    if counter is not None:
+        _need(counter.dtype == torch.int64 and counter.numel() == 1 and counter.get_device() == index,
+              "counter must be one int64 value on the device")
+        counter_at = counter.data_ptr()
+    _call(index, "muon_dropout", _dropout_args(
+        x.data_ptr(), r_at, y.data_ptr(), counter_at, rows, cols, ld, ld_r, ld_y, seed & _U64, offset & _U64,
+        p, _dtype(name, x)))
+    return y
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, *,
+            counter: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x with a share p of its elements zero and the others divided by 1 - p
+    (+ residual), rows x cols, fp32 or bf16.
+
+    Which elements are dropped follows from seed, offset and an element's place
+    alone, so that no mask is kept: :func:`dropout_backward` is given the same
+    two.  Calls of one seed need offsets of their own.  p is taken to the
+    nearest 2^-16.  counter: one int64 value on the device that is added to the
+    offset when the kernel runs (captured graphs).  out may be x or residual."""
+    return _drop("x", x, p, seed, offset, counter, residual, out)
+
+
+def dropout_backward(dy: torch.Tensor, p: float, seed: int, offset: int = 0, *,
+                     counter: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of dropout's x (that of the residual is dy itself)."""
+    return _drop("dy", dy, p, seed, offset, counter, None, out)

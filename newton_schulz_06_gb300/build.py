@@ -32,7 +32,7 @@ LIB = os.path.join(PKG, "libmuon.so")
 TORCH_LIB = os.path.join(PKG, "libmuon_torch.so")
 SOURCES = ["ew_kernels.cu", "ns_kernels.cu", "ns2_kernels.cu", "muon_api.cpp",
            "muon_noalloc.cu", "ops_api.cpp", "checkpoint8.cu", "layer_norm.cu",
-           "weight_grad.cu", "route.cu"]
+           "weight_grad.cu", "route.cu", "gated_ffn.cu", "rotary.cu", "dropout.cu"]
 HEADERS = [os.path.join(CSRC, "muon_internal.h"), os.path.join(CSRC, "tc_ptx.cuh"),
            os.path.join(CSRC, "ops_internal.h"), os.path.join(CSRC, "tc_wait.cuh"),
            os.path.join(CSRC, "weight_grad_stages.h"), os.path.join(CSRC, "norm_ring.h"),

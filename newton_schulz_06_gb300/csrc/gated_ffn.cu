@@ -1,0 +1,960 @@
+// The gated feed-forward block and its gradient (muon_gated_ffn,
+// muon_gated_ffn_grad): five grouped products, one kernel each, over all
+// experts' rows at once.
+//
+//   UP      h = act(x Wg^T) * (x Wu^T)  (g and u kept if asked for)
+//   DOWN    y = h Wd^T
+//   DHIDDEN dh = dy Wd, at once turned into dg, du and h
+//   DX      dx = dg Wg + du Wu, one sum over both products
+//   DW      dWg = dg^T x, dWu = du^T x, dWd = dy^T h
+//
+// All are out[n][m] = sum over k of B[n][k] A[m][k].  A CTA pair (tcgen05
+// cta_group::2) computes 256 m x up to 256 n: the matrices of an expert are the
+// instruction's M side and its rows (tokens) the N side, because N may be any
+// multiple of 32 while M is always 256: an expert's last rows then cost what
+// they are, where a last tile of 256 tokens costs 256 (128 experts of about 500
+// tokens would waste a quarter).  UP takes 64 rows of Wg and the same 64 of Wu
+// as a CTA's 128 rows, so that a tile has both factors of its h.
+//
+// TMEM holds m in lanes and n in columns, memory wants m along rows: the
+// epilogue turns 16 columns at a time in shared memory (fp32), after which a
+// thread has eight neighbours of an output row, reads what it needs beside
+// them, and stores 16 bytes.
+//
+// Roles in a CTA: warp 0 loads (TMA), warp 1 issues the products (the pair's
+// leader only), warps 2-9 are the epilogue, in two teams of four that take a
+// tile's columns in turn, warp 10 clears what DW loads past an expert's last
+// token.  Two accumulators, so that a tile is written out while the next one's
+// products run.  Pairs walk the tiles in turn.
+//
+// Every wait is bounded; one that runs out raises g_ffn_err (muon_ops_sync).
+#include <cudaTypedefs.h>
+
+#include "ops_internal.h"
+#include "tc_wait.cuh"
+
+namespace muon {
+namespace ops {
+namespace {
+
+using namespace ptx;
+
+constexpr int F_K = 64;                            // of the sums, a step
+constexpr int F_BOX = 64 * 64 * 2;                 // a TMA box: 64 rows of 64 bf16
+constexpr int F_STAGES = 5;
+constexpr int F_OP_BYTES = 2 * F_BOX;              // an operand's part of a CTA, a step
+constexpr int F_STAGE_BYTES = 2 * F_OP_BYTES;
+constexpr int F_EXPERTS = 1024;
+constexpr int F_COLS = 16;                         // columns that are turned at a time
+constexpr int F_ROW = 132;                         // floats of a turned row: 128 and a gap
+constexpr int F_TURN_BYTES = F_COLS * F_ROW * 4;
+constexpr int F_BAR_OFF = F_STAGES * F_STAGE_BYTES;
+constexpr int F_TURN_OFF = F_BAR_OFF + 512;
+constexpr int F_TABLE_OFF = F_TURN_OFF + 4 * F_TURN_BYTES;       // two teams, two buffers
+constexpr int F_SMEM = F_TABLE_OFF + 2 * (F_EXPERTS + 1) * 4 + 1024;
+static_assert(F_SMEM <= 232448, "shared memory per CTA");
+constexpr int F_EPI_WARPS = 8;
+constexpr int F_PATCH_WARP = 2 + F_EPI_WARPS;
+constexpr int F_THREADS = 32 * (F_PATCH_WARP + 1);
+constexpr int F_TMEM_COLS = 512;
+constexpr int F_PAIRS = 76;                        // a pair per two of the 152 SMs
+constexpr int F_BAND = 8;
+
+__device__ int g_ffn_err;
+
+enum Op { UP, DOWN, DHIDDEN, DX, DW };
+
+// One output matrix (or as many as there are experts).
+struct Out {
+    void* p;
+    int64_t ld, stride;
+    int32_t vec;             // rows lie on 16 bytes
+};
+
+// One of the sums' operand pairs: a is M's side, b is N's.
+struct Maps {
+    CUtensorMap a, b;
+};
+
+struct FfnLaunch {
+    Maps maps[3];            // UP: Wg with x, Wu; DX: Wg with dg, Wu with du; DW: its three products
+    Out out[3];              // UP: h, g, u; DHIDDEN: dg, du, h; DW: dWg, dWu, dWd
+    const void *gate, *up;   // DHIDDEN reads them
+    int64_t ld_kept;
+    int32_t kept_vec;
+    const int32_t* offsets;
+    int64_t rows;
+    int32_t experts;
+    int32_t m[2], k;         // extents; DW: m[0] is hidden, m[1] inner; else m[0]
+    int32_t a_by_expert[3];  // an expert's own matrix, or one for all
+    int32_t products;        // DW: which of them, as bits
+    int32_t tile_n;          // rows of N a tile, a multiple of 32
+    int32_t act;
+    int32_t out_f32, accumulate;
+    unsigned long long wait_limit_ns;
+};
+
+// A tile.
+struct Item {
+    int32_t e, j;            // expert, product (DW)
+    int32_t m0, n0;          // its first m (UP: of h), its first row of N
+    int32_t n_end;           // N's rows end here
+    int32_t n;               // the instruction's N
+    int32_t t0, steps;       // DW: the expert's first token; steps of 64
+    int32_t tail;            // DW: tokens of the last step, if not 64
+};
+
+template <int OP>
+struct Tiles {
+    const FfnLaunch& p;
+    const int32_t *begin, *first;        // experts' first rows, and their first tile rows
+    int32_t total, tiles_m;
+    int32_t base[3], count[3], per;      // DW: a product's first tile, its tiles, all of a matrix
+    __device__ __forceinline__ Tiles(const FfnLaunch& l, const int32_t* table) : p(l) {
+        begin = table;
+        first = table + p.experts + 1;
+        if constexpr (OP == DW) {
+            per = 0;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                const int32_t m = (p.m[j == 2] + 255) / 256, n = (p.m[j != 2] + p.tile_n - 1) / p.tile_n;
+                base[j] = per;
+                count[j] = p.products >> j & 1 ? m * n : 0;
+                per += count[j];
+            }
+            total = per * p.experts;
+        } else {
+            tiles_m = (p.m[0] + (OP == UP ? 127 : 255)) / (OP == UP ? 128 : 256);
+            total = first[p.experts] * tiles_m;
+        }
+    }
+    __device__ __forceinline__ Item at(int32_t it) const {
+        Item x;
+        x.tail = 0;
+        x.j = 0;
+        int32_t in, tn, tm;
+        if constexpr (OP == DW) {
+            x.e = it / per;
+            in = it - x.e * per;
+            x.j = in < base[1] ? 0 : in < base[2] ? 1 : 2;
+            in -= x.j == 0 ? 0 : x.j == 1 ? base[1] : base[2];
+            tm = (p.m[x.j == 2] + 255) / 256;
+            tn = (p.m[x.j != 2] + p.tile_n - 1) / p.tile_n;
+            x.n_end = p.m[x.j != 2];
+            x.t0 = begin[x.e];
+            const int32_t len = begin[x.e + 1] - x.t0;
+            x.steps = (len + F_K - 1) / F_K;
+            x.tail = len % F_K;
+        } else {
+            // the expert whose tiles these are
+            int32_t lo = 0, hi = p.experts;
+            const int32_t row = it / tiles_m;
+            while (hi - lo > 1) {
+                const int32_t mid = (lo + hi) >> 1;
+                if (first[mid] <= row) lo = mid;
+                else hi = mid;
+            }
+            x.e = lo;
+            in = it - first[lo] * tiles_m;
+            tm = tiles_m;
+            tn = first[lo + 1] - first[lo];
+            x.n_end = begin[lo + 1];
+            x.t0 = 0;
+            x.steps = (p.k + F_K - 1) / F_K * (OP == DX ? 2 : 1);
+        }
+        // bands of eight tiles of N, column by column: the tiles that run
+        // together share their operands in L2
+        const int32_t band = in / (F_BAND * tm), high = min(F_BAND, tn - band * F_BAND);
+        in -= band * F_BAND * tm;
+        const int32_t m = in / high, n = band * F_BAND + in - m * high;
+        x.m0 = m * (OP == UP ? 128 : 256);
+        x.n0 = (OP == DW ? 0 : begin[x.e]) + n * p.tile_n;
+        x.n = min(p.tile_n, (x.n_end - x.n0 + 31) / 32 * 32);
+        return x;
+    }
+};
+
+__device__ __forceinline__ void load_box(uint32_t dst, const void* tmap, uint32_t cluster_bar, int x, int y,
+                                         int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::"
+        "complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit_pair_multicast(uint32_t bar) {
+    const uint16_t mask = 0x3;
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster."
+        "multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(mask)
+        : "memory");
+}
+__device__ __forceinline__ void commit_pair_local(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+// 16 fp32 columns of this warp's TMEM lanes.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// A barrier of one team's 128 threads.
+__device__ __forceinline__ void team_sync(int team) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + team) : "memory");
+}
+
+// 1 / (1 + e^-v).  The exponential and the reciprocal are good to a few 2^-23,
+// a thousandth of the bf16 rounding behind them.
+__device__ __forceinline__ float logistic(float v) { return __frcp_rn(1.f + __expf(-v)); }
+
+// act(g), and its derivative to d.
+__device__ __forceinline__ float activate(int act, float g, float& d) {
+    if (act == MUON_ACT_SILU) {
+        const float s = logistic(g);
+        d = s * fmaf(g, 1.f - s, 1.f);
+        return g * s;
+    }
+    if (act == MUON_ACT_GELU) {
+        const float c = fmaf(0.5f, erff(g * 0.70710678f), 0.5f);
+        d = fmaf(g * 0.39894228f, __expf(-0.5f * g * g), c);
+        return g * c;
+    }
+    // (1 + tanh z) / 2 is the logistic function of 2 z, which is 0 or 1 long
+    // before the limit on g^2 (no infinity to multiply by 0)
+    const float q = fminf(g * g, 1000.f), s = logistic(g * fmaf(0.071354816f, q, 1.5957691f));
+    d = s * fmaf(g * (1.f - s), fmaf(0.21406445f, q, 1.5957691f), 1.f);
+    return g * s;
+}
+
+// Eight neighbours of a turned row.  The two halves are read in an order that
+// lets eight threads' 16 bytes fall on all banks.
+__device__ __forceinline__ void turned8(const float* row, int group, float (&v)[8]) {
+    const int swap = group >> 2 & 1;
+    const float4 a = *reinterpret_cast<const float4*>(row + 8 * group + 4 * swap);
+    const float4 b = *reinterpret_cast<const float4*>(row + 8 * group + 4 * (swap ^ 1));
+    const float4 lo = swap ? b : a, hi = swap ? a : b;
+    v[0] = lo.x;
+    v[1] = lo.y;
+    v[2] = lo.z;
+    v[3] = lo.w;
+    v[4] = hi.x;
+    v[5] = hi.y;
+    v[6] = hi.z;
+    v[7] = hi.w;
+}
+
+// Eight neighbours of a bf16 row, of which `left` are there.
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int left, bool vec) {
+    if (vec && left >= 8) return *reinterpret_cast<const uint4*>(p);
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    uint16_t* h = reinterpret_cast<uint16_t*>(&q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) h[i] = reinterpret_cast<const uint16_t*>(p)[i];
+    return q;
+}
+__device__ __forceinline__ void widen8(const uint4& q, float (&v)[8]) {
+    const float2 f[4] = {bf16x2_f32(q.x), bf16x2_f32(q.y), bf16x2_f32(q.z), bf16x2_f32(q.w)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = f[i].x;
+        v[2 * i + 1] = f[i].y;
+    }
+}
+__device__ __forceinline__ void put8(const Out& o, int64_t at, int left, const float (&v)[8]) {
+    __nv_bfloat16* const p = static_cast<__nv_bfloat16*>(o.p) + at;
+    if (o.vec && left >= 8) {
+        store8_bf16(p, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) p[i] = __float2bfloat16_rn(v[i]);
+}
+// A weight gradient's eight, added to what is there if asked for.
+__device__ __forceinline__ void put8_grad(const Out& o, int64_t at, int left, bool f32, bool add,
+                                          float (&v)[8]) {
+    if (!f32) {
+        if (add) {
+            float c[8];
+            widen8(load8(static_cast<const __nv_bfloat16*>(o.p) + at, left, o.vec), c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += c[i];
+        }
+        put8(o, at, left, v);
+        return;
+    }
+    float* const p = static_cast<float*>(o.p) + at;
+    if (o.vec && left >= 8) {
+        float4* const q = reinterpret_cast<float4*>(p);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float4 f = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+            if (add) {
+                const float4 c = q[h];
+                f = make_float4(f.x + c.x, f.y + c.y, f.z + c.z, f.w + c.w);
+            }
+            q[h] = f;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) p[i] = add ? p[i] + v[i] : v[i];
+}
+
+template <int OP>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
+    gated_ffn_kernel(const __grid_constant__ FfnLaunch p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + F_BAR_OFF);   // a step's loads (leader's)
+    uint64_t* empty_bar = full_bar + F_STAGES;      // its products have run
+    uint64_t* tail_bar = empty_bar + F_STAGES;      // DW: this CTA's loads of a short step
+    uint64_t* patch_bar = tail_bar + F_STAGES;      // which both CTAs have cleared (leader's)
+    uint64_t* tfull_bar = patch_bar + F_STAGES;
+    uint64_t* tempty_bar = tfull_bar + 2;
+    uint64_t* drain_bar = tempty_bar + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int32_t* const table = reinterpret_cast<int32_t*>(smem + F_TABLE_OFF);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1;
+    const int npairs = gridDim.x >> 1;
+    constexpr bool A_MN = OP == DHIDDEN || OP == DX || OP == DW, B_MN = OP == DW;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < F_STAGES; ++s) {
+            mbar_init(smem_u32(&full_bar[s]), 1);
+            mbar_init(smem_u32(&empty_bar[s]), 1);
+            mbar_init(smem_u32(&tail_bar[s]), 1);
+            mbar_init(smem_u32(&patch_bar[s]), 2);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&tfull_bar[a]), 1);
+            mbar_init(smem_u32(&tempty_bar[a]), 2 * F_EPI_WARPS);
+        }
+        mbar_init(smem_u32(drain_bar), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile(
+            "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                smem_u32(tmem_slot)),
+            "r"(F_TMEM_COLS)
+            : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (warp == 2) {
+        // the experts' first rows (rising, within the rows there are) and
+        // their first rows of tiles
+        int32_t rows = 0, tiles = 0;
+        for (int e0 = 0; e0 <= p.experts; e0 += 32) {
+            const int e = e0 + lane;
+            int32_t b = e <= p.experts ? (p.offsets ? p.offsets[e] : e ? int32_t(p.rows) : 0) : 0;
+            b = min(max(b, 0), int32_t(p.rows));
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t v = __shfl_up_sync(0xffffffffu, b, o);
+                if (lane >= o) b = max(b, v);
+            }
+            b = max(b, rows);
+            const int32_t before = __shfl_up_sync(0xffffffffu, b, 1);
+            // tiles of the expert before e
+            int32_t n = e ? (b - (lane ? before : rows) + p.tile_n - 1) / p.tile_n : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t v = __shfl_up_sync(0xffffffffu, n, o);
+                if (lane >= o) n += v;
+            }
+            n += tiles;
+            if (e <= p.experts) {
+                table[e] = b;
+                table[p.experts + 1 + e] = n;
+            }
+            rows = __shfl_sync(0xffffffffu, b, 31);
+            tiles = __shfl_sync(0xffffffffu, n, 31);
+        }
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint64_t limit = p.wait_limit_ns;
+    const Tiles<OP> tiles(p, table);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0) {
+            uint32_t step = 0;
+            // a bit a stage: its last load was a short step's, and the parities
+            // that follow its loads of either kind
+            uint32_t tails = 0, tail_phase = 0, full_phase = 0;
+            bool ok = true;
+            for (int32_t it = pair; ok && it < tiles.total; it += npairs) {
+                const Item x = tiles.at(it);
+                const int boxes = (x.n / 2 + 63) / 64;
+                const uint32_t bytes = F_OP_BYTES + boxes * F_BOX;
+                const int m0 = x.m0 + static_cast<int>(rank) * (OP == UP ? 64 : 128);
+                const int n0 = x.n0 + static_cast<int>(rank) * (x.n / 2);
+                const int half = (p.k + F_K - 1) / F_K;      // DX: steps of the first product
+                for (int s = 0; s < x.steps; ++s, ++step) {
+                    const uint32_t slot = step % F_STAGES;
+                    if (!wait_soon(smem_u32(&empty_bar[slot]), (step / F_STAGES & 1) ^ 1, abort_flag,
+                                   &g_ffn_err, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool tail = OP == DW && x.tail && s == x.steps - 1;
+                    uint32_t bar = smem_u32(&full_bar[slot]);
+                    if (tail) {
+                        bar = smem_u32(&tail_bar[slot]);
+                        mbar_expect_tx(bar, bytes);
+                        tails |= 1u << slot;
+                        tail_phase ^= 1u << slot;
+                        bar = map_to_rank(bar, rank);
+                    } else {
+                        if (rank == 0) mbar_expect_tx(bar, 2 * bytes);
+                        tails &= ~(1u << slot);
+                        full_phase ^= 1u << slot;
+                        bar = map_to_rank(bar, 0);
+                    }
+                    const uint32_t a = smem_u32(smem + slot * F_STAGE_BYTES), b = a + F_OP_BYTES;
+                    const int j = OP == DW ? x.j : OP == DX ? s >= half : 0;
+                    const int k0 = OP == DW ? x.t0 + s * F_K : (OP == DX && j ? s - half : s) * F_K;
+                    const Maps& m = p.maps[j];
+                    const int z = p.a_by_expert[j] ? x.e : 0;
+                    if constexpr (OP == UP) {
+                        load_box(a, &m.a, bar, k0, m0, z);
+                        load_box(a + F_BOX, &p.maps[1].a, bar, k0, m0, p.a_by_expert[1] ? x.e : 0);
+                    } else if constexpr (A_MN) {
+                        load_box(a, &m.a, bar, m0, k0, z);
+                        load_box(a + F_BOX, &m.a, bar, m0 + 64, k0, z);
+                    } else {
+                        load_box(a, &m.a, bar, k0, m0, z);
+                        load_box(a + F_BOX, &m.a, bar, k0, m0 + 64, z);
+                    }
+                    for (int i = 0; i < boxes; ++i) {
+                        if constexpr (B_MN) load_box(b + i * F_BOX, &m.b, bar, n0 + 64 * i, k0, 0);
+                        else load_box(b + i * F_BOX, &m.b, bar, k0, n0 + 64 * i, 0);
+                    }
+                }
+            }
+            if (!ok) {
+                // the last load of each stage: the leader's barriers count both CTAs'
+                for (uint32_t i = step - min(step, uint32_t(F_STAGES)); i < step; ++i) {
+                    const uint32_t slot = i % F_STAGES;
+                    if (tails >> slot & 1)
+                        wait_quiet(smem_u32(&tail_bar[slot]), (tail_phase >> slot & 1) ^ 1, limit);
+                    else if (rank == 0)
+                        wait_quiet(smem_u32(&full_bar[slot]), (full_phase >> slot & 1) ^ 1, limit);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------- products (leader)
+        if (lane == 0 && rank == 0) {
+            uint32_t step = 0;
+            uint32_t full_phase = 0, patch_phase = 0;       // a bit a stage
+            uint32_t uses[2] = {0, 0};
+            uint32_t acc = 0;
+            bool ok = true, any = false;
+            const uint64_t a_desc = smem_desc(smem_u32(smem), A_MN ? F_BOX : 16, 1024);
+            const uint64_t b_desc = smem_desc(smem_u32(smem + F_OP_BYTES), B_MN ? F_BOX : 16, 1024);
+            for (int32_t it = pair; ok && it < tiles.total; it += npairs) {
+                const Item x = tiles.at(it);
+                if (x.steps == 0) continue;
+                const uint32_t use = acc ? uses[1]++ : uses[0]++;
+                if (!wait_soon(smem_u32(&tempty_bar[acc]), (use & 1) ^ 1, abort_flag, &g_ffn_err, limit)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t idesc = instr_desc(256, x.n, B_MN) | (A_MN ? 1u << 15 : 0u);
+                for (int s = 0; s < x.steps; ++s, ++step) {
+                    const uint32_t slot = step % F_STAGES;
+                    const bool tail = OP == DW && x.tail && s == x.steps - 1;
+                    const uint32_t bar = smem_u32(tail ? &patch_bar[slot] : &full_bar[slot]);
+                    uint32_t& phase = tail ? patch_phase : full_phase;
+                    if (!wait_soon(bar, phase >> slot & 1, abort_flag, &g_ffn_err, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    phase ^= 1u << slot;
+                    tc_fence_after();
+                    const uint64_t ad = a_desc + (slot * F_STAGE_BYTES >> 4);
+                    const uint64_t bd = b_desc + (slot * F_STAGE_BYTES >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < F_K / 16; ++kk)
+                        mma_pair(tmem_base + acc * 256, ad + uint64_t(kk * (A_MN ? 2048 : 32) >> 4),
+                                 bd + uint64_t(kk * (B_MN ? 2048 : 32) >> 4), idesc, (s || kk) ? 1u : 0u);
+                    any = true;
+                    commit_pair_multicast(smem_u32(&empty_bar[slot]));
+                }
+                if (ok) commit_pair_multicast(smem_u32(&tfull_bar[acc]));
+                acc ^= 1;
+            }
+            if (!ok && any) {
+                commit_pair_local(smem_u32(drain_bar));
+                wait_quiet(smem_u32(drain_bar), 0, limit);
+            }
+        }
+    } else if (warp == F_PATCH_WARP) {
+        // ---------------------------------------------------- short steps of DW
+        if constexpr (OP == DW) {
+            uint32_t step = 0, phase = 0;
+            const uint32_t patch_leader = map_to_rank(smem_u32(patch_bar), 0);
+            for (int32_t it = pair; it < tiles.total; it += npairs) {
+                const Item x = tiles.at(it);
+                step += x.steps;
+                if (!x.steps || !x.tail) continue;
+                const uint32_t slot = (step - 1) % F_STAGES;
+                const bool got = wait_soon(smem_u32(&tail_bar[slot]), phase >> slot & 1, abort_flag,
+                                           &g_ffn_err, limit);
+                if (!__all_sync(0xffffffffu, got)) break;
+                phase ^= 1u << slot;
+                // tokens of the next expert, or of none: 0 times a NaN of
+                // theirs would be a NaN here, so both operands are cleared
+                uint8_t* const stage = smem + slot * F_STAGE_BYTES;
+                const int boxes = 2 + (x.n / 2 + 63) / 64;
+                for (int box = 0; box < boxes; ++box)
+                    for (int c = x.tail * 8 + lane; c < 64 * 8; c += 32)
+                        *reinterpret_cast<uint4*>(stage + box * F_BOX + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(patch_leader + 8 * slot);
+            }
+        }
+    } else {
+        // --------------------------------------------------------- write out
+        const int lg = warp & 3;                    // this warp's 32 TMEM lanes
+        const int team = (warp - 2) / 4;
+        const int tid = (warp - 2) % 4 * 32 + lane;
+        float* const turn0 = reinterpret_cast<float*>(smem + F_TURN_OFF) + team * 2 * F_COLS * F_ROW;
+        const uint32_t tempty_leader = map_to_rank(smem_u32(tempty_bar), 0);
+        uint32_t uses[2] = {0, 0};
+        uint32_t acc = 0, flip = 0;
+        constexpr int GROUPS = OP == UP ? 8 : 16;   // of eight outputs of a row
+        constexpr int UNITS = F_COLS * GROUPS / 128;
+        for (int32_t it = pair; it < tiles.total; it += npairs) {
+            const Item x = tiles.at(it);
+            if (x.steps) {
+                const uint32_t use = acc ? uses[1]++ : uses[0]++;
+                const bool got = wait_soon(smem_u32(&tfull_bar[acc]), use & 1, abort_flag, &g_ffn_err, limit);
+                // the team's barriers need all four warps: a wait that ran out
+                // for one leaves them all
+                int bad = !got;
+                asm volatile(
+                    "{\n\t.reg .pred a, b;\n\t"
+                    "setp.ne.s32 a, %0, 0;\n\t"
+                    "barrier.red.or.pred b, %1, 128, a;\n\t"
+                    "selp.s32 %0, 1, 0, b;\n\t}"
+                    : "+r"(bad)
+                    : "r"(1 + team)
+                    : "memory");
+                if (bad) break;
+                tc_fence_after();
+            }
+            const uint32_t taddr = tmem_base + acc * 256 + (static_cast<uint32_t>(lg * 32) << 16);
+            const int n_real = min(x.n, x.n_end - x.n0);
+            const int m0 = x.m0 + static_cast<int>(rank) * (OP == UP ? 64 : 128);
+            const int m_end = OP == DW ? p.m[x.j == 2] : p.m[0];
+            int last = (n_real - 1) / F_COLS;       // this team's last columns
+            if ((last & 1) != team) --last;
+            auto release = [&] {
+                if (!x.steps) return;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * acc);
+            };
+            if (last < 0) release();
+            for (int c = team; c <= last; c += 2) {
+                const int n0 = x.n0 + c * F_COLS;
+                // what is read beside the sums, ahead of them
+                uint4 kg[UNITS], ku[UNITS];
+                if constexpr (OP == DHIDDEN) {
+#pragma unroll
+                    for (int i = 0; i < UNITS; ++i) {
+                        const int u = tid + 128 * i, row = n0 + u / GROUPS, m = m0 + u % GROUPS * 8;
+                        kg[i] = ku[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (row < x.n_end && m < m_end) {
+                            const int64_t at = row * p.ld_kept + m;
+                            kg[i] = load8(static_cast<const __nv_bfloat16*>(p.gate) + at, m_end - m, p.kept_vec);
+                            ku[i] = load8(static_cast<const __nv_bfloat16*>(p.up) + at, m_end - m, p.kept_vec);
+                        }
+                    }
+                }
+                uint32_t raw[16];
+                if (x.steps) {
+                    tmem_ld16(taddr + c * F_COLS, raw);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) raw[i] = 0u;
+                }
+                if (c == last) release();
+                float* const turn = turn0 + flip * F_COLS * F_ROW;
+                flip ^= 1;
+#pragma unroll
+                for (int i = 0; i < F_COLS; ++i) turn[i * F_ROW + lg * 32 + lane] = __uint_as_float(raw[i]);
+                // the other buffer is written next, so one barrier is enough:
+                // its readers have passed this one
+                team_sync(team);
+#pragma unroll
+                for (int i = 0; i < UNITS; ++i) {
+                    const int u = tid + 128 * i, r = u / GROUPS, group = u % GROUPS;
+                    const int row = n0 + r, m = m0 + group * 8, left = m_end - m;
+                    if (row >= x.n_end || left <= 0) continue;
+                    float v[8];
+                    turned8(turn + r * F_ROW, group, v);
+                    if constexpr (OP == UP) {
+                        float w[8], h[8], d;
+                        turned8(turn + r * F_ROW, 8 + group, w);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) h[q] = activate(p.act, v[q], d) * w[q];
+                        put8(p.out[0], row * p.out[0].ld + m, left, h);
+                        if (p.out[1].p) {
+                            put8(p.out[1], row * p.out[1].ld + m, left, v);
+                            put8(p.out[2], row * p.out[2].ld + m, left, w);
+                        }
+                    } else if constexpr (OP == DHIDDEN) {
+                        float g[8], w[8], h[8];
+                        widen8(kg[i], g);
+                        widen8(ku[i], w);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            float d;
+                            const float a = activate(p.act, g[q], d);
+                            h[q] = a * w[q];
+                            g[q] = v[q] * w[q] * d;
+                            w[q] = v[q] * a;
+                        }
+                        put8(p.out[0], row * p.out[0].ld + m, left, g);
+                        put8(p.out[1], row * p.out[1].ld + m, left, w);
+                        if (p.out[2].p) put8(p.out[2], row * p.out[2].ld + m, left, h);
+                    } else if constexpr (OP == DW) {
+                        const Out& o = p.out[x.j];
+                        put8_grad(o, x.e * o.stride + row * o.ld + m, left, p.out_f32, p.accumulate, v);
+                    } else {
+                        put8(p.out[0], row * p.out[0].ld + m, left, v);
+                    }
+                }
+            }
+            if (x.steps) acc ^= 1;
+        }
+    }
+
+    tc_fence_before();
+    cluster_sync_all();      // no CTA leaves while its pair may still touch it
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                     "r"(F_TMEM_COLS)
+                     : "memory");
+    }
+}
+
+// A tensor that TMA cannot read, to dense rows of ld elements (a multiple of 8).
+__global__ void __launch_bounds__(256)
+    dense_kernel(const __nv_bfloat16* src, int64_t matrices, int64_t rows, int64_t cols, int64_t ld_src,
+                 int64_t stride_src, __nv_bfloat16* dst, int64_t ld) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    for (int64_t r = blockIdx.x; r < matrices * rows; r += gridDim.x) {
+        const int64_t e = r / rows;
+        const __nv_bfloat16* const from = src + e * stride_src + (r - e * rows) * ld_src;
+        for (int64_t c = threadIdx.x; c < cols; c += 256) dst[r * ld + c] = from[c];
+    }
+}
+
+// ------------------------------------------------------------------- host
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// An operand as the products read it: its own memory, or a dense copy in the
+// workspace.
+struct Operand {
+    const void* p;
+    int64_t matrices, rows, cols, ld, stride;
+    size_t copy = 0;         // offset of the copy
+    bool copied = false;
+};
+
+bool tma_reads(const Operand& o) {
+    return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && (o.rows <= 1 || (o.ld % 8 == 0 && o.ld >= o.cols)) &&
+           (o.matrices <= 1 || o.stride % 8 == 0);
+}
+
+struct Space {
+    size_t bytes = 0;
+    size_t take(size_t n) {
+        const size_t at = bytes;
+        bytes += align256(n);
+        return at;
+    }
+    Operand operand(const void* p, int64_t matrices, int64_t rows, int64_t cols, int64_t ld, int64_t stride) {
+        // one matrix for all experts stays one
+        Operand o{p, stride == 0 ? 1 : matrices, rows, cols, ld, stride};
+        if (rows && !tma_reads(o)) {
+            o.copied = true;
+            const int64_t wide = ceil_div(cols, 8) * 8;
+            o.copy = take(size_t(o.matrices) * rows * wide * 2);
+        }
+        return o;
+    }
+};
+
+cudaError_t settle(Operand& o, char* base, cudaStream_t s) {
+    if (!o.copied) return cudaSuccess;
+    auto* const to = reinterpret_cast<__nv_bfloat16*>(base + o.copy);
+    const int64_t ld = ceil_div(o.cols, 8) * 8, rows = o.matrices * o.rows;
+    const cudaError_t e = launch_kernel(dense_kernel, dim3(static_cast<unsigned>(rows < 152 * 8 ? rows : 152 * 8)),
+                                        dim3(256), 0, s, static_cast<const __nv_bfloat16*>(o.p), o.matrices,
+                                        o.rows, o.cols, o.ld, o.stride, to, ld);
+    o.p = to;
+    o.ld = ld;
+    o.stride = o.rows * ld;
+    return e;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+// A map of 64 x 64 boxes; zeros come back past a matrix's rows and columns.
+bool encode(CUtensorMap* tm, const Operand& o) {
+    if (!encoder()) return false;
+    const int64_t ld = o.rows > 1 ? o.ld : ceil_div(o.cols, 8) * 8;
+    const int64_t stride = o.matrices > 1 ? o.stride : o.rows * ld;
+    cuuint64_t dims[3] = {cuuint64_t(o.cols), cuuint64_t(o.rows), cuuint64_t(o.matrices)};
+    cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride) * 2};
+    cuuint32_t box[3] = {64, 64, 1}, el[3] = {1, 1, 1};
+    return encoder()(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, el,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+Out output(void* p, int64_t ld, int64_t rows, int64_t matrices = 1, int64_t stride = 0, int size = 2) {
+    return Out{p, ld, stride,
+               reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld * size % 16 == 0) &&
+                   (matrices <= 1 || stride * size % 16 == 0)};
+}
+
+using Kernel = void (*)(FfnLaunch);
+
+cudaError_t launch_op(Op op, const FfnLaunch& p, int64_t items, cudaStream_t s) {
+    static const Kernel kernel[5] = {gated_ffn_kernel<UP>, gated_ffn_kernel<DOWN>, gated_ffn_kernel<DHIDDEN>,
+                                     gated_ffn_kernel<DX>, gated_ffn_kernel<DW>};
+    static int attr_done[64] = {0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+        for (int i = 0; i < 5; ++i) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(kernel[i], cudaFuncAttributeMaxDynamicSharedMemorySize, F_SMEM);
+            if (e != cudaSuccess) return e;
+        }
+        if (dev >= 0 && dev < 64) attr_done[dev] = 1;
+    }
+    const int pairs = static_cast<int>(items < F_PAIRS ? items : F_PAIRS);
+    return launch_kernel(kernel[op], dim3(2 * pairs), dim3(F_THREADS), F_SMEM, s, p);
+}
+
+FfnLaunch common(const int32_t* offsets, int64_t rows, int64_t experts, int act) {
+    FfnLaunch p = {};
+    p.offsets = offsets;
+    p.rows = rows;
+    p.experts = static_cast<int32_t>(experts);
+    p.act = act;
+    p.tile_n = 256;
+    p.wait_limit_ns = wait_limit_ns();
+    return p;
+}
+
+// Tiles of 256 rows that the experts' rows can make, at most.
+int64_t row_tiles(int64_t rows, int64_t experts, int tile_n) { return rows / tile_n + experts; }
+
+struct Forward {
+    Space space;
+    Operand x, gate, up, down, h;
+    size_t h_at;
+};
+Forward plan(const muon_gated_ffn_args& a) {
+    Forward f;
+    const int64_t ld_h = ceil_div(a.inner, 8) * 8;
+    f.h_at = f.space.take(size_t(a.rows) * ld_h * 2);
+    f.h = Operand{nullptr, 1, a.rows, a.inner, ld_h, 0};
+    f.x = f.space.operand(a.x, 1, a.rows, a.hidden, a.ld_x, 0);
+    f.gate = f.space.operand(a.w_gate, a.experts, a.inner, a.hidden, a.ld_gate, a.stride_gate);
+    f.up = f.space.operand(a.w_up, a.experts, a.inner, a.hidden, a.ld_up, a.stride_up);
+    f.down = f.space.operand(a.w_down, a.experts, a.hidden, a.inner, a.ld_down, a.stride_down);
+    return f;
+}
+
+struct Backward {
+    Space space;
+    Operand dy, x, gate, up, down, dg, du, h;
+    size_t d_at[3] = {0, 0, 0};      // dg, du, h where the caller gives none
+    bool own[3] = {false, false, false};
+};
+Backward plan(const muon_gated_ffn_grad_args& a) {
+    Backward b;
+    const int64_t ld = ceil_div(a.inner, 8) * 8;
+    void* const given[3] = {a.dgate, a.dup, a.h};
+    Operand* const d[3] = {&b.dg, &b.du, &b.h};
+    for (int i = 0; i < 3; ++i) {
+        const bool needed = i < 2 || a.dw_down;
+        b.own[i] = !given[i] && needed;
+        if (b.own[i]) {
+            b.d_at[i] = b.space.take(size_t(a.rows) * ld * 2);
+            *d[i] = Operand{nullptr, 1, a.rows, a.inner, ld, 0};
+        } else {
+            // copied after DHIDDEN has written it
+            const bool read = i == 2 ? a.dw_down != nullptr : a.dx || (i ? a.dw_up : a.dw_gate);
+            if (read) *d[i] = b.space.operand(given[i], 1, a.rows, a.inner, a.ld_d, 0);
+            else *d[i] = Operand{given[i], 1, a.rows, a.inner, a.ld_d, 0};
+        }
+    }
+    b.dy = b.space.operand(a.dy, 1, a.rows, a.hidden, a.ld_dy, 0);
+    if (a.dw_gate || a.dw_up) b.x = b.space.operand(a.x, 1, a.rows, a.hidden, a.ld_x, 0);
+    if (a.dx) {
+        b.gate = b.space.operand(a.w_gate, a.experts, a.inner, a.hidden, a.ld_gate, a.stride_gate);
+        b.up = b.space.operand(a.w_up, a.experts, a.inner, a.hidden, a.ld_up, a.stride_up);
+    }
+    b.down = b.space.operand(a.w_down, a.experts, a.hidden, a.inner, a.ld_down, a.stride_down);
+    return b;
+}
+
+#define RETURN_IF_CUDA(expr)                       \
+    do {                                           \
+        const cudaError_t e_ = (expr);             \
+        if (e_ != cudaSuccess) return e_;          \
+    } while (0)
+
+}  // namespace
+
+size_t gated_ffn_workspace(const muon_gated_ffn_args& a) { return plan(a).space.bytes; }
+size_t gated_ffn_grad_workspace(const muon_gated_ffn_grad_args& a) { return plan(a).space.bytes; }
+
+cudaError_t launch_gated_ffn(const muon_gated_ffn_args& a, void* ws, cudaStream_t s) {
+    if (a.rows == 0) return cudaSuccess;
+    Forward f = plan(a);
+    char* const base = static_cast<char*>(ws);
+    f.h.p = base + f.h_at;
+    for (Operand* o : {&f.x, &f.gate, &f.up, &f.down}) RETURN_IF_CUDA(settle(*o, base, s));
+    FfnLaunch p = common(a.offsets, a.rows, a.experts, a.activation);
+    p.m[0] = static_cast<int32_t>(a.inner);
+    p.k = static_cast<int32_t>(a.hidden);
+    p.a_by_expert[0] = f.gate.matrices > 1;
+    p.a_by_expert[1] = f.up.matrices > 1;
+    p.out[0] = output(base + f.h_at, f.h.ld, a.rows);
+    p.out[1] = output(a.gate, a.ld_kept, a.rows);
+    p.out[2] = output(a.up, a.ld_kept, a.rows);
+    if (!encode(&p.maps[0].a, f.gate) || !encode(&p.maps[1].a, f.up) || !encode(&p.maps[0].b, f.x))
+        return cudaErrorInvalidValue;
+    const int64_t rt = row_tiles(a.rows, a.experts, p.tile_n);
+    RETURN_IF_CUDA(launch_op(UP, p, rt * ceil_div(a.inner, 128), s));
+    p.m[0] = static_cast<int32_t>(a.hidden);
+    p.k = static_cast<int32_t>(a.inner);
+    p.a_by_expert[0] = f.down.matrices > 1;
+    p.out[0] = output(a.y, a.ld_y, a.rows);
+    if (!encode(&p.maps[0].a, f.down) || !encode(&p.maps[0].b, f.h)) return cudaErrorInvalidValue;
+    return launch_op(DOWN, p, rt * ceil_div(a.hidden, 256), s);
+}
+
+cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, cudaStream_t s) {
+    Backward b = plan(a);
+    char* const base = static_cast<char*>(ws);
+    Operand* const d[3] = {&b.dg, &b.du, &b.h};
+    const bool grads = a.dw_gate || a.dw_up || a.dw_down;
+    FfnLaunch p = common(a.offsets, a.rows, a.experts, a.activation);
+    const int64_t rt = row_tiles(a.rows, a.experts, p.tile_n);
+    if (a.rows) {
+        for (Operand* o : {&b.dy, &b.x, &b.gate, &b.up, &b.down}) RETURN_IF_CUDA(settle(*o, base, s));
+        p.m[0] = static_cast<int32_t>(a.inner);
+        p.k = static_cast<int32_t>(a.hidden);
+        p.a_by_expert[0] = b.down.matrices > 1;
+        p.gate = a.gate;
+        p.up = a.up;
+        p.ld_kept = a.ld_kept;
+        p.kept_vec = output(const_cast<void*>(a.gate), a.ld_kept, a.rows).vec &&
+                     output(const_cast<void*>(a.up), a.ld_kept, a.rows).vec;
+        for (int i = 0; i < 3; ++i) {
+            if (b.own[i]) d[i]->p = base + b.d_at[i];
+            p.out[i] = output(const_cast<void*>(d[i]->p), d[i]->ld, a.rows);
+        }
+        if (!encode(&p.maps[0].a, b.down) || !encode(&p.maps[0].b, b.dy)) return cudaErrorInvalidValue;
+        RETURN_IF_CUDA(launch_op(DHIDDEN, p, rt * ceil_div(a.inner, 256), s));
+        for (Operand* o : d) RETURN_IF_CUDA(settle(*o, base, s));
+        if (a.dx) {
+            p.m[0] = static_cast<int32_t>(a.hidden);
+            p.k = static_cast<int32_t>(a.inner);
+            p.a_by_expert[0] = b.gate.matrices > 1;
+            p.a_by_expert[1] = b.up.matrices > 1;
+            p.out[0] = output(a.dx, a.ld_dx, a.rows);
+            if (!encode(&p.maps[0].a, b.gate) || !encode(&p.maps[1].a, b.up) || !encode(&p.maps[0].b, b.dg) ||
+                !encode(&p.maps[1].b, b.du))
+                return cudaErrorInvalidValue;
+            RETURN_IF_CUDA(launch_op(DX, p, rt * ceil_div(a.hidden, 256), s));
+        }
+    }
+    if (!grads) return cudaSuccess;
+    p.m[0] = static_cast<int32_t>(a.hidden);
+    p.m[1] = static_cast<int32_t>(a.inner);
+    p.out_f32 = a.g_dtype == MUON_F32;
+    p.accumulate = a.accumulate;
+    const int size = p.out_f32 ? 4 : 2;
+    p.out[0] = output(a.dw_gate, a.ld_dw_gate, a.inner, a.experts, a.stride_dw_gate, size);
+    p.out[1] = output(a.dw_up, a.ld_dw_up, a.inner, a.experts, a.stride_dw_up, size);
+    p.out[2] = output(a.dw_down, a.ld_dw_down, a.hidden, a.experts, a.stride_dw_down, size);
+    int64_t items = 0;
+    const Operand* const left[3] = {&b.x, &b.x, &b.h};
+    const Operand* const right[3] = {&b.dg, &b.du, &b.dy};
+    for (int j = 0; j < 3; ++j) {
+        p.a_by_expert[j] = 0;
+        if (!p.out[j].p) continue;
+        p.products |= 1 << j;
+        const int64_t m = j == 2 ? a.inner : a.hidden, n = j == 2 ? a.hidden : a.inner;
+        items += a.experts * ceil_div(m, 256) * ceil_div(n, p.tile_n);
+        if (a.rows && (!encode(&p.maps[j].a, *left[j]) || !encode(&p.maps[j].b, *right[j])))
+            return cudaErrorInvalidValue;
+    }
+    return launch_op(DW, p, items, s);
+}
+
+cudaError_t ffn_error_word(void** word) { return cudaGetSymbolAddress(word, g_ffn_err); }
+
+}  // namespace ops
+}  // namespace muon

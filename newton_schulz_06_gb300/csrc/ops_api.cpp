@@ -1,6 +1,7 @@
 // C entry points of the operators of a block's training step (last section
 // of include/muon.h): argument checks, then the launch.  Every check runs
 // before any CUDA call.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 
@@ -120,6 +121,63 @@ int check_route(const Err& err, int64_t tokens, int64_t experts, int64_t k, int 
     if (experts < 1 || experts > 1024) return err.bad("experts out of range (1 .. 1024)");
     if (k < 1 || k > 32 || k > experts) return err.bad("k out of range (1 .. min(experts, 32))");
     if (tokens < 0 || tokens > MAX_ROWS / k) return err.bad("tokens out of range");
+    return MUON_OK;
+}
+
+// Rows, widths, experts and the number of tiles of a gated feed-forward block.
+int check_ffn(const Err& err, int64_t rows, int64_t hidden, int64_t inner, int64_t experts,
+              const int32_t* offsets, int activation) {
+    constexpr int64_t WIDEST = 262144;
+    if (rows < 0 || rows > MAX_ROWS - 256) return err.bad("rows out of range");
+    if (hidden < 1 || hidden > WIDEST) return err.bad("hidden out of range");
+    if (inner < 1 || inner > WIDEST) return err.bad("inner out of range");
+    if (experts < 1 || experts > 1024) return err.bad("experts out of range (1 .. 1024)");
+    if (!offsets && experts != 1) return err.bad("experts without offsets");
+    if (activation < MUON_ACT_SILU || activation > MUON_ACT_GELU_TANH) return err.bad("unknown activation");
+    // the kernels count tiles of 32 rows and 128 columns, and of 32 x 256, in 32 bits
+    const int64_t wide = hidden > inner ? hidden : inner;
+    if ((rows / 32 + experts) * ops::ceil_div(wide, 128) > (int64_t(1) << 30) ||
+        experts * ops::ceil_div(wide, 256) * ops::ceil_div(wide, 32) > (int64_t(1) << 28))
+        return err.fail(MUON_ERR_UNSUPPORTED, "too many tiles");
+    return check_vector(err, "offsets", offsets, MUON_F32);
+}
+
+// A matrix an expert, or one for all (stride 0).
+int check_weights(const Err& err, const char* name, const void* p, int64_t n, int64_t k, int64_t ld,
+                  int64_t experts, int64_t stride) {
+    RETURN_IF(check_tensor(err, name, p, MUON_BF16, n, k, ld, true));
+    if (experts > 1 && stride < 0) return err.bad(name, "has a negative stride");
+    return MUON_OK;
+}
+int check_grads(const Err& err, const char* name, const void* p, int dtype, int64_t n, int64_t k, int64_t ld,
+                int64_t experts, int64_t stride) {
+    if (!p) return MUON_OK;
+    RETURN_IF(check_tensor(err, name, p, dtype, n, k, ld, false));
+    if (experts > 1 && stride < (n > 1 ? (n - 1) * ld : 0) + k) return err.bad(name, "has too small a stride");
+    return MUON_OK;
+}
+
+int check_forward(const Err& err, const muon_gated_ffn_args* a) {
+    if (!a) return err.bad("args is NULL");
+    return check_ffn(err, a->rows, a->hidden, a->inner, a->experts, a->offsets, a->activation);
+}
+int check_backward(const Err& err, const muon_gated_ffn_grad_args* a) {
+    if (!a) return err.bad("args is NULL");
+    RETURN_IF(check_ffn(err, a->rows, a->hidden, a->inner, a->experts, a->offsets, a->activation));
+    if (!dtype_ok(a->g_dtype)) return err.bad("unknown element type");
+    return MUON_OK;
+}
+
+int check_rotary_tensor(const Err& err, const char* name, const muon_rotary_tensor& t, int dtype,
+                        int64_t tokens) {
+    if (t.heads < 0 || t.heads > 65536) return err.bad(name, "has heads out of range");
+    if (t.heads == 0 || tokens == 0) return MUON_OK;
+    if (!t.x || !t.y) return err.bad(name, "is NULL");
+    if (!aligned(t.x, dtype) || !aligned(t.y, dtype)) return err.bad(name, "is not aligned to its elements");
+    if (t.x_batch < 0 || t.x_seq < 0 || t.x_head < 0 || t.y_batch < 0 || t.y_seq < 0 || t.y_head < 0)
+        return err.bad(name, "has a negative stride");
+    if (t.x == t.y && (t.x_batch != t.y_batch || t.x_seq != t.y_seq || t.x_head != t.y_head))
+        return err.bad(name, "is written in place with other strides");
     return MUON_OK;
 }
 
@@ -287,6 +345,147 @@ MUON_API int muon_route_grad(const muon_route_grad_args* a, void* cuda_stream, c
         return err.bad("dlogits is logits with another leading dimension");
     if (a->tokens == 0) return MUON_OK;
     return err.done(ops::launch_route_grad(*a, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+MUON_API int muon_gated_ffn_workspace(const muon_gated_ffn_args* a, size_t* bytes) {
+    const Err err{nullptr, 0};
+    if (!bytes) return MUON_ERR_INVALID_ARG;
+    RETURN_IF(check_forward(err, a));
+    *bytes = ops::gated_ffn_workspace(*a);
+    return MUON_OK;
+}
+
+MUON_API int muon_gated_ffn(const muon_gated_ffn_args* a, void* ws, size_t bytes, void* cuda_stream,
+                            char* err_buf, size_t err_len) {
+    const Err err{err_buf, err_len};
+    RETURN_IF(check_forward(err, a));
+    RETURN_IF(check_tensor(err, "x", a->x, MUON_BF16, a->rows, a->hidden, a->ld_x, true));
+    RETURN_IF(check_weights(err, "w_gate", a->w_gate, a->inner, a->hidden, a->ld_gate, a->experts, a->stride_gate));
+    RETURN_IF(check_weights(err, "w_up", a->w_up, a->inner, a->hidden, a->ld_up, a->experts, a->stride_up));
+    RETURN_IF(check_weights(err, "w_down", a->w_down, a->hidden, a->inner, a->ld_down, a->experts, a->stride_down));
+    RETURN_IF(check_tensor(err, "y", a->y, MUON_BF16, a->rows, a->hidden, a->ld_y, false));
+    if (!a->gate != !a->up) return err.bad("one of gate and up without the other");
+    if (a->gate) {
+        RETURN_IF(check_tensor(err, "gate", a->gate, MUON_BF16, a->rows, a->inner, a->ld_kept, false));
+        RETURN_IF(check_tensor(err, "up", a->up, MUON_BF16, a->rows, a->inner, a->ld_kept, false));
+    }
+    RETURN_IF(check_workspace(err, ws, bytes, ops::gated_ffn_workspace(*a)));
+    return err.done(ops::launch_gated_ffn(*a, ws, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+MUON_API int muon_gated_ffn_grad_workspace(const muon_gated_ffn_grad_args* a, size_t* bytes) {
+    const Err err{nullptr, 0};
+    if (!bytes) return MUON_ERR_INVALID_ARG;
+    RETURN_IF(check_backward(err, a));
+    *bytes = ops::gated_ffn_grad_workspace(*a);
+    return MUON_OK;
+}
+
+MUON_API int muon_gated_ffn_grad(const muon_gated_ffn_grad_args* a, void* ws, size_t bytes, void* cuda_stream,
+                                 char* err_buf, size_t err_len) {
+    const Err err{err_buf, err_len};
+    RETURN_IF(check_backward(err, a));
+    const bool x_grads = a->dw_gate || a->dw_up;
+    RETURN_IF(check_tensor(err, "dy", a->dy, MUON_BF16, a->rows, a->hidden, a->ld_dy, true));
+    if (x_grads) RETURN_IF(check_tensor(err, "x", a->x, MUON_BF16, a->rows, a->hidden, a->ld_x, true));
+    RETURN_IF(check_tensor(err, "gate", a->gate, MUON_BF16, a->rows, a->inner, a->ld_kept, true));
+    RETURN_IF(check_tensor(err, "up", a->up, MUON_BF16, a->rows, a->inner, a->ld_kept, true));
+    if (a->dx) {
+        RETURN_IF(check_weights(err, "w_gate", a->w_gate, a->inner, a->hidden, a->ld_gate, a->experts,
+                                a->stride_gate));
+        RETURN_IF(check_weights(err, "w_up", a->w_up, a->inner, a->hidden, a->ld_up, a->experts, a->stride_up));
+        RETURN_IF(check_tensor(err, "dx", a->dx, MUON_BF16, a->rows, a->hidden, a->ld_dx, false));
+    }
+    RETURN_IF(check_weights(err, "w_down", a->w_down, a->hidden, a->inner, a->ld_down, a->experts, a->stride_down));
+    RETURN_IF(check_grads(err, "dw_gate", a->dw_gate, a->g_dtype, a->inner, a->hidden, a->ld_dw_gate, a->experts,
+                          a->stride_dw_gate));
+    RETURN_IF(check_grads(err, "dw_up", a->dw_up, a->g_dtype, a->inner, a->hidden, a->ld_dw_up, a->experts,
+                          a->stride_dw_up));
+    RETURN_IF(check_grads(err, "dw_down", a->dw_down, a->g_dtype, a->hidden, a->inner, a->ld_dw_down, a->experts,
+                          a->stride_dw_down));
+    void* const made[3] = {a->dgate, a->dup, a->h};
+    for (const void* m : made)
+        if (m) RETURN_IF(check_tensor(err, "dgate, dup or h", m, MUON_BF16, a->rows, a->inner, a->ld_d, false));
+    RETURN_IF(check_workspace(err, ws, bytes, ops::gated_ffn_grad_workspace(*a)));
+    return err.done(ops::launch_gated_ffn_grad(*a, ws, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+MUON_API int muon_rotary(const muon_rotary_args* a, void* cuda_stream, char* err_buf, size_t err_len) {
+    const Err err{err_buf, err_len};
+    if (!a) return err.bad("args is NULL");
+    if (!dtype_ok(a->x_dtype)) return err.bad("unknown element type");
+    if (a->layout != MUON_ROTARY_HALF && a->layout != MUON_ROTARY_INTERLEAVED) return err.bad("unknown layout");
+    if (a->pairs < 1 || a->pairs > 256) return err.bad("pairs out of range (1 .. 256)");
+    if (a->head < 2 * a->pairs || a->head > 65536) return err.bad("head out of range (2 * pairs .. 65536)");
+    if (a->batch < 0 || a->seq < 0 || a->batch > MAX_ROWS || a->seq > MAX_ROWS ||
+        a->batch * a->seq > MAX_ROWS)
+        return err.bad("batch or seq out of range");
+    if (!std::isfinite(a->scale)) return err.bad("scale is not finite");
+    if (!a->turns) return err.bad("turns is NULL");
+    RETURN_IF(check_rotary_tensor(err, "q", a->q, a->x_dtype, a->batch * a->seq));
+    RETURN_IF(check_rotary_tensor(err, "k", a->k, a->x_dtype, a->batch * a->seq));
+    if (a->positions) {
+        if (a->stride_positions < 0) return err.bad("positions has a negative stride");
+        if (reinterpret_cast<uintptr_t>(a->positions) % (a->positions_64 ? 8 : 4) != 0)
+            return err.bad("positions is not aligned to its elements");
+    }
+    if (a->q.heads + a->k.heads > 65536) return err.bad("heads out of range");
+    if (a->batch * a->seq == 0 || a->q.heads + a->k.heads == 0) return MUON_OK;
+    return err.done(ops::launch_rotary(*a, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+MUON_API int muon_rotary_frequencies(int64_t pairs, double base, int scaling, double factor, double original,
+                                     double fast, double slow, uint64_t* turns, float* scale, char* err_buf,
+                                     size_t err_len) {
+    const Err err{err_buf, err_len};
+    if (!turns || !scale) return err.bad("turns or scale is NULL");
+    if (pairs < 1 || pairs > 256) return err.bad("pairs out of range (1 .. 256)");
+    if (!(base > 1.0) || !std::isfinite(base)) return err.bad("base is not above 1");
+    if (scaling < MUON_ROTARY_PLAIN || scaling > MUON_ROTARY_YARN) return err.bad("unknown scaling");
+    if (!(factor >= 1.0) || !std::isfinite(factor)) return err.bad("factor is below 1");
+    if (scaling == MUON_ROTARY_NTK) {
+        if (pairs < 2) return err.bad("pairs must be 2 or more with this scaling");
+        base *= std::pow(factor, double(pairs) / double(pairs - 1));
+    }
+    constexpr double TURN = 6.283185307179586476925;
+    double low = 0.0, high = 0.0;
+    if (scaling == MUON_ROTARY_YARN) {
+        if (!(original >= 1.0) || !std::isfinite(original)) return err.bad("original is below 1");
+        if (!(slow > 0.0) || !(fast > slow) || !std::isfinite(fast)) return err.bad("need 0 < slow < fast");
+        // the pair that turns so many times in the original positions
+        const auto place = [&](double n) { return double(pairs) * std::log(original / (n * TURN)) / std::log(base); };
+        low = std::fmax(std::floor(place(fast)), 0.0);
+        high = std::fmin(std::ceil(place(slow)), double(2 * pairs - 1));
+    }
+    for (int64_t i = 0; i < pairs; ++i) {
+        double f = std::pow(base, -double(i) / double(pairs));
+        if (scaling == MUON_ROTARY_LINEAR) f /= factor;
+        if (scaling == MUON_ROTARY_YARN) {
+            const double r = std::fmin(std::fmax((double(i) - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
+            f = f / factor * r + f * (1.0 - r);
+        }
+        turns[i] = static_cast<uint64_t>(std::ldexp(f / TURN, 64));
+    }
+    *scale = scaling == MUON_ROTARY_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+    return MUON_OK;
+}
+
+MUON_API int muon_dropout(const muon_dropout_args* a, void* cuda_stream, char* err_buf, size_t err_len) {
+    const Err err{err_buf, err_len};
+    if (!a) return err.bad("args is NULL");
+    RETURN_IF(check_shape(err, a->rows, a->cols));
+    if (!dtype_ok(a->x_dtype)) return err.bad("unknown element type");
+    if (!(a->p >= 0.0 && a->p <= 1.0)) return err.bad("p out of range (0 .. 1)");
+    RETURN_IF(check_tensor(err, "x", a->x, a->x_dtype, a->rows, a->cols, a->ld_x, true));
+    if (a->residual)
+        RETURN_IF(check_tensor(err, "residual", a->residual, a->x_dtype, a->rows, a->cols, a->ld_r, true));
+    RETURN_IF(check_tensor(err, "y", a->y, a->x_dtype, a->rows, a->cols, a->ld_y, false));
+    if (reinterpret_cast<uintptr_t>(a->counter) % 8 != 0) return err.bad("counter is not aligned to its elements");
+    if (a->rows > 1 && a->x == a->y && a->ld_x != a->ld_y) return err.bad("y is x with another leading dimension");
+    if (a->rows > 1 && a->residual == a->y && a->ld_r != a->ld_y)
+        return err.bad("y is residual with another leading dimension");
+    if (a->rows == 0) return MUON_OK;
+    return err.done(ops::launch_dropout(*a, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 MUON_API int muon_ops_sync(void* cuda_stream, char* err_buf, size_t err_len) {

@@ -26,10 +26,17 @@ cudaError_t launch_weight_grad(const muon_weight_grad_args& a, void* ws, cudaStr
 size_t route_workspace(const muon_route_args& a);
 cudaError_t launch_route(const muon_route_args& a, void* ws, cudaStream_t s);
 cudaError_t launch_route_grad(const muon_route_grad_args& a, cudaStream_t s);
+size_t gated_ffn_workspace(const muon_gated_ffn_args& a);
+cudaError_t launch_gated_ffn(const muon_gated_ffn_args& a, void* ws, cudaStream_t s);
+size_t gated_ffn_grad_workspace(const muon_gated_ffn_grad_args& a);
+cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, cudaStream_t s);
+cudaError_t launch_rotary(const muon_rotary_args& a, cudaStream_t s);
+cudaError_t launch_dropout(const muon_dropout_args& a, cudaStream_t s);
 // Waits for the stream; *code: the device error word (DEV_ERR_*), cleared.
 cudaError_t ops_status(cudaStream_t s, int* code);
-// Device address of the layer norm's error word.
+// Device addresses of the layer norm's and the feed-forward block's error words.
 cudaError_t norm_error_word(void** word);
+cudaError_t ffn_error_word(void** word);
 // A kernel whose wait nothing satisfies: it runs out after the limit.
 cudaError_t launch_ring_timeout(unsigned long long limit_ns, cudaStream_t s);
 // Limit of the kernels' waits (MUON_WAIT_LIMIT_MS, else two seconds).

@@ -1301,10 +1301,11 @@ cudaError_t launch_weight_grad(const muon_weight_grad_args& a, void* ws, cudaStr
 
 cudaError_t ops_status(cudaStream_t s, int* code) {
     *code = 0;
-    void* words[2];
+    void* words[3];
     cudaError_t e = cudaGetSymbolAddress(&words[0], g_ops_err);
     if (e == cudaSuccess) e = norm_error_word(&words[1]);
-    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+    if (e == cudaSuccess) e = ffn_error_word(&words[2]);
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
         int c = 0;
         e = cudaMemcpyAsync(&c, words[i], sizeof(int), cudaMemcpyDeviceToHost, s);
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);

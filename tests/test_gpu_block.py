@@ -1,0 +1,614 @@
+"""The operators inside a block against their 64-bit forms.  Bounds are those
+of block_oracle: every rounding to bf16 is off by at most half a step, sums as
+the tensor cores make them, and each error is carried through what follows."""
+import math
+
+import pytest
+import torch
+
+import block_oracle as O
+from block_oracle import D, HALF, U32
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def ns():
+    import newton_schulz_06_gb300 as ns
+    return ns
+
+
+def rand(seed, *shape, scale=1.0, dtype=F32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dtype).to(DEV)
+
+
+def strided(t, lead, pad):
+    """t as a view: `lead` elements into a buffer whose rows are `pad` longer."""
+    rows, cols = t.shape
+    buf = torch.full((rows * (cols + pad) + lead + 8,), 7.0, dtype=t.dtype, device=t.device)
+    v = buf[lead:lead + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    v.copy_(t)
+    return v
+
+
+def near(got, want, bound, what):
+    """|got - want| <= bound where want is finite; NaN and infinities alike."""
+    got = got.to(D)
+    assert got.shape == want.shape, (what, got.shape, want.shape)
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), what
+    fine = torch.isfinite(want)
+    assert torch.equal(got[~fine & ~torch.isnan(want)], want[~fine & ~torch.isnan(want)]), what
+    over = fine & ((got - want).abs() > bound)
+    if bool(over.any()):
+        at = tuple(over.nonzero()[0].tolist())
+        raise AssertionError(f"{what}: {int(over.sum())} of {over.numel()} off, first at {at}: "
+                             f"{got[at].item()} for {want[at].item()}, bound {bound[at].item():.3e}")
+
+
+def close_norm(got, want, what, most=4e-3):
+    """The whole is as near as roundings of random signs leave it: error and
+    value of an output are sums over the same random terms, so that their squares'
+    ratio is the roundings' (below 2^-8.5 each, a few of them) for many outputs.
+    That of a few, where the terms may cancel, has only its bound (near)."""
+    if want.numel() < 1000:
+        return
+    off, size = (got.to(D) - want).norm().item(), want.norm().item()
+    assert off <= most * size + 1e-30, (what, off, size)
+
+
+# ----------------------------------------------------------------- dropout
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols,p", [(1, 1, 0.5), (1, 7, 0.3), (3, 8, 0.5), (64, 40, 0.1), (5, 33, 0.25),
+                                         (2, 2047, 0.9), (33, 264, 0.0), (4, 16, 1.0), (3, 100, 1e-6)])
+def test_dropout(ns, rows, cols, p, dtype):
+    x, r = rand(1, rows, cols, dtype=dtype), rand(2, rows, cols, dtype=dtype)
+    for seed, offset in ((0, 0), (123456789012345678, 987654321987), (2 ** 64 - 1, 2 ** 64 - 1)):
+        for res in (None, r):
+            want = O.dropout(x, p, seed, offset, res)
+            got = ns.dropout(x, p, seed, offset, residual=res)
+            assert got.dtype == dtype
+            # the scale, the product and the sum are rounded once each
+            size = want.abs() + (0 if res is None else 2 * res.cpu().to(D).abs())
+            near(got.cpu(), want, (3 * U32 + HALF[dtype]) * size + 1e-38, "y")
+    assert torch.equal(ns.dropout_backward(x, p, 5, 6), ns.dropout(x, p, 5, 6))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols", [40, 41, 2048])
+def test_dropout_goes_by_the_element_not_its_address(ns, cols, dtype):
+    x, r = rand(3, 29, cols, dtype=dtype), rand(4, 29, cols, dtype=dtype)
+    want = ns.dropout(x, 0.4, 11, 12, residual=r)
+    for lead, pad in ((0, 8), (1, 0), (3, 5), (8, 16), (0, 1)):
+        out = strided(torch.zeros_like(x), lead, pad)
+        base = out._base.clone()
+        got = ns.dropout(strided(x, lead, pad), 0.4, 11, 12, residual=strided(r, pad, lead), out=out)
+        assert got is out and torch.equal(got, want)
+        rest = out._base.clone()
+        rest[lead:lead + 29 * (cols + pad)].view(29, cols + pad)[:, :cols] = 0
+        base[lead:lead + 29 * (cols + pad)].view(29, cols + pad)[:, :cols] = 0
+        assert torch.equal(rest, base)                      # nothing outside the view
+    for into in (0, 1):
+        a, b = x.clone(), r.clone()
+        assert torch.equal(ns.dropout(a, 0.4, 11, 12, residual=b, out=(a, b)[into]), want)
+    row = ns.dropout(x[:1].expand(29, -1), 0.4, 11, 12)
+    assert torch.equal(row, ns.dropout(x[:1].expand(29, -1).contiguous(), 0.4, 11, 12))
+
+
+def test_dropout_of_what_is_not_finite(ns):
+    """A dropped element is 0 whatever it holds; p = 1 drops all."""
+    x = torch.full((8, 64), math.nan, device=DEV)
+    x[4:] = math.inf
+    y = ns.dropout(x, 0.5, 3, 4)
+    keep = torch.tensor(O.kept(512, 0.5, 3, 4)).view(8, 64).to(DEV)
+    assert bool((y[~keep] == 0).all()) and bool(torch.isnan(y[:4][keep[:4]]).all())
+    assert bool(torch.isinf(y[4:][keep[4:]]).all())
+    assert not ns.dropout(x, 1.0, 3, 4).any()
+    r = rand(5, 8, 64)
+    assert torch.equal(ns.dropout(x, 1.0, 3, 4, residual=r), r)
+
+
+def test_dropout_counter_is_read_by_the_kernel(ns):
+    """A captured graph whose counter moves drops other elements each time, and
+    its backward pass the same ones."""
+    x = rand(6, 64, 256)
+    step = torch.zeros(1, dtype=torch.int64, device=DEV)
+    ns.dropout(x, 0.3, 9, 100, counter=step)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = ns.dropout(x, 0.3, 9, 100, counter=step)
+        dx = ns.dropout_backward(x, 0.3, 9, 100, counter=step)
+        step += 1
+    seen = []
+    for i in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ns.dropout(x, 0.3, 9, 100 + i)) and torch.equal(dx, y)
+        seen.append(y.clone())
+    assert not torch.equal(seen[0], seen[1]) and not torch.equal(seen[1], seen[2])
+    # offsets add up modulo 2^64
+    step.fill_(-1)
+    assert torch.equal(ns.dropout(x, 0.3, 9, 0, counter=step), ns.dropout(x, 0.3, 9, 2 ** 64 - 1))
+
+
+def test_dropout_share_and_mean(ns):
+    """Of 2^24 elements the kept share is p's to six deviations, in every place
+    of a block and across blocks."""
+    n, p = 1 << 24, 0.1
+    y = ns.dropout(torch.ones(4096, 4096, device=DEV), p, 77, 88)
+    keep = (y != 0).view(-1, 8)
+    limit = math.floor(p * 65536 + 0.5)
+    q = 1 - limit / 65536
+    dev = math.sqrt(q * (1 - q) / (n / 8))
+    assert ((keep.double().mean(0) - q).abs() < 6 * dev).all()
+    assert abs(keep.double().mean().item() - q) < 6 * dev / math.sqrt(8)
+    assert abs((keep[1:] & keep[:-1]).double().mean().item() - q * q) < 6 * math.sqrt(q * q * 2 / n)
+    assert (y[y != 0] == torch.tensor(65536 / (65536 - limit), dtype=F32)).all()
+
+
+def test_dropout_past_32_bits(ns):
+    """The last rows of more than 2^32 elements get the numbers of their place."""
+    rows, cols = (1 << 22) + 5, 1040
+    x = torch.ones(rows, cols, dtype=BF, device=DEV)
+    y = ns.dropout(x, 0.5, 21, 22, out=x)
+    for r in (0, 4130000, rows - 1):
+        first = r * cols // 8
+        keep = []
+        for b in range(first, first + cols // 8):
+            for w in O.philox((b & 0xFFFFFFFF, b >> 32, 22, 0), (21, 0)):
+                keep += [(w & 0xFFFF) >= 32768, (w >> 16) >= 32768]
+        assert torch.equal(y[r].cpu() != 0, torch.tensor(keep))
+    del x, y
+    torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ rotary
+
+def positions_of(batch, seq, positions, offset):
+    at = torch.arange(seq, device=DEV)[None] if positions is None else positions.long().view(-1, seq)
+    return at.expand(batch, seq) + offset
+
+
+def check_rotary(ns, x, got, plan_args, layout, positions, offset, inverse, what):
+    batched = x if x.dim() == 4 else x[None]
+    freq, scale = O.frequencies(**plan_args)
+    want, bound = O.rotary(batched, positions_of(batched.shape[0], batched.shape[1], positions, offset),
+                           plan_args["dim"], freq, scale, layout, inverse)
+    near(got if x.dim() == 4 else got[None], want, bound, what)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("batch,seq,heads,kheads,head,dim", [
+    (1, 1, 1, 1, 2, 2), (1, 3, 32, 4, 128, 128), (2, 37, 3, 1, 192, 64), (3, 5, 2, 2, 100, 74),
+    (1, 130, 1, 7, 64, 64), (2, 9, 16, 16, 66, 66), (1, 1, 128, 1, 512, 512), (1, 700, 2, 1, 96, 32),
+    (5, 1, 5, 3, 130, 6)])
+def test_rotary(ns, batch, seq, heads, kheads, head, dim, layout, dtype):
+    q, k = rand(10, batch, seq, heads, head, dtype=dtype), rand(11, batch, seq, kheads, head, dtype=dtype)
+    plan = ns.RotaryPlan(dim, layout=layout)
+    args = dict(dim=dim)
+    for inverse, turn in ((False, ns.rotary), (True, ns.rotary_backward)):
+        yq, yk = turn(q, k, plan)
+        check_rotary(ns, q, yq, args, layout, None, 0, inverse, "q")
+        check_rotary(ns, k, yk, args, layout, None, 0, inverse, "k")
+    one, none = ns.rotary(q, None, plan, offset=77)
+    assert none is None
+    check_rotary(ns, q, one, args, layout, None, 77, False, "q alone")
+    a, b = q.clone(), k.clone()
+    ya, yb = ns.rotary(a, b, plan, offset=77, out_q=a, out_k=b)
+    assert ya is a and torch.equal(a, one)
+    if batch == 1:
+        assert torch.equal(ns.rotary(q[0], k[0], plan, offset=77)[1], yb[0])
+
+
+@pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("linear", 4.0), ("ntk", 8.0), ("yarn", 32.0),
+                                            ("yarn", 1.0)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_far_positions(ns, layout, scaling, factor):
+    """Positions up to 2^31 and below zero, in both widths."""
+    args = dict(dim=64, base=500000.0, scaling=scaling, factor=factor, original=8192)
+    plan = ns.RotaryPlan(layout=layout, **args)
+    q, k = rand(12, 2, 50, 4, 64), rand(13, 2, 50, 2, 64, dtype=F32)
+    g = torch.Generator().manual_seed(14)
+    far = torch.randint(0, 1 << 31, (2, 50), generator=g)
+    far[0, :5] = torch.tensor([0, 1, (1 << 31) - 1, -1, -(1 << 31)])
+    for positions in (far.to(DEV), far.to(torch.int32).to(DEV), far[1].to(DEV), far[:1].to(torch.int32).to(DEV)):
+        yq, yk = ns.rotary(q, k, plan, positions=positions)
+        check_rotary(ns, q, yq, args, layout, positions, 0, False, "q")
+        check_rotary(ns, k, yk, args, layout, positions, 0, False, "k")
+    # what is added to a position is added in 64 bits
+    moved = ns.rotary(q, k, plan, positions=far.to(torch.int32).to(DEV), offset=1 << 20)[0]
+    check_rotary(ns, q, moved, args, layout, far.to(DEV), 1 << 20, False, "offset")
+
+
+def test_rotary_frequencies(ns):
+    for args in (dict(dim=128), dict(dim=2), dict(dim=64, scaling="linear", factor=3.0),
+                 dict(dim=96, scaling="ntk", factor=16.0, base=1e6),
+                 dict(dim=128, scaling="yarn", factor=40.0, original=4096, fast=16.0, slow=2.0)):
+        plan = ns.RotaryPlan(**args)
+        freq, scale = O.frequencies(**args)
+        assert abs(plan.scale - scale) <= U32 * scale
+        for a, b in zip(plan.frequencies, freq):
+            assert abs(a - b) <= 2.0 ** -50 * b + 2 * math.pi * 2.0 ** -64
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_of_views(ns, layout, dtype):
+    """Transposed batches, the last values of longer heads, odd addresses, one
+    head for all, in place and not: the same bits as dense tensors, nothing
+    outside the views."""
+    plan = ns.RotaryPlan(32, layout=layout)
+    x, k = rand(15, 2, 21, 6, 32, dtype=dtype), rand(16, 2, 21, 1, 32, dtype=dtype)
+    wq, wk = ns.rotary(x, k, plan, offset=3)
+    # batch x heads x seq x head
+    t = x.transpose(1, 2).contiguous().transpose(1, 2)
+    out = torch.empty(2, 6, 21, 32, dtype=dtype, device=DEV).transpose(1, 2)
+    assert torch.equal(ns.rotary(t, k, plan, offset=3, out_q=out)[0], wq) and torch.equal(out, wq)
+    # the last 32 of 96, in place
+    for lead in (0, 1, 2):
+        buf = torch.full((2 * 21 * 6 * 96 + 8,), 5.0, dtype=dtype, device=DEV)
+        long = buf[lead:lead + 2 * 21 * 6 * 96].view(2, 21, 6, 96)
+        part = long[..., 64:]
+        part.copy_(x)
+        ns.rotary(part, k, plan, offset=3, out_q=part)
+        assert torch.equal(part, wq)
+        part.fill_(5.0)
+        assert bool((buf == 5.0).all())
+    # the keys' values beside others in a wider row
+    row = torch.full((2, 21, 71), 5.0, dtype=dtype, device=DEV)
+    kv = row[..., 39:].unflatten(-1, (1, 32))
+    kv.copy_(k)
+    assert torch.equal(ns.rotary(x, kv, plan, offset=3, out_k=kv)[1], wk)
+    assert bool((row[..., :39] == 5.0).all())
+    same = k.expand(2, 21, 4, 32)
+    assert torch.equal(ns.rotary(same, None, plan, offset=3)[0], wk.expand(2, 21, 4, 32))
+
+
+def test_rotary_gradient_is_that_of_the_rotation(ns):
+    """<dy, R x> = <R^T dy, x>, and turning back gives x where the scale is 1."""
+    for layout in ("half", "interleaved"):
+        plan = ns.RotaryPlan(64, layout=layout, scaling="yarn", factor=16.0)
+        x, dy = rand(17, 40, 3, 80), rand(18, 40, 3, 80)
+        y, dx = ns.rotary(x, None, plan)[0], ns.rotary_backward(dy, None, plan)[0]
+        a, b = (dy.double() * y.double()).sum(), (dx.double() * x.double()).sum()
+        # each of the 9600 terms is off by at most 2^-20 of its size
+        assert abs((a - b).item()) <= 2.0 ** -20 * 2 * (dy.double().abs() * y.double().abs()).sum().item() + 1e-3
+        plain = ns.RotaryPlan(64, layout=layout)
+        there = ns.rotary(x, None, plain, offset=123456)[0]
+        back = ns.rotary_backward(there, None, plain, offset=123456)[0]
+        assert (back - x).abs().max().item() <= 2.0 ** -18 * x.abs().max().item()
+
+
+def test_rotary_of_nothing(ns):
+    plan = ns.RotaryPlan(16)
+    for shape in ((0, 3, 16), (2, 0, 3, 16), (5, 0, 16)):
+        q = torch.empty(shape, device=DEV)
+        y, k = ns.rotary(q, q, plan)
+        assert y.shape == shape and k.shape == shape
+
+
+# ------------------------------------------------------- gated feed-forward
+
+def weights(seed, hidden, inner, experts=0):
+    lead = (experts,) if experts else ()
+    return (rand(seed, *lead, inner, hidden, scale=hidden ** -0.5, dtype=BF),
+            rand(seed + 1, *lead, inner, hidden, scale=hidden ** -0.5, dtype=BF),
+            rand(seed + 2, *lead, hidden, inner, scale=inner ** -0.5, dtype=BF))
+
+
+def bounds_of(counts, device=DEV):
+    return torch.tensor([0, *counts]).cumsum(0).to(torch.int32).to(device)
+
+
+def check_forward(x, w, y, saved, offsets=None, name="silu"):
+    (y64, g64, u64), (by, bg, bu) = O.ffn(x, *w, offsets, name)
+    live = ~torch.isnan(y64[:, 0])
+    for got, want, bound, what in ((y, y64, by, "y"), (saved[0], g64, bg, "g"), (saved[1], u64, bu, "u")):
+        near(got[live], want[live], bound[live], what)
+        close_norm(got[live], want[live], what)
+
+
+def check_backward(dy, x, saved, w, got, offsets=None, name="silu", before=None):
+    dtype = next(g.dtype for g in got[1:] if g is not None)
+    want, bounds = O.ffn_grad(dy, x, *saved, *w, offsets, name, dtype, before)
+    live = ~torch.isnan(want[0][:, 0])
+    near(got[0][live], want[0][live], bounds[0][live], "dx")
+    close_norm(got[0][live], want[0][live], "dx")
+    for i, what in ((1, "dw_gate"), (2, "dw_up"), (3, "dw_down")):
+        if got[i] is not None:
+            near(got[i], want[i], bounds[i], what)
+            close_norm(got[i], want[i], what)
+
+
+DENSE = [(1, 8, 8), (1, 64, 32), (5, 2048, 768), (2, 72, 136), (31, 100, 33), (33, 33, 100), (64, 256, 128),
+         (127, 264, 520), (257, 128, 256), (300, 1, 1), (1000, 520, 264), (513, 1000, 7), (700, 2056, 1032)]
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("tokens,hidden,inner", DENSE)
+def test_gated_ffn(ns, tokens, hidden, inner, name):
+    x, w = rand(20, tokens, hidden, dtype=BF), weights(21, hidden, inner)
+    y, saved = ns.gated_ffn(x, *w, activation=name)
+    check_forward(x, w, y, saved, None, name)
+    again, none = ns.gated_ffn(x, *w, activation=name, keep=False)
+    assert none is None and torch.equal(again, y)
+    dy = rand(24, tokens, hidden, scale=0.1, dtype=BF)
+    got = ns.gated_ffn_backward(dy, x, saved, *w, activation=name)
+    check_backward(dy, x, saved, w, got, None, name)
+    ns.ops_sync()
+
+
+@pytest.mark.parametrize("counts", [[5], [0], [0, 0, 0], [1, 0, 2, 63, 64, 65, 0, 200, 1], [300, 0, 0, 0],
+                                    [0, 0, 17], [128, 128, 128], [7] * 40, [600, 3], [31, 33, 255, 257]])
+@pytest.mark.parametrize("hidden,inner,dtype", [(64, 96, BF), (264, 520, F32), (100, 33, BF)])
+def test_gated_ffn_of_experts(ns, counts, hidden, inner, dtype):
+    t = sum(counts)
+    offsets = bounds_of(counts)
+    x, w = rand(30, t, hidden, dtype=BF), weights(31, hidden, inner, len(counts))
+    y, saved = ns.gated_ffn(x, *w, offsets=offsets)
+    check_forward(x, w, y, saved, offsets)
+    dy = rand(34, t, hidden, scale=0.1, dtype=BF)
+    got = ns.gated_ffn_backward(dy, x, saved, *w, offsets=offsets, dtype=dtype)
+    check_backward(dy, x, saved, w, got, offsets)
+    for e, c in enumerate(counts):
+        if c == 0:
+            assert not any(g[e].any() for g in got[1:])
+    # added to what is there
+    base = [rand(35 + i, *v.shape, dtype=dtype) for i, v in enumerate(w)]
+    into = [b.clone() for b in base]
+    more = ns.gated_ffn_backward(dy, x, saved, *w, offsets=offsets, grads=into, accumulate=True)
+    assert all(a is b for a, b in zip(more[1:], into))
+    assert torch.equal(more[0], got[0])
+    check_backward(dy, x, saved, w, more, offsets, before=base)
+    ns.ops_sync()
+
+
+def test_gated_ffn_rows_of_no_expert_stay(ns):
+    """Rows before the first and behind the last expert are not written."""
+    x, w = rand(40, 100, 64, dtype=BF), weights(41, 64, 40, 3)
+    offsets = torch.tensor([10, 40, 40, 77], dtype=torch.int32, device=DEV)
+    out = torch.full((100, 64), 3.0, dtype=BF, device=DEV)
+    y, saved = ns.gated_ffn(x, *w, offsets=offsets, out=out)
+    assert bool((y[:10] == 3).all()) and bool((y[77:] == 3).all())
+    check_forward(x, w, y, saved, offsets)
+    dy = rand(44, 100, 64, dtype=BF)
+    dx = torch.full((100, 64), 3.0, dtype=BF, device=DEV)
+    # what the rows of no expert hold is read nowhere
+    for v in (x, dy, *saved):
+        v[:10] = math.nan
+        v[77:] = math.nan
+    got = ns.gated_ffn_backward(dy, x, saved, *w, offsets=offsets, out=dx)
+    assert bool((dx[:10] == 3).all()) and bool((dx[77:] == 3).all())
+    check_backward(dy, x, saved, w, got, offsets)
+
+
+@pytest.mark.parametrize("bad", [1, 3])
+def test_gated_ffn_experts_do_not_see_each_other(ns, bad):
+    """An expert whose rows and matrices hold NaN and infinities leaves the
+    others as they are, whatever tile or step their rows share."""
+    counts = [30, 3, 61, 2, 100]
+    offsets = bounds_of(counts)
+    t, hidden, inner = sum(counts), 100, 72
+    x, w, dy = rand(50, t, hidden, dtype=BF), weights(51, hidden, inner, 5), rand(54, t, hidden, dtype=BF)
+    y, saved = ns.gated_ffn(x, *w, offsets=offsets)
+    clean = ns.gated_ffn_backward(dy, x, saved, *w, offsets=offsets)
+    a, b = offsets[bad].item(), offsets[bad + 1].item()
+    x2, dy2, w2 = x.clone(), dy.clone(), [v.clone() for v in w]
+    x2[a:b], dy2[a:b] = math.nan, math.inf
+    for v in w2:
+        v[bad] = math.nan
+    y2, saved2 = ns.gated_ffn(x2, *w2, offsets=offsets)
+    got = ns.gated_ffn_backward(dy2, x2, saved2, *w2, offsets=offsets)
+    mine = torch.zeros(t, dtype=torch.bool, device=DEV)
+    mine[a:b] = True
+    for one, two in ((y2, y), (saved2[0], saved[0]), (got[0], clean[0])):
+        assert torch.equal(one[~mine], two[~mine]) and bool(torch.isnan(one[mine]).all())
+    for one, two in zip(got[1:], clean[1:]):
+        for e in range(5):
+            assert bool(torch.isnan(one[e]).all()) if e == bad else torch.equal(one[e], two[e])
+
+
+def test_gated_ffn_offsets_out_of_order_are_limited(ns):
+    x, w = rand(60, 50, 64, dtype=BF), weights(61, 64, 40, 4)
+    offsets = torch.tensor([-5, 20, 10, 30, 2000000000], dtype=torch.int32, device=DEV)
+    y, saved = ns.gated_ffn(x, *w, offsets=offsets)
+    check_forward(x, w, y, saved, offsets)
+    dy = rand(64, 50, 64, dtype=BF)
+    check_backward(dy, x, saved, w, ns.gated_ffn_backward(dy, x, saved, *w, offsets=offsets), offsets)
+
+
+def test_gated_ffn_many_experts(ns):
+    """As many experts as a router may have, most without rows."""
+    g = torch.Generator().manual_seed(70)
+    counts = torch.randint(0, 4, (1024,), generator=g).tolist()
+    offsets = bounds_of(counts)
+    x, w = rand(71, sum(counts), 64, dtype=BF), weights(72, 64, 32, 1024)
+    y, saved = ns.gated_ffn(x, *w, offsets=offsets)
+    check_forward(x, w, y, saved, offsets)
+    dy = rand(75, sum(counts), 64, dtype=BF)
+    check_backward(dy, x, saved, w, ns.gated_ffn_backward(dy, x, saved, *w, offsets=offsets), offsets)
+
+
+@pytest.mark.parametrize("experts", [0, 3])
+def test_gated_ffn_of_views(ns, experts):
+    """Rows and matrices at any address and stride give the same bits, and
+    nothing is written outside the views."""
+    t, hidden, inner = 150, 104, 72
+    offsets = bounds_of([50, 0, 100]) if experts else None
+    x, dy, w = rand(80, t, hidden, dtype=BF), rand(81, t, hidden, dtype=BF), weights(82, hidden, inner, experts)
+    y, saved = ns.gated_ffn(x, *w, offsets=offsets)
+    want = ns.gated_ffn_backward(dy, x, saved, *w, offsets=offsets)
+
+    def wide(v, lead, pad):
+        if v.dim() == 2:
+            return strided(v, lead, pad)
+        e, r, c = v.shape
+        buf = torch.full((lead + e * (r + 1) * (c + pad) + 8,), 7.0, dtype=v.dtype, device=DEV)
+        out = buf[lead:lead + e * (r + 1) * (c + pad)].view(e, r + 1, c + pad)[:, :r, :c]
+        out.copy_(v)
+        return out
+
+    for lead, pad in ((1, 0), (3, 5), (8, 8), (0, 1)):
+        x2, dy2, w2 = wide(x, lead, pad), wide(dy, lead, pad), [wide(v, lead, pad) for v in w]
+        s2 = [wide(v, lead, pad) for v in saved]
+        out, dx = wide(torch.zeros_like(x), lead, pad), wide(torch.zeros_like(x), lead, pad)
+        grads = [wide(torch.zeros_like(v), lead, pad) for v in w]
+        before = [v._base.clone() for v in (out, dx, *grads)]
+        got, _ = ns.gated_ffn(x2, *w2, offsets=offsets, out=out)
+        assert torch.equal(got, y)
+        got = ns.gated_ffn_backward(dy2, x2, s2, *w2, offsets=offsets, out=dx, grads=grads)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        for v, b in zip((out, dx, *grads), before):
+            v.zero_()
+            assert torch.equal(v._base, b)
+    # rows and matrices that are one for all
+    row = ns.gated_ffn(x[:1].expand(t, -1), *w, offsets=offsets, keep=False)[0]
+    assert torch.equal(row, ns.gated_ffn(x[:1].expand(t, -1).contiguous(), *w, offsets=offsets, keep=False)[0])
+    if experts:
+        same = [v[:1].expand(3, -1, -1) for v in w]
+        full = [v.contiguous() for v in same]
+        a, sa = ns.gated_ffn(x, *same, offsets=offsets)
+        b, sb = ns.gated_ffn(x, *full, offsets=offsets)
+        assert torch.equal(a, b)
+        for one, two in zip(ns.gated_ffn_backward(dy, x, sa, *same, offsets=offsets),
+                            ns.gated_ffn_backward(dy, x, sb, *full, offsets=offsets)):
+            assert torch.equal(one, two)
+
+
+def test_gated_ffn_of_no_rows(ns):
+    w = weights(90, 64, 40)
+    x = torch.empty(0, 64, dtype=BF, device=DEV)
+    y, saved = ns.gated_ffn(x, *w)
+    assert y.shape == (0, 64) and saved[0].shape == (0, 40)
+    base = [torch.ones_like(v) for v in w]
+    got = ns.gated_ffn_backward(x, x, saved, *w, grads=[b.clone() for b in base])
+    assert not any(g.any() for g in got[1:])
+    got = ns.gated_ffn_backward(x, x, saved, *w, grads=[b.clone() for b in base], accumulate=True)
+    assert all(torch.equal(g, b) for g, b in zip(got[1:], base))
+
+
+@pytest.mark.parametrize("counts", [None, [40, 0, 1, 159]])
+def test_gated_ffn_from_a_checkpoint(ns, counts):
+    """x kept in 8 bits, with a norm's weight and bias: the gradients of w_gate
+    and w_up are those of what the checkpoint stands for."""
+    t, hidden, inner = 200, 136, 72
+    offsets = None if counts is None else bounds_of(counts)
+    w = weights(91, hidden, inner, 0 if counts is None else 4)
+    h, dy = ns.checkpoint8(rand(94, t, hidden)), rand(95, t, hidden, scale=0.1, dtype=BF)
+    gain, shift = rand(96, hidden), rand(97, hidden)
+    x64 = h.values(F32).to(D) * gain.to(D) + shift.to(D)
+    _, saved = ns.gated_ffn(x64.to(BF), *w, offsets=offsets)
+    for dtype in (BF, F32):
+        got = ns.gated_ffn_backward(dy, h, saved, *w, offsets=offsets, weight=gain, bias=shift, dtype=dtype)
+        want, bounds = O.ffn_grad(dy, x64, *saved, *w, offsets, "silu", dtype)
+        # the weight and the bias act on sums: their terms' sizes add up
+        for i in (1, 2):
+            close_norm(got[i], want[i], i)
+        near(got[0], want[0], bounds[0], "dx")
+        near(got[3], want[3], bounds[3], "dw_down")
+        into = [g.clone() for g in got[1:]]
+        twice = ns.gated_ffn_backward(dy, h, saved, *w, offsets=offsets, weight=gain, bias=shift, grads=into,
+                                      accumulate=True)
+        for a, b in zip(twice[1:], got[1:]):
+            close_norm(a, 2 * b.to(D), "added")
+    none = ns.gated_ffn_backward(dy, None, saved, *w, offsets=offsets, dtype=F32)
+    assert none[1] is None and none[2] is None and torch.equal(none[3], got[3]) and torch.equal(none[0], got[0])
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+def test_gated_ffn_gradient_is_that_of_differences(ns, name):
+    """Along a direction, the 64-bit form's difference quotient is the inner
+    product with the kernel's gradients."""
+    t, hidden, inner = 64, 48, 40
+    x, w = rand(100, t, hidden, dtype=BF), weights(101, hidden, inner)
+    dy = rand(104, t, hidden, dtype=BF)
+    g64, u64 = x.to(D) @ w[0].to(D).t(), x.to(D) @ w[1].to(D).t()
+    got = ns.gated_ffn_backward(dy, x, (g64.to(BF), u64.to(BF)), *w, activation=name, dtype=F32)
+    args = [v.to(D) for v in (x, *w)]
+    for i in range(4):
+        way = rand(105 + i, *args[i].shape).to(D)
+
+        def value(step):
+            a = list(args)
+            a[i] = a[i] + step * way
+            h = O.act(name, a[0] @ a[1].t())[0] * (a[0] @ a[2].t())
+            return ((h @ a[3].t()) * dy.to(D)).sum()
+
+        want = ((value(1e-5) - value(-1e-5)) / 2e-5).item()
+        have = (got[i].to(D) * way).sum().item()
+        # a norm-wise error of 1e-2 in the gradient, against a random direction
+        assert abs(have - want) <= 1e-2 * got[i].to(D).norm().item() * 6, (i, have, want)
+
+
+def test_gated_ffn_saturates(ns):
+    """Gates far on both sides: act(g) is g or 0 and its derivative 1 or 0."""
+    hidden, inner = 64, 32
+    x = torch.zeros(4, hidden, dtype=BF, device=DEV)
+    x[0, 0], x[1, 0], x[2, 0] = 1e4, -1e4, 1e30
+    w = [torch.zeros(inner, hidden, dtype=BF, device=DEV) for _ in range(2)]
+    w[0][:, 0], w[1][:, 0] = 1.0, 1e-3
+    wd = torch.eye(hidden, inner, dtype=BF, device=DEV)
+    for name in ("silu", "gelu", "gelu_tanh"):
+        y, saved = ns.gated_ffn(x, *w, wd, activation=name)
+        (y64, _, _), (by, _, _) = O.ffn(x, *w, wd, None, name)
+        near(y, y64, by, name)
+        got = ns.gated_ffn_backward(x, x, saved, *w, wd, activation=name)
+        assert all(bool(torch.isfinite(g.float()[:2]).all()) for g in got[:1])
+
+
+def test_run_of_a_block(ns):
+    """The operators as a block's step uses them, in eager order and captured:
+    norm, rotary, dropout with a residual, router, experts, and back."""
+    T, H, E, K, inner = 96, 64, 8, 2, 48
+    plan = ns.RotaryPlan(32)
+    w = weights(110, H, inner, E)
+    x, dout = rand(113, T, H, dtype=BF), rand(114, T, H, scale=0.1, dtype=BF)
+    router = rand(115, E, H, scale=0.1)
+    step = torch.zeros(1, dtype=torch.int64, device=DEV)
+
+    def run():
+        y, rstd, saved8 = ns.layer_norm_checkpoint(x)
+        q, _ = ns.rotary(y.view(T, 2, 32), None, plan)
+        a = ns.dropout(q.reshape(T, H), 0.2, 1, counter=step, residual=x)
+        r = ns.route(a.float() @ router.t(), K)
+        order = torch.argsort(r.indices.flatten(), stable=True)
+        token = order // K
+        rows = a[token]
+        f, kept = ns.gated_ffn(rows, *w, offsets=r.offsets)
+        df = dout[token]
+        drows, *dw = ns.gated_ffn_backward(df, rows, kept, *w, offsets=r.offsets)
+        da = torch.zeros(T, H, device=DEV).index_add_(0, token, drows.float()).to(BF)
+        dq = ns.dropout_backward(da, 0.2, 1, counter=step)
+        dy = ns.rotary_backward(dq.view(T, 2, 32), None, plan)[0].reshape(T, H)
+        dx, _, _ = ns.layer_norm_backward(dy, saved8, None, rstd)
+        return f, dx + da, *dw
+
+    eager = [v.clone() for v in run()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = run()
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(eager, other):
+        assert torch.equal(a, b)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        captured = run()
+    g2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g2):
+        second = run()
+    for graph, outs in ((g, captured), (g2, second), (g, captured)):
+        for v in outs:
+            v.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager, outs):
+            assert torch.equal(a, b)
+    ns.ops_sync()
