@@ -41,16 +41,19 @@ using namespace ptx;
 
 constexpr int F_K = 64;                            // of the sums, a step
 constexpr int F_BOX = 64 * 64 * 2;                 // a TMA box: 64 rows of 64 bf16
-constexpr int F_STAGES = 5;
+constexpr int F_STAGES = 6;
 constexpr int F_OP_BYTES = 2 * F_BOX;              // an operand's part of a CTA, a step
 constexpr int F_STAGE_BYTES = 2 * F_OP_BYTES;
 constexpr int F_EXPERTS = 1024;
-constexpr int F_COLS = 16;                         // columns that are turned at a time
+constexpr int F_COLS = 16;                         // columns that are turned at a time in fp32
 constexpr int F_ROW = 132;                         // floats of a turned row: 128 and a gap
-constexpr int F_TURN_BYTES = F_COLS * F_ROW * 4;
+constexpr int F_COLS16 = 32;                       // and in bf16
+constexpr int F_ROW16 = 136;
+constexpr int F_TURN_BYTES = F_COLS16 * F_ROW16 * 2;
+static_assert(F_TURN_BYTES >= F_COLS * F_ROW * 4 && F_TURN_BYTES % 16 == 0, "a team's buffer");
 constexpr int F_BAR_OFF = F_STAGES * F_STAGE_BYTES;
 constexpr int F_TURN_OFF = F_BAR_OFF + 512;
-constexpr int F_TABLE_OFF = F_TURN_OFF + 4 * F_TURN_BYTES;       // two teams, two buffers
+constexpr int F_TABLE_OFF = F_TURN_OFF + 2 * F_TURN_BYTES;       // two teams
 constexpr int F_SMEM = F_TABLE_OFF + 2 * (F_EXPERTS + 1) * 4 + 1024;
 static_assert(F_SMEM <= 232448, "shared memory per CTA");
 constexpr int F_EPI_WARPS = 8;
@@ -215,32 +218,70 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
         : "r"(addr));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+// 16 columns of 32 lanes as bf16 pairs of neighbouring columns, in the layout
+// that stmatrix takes: r[j][i] is of columns 8 j .. 8 j + 7 and lanes 8 i .. 8 i + 7.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t addr, uint32_t (&r)[2][4]) {
+    uint32_t v[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(v[h][0]), "=r"(v[h][1]), "=r"(v[h][2]), "=r"(v[h][3]), "=r"(v[h][4]), "=r"(v[h][5]),
+              "=r"(v[h][6]), "=r"(v[h][7])
+            : "r"(addr + (static_cast<uint32_t>(16 * h) << 16)));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t* const p = &v[i / 2][4 * j + i % 2 * 2];
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(p[0]), __uint_as_float(p[1]));
+            r[j][i] = reinterpret_cast<const uint32_t&>(b);
+        }
+}
+// Four 8 x 8 matrices, turned: lanes 8 i .. 8 i + 7 give the places of matrix
+// i's eight columns.
+__device__ __forceinline__ void store_turned(uint32_t to, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
 // A barrier of one team's 128 threads.
 __device__ __forceinline__ void team_sync(int team) {
     asm volatile("bar.sync %0, 128;" ::"r"(1 + team) : "memory");
 }
 
 // 1 / (1 + e^-v).  The exponential and the reciprocal are good to a few 2^-23,
-// a thousandth of the bf16 rounding behind them.
-__device__ __forceinline__ float logistic(float v) { return __frcp_rn(1.f + __expf(-v)); }
+// a thousandth of the bf16 rounding behind them.  (With a reciprocal rounded
+// to nearest, UP's write-out took 1550 cycles for 16 columns, not 600.)
+__device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
-// act(g), and its derivative to d.
-__device__ __forceinline__ float activate(int act, float g, float& d) {
+// a = act(g) and d = act'(g), eight at a time.
+__device__ __forceinline__ void activate8(int act, const float (&g)[8], float (&a)[8], float (&d)[8]) {
     if (act == MUON_ACT_SILU) {
-        const float s = logistic(g);
-        d = s * fmaf(g, 1.f - s, 1.f);
-        return g * s;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float s = logistic(g[i]);
+            a[i] = g[i] * s;
+            d[i] = fmaf(a[i], 1.f - s, s);
+        }
+    } else if (act == MUON_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float c = fmaf(0.5f, erff(g[i] * 0.70710678f), 0.5f);
+            a[i] = g[i] * c;
+            d[i] = fmaf(g[i] * 0.39894228f, __expf(-0.5f * g[i] * g[i]), c);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // (1 + tanh z) / 2 is the logistic function of 2 z, which is 0 or 1
+            // long before the limit on g^2 (no infinity to multiply by 0)
+            const float q = fminf(g[i] * g[i], 1000.f), s = logistic(g[i] * fmaf(0.071354816f, q, 1.5957691f));
+            a[i] = g[i] * s;
+            d[i] = fmaf(a[i] * (1.f - s), fmaf(0.21406445f, q, 1.5957691f), s);
+        }
     }
-    if (act == MUON_ACT_GELU) {
-        const float c = fmaf(0.5f, erff(g * 0.70710678f), 0.5f);
-        d = fmaf(g * 0.39894228f, __expf(-0.5f * g * g), c);
-        return g * c;
-    }
-    // (1 + tanh z) / 2 is the logistic function of 2 z, which is 0 or 1 long
-    // before the limit on g^2 (no infinity to multiply by 0)
-    const float q = fminf(g * g, 1000.f), s = logistic(g * fmaf(0.071354816f, q, 1.5957691f));
-    d = s * fmaf(g * (1.f - s), fmaf(0.21406445f, q, 1.5957691f), 1.f);
-    return g * s;
 }
 
 // Eight neighbours of a turned row.  The two halves are read in an order that
@@ -554,14 +595,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const int lg = warp & 3;                    // this warp's 32 TMEM lanes
         const int team = (warp - 2) / 4;
         const int tid = (warp - 2) % 4 * 32 + lane;
-        float* const turn0 = reinterpret_cast<float*>(smem + F_TURN_OFF) + team * 2 * F_COLS * F_ROW;
+        uint8_t* const turn_at = smem + F_TURN_OFF + team * F_TURN_BYTES;
+        float* const turn = reinterpret_cast<float*>(turn_at);
         const uint32_t tempty_leader = map_to_rank(smem_u32(tempty_bar), 0);
         uint32_t uses[2] = {0, 0};
-        uint32_t acc = 0, flip = 0;
+        uint32_t acc = 0;
         constexpr int GROUPS = OP == UP ? 8 : 16;   // of eight outputs of a row
         constexpr int UNITS = F_COLS * GROUPS / 128;
+        // what DHIDDEN reads beside the sums, 16 columns ahead of their use
+        uint4 kg[UNITS], ku[UNITS];
+        auto fetch = [&](const Item& x, int c) {
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) {
+                const int u = tid + 128 * i, row = x.n0 + c * F_COLS + u / GROUPS;
+                const int m = x.m0 + static_cast<int>(rank) * 128 + u % GROUPS * 8;
+                kg[i] = ku[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (row < x.n_end && m < p.m[0]) {
+                    const int64_t at = row * p.ld_kept + m;
+                    kg[i] = load8(static_cast<const __nv_bfloat16*>(p.gate) + at, p.m[0] - m, p.kept_vec);
+                    ku[i] = load8(static_cast<const __nv_bfloat16*>(p.up) + at, p.m[0] - m, p.kept_vec);
+                }
+            }
+        };
         for (int32_t it = pair; it < tiles.total; it += npairs) {
             const Item x = tiles.at(it);
+            if constexpr (OP == DHIDDEN) fetch(x, team);
             if (x.steps) {
                 const uint32_t use = acc ? uses[1]++ : uses[0]++;
                 const bool got = wait_soon(smem_u32(&tfull_bar[acc]), use & 1, abort_flag, &g_ffn_err, limit);
@@ -583,83 +641,120 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             const int n_real = min(x.n, x.n_end - x.n0);
             const int m0 = x.m0 + static_cast<int>(rank) * (OP == UP ? 64 : 128);
             const int m_end = OP == DW ? p.m[x.j == 2] : p.m[0];
-            int last = (n_real - 1) / F_COLS;       // this team's last columns
-            if ((last & 1) != team) --last;
             auto release = [&] {
                 if (!x.steps) return;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * acc);
             };
+            // the teams take blocks of columns in turn; this one's last
+            const bool flat = OP == DOWN || OP == DX || (OP == DW && !p.out_f32 && !p.accumulate);
+            int last = (n_real - 1) / (flat ? F_COLS16 : F_COLS);
+            if ((last & 1) != team) --last;
             if (last < 0) release();
-            for (int c = team; c <= last; c += 2) {
-                const int n0 = x.n0 + c * F_COLS;
-                // what is read beside the sums, ahead of them
-                uint4 kg[UNITS], ku[UNITS];
-                if constexpr (OP == DHIDDEN) {
+            if constexpr (OP == DOWN || OP == DX || OP == DW) {
+                if (flat) {
+                    const Out& o = p.out[OP == DW ? x.j : 0];
+                    __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(o.p) + (OP == DW ? x.e * o.stride : 0);
+                    const uint32_t mine = smem_u32(turn_at) + (lane % 8 * F_ROW16 + lg * 32 + lane / 8 * 8) * 2;
+                    for (int c = team; c <= last; c += 2) {
+                        team_sync(team);          // the last columns have been read
 #pragma unroll
-                    for (int i = 0; i < UNITS; ++i) {
-                        const int u = tid + 128 * i, row = n0 + u / GROUPS, m = m0 + u % GROUPS * 8;
-                        kg[i] = ku[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (row < x.n_end && m < m_end) {
-                            const int64_t at = row * p.ld_kept + m;
-                            kg[i] = load8(static_cast<const __nv_bfloat16*>(p.gate) + at, m_end - m, p.kept_vec);
-                            ku[i] = load8(static_cast<const __nv_bfloat16*>(p.up) + at, m_end - m, p.kept_vec);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t r[2][4];
+                            if (x.steps) {
+                                tmem_ld_frag(taddr + c * F_COLS16 + 16 * h, r);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) r[i / 4][i % 4] = 0u;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                store_turned(mine + (16 * h + 8 * j) * F_ROW16 * 2, r[j]);
+                        }
+                        if (c == last) release();
+                        team_sync(team);
+                        const int m = m0 + tid % 16 * 8, left = m_end - m;
+                        const int row0 = x.n0 + c * F_COLS16 + tid / 16;
+#pragma unroll
+                        for (int i = 0; i < F_COLS16 / 8; ++i) {
+                            const uint4 q = *reinterpret_cast<const uint4*>(
+                                turn_at + ((tid / 16 + 8 * i) * F_ROW16 + tid % 16 * 8) * 2);
+                            if (row0 + 8 * i < x.n_end) {
+                                __nv_bfloat16* const at = to + (row0 + 8 * i) * o.ld + m;
+                                if (o.vec && left >= 8) {
+                                    *reinterpret_cast<uint4*>(at) = q;
+                                } else {
+                                    const uint16_t* const h = reinterpret_cast<const uint16_t*>(&q);
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k)
+                                        if (k < left) reinterpret_cast<uint16_t*>(at)[k] = h[k];
+                                }
+                            }
                         }
                     }
                 }
-                uint32_t raw[16];
-                if (x.steps) {
-                    tmem_ld16(taddr + c * F_COLS, raw);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) raw[i] = 0u;
-                }
-                if (c == last) release();
-                float* const turn = turn0 + flip * F_COLS * F_ROW;
-                flip ^= 1;
-#pragma unroll
-                for (int i = 0; i < F_COLS; ++i) turn[i * F_ROW + lg * 32 + lane] = __uint_as_float(raw[i]);
-                // the other buffer is written next, so one barrier is enough:
-                // its readers have passed this one
-                team_sync(team);
-#pragma unroll
-                for (int i = 0; i < UNITS; ++i) {
-                    const int u = tid + 128 * i, r = u / GROUPS, group = u % GROUPS;
-                    const int row = n0 + r, m = m0 + group * 8, left = m_end - m;
-                    if (row >= x.n_end || left <= 0) continue;
-                    float v[8];
-                    turned8(turn + r * F_ROW, group, v);
-                    if constexpr (OP == UP) {
-                        float w[8], h[8], d;
-                        turned8(turn + r * F_ROW, 8 + group, w);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) h[q] = activate(p.act, v[q], d) * w[q];
-                        put8(p.out[0], row * p.out[0].ld + m, left, h);
-                        if (p.out[1].p) {
-                            put8(p.out[1], row * p.out[1].ld + m, left, v);
-                            put8(p.out[2], row * p.out[2].ld + m, left, w);
-                        }
-                    } else if constexpr (OP == DHIDDEN) {
-                        float g[8], w[8], h[8];
-                        widen8(kg[i], g);
-                        widen8(ku[i], w);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            float d;
-                            const float a = activate(p.act, g[q], d);
-                            h[q] = a * w[q];
-                            g[q] = v[q] * w[q] * d;
-                            w[q] = v[q] * a;
-                        }
-                        put8(p.out[0], row * p.out[0].ld + m, left, g);
-                        put8(p.out[1], row * p.out[1].ld + m, left, w);
-                        if (p.out[2].p) put8(p.out[2], row * p.out[2].ld + m, left, h);
-                    } else if constexpr (OP == DW) {
-                        const Out& o = p.out[x.j];
-                        put8_grad(o, x.e * o.stride + row * o.ld + m, left, p.out_f32, p.accumulate, v);
+            }
+            if constexpr (OP == UP || OP == DHIDDEN || OP == DW) {
+                for (int c = flat ? last + 1 : team; c <= last; c += 2) {
+                    const int n0 = x.n0 + c * F_COLS;
+                    uint32_t raw[16];
+                    if (x.steps) {
+                        tmem_ld16(taddr + c * F_COLS, raw);
                     } else {
-                        put8(p.out[0], row * p.out[0].ld + m, left, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) raw[i] = 0u;
+                    }
+                    if (c == last) release();
+                    team_sync(team);              // the last columns have been read
+#pragma unroll
+                    for (int i = 0; i < F_COLS; ++i)
+                        turn[i * F_ROW + lg * 32 + lane] = __uint_as_float(raw[i]);
+                    team_sync(team);
+                    uint4 g8[UNITS], u8[UNITS];
+                    if constexpr (OP == DHIDDEN) {
+#pragma unroll
+                        for (int i = 0; i < UNITS; ++i) {
+                            g8[i] = kg[i];
+                            u8[i] = ku[i];
+                        }
+                        if (c < last) fetch(x, c + 2);
+                    }
+#pragma unroll
+                    for (int i = 0; i < UNITS; ++i) {
+                        const int u = tid + 128 * i, r = u / GROUPS, group = u % GROUPS;
+                        const int row = n0 + r, m = m0 + group * 8, left = m_end - m;
+                        if (row >= x.n_end || left <= 0) continue;
+                        float v[8], w[8], a[8], d[8];
+                        turned8(turn + r * F_ROW, group, v);
+                        if constexpr (OP == UP) {
+                            turned8(turn + r * F_ROW, 8 + group, w);
+                            activate8(p.act, v, a, d);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) a[q] *= w[q];
+                            put8(p.out[0], row * p.out[0].ld + m, left, a);
+                            if (p.out[1].p) {
+                                put8(p.out[1], row * p.out[1].ld + m, left, v);
+                                put8(p.out[2], row * p.out[2].ld + m, left, w);
+                            }
+                        } else if constexpr (OP == DHIDDEN) {
+                            float g[8];
+                            widen8(g8[i], g);
+                            widen8(u8[i], w);
+                            activate8(p.act, g, a, d);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                d[q] *= v[q] * w[q];
+                                v[q] *= a[q];
+                                a[q] *= w[q];
+                            }
+                            put8(p.out[0], row * p.out[0].ld + m, left, d);
+                            put8(p.out[1], row * p.out[1].ld + m, left, v);
+                            if (p.out[2].p) put8(p.out[2], row * p.out[2].ld + m, left, a);
+                        } else {
+                            const Out& o = p.out[x.j];
+                            put8_grad(o, x.e * o.stride + row * o.ld + m, left, p.out_f32, p.accumulate, v);
+                        }
                     }
                 }
             }
