@@ -21,10 +21,10 @@
 // thread has eight neighbours of an output row, reads what it needs beside
 // them, and stores 16 bytes.
 //
-// Roles in a CTA: warp 0 loads (TMA), warp 1 issues the products (the pair's
-// leader only), warps 2-9 are the epilogue, in two teams of four that take a
-// tile's columns in turn, warp 10 clears what DW loads past an expert's last
-// token.  Two accumulators, so that a tile is written out while the next one's
+// Roles in a CTA: warps 0 and 11 load (TMA), warp 1 issues the products (the
+// pair's leader only), warps 2-9 are the epilogue, in two teams of four that
+// take a tile's columns in turn, warp 10 clears what DW loads past an expert's
+// last token.  Two accumulators, so that a tile is written out while the next one's
 // products run.  Pairs walk the tiles in turn.
 //
 // Every wait is bounded; one that runs out raises g_ffn_err (muon_ops_sync).
@@ -58,7 +58,8 @@ constexpr int F_SMEM = F_TABLE_OFF + 2 * (F_EXPERTS + 1) * 4 + 1024;
 static_assert(F_SMEM <= 232448, "shared memory per CTA");
 constexpr int F_EPI_WARPS = 8;
 constexpr int F_PATCH_WARP = 2 + F_EPI_WARPS;
-constexpr int F_THREADS = 32 * (F_PATCH_WARP + 1);
+constexpr int F_LOAD_B_WARP = F_PATCH_WARP + 1;
+constexpr int F_THREADS = 32 * (F_LOAD_B_WARP + 1);
 constexpr int F_TMEM_COLS = 512;
 constexpr int F_PAIRS = 76;                        // a pair per two of the 152 SMs
 constexpr int F_BAND = 8;
@@ -74,9 +75,10 @@ struct Out {
     int32_t vec;             // rows lie on 16 bytes
 };
 
-// One of the sums' operand pairs: a is M's side, b is N's.
+// One of the sums' operand pairs: a is M's side, b is N's (b64: in boxes of 64
+// rows, for the tiles that have no more a CTA).
 struct Maps {
-    CUtensorMap a, b;
+    CUtensorMap a, b, b64;
 };
 
 struct FfnLaunch {
@@ -361,6 +363,91 @@ __device__ __forceinline__ void put8_grad(const Out& o, int64_t at, int left, bo
         if (i < left) p[i] = add ? p[i] + v[i] : v[i];
 }
 
+// The loads of one operand: a thread of its own each, because issuing them
+// costs a thread about 100 cycles a box, and products wait for nothing else
+// where the sums are long (8192 tokens of 4096 x 11008 and all four boxes of a
+// step from one thread: 735 cycles a step, of 512 that the products take).
+template <int OP, bool A>
+__device__ __forceinline__ void load_operand(const FfnLaunch& p, const Tiles<OP>& tiles, uint8_t* smem, int pair,
+                                             int npairs, uint32_t rank, volatile int* abort_flag) {
+    constexpr bool A_MN = OP == DHIDDEN || OP == DX || OP == DW, B_MN = OP == DW;
+    const uint32_t full = smem_u32(smem + F_BAR_OFF), empty = full + 8 * F_STAGES, tail_bar = empty + 8 * F_STAGES;
+    const uint32_t full_leader = map_to_rank(full, 0), tail_own = map_to_rank(tail_bar, rank);
+    const uint32_t stage0 = smem_u32(smem) + (A ? 0 : F_OP_BYTES);
+    uint32_t slot = 0, parity = 1;
+    // a bit a stage: it has been loaded, its last load was a short step's, and
+    // the parities that follow its loads of either kind
+    uint32_t used = 0, tails = 0, tail_phase = 0, full_phase = 0;
+    bool ok = true;
+    for (int32_t it = pair; ok && it < tiles.total; it += npairs) {
+        const Item x = tiles.at(it);
+        const int boxes = (x.n / 2 + 63) / 64;
+        const uint32_t bytes = F_OP_BYTES + boxes * F_BOX;
+        const int m0 = x.m0 + static_cast<int>(rank) * (OP == UP ? 64 : 128);
+        const int n0 = x.n0 + static_cast<int>(rank) * (x.n / 2);
+        int s = 0;
+        // DX has two sums' worth of steps, of one operand pair each
+#pragma unroll 1
+        for (int part = 0; ok && part < (OP == DX ? 2 : 1); ++part) {
+            const int j = OP == DW ? x.j : part;
+            const int end = OP == DX ? x.steps / 2 * (part + 1) : x.steps;
+            const Maps& m = p.maps[j];
+            const int z = p.a_by_expert[j] ? x.e : 0, z1 = p.a_by_expert[1] ? x.e : 0;
+            const CUtensorMap* const tb = B_MN || boxes > 1 ? &m.b : &m.b64;
+            int k0 = OP == DW ? x.t0 : 0;
+#pragma unroll 1
+            for (; s < end; ++s, k0 += F_K) {
+                if (!wait_soon(empty + 8 * slot, parity, abort_flag, &g_ffn_err, p.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                uint32_t bar = full_leader + 8 * slot;
+                if (OP == DW && x.tail && s == x.steps - 1) {
+                    if (A) mbar_expect_tx(tail_bar + 8 * slot, bytes);
+                    tails |= 1u << slot;
+                    tail_phase ^= 1u << slot;
+                    bar = tail_own + 8 * slot;
+                } else {
+                    if (A && rank == 0) mbar_expect_tx(full + 8 * slot, 2 * bytes);
+                    tails &= ~(1u << slot);
+                    full_phase ^= 1u << slot;
+                }
+                used |= 1u << slot;
+                const uint32_t to = stage0 + slot * F_STAGE_BYTES;
+                if constexpr (A) {
+                    if constexpr (OP == UP) {
+                        load_box(to, &m.a, bar, k0, m0, z);
+                        load_box(to + F_BOX, &p.maps[1].a, bar, k0, m0, z1);
+                    } else if constexpr (A_MN) {
+                        load_box(to, &m.a, bar, m0, k0, z);
+                        load_box(to + F_BOX, &m.a, bar, m0 + 64, k0, z);
+                    } else {
+                        load_box(to, &m.a, bar, k0, m0, z);
+                    }
+                } else if constexpr (B_MN) {
+                    load_box(to, tb, bar, n0, k0, 0);
+                    if (boxes > 1) load_box(to + F_BOX, tb, bar, n0 + 64, k0, 0);
+                } else {
+                    load_box(to, tb, bar, k0, n0, 0);
+                }
+                if (++slot == F_STAGES) {
+                    slot = 0;
+                    parity ^= 1;
+                }
+            }
+        }
+    }
+    if (!ok && A) {
+        // the last loads of each stage (the leader's barriers count both
+        // CTAs', and both operands')
+        for (uint32_t i = 0; i < F_STAGES; ++i) {
+            if (!(used >> i & 1)) continue;
+            if (tails >> i & 1) wait_quiet(tail_bar + 8 * i, (tail_phase >> i & 1) ^ 1, p.wait_limit_ns);
+            else if (rank == 0) wait_quiet(full + 8 * i, (full_phase >> i & 1) ^ 1, p.wait_limit_ns);
+        }
+    }
+}
+
 template <int OP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     gated_ffn_kernel(const __grid_constant__ FfnLaunch p) {
@@ -449,73 +536,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     const Tiles<OP> tiles(p, table);
 
     if (warp == 0) {
-        // ------------------------------------------------------------ loads
-        if (lane == 0) {
-            uint32_t step = 0;
-            // a bit a stage: its last load was a short step's, and the parities
-            // that follow its loads of either kind
-            uint32_t tails = 0, tail_phase = 0, full_phase = 0;
-            bool ok = true;
-            for (int32_t it = pair; ok && it < tiles.total; it += npairs) {
-                const Item x = tiles.at(it);
-                const int boxes = (x.n / 2 + 63) / 64;
-                const uint32_t bytes = F_OP_BYTES + boxes * F_BOX;
-                const int m0 = x.m0 + static_cast<int>(rank) * (OP == UP ? 64 : 128);
-                const int n0 = x.n0 + static_cast<int>(rank) * (x.n / 2);
-                const int half = (p.k + F_K - 1) / F_K;      // DX: steps of the first product
-                for (int s = 0; s < x.steps; ++s, ++step) {
-                    const uint32_t slot = step % F_STAGES;
-                    if (!wait_soon(smem_u32(&empty_bar[slot]), (step / F_STAGES & 1) ^ 1, abort_flag,
-                                   &g_ffn_err, limit)) {
-                        ok = false;
-                        break;
-                    }
-                    const bool tail = OP == DW && x.tail && s == x.steps - 1;
-                    uint32_t bar = smem_u32(&full_bar[slot]);
-                    if (tail) {
-                        bar = smem_u32(&tail_bar[slot]);
-                        mbar_expect_tx(bar, bytes);
-                        tails |= 1u << slot;
-                        tail_phase ^= 1u << slot;
-                        bar = map_to_rank(bar, rank);
-                    } else {
-                        if (rank == 0) mbar_expect_tx(bar, 2 * bytes);
-                        tails &= ~(1u << slot);
-                        full_phase ^= 1u << slot;
-                        bar = map_to_rank(bar, 0);
-                    }
-                    const uint32_t a = smem_u32(smem + slot * F_STAGE_BYTES), b = a + F_OP_BYTES;
-                    const int j = OP == DW ? x.j : OP == DX ? s >= half : 0;
-                    const int k0 = OP == DW ? x.t0 + s * F_K : (OP == DX && j ? s - half : s) * F_K;
-                    const Maps& m = p.maps[j];
-                    const int z = p.a_by_expert[j] ? x.e : 0;
-                    if constexpr (OP == UP) {
-                        load_box(a, &m.a, bar, k0, m0, z);
-                        load_box(a + F_BOX, &p.maps[1].a, bar, k0, m0, p.a_by_expert[1] ? x.e : 0);
-                    } else if constexpr (A_MN) {
-                        load_box(a, &m.a, bar, m0, k0, z);
-                        load_box(a + F_BOX, &m.a, bar, m0 + 64, k0, z);
-                    } else {
-                        load_box(a, &m.a, bar, k0, m0, z);
-                        load_box(a + F_BOX, &m.a, bar, k0, m0 + 64, z);
-                    }
-                    for (int i = 0; i < boxes; ++i) {
-                        if constexpr (B_MN) load_box(b + i * F_BOX, &m.b, bar, n0 + 64 * i, k0, 0);
-                        else load_box(b + i * F_BOX, &m.b, bar, k0, n0 + 64 * i, 0);
-                    }
-                }
-            }
-            if (!ok) {
-                // the last load of each stage: the leader's barriers count both CTAs'
-                for (uint32_t i = step - min(step, uint32_t(F_STAGES)); i < step; ++i) {
-                    const uint32_t slot = i % F_STAGES;
-                    if (tails >> slot & 1)
-                        wait_quiet(smem_u32(&tail_bar[slot]), (tail_phase >> slot & 1) ^ 1, limit);
-                    else if (rank == 0)
-                        wait_quiet(smem_u32(&full_bar[slot]), (full_phase >> slot & 1) ^ 1, limit);
-                }
-            }
-        }
+        // ------------------------------------------------------ loads of A, of B
+        if (lane == 0) load_operand<OP, true>(p, tiles, smem, pair, npairs, rank, abort_flag);
+    } else if (warp == F_LOAD_B_WARP) {
+        if (lane == 0) load_operand<OP, false>(p, tiles, smem, pair, npairs, rank, abort_flag);
     } else if (warp == 1) {
         // ------------------------------------------------- products (leader)
         if (lane == 0 && rank == 0) {
@@ -848,18 +872,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// A map of 64 x 64 boxes; zeros come back past a matrix's rows and columns.
-bool encode(CUtensorMap* tm, const Operand& o) {
+// A map of boxes of `high` rows of 64; zeros come back past a matrix's rows and
+// columns.
+bool encode(CUtensorMap* tm, const Operand& o, unsigned high = 64) {
     if (!encoder()) return false;
     const int64_t ld = o.rows > 1 ? o.ld : ceil_div(o.cols, 8) * 8;
     const int64_t stride = o.matrices > 1 ? o.stride : o.rows * ld;
     cuuint64_t dims[3] = {cuuint64_t(o.cols), cuuint64_t(o.rows), cuuint64_t(o.matrices)};
     cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride) * 2};
-    cuuint32_t box[3] = {64, 64, 1}, el[3] = {1, 1, 1};
+    cuuint32_t box[3] = {64, high, 1}, el[3] = {1, 1, 1};
     return encoder()(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, el,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// N's side, whose rows are the operand's.
+bool encode_rows(Maps& m, const Operand& o) { return encode(&m.b, o, 128) && encode(&m.b64, o, 64); }
 
 Out output(void* p, int64_t ld, int64_t rows, int64_t matrices = 1, int64_t stride = 0, int size = 2) {
     return Out{p, ld, stride,
@@ -977,7 +1005,7 @@ cudaError_t launch_gated_ffn(const muon_gated_ffn_args& a, void* ws, cudaStream_
     p.out[0] = output(base + f.h_at, f.h.ld, a.rows);
     p.out[1] = output(a.gate, a.ld_kept, a.rows);
     p.out[2] = output(a.up, a.ld_kept, a.rows);
-    if (!encode(&p.maps[0].a, f.gate) || !encode(&p.maps[1].a, f.up) || !encode(&p.maps[0].b, f.x))
+    if (!encode(&p.maps[0].a, f.gate) || !encode(&p.maps[1].a, f.up) || !encode_rows(p.maps[0], f.x))
         return cudaErrorInvalidValue;
     const int64_t rt = row_tiles(a.rows, a.experts, p.tile_n);
     RETURN_IF_CUDA(launch_op(UP, p, rt * ceil_div(a.inner, 128), s));
@@ -985,7 +1013,7 @@ cudaError_t launch_gated_ffn(const muon_gated_ffn_args& a, void* ws, cudaStream_
     p.k = static_cast<int32_t>(a.inner);
     p.a_by_expert[0] = f.down.matrices > 1;
     p.out[0] = output(a.y, a.ld_y, a.rows);
-    if (!encode(&p.maps[0].a, f.down) || !encode(&p.maps[0].b, f.h)) return cudaErrorInvalidValue;
+    if (!encode(&p.maps[0].a, f.down, 128) || !encode_rows(p.maps[0], f.h)) return cudaErrorInvalidValue;
     return launch_op(DOWN, p, rt * ceil_div(a.hidden, 256), s);
 }
 
@@ -1010,7 +1038,7 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
             if (b.own[i]) d[i]->p = base + b.d_at[i];
             p.out[i] = output(const_cast<void*>(d[i]->p), d[i]->ld, a.rows);
         }
-        if (!encode(&p.maps[0].a, b.down) || !encode(&p.maps[0].b, b.dy)) return cudaErrorInvalidValue;
+        if (!encode(&p.maps[0].a, b.down) || !encode_rows(p.maps[0], b.dy)) return cudaErrorInvalidValue;
         RETURN_IF_CUDA(launch_op(DHIDDEN, p, rt * ceil_div(a.inner, 256), s));
         for (Operand* o : d) RETURN_IF_CUDA(settle(*o, base, s));
         if (a.dx) {
@@ -1019,8 +1047,8 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
             p.a_by_expert[0] = b.gate.matrices > 1;
             p.a_by_expert[1] = b.up.matrices > 1;
             p.out[0] = output(a.dx, a.ld_dx, a.rows);
-            if (!encode(&p.maps[0].a, b.gate) || !encode(&p.maps[1].a, b.up) || !encode(&p.maps[0].b, b.dg) ||
-                !encode(&p.maps[1].b, b.du))
+            if (!encode(&p.maps[0].a, b.gate) || !encode(&p.maps[1].a, b.up) || !encode_rows(p.maps[0], b.dg) ||
+                !encode_rows(p.maps[1], b.du))
                 return cudaErrorInvalidValue;
             RETURN_IF_CUDA(launch_op(DX, p, rt * ceil_div(a.hidden, 256), s));
         }
