@@ -75,10 +75,12 @@ struct Out {
     int32_t vec;             // rows lie on 16 bytes
 };
 
-// One of the sums' operand pairs: a is M's side, b is N's (b64: in boxes of 64
-// rows, for the tiles that have no more a CTA).
+// One of the sums' operand pairs: a is M's side, b is N's (b64: in boxes of 64,
+// for the tiles that have no more a CTA).  wide_a, wide_b: a box has 128
+// columns of an operand whose rows are k (blocks()).
 struct Maps {
     CUtensorMap a, b, b64;
+    int32_t wide_a, wide_b;
 };
 
 struct FfnLaunch {
@@ -185,6 +187,14 @@ __device__ __forceinline__ void load_box(uint32_t dst, const void* tmap, uint32_
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::"
         "complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
+        : "memory");
+}
+__device__ __forceinline__ void load_box(uint32_t dst, const void* tmap, uint32_t cluster_bar, int x, int y,
+                                         int block, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::"
+        "complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(block), "r"(z), "r"(cluster_bar)
         : "memory");
 }
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -393,7 +403,7 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, const Tiles<OP>
             const int end = OP == DX ? x.steps / 2 * (part + 1) : x.steps;
             const Maps& m = p.maps[j];
             const int z = p.a_by_expert[j] ? x.e : 0, z1 = p.a_by_expert[1] ? x.e : 0;
-            const CUtensorMap* const tb = B_MN || boxes > 1 ? &m.b : &m.b64;
+            const CUtensorMap* const tb = boxes > 1 ? &m.b : &m.b64;
             int k0 = OP == DW ? x.t0 : 0;
 #pragma unroll 1
             for (; s < end; ++s, k0 += F_K) {
@@ -419,14 +429,22 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, const Tiles<OP>
                         load_box(to, &m.a, bar, k0, m0, z);
                         load_box(to + F_BOX, &p.maps[1].a, bar, k0, m0, z1);
                     } else if constexpr (A_MN) {
-                        load_box(to, &m.a, bar, m0, k0, z);
-                        load_box(to + F_BOX, &m.a, bar, m0 + 64, k0, z);
+                        if (m.wide_a) {
+                            load_box(to, &m.a, bar, 0, k0, m0 / 64, z);
+                        } else {
+                            load_box(to, &m.a, bar, m0, k0, 0, z);
+                            load_box(to + F_BOX, &m.a, bar, m0 + 64, k0, 0, z);
+                        }
                     } else {
                         load_box(to, &m.a, bar, k0, m0, z);
                     }
                 } else if constexpr (B_MN) {
-                    load_box(to, tb, bar, n0, k0, 0);
-                    if (boxes > 1) load_box(to + F_BOX, tb, bar, n0 + 64, k0, 0);
+                    if (m.wide_b && x.n == 256) {
+                        load_box(to, &m.b, bar, 0, k0, n0 / 64, 0);
+                    } else {
+                        load_box(to, &m.b64, bar, n0, k0, 0, 0);
+                        if (boxes > 1) load_box(to + F_BOX, &m.b64, bar, n0 + 64, k0, 0, 0);
+                    }
                 } else {
                     load_box(to, tb, bar, k0, n0, 0);
                 }
@@ -872,22 +890,46 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// A map of boxes of `high` rows of 64; zeros come back past a matrix's rows and
-// columns.
-bool encode(CUtensorMap* tm, const Operand& o, unsigned high = 64) {
+bool encode(CUtensorMap* tm, const void* base, unsigned rank, const int64_t* dims, const int64_t* strides,
+            const unsigned* box) {
     if (!encoder()) return false;
-    const int64_t ld = o.rows > 1 ? o.ld : ceil_div(o.cols, 8) * 8;
-    const int64_t stride = o.matrices > 1 ? o.stride : o.rows * ld;
-    cuuint64_t dims[3] = {cuuint64_t(o.cols), cuuint64_t(o.rows), cuuint64_t(o.matrices)};
-    cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride) * 2};
-    cuuint32_t box[3] = {64, high, 1}, el[3] = {1, 1, 1};
-    return encoder()(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, el,
+    cuuint64_t d[4], st[3];
+    cuuint32_t bx[4], el[4] = {1, 1, 1, 1};
+    for (unsigned i = 0; i < rank; ++i) {
+        d[i] = cuuint64_t(dims[i]);
+        bx[i] = box[i];
+        if (i + 1 < rank) st[i] = cuuint64_t(strides[i]) * 2;
+    }
+    return encoder()(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, st, bx, el,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+int64_t row_stride(const Operand& o) { return o.rows > 1 ? o.ld : ceil_div(o.cols, 8) * 8; }
+int64_t matrix_stride(const Operand& o) { return o.matrices > 1 ? o.stride : o.rows * row_stride(o); }
+
+// An operand whose columns are k, in boxes of `high` rows of 64; zeros come
+// back past a matrix's rows and columns.
+bool rows_map(CUtensorMap* tm, const Operand& o, unsigned high) {
+    const int64_t dims[3] = {o.cols, o.rows, o.matrices}, strides[2] = {row_stride(o), matrix_stride(o)};
+    const unsigned box[3] = {64, high, 1};
+    return encode(tm, o.p, 3, dims, strides, box);
+}
+// An operand whose rows are k, in boxes of 64 rows of 64 columns; wide: two of
+// those side by side, as blocks of columns, which its columns must be whole
+// ones of.
+bool boxes_map(CUtensorMap* tm, const Operand& o, bool wide) {
+    const int64_t dims[4] = {wide ? 64 : o.cols, o.rows, wide ? o.cols / 64 : 1, o.matrices};
+    const int64_t strides[3] = {row_stride(o), wide ? 64 : row_stride(o), matrix_stride(o)};
+    const unsigned box[4] = {64, 64, wide ? 2u : 1u, 1};
+    return encode(tm, o.p, 4, dims, strides, box);
+}
+bool columns_map(CUtensorMap* tm, const Operand& o, int32_t* wide) {
+    *wide = o.cols % 64 == 0;
+    return boxes_map(tm, o, *wide != 0);
+}
 
 // N's side, whose rows are the operand's.
-bool encode_rows(Maps& m, const Operand& o) { return encode(&m.b, o, 128) && encode(&m.b64, o, 64); }
+bool rows_of_n(Maps& m, const Operand& o) { return rows_map(&m.b, o, 128) && rows_map(&m.b64, o, 64); }
 
 Out output(void* p, int64_t ld, int64_t rows, int64_t matrices = 1, int64_t stride = 0, int size = 2) {
     return Out{p, ld, stride,
@@ -1005,7 +1047,7 @@ cudaError_t launch_gated_ffn(const muon_gated_ffn_args& a, void* ws, cudaStream_
     p.out[0] = output(base + f.h_at, f.h.ld, a.rows);
     p.out[1] = output(a.gate, a.ld_kept, a.rows);
     p.out[2] = output(a.up, a.ld_kept, a.rows);
-    if (!encode(&p.maps[0].a, f.gate) || !encode(&p.maps[1].a, f.up) || !encode_rows(p.maps[0], f.x))
+    if (!rows_map(&p.maps[0].a, f.gate, 64) || !rows_map(&p.maps[1].a, f.up, 64) || !rows_of_n(p.maps[0], f.x))
         return cudaErrorInvalidValue;
     const int64_t rt = row_tiles(a.rows, a.experts, p.tile_n);
     RETURN_IF_CUDA(launch_op(UP, p, rt * ceil_div(a.inner, 128), s));
@@ -1013,7 +1055,7 @@ cudaError_t launch_gated_ffn(const muon_gated_ffn_args& a, void* ws, cudaStream_
     p.k = static_cast<int32_t>(a.inner);
     p.a_by_expert[0] = f.down.matrices > 1;
     p.out[0] = output(a.y, a.ld_y, a.rows);
-    if (!encode(&p.maps[0].a, f.down, 128) || !encode_rows(p.maps[0], f.h)) return cudaErrorInvalidValue;
+    if (!rows_map(&p.maps[0].a, f.down, 128) || !rows_of_n(p.maps[0], f.h)) return cudaErrorInvalidValue;
     return launch_op(DOWN, p, rt * ceil_div(a.hidden, 256), s);
 }
 
@@ -1038,7 +1080,7 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
             if (b.own[i]) d[i]->p = base + b.d_at[i];
             p.out[i] = output(const_cast<void*>(d[i]->p), d[i]->ld, a.rows);
         }
-        if (!encode(&p.maps[0].a, b.down) || !encode_rows(p.maps[0], b.dy)) return cudaErrorInvalidValue;
+        if (!columns_map(&p.maps[0].a, b.down, &p.maps[0].wide_a) || !rows_of_n(p.maps[0], b.dy)) return cudaErrorInvalidValue;
         RETURN_IF_CUDA(launch_op(DHIDDEN, p, rt * ceil_div(a.inner, 256), s));
         for (Operand* o : d) RETURN_IF_CUDA(settle(*o, base, s));
         if (a.dx) {
@@ -1047,8 +1089,9 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
             p.a_by_expert[0] = b.gate.matrices > 1;
             p.a_by_expert[1] = b.up.matrices > 1;
             p.out[0] = output(a.dx, a.ld_dx, a.rows);
-            if (!encode(&p.maps[0].a, b.gate) || !encode(&p.maps[1].a, b.up) || !encode_rows(p.maps[0], b.dg) ||
-                !encode_rows(p.maps[1], b.du))
+            if (!columns_map(&p.maps[0].a, b.gate, &p.maps[0].wide_a) ||
+                !columns_map(&p.maps[1].a, b.up, &p.maps[1].wide_a) || !rows_of_n(p.maps[0], b.dg) ||
+                !rows_of_n(p.maps[1], b.du))
                 return cudaErrorInvalidValue;
             RETURN_IF_CUDA(launch_op(DX, p, rt * ceil_div(a.hidden, 256), s));
         }
@@ -1071,7 +1114,9 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
         p.products |= 1 << j;
         const int64_t m = j == 2 ? a.inner : a.hidden, n = j == 2 ? a.hidden : a.inner;
         items += a.experts * ceil_div(m, 256) * ceil_div(n, p.tile_n);
-        if (a.rows && (!encode(&p.maps[j].a, *left[j]) || !encode(&p.maps[j].b, *right[j])))
+        Maps& of = p.maps[j];
+        if (a.rows && (!columns_map(&of.a, *left[j], &of.wide_a) || !columns_map(&of.b, *right[j], &of.wide_b) ||
+                       !boxes_map(&of.b64, *right[j], false)))
             return cudaErrorInvalidValue;
     }
     return launch_op(DW, p, items, s);
