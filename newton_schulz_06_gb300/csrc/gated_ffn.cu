@@ -54,7 +54,7 @@ static_assert(F_TURN_BYTES >= F_COLS * F_ROW * 4 && F_TURN_BYTES % 16 == 0, "a t
 constexpr int F_BAR_OFF = F_STAGES * F_STAGE_BYTES;
 constexpr int F_TURN_OFF = F_BAR_OFF + 512;
 constexpr int F_TABLE_OFF = F_TURN_OFF + 2 * F_TURN_BYTES;       // two teams
-constexpr int F_SMEM = F_TABLE_OFF + 2 * (F_EXPERTS + 1) * 4 + 1024;
+constexpr int F_SMEM = F_TABLE_OFF + 3 * (F_EXPERTS + 1) * 4 + 1024;
 static_assert(F_SMEM <= 232448, "shared memory per CTA");
 constexpr int F_EPI_WARPS = 8;
 constexpr int F_PATCH_WARP = 2 + F_EPI_WARPS;
@@ -88,66 +88,105 @@ struct FfnLaunch {
     Out out[3];              // UP: h, g, u; DHIDDEN: dg, du, h; DW: dWg, dWu, dWd
     const void *gate, *up;   // DHIDDEN reads them
     int64_t ld_kept;
-    int32_t kept_vec;
+    int32_t vec;             // UP, DHIDDEN: rows of all that is read and written here lie on 16 bytes
     const int32_t* offsets;
     int64_t rows;
     int32_t experts;
     int32_t m[2], k;         // extents; DW: m[0] is hidden, m[1] inner; else m[0]
     int32_t a_by_expert[3];  // an expert's own matrix, or one for all
     int32_t products;        // DW: which of them, as bits
-    int32_t tile_n;          // rows of N a tile, a multiple of 32
     int32_t act;
     int32_t out_f32, accumulate;
     unsigned long long wait_limit_ns;
+};
+
+// x / d by d's reciprocal: a sixth of the time of a division, which every role
+// does three of for a tile (800 cycles a tile, of 5000 with eight steps).
+struct Divisor {
+    uint32_t d;
+    float inv;
+    __device__ __forceinline__ void set(uint32_t v) {
+        d = v;
+        inv = __frcp_rn(__uint2float_rn(v));
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t x) const {
+        uint32_t q = __float2uint_rz(__uint2float_rz(x) * inv);
+        int32_t r = static_cast<int32_t>(x - q * d);
+        while (r < 0) {
+            --q;
+            r += d;
+        }
+        while (r >= static_cast<int32_t>(d)) {
+            ++q;
+            r -= d;
+        }
+        return q;
+    }
 };
 
 // A tile.
 struct Item {
     int32_t e, j;            // expert, product (DW)
     int32_t m0, n0;          // its first m (UP: of h), its first row of N
-    int32_t n_end;           // N's rows end here
+    int32_t n_end;           // its rows of N end here
     int32_t n;               // the instruction's N
     int32_t t0, steps;       // DW: the expert's first token; steps of 64
     int32_t tail;            // DW: tokens of the last step, if not 64
 };
 
+// The tiles' places.  An expert's rows are split evenly over as few tiles as
+// they need (300 rows: 160 and 140, not 256 and 44), because a narrow tile
+// loads all of its matrix rows like any other.
 template <int OP>
 struct Tiles {
     const FfnLaunch& p;
-    const int32_t *begin, *first;        // experts' first rows, and their first tile rows
-    int32_t total, tiles_m;
-    int32_t base[3], count[3], per;      // DW: a product's first tile, its tiles, all of a matrix
+    const int32_t *begin, *first, *high;     // experts' first rows, first tile rows, rows of a tile
+    int32_t total, steps;
+    Divisor tiles_m, band;                   // tiles across M, and in a band
+    Divisor per, across[2], bands[2];        // DW: a matrix's tiles; by product (2: the last one)
+    int32_t base[2];                         // the second and third product's first tile
     __device__ __forceinline__ Tiles(const FfnLaunch& l, const int32_t* table) : p(l) {
         begin = table;
-        first = table + p.experts + 1;
+        first = begin + p.experts + 1;
+        high = first + p.experts + 1;
         if constexpr (OP == DW) {
-            per = 0;
+            uint32_t all = 0;
 #pragma unroll
             for (int j = 0; j < 3; ++j) {
-                const int32_t m = (p.m[j == 2] + 255) / 256, n = (p.m[j != 2] + p.tile_n - 1) / p.tile_n;
-                base[j] = per;
-                count[j] = p.products >> j & 1 ? m * n : 0;
-                per += count[j];
+                const int32_t m = (p.m[j == 2] + 255) / 256, n = (p.m[j != 2] + 255) / 256;
+                if (j) base[j - 1] = all;
+                all += p.products >> j & 1 ? m * n : 0;
             }
-            total = per * p.experts;
+            per.set(all);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                across[i].set((p.m[i] + 255) / 256);
+                bands[i].set(F_BAND * across[i].d);
+            }
+            total = all * p.experts;
         } else {
-            tiles_m = (p.m[0] + (OP == UP ? 127 : 255)) / (OP == UP ? 128 : 256);
-            total = first[p.experts] * tiles_m;
+            tiles_m.set((p.m[0] + (OP == UP ? 127 : 255)) / (OP == UP ? 128 : 256));
+            band.set(F_BAND * tiles_m.d);
+            total = first[p.experts] * tiles_m.d;
+            steps = (p.k + F_K - 1) / F_K * (OP == DX ? 2 : 1);
         }
     }
     __device__ __forceinline__ Item at(int32_t it) const {
         Item x;
         x.tail = 0;
         x.j = 0;
-        int32_t in, tn, tm;
+        int32_t in, tn, size, end;
+        Divisor tm, b;
         if constexpr (OP == DW) {
-            x.e = it / per;
-            in = it - x.e * per;
-            x.j = in < base[1] ? 0 : in < base[2] ? 1 : 2;
-            in -= x.j == 0 ? 0 : x.j == 1 ? base[1] : base[2];
-            tm = (p.m[x.j == 2] + 255) / 256;
-            tn = (p.m[x.j != 2] + p.tile_n - 1) / p.tile_n;
-            x.n_end = p.m[x.j != 2];
+            x.e = per.of(it);
+            in = it - x.e * per.d;
+            x.j = in < base[0] ? 0 : in < base[1] ? 1 : 2;
+            in -= x.j == 0 ? 0 : x.j == 1 ? base[0] : base[1];
+            tm = x.j == 2 ? across[1] : across[0];
+            b = x.j == 2 ? bands[1] : bands[0];
+            end = p.m[x.j != 2];
+            size = 256;
+            tn = x.j == 2 ? across[0].d : across[1].d;
             x.t0 = begin[x.e];
             const int32_t len = begin[x.e + 1] - x.t0;
             x.steps = (len + F_K - 1) / F_K;
@@ -155,28 +194,33 @@ struct Tiles {
         } else {
             // the expert whose tiles these are
             int32_t lo = 0, hi = p.experts;
-            const int32_t row = it / tiles_m;
+            const int32_t row = tiles_m.of(it);
             while (hi - lo > 1) {
                 const int32_t mid = (lo + hi) >> 1;
                 if (first[mid] <= row) lo = mid;
                 else hi = mid;
             }
             x.e = lo;
-            in = it - first[lo] * tiles_m;
+            in = it - first[lo] * tiles_m.d;
             tm = tiles_m;
+            b = band;
             tn = first[lo + 1] - first[lo];
-            x.n_end = begin[lo + 1];
+            size = high[lo];
+            end = begin[lo + 1];
             x.t0 = 0;
-            x.steps = (p.k + F_K - 1) / F_K * (OP == DX ? 2 : 1);
+            x.steps = steps;
         }
         // bands of eight tiles of N, column by column: the tiles that run
         // together share their operands in L2
-        const int32_t band = in / (F_BAND * tm), high = min(F_BAND, tn - band * F_BAND);
-        in -= band * F_BAND * tm;
-        const int32_t m = in / high, n = band * F_BAND + in - m * high;
+        const int32_t nb = b.of(in), rows = min(F_BAND, tn - nb * F_BAND);
+        in -= nb * b.d;
+        // in / rows, exact: in is at most 8 x 2048 (tiles across 262144)
+        const int32_t m = rows == F_BAND ? in >> 3 : static_cast<int32_t>(__fdividef(in + 0.5f, rows));
+        const int32_t n = nb * F_BAND + in - m * rows;
         x.m0 = m * (OP == UP ? 128 : 256);
-        x.n0 = (OP == DW ? 0 : begin[x.e]) + n * p.tile_n;
-        x.n = min(p.tile_n, (x.n_end - x.n0 + 31) / 32 * 32);
+        x.n0 = (OP == DW ? 0 : begin[x.e]) + n * size;
+        x.n_end = min(end, x.n0 + size);
+        x.n = (x.n_end - x.n0 + 31) & ~31;
         return x;
     }
 };
@@ -373,6 +417,63 @@ __device__ __forceinline__ void put8_grad(const Out& o, int64_t at, int left, bo
         if (i < left) p[i] = add ? p[i] + v[i] : v[i];
 }
 
+// 16 turned columns (rows of the outputs from n0 on) in UP, DHIDDEN and, with
+// sums that stay fp32, DW.  WHOLE: all of their rows and columns are there and
+// on 16 bytes, so that nothing keeps one unit's instructions from the other's.
+// g8, u8: DHIDDEN's g and u.
+template <int OP>
+struct Units {
+    static constexpr int GROUPS = OP == UP ? 8 : 16;      // of eight outputs of a row
+    static constexpr int N = F_COLS * GROUPS / 128;       // a thread's
+};
+template <int OP, bool WHOLE>
+__device__ __forceinline__ void finish_turned(const FfnLaunch& p, const Item& x, const float* turn, int n0, int m0,
+                                              int m_end, int tid, const uint4 (&g8)[Units<OP>::N],
+                                              const uint4 (&u8)[Units<OP>::N]) {
+    constexpr int GROUPS = Units<OP>::GROUPS;
+#pragma unroll
+    for (int i = 0; i < Units<OP>::N; ++i) {
+        const int r = (tid + 128 * i) / GROUPS, group = tid % GROUPS;
+        const int row = n0 + r, m = m0 + group * 8, left = WHOLE ? 8 : m_end - m;
+        if (!WHOLE && (row >= x.n_end || left <= 0)) continue;
+        auto put = [&](const Out& o, const float (&f)[8]) {
+            const int64_t at = row * o.ld + m;
+            if (WHOLE) store8_bf16(static_cast<__nv_bfloat16*>(o.p) + at, f);
+            else put8(o, at, left, f);
+        };
+        float v[8], w[8], a[8], d[8];
+        turned8(turn + r * F_ROW, group, v);
+        if constexpr (OP == UP) {
+            turned8(turn + r * F_ROW, 8 + group, w);
+            activate8(p.act, v, a, d);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) a[q] *= w[q];
+            put(p.out[0], a);
+            if (p.out[1].p) {
+                put(p.out[1], v);
+                put(p.out[2], w);
+            }
+        } else if constexpr (OP == DHIDDEN) {
+            float g[8];
+            widen8(g8[i], g);
+            widen8(u8[i], w);
+            activate8(p.act, g, a, d);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                d[q] *= v[q] * w[q];
+                v[q] *= a[q];
+                a[q] *= w[q];
+            }
+            put(p.out[0], d);
+            put(p.out[1], v);
+            if (p.out[2].p) put(p.out[2], a);
+        } else {
+            const Out& o = p.out[x.j];
+            put8_grad(o, x.e * o.stride + row * o.ld + m, left, p.out_f32, p.accumulate, v);
+        }
+    }
+}
+
 // The loads of one operand: a thread of its own each, because issuing them
 // costs a thread about 100 cycles a box, and products wait for nothing else
 // where the sums are long (8192 tokens of 4096 x 11008 and all four boxes of a
@@ -530,8 +631,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             }
             b = max(b, rows);
             const int32_t before = __shfl_up_sync(0xffffffffu, b, 1);
-            // tiles of the expert before e
-            int32_t n = e ? (b - (lane ? before : rows) + p.tile_n - 1) / p.tile_n : 0;
+            // tiles of the expert before e, and their rows
+            const int32_t len = e ? b - (lane ? before : rows) : 0;
+            int32_t n = (len + 255) / 256;
+            if (n && e <= p.experts) table[2 * (p.experts + 1) + e - 1] = ((len + n - 1) / n + 31) & ~31;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int32_t v = __shfl_up_sync(0xffffffffu, n, o);
@@ -642,20 +745,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const uint32_t tempty_leader = map_to_rank(smem_u32(tempty_bar), 0);
         uint32_t uses[2] = {0, 0};
         uint32_t acc = 0;
-        constexpr int GROUPS = OP == UP ? 8 : 16;   // of eight outputs of a row
-        constexpr int UNITS = F_COLS * GROUPS / 128;
         // what DHIDDEN reads beside the sums, 16 columns ahead of their use
+        constexpr int UNITS = Units<OP>::N;
         uint4 kg[UNITS], ku[UNITS];
         auto fetch = [&](const Item& x, int c) {
+            const int row0 = x.n0 + c * F_COLS + tid / 16, m = x.m0 + static_cast<int>(rank) * 128 + tid % 16 * 8;
+            const int64_t at = row0 * p.ld_kept + m;
+            const __nv_bfloat16* const g = static_cast<const __nv_bfloat16*>(p.gate) + at;
+            const __nv_bfloat16* const u = static_cast<const __nv_bfloat16*>(p.up) + at;
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
-                const int u = tid + 128 * i, row = x.n0 + c * F_COLS + u / GROUPS;
-                const int m = x.m0 + static_cast<int>(rank) * 128 + u % GROUPS * 8;
                 kg[i] = ku[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (row < x.n_end && m < p.m[0]) {
-                    const int64_t at = row * p.ld_kept + m;
-                    kg[i] = load8(static_cast<const __nv_bfloat16*>(p.gate) + at, p.m[0] - m, p.kept_vec);
-                    ku[i] = load8(static_cast<const __nv_bfloat16*>(p.up) + at, p.m[0] - m, p.kept_vec);
+                const int left = row0 + 8 * i < x.n_end ? p.m[0] - m : 0;
+                if (p.vec && left >= 8) {
+                    kg[i] = *reinterpret_cast<const uint4*>(g + 8 * i * p.ld_kept);
+                    ku[i] = *reinterpret_cast<const uint4*>(u + 8 * i * p.ld_kept);
+                } else if (left > 0) {
+                    kg[i] = load8(g + 8 * i * p.ld_kept, left, false);
+                    ku[i] = load8(u + 8 * i * p.ld_kept, left, false);
                 }
             }
         };
@@ -680,7 +787,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 tc_fence_after();
             }
             const uint32_t taddr = tmem_base + acc * 256 + (static_cast<uint32_t>(lg * 32) << 16);
-            const int n_real = min(x.n, x.n_end - x.n0);
+            const int n_real = x.n_end - x.n0;
             const int m0 = x.m0 + static_cast<int>(rank) * (OP == UP ? 64 : 128);
             const int m_end = OP == DW ? p.m[x.j == 2] : p.m[0];
             auto release = [&] {
@@ -762,42 +869,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                         }
                         if (c < last) fetch(x, c + 2);
                     }
-#pragma unroll
-                    for (int i = 0; i < UNITS; ++i) {
-                        const int u = tid + 128 * i, r = u / GROUPS, group = u % GROUPS;
-                        const int row = n0 + r, m = m0 + group * 8, left = m_end - m;
-                        if (row >= x.n_end || left <= 0) continue;
-                        float v[8], w[8], a[8], d[8];
-                        turned8(turn + r * F_ROW, group, v);
-                        if constexpr (OP == UP) {
-                            turned8(turn + r * F_ROW, 8 + group, w);
-                            activate8(p.act, v, a, d);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) a[q] *= w[q];
-                            put8(p.out[0], row * p.out[0].ld + m, left, a);
-                            if (p.out[1].p) {
-                                put8(p.out[1], row * p.out[1].ld + m, left, v);
-                                put8(p.out[2], row * p.out[2].ld + m, left, w);
-                            }
-                        } else if constexpr (OP == DHIDDEN) {
-                            float g[8];
-                            widen8(g8[i], g);
-                            widen8(u8[i], w);
-                            activate8(p.act, g, a, d);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                d[q] *= v[q] * w[q];
-                                v[q] *= a[q];
-                                a[q] *= w[q];
-                            }
-                            put8(p.out[0], row * p.out[0].ld + m, left, d);
-                            put8(p.out[1], row * p.out[1].ld + m, left, v);
-                            if (p.out[2].p) put8(p.out[2], row * p.out[2].ld + m, left, a);
-                        } else {
-                            const Out& o = p.out[x.j];
-                            put8_grad(o, x.e * o.stride + row * o.ld + m, left, p.out_f32, p.accumulate, v);
-                        }
-                    }
+                    if (OP != DW && p.vec && n0 + F_COLS <= x.n_end && m0 + (OP == UP ? 64 : 128) <= m_end)
+                        finish_turned<OP, true>(p, x, turn, n0, m0, m_end, tid, g8, u8);
+                    else
+                        finish_turned<OP, false>(p, x, turn, n0, m0, m_end, tid, g8, u8);
                 }
             }
             if (x.steps) acc ^= 1;
@@ -963,13 +1038,12 @@ FfnLaunch common(const int32_t* offsets, int64_t rows, int64_t experts, int act)
     p.rows = rows;
     p.experts = static_cast<int32_t>(experts);
     p.act = act;
-    p.tile_n = 256;
     p.wait_limit_ns = wait_limit_ns();
     return p;
 }
 
 // Tiles of 256 rows that the experts' rows can make, at most.
-int64_t row_tiles(int64_t rows, int64_t experts, int tile_n) { return rows / tile_n + experts; }
+int64_t row_tiles(int64_t rows, int64_t experts) { return rows / 256 + experts; }
 
 struct Forward {
     Space space;
@@ -1047,9 +1121,10 @@ cudaError_t launch_gated_ffn(const muon_gated_ffn_args& a, void* ws, cudaStream_
     p.out[0] = output(base + f.h_at, f.h.ld, a.rows);
     p.out[1] = output(a.gate, a.ld_kept, a.rows);
     p.out[2] = output(a.up, a.ld_kept, a.rows);
+    p.vec = p.out[1].vec && p.out[2].vec;
     if (!rows_map(&p.maps[0].a, f.gate, 64) || !rows_map(&p.maps[1].a, f.up, 64) || !rows_of_n(p.maps[0], f.x))
         return cudaErrorInvalidValue;
-    const int64_t rt = row_tiles(a.rows, a.experts, p.tile_n);
+    const int64_t rt = row_tiles(a.rows, a.experts);
     RETURN_IF_CUDA(launch_op(UP, p, rt * ceil_div(a.inner, 128), s));
     p.m[0] = static_cast<int32_t>(a.hidden);
     p.k = static_cast<int32_t>(a.inner);
@@ -1065,7 +1140,7 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
     Operand* const d[3] = {&b.dg, &b.du, &b.h};
     const bool grads = a.dw_gate || a.dw_up || a.dw_down;
     FfnLaunch p = common(a.offsets, a.rows, a.experts, a.activation);
-    const int64_t rt = row_tiles(a.rows, a.experts, p.tile_n);
+    const int64_t rt = row_tiles(a.rows, a.experts);
     if (a.rows) {
         for (Operand* o : {&b.dy, &b.x, &b.gate, &b.up, &b.down}) RETURN_IF_CUDA(settle(*o, base, s));
         p.m[0] = static_cast<int32_t>(a.inner);
@@ -1074,11 +1149,12 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
         p.gate = a.gate;
         p.up = a.up;
         p.ld_kept = a.ld_kept;
-        p.kept_vec = output(const_cast<void*>(a.gate), a.ld_kept, a.rows).vec &&
-                     output(const_cast<void*>(a.up), a.ld_kept, a.rows).vec;
+        p.vec = output(const_cast<void*>(a.gate), a.ld_kept, a.rows).vec &&
+                output(const_cast<void*>(a.up), a.ld_kept, a.rows).vec;
         for (int i = 0; i < 3; ++i) {
             if (b.own[i]) d[i]->p = base + b.d_at[i];
             p.out[i] = output(const_cast<void*>(d[i]->p), d[i]->ld, a.rows);
+            p.vec = p.vec && p.out[i].vec;
         }
         if (!columns_map(&p.maps[0].a, b.down, &p.maps[0].wide_a) || !rows_of_n(p.maps[0], b.dy)) return cudaErrorInvalidValue;
         RETURN_IF_CUDA(launch_op(DHIDDEN, p, rt * ceil_div(a.inner, 256), s));
@@ -1113,7 +1189,7 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
         if (!p.out[j].p) continue;
         p.products |= 1 << j;
         const int64_t m = j == 2 ? a.inner : a.hidden, n = j == 2 ? a.hidden : a.inner;
-        items += a.experts * ceil_div(m, 256) * ceil_div(n, p.tile_n);
+        items += a.experts * ceil_div(m, 256) * ceil_div(n, 256);
         Maps& of = p.maps[j];
         if (a.rows && (!columns_map(&of.a, *left[j], &of.wide_a) || !columns_map(&of.b, *right[j], &of.wide_b) ||
                        !boxes_map(&of.b64, *right[j], false)))
