@@ -24,7 +24,7 @@
 // Roles in a CTA: warps 0 and 11 load (TMA), warp 1 issues the products (the
 // pair's leader only), warps 2-9 are the epilogue, in two teams of four that
 // take a tile's columns in turn, warp 10 clears what DW loads past an expert's
-// last token.  Two accumulators, so that a tile is written out while the next one's
+// last token, warp 12 finds the tiles.  Two accumulators, so that a tile is written out while the next one's
 // products run.  Pairs walk the tiles in turn.
 //
 // Every wait is bounded; one that runs out raises g_ffn_err (muon_ops_sync).
@@ -52,14 +52,17 @@ constexpr int F_ROW16 = 136;
 constexpr int F_TURN_BYTES = F_COLS16 * F_ROW16 * 2;
 static_assert(F_TURN_BYTES >= F_COLS * F_ROW * 4 && F_TURN_BYTES % 16 == 0, "a team's buffer");
 constexpr int F_BAR_OFF = F_STAGES * F_STAGE_BYTES;
-constexpr int F_TURN_OFF = F_BAR_OFF + 512;
+constexpr int F_ITEM_OFF = F_BAR_OFF + 384;       // tiles handed out
+constexpr int F_TURN_OFF = F_ITEM_OFF + 256;
 constexpr int F_TABLE_OFF = F_TURN_OFF + 2 * F_TURN_BYTES;       // two teams
 constexpr int F_SMEM = F_TABLE_OFF + 3 * (F_EXPERTS + 1) * 4 + 1024;
 static_assert(F_SMEM <= 232448, "shared memory per CTA");
 constexpr int F_EPI_WARPS = 8;
 constexpr int F_PATCH_WARP = 2 + F_EPI_WARPS;
 constexpr int F_LOAD_B_WARP = F_PATCH_WARP + 1;
-constexpr int F_THREADS = 32 * (F_LOAD_B_WARP + 1);
+constexpr int F_TILE_WARP = F_LOAD_B_WARP + 1;
+constexpr int F_THREADS = 32 * (F_TILE_WARP + 1);
+constexpr int F_ITEMS = 4;                         // tiles found ahead
 constexpr int F_TMEM_COLS = 512;
 constexpr int F_PAIRS = 76;                        // a pair per two of the 152 SMs
 constexpr int F_BAND = 8;
@@ -100,8 +103,7 @@ struct FfnLaunch {
     unsigned long long wait_limit_ns;
 };
 
-// x / d by d's reciprocal: a sixth of the time of a division, which every role
-// does three of for a tile (800 cycles a tile, of 5000 with eight steps).
+// x / d by d's reciprocal, a sixth of the time of a division.
 struct Divisor {
     uint32_t d;
     float inv;
@@ -125,14 +127,15 @@ struct Divisor {
 };
 
 // A tile.
-struct Item {
-    int32_t e, j;            // expert, product (DW)
+struct alignas(16) Item {
+    int32_t e, j;            // expert (below 0: there is no more), product (DW)
     int32_t m0, n0;          // its first m (UP: of h), its first row of N
     int32_t n_end;           // its rows of N end here
     int32_t n;               // the instruction's N
     int32_t t0, steps;       // DW: the expert's first token; steps of 64
     int32_t tail;            // DW: tokens of the last step, if not 64
 };
+static_assert(F_ITEMS * sizeof(Item) <= 256, "tiles handed out");
 
 // The tiles' places.  An expert's rows are split evenly over as few tiles as
 // they need (300 rows: 160 and 140, not 256 and 44), because a narrow tile
@@ -222,6 +225,31 @@ struct Tiles {
         x.n_end = min(end, x.n0 + size);
         x.n = (x.n_end - x.n0 + 31) & ~31;
         return x;
+    }
+};
+
+// The tiles as one warp finds them for all others: finding a tile takes 500 to
+// 1200 cycles, in which a role that did it itself kept the tensor cores waiting
+// (of 5000 a tile that has eight steps).
+struct Feed {
+    const Item* items;
+    uint32_t full, empty;
+    uint32_t n = 0;
+    __device__ __forceinline__ Feed(const uint8_t* smem, uint32_t bars)
+        : items(reinterpret_cast<const Item*>(smem + F_ITEM_OFF)), full(bars), empty(bars + 8 * F_ITEMS) {}
+    // The next tile, for a thread or a whole warp: false where the wait ran
+    // out.
+    template <bool WARP>
+    __device__ __forceinline__ bool next(Item& x, volatile int* abort_flag, uint64_t limit) {
+        const uint32_t slot = n % F_ITEMS;
+        bool got = wait_soon(full + 8 * slot, n / F_ITEMS & 1, abort_flag, &g_ffn_err, limit);
+        if (WARP) got = __all_sync(0xffffffffu, got);
+        if (!got) return false;
+        x = items[slot];
+        if (WARP) __syncwarp();
+        if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * slot);
+        ++n;
+        return true;
     }
 };
 
@@ -479,8 +507,8 @@ __device__ __forceinline__ void finish_turned(const FfnLaunch& p, const Item& x,
 // where the sums are long (8192 tokens of 4096 x 11008 and all four boxes of a
 // step from one thread: 735 cycles a step, of 512 that the products take).
 template <int OP, bool A>
-__device__ __forceinline__ void load_operand(const FfnLaunch& p, const Tiles<OP>& tiles, uint8_t* smem, int pair,
-                                             int npairs, uint32_t rank, volatile int* abort_flag) {
+__device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint8_t* smem, uint32_t rank,
+                                             volatile int* abort_flag) {
     constexpr bool A_MN = OP == DHIDDEN || OP == DX || OP == DW, B_MN = OP == DW;
     const uint32_t full = smem_u32(smem + F_BAR_OFF), empty = full + 8 * F_STAGES, tail_bar = empty + 8 * F_STAGES;
     const uint32_t full_leader = map_to_rank(full, 0), tail_own = map_to_rank(tail_bar, rank);
@@ -490,8 +518,9 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, const Tiles<OP>
     // the parities that follow its loads of either kind
     uint32_t used = 0, tails = 0, tail_phase = 0, full_phase = 0;
     bool ok = true;
-    for (int32_t it = pair; ok && it < tiles.total; it += npairs) {
-        const Item x = tiles.at(it);
+    for (Item x; ok;) {
+        ok = feed.next<false>(x, abort_flag, p.wait_limit_ns);
+        if (!ok || x.e < 0) break;
         const int boxes = (x.n / 2 + 63) / 64;
         const uint32_t bytes = F_OP_BYTES + boxes * F_BOX;
         const int m0 = x.m0 + static_cast<int>(rank) * (OP == UP ? 64 : 128);
@@ -580,7 +609,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     uint64_t* tfull_bar = patch_bar + F_STAGES;
     uint64_t* tempty_bar = tfull_bar + 2;
     uint64_t* drain_bar = tempty_bar + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+    uint64_t* item_bar = drain_bar + 1;             // a tile is there; its place is free
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_bar + 2 * F_ITEMS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int32_t* const table = reinterpret_cast<int32_t*>(smem + F_TABLE_OFF);
 
@@ -603,6 +633,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             mbar_init(smem_u32(&tempty_bar[a]), 2 * F_EPI_WARPS);
         }
         mbar_init(smem_u32(drain_bar), 1);
+        for (int i = 0; i < F_ITEMS; ++i) {
+            mbar_init(smem_u32(&item_bar[i]), 1);
+            // both loading threads, the products' thread, the epilogue's warps, and DW's clearing warp
+            mbar_init(smem_u32(&item_bar[F_ITEMS + i]), 3 + F_EPI_WARPS + (OP == DW));
+        }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -654,16 +689,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const uint64_t limit = p.wait_limit_ns;
-    const Tiles<OP> tiles(p, table);
+    Feed feed(smem, smem_u32(item_bar));
 
     if (warp == 0) {
         // ------------------------------------------------------ loads of A, of B
-        if (lane == 0) load_operand<OP, true>(p, tiles, smem, pair, npairs, rank, abort_flag);
+        if (lane == 0) load_operand<OP, true>(p, feed, smem, rank, abort_flag);
     } else if (warp == F_LOAD_B_WARP) {
-        if (lane == 0) load_operand<OP, false>(p, tiles, smem, pair, npairs, rank, abort_flag);
+        if (lane == 0) load_operand<OP, false>(p, feed, smem, rank, abort_flag);
     } else if (warp == 1) {
         // ------------------------------------------------- products (leader)
-        if (lane == 0 && rank == 0) {
+        if (lane == 0 && rank != 0) {
+            // the other CTA's thread lets its tiles pass
+            for (Item x; feed.next<false>(x, abort_flag, limit) && x.e >= 0;) {
+            }
+        } else if (lane == 0) {
             uint32_t step = 0;
             uint32_t full_phase = 0, patch_phase = 0;       // a bit a stage
             uint32_t uses[2] = {0, 0};
@@ -671,8 +710,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             bool ok = true, any = false;
             const uint64_t a_desc = smem_desc(smem_u32(smem), A_MN ? F_BOX : 16, 1024);
             const uint64_t b_desc = smem_desc(smem_u32(smem + F_OP_BYTES), B_MN ? F_BOX : 16, 1024);
-            for (int32_t it = pair; ok && it < tiles.total; it += npairs) {
-                const Item x = tiles.at(it);
+            for (Item x; ok;) {
+                ok = feed.next<false>(x, abort_flag, limit);
+                if (!ok || x.e < 0) break;
                 if (x.steps == 0) continue;
                 const uint32_t use = acc ? uses[1]++ : uses[0]++;
                 if (!wait_soon(smem_u32(&tempty_bar[acc]), (use & 1) ^ 1, abort_flag, &g_ffn_err, limit)) {
@@ -709,13 +749,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 wait_quiet(smem_u32(drain_bar), 0, limit);
             }
         }
+    } else if (warp == F_TILE_WARP) {
+        // ------------------------------------------------------------ tiles
+        if (lane == 0) {
+            const Tiles<OP> tiles(p, table);
+            Item* const items = reinterpret_cast<Item*>(smem + F_ITEM_OFF);
+            int32_t it = pair;
+            for (uint32_t n = 0;; ++n, it += npairs) {
+                Item x{};
+                x.e = -1;
+                if (it < tiles.total) x = tiles.at(it);
+                const uint32_t slot = n % F_ITEMS;
+                if (!wait_soon(smem_u32(&item_bar[F_ITEMS + slot]), (n / F_ITEMS & 1) ^ 1, abort_flag, &g_ffn_err,
+                               limit))
+                    break;
+                items[slot] = x;
+                mbar_arrive(smem_u32(&item_bar[slot]));
+                if (x.e < 0) break;
+            }
+        }
     } else if (warp == F_PATCH_WARP) {
         // ---------------------------------------------------- short steps of DW
         if constexpr (OP == DW) {
             uint32_t step = 0, phase = 0;
             const uint32_t patch_leader = map_to_rank(smem_u32(patch_bar), 0);
-            for (int32_t it = pair; it < tiles.total; it += npairs) {
-                const Item x = tiles.at(it);
+            for (Item x; feed.next<true>(x, abort_flag, limit) && x.e >= 0;) {
                 step += x.steps;
                 if (!x.steps || !x.tail) continue;
                 const uint32_t slot = (step - 1) % F_STAGES;
@@ -745,10 +803,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const uint32_t tempty_leader = map_to_rank(smem_u32(tempty_bar), 0);
         uint32_t uses[2] = {0, 0};
         uint32_t acc = 0;
-        // what DHIDDEN reads beside the sums, 16 columns ahead of their use
+        // what DHIDDEN reads beside the sums, 16 columns ahead of their use, in
+        // two sets of registers (one set and a copy waits for the loads that
+        // it has just asked for: 1950 cycles for 16 columns, not 1150)
         constexpr int UNITS = Units<OP>::N;
-        uint4 kg[UNITS], ku[UNITS];
-        auto fetch = [&](const Item& x, int c) {
+        uint4 kg[2][UNITS], ku[2][UNITS];
+        auto fetch = [&](const Item& x, int c, uint4 (&kg)[UNITS], uint4 (&ku)[UNITS]) {
             const int row0 = x.n0 + c * F_COLS + tid / 16, m = x.m0 + static_cast<int>(rank) * 128 + tid % 16 * 8;
             const int64_t at = row0 * p.ld_kept + m;
             const __nv_bfloat16* const g = static_cast<const __nv_bfloat16*>(p.gate) + at;
@@ -766,26 +826,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 }
             }
         };
-        for (int32_t it = pair; it < tiles.total; it += npairs) {
-            const Item x = tiles.at(it);
-            if constexpr (OP == DHIDDEN) fetch(x, team);
-            if (x.steps) {
-                const uint32_t use = acc ? uses[1]++ : uses[0]++;
-                const bool got = wait_soon(smem_u32(&tfull_bar[acc]), use & 1, abort_flag, &g_ffn_err, limit);
-                // the team's barriers need all four warps: a wait that ran out
-                // for one leaves them all
-                int bad = !got;
-                asm volatile(
-                    "{\n\t.reg .pred a, b;\n\t"
-                    "setp.ne.s32 a, %0, 0;\n\t"
-                    "barrier.red.or.pred b, %1, 128, a;\n\t"
-                    "selp.s32 %0, 1, 0, b;\n\t}"
-                    : "+r"(bad)
-                    : "r"(1 + team)
-                    : "memory");
-                if (bad) break;
-                tc_fence_after();
+        for (Item x;;) {
+            bool got = feed.next<true>(x, abort_flag, limit);
+            if (got && x.e >= 0) {
+                if constexpr (OP == DHIDDEN) fetch(x, team, kg[0], ku[0]);
+                if (x.steps) {
+                    const uint32_t use = acc ? uses[1]++ : uses[0]++;
+                    got = wait_soon(smem_u32(&tfull_bar[acc]), use & 1, abort_flag, &g_ffn_err, limit);
+                }
             }
+            // the team's barriers need all four warps: a wait that ran out for
+            // one leaves them all
+            int bad = !got;
+            asm volatile(
+                "{\n\t.reg .pred a, b;\n\t"
+                "setp.ne.s32 a, %0, 0;\n\t"
+                "barrier.red.or.pred b, %1, 128, a;\n\t"
+                "selp.s32 %0, 1, 0, b;\n\t}"
+                : "+r"(bad)
+                : "r"(1 + team)
+                : "memory");
+            if (bad || x.e < 0) break;
+            tc_fence_after();
             const uint32_t taddr = tmem_base + acc * 256 + (static_cast<uint32_t>(lg * 32) << 16);
             const int n_real = x.n_end - x.n0;
             const int m0 = x.m0 + static_cast<int>(rank) * (OP == UP ? 64 : 128);
@@ -845,7 +907,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 }
             }
             if constexpr (OP == UP || OP == DHIDDEN || OP == DW) {
-                for (int c = flat ? last + 1 : team; c <= last; c += 2) {
+                auto turn_and_finish = [&](int c, uint4 (&g8)[UNITS], uint4 (&u8)[UNITS], uint4 (&g8_next)[UNITS],
+                                           uint4 (&u8_next)[UNITS]) {
                     const int n0 = x.n0 + c * F_COLS;
                     uint32_t raw[16];
                     if (x.steps) {
@@ -860,19 +923,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     for (int i = 0; i < F_COLS; ++i)
                         turn[i * F_ROW + lg * 32 + lane] = __uint_as_float(raw[i]);
                     team_sync(team);
-                    uint4 g8[UNITS], u8[UNITS];
-                    if constexpr (OP == DHIDDEN) {
-#pragma unroll
-                        for (int i = 0; i < UNITS; ++i) {
-                            g8[i] = kg[i];
-                            u8[i] = ku[i];
-                        }
-                        if (c < last) fetch(x, c + 2);
-                    }
+                    if (OP == DHIDDEN && c < last) fetch(x, c + 2, g8_next, u8_next);
                     if (OP != DW && p.vec && n0 + F_COLS <= x.n_end && m0 + (OP == UP ? 64 : 128) <= m_end)
                         finish_turned<OP, true>(p, x, turn, n0, m0, m_end, tid, g8, u8);
                     else
                         finish_turned<OP, false>(p, x, turn, n0, m0, m_end, tid, g8, u8);
+                };
+                for (int c = flat ? last + 1 : team; c <= last; c += 4) {
+                    turn_and_finish(c, kg[0], ku[0], kg[1], ku[1]);
+                    if (c + 2 <= last) turn_and_finish(c + 2, kg[1], ku[1], kg[0], ku[0]);
                 }
             }
             if (x.steps) acc ^= 1;
