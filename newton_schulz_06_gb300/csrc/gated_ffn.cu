@@ -41,7 +41,6 @@ using namespace ptx;
 
 constexpr int F_K = 64;                            // of the sums, a step
 constexpr int F_BOX = 64 * 64 * 2;                 // a TMA box: 64 rows of 64 bf16
-constexpr int F_STAGES = 6;
 constexpr int F_OP_BYTES = 2 * F_BOX;              // an operand's part of a CTA, a step
 constexpr int F_STAGE_BYTES = 2 * F_OP_BYTES;
 constexpr int F_EXPERTS = 1024;
@@ -51,12 +50,7 @@ constexpr int F_COLS16 = 32;                       // and in bf16
 constexpr int F_ROW16 = 136;
 constexpr int F_TURN_BYTES = F_COLS16 * F_ROW16 * 2;
 static_assert(F_TURN_BYTES >= F_COLS * F_ROW * 4 && F_TURN_BYTES % 16 == 0, "a team's buffer");
-constexpr int F_BAR_OFF = F_STAGES * F_STAGE_BYTES;
-constexpr int F_ITEM_OFF = F_BAR_OFF + 384;       // tiles handed out
-constexpr int F_TURN_OFF = F_ITEM_OFF + 256;
-constexpr int F_TABLE_OFF = F_TURN_OFF + 2 * F_TURN_BYTES;       // two teams
-constexpr int F_SMEM = F_TABLE_OFF + 3 * (F_EXPERTS + 1) * 4 + 1024;
-static_assert(F_SMEM <= 232448, "shared memory per CTA");
+constexpr int F_KEPT_BYTES = 4 * 128 * 16;         // a team's g and u of 16 columns (DHIDDEN)
 constexpr int F_EPI_WARPS = 8;
 constexpr int F_PATCH_WARP = 2 + F_EPI_WARPS;
 constexpr int F_LOAD_B_WARP = F_PATCH_WARP + 1;
@@ -70,6 +64,19 @@ constexpr int F_BAND = 8;
 __device__ int g_ffn_err;
 
 enum Op { UP, DOWN, DHIDDEN, DX, DW };
+
+// Where things are in shared memory.
+template <int OP>
+struct Space {
+    static constexpr int STAGES = OP == DHIDDEN ? 5 : 6;
+    static constexpr int BARS = STAGES * F_STAGE_BYTES;
+    static constexpr int ITEMS = BARS + 384;                 // tiles handed out
+    static constexpr int TURN = ITEMS + 256;
+    static constexpr int KEPT = TURN + 2 * F_TURN_BYTES;     // two teams'
+    static constexpr int TABLE = KEPT + (OP == DHIDDEN ? 2 * F_KEPT_BYTES : 0);
+    static constexpr int BYTES = TABLE + 3 * (F_EXPERTS + 1) * 4 + 1024;
+    static_assert(BYTES <= 232448, "shared memory per CTA");
+};
 
 // One output matrix (or as many as there are experts).
 struct Out {
@@ -235,8 +242,8 @@ struct Feed {
     const Item* items;
     uint32_t full, empty;
     uint32_t n = 0;
-    __device__ __forceinline__ Feed(const uint8_t* smem, uint32_t bars)
-        : items(reinterpret_cast<const Item*>(smem + F_ITEM_OFF)), full(bars), empty(bars + 8 * F_ITEMS) {}
+    __device__ __forceinline__ Feed(const void* at, uint32_t bars)
+        : items(static_cast<const Item*>(at)), full(bars), empty(bars + 8 * F_ITEMS) {}
     // The next tile, for a thread or a whole warp: false where the wait ran
     // out.
     template <bool WARP>
@@ -330,6 +337,11 @@ __device__ __forceinline__ void store_turned(uint32_t to, const uint32_t (&r)[4]
                  "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
+// 16 bytes to shared memory, and a wait for all of this thread's.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // A barrier of one team's 128 threads.
 __device__ __forceinline__ void team_sync(int team) {
     asm volatile("bar.sync %0, 128;" ::"r"(1 + team) : "memory");
@@ -510,7 +522,8 @@ template <int OP, bool A>
 __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint8_t* smem, uint32_t rank,
                                              volatile int* abort_flag) {
     constexpr bool A_MN = OP == DHIDDEN || OP == DX || OP == DW, B_MN = OP == DW;
-    const uint32_t full = smem_u32(smem + F_BAR_OFF), empty = full + 8 * F_STAGES, tail_bar = empty + 8 * F_STAGES;
+    constexpr int STAGES = Space<OP>::STAGES;
+    const uint32_t full = smem_u32(smem + Space<OP>::BARS), empty = full + 8 * STAGES, tail_bar = empty + 8 * STAGES;
     const uint32_t full_leader = map_to_rank(full, 0), tail_own = map_to_rank(tail_bar, rank);
     const uint32_t stage0 = smem_u32(smem) + (A ? 0 : F_OP_BYTES);
     uint32_t slot = 0, parity = 1;
@@ -578,7 +591,7 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
                 } else {
                     load_box(to, tb, bar, k0, n0, 0);
                 }
-                if (++slot == F_STAGES) {
+                if (++slot == STAGES) {
                     slot = 0;
                     parity ^= 1;
                 }
@@ -588,7 +601,7 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
     if (!ok && A) {
         // the last loads of each stage (the leader's barriers count both
         // CTAs', and both operands')
-        for (uint32_t i = 0; i < F_STAGES; ++i) {
+        for (uint32_t i = 0; i < STAGES; ++i) {
             if (!(used >> i & 1)) continue;
             if (tails >> i & 1) wait_quiet(tail_bar + 8 * i, (tail_phase >> i & 1) ^ 1, p.wait_limit_ns);
             else if (rank == 0) wait_quiet(full + 8 * i, (full_phase >> i & 1) ^ 1, p.wait_limit_ns);
@@ -602,17 +615,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + F_BAR_OFF);   // a step's loads (leader's)
-    uint64_t* empty_bar = full_bar + F_STAGES;      // its products have run
-    uint64_t* tail_bar = empty_bar + F_STAGES;      // DW: this CTA's loads of a short step
-    uint64_t* patch_bar = tail_bar + F_STAGES;      // which both CTAs have cleared (leader's)
-    uint64_t* tfull_bar = patch_bar + F_STAGES;
+    using S = Space<OP>;
+    constexpr int STAGES = S::STAGES;
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + S::BARS);   // a step's loads (leader's)
+    uint64_t* empty_bar = full_bar + STAGES;      // its products have run
+    uint64_t* tail_bar = empty_bar + STAGES;      // DW: this CTA's loads of a short step
+    uint64_t* patch_bar = tail_bar + STAGES;      // which both CTAs have cleared (leader's)
+    uint64_t* tfull_bar = patch_bar + STAGES;
     uint64_t* tempty_bar = tfull_bar + 2;
     uint64_t* drain_bar = tempty_bar + 2;
     uint64_t* item_bar = drain_bar + 1;             // a tile is there; its place is free
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_bar + 2 * F_ITEMS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int32_t* const table = reinterpret_cast<int32_t*>(smem + F_TABLE_OFF);
+    int32_t* const table = reinterpret_cast<int32_t*>(smem + S::TABLE);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -622,7 +637,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     constexpr bool A_MN = OP == DHIDDEN || OP == DX || OP == DW, B_MN = OP == DW;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < F_STAGES; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&full_bar[s]), 1);
             mbar_init(smem_u32(&empty_bar[s]), 1);
             mbar_init(smem_u32(&tail_bar[s]), 1);
@@ -689,7 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const uint64_t limit = p.wait_limit_ns;
-    Feed feed(smem, smem_u32(item_bar));
+    Feed feed(smem + S::ITEMS, smem_u32(item_bar));
 
     if (warp == 0) {
         // ------------------------------------------------------ loads of A, of B
@@ -722,7 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 tc_fence_after();
                 const uint32_t idesc = instr_desc(256, x.n, B_MN) | (A_MN ? 1u << 15 : 0u);
                 for (int s = 0; s < x.steps; ++s, ++step) {
-                    const uint32_t slot = step % F_STAGES;
+                    const uint32_t slot = step % STAGES;
                     const bool tail = OP == DW && x.tail && s == x.steps - 1;
                     const uint32_t bar = smem_u32(tail ? &patch_bar[slot] : &full_bar[slot]);
                     uint32_t& phase = tail ? patch_phase : full_phase;
@@ -753,7 +768,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         // ------------------------------------------------------------ tiles
         if (lane == 0) {
             const Tiles<OP> tiles(p, table);
-            Item* const items = reinterpret_cast<Item*>(smem + F_ITEM_OFF);
+            Item* const items = reinterpret_cast<Item*>(smem + S::ITEMS);
             int32_t it = pair;
             for (uint32_t n = 0;; ++n, it += npairs) {
                 Item x{};
@@ -776,7 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             for (Item x; feed.next<true>(x, abort_flag, limit) && x.e >= 0;) {
                 step += x.steps;
                 if (!x.steps || !x.tail) continue;
-                const uint32_t slot = (step - 1) % F_STAGES;
+                const uint32_t slot = (step - 1) % STAGES;
                 const bool got = wait_soon(smem_u32(&tail_bar[slot]), phase >> slot & 1, abort_flag,
                                            &g_ffn_err, limit);
                 if (!__all_sync(0xffffffffu, got)) break;
@@ -798,38 +813,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const int lg = warp & 3;                    // this warp's 32 TMEM lanes
         const int team = (warp - 2) / 4;
         const int tid = (warp - 2) % 4 * 32 + lane;
-        uint8_t* const turn_at = smem + F_TURN_OFF + team * F_TURN_BYTES;
+        uint8_t* const turn_at = smem + S::TURN + team * F_TURN_BYTES;
         float* const turn = reinterpret_cast<float*>(turn_at);
         const uint32_t tempty_leader = map_to_rank(smem_u32(tempty_bar), 0);
         uint32_t uses[2] = {0, 0};
         uint32_t acc = 0;
-        // what DHIDDEN reads beside the sums, 16 columns ahead of their use, in
-        // two sets of registers (one set and a copy waits for the loads that
-        // it has just asked for: 1950 cycles for 16 columns, not 1150)
+        // what DHIDDEN reads beside the sums comes 16 columns ahead of its use
+        // by asynchronous copies (loads to registers made what the thread then
+        // reads from shared memory wait for them too: 1950 cycles for 16
+        // columns, not 1150)
         constexpr int UNITS = Units<OP>::N;
-        uint4 kg[2][UNITS], ku[2][UNITS];
-        auto fetch = [&](const Item& x, int c, uint4 (&kg)[UNITS], uint4 (&ku)[UNITS]) {
+        uint4* const kept = reinterpret_cast<uint4*>(smem + S::KEPT + team * F_KEPT_BYTES) + tid;
+        auto fetch = [&](const Item& x, int c) {
             const int row0 = x.n0 + c * F_COLS + tid / 16, m = x.m0 + static_cast<int>(rank) * 128 + tid % 16 * 8;
             const int64_t at = row0 * p.ld_kept + m;
-            const __nv_bfloat16* const g = static_cast<const __nv_bfloat16*>(p.gate) + at;
-            const __nv_bfloat16* const u = static_cast<const __nv_bfloat16*>(p.up) + at;
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
-                kg[i] = ku[i] = make_uint4(0u, 0u, 0u, 0u);
-                const int left = row0 + 8 * i < x.n_end ? p.m[0] - m : 0;
-                if (p.vec && left >= 8) {
-                    kg[i] = *reinterpret_cast<const uint4*>(g + 8 * i * p.ld_kept);
-                    ku[i] = *reinterpret_cast<const uint4*>(u + 8 * i * p.ld_kept);
-                } else if (left > 0) {
-                    kg[i] = load8(g + 8 * i * p.ld_kept, left, false);
-                    ku[i] = load8(u + 8 * i * p.ld_kept, left, false);
+                if (p.vec && row0 + 8 * i < x.n_end && m + 8 <= p.m[0]) {
+                    copy16(kept + 256 * i, static_cast<const __nv_bfloat16*>(p.gate) + at + 8 * i * p.ld_kept);
+                    copy16(kept + 256 * i + 128, static_cast<const __nv_bfloat16*>(p.up) + at + 8 * i * p.ld_kept);
                 }
             }
         };
         for (Item x;;) {
             bool got = feed.next<true>(x, abort_flag, limit);
             if (got && x.e >= 0) {
-                if constexpr (OP == DHIDDEN) fetch(x, team, kg[0], ku[0]);
+                if constexpr (OP == DHIDDEN) fetch(x, team);
                 if (x.steps) {
                     const uint32_t use = acc ? uses[1]++ : uses[0]++;
                     got = wait_soon(smem_u32(&tfull_bar[acc]), use & 1, abort_flag, &g_ffn_err, limit);
@@ -907,8 +916,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 }
             }
             if constexpr (OP == UP || OP == DHIDDEN || OP == DW) {
-                auto turn_and_finish = [&](int c, uint4 (&g8)[UNITS], uint4 (&u8)[UNITS], uint4 (&g8_next)[UNITS],
-                                           uint4 (&u8_next)[UNITS]) {
+                for (int c = flat ? last + 1 : team; c <= last; c += 2) {
                     const int n0 = x.n0 + c * F_COLS;
                     uint32_t raw[16];
                     if (x.steps) {
@@ -923,15 +931,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     for (int i = 0; i < F_COLS; ++i)
                         turn[i * F_ROW + lg * 32 + lane] = __uint_as_float(raw[i]);
                     team_sync(team);
-                    if (OP == DHIDDEN && c < last) fetch(x, c + 2, g8_next, u8_next);
-                    if (OP != DW && p.vec && n0 + F_COLS <= x.n_end && m0 + (OP == UP ? 64 : 128) <= m_end)
+                    if (OP != DW && p.vec && n0 + F_COLS <= x.n_end && m0 + (OP == UP ? 64 : 128) <= m_end) {
+                        uint4 g8[UNITS], u8[UNITS];
+                        if constexpr (OP == DHIDDEN) {
+                            copies_done();
+#pragma unroll
+                            for (int i = 0; i < UNITS; ++i) {
+                                g8[i] = kept[256 * i];
+                                u8[i] = kept[256 * i + 128];
+                            }
+                        }
+                        if (OP == DHIDDEN && c < last) fetch(x, c + 2);
                         finish_turned<OP, true>(p, x, turn, n0, m0, m_end, tid, g8, u8);
-                    else
+                    } else {
+                        uint4 g8[UNITS], u8[UNITS];
+                        if constexpr (OP == DHIDDEN) {
+                            copies_done();
+#pragma unroll
+                            for (int i = 0; i < UNITS; ++i) {
+                                const int row = n0 + tid / 16 + 8 * i, m = m0 + tid % 16 * 8;
+                                const int64_t at = row * p.ld_kept + m;
+                                const int left = row < x.n_end ? m_end - m : 0;
+                                g8[i] = load8(static_cast<const __nv_bfloat16*>(p.gate) + at, left, p.vec);
+                                u8[i] = load8(static_cast<const __nv_bfloat16*>(p.up) + at, left, p.vec);
+                            }
+                        }
+                        if (OP == DHIDDEN && c < last) fetch(x, c + 2);
                         finish_turned<OP, false>(p, x, turn, n0, m0, m_end, tid, g8, u8);
-                };
-                for (int c = flat ? last + 1 : team; c <= last; c += 4) {
-                    turn_and_finish(c, kg[0], ku[0], kg[1], ku[1]);
-                    if (c + 2 <= last) turn_and_finish(c + 2, kg[1], ku[1], kg[0], ku[0]);
+                    }
                 }
             }
             if (x.steps) acc ^= 1;
@@ -979,7 +1006,7 @@ bool tma_reads(const Operand& o) {
            (o.matrices <= 1 || o.stride % 8 == 0);
 }
 
-struct Space {
+struct Workspace {
     size_t bytes = 0;
     size_t take(size_t n) {
         const size_t at = bytes;
@@ -1076,19 +1103,21 @@ using Kernel = void (*)(FfnLaunch);
 cudaError_t launch_op(Op op, const FfnLaunch& p, int64_t items, cudaStream_t s) {
     static const Kernel kernel[5] = {gated_ffn_kernel<UP>, gated_ffn_kernel<DOWN>, gated_ffn_kernel<DHIDDEN>,
                                      gated_ffn_kernel<DX>, gated_ffn_kernel<DW>};
+    static const int size[5] = {Space<UP>::BYTES, Space<DOWN>::BYTES, Space<DHIDDEN>::BYTES, Space<DX>::BYTES,
+                                Space<DW>::BYTES};
     static int attr_done[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_done[dev]) {
         for (int i = 0; i < 5; ++i) {
             const cudaError_t e =
-                cudaFuncSetAttribute(kernel[i], cudaFuncAttributeMaxDynamicSharedMemorySize, F_SMEM);
+                cudaFuncSetAttribute(kernel[i], cudaFuncAttributeMaxDynamicSharedMemorySize, size[i]);
             if (e != cudaSuccess) return e;
         }
         if (dev >= 0 && dev < 64) attr_done[dev] = 1;
     }
     const int pairs = static_cast<int>(items < F_PAIRS ? items : F_PAIRS);
-    return launch_kernel(kernel[op], dim3(2 * pairs), dim3(F_THREADS), F_SMEM, s, p);
+    return launch_kernel(kernel[op], dim3(2 * pairs), dim3(F_THREADS), size[op], s, p);
 }
 
 FfnLaunch common(const int32_t* offsets, int64_t rows, int64_t experts, int act) {
@@ -1105,7 +1134,7 @@ FfnLaunch common(const int32_t* offsets, int64_t rows, int64_t experts, int act)
 int64_t row_tiles(int64_t rows, int64_t experts) { return rows / 256 + experts; }
 
 struct Forward {
-    Space space;
+    Workspace space;
     Operand x, gate, up, down, h;
     size_t h_at;
 };
@@ -1122,7 +1151,7 @@ Forward plan(const muon_gated_ffn_args& a) {
 }
 
 struct Backward {
-    Space space;
+    Workspace space;
     Operand dy, x, gate, up, down, dg, du, h;
     size_t d_at[3] = {0, 0, 0};      // dg, du, h where the caller gives none
     bool own[3] = {false, false, false};
