@@ -337,6 +337,21 @@ __device__ __forceinline__ void store_turned(uint32_t to, const uint32_t (&r)[4]
                  "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
+// Whether a barrier's phase is over, without waiting.  Asked of the next step's
+// barrier before this step's work is issued, the answer's 220 cycles are hidden
+// behind it (the products' thread took 590 cycles a step otherwise, of 512 that
+// the products take).
+__device__ __forceinline__ bool is_over(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, P;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // 16 bytes to shared memory, and a wait for all of this thread's.
 __device__ __forceinline__ void copy16(void* to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
@@ -530,7 +545,7 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
     // a bit a stage: it has been loaded, its last load was a short step's, and
     // the parities that follow its loads of either kind
     uint32_t used = 0, tails = 0, tail_phase = 0, full_phase = 0;
-    bool ok = true;
+    bool ok = true, free_next = false;
     for (Item x; ok;) {
         ok = feed.next<false>(x, abort_flag, p.wait_limit_ns);
         if (!ok || x.e < 0) break;
@@ -550,10 +565,12 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
             int k0 = OP == DW ? x.t0 : 0;
 #pragma unroll 1
             for (; s < end; ++s, k0 += F_K) {
-                if (!wait_soon(empty + 8 * slot, parity, abort_flag, &g_ffn_err, p.wait_limit_ns)) {
+                if (!free_next && !wait_soon(empty + 8 * slot, parity, abort_flag, &g_ffn_err, p.wait_limit_ns)) {
                     ok = false;
                     break;
                 }
+                const uint32_t ahead = slot + 1 == STAGES ? 0 : slot + 1;
+                free_next = is_over(empty + 8 * ahead, ahead ? parity : parity ^ 1);
                 uint32_t bar = full_leader + 8 * slot;
                 if (OP == DW && x.tail && s == x.steps - 1) {
                     if (A) mbar_expect_tx(tail_bar + 8 * slot, bytes);
@@ -718,7 +735,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             for (Item x; feed.next<false>(x, abort_flag, limit) && x.e >= 0;) {
             }
         } else if (lane == 0) {
-            uint32_t step = 0;
+            uint32_t slot = 0;
             uint32_t full_phase = 0, patch_phase = 0;       // a bit a stage
             uint32_t uses[2] = {0, 0};
             uint32_t acc = 0;
@@ -736,17 +753,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t idesc = instr_desc(256, x.n, B_MN) | (A_MN ? 1u << 15 : 0u);
-                for (int s = 0; s < x.steps; ++s, ++step) {
-                    const uint32_t slot = step % STAGES;
-                    const bool tail = OP == DW && x.tail && s == x.steps - 1;
+                const int short_step = OP == DW && x.tail ? x.steps - 1 : -1;
+                bool there = false;
+#pragma unroll 1
+                for (int s = 0; s < x.steps; ++s) {
+                    const bool tail = s == short_step;
                     const uint32_t bar = smem_u32(tail ? &patch_bar[slot] : &full_bar[slot]);
                     uint32_t& phase = tail ? patch_phase : full_phase;
-                    if (!wait_soon(bar, phase >> slot & 1, abort_flag, &g_ffn_err, limit)) {
+                    if (!there && !wait_soon(bar, phase >> slot & 1, abort_flag, &g_ffn_err, limit)) {
                         ok = false;
                         break;
                     }
                     phase ^= 1u << slot;
-                    tc_fence_after();
+                    if (tail) tc_fence_after();
+                    const uint32_t next = slot + 1 == STAGES ? 0 : slot + 1;
+                    there = s + 1 != short_step && is_over(smem_u32(&full_bar[next]), full_phase >> next & 1);
                     const uint64_t ad = a_desc + (slot * F_STAGE_BYTES >> 4);
                     const uint64_t bd = b_desc + (slot * F_STAGE_BYTES >> 4);
 #pragma unroll
@@ -755,6 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                                  bd + uint64_t(kk * (B_MN ? 2048 : 32) >> 4), idesc, (s || kk) ? 1u : 0u);
                     any = true;
                     commit_pair_multicast(smem_u32(&empty_bar[slot]));
+                    slot = next;
                 }
                 if (ok) commit_pair_multicast(smem_u32(&tfull_bar[acc]));
                 acc ^= 1;
