@@ -28,6 +28,8 @@
 // products run.  Pairs walk the tiles in turn.
 //
 // Every wait is bounded; one that runs out raises g_ffn_err (muon_ops_sync).
+#include <algorithm>
+
 #include <cudaTypedefs.h>
 
 #include "ops_internal.h"
@@ -105,6 +107,12 @@ struct FfnLaunch {
     int32_t m[2], k;         // extents; DW: m[0] is hidden, m[1] inner; else m[0]
     int32_t a_by_expert[3];  // an expert's own matrix, or one for all
     int32_t products;        // DW: which of them, as bits
+    int32_t tile_n;          // one dense block: rows of N a tile, a multiple of 32
+    int32_t splits;          // parts of the sums that tiles of their own take
+    float* part;             // splits > 1: their sums, split by split,
+    int64_t part_stride;
+    int64_t part_ld[2];      // in rows of these lengths (by m's extent; UP: g, then u),
+    int64_t part_at[3];      // DW: a product's after another's
     int32_t act;
     int32_t out_f32, accumulate;
     unsigned long long wait_limit_ns;
@@ -139,7 +147,9 @@ struct alignas(16) Item {
     int32_t m0, n0;          // its first m (UP: of h), its first row of N
     int32_t n_end;           // its rows of N end here
     int32_t n;               // the instruction's N
-    int32_t t0, steps;       // DW: the expert's first token; steps of 64
+    int32_t steps;           // of 64,
+    int32_t s0, split;       // from this one of the whole sum on; which part of it that is
+    int32_t t0;              // DW: the first token
     int32_t tail;            // DW: tokens of the last step, if not 64
 };
 static_assert(F_ITEMS * sizeof(Item) <= 256, "tiles handed out");
@@ -152,6 +162,7 @@ struct Tiles {
     const FfnLaunch& p;
     const int32_t *begin, *first, *high;     // experts' first rows, first tile rows, rows of a tile
     int32_t total, steps;
+    Divisor whole;                           // tiles of the whole sums
     Divisor tiles_m, band;                   // tiles across M, and in a band
     Divisor per, across[2], bands[2];        // DW: a matrix's tiles; by product (2: the last one)
     int32_t base[2];                         // the second and third product's first tile
@@ -173,19 +184,22 @@ struct Tiles {
                 across[i].set((p.m[i] + 255) / 256);
                 bands[i].set(F_BAND * across[i].d);
             }
-            total = all * p.experts;
+            whole.set(all * p.experts);
         } else {
             tiles_m.set((p.m[0] + (OP == UP ? 127 : 255)) / (OP == UP ? 128 : 256));
             band.set(F_BAND * tiles_m.d);
-            total = first[p.experts] * tiles_m.d;
+            whole.set(first[p.experts] * tiles_m.d);
             steps = (p.k + F_K - 1) / F_K * (OP == DX ? 2 : 1);
         }
+        total = whole.d * p.splits;
     }
     __device__ __forceinline__ Item at(int32_t it) const {
         Item x;
         x.tail = 0;
         x.j = 0;
-        int32_t in, tn, size, end;
+        x.split = p.splits > 1 ? whole.of(it) : 0;
+        it -= x.split * whole.d;
+        int32_t in, tn, size, end, all;
         Divisor tm, b;
         if constexpr (OP == DW) {
             x.e = per.of(it);
@@ -199,7 +213,7 @@ struct Tiles {
             tn = x.j == 2 ? across[0].d : across[1].d;
             x.t0 = begin[x.e];
             const int32_t len = begin[x.e + 1] - x.t0;
-            x.steps = (len + F_K - 1) / F_K;
+            all = (len + F_K - 1) / F_K;
             x.tail = len % F_K;
         } else {
             // the expert whose tiles these are
@@ -218,7 +232,16 @@ struct Tiles {
             size = high[lo];
             end = begin[lo + 1];
             x.t0 = 0;
-            x.steps = steps;
+            all = steps;
+        }
+        x.s0 = 0;
+        x.steps = all;
+        if (p.splits > 1) {
+            x.s0 = static_cast<int32_t>(int64_t(all) * x.split / p.splits);
+            const int32_t s1 = static_cast<int32_t>(int64_t(all) * (x.split + 1) / p.splits);
+            x.steps = s1 - x.s0;
+            x.t0 += x.s0 * F_K;
+            if (s1 < all) x.tail = 0;
         }
         // bands of eight tiles of N, column by column: the tiles that run
         // together share their operands in L2
@@ -488,6 +511,55 @@ struct Units {
     static constexpr int GROUPS = OP == UP ? 8 : 16;      // of eight outputs of a row
     static constexpr int N = F_COLS * GROUPS / 128;       // a thread's
 };
+
+// Eight neighbours of an output row: v are their sums (UP: g's, and w u's).
+template <int OP, bool WHOLE>
+__device__ __forceinline__ void finish8(const FfnLaunch& p, int e, int j, int row, int m, int left, float (&v)[8],
+                                        float (&w)[8], const uint4& g8, const uint4& u8) {
+    auto put = [&](const Out& o, const float (&f)[8]) {
+        const int64_t at = row * o.ld + m;
+        if (WHOLE) store8_bf16(static_cast<__nv_bfloat16*>(o.p) + at, f);
+        else put8(o, at, left, f);
+    };
+    float a[8], d[8];
+    if constexpr (OP == UP) {
+        activate8(p.act, v, a, d);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[q] *= w[q];
+        put(p.out[0], a);
+        if (p.out[1].p) {
+            put(p.out[1], v);
+            put(p.out[2], w);
+        }
+    } else if constexpr (OP == DHIDDEN) {
+        float g[8];
+        widen8(g8, g);
+        widen8(u8, w);
+        activate8(p.act, g, a, d);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            d[q] *= v[q] * w[q];
+            v[q] *= a[q];
+            a[q] *= w[q];
+        }
+        put(p.out[0], d);
+        put(p.out[1], v);
+        if (p.out[2].p) put(p.out[2], a);
+    } else if constexpr (OP == DW) {
+        const Out& o = p.out[j];
+        put8_grad(o, e * o.stride + row * o.ld + m, left, p.out_f32, p.accumulate, v);
+    } else {
+        put(p.out[0], v);
+    }
+}
+
+// DHIDDEN's g and u of eight places, of which `left` are there.
+__device__ __forceinline__ void load_kept(const FfnLaunch& p, int row, int m, int left, uint4& g8, uint4& u8) {
+    const int64_t at = row * p.ld_kept + m;
+    g8 = load8(static_cast<const __nv_bfloat16*>(p.gate) + at, left, p.vec);
+    u8 = load8(static_cast<const __nv_bfloat16*>(p.up) + at, left, p.vec);
+}
+
 template <int OP, bool WHOLE>
 __device__ __forceinline__ void finish_turned(const FfnLaunch& p, const Item& x, const float* turn, int n0, int m0,
                                               int m_end, int tid, const uint4 (&g8)[Units<OP>::N],
@@ -498,40 +570,32 @@ __device__ __forceinline__ void finish_turned(const FfnLaunch& p, const Item& x,
         const int r = (tid + 128 * i) / GROUPS, group = tid % GROUPS;
         const int row = n0 + r, m = m0 + group * 8, left = WHOLE ? 8 : m_end - m;
         if (!WHOLE && (row >= x.n_end || left <= 0)) continue;
-        auto put = [&](const Out& o, const float (&f)[8]) {
-            const int64_t at = row * o.ld + m;
-            if (WHOLE) store8_bf16(static_cast<__nv_bfloat16*>(o.p) + at, f);
-            else put8(o, at, left, f);
-        };
-        float v[8], w[8], a[8], d[8];
+        float v[8], w[8];
         turned8(turn + r * F_ROW, group, v);
-        if constexpr (OP == UP) {
-            turned8(turn + r * F_ROW, 8 + group, w);
-            activate8(p.act, v, a, d);
+        if (OP == UP) turned8(turn + r * F_ROW, 8 + group, w);
+        finish8<OP, WHOLE>(p, x.e, x.j, row, m, left, v, w, g8[i], u8[i]);
+    }
+}
+
+// The sums of a part, as they are (rows of whole groups of eight).
+template <int OP>
+__device__ __forceinline__ void store_part(const FfnLaunch& p, const Item& x, const float* turn, int n0, int m0,
+                                           int m_end, int tid) {
+    constexpr int GROUPS = Units<OP>::GROUPS;
+    const int64_t ld = p.part_ld[OP == DW && x.j == 2];
+    float* const to = p.part + x.split * p.part_stride + (OP == DW ? p.part_at[x.j] : 0);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) a[q] *= w[q];
-            put(p.out[0], a);
-            if (p.out[1].p) {
-                put(p.out[1], v);
-                put(p.out[2], w);
-            }
-        } else if constexpr (OP == DHIDDEN) {
-            float g[8];
-            widen8(g8[i], g);
-            widen8(u8[i], w);
-            activate8(p.act, g, a, d);
+    for (int i = 0; i < Units<OP>::N; ++i) {
+        const int r = (tid + 128 * i) / GROUPS, group = tid % GROUPS;
+        const int row = n0 + r, m = m0 + group * 8;
+        if (row >= x.n_end || m >= m_end) continue;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                d[q] *= v[q] * w[q];
-                v[q] *= a[q];
-                a[q] *= w[q];
-            }
-            put(p.out[0], d);
-            put(p.out[1], v);
-            if (p.out[2].p) put(p.out[2], a);
-        } else {
-            const Out& o = p.out[x.j];
-            put8_grad(o, x.e * o.stride + row * o.ld + m, left, p.out_f32, p.accumulate, v);
+        for (int h = 0; h < (OP == UP ? 2 : 1); ++h) {
+            float v[8];
+            turned8(turn + r * F_ROW, 8 * h + group, v);
+            float4* const q = reinterpret_cast<float4*>(to + row * ld + h * (ld / 2) + m);
+            q[0] = make_float4(v[0], v[1], v[2], v[3]);
+            q[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
     }
 }
@@ -560,16 +624,17 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
         const uint32_t bytes = F_OP_BYTES + boxes * F_BOX;
         const int m0 = x.m0 + static_cast<int>(rank) * (OP == UP ? 64 : 128);
         const int n0 = x.n0 + static_cast<int>(rank) * (x.n / 2);
-        int s = 0;
+        int s = x.s0;
+        const int stop = x.s0 + x.steps, half = (p.k + F_K - 1) / F_K;
         // DX has two sums' worth of steps, of one operand pair each
 #pragma unroll 1
-        for (int part = 0; ok && part < (OP == DX ? 2 : 1); ++part) {
+        for (int part = OP == DX && s >= half; ok && s < stop; ++part) {
             const int j = OP == DW ? x.j : part;
-            const int end = OP == DX ? x.steps / 2 * (part + 1) : x.steps;
+            const int end = OP == DX && part == 0 ? min(half, stop) : stop;
             const Maps& m = p.maps[j];
             const int z = p.a_by_expert[j] ? x.e : 0, z1 = p.a_by_expert[1] ? x.e : 0;
             const CUtensorMap* const tb = boxes > 1 ? &m.b : &m.b64;
-            int k0 = OP == DW ? x.t0 : 0;
+            int k0 = OP == DW ? x.t0 : (OP == DX ? s - part * half : s) * F_K;
 #pragma unroll 1
             for (; s < end; ++s, k0 += F_K) {
                 if (!free_next && !wait_soon(empty + 8 * slot, parity, abort_flag, &g_ffn_err, p.wait_limit_ns)) {
@@ -579,7 +644,7 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
                 const uint32_t ahead = slot + 1 == STAGES ? 0 : slot + 1;
                 free_next = is_over(empty + 8 * ahead, ahead ? parity : parity ^ 1);
                 uint32_t bar = full_leader + 8 * slot;
-                if (OP == DW && x.tail && s == x.steps - 1) {
+                if (OP == DW && x.tail && s == stop - 1) {
                     if (A) mbar_expect_tx(tail_bar + 8 * slot, bytes);
                     tails |= 1u << slot;
                     tail_phase ^= 1u << slot;
@@ -707,8 +772,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             const int32_t before = __shfl_up_sync(0xffffffffu, b, 1);
             // tiles of the expert before e, and their rows
             const int32_t len = e ? b - (lane ? before : rows) : 0;
-            int32_t n = (len + 255) / 256;
-            if (n && e <= p.experts) table[2 * (p.experts + 1) + e - 1] = ((len + n - 1) / n + 31) & ~31;
+            int32_t n = p.tile_n ? (len + p.tile_n - 1) / p.tile_n : (len + 255) / 256;
+            if (n && e <= p.experts)
+                table[2 * (p.experts + 1) + e - 1] = p.tile_n ? p.tile_n : ((len + n - 1) / n + 31) & ~31;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int32_t v = __shfl_up_sync(0xffffffffu, n, o);
@@ -869,7 +935,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         for (Item x;;) {
             bool got = feed.next<true>(x, abort_flag, limit);
             if (got && x.e >= 0) {
-                if constexpr (OP == DHIDDEN) fetch(x, team);
+                if (OP == DHIDDEN && p.splits == 1) fetch(x, team);
                 if (x.steps) {
                     const uint32_t use = acc ? uses[1]++ : uses[0]++;
                     got = wait_soon(smem_u32(&tfull_bar[acc]), use & 1, abort_flag, &g_ffn_err, limit);
@@ -899,7 +965,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * acc);
             };
             // the teams take blocks of columns in turn; this one's last
-            const bool flat = OP == DOWN || OP == DX || (OP == DW && !p.out_f32 && !p.accumulate);
+            const bool flat = (OP == DOWN || OP == DX || (OP == DW && !p.out_f32 && !p.accumulate)) && p.splits == 1;
             int last = (n_real - 1) / (flat ? F_COLS16 : F_COLS);
             if ((last & 1) != team) --last;
             if (last < 0) release();
@@ -946,7 +1012,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     }
                 }
             }
-            if constexpr (OP == UP || OP == DHIDDEN || OP == DW) {
+            {
                 for (int c = flat ? last + 1 : team; c <= last; c += 2) {
                     const int n0 = x.n0 + c * F_COLS;
                     uint32_t raw[16];
@@ -962,7 +1028,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     for (int i = 0; i < F_COLS; ++i)
                         turn[i * F_ROW + lg * 32 + lane] = __uint_as_float(raw[i]);
                     team_sync(team);
-                    if (OP != DW && p.vec && n0 + F_COLS <= x.n_end && m0 + (OP == UP ? 64 : 128) <= m_end) {
+                    if (p.splits > 1) {
+                        store_part<OP>(p, x, turn, n0, m0, m_end, tid);
+                    } else if (OP != DW && p.vec && n0 + F_COLS <= x.n_end && m0 + (OP == UP ? 64 : 128) <= m_end) {
                         uint4 g8[UNITS], u8[UNITS];
                         if constexpr (OP == DHIDDEN) {
                             copies_done();
@@ -981,10 +1049,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
 #pragma unroll
                             for (int i = 0; i < UNITS; ++i) {
                                 const int row = n0 + tid / 16 + 8 * i, m = m0 + tid % 16 * 8;
-                                const int64_t at = row * p.ld_kept + m;
-                                const int left = row < x.n_end ? m_end - m : 0;
-                                g8[i] = load8(static_cast<const __nv_bfloat16*>(p.gate) + at, left, p.vec);
-                                u8[i] = load8(static_cast<const __nv_bfloat16*>(p.up) + at, left, p.vec);
+                                load_kept(p, row, m, row < x.n_end ? m_end - m : 0, g8[i], u8[i]);
                             }
                         }
                         if (OP == DHIDDEN && c < last) fetch(x, c + 2);
@@ -1004,6 +1069,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                      "r"(F_TMEM_COLS)
                      : "memory");
     }
+}
+
+// The parts of a split sum in order, and what becomes of it: a thread has
+// eight neighbours of an output row.  gridDim.y: DW's products.
+template <int OP>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ FfnLaunch p) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int j = OP == DW ? blockIdx.y : 0;
+    if (OP == DW && !(p.products >> j & 1)) return;
+    const int m_end = p.m[OP == DW && j == 2];
+    const int64_t rows = OP == DW ? p.m[j != 2] : p.rows;
+    const int64_t ld = p.part_ld[OP == DW && j == 2];
+    const int64_t groups = (m_end + 7) / 8;
+    const int64_t u = blockIdx.x * int64_t(128) + threadIdx.x;
+    if (u >= rows * groups) return;
+    const int row = static_cast<int>(u / groups), m = static_cast<int>(u - row * groups) * 8;
+    const int left = m_end - m;
+    uint4 g8 = make_uint4(0u, 0u, 0u, 0u), u8 = g8;
+    if (OP == DHIDDEN) load_kept(p, row, m, left, g8, u8);
+    const float* const from = p.part + (OP == DW ? p.part_at[j] : 0) + row * ld + m;
+    float v[8] = {}, w[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+        const float4* const q = reinterpret_cast<const float4*>(from + s * p.part_stride);
+        const float4 a = q[0], b = q[1];
+        const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += f[i];
+        if (OP == UP) {
+            const float4* const r = reinterpret_cast<const float4*>(from + s * p.part_stride + ld / 2);
+            const float4 c = r[0], d = r[1];
+            const float g[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] += g[i];
+        }
+    }
+    finish8<OP, false>(p, 0, j, row, m, left, v, w, g8, u8);
 }
 
 // A tensor that TMA cannot read, to dense rows of ld elements (a multiple of 8).
@@ -1134,6 +1237,8 @@ using Kernel = void (*)(FfnLaunch);
 cudaError_t launch_op(Op op, const FfnLaunch& p, int64_t items, cudaStream_t s) {
     static const Kernel kernel[5] = {gated_ffn_kernel<UP>, gated_ffn_kernel<DOWN>, gated_ffn_kernel<DHIDDEN>,
                                      gated_ffn_kernel<DX>, gated_ffn_kernel<DW>};
+    static const Kernel join[5] = {join_kernel<UP>, join_kernel<DOWN>, join_kernel<DHIDDEN>, join_kernel<DX>,
+                                   join_kernel<DW>};
     static const int size[5] = {Space<UP>::BYTES, Space<DOWN>::BYTES, Space<DHIDDEN>::BYTES, Space<DX>::BYTES,
                                 Space<DW>::BYTES};
     static int attr_done[64] = {0};
@@ -1147,8 +1252,88 @@ cudaError_t launch_op(Op op, const FfnLaunch& p, int64_t items, cudaStream_t s) 
         }
         if (dev >= 0 && dev < 64) attr_done[dev] = 1;
     }
+    items *= p.splits;
     const int pairs = static_cast<int>(items < F_PAIRS ? items : F_PAIRS);
-    return launch_kernel(kernel[op], dim3(2 * pairs), dim3(F_THREADS), size[op], s, p);
+    const cudaError_t e = launch_kernel(kernel[op], dim3(2 * pairs), dim3(F_THREADS), size[op], s, p);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    int64_t units = p.rows * ceil_div(p.m[0], 8);
+    if (op == DW) {
+        const int64_t a = int64_t(p.m[1]) * ceil_div(p.m[0], 8), b = int64_t(p.m[0]) * ceil_div(p.m[1], 8);
+        units = a > b ? a : b;
+    }
+    return launch_kernel(join[op], dim3(static_cast<unsigned>(ceil_div(units, 128)), op == DW ? 3 : 1), dim3(128), 0,
+                         s, p);
+}
+
+// How one dense block's product is cut up.
+struct Cut {
+    int tile_n = 0, splits = 1;
+    int64_t row_tiles = 0;
+    int64_t ld[2] = {0, 0}, at[3] = {0, 0, 0}, stride = 0;     // of the parts
+    size_t bytes = 0;
+};
+
+// Parts that the sums are cut into, so that every pair has a tile, of four
+// steps at least.  Joining them costs a launch and their way through L2, about
+// 4 us, which eight steps (0.3 us each) of what is saved must outweigh twice.
+int split_count(int64_t tiles, int64_t steps) {
+    int64_t s = F_PAIRS / tiles;
+    if (s > steps / 4) s = steps / 4;
+    return s >= 2 && steps - steps / s >= 24 ? static_cast<int>(s) : 1;
+}
+
+// op, for rows x ... of one dense block (experts: a tile's rows go by the
+// expert, and nothing is split: one of many has its own tiles).
+Cut cut(Op op, bool dense, int64_t rows, int64_t experts, int64_t m, int64_t k) {
+    Cut c;
+    c.row_tiles = rows / 256 + experts;
+    if (!dense || rows == 0) return c;
+    // tiles of as many rows as make the pairs' rounds come out best: a round of
+    // narrower tiles takes less, though not in proportion, because the
+    // matrices' part of the loads stays (4096 rows of 4096 x 4096: 19 tiles of
+    // 224 rows are four rounds, as 16 of 256 are)
+    const int64_t across = ceil_div(m, op == UP ? 128 : 256), least = ceil_div(rows, 256);
+    int64_t best = -1;
+    for (int64_t n = least; n <= least + std::min(least / 2, int64_t(32)); ++n) {
+        const int64_t size = ceil_div(ceil_div(rows, n), 32) * 32, tiles = ceil_div(rows, size) * across;
+        const int64_t cost = ceil_div(tiles, F_PAIRS) * (256 + size);
+        if (best < 0 || cost < best) {
+            best = cost;
+            c.tile_n = static_cast<int>(size);
+            c.row_tiles = ceil_div(rows, size);
+        }
+    }
+    c.splits = split_count(c.row_tiles * across, ceil_div(k, F_K) * (op == DX ? 2 : 1));
+    if (c.splits > 1) {
+        c.ld[0] = ceil_div(m, 8) * 8 * (op == UP ? 2 : 1);
+        c.stride = rows * c.ld[0];
+        c.bytes = size_t(c.splits) * c.stride * 4;
+    }
+    return c;
+}
+Cut cut_grads(bool dense, int64_t rows, int64_t hidden, int64_t inner, int products) {
+    Cut c;
+    if (!dense) return c;
+    int64_t tiles = 0;
+    c.ld[0] = ceil_div(hidden, 8) * 8;
+    c.ld[1] = ceil_div(inner, 8) * 8;
+    for (int j = 0; j < 3; ++j) {
+        if (!(products >> j & 1)) continue;
+        tiles += ceil_div(hidden, 256) * ceil_div(inner, 256);
+        c.at[j] = c.stride;
+        c.stride += j == 2 ? hidden * c.ld[1] : inner * c.ld[0];
+    }
+    c.splits = tiles ? split_count(tiles, ceil_div(rows, F_K)) : 1;
+    if (c.splits > 1) c.bytes = size_t(c.splits) * c.stride * 4;
+    return c;
+}
+void apply(FfnLaunch& p, const Cut& c, char* parts) {
+    p.tile_n = c.tile_n;
+    p.splits = c.splits;
+    p.part = reinterpret_cast<float*>(parts);
+    p.part_stride = c.stride;
+    for (int i = 0; i < 2; ++i) p.part_ld[i] = c.ld[i];
+    for (int i = 0; i < 3; ++i) p.part_at[i] = c.at[i];
 }
 
 FfnLaunch common(const int32_t* offsets, int64_t rows, int64_t experts, int act) {
@@ -1161,13 +1346,11 @@ FfnLaunch common(const int32_t* offsets, int64_t rows, int64_t experts, int act)
     return p;
 }
 
-// Tiles of 256 rows that the experts' rows can make, at most.
-int64_t row_tiles(int64_t rows, int64_t experts) { return rows / 256 + experts; }
-
 struct Forward {
     Workspace space;
     Operand x, gate, up, down, h;
-    size_t h_at;
+    size_t h_at, part_at;
+    Cut cut_up, cut_down;
 };
 Forward plan(const muon_gated_ffn_args& a) {
     Forward f;
@@ -1178,6 +1361,9 @@ Forward plan(const muon_gated_ffn_args& a) {
     f.gate = f.space.operand(a.w_gate, a.experts, a.inner, a.hidden, a.ld_gate, a.stride_gate);
     f.up = f.space.operand(a.w_up, a.experts, a.inner, a.hidden, a.ld_up, a.stride_up);
     f.down = f.space.operand(a.w_down, a.experts, a.hidden, a.inner, a.ld_down, a.stride_down);
+    f.cut_up = cut(UP, !a.offsets, a.rows, a.experts, a.inner, a.hidden);
+    f.cut_down = cut(DOWN, !a.offsets, a.rows, a.experts, a.hidden, a.inner);
+    f.part_at = f.space.take(std::max(f.cut_up.bytes, f.cut_down.bytes));
     return f;
 }
 
@@ -1186,6 +1372,8 @@ struct Backward {
     Operand dy, x, gate, up, down, dg, du, h;
     size_t d_at[3] = {0, 0, 0};      // dg, du, h where the caller gives none
     bool own[3] = {false, false, false};
+    size_t part_at;
+    Cut cut_dh, cut_dx, cut_dw;
 };
 Backward plan(const muon_gated_ffn_grad_args& a) {
     Backward b;
@@ -1212,6 +1400,11 @@ Backward plan(const muon_gated_ffn_grad_args& a) {
         b.up = b.space.operand(a.w_up, a.experts, a.inner, a.hidden, a.ld_up, a.stride_up);
     }
     b.down = b.space.operand(a.w_down, a.experts, a.hidden, a.inner, a.ld_down, a.stride_down);
+    b.cut_dh = cut(DHIDDEN, !a.offsets, a.rows, a.experts, a.inner, a.hidden);
+    if (a.dx) b.cut_dx = cut(DX, !a.offsets, a.rows, a.experts, a.hidden, a.inner);
+    b.cut_dw = cut_grads(!a.offsets, a.rows, a.hidden, a.inner,
+                         (a.dw_gate ? 1 : 0) | (a.dw_up ? 2 : 0) | (a.dw_down ? 4 : 0));
+    b.part_at = b.space.take(std::max(b.cut_dh.bytes, std::max(b.cut_dx.bytes, b.cut_dw.bytes)));
     return b;
 }
 
@@ -1243,14 +1436,15 @@ cudaError_t launch_gated_ffn(const muon_gated_ffn_args& a, void* ws, cudaStream_
     p.vec = p.out[1].vec && p.out[2].vec;
     if (!rows_map(&p.maps[0].a, f.gate, 64) || !rows_map(&p.maps[1].a, f.up, 64) || !rows_of_n(p.maps[0], f.x))
         return cudaErrorInvalidValue;
-    const int64_t rt = row_tiles(a.rows, a.experts);
-    RETURN_IF_CUDA(launch_op(UP, p, rt * ceil_div(a.inner, 128), s));
+    apply(p, f.cut_up, base + f.part_at);
+    RETURN_IF_CUDA(launch_op(UP, p, f.cut_up.row_tiles * ceil_div(a.inner, 128), s));
     p.m[0] = static_cast<int32_t>(a.hidden);
     p.k = static_cast<int32_t>(a.inner);
     p.a_by_expert[0] = f.down.matrices > 1;
     p.out[0] = output(a.y, a.ld_y, a.rows);
     if (!rows_map(&p.maps[0].a, f.down, 128) || !rows_of_n(p.maps[0], f.h)) return cudaErrorInvalidValue;
-    return launch_op(DOWN, p, rt * ceil_div(a.hidden, 256), s);
+    apply(p, f.cut_down, base + f.part_at);
+    return launch_op(DOWN, p, f.cut_down.row_tiles * ceil_div(a.hidden, 256), s);
 }
 
 cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, cudaStream_t s) {
@@ -1259,7 +1453,6 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
     Operand* const d[3] = {&b.dg, &b.du, &b.h};
     const bool grads = a.dw_gate || a.dw_up || a.dw_down;
     FfnLaunch p = common(a.offsets, a.rows, a.experts, a.activation);
-    const int64_t rt = row_tiles(a.rows, a.experts);
     if (a.rows) {
         for (Operand* o : {&b.dy, &b.x, &b.gate, &b.up, &b.down}) RETURN_IF_CUDA(settle(*o, base, s));
         p.m[0] = static_cast<int32_t>(a.inner);
@@ -1276,7 +1469,8 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
             p.vec = p.vec && p.out[i].vec;
         }
         if (!columns_map(&p.maps[0].a, b.down, &p.maps[0].wide_a) || !rows_of_n(p.maps[0], b.dy)) return cudaErrorInvalidValue;
-        RETURN_IF_CUDA(launch_op(DHIDDEN, p, rt * ceil_div(a.inner, 256), s));
+        apply(p, b.cut_dh, base + b.part_at);
+        RETURN_IF_CUDA(launch_op(DHIDDEN, p, b.cut_dh.row_tiles * ceil_div(a.inner, 256), s));
         for (Operand* o : d) RETURN_IF_CUDA(settle(*o, base, s));
         if (a.dx) {
             p.m[0] = static_cast<int32_t>(a.hidden);
@@ -1288,7 +1482,8 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
                 !columns_map(&p.maps[1].a, b.up, &p.maps[1].wide_a) || !rows_of_n(p.maps[0], b.dg) ||
                 !rows_of_n(p.maps[1], b.du))
                 return cudaErrorInvalidValue;
-            RETURN_IF_CUDA(launch_op(DX, p, rt * ceil_div(a.hidden, 256), s));
+            apply(p, b.cut_dx, base + b.part_at);
+            RETURN_IF_CUDA(launch_op(DX, p, b.cut_dx.row_tiles * ceil_div(a.hidden, 256), s));
         }
     }
     if (!grads) return cudaSuccess;
@@ -1314,6 +1509,7 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
                        !boxes_map(&of.b64, *right[j], false)))
             return cudaErrorInvalidValue;
     }
+    apply(p, b.cut_dw, base + b.part_at);
     return launch_op(DW, p, items, s);
 }
 

@@ -343,6 +343,25 @@ def test_gated_ffn(ns, tokens, hidden, inner, name):
     ns.ops_sync()
 
 
+@pytest.mark.parametrize("tokens,hidden,inner,dtype", [(3, 4096, 520, BF), (40, 7168, 256, BF), (1, 520, 4100, BF),
+                                                       (70, 2049, 2050, BF), (3000, 264, 136, BF),
+                                                       (4100, 100, 72, F32), (2500, 513, 31, F32)])
+def test_gated_ffn_of_few_tiles(ns, tokens, hidden, inner, dtype):
+    """Long sums of few outputs, which are cut into parts and joined."""
+    x, w = rand(25, tokens, hidden, dtype=BF), weights(26, hidden, inner)
+    y, saved = ns.gated_ffn(x, *w)
+    check_forward(x, w, y, saved)
+    dy = rand(29, tokens, hidden, scale=0.1, dtype=BF)
+    got = ns.gated_ffn_backward(dy, x, saved, *w, dtype=dtype)
+    check_backward(dy, x, saved, w, got)
+    base = [rand(30 + i, *v.shape, dtype=dtype) for i, v in enumerate(w)]
+    more = ns.gated_ffn_backward(dy, x, saved, *w, grads=[b.clone() for b in base], accumulate=True)
+    check_backward(dy, x, saved, w, more, before=base)
+    again = ns.gated_ffn_backward(dy, x, saved, *w, dtype=dtype)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    ns.ops_sync()
+
+
 @pytest.mark.parametrize("counts", [[5], [0], [0, 0, 0], [1, 0, 2, 63, 64, 65, 0, 200, 1], [300, 0, 0, 0],
                                     [0, 0, 17], [128, 128, 128], [7] * 40, [600, 3], [31, 33, 255, 257]])
 @pytest.mark.parametrize("hidden,inner,dtype", [(64, 96, BF), (264, 520, F32), (100, 33, BF)])
