@@ -634,8 +634,8 @@ MUON_API int muon_gated_ffn_grad(const muon_gated_ffn_grad_args* args, void* wor
  * frequency in turns per position times 2^64 (muon_rotary_frequencies), so
  * that position * turns modulo 2^64 is the angle without whole turns: good to
  * 2^-53 of itself, whole turns included, and to 2^-64 turns a position.
- * 0 <= batch * seq < 2^31, 1 <= pairs <= 256, 2 * pairs <= head <= 65536, heads of
- * both 1 .. 65536. */
+ * 0 <= batch * seq < 2^31, 1 <= pairs <= 256, 2 * pairs <= head <= 65536, 0 <=
+ * heads <= 65536 each, a position's values of both at most 2^28. */
 #define MUON_ROTARY_HALF 0
 #define MUON_ROTARY_INTERLEAVED 1
 typedef struct {

@@ -228,62 +228,72 @@ class RotaryPlan:
 
 
 def _heads(name: str, t: torch.Tensor, index: int):
-    """Checks a tensor of (batch x) seq x heads x head; (shape with a batch,
-    strides with one)."""
-    if t.dim() not in (3, 4):
+    """Checks a tensor of (batch x) seq x heads x head: (its shape with a batch,
+    its strides of batch, seq and heads)."""
+    shape, strides = t.shape, t.stride()
+    n = len(shape)
+    if n != 4 and n != 3:
         raise ValueError(f"{name} must be seq x heads x head, or batch x seq x heads x head, got "
-                         f"{tuple(t.shape)}")
+                         f"{tuple(shape)}")
     on = t.get_device()
-    if on < 0 or (index >= 0 and on != index):
+    if on < 0 or on != index:
         raise ValueError(f"{name} must be a CUDA tensor of its operator's device, is on {t.device}")
-    shape, strides = tuple(t.shape), t.stride()
     if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s heads must be dense (stride(-1) == 1)")
-    if len(shape) == 3:
-        shape, strides = (1, *shape), (0, *strides)
-    return shape, strides
+    if n == 3:
+        return (1, *shape), (0, strides[0], strides[1])
+    return shape, strides[:3]
+
+
+def _turned(name: str, x: torch.Tensor, out, shape, strides, index: int):
+    """(the C argument of one tensor, its output: given or new)."""
+    batch, seq, heads, head = shape
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        row = heads * head
+        to = (seq * row, row, head)
+    else:
+        if out.dtype != x.dtype or out.shape != x.shape:
+            raise ValueError(f"out_{name} must be {tuple(x.shape)} of {x.dtype}, got {tuple(out.shape)} of "
+                             f"{out.dtype}")
+        to = _heads(f"out_{name}", out, index)[1]
+        for n, stride in zip(shape, to):
+            _need(stride > 0 or n <= 1, f"out_{name} has places that share memory")
+    return (x.data_ptr(), out.data_ptr(), heads, *strides, *to), out
 
 
 def _turn(q, k, plan: RotaryPlan, positions, offset: int, out_q, out_k, inverse: bool):
     index = q.get_device()
-    shape, _ = _heads("q", q, index)
+    shape, strides = _heads("q", q, index)
     batch, seq, _, head = shape
     dtype = _dtype("q", q)
-    _need(plan.dim <= head, f"heads of {head} values are shorter than the plan's {plan.dim}")
-    tensors, outs = [], []
-    for name, x, out in (("q", q, out_q), ("k", k, out_k)):
-        if x is None:
-            _need(out is None, f"out_{name} without {name}")
-            tensors.append(_NO_TENSOR)
-            outs.append(None)
-            continue
-        s, strides = _heads(name, x, index)
-        _need(x.dim() == q.dim() and (s[0], s[1], s[3]) == (batch, seq, head) and x.dtype == q.dtype,
-              f"{name} must match q in all but its heads, got {tuple(x.shape)} of {x.dtype}")
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        _need(out.dtype == x.dtype and out.shape == x.shape,
-              f"out_{name} must be {tuple(x.shape)} of {x.dtype}, got {tuple(out.shape)} of {out.dtype}")
-        o = _heads(f"out_{name}", out, index)[1]
-        for n, st in zip(s[:3], o[:3]):
-            _need(st > 0 or n <= 1, f"out_{name} has places that share memory")
-        tensors.append((x.data_ptr(), out.data_ptr(), s[2], *strides[:3], *o[:3]))
-        outs.append(out)
+    if plan.dim > head:
+        raise ValueError(f"heads of {head} values are shorter than the plan's {plan.dim}")
+    first, out_q = _turned("q", q, out_q, shape, strides, index)
+    second = _NO_TENSOR
+    if k is not None:
+        shape_k, strides = _heads("k", k, index)
+        if k.dtype != q.dtype or shape_k[0] != batch or shape_k[1] != seq or shape_k[3] != head \
+                or k.dim() != q.dim():
+            raise ValueError(f"k must match q in all but its heads, got {tuple(k.shape)} of {k.dtype}")
+        second, out_k = _turned("k", k, out_k, shape_k, strides, index)
+    else:
+        _need(out_k is None, "out_k without k")
     at = stride = wide = 0
     if positions is not None:
         if positions.dtype not in (_I32, torch.int64):
             raise ValueError(f"positions must be int32 or int64, got {positions.dtype}")
         _need(positions.get_device() == index, f"positions must be on {q.device}")
-        want = positions.shape
-        _need(tuple(want) in ((seq,), (1, seq), (batch, seq)),
-              f"positions must be {(seq,)} or {(batch, seq)}, got {tuple(want)}")
+        want = tuple(positions.shape)
+        _need(want in ((seq,), (1, seq), (batch, seq)),
+              f"positions must be {(seq,)} or {(batch, seq)}, got {want}")
         _need(positions.stride(-1) == 1 or seq <= 1, "positions must be dense along seq")
         at, wide = positions.data_ptr(), positions.dtype == torch.int64
         stride = positions.stride(0) if len(want) == 2 and want[0] > 1 else 0
     _call(index, "muon_rotary", _rotary_args(
-        *tensors[0], *tensors[1], at, plan._at, batch, seq, head, plan.dim // 2, stride, offset, dtype,
+        *first, *second, at, plan._at, batch, seq, head, plan.dim // 2, stride, offset, dtype,
         plan.layout, wide, inverse, plan.scale))
-    return tuple(outs)
+    return out_q, out_k
 
 
 def rotary(q: torch.Tensor, k: Optional[torch.Tensor], plan: RotaryPlan, *,

@@ -83,9 +83,9 @@ struct Eight {
 // One element.  A dropped one is 0 whatever x holds there.
 template <typename T>
 __device__ __forceinline__ void one(const DropLaunch& p, const uint4& z, int i, int64_t row, int64_t col) {
-    float v = kept(z, i, p.limit) ? to_f32(static_cast<const T*>(p.x)[row * p.ld_x + col]) * p.scale : 0.f;
-    if (p.r) v += to_f32(static_cast<const T*>(p.r)[row * p.ld_r + col]);
-    from_f32(static_cast<T*>(p.y) + row * p.ld_y + col, v);
+    const float x = to_f32(static_cast<const T*>(p.x)[row * p.ld_x + col]);
+    const float r = p.r ? to_f32(static_cast<const T*>(p.r)[row * p.ld_r + col]) : 0.f;
+    from_f32(static_cast<T*>(p.y) + row * p.ld_y + col, kept(z, i, p.limit) ? __fmaf_rn(x, p.scale, r) : r);
 }
 
 // Blocks whose eight elements are neighbours on 16 bytes: rows of a multiple
@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(256) dropout_vec_kernel(const __grid_constant_
     if (RES) r.get(g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        f[i] = kept(z, i, p.limit) ? f[i] * p.scale : 0.f;
-        if (RES) f[i] += g[i];
+        const float b = RES ? g[i] : 0.f;
+        f[i] = kept(z, i, p.limit) ? __fmaf_rn(f[i], p.scale, b) : b;
     }
     Eight<T>::put(static_cast<T*>(p.y) + row * p.ld_y + col, f);
 }

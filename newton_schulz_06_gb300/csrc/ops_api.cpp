@@ -429,7 +429,7 @@ MUON_API int muon_rotary(const muon_rotary_args* a, void* cuda_stream, char* err
         if (reinterpret_cast<uintptr_t>(a->positions) % (a->positions_64 ? 8 : 4) != 0)
             return err.bad("positions is not aligned to its elements");
     }
-    if (a->q.heads + a->k.heads > 65536) return err.bad("heads out of range");
+    if ((a->q.heads + a->k.heads) * a->head > (int64_t(1) << 28)) return err.bad("heads out of range");
     if (a->batch * a->seq == 0 || a->q.heads + a->k.heads == 0) return MUON_OK;
     return err.done(ops::launch_rotary(*a, static_cast<cudaStream_t>(cuda_stream)));
 }

@@ -19,44 +19,59 @@ namespace {
 constexpr int R_THREADS = 256;
 constexpr int R_PAIRS = 1024;             // cosines and sines of a block (or one token's)
 
+// u / d for u below 2^31 as a multiplication and a shift ("Division by invariant
+// integers using multiplication", Granlund and Montgomery, 1994).
+struct Quotient {
+    uint32_t d, m, shift;
+    void set(int64_t v) {
+        d = static_cast<uint32_t>(v);
+        int log = 0;
+        while ((int64_t(1) << log) < v) ++log;
+        m = log ? static_cast<uint32_t>((uint64_t(1) << (31 + log)) / d + 1) : 0;
+        shift = log ? log - 1 : 0;
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t u) const { return d == 1 ? u : __umulhi(u, m) >> shift; }
+};
+
 struct RotaryLaunch {
     muon_rotary_tensor t[2];
     const void* positions;
     int64_t stride_pos;
     int64_t offset;
-    uint32_t tokens, seq;                 // tokens: batch * seq
-    uint32_t tokens_block;
-    uint32_t head, pairs;                 // a head's values, and its pairs that turn
-    uint32_t units;                       // of a head: groups of W pairs, then of W other values
+    uint32_t tokens, tokens_block;        // tokens: batch * seq
+    uint32_t head;
+    Quotient seq, pairs;                  // pairs of a head that turn
+    Quotient per_head, per_token;         // units of a head (groups of W pairs, then of W other values), of a token
     int32_t wide_pos, copy;               // positions are 64-bit; the other values are copied
     float scale, sign;
     uint64_t turns[256];
 };
 
-// N neighbouring values, W of them an access.
+// N neighbouring values as they are in memory, W of them an access.
 template <typename T, int W, int N>
 struct Group {
     struct alignas(sizeof(T) * W) Raw {
         T v[W];
     };
-    static __device__ __forceinline__ void load(const T* p, float (&f)[N]) {
+    Raw raw[N / W];
+    __device__ __forceinline__ void load(const T* p, int accesses) {
 #pragma unroll
-        for (int k = 0; k < N / W; ++k) {
-            const Raw r = reinterpret_cast<const Raw*>(p)[k];
-#pragma unroll
-            for (int i = 0; i < W; ++i) f[k * W + i] = to_f32(r.v[i]);
-        }
+        for (int k = 0; k < N / W; ++k)
+            if (k < accesses) raw[k] = reinterpret_cast<const Raw*>(p)[k];
     }
-    static __device__ __forceinline__ void store(T* p, const float (&f)[N]) {
+    __device__ __forceinline__ void store(T* p, int accesses) const {
 #pragma unroll
-        for (int k = 0; k < N / W; ++k) {
-            Raw r;
-#pragma unroll
-            for (int i = 0; i < W; ++i) from_f32(&r.v[i], f[k * W + i]);
-            reinterpret_cast<Raw*>(p)[k] = r;
-        }
+        for (int k = 0; k < N / W; ++k)
+            if (k < accesses) reinterpret_cast<Raw*>(p)[k] = raw[k];
     }
+    __device__ __forceinline__ float get(int i) const { return to_f32(raw[i / W].v[i % W]); }
+    __device__ __forceinline__ void set(int i, float f) { from_f32(&raw[i / W].v[i % W], f); }
 };
+
+// a c + b s, rounded the same way in all kernels.
+__device__ __forceinline__ float turned(float a, float c, float b, float s) {
+    return __fmaf_rn(a, c, __fmul_rn(b, s));
+}
 
 // HALF: pair i is values i and i + pairs of a head; else 2 i and 2 i + 1.
 // W: values of a load or store.  A unit of a thread's work is W pairs of HALF,
@@ -68,10 +83,10 @@ __global__ void __launch_bounds__(R_THREADS) rotary_kernel(const __grid_constant
     allow_dependent_launch();
     const uint32_t first = blockIdx.x * p.tokens_block;
     const uint32_t tokens = min(p.tokens_block, p.tokens - first);
-    float* const sine = trig + p.tokens_block * p.pairs;
-    for (uint32_t u = threadIdx.x; u < tokens * p.pairs; u += R_THREADS) {
-        const uint32_t t = u / p.pairs, i = u - t * p.pairs;
-        const uint32_t b = (first + t) / p.seq, s = first + t - b * p.seq;
+    float* const sine = trig + p.tokens_block * p.pairs.d;
+    for (uint32_t u = threadIdx.x; u < tokens * p.pairs.d; u += R_THREADS) {
+        const uint32_t t = p.pairs.of(u), i = u - t * p.pairs.d;
+        const uint32_t b = p.seq.of(first + t), s = first + t - b * p.seq.d;
         int64_t at = s;
         if (p.positions) {
             const int64_t k = int64_t(b) * p.stride_pos + s;
@@ -86,51 +101,55 @@ __global__ void __launch_bounds__(R_THREADS) rotary_kernel(const __grid_constant
         sine[u] = n * p.scale * p.sign;
     }
     __syncthreads();
-    const uint32_t heads = static_cast<uint32_t>(p.t[0].heads + p.t[1].heads);
-    const uint32_t per_token = heads * p.units;
+    const uint32_t q_heads = static_cast<uint32_t>(p.t[0].heads);
     constexpr int N = HALF || W > 1 ? W : 2;              // values of an operand
     constexpr uint32_t PW = HALF ? N : N / 2;             // pairs of a unit
-    const uint32_t turning = p.pairs / PW;                // units that turn
-    for (uint32_t u = threadIdx.x; u < tokens * per_token; u += R_THREADS) {
-        const uint32_t t = u / per_token, in = u - t * per_token;
-        uint32_t h = in / p.units;
-        const uint32_t unit = in - h * p.units;
-        const int which = h >= p.t[0].heads;
-        if (which) h -= static_cast<uint32_t>(p.t[0].heads);
+    const uint32_t turning = p.pairs.d / PW;              // units that turn
+    for (uint32_t u = threadIdx.x; u < tokens * p.per_token.d; u += R_THREADS) {
+        const uint32_t t = p.per_token.of(u), in = u - t * p.per_token.d;
+        uint32_t h = p.per_head.of(in);
+        const uint32_t unit = in - h * p.per_head.d;
+        const uint32_t b = p.seq.of(first + t), s = first + t - b * p.seq.d;
+        const int which = h >= q_heads;
+        if (which) h -= q_heads;
         const muon_rotary_tensor& x = p.t[which];
-        const uint32_t b = (first + t) / p.seq, s = first + t - b * p.seq;
-        const T* const from = static_cast<const T*>(x.x) + b * x.x_batch + s * x.x_seq + h * x.x_head;
-        T* const to = static_cast<T*>(x.y) + b * x.y_batch + s * x.y_seq + h * x.y_head;
-        if (unit >= turning) {
-            const uint32_t at = 2 * p.pairs + (unit - turning) * W;
-            float f[W];
-            Group<T, W, W>::load(from + at, f);
-            Group<T, W, W>::store(to + at, f);
-            continue;
-        }
-        const float* const c = trig + t * p.pairs + unit * PW;
-        const float* const n = sine + t * p.pairs + unit * PW;
-        if constexpr (HALF) {
-            float a[N], d[N], y[N], z[N];
-            Group<T, W, N>::load(from + unit * N, a);
-            Group<T, W, N>::load(from + p.pairs + unit * N, d);
+        const bool turns = unit < turning;
+        // where this unit's values are: those that turn and those that do not
+        // are loaded and stored by the same instructions (a branch each took
+        // 8191 tokens of 65 heads, 64 of 192 values, from 72 to 86 us)
+        const uint32_t rest = 2 * p.pairs.d + (unit - turning) * (HALF ? 2 * W : N);
+        const uint32_t at = turns ? unit * N : rest, at2 = turns ? p.pairs.d + unit * N : rest + W;
+        const bool second = HALF && (turns || at2 < p.head);
+        const int64_t in_x = b * x.x_batch + s * x.x_seq + h * x.x_head;
+        const int64_t in_y = b * x.y_batch + s * x.y_seq + h * x.y_head;
+        const T* const from = static_cast<const T*>(x.x) + in_x;
+        T* const to = static_cast<T*>(x.y) + in_y;
+        // (one value at a time, the last of an odd rest is alone)
+        const int accesses = N > W && at + 1 == p.head ? 1 : N / W;
+        Group<T, W, N> v, w;
+        v.load(from + at, accesses);
+        if (second) w.load(from + at2, 1);
+        if (turns) {
+            const float* const c = trig + t * p.pairs.d + unit * PW;
+            const float* const n = sine + t * p.pairs.d + unit * PW;
+            if constexpr (HALF) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                y[i] = a[i] * c[i] - d[i] * n[i];
-                z[i] = d[i] * c[i] + a[i] * n[i];
-            }
-            Group<T, W, N>::store(to + unit * N, y);
-            Group<T, W, N>::store(to + p.pairs + unit * N, z);
-        } else {
-            float a[N], y[N];
-            Group<T, W, N>::load(from + unit * N, a);
+                for (int i = 0; i < N; ++i) {
+                    const float f = v.get(i), g = w.get(i);
+                    v.set(i, turned(f, c[i], g, -n[i]));
+                    w.set(i, turned(g, c[i], f, n[i]));
+                }
+            } else {
 #pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                y[i] = a[i] * c[i / 2] - a[i + 1] * n[i / 2];
-                y[i + 1] = a[i + 1] * c[i / 2] + a[i] * n[i / 2];
+                for (int i = 0; i < N; i += 2) {
+                    const float f = v.get(i), g = v.get(i + 1);
+                    v.set(i, turned(f, c[i / 2], g, -n[i / 2]));
+                    v.set(i + 1, turned(g, c[i / 2], f, n[i / 2]));
+                }
             }
-            Group<T, W, N>::store(to + unit * N, y);
         }
+        v.store(to + at, accesses);
+        if (second) w.store(to + at2, 1);
     }
 }
 
@@ -162,7 +181,7 @@ cudaError_t launch(const RotaryLaunch& p, bool half, cudaStream_t s) {
     const int64_t blocks = ceil_div(p.tokens, p.tokens_block);
     void (*const kernel)(RotaryLaunch) = half ? rotary_kernel<T, W, true> : rotary_kernel<T, W, false>;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(R_THREADS),
-                         size_t(2) * p.tokens_block * p.pairs * sizeof(float), s, p);
+                         size_t(2) * p.tokens_block * p.pairs.d * sizeof(float), s, p);
 }
 
 template <typename T>
@@ -170,14 +189,20 @@ cudaError_t launch(RotaryLaunch p, const muon_rotary_args& a, cudaStream_t s) {
     const bool half = a.layout == MUON_ROTARY_HALF;
     const int w = group_width<T>(a, p.copy);
     const int64_t turning = half ? a.pairs / w : a.pairs / (w > 1 ? w / 2 : 1);
-    p.units = static_cast<uint32_t>(turning + (p.copy ? (a.head - 2 * a.pairs) / w : 0));
-    // as many tokens a block as give every thread four units and a cosine,
-    // and no more than leave every SM a block
-    const int64_t units = (a.q.heads + a.k.heads) * p.units;
+    // a unit of the rest is as many values as one of those that turn
+    const int64_t values = half ? 2 * w : w > 1 ? w : 2;
+    const int64_t per_head = turning + (p.copy ? ceil_div(a.head - 2 * a.pairs, values) : 0);
+    // as many tokens a block as give every thread four units, and no more than
+    // leave every SM a block (with eight tokens of 65 heads of 192 a block, so
+    // that every thread made a cosine, 8191 tokens took 108 us)
+    const int64_t units = (a.q.heads + a.k.heads) * per_head;
+    p.per_head.set(per_head);
+    p.per_token.set(units);
     int64_t t = ceil_div(4 * R_THREADS, units);
-    if (t * a.pairs < R_THREADS) t = ceil_div(R_THREADS, a.pairs);
     if (t > R_PAIRS / a.pairs) t = R_PAIRS / a.pairs;
     if (t > ceil_div(p.tokens, 152)) t = ceil_div(p.tokens, 152);
+    // (the units of a block are counted in 32 bits)
+    if (t > (int64_t(1) << 28) / units) t = (int64_t(1) << 28) / units;
     p.tokens_block = static_cast<uint32_t>(t < 1 ? 1 : t);
     if constexpr (sizeof(T) == 2)
         if (w == 8) return launch<T, 8>(p, half, s);
@@ -197,9 +222,9 @@ cudaError_t launch_rotary(const muon_rotary_args& a, cudaStream_t s) {
     p.stride_pos = a.stride_positions;
     p.offset = a.offset;
     p.tokens = static_cast<uint32_t>(a.batch * a.seq);
-    p.seq = static_cast<uint32_t>(a.seq);
     p.head = static_cast<uint32_t>(a.head);
-    p.pairs = static_cast<uint32_t>(a.pairs);
+    p.seq.set(a.seq);
+    p.pairs.set(a.pairs);
     p.scale = a.scale;
     p.sign = a.inverse ? -1.f : 1.f;
     const bool rest = a.head > 2 * a.pairs;

@@ -115,7 +115,8 @@ def rotary(L, q=None, k=None, **kw):
     (dict(scale=math.nan), "scale"), (dict(positions=P + 4, positions_64=1), "positions"),
     (dict(positions=P + 2), "positions"), (dict(positions=P, stride_positions=-1), "positions"),
     (dict(q=dict(x=None)), "q is NULL"), (dict(k=dict(y=None)), "k is NULL"), (dict(q=dict(x=P + 1)), "aligned"),
-    (dict(k=dict(heads=-1)), "heads"), (dict(q=dict(heads=65536)), "heads"),
+    (dict(k=dict(heads=-1)), "heads"), (dict(q=dict(heads=65537)), "heads"),
+    (dict(q=dict(heads=65536), head=4096), "heads"),
     (dict(q=dict(x_seq=-16)), "negative"), (dict(k=dict(y_head=32)), "in place")])
 def test_rotary_refuses(L, kw, word):
     rc, msg = rotary(L, **kw)

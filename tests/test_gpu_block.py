@@ -186,7 +186,7 @@ def check_rotary(ns, x, got, plan_args, layout, positions, offset, inverse, what
 @pytest.mark.parametrize("batch,seq,heads,kheads,head,dim", [
     (1, 1, 1, 1, 2, 2), (1, 3, 32, 4, 128, 128), (2, 37, 3, 1, 192, 64), (3, 5, 2, 2, 100, 74),
     (1, 130, 1, 7, 64, 64), (2, 9, 16, 16, 66, 66), (1, 1, 128, 1, 512, 512), (1, 700, 2, 1, 96, 32),
-    (5, 1, 5, 3, 130, 6)])
+    (5, 1, 5, 3, 130, 6), (1, 7, 3, 2, 131, 6), (2, 11, 2, 1, 17, 16), (1, 9, 4, 2, 40, 24)])
 def test_rotary(ns, batch, seq, heads, kheads, head, dim, layout, dtype):
     q, k = rand(10, batch, seq, heads, head, dtype=dtype), rand(11, batch, seq, kheads, head, dtype=dtype)
     plan = ns.RotaryPlan(dim, layout=layout)
