@@ -8,8 +8,9 @@
 // not by the memory layout, the grid or the type.
 //
 // Sixteen bits an element, not 32: a block of ten rounds costs about 60
-// instructions, and at 15 an element they, not memory, would bound bf16 rows.
-// p is therefore a multiple of 2^-16 (the nearest), and the scale is that of
+// instructions, and at 15 an element they, not memory, would bound bf16 rows
+// (with 8 they still do without a residual: 16384 x 7168 in 90 us, 70 by the
+// bytes; with one 108 us, 6.5 TB/s).  p is therefore a multiple of 2^-16 (the nearest), and the scale is that of
 // the multiple, so that the mean of y is that of x.
 #include "ops_internal.h"
 
@@ -23,32 +24,34 @@ struct DropLaunch {
     int64_t rows, cols, ld_x, ld_r, ld_y;
     int64_t n;                     // elements
     const int64_t* counter;        // added to the offset, or null
-    uint64_t seed, offset;
-    uint32_t limit;                // numbers below it drop their element
+    uint64_t offset;
+    uint32_t key[2][10];           // the rounds'
+    uint32_t limit;                // numbers below it drop their element; times 2^16,
+    int32_t all;                   // or all are dropped
     float scale;
 };
 
 // The eight numbers of a block, two a word, the low half first.
-__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
+__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, const DropLaunch& p) {
     uint32_t c0 = uint32_t(block), c1 = uint32_t(block >> 32);
     uint32_t c2 = uint32_t(offset), c3 = uint32_t(offset >> 32);
-    uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t a = uint64_t(0xD2511F53u) * c0, b = uint64_t(0xCD9E8D57u) * c2;
-        c0 = uint32_t(b >> 32) ^ c1 ^ k0;
+        c0 = uint32_t(b >> 32) ^ c1 ^ p.key[0][r];
         c1 = uint32_t(b);
-        c2 = uint32_t(a >> 32) ^ c3 ^ k1;
+        c2 = uint32_t(a >> 32) ^ c3 ^ p.key[1][r];
         c3 = uint32_t(a);
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
-    return make_uint4(c0, c1, c2, c3);
+    // (no number is as large as the limit of all)
+    return p.all ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(c0, c1, c2, c3);
 }
 
+// A high half is compared in its place, with what is below it: that decides
+// nothing.
 __device__ __forceinline__ bool kept(const uint4& z, int i, uint32_t limit) {
     const uint32_t w[4] = {z.x, z.y, z.z, z.w};
-    return (i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu) >= limit;
+    return (i & 1 ? w[i / 2] : w[i / 2] << 16) >= limit;
 }
 
 // Eight neighbouring elements on 16 bytes.
@@ -90,34 +93,46 @@ __device__ __forceinline__ void one(const DropLaunch& p, const uint4& z, int i, 
 
 // Blocks whose eight elements are neighbours on 16 bytes: rows of a multiple
 // of eight, or dense tensors taken as one row (whose last block may be short).
-template <typename T, bool RES>
+// U: blocks a thread takes, whose loads are all out before the first numbers
+// are made.
+template <typename T, bool RES, int U>
 __global__ void __launch_bounds__(256) dropout_vec_kernel(const __grid_constant__ DropLaunch p) {
     grid_dependency_wait();
     allow_dependent_launch();
     const uint64_t offset = p.offset + (p.counter ? static_cast<uint64_t>(*p.counter) : 0u);
-    const int64_t blocks = (p.n + 7) / 8;
     const int64_t per_row = (p.cols + 7) / 8;
-    const int64_t b = blockIdx.x * int64_t(256) + threadIdx.x;
-    if (b >= blocks) return;
-    const int64_t row = p.rows == 1 ? 0 : b / per_row, col = (b - row * per_row) * 8;
-    if (p.n - b * 8 < 8) {
-        const uint4 z = philox(b, offset, p.seed);
-        for (int i = 0; i < p.n - b * 8; ++i) one<T>(p, z, i, row, col + i);
-        return;
-    }
-    Eight<T> x, r;
-    x.load(static_cast<const T*>(p.x) + row * p.ld_x + col);
-    if (RES) r.load(static_cast<const T*>(p.r) + row * p.ld_r + col);
-    const uint4 z = philox(b, offset, p.seed);
-    float f[8], g[8];
-    x.get(f);
-    if (RES) r.get(g);
+    const int64_t first = blockIdx.x * int64_t(256 * U) + threadIdx.x;
+    Eight<T> x[U], r[U];
+    int64_t row[U], col[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float b = RES ? g[i] : 0.f;
-        f[i] = kept(z, i, p.limit) ? __fmaf_rn(f[i], p.scale, b) : b;
+    for (int k = 0; k < U; ++k) {
+        const int64_t b = first + 256 * k;
+        row[k] = p.rows == 1 ? 0 : b / per_row;
+        col[k] = (b - row[k] * per_row) * 8;
+        if (p.n - b * 8 >= 8) {
+            x[k].load(static_cast<const T*>(p.x) + row[k] * p.ld_x + col[k]);
+            if (RES) r[k].load(static_cast<const T*>(p.r) + row[k] * p.ld_r + col[k]);
+        }
     }
-    Eight<T>::put(static_cast<T*>(p.y) + row * p.ld_y + col, f);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int64_t b = first + 256 * k, left = p.n - b * 8;
+        if (left <= 0) return;
+        const uint4 z = philox(b, offset, p);
+        if (left < 8) {
+            for (int i = 0; i < left; ++i) one<T>(p, z, i, row[k], col[k] + i);
+            return;
+        }
+        float f[8], g[8];
+        x[k].get(f);
+        if (RES) r[k].get(g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float o = RES ? g[i] : 0.f;
+            f[i] = kept(z, i, p.limit) ? __fmaf_rn(f[i], p.scale, o) : o;
+        }
+        Eight<T>::put(static_cast<T*>(p.y) + row[k] * p.ld_y + col[k], f);
+    }
 }
 
 // Any rows: a block's elements one by one, also over the ends of rows.
@@ -128,7 +143,7 @@ __global__ void __launch_bounds__(256) dropout_any_kernel(const __grid_constant_
     const uint64_t offset = p.offset + (p.counter ? static_cast<uint64_t>(*p.counter) : 0u);
     const int64_t b = blockIdx.x * int64_t(256) + threadIdx.x;
     if (b * 8 >= p.n) return;
-    const uint4 z = philox(b, offset, p.seed);
+    const uint4 z = philox(b, offset, p);
     int64_t row = b * 8 / p.cols, col = b * 8 - row * p.cols;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -153,12 +168,18 @@ cudaError_t launch(DropLaunch p, cudaStream_t s) {
         p.rows = 1;
         p.cols = p.n;
     }
+    // two blocks a thread where that leaves every SM two blocks of threads
+    // (16384 x 7168 bf16: 90 us, with a residual 108; one a thread 99 and 115,
+    // four 92 and 110)
     const int64_t blocks = ceil_div(ceil_div(p.n, 8), 256);
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    void (*const kernel)(DropLaunch) = !vec  ? dropout_any_kernel<T>
-                                       : p.r ? dropout_vec_kernel<T, true>
-                                             : dropout_vec_kernel<T, false>;
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p);
+    const int u = vec && blocks >= 2 * 2 * 152 ? 2 : 1;
+    const int64_t grid = ceil_div(blocks, u);
+    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    void (*const kernel)(DropLaunch) =
+        !vec     ? dropout_any_kernel<T>
+        : u == 2 ? (p.r ? dropout_vec_kernel<T, true, 2> : dropout_vec_kernel<T, false, 2>)
+                 : (p.r ? dropout_vec_kernel<T, true, 1> : dropout_vec_kernel<T, false, 1>);
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p);
 }
 
 }  // namespace
@@ -175,10 +196,15 @@ cudaError_t launch_dropout(const muon_dropout_args& a, cudaStream_t s) {
     p.ld_y = a.ld_y;
     p.n = a.rows * a.cols;
     p.counter = a.counter;
-    p.seed = a.seed;
     p.offset = a.offset;
-    p.limit = static_cast<uint32_t>(a.p * 65536.0 + 0.5);
-    p.scale = p.limit < 65536u ? static_cast<float>(65536.0 / (65536.0 - p.limit)) : 0.f;
+    for (uint32_t i = 0; i < 10; ++i) {
+        p.key[0][i] = static_cast<uint32_t>(a.seed) + i * 0x9E3779B9u;
+        p.key[1][i] = static_cast<uint32_t>(a.seed >> 32) + i * 0xBB67AE85u;
+    }
+    const uint32_t limit = static_cast<uint32_t>(a.p * 65536.0 + 0.5);
+    p.all = limit == 65536u;
+    p.limit = p.all ? 0xffffffffu : limit << 16;
+    p.scale = p.all ? 0.f : static_cast<float>(65536.0 / (65536.0 - limit));
     return a.x_dtype == MUON_F32 ? launch<float>(p, s) : launch<__nv_bfloat16>(p, s);
 }
 
