@@ -812,47 +812,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             uint32_t full_phase = 0, patch_phase = 0;       // a bit a stage
             uint32_t uses[2] = {0, 0};
             uint32_t acc = 0;
-            bool ok = true, any = false;
+            bool any = false;
             const uint64_t a_desc = smem_desc(smem_u32(smem), A_MN ? F_BOX : 16, 1024);
             const uint64_t b_desc = smem_desc(smem_u32(smem + F_OP_BYTES), B_MN ? F_BOX : 16, 1024);
-            for (Item x; ok;) {
-                ok = feed.next<false>(x, abort_flag, limit);
-                if (!ok || x.e < 0) break;
-                if (x.steps == 0) continue;
+            const uint32_t full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
+            uint32_t idesc = 0, d_tmem = 0;
+            auto products = [&](uint32_t fresh) {
+                const uint64_t ad = a_desc + (slot * F_STAGE_BYTES >> 4);
+                const uint64_t bd = b_desc + (slot * F_STAGE_BYTES >> 4);
+#pragma unroll
+                for (int kk = 0; kk < F_K / 16; ++kk)
+                    mma_pair(d_tmem, ad + uint64_t(kk * (A_MN ? 2048 : 32) >> 4),
+                             bd + uint64_t(kk * (B_MN ? 2048 : 32) >> 4), idesc, kk ? 1u : fresh);
+                commit_pair_multicast(empty0 + 8 * slot);
+            };
+            // The next tile and its accumulator are asked for while this one's
+            // products run: one after the other they took 800 cycles between
+            // two tiles.  The loop over steps has nothing in it that it could do without:
+            // its thread is what the products wait for where the sums are long.
+            Item x, y;
+            y.e = -1;
+            bool there = false, free_acc = false;
+            bool ok = feed.next<false>(x, abort_flag, limit);
+            while (ok && x.e >= 0) {
+                if (x.steps == 0) {
+                    ok = feed.next<false>(x, abort_flag, limit);
+                    continue;
+                }
                 const uint32_t use = acc ? uses[1]++ : uses[0]++;
-                if (!wait_soon(smem_u32(&tempty_bar[acc]), (use & 1) ^ 1, abort_flag, &g_ffn_err, limit)) {
+                if (!free_acc &&
+                    !wait_soon(smem_u32(&tempty_bar[acc]), (use & 1) ^ 1, abort_flag, &g_ffn_err, limit)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t idesc = instr_desc(256, x.n, B_MN) | (A_MN ? 1u << 15 : 0u);
-                const int short_step = OP == DW && x.tail ? x.steps - 1 : -1;
-                bool there = false;
+                idesc = instr_desc(256, x.n, B_MN) | (A_MN ? 1u << 15 : 0u);
+                d_tmem = tmem_base + acc * 256;
+                uint32_t fresh = 0;
+                any = true;
 #pragma unroll 1
-                for (int s = 0; s < x.steps; ++s) {
-                    const bool tail = s == short_step;
-                    const uint32_t bar = smem_u32(tail ? &patch_bar[slot] : &full_bar[slot]);
-                    uint32_t& phase = tail ? patch_phase : full_phase;
-                    if (!there && !wait_soon(bar, phase >> slot & 1, abort_flag, &g_ffn_err, limit)) {
+                for (int s = x.steps - 1; s > 0; --s) {
+                    if (!there &&
+                        !wait_soon(full0 + 8 * slot, full_phase >> slot & 1, abort_flag, &g_ffn_err, limit)) {
                         ok = false;
                         break;
                     }
-                    phase ^= 1u << slot;
-                    if (tail) tc_fence_after();
+                    full_phase ^= 1u << slot;
                     const uint32_t next = slot + 1 == STAGES ? 0 : slot + 1;
-                    there = s + 1 != short_step && is_over(smem_u32(&full_bar[next]), full_phase >> next & 1);
-                    const uint64_t ad = a_desc + (slot * F_STAGE_BYTES >> 4);
-                    const uint64_t bd = b_desc + (slot * F_STAGE_BYTES >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < F_K / 16; ++kk)
-                        mma_pair(tmem_base + acc * 256, ad + uint64_t(kk * (A_MN ? 2048 : 32) >> 4),
-                                 bd + uint64_t(kk * (B_MN ? 2048 : 32) >> 4), idesc, (s || kk) ? 1u : 0u);
-                    any = true;
-                    commit_pair_multicast(smem_u32(&empty_bar[slot]));
+                    there = is_over(full0 + 8 * next, full_phase >> next & 1);
+                    products(fresh);
+                    fresh = 1;
                     slot = next;
                 }
-                if (ok) commit_pair_multicast(smem_u32(&tfull_bar[acc]));
+                if (!ok || !(ok = feed.next<false>(y, abort_flag, limit))) break;
+                // the last step, which DW's may be a short one
+                if (OP == DW && x.tail) {
+                    if (!wait_soon(smem_u32(&patch_bar[slot]), patch_phase >> slot & 1, abort_flag, &g_ffn_err,
+                                   limit)) {
+                        ok = false;
+                        break;
+                    }
+                    patch_phase ^= 1u << slot;
+                    tc_fence_after();
+                } else {
+                    if (!there &&
+                        !wait_soon(full0 + 8 * slot, full_phase >> slot & 1, abort_flag, &g_ffn_err, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    full_phase ^= 1u << slot;
+                }
+                free_acc = is_over(smem_u32(&tempty_bar[acc ^ 1]), ((acc ? uses[0] : uses[1]) & 1) ^ 1);
+                products(fresh);
+                slot = slot + 1 == STAGES ? 0 : slot + 1;
+                commit_pair_multicast(smem_u32(&tfull_bar[acc]));
+                there = false;
                 acc ^= 1;
+                x = y;
             }
             if (!ok && any) {
                 commit_pair_local(smem_u32(drain_bar));
