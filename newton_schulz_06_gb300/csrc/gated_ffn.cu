@@ -382,6 +382,23 @@ __device__ __forceinline__ bool is_over(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// The same, and a wait, for a whole warp, whose lanes agree.
+__device__ __forceinline__ bool is_over_warp(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, is_over(bar, parity));
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
+    return __all_sync(0xffffffffu, wait_soon(bar, parity, abort_flag, &g_ffn_err, limit));
+}
+// One lane of a whole warp.
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "elect.sync _|P, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, P;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
 // 16 bytes to shared memory, and a wait for all of this thread's.
 __device__ __forceinline__ void copy16(void* to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
@@ -807,7 +824,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             // the other CTA's thread lets its tiles pass
             for (Item x; feed.next<false>(x, abort_flag, limit) && x.e >= 0;) {
             }
-        } else if (lane == 0) {
+        } else if (rank == 0) {
             uint32_t slot = 0;
             uint32_t full_phase = 0, patch_phase = 0;       // a bit a stage
             uint32_t uses[2] = {0, 0};
@@ -820,28 +837,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             auto products = [&](uint32_t fresh) {
                 const uint64_t ad = a_desc + (slot * F_STAGE_BYTES >> 4);
                 const uint64_t bd = b_desc + (slot * F_STAGE_BYTES >> 4);
+                if (elected()) {
 #pragma unroll
-                for (int kk = 0; kk < F_K / 16; ++kk)
-                    mma_pair(d_tmem, ad + uint64_t(kk * (A_MN ? 2048 : 32) >> 4),
-                             bd + uint64_t(kk * (B_MN ? 2048 : 32) >> 4), idesc, kk ? 1u : fresh);
-                commit_pair_multicast(empty0 + 8 * slot);
+                    for (int kk = 0; kk < F_K / 16; ++kk)
+                        mma_pair(d_tmem, ad + uint64_t(kk * (A_MN ? 2048 : 32) >> 4),
+                                 bd + uint64_t(kk * (B_MN ? 2048 : 32) >> 4), idesc, kk ? 1u : fresh);
+                    commit_pair_multicast(empty0 + 8 * slot);
+                }
+                __syncwarp();
+            };
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                return wait_warp(bar, parity, abort_flag, limit);
             };
             // The next tile and its accumulator are asked for while this one's
             // products run: one after the other they took 800 cycles between
-            // two tiles.  The loop over steps has nothing in it that it could do without:
-            // its thread is what the products wait for where the sums are long.
+            // two tiles.  The loop over steps has nothing in it that it could do
+            // without, and all lanes run it, so that one of them issues products from
+            // values the whole warp shares: the products wait for this loop
+            // where the sums are long (8192 tokens of 4096 x 11008, forward: 1400 us
+            // with the short step and the tile's end in the loop, 1297
+            // without, 1250 with the whole warp).
             Item x, y;
             y.e = -1;
             bool there = false, free_acc = false;
-            bool ok = feed.next<false>(x, abort_flag, limit);
+            bool ok = feed.next<true>(x, abort_flag, limit);
             while (ok && x.e >= 0) {
                 if (x.steps == 0) {
-                    ok = feed.next<false>(x, abort_flag, limit);
+                    ok = feed.next<true>(x, abort_flag, limit);
                     continue;
                 }
                 const uint32_t use = acc ? uses[1]++ : uses[0]++;
-                if (!free_acc &&
-                    !wait_soon(smem_u32(&tempty_bar[acc]), (use & 1) ^ 1, abort_flag, &g_ffn_err, limit)) {
+                if (!free_acc && !wait(smem_u32(&tempty_bar[acc]), (use & 1) ^ 1)) {
                     ok = false;
                     break;
                 }
@@ -852,45 +878,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 any = true;
 #pragma unroll 1
                 for (int s = x.steps - 1; s > 0; --s) {
-                    if (!there &&
-                        !wait_soon(full0 + 8 * slot, full_phase >> slot & 1, abort_flag, &g_ffn_err, limit)) {
+                    if (!there && !wait(full0 + 8 * slot, full_phase >> slot & 1)) {
                         ok = false;
                         break;
                     }
                     full_phase ^= 1u << slot;
                     const uint32_t next = slot + 1 == STAGES ? 0 : slot + 1;
-                    there = is_over(full0 + 8 * next, full_phase >> next & 1);
+                    there = is_over_warp(full0 + 8 * next, full_phase >> next & 1);
                     products(fresh);
                     fresh = 1;
                     slot = next;
                 }
-                if (!ok || !(ok = feed.next<false>(y, abort_flag, limit))) break;
+                if (!ok || !(ok = feed.next<true>(y, abort_flag, limit))) break;
                 // the last step, which DW's may be a short one
                 if (OP == DW && x.tail) {
-                    if (!wait_soon(smem_u32(&patch_bar[slot]), patch_phase >> slot & 1, abort_flag, &g_ffn_err,
-                                   limit)) {
+                    if (!wait(smem_u32(&patch_bar[slot]), patch_phase >> slot & 1)) {
                         ok = false;
                         break;
                     }
                     patch_phase ^= 1u << slot;
                     tc_fence_after();
                 } else {
-                    if (!there &&
-                        !wait_soon(full0 + 8 * slot, full_phase >> slot & 1, abort_flag, &g_ffn_err, limit)) {
+                    if (!there && !wait(full0 + 8 * slot, full_phase >> slot & 1)) {
                         ok = false;
                         break;
                     }
                     full_phase ^= 1u << slot;
                 }
-                free_acc = is_over(smem_u32(&tempty_bar[acc ^ 1]), ((acc ? uses[0] : uses[1]) & 1) ^ 1);
+                free_acc = is_over_warp(smem_u32(&tempty_bar[acc ^ 1]), ((acc ? uses[0] : uses[1]) & 1) ^ 1);
                 products(fresh);
                 slot = slot + 1 == STAGES ? 0 : slot + 1;
-                commit_pair_multicast(smem_u32(&tfull_bar[acc]));
+                if (elected()) commit_pair_multicast(smem_u32(&tfull_bar[acc]));
+                __syncwarp();
                 there = false;
                 acc ^= 1;
                 x = y;
             }
-            if (!ok && any) {
+            if (!ok && any && lane == 0) {
                 commit_pair_local(smem_u32(drain_bar));
                 wait_quiet(smem_u32(drain_bar), 0, limit);
             }
