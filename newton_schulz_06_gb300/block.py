@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional, Tuple, Union
 
 import torch
@@ -96,7 +97,10 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     no expert are not written (a new y holds anything there).
     activation: "silu", "gelu" (by erf) or "gelu_tanh".
     Returns (y, saved): saved is (g, u), both rows x inner, for
-    :func:`gated_ffn_backward`, or None without keep."""
+    :func:`gated_ffn_backward`, or None without keep.  They are rounded to
+    bf16, which is half of the error that the gradients then have.  out may be x.
+    The last bits of a row may depend on the number of rows beside it (long sums
+    of few rows are added up in parts)."""
     rows, hidden, ld_x, index = _matrix("x", x)
     _need(x.dtype == _BF16, f"x must be bfloat16, got {x.dtype}")
     act = _activation(activation)
@@ -203,7 +207,7 @@ class RotaryPlan:
     for those that turn more than fast times, a ramp between, and the result
     times 0.1 ln(factor) + 1).  A plan is host data and serves any device."""
 
-    __slots__ = ("dim", "layout", "scale", "_turns", "_at")
+    __slots__ = ("dim", "layout", "scale", "_turns")
 
     def __init__(self, dim: int, *, base: float = 10000.0, layout: str = "half", scaling: str = "none",
                  factor: float = 1.0, original: float = 4096, fast: float = 32.0, slow: float = 1.0):
@@ -219,12 +223,13 @@ class RotaryPlan:
         if rc < 0:
             raise MuonError(rc, f"muon_rotary_frequencies: {err.value.decode(errors='replace')}")
         self.dim, self.layout, self.scale = dim, _LAYOUTS[layout], scale.value
-        self._turns, self._at = turns, ctypes.addressof(turns)
+        self._turns = bytes(turns)       # one 64-bit fraction of a turn a pair
 
     @property
     def frequencies(self) -> Tuple[float, ...]:
         """Radians a position of every pair."""
-        return tuple(t * (2.0 * math.pi) * 2.0 ** -64 for t in self._turns)
+        return tuple(t * (2.0 * math.pi) * 2.0 ** -64
+                     for t in struct.unpack(f"={self.dim // 2}Q", self._turns))
 
 
 def _heads(name: str, t: torch.Tensor, index: int):
@@ -262,6 +267,11 @@ def _turned(name: str, x: torch.Tensor, out, shape, strides, index: int):
     return (x.data_ptr(), out.data_ptr(), heads, *strides, *to), out
 
 
+def _address(b: bytes) -> int:
+    """Where an object's bytes are, for a call that reads them before it returns."""
+    return ctypes.cast(b, ctypes.c_void_p).value
+
+
 def _turn(q, k, plan: RotaryPlan, positions, offset: int, out_q, out_k, inverse: bool):
     index = q.get_device()
     shape, strides = _heads("q", q, index)
@@ -291,7 +301,7 @@ def _turn(q, k, plan: RotaryPlan, positions, offset: int, out_q, out_k, inverse:
         at, wide = positions.data_ptr(), positions.dtype == torch.int64
         stride = positions.stride(0) if len(want) == 2 and want[0] > 1 else 0
     _call(index, "muon_rotary", _rotary_args(
-        *first, *second, at, plan._at, batch, seq, head, plan.dim // 2, stride, offset, dtype,
+        *first, *second, at, _address(plan._turns), batch, seq, head, plan.dim // 2, stride, offset, dtype,
         plan.layout, wide, inverse, plan.scale))
     return out_q, out_k
 

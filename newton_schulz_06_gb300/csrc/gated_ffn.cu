@@ -1334,12 +1334,15 @@ struct Cut {
 };
 
 // Parts that the sums are cut into, so that every pair has a tile, of four
-// steps at least.  Joining them costs a launch and their way through L2, about
-// 4 us, which eight steps (0.3 us each) of what is saved must outweigh twice.
+// steps at least.  Joining them costs a launch, 3 us of the caller's time and
+// about as much of the GPU's, so that 48 steps (0.2 us each, and more where the
+// matrices come from memory) have to be saved: 64 tokens of 7168 x 2048 take 28 us
+// forward and 70 back, 41 and 95 unsplit; 5 tokens of 2048 x 768, 28 steps saved
+// forward, took 15 us instead of 17, but the caller 26 instead of 23.
 int split_count(int64_t tiles, int64_t steps) {
     int64_t s = F_PAIRS / tiles;
     if (s > steps / 4) s = steps / 4;
-    return s >= 2 && steps - steps / s >= 24 ? static_cast<int>(s) : 1;
+    return s >= 2 && steps - steps / s >= 48 ? static_cast<int>(s) : 1;
 }
 
 // op, for rows x ... of one dense block (experts: a tile's rows go by the

@@ -403,6 +403,9 @@ MUON_API int muon_gated_ffn_grad(const muon_gated_ffn_grad_args* a, void* ws, si
                           a->stride_dw_up));
     RETURN_IF(check_grads(err, "dw_down", a->dw_down, a->g_dtype, a->hidden, a->inner, a->ld_dw_down, a->experts,
                           a->stride_dw_down));
+    // dy and x are read after dx is written
+    if (a->rows && a->dx && ((a->dw_down && a->dx == a->dy) || (x_grads && a->dx == a->x)))
+        return err.bad("dx is dy or x, which a weight's gradient reads");
     void* const made[3] = {a->dgate, a->dup, a->h};
     for (const void* m : made)
         if (m) RETURN_IF(check_tensor(err, "dgate, dup or h", m, MUON_BF16, a->rows, a->inner, a->ld_d, false));

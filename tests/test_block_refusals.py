@@ -37,7 +37,7 @@ def fields(struct, base, **kw):
 
 FFN = dict(x=P, w_gate=P, w_up=P, w_down=P, y=P, gate=P, up=P, rows=4, hidden=64, inner=32, experts=1,
            ld_x=64, ld_gate=64, ld_up=64, ld_down=32, ld_y=64, ld_kept=32)
-GRAD = dict(dy=P, x=P, gate=P, up=P, w_gate=P, w_up=P, w_down=P, dx=P, dw_gate=P, dw_up=P, dw_down=P, rows=4,
+GRAD = dict(dy=P, x=P, gate=P, up=P, w_gate=P, w_up=P, w_down=P, dx=P + 1024, dw_gate=P, dw_up=P, dw_down=P, rows=4,
             hidden=64, inner=32, experts=1, ld_dy=64, ld_x=64, ld_kept=32, ld_gate=64, ld_up=64, ld_down=32,
             ld_dx=64, ld_dw_gate=64, ld_dw_up=64, ld_dw_down=32, g_dtype=1)
 EXPERTS = dict(offsets=P, experts=3, stride_gate=2048, stride_up=2048, stride_down=2048, stride_dw_gate=2048,
@@ -68,7 +68,8 @@ def test_gated_ffn_refuses(L, kw, word):
     (dict(up=P + 1), "up is not aligned"), (dict(ld_kept=8), "gate"), (dict(w_gate=None), "w_gate"),
     (dict(w_down=None), "w_down"), (dict(ld_dx=63), "dx"), (dict(ld_dw_gate=0), "dw_gate"),
     (dict(dw_up=P + 2, g_dtype=0), "dw_up"), (dict(ld_dw_down=31), "dw_down"), (dict(h=P, ld_d=31), "dgate, dup or h"),
-    (dict(dgate=P + 1, ld_d=32), "dgate, dup or h"), ({**EXPERTS, "stride_dw_down": 2047}, "dw_down"),
+    (dict(dgate=P + 1, ld_d=32), "dgate, dup or h"), (dict(dx=P, dy=P, x=P + 64), "dx is dy or x"),
+    (dict(dx=P, x=P, dy=P + 64), "dx is dy or x"), ({**EXPERTS, "stride_dw_down": 2047}, "dw_down"),
     ({**EXPERTS, "stride_up": -8}, "w_up")])
 def test_gated_ffn_grad_refuses(L, kw, word):
     a = fields(L.GatedFfnGradArgs, GRAD, **kw)
@@ -148,6 +149,11 @@ def test_rotary_frequencies(L):
         assert abs(plan.scale - scale) <= O.U32 * scale and len(plan.frequencies) == args["dim"] // 2
         for a, b in zip(plan.frequencies, freq):
             assert abs(a - b) <= 2.0 ** -50 * b + 2 * math.pi * 2.0 ** -64
+    import copy
+    import pickle
+    for twin in (copy.deepcopy(plan), pickle.loads(pickle.dumps(plan))):
+        assert twin.frequencies == plan.frequencies and (twin.dim, twin.layout, twin.scale) == (
+            plan.dim, plan.layout, plan.scale)
     for bad in (dict(dim=3), dict(dim=0), dict(dim=514), dict(dim=8, layout="both"), dict(dim=8, scaling="more")):
         with pytest.raises(ValueError):
             ns.RotaryPlan(**bad)

@@ -345,7 +345,8 @@ def test_gated_ffn(ns, tokens, hidden, inner, name):
 
 @pytest.mark.parametrize("tokens,hidden,inner,dtype", [(3, 4096, 520, BF), (40, 7168, 256, BF), (1, 520, 4100, BF),
                                                        (70, 2049, 2050, BF), (3000, 264, 136, BF),
-                                                       (4100, 100, 72, F32), (2500, 513, 31, F32)])
+                                                       (4100, 264, 136, BF), (4100, 100, 72, F32),
+                                                       (4500, 513, 31, F32)])
 def test_gated_ffn_of_few_tiles(ns, tokens, hidden, inner, dtype):
     """Long sums of few outputs, which are cut into parts and joined."""
     x, w = rand(25, tokens, hidden, dtype=BF), weights(26, hidden, inner)
@@ -512,11 +513,12 @@ def test_gated_ffn_of_no_rows(ns):
     assert all(torch.equal(g, b) for g, b in zip(got[1:], base))
 
 
+@pytest.mark.parametrize("inner", [72, 45])
 @pytest.mark.parametrize("counts", [None, [40, 0, 1, 159]])
-def test_gated_ffn_from_a_checkpoint(ns, counts):
+def test_gated_ffn_from_a_checkpoint(ns, counts, inner):
     """x kept in 8 bits, with a norm's weight and bias: the gradients of w_gate
     and w_up are those of what the checkpoint stands for."""
-    t, hidden, inner = 200, 136, 72
+    t, hidden = 200, 136
     offsets = None if counts is None else bounds_of(counts)
     w = weights(91, hidden, inner, 0 if counts is None else 4)
     h, dy = ns.checkpoint8(rand(94, t, hidden)), rand(95, t, hidden, scale=0.1, dtype=BF)
@@ -538,6 +540,64 @@ def test_gated_ffn_from_a_checkpoint(ns, counts):
             close_norm(a, 2 * b.to(D), "added")
     none = ns.gated_ffn_backward(dy, None, saved, *w, offsets=offsets, dtype=F32)
     assert none[1] is None and none[2] is None and torch.equal(none[3], got[3]) and torch.equal(none[0], got[0])
+
+
+def test_gated_ffn_some_gradients_and_in_place(ns):
+    """Any of the weights' gradients alone, what is made on the way in tensors
+    of the caller's (through the C entry), and y in x's place."""
+    import ctypes
+
+    from newton_schulz_06_gb300 import _lib
+    t, hidden, inner = 150, 104, 45
+    x, w, dy = rand(120, t, hidden, dtype=BF), weights(121, hidden, inner), rand(124, t, hidden, dtype=BF)
+    y, saved = ns.gated_ffn(x, *w)
+    want = ns.gated_ffn_backward(dy, x, saved, *w)
+    for i in range(3):
+        grads = [None, None, None]
+        grads[i] = torch.empty_like(w[i])
+        got = ns.gated_ffn_backward(dy, x, saved, *w, grads=grads)
+        assert torch.equal(got[0], want[0])
+        assert all((g is None) if j != i else torch.equal(g, want[j + 1]) for j, g in enumerate(got[1:]))
+    made = [torch.empty(t, inner, dtype=BF, device=DEV) for _ in range(3)]
+    a = _lib.GatedFfnGradArgs(dy=dy.data_ptr(), gate=saved[0].data_ptr(), up=saved[1].data_ptr(),
+                              w_down=w[2].data_ptr(), dgate=made[0].data_ptr(), dup=made[1].data_ptr(),
+                              h=made[2].data_ptr(), rows=t, hidden=hidden, inner=inner, experts=1, ld_dy=hidden,
+                              ld_kept=inner, ld_down=inner, ld_d=inner)
+    size = ctypes.c_size_t()
+    L = _lib.lib()
+    assert L.muon_gated_ffn_grad_workspace(ctypes.byref(a), ctypes.byref(size)) == 0
+    ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=DEV)
+    assert L.muon_gated_ffn_grad(ctypes.byref(a), ws.data_ptr(), size.value,
+                                 torch.cuda.current_stream().cuda_stream, None, 0) == 0
+    f, df, _ = O.act("silu", saved[0].to(D))
+    dh = dy.to(D) @ w[2].to(D)
+    for got, exact in zip(made, (dh * saved[1].to(D) * df, dh * f, f * saved[1].to(D))):
+        close_norm(got, exact, "made")
+    z = x.clone()
+    assert ns.gated_ffn(z, *w, out=z)[0] is z and torch.equal(z, y)
+
+
+def test_gated_ffn_past_32_bits(ns):
+    """Rows whose kept values lie past 2^31 elements."""
+    rows, hidden, inner, n = 270000, 64, 8192, 40
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GiB of device memory")
+    x, w = torch.zeros(rows, hidden, dtype=BF, device=DEV), weights(130, hidden, inner)
+    x[-n:] = rand(133, n, hidden, dtype=BF)
+    y, saved = ns.gated_ffn(x, *w)
+    assert not y[:-n].any() and not saved[0][:-n].any()
+    tail = [v[-n:].clone() for v in saved]
+    check_forward(x[-n:], w, y[-n:], tail)
+    dy = torch.zeros_like(x)
+    dy[-n:] = rand(134, n, hidden, scale=0.1, dtype=BF)
+    got = ns.gated_ffn_backward(dy, x, saved, *w)
+    assert not got[0][:-n].any()
+    want, bounds = O.ffn_grad(dy[-n:], x[-n:], *tail, *w)
+    for i, what in enumerate(("dx", "dw_gate", "dw_up", "dw_down")):
+        near(got[i][-n:] if i == 0 else got[i], want[i], bounds[i], what)
+    del saved, got
+    torch.cuda.empty_cache()
 
 
 @pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
@@ -631,3 +691,67 @@ def test_run_of_a_block(ns):
         for a, b in zip(eager, outs):
             assert torch.equal(a, b)
     ns.ops_sync()
+
+
+def test_example_block(ns):
+    """The example's block: its gradients are those of the same block with
+    autograd in 64 bits, within what bf16 and 8-bit activations cost."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "train_gated_block.py")
+    spec = importlib.util.spec_from_file_location("train_gated_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    T, H = 96, 64
+    block = ex.Block(hidden=H, heads=4, kv_heads=2, head=16, inner=48, experts=8, k=2, p=0.2)
+    x, dout = rand(140, T, H, dtype=BF), rand(141, T, H, dtype=BF)
+    out = block.forward(x, step=3)
+    dx = block.backward(dout)
+    names = ("wq", "wk", "wv", "wo", "router", "w_gate", "w_up", "w_down", "gain1", "shift1", "gain2", "shift2")
+    leaf = {n: getattr(block, n).to("cpu", D).requires_grad_() for n in names}
+    xr = x.to("cpu", D).requires_grad_()
+    kept = block.kept
+    freq, _ = O.frequencies(16)
+    angle = torch.arange(T, dtype=D)[:, None] * torch.tensor(freq, dtype=D)
+
+    def turn(v):
+        c, s = torch.cos(angle)[:, None], torch.sin(angle)[:, None]
+        a, b = v[..., :8], v[..., 8:]
+        return torch.cat([a * c - b * s, b * c + a * s], -1)
+
+    def drop(v, offset):
+        keep = torch.tensor(O.kept(T * H, 0.2, block.seed, offset)).view(T, H)
+        return v * keep * (65536 / (65536 - math.floor(0.2 * 65536 + 0.5)))
+
+    norm = torch.nn.functional.layer_norm
+    y1 = norm(xr, (H,), leaf["gain1"], leaf["shift1"])
+    q, k, v = (y1 @ leaf[n].t() for n in ("wq", "wk", "wv"))
+    q, k, v = turn(q.view(T, 4, 16)), turn(k.view(T, 2, 16)), v.view(T, 2, 16)
+    k, v = k.repeat_interleave(2, 1), v.repeat_interleave(2, 1)
+    s = torch.einsum("qhd,khd->hqk", q, k) / 4
+    s = s.masked_fill(torch.ones(T, T).triu(1).bool(), -math.inf)
+    a = torch.einsum("hqk,khd->qhd", torch.softmax(s, -1), v).reshape(T, -1)
+    x1 = xr + drop(a @ leaf["wo"].t(), 6)
+    y2 = norm(x1, (H,), leaf["gain2"], leaf["shift2"])
+    p = torch.softmax(y2 @ leaf["router"].t(), -1)
+    idx = kept["routing"].indices.cpu().long()
+    w = p.gather(1, idx)
+    w = w / w.sum(-1, keepdim=True)
+    g = torch.einsum("tkih,th->tki", leaf["w_gate"][idx], y2)
+    u = torch.einsum("tkih,th->tki", leaf["w_up"][idx], y2)
+    f = torch.einsum("tkhi,tki->tkh", leaf["w_down"][idx], torch.nn.functional.silu(g) * u)
+    ref = x1 + drop((w[..., None] * f).sum(1), 7)
+    counts = torch.bincount(idx.flatten(), minlength=8).to(D)
+    balance = 0.01 * 8 / (2 * T) * (counts * p.mean(0)).sum()
+    ((ref * dout.to("cpu", D)).sum() + balance).backward()
+    got = {n: block.grads[n] for n in names}
+    # a value has passed about ten roundings to bf16 and one to 8 bits on its
+    # way: a few percent of the norm
+    for name, have, want in (("out", out, ref.detach()), ("dx", dx, xr.grad),
+                             *((n, got[n], leaf[n].grad) for n in names)):
+        off = (have.to("cpu", D) - want).norm() / want.norm()
+        assert off <= 0.08, (name, off.item())
+    block.muon.close()
+    losses = ex.train(steps=3, tokens=128, hidden=64, inner=32, experts=4)
+    assert len(losses) == 3 and all(math.isfinite(v) for v in losses)
