@@ -16,16 +16,28 @@
 // tokens would waste a quarter).  UP takes 64 rows of Wg and the same 64 of Wu
 // as a CTA's 128 rows, so that a tile has both factors of its h.
 //
-// TMEM holds m in lanes and n in columns, memory wants m along rows: the
-// epilogue turns 16 columns at a time in shared memory (fp32), after which a
-// thread has eight neighbours of an output row, reads what it needs beside
-// them, and stores 16 bytes.
+// TMEM holds m in lanes and n in columns, memory wants m along rows.  Sums that
+// leave as bf16 (DOWN, DX, DW) are turned by stmatrix, 32 columns at a time;
+// those that something is still done to (UP, DHIDDEN, fp32 or added gradients,
+// parts of a split) go through shared memory in fp32, 16 columns at a time, after
+// which a thread has eight neighbours of an output row, reads what it needs
+// beside them, and stores 16 bytes.
 //
 // Roles in a CTA: warps 0 and 11 load (TMA), warp 1 issues the products (the
 // pair's leader only), warps 2-9 are the epilogue, in two teams of four that
 // take a tile's columns in turn, warp 10 clears what DW loads past an expert's
-// last token, warp 12 finds the tiles.  Two accumulators, so that a tile is written out while the next one's
-// products run.  Pairs walk the tiles in turn.
+// last token, warp 12 finds the tiles.  Two accumulators, so that a tile is
+// written out while the next one's products run.  Pairs walk the tiles in turn.
+//
+// What bounds it.  Long sums: the tensor cores, at the rate that the power
+// limit leaves the library's product too (8192 tokens of 4096 x 11008: forward
+// 1245 us, 1.78 PFLOP/s; DX 846 us, 1.75; DW, both of whose operands have k as
+// rows, 1343 us, 1.65; DHIDDEN 496 us, 1.49, whose write-out reads two
+// and writes three values a sum).  128 experts of 2048 x 768 over 65536 rows:
+// forward 426 us and DX 290, the loads of tiles that are not full and the ends of
+// tiles of 12 to 32 steps; DHIDDEN 214, memory (5.5 TB/s); DW 510, tiles of
+// eight steps whose 1.2 GB of results leave meanwhile (442 us without storing
+// them).
 //
 // Every wait is bounded; one that runs out raises g_ffn_err (muon_ops_sync).
 #include <algorithm>
@@ -76,7 +88,7 @@ struct Space {
     static constexpr int TURN = ITEMS + 256;
     static constexpr int KEPT = TURN + 2 * F_TURN_BYTES;     // two teams'
     static constexpr int TABLE = KEPT + (OP == DHIDDEN ? 2 * F_KEPT_BYTES : 0);
-    static constexpr int BYTES = TABLE + 3 * (F_EXPERTS + 1) * 4 + 1024;
+    static constexpr int BYTES = TABLE + 2 * (F_EXPERTS + 1) * 4 + 1024;
     static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
@@ -107,7 +119,7 @@ struct FfnLaunch {
     int32_t m[2], k;         // extents; DW: m[0] is hidden, m[1] inner; else m[0]
     int32_t a_by_expert[3];  // an expert's own matrix, or one for all
     int32_t products;        // DW: which of them, as bits
-    int32_t tile_n;          // one dense block: rows of N a tile, a multiple of 32
+    int32_t tile_n;          // rows of N a tile, a multiple of 32
     int32_t splits;          // parts of the sums that tiles of their own take
     float* part;             // splits > 1: their sums, split by split,
     int64_t part_stride;
@@ -154,13 +166,11 @@ struct alignas(16) Item {
 };
 static_assert(F_ITEMS * sizeof(Item) <= 256, "tiles handed out");
 
-// The tiles' places.  An expert's rows are split evenly over as few tiles as
-// they need (300 rows: 160 and 140, not 256 and 44), because a narrow tile
-// loads all of its matrix rows like any other.
+// The tiles' places.
 template <int OP>
 struct Tiles {
     const FfnLaunch& p;
-    const int32_t *begin, *first, *high;     // experts' first rows, first tile rows, rows of a tile
+    const int32_t *begin, *first;            // experts' first rows, and first rows of tiles
     int32_t total, steps;
     Divisor whole;                           // tiles of the whole sums
     Divisor tiles_m, band;                   // tiles across M, and in a band
@@ -169,7 +179,6 @@ struct Tiles {
     __device__ __forceinline__ Tiles(const FfnLaunch& l, const int32_t* table) : p(l) {
         begin = table;
         first = begin + p.experts + 1;
-        high = first + p.experts + 1;
         if constexpr (OP == DW) {
             uint32_t all = 0;
 #pragma unroll
@@ -229,7 +238,7 @@ struct Tiles {
             tm = tiles_m;
             b = band;
             tn = first[lo + 1] - first[lo];
-            size = high[lo];
+            size = p.tile_n;
             end = begin[lo + 1];
             x.t0 = 0;
             all = steps;
@@ -787,11 +796,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             }
             b = max(b, rows);
             const int32_t before = __shfl_up_sync(0xffffffffu, b, 1);
-            // tiles of the expert before e, and their rows
+            // tiles of the expert before e
             const int32_t len = e ? b - (lane ? before : rows) : 0;
-            int32_t n = p.tile_n ? (len + p.tile_n - 1) / p.tile_n : (len + 255) / 256;
-            if (n && e <= p.experts)
-                table[2 * (p.experts + 1) + e - 1] = p.tile_n ? p.tile_n : ((len + n - 1) / n + 31) & ~31;
+            int32_t n = (len + p.tile_n - 1) / p.tile_n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int32_t v = __shfl_up_sync(0xffffffffu, n, o);
@@ -1327,7 +1334,7 @@ cudaError_t launch_op(Op op, const FfnLaunch& p, int64_t items, cudaStream_t s) 
 
 // How one dense block's product is cut up.
 struct Cut {
-    int tile_n = 0, splits = 1;
+    int tile_n = 256, splits = 1;
     int64_t row_tiles = 0;
     int64_t ld[2] = {0, 0}, at[3] = {0, 0, 0}, stride = 0;     // of the parts
     size_t bytes = 0;
@@ -1353,8 +1360,9 @@ Cut cut(Op op, bool dense, int64_t rows, int64_t experts, int64_t m, int64_t k) 
     if (!dense || rows == 0) return c;
     // tiles of as many rows as make the pairs' rounds come out best: a round of
     // narrower tiles takes less, though not in proportion, because the
-    // matrices' part of the loads stays (4096 rows of 4096 x 4096: 19 tiles of
-    // 224 rows are four rounds, as 16 of 256 are)
+    // matrices' part of the loads stays (4096 rows of 4096 x 4096, DHIDDEN: 19
+    // tiles of 224 rows are four rounds and take 105 us, 16 of 256 are four, too,
+    // and take 112; 4097 rows of 7168 x 2048 forward: 208 and 216)
     const int64_t across = ceil_div(m, op == UP ? 128 : 256), least = ceil_div(rows, 256);
     int64_t best = -1;
     for (int64_t n = least; n <= least + std::min(least / 2, int64_t(32)); ++n) {
