@@ -468,15 +468,11 @@ __device__ __forceinline__ void turned8(const float* row, int group, float (&v)[
     v[7] = hi.w;
 }
 
-// Eight neighbours of a bf16 row, of which `left` are there.
-__device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int left, bool vec) {
-    if (vec && left >= 8) return *reinterpret_cast<const uint4*>(p);
-    uint4 q = make_uint4(0u, 0u, 0u, 0u);
-    uint16_t* h = reinterpret_cast<uint16_t*>(&q);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < left) h[i] = reinterpret_cast<const uint16_t*>(p)[i];
-    return q;
+// Eight neighbours of a bf16 row, of which `left` (0 or less: none) are there.
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int left) {
+    Vec<__nv_bfloat16, false> v;
+    v.load(p, left);
+    return v.raw;
 }
 __device__ __forceinline__ void widen8(const uint4& q, float (&v)[8]) {
     const float2 f[4] = {bf16x2_f32(q.x), bf16x2_f32(q.y), bf16x2_f32(q.z), bf16x2_f32(q.w)};
@@ -486,29 +482,24 @@ __device__ __forceinline__ void widen8(const uint4& q, float (&v)[8]) {
         v[2 * i + 1] = f[i].y;
     }
 }
-__device__ __forceinline__ void put8(const Out& o, int64_t at, int left, const float (&v)[8]) {
-    __nv_bfloat16* const p = static_cast<__nv_bfloat16*>(o.p) + at;
-    if (o.vec && left >= 8) {
-        store8_bf16(p, v);
-        return;
-    }
+__device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
+    uint4 q;
+    __nv_bfloat162* const h = reinterpret_cast<__nv_bfloat162*>(&q);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < left) p[i] = __float2bfloat16_rn(v[i]);
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    return q;
 }
-// A weight gradient's eight, added to what is there if asked for.
-__device__ __forceinline__ void put8_grad(const Out& o, int64_t at, int left, bool f32, bool add,
-                                          float (&v)[8]) {
-    if (!f32) {
-        if (add) {
-            float c[8];
-            widen8(load8(static_cast<const __nv_bfloat16*>(o.p) + at, left, o.vec), c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += c[i];
-        }
-        put8(o, at, left, v);
-        return;
-    }
+// Eight neighbours of a bf16 row to any address.  All lanes of a warp call
+// this, each eight past the lane before it or at the start of a run; valid:
+// what of the run is left (0 or less: nothing).
+__device__ __forceinline__ void put8(const Out& o, int64_t at, int valid, bool start, const uint4& q) {
+    Vec<__nv_bfloat16, false> v;
+    v.raw = q;
+    v.store(static_cast<__nv_bfloat16*>(o.p) + at, valid, start);
+}
+// A weight gradient's eight, of which `left` are there, added to what is there
+// if asked for.
+__device__ __forceinline__ void put8_f32(const Out& o, int64_t at, int left, bool add, const float (&v)[8]) {
     float* const p = static_cast<float*>(o.p) + at;
     if (o.vec && left >= 8) {
         float4* const q = reinterpret_cast<float4*>(p);
@@ -539,13 +530,15 @@ struct Units {
 };
 
 // Eight neighbours of an output row: v are their sums (UP: g's, and w u's).
+// valid, start: as put8 has them; left: of the eight that are there.  All lanes
+// of a warp call this; WHOLE: all eight are there, on 16 bytes.
 template <int OP, bool WHOLE>
-__device__ __forceinline__ void finish8(const FfnLaunch& p, int e, int j, int row, int m, int left, float (&v)[8],
-                                        float (&w)[8], const uint4& g8, const uint4& u8) {
+__device__ __forceinline__ void finish8(const FfnLaunch& p, int e, int j, int row, int m, int valid, bool start,
+                                        float (&v)[8], float (&w)[8], const uint4& g8, const uint4& u8) {
     auto put = [&](const Out& o, const float (&f)[8]) {
         const int64_t at = row * o.ld + m;
-        if (WHOLE) store8_bf16(static_cast<__nv_bfloat16*>(o.p) + at, f);
-        else put8(o, at, left, f);
+        if (WHOLE) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(o.p) + at) = narrow8(f);
+        else put8(o, at, valid, start, narrow8(f));
     };
     float a[8], d[8];
     if constexpr (OP == UP) {
@@ -573,7 +566,19 @@ __device__ __forceinline__ void finish8(const FfnLaunch& p, int e, int j, int ro
         if (p.out[2].p) put(p.out[2], a);
     } else if constexpr (OP == DW) {
         const Out& o = p.out[j];
-        put8_grad(o, e * o.stride + row * o.ld + m, left, p.out_f32, p.accumulate, v);
+        const int64_t at = e * o.stride + row * o.ld + m;
+        const int left = min(valid, 8);
+        if (p.out_f32) {
+            put8_f32(o, at, left, p.accumulate, v);
+            return;
+        }
+        if (p.accumulate) {
+            float c[8];
+            widen8(load8(static_cast<const __nv_bfloat16*>(o.p) + at, left), c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += c[i];
+        }
+        put8(o, at, valid, start, narrow8(v));
     } else {
         put(p.out[0], v);
     }
@@ -582,8 +587,8 @@ __device__ __forceinline__ void finish8(const FfnLaunch& p, int e, int j, int ro
 // DHIDDEN's g and u of eight places, of which `left` are there.
 __device__ __forceinline__ void load_kept(const FfnLaunch& p, int row, int m, int left, uint4& g8, uint4& u8) {
     const int64_t at = row * p.ld_kept + m;
-    g8 = load8(static_cast<const __nv_bfloat16*>(p.gate) + at, left, p.vec);
-    u8 = load8(static_cast<const __nv_bfloat16*>(p.up) + at, left, p.vec);
+    g8 = load8(static_cast<const __nv_bfloat16*>(p.gate) + at, left);
+    u8 = load8(static_cast<const __nv_bfloat16*>(p.up) + at, left);
 }
 
 template <int OP, bool WHOLE>
@@ -594,12 +599,12 @@ __device__ __forceinline__ void finish_turned(const FfnLaunch& p, const Item& x,
 #pragma unroll
     for (int i = 0; i < Units<OP>::N; ++i) {
         const int r = (tid + 128 * i) / GROUPS, group = tid % GROUPS;
-        const int row = n0 + r, m = m0 + group * 8, left = WHOLE ? 8 : m_end - m;
-        if (!WHOLE && (row >= x.n_end || left <= 0)) continue;
+        const int row = n0 + r, m = m0 + group * 8;
+        const int valid = row < x.n_end ? min(m_end - m, 8 * (GROUPS - group)) : 0;
         float v[8], w[8];
         turned8(turn + r * F_ROW, group, v);
         if (OP == UP) turned8(turn + r * F_ROW, 8 + group, w);
-        finish8<OP, WHOLE>(p, x.e, x.j, row, m, left, v, w, g8[i], u8[i]);
+        finish8<OP, WHOLE>(p, x.e, x.j, row, m, valid, group == 0, v, w, g8[i], u8[i]);
     }
 }
 
@@ -1039,7 +1044,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             if constexpr (OP == DOWN || OP == DX || OP == DW) {
                 if (flat) {
                     const Out& o = p.out[OP == DW ? x.j : 0];
-                    __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(o.p) + (OP == DW ? x.e * o.stride : 0);
                     const uint32_t mine = smem_u32(turn_at) + (lane % 8 * F_ROW16 + lg * 32 + lane / 8 * 8) * 2;
                     for (int c = team; c <= last; c += 2) {
                         team_sync(team);          // the last columns have been read
@@ -1058,23 +1062,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                         }
                         if (c == last) release();
                         team_sync(team);
-                        const int m = m0 + tid % 16 * 8, left = m_end - m;
-                        const int row0 = x.n0 + c * F_COLS16 + tid / 16;
+                        const int m = m0 + tid % 16 * 8, row0 = x.n0 + c * F_COLS16 + tid / 16;
+                        const int left = min(m_end - m, 8 * (16 - tid % 16));
+                        const bool whole = o.vec && m0 + 128 <= m_end;
 #pragma unroll
                         for (int i = 0; i < F_COLS16 / 8; ++i) {
                             const uint4 q = *reinterpret_cast<const uint4*>(
                                 turn_at + ((tid / 16 + 8 * i) * F_ROW16 + tid % 16 * 8) * 2);
-                            if (row0 + 8 * i < x.n_end) {
-                                __nv_bfloat16* const at = to + (row0 + 8 * i) * o.ld + m;
-                                if (o.vec && left >= 8) {
-                                    *reinterpret_cast<uint4*>(at) = q;
-                                } else {
-                                    const uint16_t* const h = reinterpret_cast<const uint16_t*>(&q);
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k)
-                                        if (k < left) reinterpret_cast<uint16_t*>(at)[k] = h[k];
-                                }
-                            }
+                            const int row = row0 + 8 * i;
+                            const int64_t at = (OP == DW ? x.e * o.stride : 0) + row * o.ld + m;
+                            if (!whole)
+                                put8(o, at, row < x.n_end ? left : 0, tid % 16 == 0, q);
+                            else if (row < x.n_end)
+                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(o.p) + at) = q;
                         }
                     }
                 }
@@ -1145,47 +1145,54 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ FfnLa
     grid_dependency_wait();
     allow_dependent_launch();
     const int j = OP == DW ? blockIdx.y : 0;
-    if (OP == DW && !(p.products >> j & 1)) return;
+    if (OP == DW && !(p.products >> j & 1)) return;    // (a whole block)
     const int m_end = p.m[OP == DW && j == 2];
     const int64_t rows = OP == DW ? p.m[j != 2] : p.rows;
     const int64_t ld = p.part_ld[OP == DW && j == 2];
     const int64_t groups = (m_end + 7) / 8;
     const int64_t u = blockIdx.x * int64_t(128) + threadIdx.x;
-    if (u >= rows * groups) return;
-    const int row = static_cast<int>(u / groups), m = static_cast<int>(u - row * groups) * 8;
-    const int left = m_end - m;
+    const bool live = u < rows * groups;
+    const int row = live ? static_cast<int>(u / groups) : 0, m = live ? static_cast<int>(u - row * groups) * 8 : 0;
+    const int left = live ? m_end - m : 0;
     uint4 g8 = make_uint4(0u, 0u, 0u, 0u), u8 = g8;
     if (OP == DHIDDEN) load_kept(p, row, m, left, g8, u8);
     const float* const from = p.part + (OP == DW ? p.part_at[j] : 0) + row * ld + m;
     float v[8] = {}, w[8] = {};
+    if (live) {
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
-        const float4* const q = reinterpret_cast<const float4*>(from + s * p.part_stride);
-        const float4 a = q[0], b = q[1];
-        const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        for (int s = 0; s < p.splits; ++s) {
+            const float4* const q = reinterpret_cast<const float4*>(from + s * p.part_stride);
+            const float4 a = q[0], b = q[1];
+            const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += f[i];
-        if (OP == UP) {
-            const float4* const r = reinterpret_cast<const float4*>(from + s * p.part_stride + ld / 2);
-            const float4 c = r[0], d = r[1];
-            const float g[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+            for (int i = 0; i < 8; ++i) v[i] += f[i];
+            if (OP == UP) {
+                const float4* const r = reinterpret_cast<const float4*>(from + s * p.part_stride + ld / 2);
+                const float4 c = r[0], d = r[1];
+                const float g[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] += g[i];
+                for (int i = 0; i < 8; ++i) w[i] += g[i];
+            }
         }
     }
-    finish8<OP, false>(p, 0, j, row, m, left, v, w, g8, u8);
+    finish8<OP, false>(p, 0, j, row, m, left, m == 0, v, w, g8, u8);
 }
 
-// A tensor that TMA cannot read, to dense rows of ld elements (a multiple of 8).
+// A tensor that TMA cannot read, to dense rows of ld elements (a multiple of 8,
+// what is past a row as zeros): eight of a row a thread, put together from the
+// two aligned pieces that hold them.
 __global__ void __launch_bounds__(256)
     dense_kernel(const __nv_bfloat16* src, int64_t matrices, int64_t rows, int64_t cols, int64_t ld_src,
                  int64_t stride_src, __nv_bfloat16* dst, int64_t ld) {
     grid_dependency_wait();
     allow_dependent_launch();
-    for (int64_t r = blockIdx.x; r < matrices * rows; r += gridDim.x) {
-        const int64_t e = r / rows;
-        const __nv_bfloat16* const from = src + e * stride_src + (r - e * rows) * ld_src;
-        for (int64_t c = threadIdx.x; c < cols; c += 256) dst[r * ld + c] = from[c];
+    const int64_t groups = ld / 8;
+    for (int64_t u = blockIdx.x * int64_t(256) + threadIdx.x; u < matrices * rows * groups;
+         u += gridDim.x * int64_t(256)) {
+        const int64_t r = u / groups, c = (u - r * groups) * 8, e = r / rows;
+        Vec<__nv_bfloat16, false> v;
+        v.load(src + e * stride_src + (r - e * rows) * ld_src + c, static_cast<int>(cols - c));
+        *reinterpret_cast<uint4*>(dst + r * ld + c) = v.raw;
     }
 }
 
@@ -1229,10 +1236,10 @@ struct Workspace {
 cudaError_t settle(Operand& o, char* base, cudaStream_t s) {
     if (!o.copied) return cudaSuccess;
     auto* const to = reinterpret_cast<__nv_bfloat16*>(base + o.copy);
-    const int64_t ld = ceil_div(o.cols, 8) * 8, rows = o.matrices * o.rows;
-    const cudaError_t e = launch_kernel(dense_kernel, dim3(static_cast<unsigned>(rows < 152 * 8 ? rows : 152 * 8)),
-                                        dim3(256), 0, s, static_cast<const __nv_bfloat16*>(o.p), o.matrices,
-                                        o.rows, o.cols, o.ld, o.stride, to, ld);
+    const int64_t ld = ceil_div(o.cols, 8) * 8, blocks = ceil_div(o.matrices * o.rows * (ld / 8), 256);
+    const cudaError_t e =
+        launch_kernel(dense_kernel, dim3(static_cast<unsigned>(std::min(blocks, int64_t(152 * 16)))), dim3(256), 0, s,
+                      static_cast<const __nv_bfloat16*>(o.p), o.matrices, o.rows, o.cols, o.ld, o.stride, to, ld);
     o.p = to;
     o.ld = ld;
     o.stride = o.rows * ld;

@@ -169,14 +169,17 @@ int check_backward(const Err& err, const muon_gated_ffn_grad_args* a) {
 }
 
 int check_rotary_tensor(const Err& err, const char* name, const muon_rotary_tensor& t, int dtype,
-                        int64_t tokens) {
+                        int64_t batch, int64_t seq) {
     if (t.heads < 0 || t.heads > 65536) return err.bad(name, "has heads out of range");
-    if (t.heads == 0 || tokens == 0) return MUON_OK;
+    if (t.heads == 0 || batch == 0 || seq == 0) return MUON_OK;
     if (!t.x || !t.y) return err.bad(name, "is NULL");
     if (!aligned(t.x, dtype) || !aligned(t.y, dtype)) return err.bad(name, "is not aligned to its elements");
     if (t.x_batch < 0 || t.x_seq < 0 || t.x_head < 0 || t.y_batch < 0 || t.y_seq < 0 || t.y_head < 0)
         return err.bad(name, "has a negative stride");
-    if (t.x == t.y && (t.x_batch != t.y_batch || t.x_seq != t.y_seq || t.x_head != t.y_head))
+    if ((batch > 1 && t.y_batch == 0) || (seq > 1 && t.y_seq == 0) || (t.heads > 1 && t.y_head == 0))
+        return err.bad(name, "is written to places that share memory");
+    if (t.x == t.y && ((batch > 1 && t.x_batch != t.y_batch) || (seq > 1 && t.x_seq != t.y_seq) ||
+                       (t.heads > 1 && t.x_head != t.y_head)))
         return err.bad(name, "is written in place with other strides");
     return MUON_OK;
 }
@@ -425,8 +428,8 @@ MUON_API int muon_rotary(const muon_rotary_args* a, void* cuda_stream, char* err
         return err.bad("batch or seq out of range");
     if (!std::isfinite(a->scale)) return err.bad("scale is not finite");
     if (!a->turns) return err.bad("turns is NULL");
-    RETURN_IF(check_rotary_tensor(err, "q", a->q, a->x_dtype, a->batch * a->seq));
-    RETURN_IF(check_rotary_tensor(err, "k", a->k, a->x_dtype, a->batch * a->seq));
+    RETURN_IF(check_rotary_tensor(err, "q", a->q, a->x_dtype, a->batch, a->seq));
+    RETURN_IF(check_rotary_tensor(err, "k", a->k, a->x_dtype, a->batch, a->seq));
     if (a->positions) {
         if (a->stride_positions < 0) return err.bad("positions has a negative stride");
         if (reinterpret_cast<uintptr_t>(a->positions) % (a->positions_64 ? 8 : 4) != 0)

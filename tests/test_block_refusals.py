@@ -118,7 +118,8 @@ def rotary(L, q=None, k=None, **kw):
     (dict(q=dict(x=None)), "q is NULL"), (dict(k=dict(y=None)), "k is NULL"), (dict(q=dict(x=P + 1)), "aligned"),
     (dict(k=dict(heads=-1)), "heads"), (dict(q=dict(heads=65537)), "heads"),
     (dict(q=dict(heads=65536), head=4096), "heads"),
-    (dict(q=dict(x_seq=-16)), "negative"), (dict(k=dict(y_head=32)), "in place")])
+    (dict(q=dict(x_seq=-16)), "negative"), (dict(q=dict(y_head=0)), "share memory"),
+    (dict(k=dict(y_seq=0)), "share memory"), (dict(k=dict(y_batch=0)), "share memory"), (dict(k=dict(y_head=32)), "in place")])
 def test_rotary_refuses(L, kw, word):
     rc, msg = rotary(L, **kw)
     assert rc == L.MUON_ERR_INVALID_ARG and word in msg, msg
