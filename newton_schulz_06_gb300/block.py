@@ -25,8 +25,9 @@ import torch
 
 from . import _lib
 from ._lib import MuonError
-from .ops import (_BF16, _ERR_LEN, _F32, _I32, _call, _call_ws, _dtype, _fn, _gradient, _local,
+from .ops import (_BF16, _ERR_LEN, _I32, _call, _call_ws, _dtype, _fn, _gradient, _local,
                   _matrix, _need, _output, _vector, Checkpoint8, weight_grad)
+from .muon import _DT
 
 _ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 _LAYOUTS = {"half": 0, "interleaved": 1}
@@ -40,11 +41,11 @@ _NO_TENSOR = (0, 0, 0, 0, 0, 0, 0, 0, 0)
 
 # ------------------------------------------------------- gated feed-forward
 
-def _bf16(name: str, t: torch.Tensor, index: int, rows: int, cols: int) -> int:
-    """Checks a bf16 matrix of rows x cols; its leading dimension."""
+def _rows(name: str, t: torch.Tensor, index: int = -1, rows: int = -1, cols: int = -1):
+    """_matrix of a bf16 tensor."""
     if t.dtype != _BF16:
         raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
-    return _matrix(name, t, index, rows, cols)[2]
+    return _matrix(name, t, index, rows, cols)
 
 
 def _experts(offsets: Optional[torch.Tensor], index: int) -> Tuple[int, int]:
@@ -56,27 +57,34 @@ def _experts(offsets: Optional[torch.Tensor], index: int) -> Tuple[int, int]:
     return experts, _vector("offsets", offsets, index, experts + 1, _I32)
 
 
+def _weight(name: str, w: torch.Tensor, shape: tuple, index: int):
+    """Checks a bf16 matrix, or experts x a matrix: (leading dimension, stride)."""
+    if w.dtype != _BF16:
+        raise ValueError(f"{name} must be bfloat16, got {w.dtype}")
+    if w.shape != shape or w.get_device() != index:
+        raise ValueError(f"{name} must be {shape} on cuda:{index}, got {tuple(w.shape)} on {w.device}")
+    stride = w.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must be row-major (stride(-1) == 1)")
+    return stride[-2], stride[0] if len(shape) == 3 else 0
+
+
 def _weights(index: int, experts: int, hidden: int, gate, up, down):
-    """Checks the three matrices (or experts x matrices); (inner, their leading
-    dimensions, their strides)."""
-    for name, w in (("w_gate", gate), ("w_up", up), ("w_down", down)):
-        if w.dtype != _BF16:
-            raise ValueError(f"{name} must be bfloat16, got {w.dtype}")
+    """Checks the three matrices (or experts x matrices); (inner, the shapes of
+    gate and up and of down, their leading dimensions, their strides)."""
     shape = gate.shape
     if len(shape) != (3 if experts else 2):
         raise ValueError(f"w_gate must be {'experts x inner x hidden' if experts else 'inner x hidden'}, "
                          f"got {tuple(shape)}")
     inner = shape[-2]
-    one, two = (inner, hidden), (hidden, inner)
     if experts:
-        one, two = (experts, *one), (experts, *two)
-    lds = []
-    strides = []
-    for name, w, s in (("w_gate", gate, one), ("w_up", up, one), ("w_down", down, two)):
-        ld, stride = _gradient(name, w, s, index)
-        lds.append(ld)
-        strides.append(stride)
-    return inner, lds, strides
+        one, two = (experts, inner, hidden), (experts, hidden, inner)
+    else:
+        one, two = (inner, hidden), (hidden, inner)
+    ld_gate, stride_gate = _weight("w_gate", gate, one, index)
+    ld_up, stride_up = _weight("w_up", up, one, index)
+    ld_down, stride_down = _weight("w_down", down, two, index)
+    return inner, one, two, (ld_gate, ld_up, ld_down), (stride_gate, stride_up, stride_down)
 
 
 def _activation(name: str) -> int:
@@ -101,20 +109,19 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     bf16, which is half of the error that the gradients then have.  out may be x.
     The last bits of a row may depend on the number of rows beside it (long sums
     of few rows are added up in parts)."""
-    rows, hidden, ld_x, index = _matrix("x", x)
-    _need(x.dtype == _BF16, f"x must be bfloat16, got {x.dtype}")
+    rows, hidden, ld_x, index = _rows("x", x)
     act = _activation(activation)
     experts, offsets_at = _experts(offsets, index)
-    inner, lds, strides = _weights(index, experts, hidden, w_gate, w_up, w_down)
+    inner, _, _, lds, strides = _weights(index, experts, hidden, w_gate, w_up, w_down)
     y, ld_y = _output("out", out, x, rows, hidden)
-    saved, gate_at, up_at = None, 0, 0
+    saved, gate_at, up_at, dev = None, 0, 0, x.device
     if keep:
-        gate = torch.empty((rows, inner), dtype=_BF16, device=x.device)
-        up = torch.empty((rows, inner), dtype=_BF16, device=x.device)
+        gate = torch.empty((rows, inner), dtype=_BF16, device=dev)
+        up = torch.empty((rows, inner), dtype=_BF16, device=dev)
         saved, gate_at, up_at = (gate, up), gate.data_ptr(), up.data_ptr()
     _call_ws(index, "muon_gated_ffn", "muon_gated_ffn_workspace", _ffn_args(
         x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), y.data_ptr(), gate_at, up_at,
-        offsets_at, rows, hidden, inner, experts or 1, ld_x, *lds, ld_y, inner, *strides, act), x.device)
+        offsets_at, rows, hidden, inner, experts or 1, ld_x, *lds, ld_y, inner, *strides, act), dev)
     return y, saved
 
 
@@ -133,15 +140,15 @@ def gated_ffn_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint8, Non
     weights' shapes, e.g. those that a Muon set steps with (new ones of dtype
     otherwise); with accumulate the gradients are added to them.  Experts
     without rows get zeros.  out: receives dx (it may not be dy)."""
-    rows, hidden, ld_dy, index = _matrix("dy", dy)
-    _need(dy.dtype == _BF16, f"dy must be bfloat16, got {dy.dtype}")
+    rows, hidden, ld_dy, index = _rows("dy", dy)
     dev = dy.device
     act = _activation(activation)
     experts, offsets_at = _experts(offsets, index)
-    inner, lds, strides = _weights(index, experts, hidden, w_gate, w_up, w_down)
+    inner, one, two, lds, strides = _weights(index, experts, hidden, w_gate, w_up, w_down)
     gate, up = saved
-    ld_kept = _bf16("gate", gate, index, rows, inner)
-    _need(_bf16("up", up, index, rows, inner) == ld_kept or rows <= 1, "gate and up differ in their strides")
+    ld_kept = _rows("gate", gate, index, rows, inner)[2]
+    if _rows("up", up, index, rows, inner)[2] != ld_kept and rows > 1:
+        raise ValueError("gate and up differ in their strides")
     checkpoint = isinstance(x, Checkpoint8)
     ld_x = x_at = 0
     if checkpoint:
@@ -150,47 +157,49 @@ def gated_ffn_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint8, Non
     else:
         _need(weight is None and bias is None, "weight and bias go with a checkpoint of x")
         if x is not None:
-            ld_x, x_at = _bf16("x", x, index, rows, hidden), x.data_ptr()
+            ld_x, x_at = _rows("x", x, index, rows, hidden)[2], x.data_ptr()
     dx, ld_dx = _output("out", out, dy, rows, hidden)
-    if out is not None and rows and (dx.data_ptr() == dy.data_ptr() or dx.data_ptr() == x_at):
+    dx_at, dy_at = dx.data_ptr(), dy.data_ptr()
+    if out is not None and rows and (dx_at == dy_at or dx_at == x_at):
         raise ValueError("out may not be dy or x: they are read after it is written")
-    need_x = x is not None
     if grads is None:
         _need(not accumulate, "accumulate needs grads to add to")
-        grads = [torch.empty(w.shape, dtype=dtype, device=dev) if need_x or i == 2 else None
-                 for i, w in enumerate((w_gate, w_up, w_down))]
+        code = _DT.get(dtype)
+        _need(code is not None, f"dtype must be float32 or bfloat16, got {dtype}")
+        dg = du = None
+        if x is not None:
+            dg, du = torch.empty(one, dtype=dtype, device=dev), torch.empty(one, dtype=dtype, device=dev)
+        dd = torch.empty(two, dtype=dtype, device=dev)
+        ld_g, size = (hidden, hidden, inner), inner * hidden
+        stride_g = (size, size, size)
     else:
-        grads = list(grads)
-        _need(len(grads) == 3, "grads must be (dw_gate, dw_up, dw_down)")
-        if not need_x:
-            grads[:2] = None, None
-    lead = (experts,) if experts else ()
-    at, ld_g, stride_g, kind = [0, 0, 0], [0, 0, 0], [0, 0, 0], None
-    for i, (name, shape) in enumerate((("dw_gate", (inner, hidden)), ("dw_up", (inner, hidden)),
-                                       ("dw_down", (hidden, inner)))):
-        g = grads[i]
-        if g is None:
-            continue
-        ld_g[i], stride_g[i] = _gradient(name, g, (*lead, *shape), index)
-        _need(kind is None or g.dtype == kind, "grads differ in type")
-        kind = g.dtype
-        if not (checkpoint and i < 2):
-            at[i] = g.data_ptr()
-    made = [None, None]
-    made_at, ld_d = (0, 0), 0
+        dg, du, dd = grads
+        if x is None:
+            dg = du = None
+        kind = next((g.dtype for g in (dg, du, dd) if g is not None), _BF16)
+        code = _DT.get(kind)
+        _need(code is not None, f"grads must be float32 or bfloat16, got {kind}")
+        ld_g, stride_g = [0, 0, 0], [0, 0, 0]
+        for i, (name, g, shape) in enumerate((("dw_gate", dg, one), ("dw_up", du, one), ("dw_down", dd, two))):
+            if g is not None:
+                ld_g[i], stride_g[i] = _gradient(name, g, shape, index)
+                _need(g.dtype == kind, "grads differ in type")
+    dgate = dup = None
+    dgate_at = dup_at = ld_d = 0
     if checkpoint:
-        made = [torch.empty((rows, inner), dtype=_BF16, device=dev) for _ in range(2)]
-        made_at, ld_d = (made[0].data_ptr(), made[1].data_ptr()), inner
-    code = _lib.MUON_BF16 if kind is None else _dtype("grads", next(g for g in grads if g is not None))
+        dgate = torch.empty((rows, inner), dtype=_BF16, device=dev)
+        dup = torch.empty((rows, inner), dtype=_BF16, device=dev)
+        dgate_at, dup_at, ld_d = dgate.data_ptr(), dup.data_ptr(), inner
     _call_ws(index, "muon_gated_ffn_grad", "muon_gated_ffn_grad_workspace", _ffn_grad_args(
-        dy.data_ptr(), x_at, gate.data_ptr(), up.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-        w_down.data_ptr(), dx.data_ptr(), *at, *made_at, 0, offsets_at, rows, hidden, inner, experts or 1,
+        dy_at, x_at, gate.data_ptr(), up.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
+        dx_at, 0 if checkpoint or dg is None else dg.data_ptr(), 0 if checkpoint or du is None else du.data_ptr(),
+        0 if dd is None else dd.data_ptr(), dgate_at, dup_at, 0, offsets_at, rows, hidden, inner, experts or 1,
         ld_dy, ld_x, ld_kept, *lds, ld_dx, ld_d, *ld_g, *strides, *stride_g, act, code, bool(accumulate)), dev)
     if checkpoint:
-        for d, g in zip(made, grads):
+        for d, g in ((dgate, dg), (dup, du)):
             if g is not None:
                 weight_grad(d, x, weight=weight, bias=bias, offsets=offsets, add=g if accumulate else None, out=g)
-    return (dx, *grads)
+    return dx, dg, du, dd
 
 
 # --------------------------------------------------------- rotary positions
