@@ -41,31 +41,11 @@ struct RotaryLaunch {
     uint32_t tokens, tokens_block;        // tokens: batch * seq
     uint32_t head;
     Quotient seq, pairs;                  // pairs of a head that turn
-    Quotient per_head, per_token;         // units of a head (groups of W pairs, then of W other values), of a token
-    int32_t wide_pos, copy;               // positions are 64-bit; the other values are copied
+    Quotient per_head, per_token;         // units of a head (those that turn, then the rest), of a token
+    uint32_t turning, rest;               // how many of each
+    int32_t wide_pos;                     // positions are 64-bit
     float scale, sign;
     uint64_t turns[256];
-};
-
-// N neighbouring values as they are in memory, W of them an access.
-template <typename T, int W, int N>
-struct Group {
-    struct alignas(sizeof(T) * W) Raw {
-        T v[W];
-    };
-    Raw raw[N / W];
-    __device__ __forceinline__ void load(const T* p, int accesses) {
-#pragma unroll
-        for (int k = 0; k < N / W; ++k)
-            if (k < accesses) raw[k] = reinterpret_cast<const Raw*>(p)[k];
-    }
-    __device__ __forceinline__ void store(T* p, int accesses) const {
-#pragma unroll
-        for (int k = 0; k < N / W; ++k)
-            if (k < accesses) reinterpret_cast<Raw*>(p)[k] = raw[k];
-    }
-    __device__ __forceinline__ float get(int i) const { return to_f32(raw[i / W].v[i % W]); }
-    __device__ __forceinline__ void set(int i, float f) { from_f32(&raw[i / W].v[i % W], f); }
 };
 
 // a c + b s, rounded the same way in all kernels.
@@ -73,10 +53,11 @@ __device__ __forceinline__ float turned(float a, float c, float b, float s) {
     return __fmaf_rn(a, c, __fmul_rn(b, s));
 }
 
-// HALF: pair i is values i and i + pairs of a head; else 2 i and 2 i + 1.
-// W: values of a load or store.  A unit of a thread's work is W pairs of HALF,
-// or W values (two at least).
-template <typename T, int W, bool HALF>
+// HALF: pair i is values i and i + pairs of a head; else 2 i and 2 i + 1.  A
+// thread's unit is 16 bytes of values, with HALF of both of their halves; of
+// a head's rest with HALF as much, from its two halves.  AL: all of these lie on
+// 16 bytes; else they are put together from aligned pieces, and across lanes.
+template <typename T, bool HALF, bool AL>
 __global__ void __launch_bounds__(R_THREADS) rotary_kernel(const __grid_constant__ RotaryLaunch p) {
     extern __shared__ float trig[];       // cosines, then sines, of tokens_block x pairs
     grid_dependency_wait();
@@ -102,96 +83,89 @@ __global__ void __launch_bounds__(R_THREADS) rotary_kernel(const __grid_constant
     }
     __syncthreads();
     const uint32_t q_heads = static_cast<uint32_t>(p.t[0].heads);
-    constexpr int N = HALF || W > 1 ? W : 2;              // values of an operand
-    constexpr uint32_t PW = HALF ? N : N / 2;             // pairs of a unit
-    const uint32_t turning = p.pairs.d / PW;              // units that turn
-    for (uint32_t u = threadIdx.x; u < tokens * p.per_token.d; u += R_THREADS) {
-        const uint32_t t = p.per_token.of(u), in = u - t * p.per_token.d;
+    constexpr uint32_t VE = 16 / sizeof(T);
+    const uint32_t total = tokens * p.per_token.d;
+    // (whole warps: they exchange what lies off 16 bytes)
+    for (uint32_t u = threadIdx.x; u - threadIdx.x % 32 < total; u += R_THREADS) {
+        const bool live = u < total;
+        const uint32_t t = live ? p.per_token.of(u) : 0, in = live ? u - t * p.per_token.d : 0;
         uint32_t h = p.per_head.of(in);
         const uint32_t unit = in - h * p.per_head.d;
         const uint32_t b = p.seq.of(first + t), s = first + t - b * p.seq.d;
         const int which = h >= q_heads;
         if (which) h -= q_heads;
         const muon_rotary_tensor& x = p.t[which];
-        const bool turns = unit < turning;
-        // where this unit's values are: those that turn and those that do not
-        // are loaded and stored by the same instructions (a branch each took
-        // 8191 tokens of 65 heads, 64 of 192 values, from 72 to 86 us)
-        const uint32_t rest = 2 * p.pairs.d + (unit - turning) * (HALF ? 2 * W : N);
-        const uint32_t at = turns ? unit * N : rest, at2 = turns ? p.pairs.d + unit * N : rest + W;
-        const bool second = HALF && (turns || at2 < p.head);
-        const int64_t in_x = b * x.x_batch + s * x.x_seq + h * x.x_head;
-        const int64_t in_y = b * x.y_batch + s * x.y_seq + h * x.y_head;
-        const T* const from = static_cast<const T*>(x.x) + in_x;
-        T* const to = static_cast<T*>(x.y) + in_y;
-        // (one value at a time, the last of an odd rest is alone)
-        const int accesses = N > W && at + 1 == p.head ? 1 : N / W;
-        Group<T, W, N> v, w;
-        v.load(from + at, accesses);
-        if (second) w.load(from + at2, 1);
+        const bool turns = unit < p.turning;
+        // Where this unit's values are, and how many are left there: those that
+        // turn and those that do not are loaded and stored by the same
+        // instructions (a branch each took 8191 tokens of 65 heads, 64 of 192
+        // values, from 72 to 86 us).
+        const uint32_t k = turns ? unit : unit - p.turning;
+        const uint32_t from1 = turns ? 0 : 2 * p.pairs.d, from2 = turns ? p.pairs.d : from1 + VE * p.rest;
+        const uint32_t to1 = turns ? (HALF ? 1 : 2) * p.pairs.d : HALF ? min(p.head, from2) : p.head;
+        const uint32_t to2 = turns ? 2 * p.pairs.d : p.head;
+        const int left1 = live ? int(to1) - int(from1 + VE * k) : 0;
+        const int left2 = live && HALF ? int(to2) - int(from2 + VE * k) : 0;
+        const T* const from = static_cast<const T*>(x.x) + (b * x.x_batch + s * x.x_seq + h * x.x_head + VE * k);
+        T* const to = static_cast<T*>(x.y) + (b * x.y_batch + s * x.y_seq + h * x.y_head + VE * k);
+        Vec<T, AL> v, w;
+        v.load(from + from1, left1);
+        if (HALF) w.load(from + from2, left2);
         if (turns) {
-            const float* const c = trig + t * p.pairs.d + unit * PW;
-            const float* const n = sine + t * p.pairs.d + unit * PW;
+            float2 f[VE / 2], g[VE / 2];
+            v.get(f);
             if constexpr (HALF) {
+                const float* const c = trig + t * p.pairs.d + VE * k;
+                const float* const n = sine + t * p.pairs.d + VE * k;
+                w.get(g);
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float f = v.get(i), g = w.get(i);
-                    v.set(i, turned(f, c[i], g, -n[i]));
-                    w.set(i, turned(g, c[i], f, n[i]));
+                for (uint32_t i = 0; i < VE / 2; ++i) {
+                    const float2 a = f[i], d = g[i];
+                    f[i] = make_float2(turned(a.x, c[2 * i], d.x, -n[2 * i]),
+                                       turned(a.y, c[2 * i + 1], d.y, -n[2 * i + 1]));
+                    g[i] = make_float2(turned(d.x, c[2 * i], a.x, n[2 * i]),
+                                       turned(d.y, c[2 * i + 1], a.y, n[2 * i + 1]));
                 }
+                w.set(g);
             } else {
+                const float* const c = trig + t * p.pairs.d + VE / 2 * k;
+                const float* const n = sine + t * p.pairs.d + VE / 2 * k;
 #pragma unroll
-                for (int i = 0; i < N; i += 2) {
-                    const float f = v.get(i), g = v.get(i + 1);
-                    v.set(i, turned(f, c[i / 2], g, -n[i / 2]));
-                    v.set(i + 1, turned(g, c[i / 2], f, n[i / 2]));
-                }
+                for (uint32_t i = 0; i < VE / 2; ++i)
+                    f[i] = make_float2(turned(f[i].x, c[i], f[i].y, -n[i]), turned(f[i].y, c[i], f[i].x, n[i]));
             }
+            v.set(f);
         }
-        v.store(to + at, accesses);
-        if (second) w.store(to + at2, 1);
+        v.store(to + from1, left1, k == 0);
+        if (HALF) w.store(to + from2, left2, k == 0);
     }
 }
 
-// The widest group, of up to 16 bytes, in which all rows, halves and rests
-// begin and end.
+// Whether all rows, halves and rests begin and end on 16 bytes.
 template <typename T>
-int group_width(const muon_rotary_args& a, bool copy) {
-    int w = 16 / sizeof(T);
-    auto fits = [&](int64_t elements) {
-        while (w > 1 && elements % w) w >>= 1;
-    };
-    fits(a.layout == MUON_ROTARY_HALF ? a.pairs : 2 * a.pairs);
-    if (copy) fits(a.head);
-    const muon_rotary_tensor* const t[2] = {&a.q, &a.k};
-    for (int i = 0; i < 2; ++i) {
-        if (!t[i]->heads) continue;
-        const void* const ptr[2] = {t[i]->x, t[i]->y};
-        for (const void* q : ptr)
-            while (w > 1 && reinterpret_cast<uintptr_t>(q) % (w * sizeof(T))) w >>= 1;
-        if (a.batch > 1) fits(t[i]->x_batch), fits(t[i]->y_batch);
-        if (a.seq > 1) fits(t[i]->x_seq), fits(t[i]->y_seq);
-        if (t[i]->heads > 1) fits(t[i]->x_head), fits(t[i]->y_head);
+bool on_16(const muon_rotary_args& a, bool copy) {
+    constexpr int64_t VE = 16 / sizeof(T);
+    bool ok = (a.layout == MUON_ROTARY_HALF ? a.pairs : 2 * a.pairs) % VE == 0 && (!copy || a.head % VE == 0);
+    const muon_rotary_tensor* const tensors[2] = {&a.q, &a.k};
+    for (const muon_rotary_tensor* t : tensors) {
+        if (!t->heads) continue;
+        ok = ok && reinterpret_cast<uintptr_t>(t->x) % 16 == 0 && reinterpret_cast<uintptr_t>(t->y) % 16 == 0 &&
+             (a.batch <= 1 || (t->x_batch % VE == 0 && t->y_batch % VE == 0)) &&
+             (a.seq <= 1 || (t->x_seq % VE == 0 && t->y_seq % VE == 0)) &&
+             (t->heads <= 1 || (t->x_head % VE == 0 && t->y_head % VE == 0));
     }
-    return w;
-}
-
-template <typename T, int W>
-cudaError_t launch(const RotaryLaunch& p, bool half, cudaStream_t s) {
-    const int64_t blocks = ceil_div(p.tokens, p.tokens_block);
-    void (*const kernel)(RotaryLaunch) = half ? rotary_kernel<T, W, true> : rotary_kernel<T, W, false>;
-    return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(R_THREADS),
-                         size_t(2) * p.tokens_block * p.pairs.d * sizeof(float), s, p);
+    return ok;
 }
 
 template <typename T>
 cudaError_t launch(RotaryLaunch p, const muon_rotary_args& a, cudaStream_t s) {
+    constexpr int64_t VE = 16 / sizeof(T);
     const bool half = a.layout == MUON_ROTARY_HALF;
-    const int w = group_width<T>(a, p.copy);
-    const int64_t turning = half ? a.pairs / w : a.pairs / (w > 1 ? w / 2 : 1);
-    // a unit of the rest is as many values as one of those that turn
-    const int64_t values = half ? 2 * w : w > 1 ? w : 2;
-    const int64_t per_head = turning + (p.copy ? ceil_div(a.head - 2 * a.pairs, values) : 0);
+    const bool rest = a.head > 2 * a.pairs;
+    const bool copy = rest && ((a.q.heads && a.q.x != a.q.y) || (a.k.heads && a.k.x != a.k.y));
+    p.turning = static_cast<uint32_t>(ceil_div((half ? 1 : 2) * a.pairs, VE));
+    p.rest = copy ? static_cast<uint32_t>(ceil_div(a.head - 2 * a.pairs, half ? 2 * VE : VE)) : 0;
+    const int64_t per_head = p.turning + p.rest;
     // as many tokens a block as give every thread four units, and no more than
     // leave every SM a block (with eight tokens of 65 heads of 192 a block, so
     // that every thread made a cosine, 8191 tokens took 108 us)
@@ -204,11 +178,12 @@ cudaError_t launch(RotaryLaunch p, const muon_rotary_args& a, cudaStream_t s) {
     // (the units of a block are counted in 32 bits)
     if (t > (int64_t(1) << 28) / units) t = (int64_t(1) << 28) / units;
     p.tokens_block = static_cast<uint32_t>(t < 1 ? 1 : t);
-    if constexpr (sizeof(T) == 2)
-        if (w == 8) return launch<T, 8>(p, half, s);
-    if (w == 4) return launch<T, 4>(p, half, s);
-    if (w == 2) return launch<T, 2>(p, half, s);
-    return launch<T, 1>(p, half, s);
+    void (*const kernel)(RotaryLaunch) =
+        on_16<T>(a, copy) ? (half ? rotary_kernel<T, true, true> : rotary_kernel<T, false, true>)
+                          : (half ? rotary_kernel<T, true, false> : rotary_kernel<T, false, false>);
+    // (a short last unit reads up to seven cosines and sines too many)
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(ceil_div(p.tokens, p.tokens_block))), dim3(R_THREADS),
+                         (size_t(2) * p.tokens_block * p.pairs.d + 8) * sizeof(float), s, p);
 }
 
 }  // namespace
@@ -227,8 +202,6 @@ cudaError_t launch_rotary(const muon_rotary_args& a, cudaStream_t s) {
     p.pairs.set(a.pairs);
     p.scale = a.scale;
     p.sign = a.inverse ? -1.f : 1.f;
-    const bool rest = a.head > 2 * a.pairs;
-    p.copy = rest && ((a.q.heads && a.q.x != a.q.y) || (a.k.heads && a.k.x != a.k.y));
     for (int64_t i = 0; i < a.pairs; ++i) p.turns[i] = a.turns[i];
     return a.x_dtype == MUON_F32 ? launch<float>(p, a, s) : launch<__nv_bfloat16>(p, a, s);
 }
