@@ -9,7 +9,9 @@
 // radians at a million.  No table of cosines is read: a block makes them for
 // its tokens once, in shared memory, and all heads use them.
 //
-// What bounds it is memory: each value is read and written once.
+// What bounds it is memory: each value is read and written once (16384 tokens
+// of 36 heads of 128 in bf16: 49 us, 6.1 TB/s; 8191 of 65 heads, of which 64 of 192
+// values turn: 71 us, 5.8 TB/s; heads off 16 bytes take two to three times as long).
 #include "ops_internal.h"
 
 namespace muon {
