@@ -106,7 +106,8 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     activation: "silu", "gelu" (by erf) or "gelu_tanh".
     Returns (y, saved): saved is (g, u), both rows x inner, for
     :func:`gated_ffn_backward`, or None without keep.  They are rounded to
-    bf16, which is half of the error that the gradients then have.  out may be x.
+    bf16, which is half of the squared error that the gradients then have.  out
+    may be x.
     The last bits of a row may depend on the number of rows beside it (long sums
     of few rows are added up in parts)."""
     rows, hidden, ld_x, index = _rows("x", x)

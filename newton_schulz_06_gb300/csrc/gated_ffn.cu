@@ -64,7 +64,7 @@ constexpr int F_COLS16 = 32;                       // and in bf16
 constexpr int F_ROW16 = 136;
 constexpr int F_TURN_BYTES = F_COLS16 * F_ROW16 * 2;
 static_assert(F_TURN_BYTES >= F_COLS * F_ROW * 4 && F_TURN_BYTES % 16 == 0, "a team's buffer");
-constexpr int F_KEPT_BYTES = 4 * 128 * 16;         // a team's g and u of 16 columns (DHIDDEN)
+constexpr int F_KEPT_BYTES = 2 * 4 * 128 * 16;     // a team's g and u of 16 columns, twice (DHIDDEN)
 constexpr int F_EPI_WARPS = 8;
 constexpr int F_PATCH_WARP = 2 + F_EPI_WARPS;
 constexpr int F_LOAD_B_WARP = F_PATCH_WARP + 1;
@@ -927,7 +927,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 acc ^= 1;
                 x = y;
             }
-            if (!ok && any && lane == 0) {
+            // (the lane that issued the products: elections of one mask agree)
+            if (!ok && any && elected()) {
                 commit_pair_local(smem_u32(drain_bar));
                 wait_quiet(smem_u32(drain_bar), 0, limit);
             }
@@ -991,17 +992,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         // what DHIDDEN reads beside the sums comes 16 columns ahead of its use
         // by asynchronous copies (loads to registers made what the thread then
         // reads from shared memory wait for them too: 1950 cycles for 16
-        // columns, not 1150)
+        // columns, not 1150), to the place that was not read last
         constexpr int UNITS = Units<OP>::N;
         uint4* const kept = reinterpret_cast<uint4*>(smem + S::KEPT + team * F_KEPT_BYTES) + tid;
+        int place = 0;
         auto fetch = [&](const Item& x, int c) {
             const int row0 = x.n0 + c * F_COLS + tid / 16, m = x.m0 + static_cast<int>(rank) * 128 + tid % 16 * 8;
             const int64_t at = row0 * p.ld_kept + m;
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
                 if (p.vec && row0 + 8 * i < x.n_end && m + 8 <= p.m[0]) {
-                    copy16(kept + 256 * i, static_cast<const __nv_bfloat16*>(p.gate) + at + 8 * i * p.ld_kept);
-                    copy16(kept + 256 * i + 128, static_cast<const __nv_bfloat16*>(p.up) + at + 8 * i * p.ld_kept);
+                    copy16(kept + 512 * place + 256 * i, static_cast<const __nv_bfloat16*>(p.gate) + at + 8 * i * p.ld_kept);
+                    copy16(kept + 512 * place + 256 * i + 128, static_cast<const __nv_bfloat16*>(p.up) + at + 8 * i * p.ld_kept);
                 }
             }
         };
@@ -1104,11 +1106,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                             copies_done();
 #pragma unroll
                             for (int i = 0; i < UNITS; ++i) {
-                                g8[i] = kept[256 * i];
-                                u8[i] = kept[256 * i + 128];
+                                g8[i] = kept[512 * place + 256 * i];
+                                u8[i] = kept[512 * place + 256 * i + 128];
                             }
+                            place ^= 1;
+                            if (c < last) fetch(x, c + 2);
                         }
-                        if (OP == DHIDDEN && c < last) fetch(x, c + 2);
                         finish_turned<OP, true>(p, x, turn, n0, m0, m_end, tid, g8, u8);
                     } else {
                         uint4 g8[UNITS], u8[UNITS];
@@ -1119,8 +1122,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                                 const int row = n0 + tid / 16 + 8 * i, m = m0 + tid % 16 * 8;
                                 load_kept(p, row, m, row < x.n_end ? m_end - m : 0, g8[i], u8[i]);
                             }
+                            place ^= 1;
+                            if (c < last) fetch(x, c + 2);
                         }
-                        if (OP == DHIDDEN && c < last) fetch(x, c + 2);
                         finish_turned<OP, false>(p, x, turn, n0, m0, m_end, tid, g8, u8);
                     }
                 }
