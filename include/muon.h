@@ -560,7 +560,8 @@ MUON_API int muon_route_grad(const muon_route_grad_args* args, void* cuda_stream
  * or gate or up.  The tensor cores cut their running sums off at the last place
  * (16384 terms of one sign lose 4e-5 of their sum); long sums of few rows are
  * added up in parts, so that a row's last bits may depend on the number of rows.
- * A stride of matrices may be 0 (one for all).  0 <= rows < 2^31 - 256,
+ * A stride of matrices may be 0 (one for all).  Operands whose rows do not all
+ * start on 16 bytes are copied to the workspace first.  0 <= rows < 2^31 - 256,
  * 1 <= hidden, inner <= 262144, 1 <= experts <= 1024. */
 #define MUON_ACT_SILU 0
 #define MUON_ACT_GELU 1

@@ -693,6 +693,44 @@ def test_run_of_a_block(ns):
     ns.ops_sync()
 
 
+def test_two_calls_at_once(ns):
+    """Calls on two streams and from two threads have workspaces of their own."""
+    import threading
+    w = weights(150, 256, 512)
+    we, offsets = weights(153, 256, 96, 5), bounds_of([100, 0, 300, 7, 93])
+    x, dy = rand(156, 500, 256, dtype=BF), rand(157, 500, 256, dtype=BF)
+
+    def dense():
+        y, s = ns.gated_ffn(x, *w)
+        return y, *ns.gated_ffn_backward(dy, x, s, *w)
+
+    def experts():
+        y, s = ns.gated_ffn(x, *we, offsets=offsets)
+        return y, *ns.gated_ffn_backward(dy, x, s, *we, offsets=offsets)
+
+    want = dense(), experts()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[], []]
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(20):
+                got[i].append((dense, experts)[i]())
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 20
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))
+    ns.ops_sync()
+
+
 def test_example_block(ns):
     """The example's block: its gradients are those of the same block with
     autograd in 64 bits, within what bf16 and 8-bit activations cost."""
