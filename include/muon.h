@@ -558,7 +558,7 @@ MUON_API int muon_route_grad(const muon_route_grad_args* args, void* cuda_stream
  * that one); rows of no expert are not written.
  * offsets = NULL: experts = 1, all rows.  y may be x, and must not overlap a weight
  * or gate or up.  The tensor cores cut their running sums off at the last place
- * (16384 terms of one sign lose 4e-5 of their sum); long sums of few rows are
+ * (16384 terms of one sign lose 9e-5 of their sum at most); long sums of few rows are
  * added up in parts, so that a row's last bits may depend on the number of rows.
  * A stride of matrices may be 0 (one for all).  Operands whose rows do not all
  * start on 16 bytes are copied to the workspace first.  0 <= rows < 2^31 - 256,
@@ -595,8 +595,10 @@ MUON_API int muon_gated_ffn(const muon_gated_ffn_args* args, void* workspace, si
  * checkpoint of x.  The weight gradients are g_dtype, dense matrices laid out
  * as their weights (leading dimensions ld_dgate ..., strides stride_dgate ...);
  * with accumulate they are added to what is there, in fp32, and rounded once.
- * An expert without rows has zero gradients.  dx may be dy only without
- * dw_down, and x only without dw_gate and dw_up.  offsets as above. */
+ * Their sums over tokens are added up to nearest every 8192 tokens (bf16) or
+ * 4096 (fp32) at most.  An expert without rows has zero gradients.  dx may be
+ * dy only without dw_down, and x only without dw_gate and dw_up.  offsets as
+ * above. */
 typedef struct {
     const void*    dy;
     const void*    x;

@@ -74,6 +74,17 @@ constexpr int F_ITEMS = 4;                         // tiles found ahead
 constexpr int F_TMEM_COLS = 512;
 constexpr int F_PAIRS = 76;                        // a pair per two of the 152 SMs
 constexpr int F_BAND = 8;
+// DW's sums are as long as an expert has tokens, and the tensor cores cut a
+// running sum off at its last place, so that sums of one sign shrink, by 7.6e-8 a
+// product of 16 tokens (200003 of them in one sum lose 1.14e-3).  Two cuts of a
+// whole place each are the most, 2^-23 of a sum that is on average 0.375 of its
+// end's place: 9e-8 a product.  After this many steps of four products a tile's
+// sums are added up to nearest, so that at most 4.6e-5 is lost of a bf16 result,
+// a fortieth of its own rounding, and 2.3e-5 of an fp32 one, about what the
+// rounding of dg, du and h leaves in a sum of 4096.  Whole gradient: 65536
+// tokens of 4096 x 4096, bf16 8040 -> 8280 us, fp32 8370 -> 8680; 4097 of 7168 x
+// 2048, fp32 441 -> 462, and 477 with the sums so far fetched only when added.
+constexpr int F_CHUNK_BF16 = 128, F_CHUNK_F32 = 64;
 
 __device__ int g_ffn_err;
 
@@ -121,6 +132,8 @@ struct FfnLaunch {
     int32_t products;        // DW: which of them, as bits
     int32_t tile_n;          // rows of N a tile, a multiple of 32
     int32_t splits;          // parts of the sums that tiles of their own take
+    int32_t chunk;           // DW: steps that one accumulator sums
+    float4* held;            // a tile's sums while its next chunk runs
     float* part;             // splits > 1: their sums, split by split,
     int64_t part_stride;
     int64_t part_ld[2];      // in rows of these lengths (by m's extent; UP: g, then u),
@@ -163,7 +176,9 @@ struct alignas(16) Item {
     int32_t s0, split;       // from this one of the whole sum on; which part of it that is
     int32_t t0;              // DW: the first token
     int32_t tail;            // DW: tokens of the last step, if not 64
+    int32_t chunk;           // DW: which end of a long sum this is (FIRST, LAST)
 };
+constexpr int FIRST = 1, LAST = 2;
 static_assert(F_ITEMS * sizeof(Item) <= 256, "tiles handed out");
 
 // The tiles' places.
@@ -206,6 +221,7 @@ struct Tiles {
         Item x;
         x.tail = 0;
         x.j = 0;
+        x.chunk = FIRST | LAST;
         x.split = p.splits > 1 ? whole.of(it) : 0;
         it -= x.split * whole.d;
         int32_t in, tn, size, end, all;
@@ -632,6 +648,39 @@ __device__ __forceinline__ void store_part(const FfnLaunch& p, const Item& x, co
     }
 }
 
+// DW's sums of the chunks before, 16 columns of them, of which a thread reads
+// back what it has written: asked for 16 columns ahead of their use.
+struct Held {
+    float4 f[Units<DW>::N][2];
+    static __device__ __forceinline__ float4* at(const FfnLaunch& p, int c, int i, int tid) {
+        return p.held + ((int64_t(blockIdx.x) * (256 / F_COLS) + c) * Units<DW>::N + i) * 256 + tid;
+    }
+    __device__ __forceinline__ void fetch(const FfnLaunch& p, int c, int tid) {
+#pragma unroll
+        for (int i = 0; i < Units<DW>::N; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) f[i][h] = at(p, c, i, tid)[128 * h];
+    }
+    // This chunk's added to them: to memory, or, of the last, to their places.
+    __device__ __forceinline__ void add(const FfnLaunch& p, const Item& x, float* turn, int c, int tid) const {
+        constexpr int GROUPS = Units<DW>::GROUPS;
+#pragma unroll
+        for (int i = 0; i < Units<DW>::N; ++i) {
+            float* const mine = turn + (tid + 128 * i) / GROUPS * F_ROW + tid % GROUPS * 8;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 v = *reinterpret_cast<const float4*>(mine + 4 * h);
+                if (!(x.chunk & FIRST)) {
+                    const float4 g = f[i][h];
+                    v = make_float4(v.x + g.x, v.y + g.y, v.z + g.z, v.w + g.w);
+                }
+                if (x.chunk & LAST) *reinterpret_cast<float4*>(mine + 4 * h) = v;
+                else at(p, c, i, tid)[128 * h] = v;
+            }
+        }
+    }
+};
+
 // The loads of one operand: a thread of its own each, because issuing them
 // costs a thread about 100 cycles a box, and products wait for nothing else
 // where the sums are long (8192 tokens of 4096 x 11008 and all four boxes of a
@@ -938,11 +987,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         if (lane == 0) {
             const Tiles<OP> tiles(p, table);
             Item* const items = reinterpret_cast<Item*>(smem + S::ITEMS);
-            int32_t it = pair;
-            for (uint32_t n = 0;; ++n, it += npairs) {
-                Item x{};
-                x.e = -1;
-                if (it < tiles.total) x = tiles.at(it);
+            int32_t it = pair, left = 0, tail = 0;
+            Item x{};
+            for (uint32_t n = 0;; ++n) {
+                // (a tile's chunks follow one another, of about one length)
+                if (left == 0) {
+                    x.e = -1;
+                    if (it < tiles.total) x = tiles.at(it);
+                    it += npairs;
+                    left = x.e < 0 ? 0 : x.steps;
+                    tail = x.tail;
+                    x.chunk = FIRST;
+                } else {
+                    x.t0 += x.steps * F_K;
+                    x.chunk = 0;
+                }
+                if (x.e >= 0) {
+                    x.steps = left;
+                    if (OP == DW && left > p.chunk) {
+                        const int32_t chunks = (left + p.chunk - 1) / p.chunk;
+                        x.steps = (left + chunks - 1) / chunks;
+                    }
+                    left -= x.steps;
+                    x.tail = left ? 0 : tail;
+                    x.chunk |= left ? 0 : LAST;
+                }
                 const uint32_t slot = n % F_ITEMS;
                 if (!wait_soon(smem_u32(&item_bar[F_ITEMS + slot]), (n / F_ITEMS & 1) ^ 1, abort_flag, &g_ffn_err,
                                limit))
@@ -1007,10 +1076,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 }
             }
         };
+        Held held;
         for (Item x;;) {
             bool got = feed.next<true>(x, abort_flag, limit);
             if (got && x.e >= 0) {
                 if (OP == DHIDDEN && p.splits == 1) fetch(x, team);
+                if (OP == DW && !(x.chunk & FIRST)) held.fetch(p, team, tid);
                 if (x.steps) {
                     const uint32_t use = acc ? uses[1]++ : uses[0]++;
                     got = wait_soon(smem_u32(&tfull_bar[acc]), use & 1, abort_flag, &g_ffn_err, limit);
@@ -1040,7 +1111,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * acc);
             };
             // the teams take blocks of columns in turn; this one's last
-            const bool flat = (OP == DOWN || OP == DX || (OP == DW && !p.out_f32 && !p.accumulate)) && p.splits == 1;
+            const bool flat = (OP == DOWN || OP == DX || (OP == DW && !p.out_f32 && !p.accumulate)) && p.splits == 1 &&
+                              x.chunk == (FIRST | LAST);
             int last = (n_real - 1) / (flat ? F_COLS16 : F_COLS);
             if ((last & 1) != team) --last;
             if (last < 0) release();
@@ -1098,6 +1170,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     for (int i = 0; i < F_COLS; ++i)
                         turn[i * F_ROW + lg * 32 + lane] = __uint_as_float(raw[i]);
                     team_sync(team);
+                    if (OP == DW && x.chunk != (FIRST | LAST)) {
+                        held.add(p, x, turn, c, tid);
+                        if (!(x.chunk & FIRST) && c < last) held.fetch(p, c + 2, tid);
+                    }
+                    if (!(x.chunk & LAST)) continue;
                     if (p.splits > 1) {
                         store_part<OP>(p, x, turn, n0, m0, m_end, tid);
                     } else if (OP != DW && p.vec && n0 + F_COLS <= x.n_end && m0 + (OP == UP ? 64 : 128) <= m_end) {
@@ -1349,7 +1426,8 @@ struct Cut {
     int tile_n = 256, splits = 1;
     int64_t row_tiles = 0;
     int64_t ld[2] = {0, 0}, at[3] = {0, 0, 0}, stride = 0;     // of the parts
-    size_t bytes = 0;
+    int chunk = 0;
+    size_t held = 0, bytes = 0;
 };
 
 // Parts that the sums are cut into, so that every pair has a tile, of four
@@ -1394,26 +1472,36 @@ Cut cut(Op op, bool dense, int64_t rows, int64_t experts, int64_t m, int64_t k) 
     }
     return c;
 }
-Cut cut_grads(bool dense, int64_t rows, int64_t hidden, int64_t inner, int products) {
+Cut cut_grads(bool dense, int64_t rows, int64_t hidden, int64_t inner, int products, bool f32) {
     Cut c;
-    if (!dense) return c;
-    int64_t tiles = 0;
-    c.ld[0] = ceil_div(hidden, 8) * 8;
-    c.ld[1] = ceil_div(inner, 8) * 8;
-    for (int j = 0; j < 3; ++j) {
-        if (!(products >> j & 1)) continue;
-        tiles += ceil_div(hidden, 256) * ceil_div(inner, 256);
-        c.at[j] = c.stride;
-        c.stride += j == 2 ? hidden * c.ld[1] : inner * c.ld[0];
+    const int64_t steps = ceil_div(rows, F_K);
+    if (dense) {
+        int64_t tiles = 0;
+        c.ld[0] = ceil_div(hidden, 8) * 8;
+        c.ld[1] = ceil_div(inner, 8) * 8;
+        for (int j = 0; j < 3; ++j) {
+            if (!(products >> j & 1)) continue;
+            tiles += ceil_div(hidden, 256) * ceil_div(inner, 256);
+            c.at[j] = c.stride;
+            c.stride += j == 2 ? hidden * c.ld[1] : inner * c.ld[0];
+        }
+        c.splits = tiles ? split_count(tiles, steps) : 1;
+        if (c.splits > 1) c.bytes = align256(size_t(c.splits) * c.stride * 4);
     }
-    c.splits = tiles ? split_count(tiles, ceil_div(rows, F_K)) : 1;
-    if (c.splits > 1) c.bytes = size_t(c.splits) * c.stride * 4;
+    c.chunk = f32 ? F_CHUNK_F32 : F_CHUNK_BF16;
+    if (products && steps > c.chunk) {
+        // a tile may have more than one chunk
+        c.held = c.bytes;
+        c.bytes += size_t(F_PAIRS) * 256 * 256 * 4;
+    }
     return c;
 }
 void apply(FfnLaunch& p, const Cut& c, char* parts) {
     p.tile_n = c.tile_n;
     p.splits = c.splits;
     p.part = reinterpret_cast<float*>(parts);
+    p.chunk = c.chunk;
+    p.held = reinterpret_cast<float4*>(parts + c.held);
     p.part_stride = c.stride;
     for (int i = 0; i < 2; ++i) p.part_ld[i] = c.ld[i];
     for (int i = 0; i < 3; ++i) p.part_at[i] = c.at[i];
@@ -1486,7 +1574,7 @@ Backward plan(const muon_gated_ffn_grad_args& a) {
     b.cut_dh = cut(DHIDDEN, !a.offsets, a.rows, a.experts, a.inner, a.hidden);
     if (a.dx) b.cut_dx = cut(DX, !a.offsets, a.rows, a.experts, a.hidden, a.inner);
     b.cut_dw = cut_grads(!a.offsets, a.rows, a.hidden, a.inner,
-                         (a.dw_gate ? 1 : 0) | (a.dw_up ? 2 : 0) | (a.dw_down ? 4 : 0));
+                         (a.dw_gate ? 1 : 0) | (a.dw_up ? 2 : 0) | (a.dw_down ? 4 : 0), a.g_dtype == MUON_F32);
     b.part_at = b.space.take(std::max(b.cut_dh.bytes, std::max(b.cut_dx.bytes, b.cut_dw.bytes)));
     return b;
 }

@@ -693,6 +693,77 @@ def test_run_of_a_block(ns):
     ns.ops_sync()
 
 
+def one_sign(tokens, size, seed):
+    """Operands whose dgate, dup and h are exact and whose weight gradients are
+    sums of one sign: silu(64) = 64 and silu'(64) = 1 in fp32, up is a power of
+    two and w_down the identity."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    dy, x = (torch.randn(tokens, size, generator=g, device=DEV).abs_().to(BF) for _ in range(2))
+    up = (2.0 ** (torch.arange(size, device=DEV) % 3)).to(BF)
+    saved = torch.full((tokens, size), 64.0, dtype=BF, device=DEV), up.expand(tokens, -1).contiguous()
+    return dy, x, saved, up.to(D), torch.eye(size, dtype=BF, device=DEV)
+
+
+def one_sign_grads(dy, x, up, a, b):
+    of_x = torch.zeros(dy.shape[1], x.shape[1], dtype=D, device=DEV)
+    of_h = torch.zeros(dy.shape[1], dtype=D, device=DEV)
+    for t in range(a, b, 16384):
+        part = dy[t:min(b, t + 16384)].to(D)
+        of_x += part.t() @ x[t:min(b, t + 16384)].to(D)
+        of_h += part.sum(0)
+    return up[:, None] * of_x, 64 * of_x, 64 * of_h[:, None] * up
+
+
+LONG = 200003
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("size,counts", [(1024, None), (256, None), (256, [LONG]), (264, [40, 0, LONG - 4200, 4097])])
+def test_gated_ffn_long_sums(ns, size, counts, accumulate):
+    """fp32 gradients: running sums of 4096 tokens at most (256 products of
+    two cuts of 2^-23 at most each), added up with one rounding each.  One running
+    sum loses 0.4 * 2^-23 a product on average, ten times as much."""
+    dy, x, saved, up, eye = one_sign(LONG, size, 1)
+    lead = () if counts is None else (len(counts),)
+    w = [eye.expand(*lead, -1, -1).contiguous()] * 3
+    ends = [0, LONG] if counts is None else [0, *torch.tensor(counts).cumsum(0).tolist()]
+    before = rand(2, *lead, size, size).abs() * 1e6
+    grads = [before.clone() for _ in range(3)]
+    ns.gated_ffn_backward(dy, x, saved, *w, grads=grads, accumulate=accumulate,
+                          offsets=None if counts is None else bounds_of(counts))
+    bound = 256 * 2 * 2.0 ** -23 + (LONG / 4096 + 30) * U32
+    assert bound < 0.12 * 0.4 * 2.0 ** -23 * LONG / 16
+    for e, (a, b) in enumerate(zip(ends, ends[1:])):
+        for got, want, name in zip(grads, one_sign_grads(dy, x, up, a, b), ("gate", "up", "down")):
+            old = before.view(-1, size, size)[e].to(D) * accumulate
+            got = got.view(-1, size, size)[e]
+            near(got, want + old, bound * want + U32 * (want + old), f"dw_{name} of {e}")
+
+
+@pytest.mark.parametrize("size,counts", [(1024, None), (256, [LONG]), (264, [40, 0, LONG - 4200, 4160])])
+def test_gated_ffn_long_sums_of_bf16(ns, size, counts):
+    """What a sum has lost shows in the mean difference of many results from
+    the exact values' roundings.  8192 tokens (512 products of two cuts of a
+    place each at most, 2^-23 of a sum that is on average 0.375 of its end's place)
+    lose 4.6e-5 at most, one running sum over all of them more than ten times that.
+    The difference is 0 or a step, 2^-7 of a value at most, at the few values that the
+    loss carries over a rounding's border: a share of 2^-7 or so of them, the
+    deviation of one's relative difference is 7e-4 and of the mean of 65536 values
+    3e-6; up to five of those count."""
+    dy, x, saved, up, eye = one_sign(LONG, size, 3)
+    lead = () if counts is None else (len(counts),)
+    w = [eye.expand(*lead, -1, -1).contiguous()] * 3
+    ends = [0, LONG] if counts is None else [0, *torch.tensor(counts).cumsum(0).tolist()]
+    _, *grads = ns.gated_ffn_backward(dy, x, saved, *w, offsets=None if counts is None else bounds_of(counts))
+    for e, (a, b) in enumerate(zip(ends, ends[1:])):
+        for got, want, name in zip(grads[:2], one_sign_grads(dy, x, up, a, b), ("gate", "up")):
+            got = got.view(-1, size, size)[e].to(D)
+            near(got, want, (HALF[BF] + 512 * 2 * 2.0 ** -23) * want, f"dw_{name} of {e}")
+            if b > a:
+                off = ((got - want.to(BF).to(D)) / want).mean().item()
+                assert abs(off) <= 4.9e-5 + 1.5e-5, (name, e, off)
+
+
 def test_two_calls_at_once(ns):
     """Calls on two streams and from two threads have workspaces of their own."""
     import threading
