@@ -44,6 +44,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "ffn_drain.h"
 #include "ops_internal.h"
 #include "tc_wait.cuh"
 
@@ -95,12 +96,14 @@ template <int OP>
 struct Space {
     static constexpr int STAGES = OP == DHIDDEN ? 5 : 6;
     static constexpr int BARS = STAGES * F_STAGE_BYTES;
+    static constexpr int ASKED = BARS + 320;                 // by the loading threads, for an abort
     static constexpr int ITEMS = BARS + 384;                 // tiles handed out
     static constexpr int TURN = ITEMS + 256;
     static constexpr int KEPT = TURN + 2 * F_TURN_BYTES;     // two teams'
     static constexpr int TABLE = KEPT + (OP == DHIDDEN ? 2 * F_KEPT_BYTES : 0);
     static constexpr int BYTES = TABLE + 2 * (F_EXPERTS + 1) * 4 + 1024;
     static_assert(BYTES <= 232448, "shared memory per CTA");
+    static_assert(8 * (4 * STAGES + 5 + 2 * F_ITEMS) + 8 <= 320 && 2 * sizeof(Asked) <= 64, "barriers and counts");
 };
 
 // One output matrix (or as many as there are experts).
@@ -324,6 +327,12 @@ __device__ __forceinline__ void load_box(uint32_t dst, const void* tmap, uint32_
         "complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(block), "r"(z), "r"(cluster_bar)
         : "memory");
+}
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                          uint32_t idesc, uint32_t accumulate) {
@@ -694,9 +703,7 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
     const uint32_t full_leader = map_to_rank(full, 0), tail_own = map_to_rank(tail_bar, rank);
     const uint32_t stage0 = smem_u32(smem) + (A ? 0 : F_OP_BYTES);
     uint32_t slot = 0, parity = 1;
-    // a bit a stage: it has been loaded, its last load was a short step's, and
-    // the parities that follow its loads of either kind
-    uint32_t used = 0, tails = 0, tail_phase = 0, full_phase = 0;
+    Asked asked = {};
     bool ok = true, free_next = false;
     for (Item x; ok;) {
         ok = feed.next<false>(x, abort_flag, p.wait_limit_ns);
@@ -727,15 +734,16 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
                 uint32_t bar = full_leader + 8 * slot;
                 if (OP == DW && x.tail && s == stop - 1) {
                     if (A) mbar_expect_tx(tail_bar + 8 * slot, bytes);
-                    tails |= 1u << slot;
-                    tail_phase ^= 1u << slot;
+                    asked.tails |= 1u << slot;
+                    asked.tail ^= 1u << slot;
                     bar = tail_own + 8 * slot;
                 } else {
                     if (A && rank == 0) mbar_expect_tx(full + 8 * slot, 2 * bytes);
-                    tails &= ~(1u << slot);
-                    full_phase ^= 1u << slot;
+                    asked.tails &= ~(1u << slot);
+                    asked.full ^= 1u << slot;
                 }
-                used |= 1u << slot;
+                asked.two = (asked.two & ~(1u << slot)) | (boxes > 1 ? 1u : 0u) << slot;
+                ++asked.steps;
                 const uint32_t to = stage0 + slot * F_STAGE_BYTES;
                 if constexpr (A) {
                     if constexpr (OP == UP) {
@@ -768,14 +776,37 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
             }
         }
     }
-    if (!ok && A) {
-        // the last loads of each stage (the leader's barriers count both
-        // CTAs', and both operands')
-        for (uint32_t i = 0; i < STAGES; ++i) {
-            if (!(used >> i & 1)) continue;
-            if (tails >> i & 1) wait_quiet(tail_bar + 8 * i, (tail_phase >> i & 1) ^ 1, p.wait_limit_ns);
-            else if (rank == 0) wait_quiet(full + 8 * i, (full_phase >> i & 1) ^ 1, p.wait_limit_ns);
-        }
+    reinterpret_cast<Asked*>(smem + Space<OP>::ASKED)[A ? 0 : 1] = asked;
+}
+
+// Waits, no longer than the limit for all of them, for the loads that a pair
+// which has given up still has in flight: this CTA's of short steps, and,
+// where the leader does it, both CTAs' of whole ones.  No thread asks for more.
+template <int OP>
+__device__ __forceinline__ void drain_loads(uint8_t* smem, uint32_t rank, uint64_t limit) {
+    constexpr int STAGES = Space<OP>::STAGES;
+    const uint32_t full = smem_u32(smem + Space<OP>::BARS), tail_bar = full + 16 * STAGES;
+    const Asked* const own = reinterpret_cast<const Asked*>(smem + Space<OP>::ASKED);
+    Asked by[4] = {own[0], own[1]};
+    const uint32_t other = map_to_rank(smem_u32(own), rank ^ 1);
+    uint32_t* const words = reinterpret_cast<uint32_t*>(by + 2);
+#pragma unroll
+    for (uint32_t i = 0; i < 2 * sizeof(Asked) / 4; ++i)
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(words[i]) : "r"(other + 4 * i) : "memory");
+    const auto bytes = [](int i, bool two) -> uint32_t { return i & 1 ? F_BOX * (two ? 2 : 1) : F_OP_BYTES; };
+    const uint64_t t0 = global_ns();
+    const auto ends = [&](uint32_t bar, const Settle& s) {
+        if (!s.wait) return true;
+        if (s.arm) mbar_expect_tx(bar, s.arm);
+        if (s.cancel) mbar_complete_tx(bar, s.cancel);
+        while (!mbar_try_wait(bar, s.parity))
+            if (global_ns() - t0 > limit) return false;
+        return true;
+    };
+#pragma unroll 1
+    for (uint32_t i = 0; i < STAGES; ++i) {
+        if (OP == DW && !ends(tail_bar + 8 * i, settle(by, 2, i, STAGES, true, bytes))) return;
+        if (rank == 0 && !ends(full + 8 * i, settle(by, 4, i, STAGES, false, bytes))) return;
     }
 }
 
@@ -874,6 +905,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     const uint64_t limit = p.wait_limit_ns;
     Feed feed(smem + S::ITEMS, smem_u32(item_bar));
+    bool any = false;        // products have been issued
 
     if (warp == 0) {
         // ------------------------------------------------------ loads of A, of B
@@ -891,7 +923,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             uint32_t full_phase = 0, patch_phase = 0;       // a bit a stage
             uint32_t uses[2] = {0, 0};
             uint32_t acc = 0;
-            bool any = false;
             const uint64_t a_desc = smem_desc(smem_u32(smem), A_MN ? F_BOX : 16, 1024);
             const uint64_t b_desc = smem_desc(smem_u32(smem + F_OP_BYTES), B_MN ? F_BOX : 16, 1024);
             const uint32_t full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
@@ -975,11 +1006,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 there = false;
                 acc ^= 1;
                 x = y;
-            }
-            // (the lane that issued the products: elections of one mask agree)
-            if (!ok && any && elected()) {
-                commit_pair_local(smem_u32(drain_bar));
-                wait_quiet(smem_u32(drain_bar), 0, limit);
             }
         }
     } else if (warp == F_TILE_WARP) {
@@ -1208,10 +1234,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             }
             if (x.steps) acc ^= 1;
         }
+        if (OP == DHIDDEN) copies_done();
     }
 
+    // A wait that ran out in one CTA is known to both before they meet, whatever
+    // of the pair had done its work by then.
+    if (*abort_flag) store_cluster(map_to_rank(smem_u32(tmem_slot + 1), rank ^ 1), 1u);
+    __syncwarp();
     tc_fence_before();
     cluster_sync_all();      // no CTA leaves while its pair may still touch it
+    if (*abort_flag) {
+        if (threadIdx.x == 0) drain_loads<OP>(smem, rank, limit);
+        // (the lane that issued the products: elections of one mask agree)
+        if (warp == 1 && any && elected()) {
+            commit_pair_local(smem_u32(drain_bar));
+            wait_quiet(smem_u32(drain_bar), 0, limit);
+        }
+        __syncwarp();
+        cluster_sync_all();
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),

@@ -1,0 +1,158 @@
+// Plays the loads of a CTA pair of the gated feed-forward kernels through on
+// the CPU, with threads of random speed that are stopped at any moment, and
+// then what the pair does about its loads in flight (ffn_drain.h).
+//
+//   ffn_drain <rule>     rule 0: each CTA's first thread waits for the stages
+//                        that it has loaded itself (must be found out by the
+//                        model); 1: the kernel's
+//
+// Prints the number of runs in which the pair left with a load in flight, and
+// of those in which a wait would not have ended.
+#include <cstdio>
+#include <cstdlib>
+#include <random>
+#include <vector>
+
+#include "ffn_drain.h"
+
+using namespace muon::ops;
+
+namespace {
+
+// One arrival a phase, and bytes.
+struct Bar {
+    int pending = 1;
+    int64_t bytes = 0;
+    uint32_t phase = 0;
+    bool over(uint32_t parity) const { return (phase & 1) != parity; }
+    void turn() {
+        if (pending == 0 && bytes == 0) {
+            ++phase;
+            pending = 1;
+        }
+    }
+    void arm(int64_t n) {
+        bytes += n;
+        --pending;
+        turn();
+    }
+    void land(int64_t n) {
+        bytes -= n;
+        turn();
+    }
+};
+
+constexpr int STEPS = 60;
+constexpr int A_BYTES = 16384, BOX = 8192;
+
+struct Step {
+    bool tail, two;
+};
+struct Load {
+    Bar* bar;
+    int bytes;
+};
+
+// threads 0, 1: A and B of the leader; 2, 3: of the other CTA
+uint32_t part(int i, bool two) { return i % 2 == 0 ? A_BYTES : BOX * (two ? 2 : 1); }
+
+// bit 0: left with a load in flight; bit 1: a wait that would not end
+int plays(std::mt19937& rng, int rule) {
+    const uint32_t stages = 5 + rng() % 2;
+    std::vector<Step> steps(STEPS);
+    for (Step& s : steps) s = {rng() % 3 == 0, rng() % 3 != 0};
+    std::vector<Bar> full(stages), tail[2];
+    tail[0].resize(stages);
+    tail[1].resize(stages);
+    std::vector<Load> flying;
+    Asked by[4] = {};
+    uint32_t products = 0;
+    const uint32_t moves = rng() % 600, lazy = rng() % 5;
+    // (the parity of a step's phase goes by the steps of its kind that its stage had)
+    auto kind = [&](uint32_t step) {
+        uint32_t n = 0;
+        for (uint32_t i = step % stages; i < step; i += stages) n += steps[i].tail == steps[step].tail;
+        return n & 1;
+    };
+    for (uint32_t m = 0; m < moves; ++m) {
+        const uint32_t what = rng() % 8;
+        if (what < 4) {
+            Asked& me = by[what];
+            const uint32_t i = me.steps, stage = i % stages, rank = what / 2;
+            if (i >= STEPS || (i >= stages && products < i - stages + 1) || (what == lazy && rng() % 8)) continue;
+            const Step& s = steps[i];
+            Bar& bar = s.tail ? tail[rank][stage] : full[stage];
+            if (s.tail && what % 2 == 0) bar.arm(part(0, s.two) + part(1, s.two));
+            if (!s.tail && what == 0) bar.arm(2 * (part(0, s.two) + part(1, s.two)));
+            // the boxes, one by one
+            const int n = part(int(what), s.two) / BOX;
+            for (int k = 0; k < n; ++k) flying.push_back({&bar, BOX});
+            const uint32_t bit = 1u << stage;
+            me.tails = s.tail ? me.tails | bit : me.tails & ~bit;
+            me.two = s.two ? me.two | bit : me.two & ~bit;
+            (s.tail ? me.tail : me.full) ^= bit;
+            ++me.steps;
+        } else if (what < 7) {
+            if (flying.empty() || rng() % 3 == 0) continue;
+            const size_t at = rng() % flying.size();
+            flying[at].bar->land(flying[at].bytes);
+            flying.erase(flying.begin() + long(at));
+        } else if (products < STEPS) {
+            const uint32_t stage = products % stages, parity = kind(products);
+            const bool there = steps[products].tail ? tail[0][stage].over(parity) && tail[1][stage].over(parity)
+                                                    : full[stage].over(parity);
+            if (there) ++products;
+        }
+    }
+    // The pair gives up here.
+    struct Wait {
+        Bar* bar;
+        uint32_t parity;
+    };
+    std::vector<Wait> waits;
+    for (uint32_t s = 0; s < stages; ++s) {
+        if (rule == 0) {
+            for (int rank = 0; rank < 2; ++rank) {
+                const Asked& a = by[2 * rank];
+                if (a.steps <= s) continue;
+                if (a.tails >> s & 1) waits.push_back({&tail[rank][s], (a.tail >> s & 1) ^ 1});
+                else if (rank == 0) waits.push_back({&full[s], (a.full >> s & 1) ^ 1});
+            }
+            continue;
+        }
+        auto apply = [&](Bar& bar, const Settle& x) {
+            if (!x.wait) return;
+            if (x.arm) bar.arm(x.arm);
+            if (x.cancel) bar.land(x.cancel);
+            waits.push_back({&bar, x.parity});
+        };
+        for (int rank = 0; rank < 2; ++rank)
+            apply(tail[rank][s], settle(by + 2 * rank, 2, s, stages, true, part));
+        apply(full[s], settle(by, 4, s, stages, false, part));
+    }
+    // The loads land in any order: when the last wait has ended, all have.
+    while (true) {
+        bool all = true;
+        for (const Wait& w : waits) all &= w.bar->over(w.parity);
+        if (all) return flying.empty() ? 0 : 1;
+        if (flying.empty()) return 2;
+        const size_t at = rng() % flying.size();
+        flying[at].bar->land(flying[at].bytes);
+        flying.erase(flying.begin() + long(at));
+    }
+}
+
+}  // namespace
+
+int main(int argc, char** argv) {
+    const int rule = argc < 2 ? 1 : std::atoi(argv[1]);
+    int left = 0, stuck = 0;
+    for (int i = 0; i < 200000; ++i) {
+        std::mt19937 rng(1000 + i);
+        const int r = plays(rng, rule);
+        left += r & 1;
+        stuck += r >> 1;
+    }
+    std::printf("%d %d\n", left, stuck);
+    return 0;
+}

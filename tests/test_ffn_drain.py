@@ -1,0 +1,49 @@
+"""A CTA pair of the gated feed-forward kernels when a bounded wait runs out:
+what it still has in flight, on the CPU (ffn_drain.cpp, which includes the
+header that the kernel takes its rules from)."""
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "newton_schulz_06_gb300", "csrc")
+
+
+@pytest.fixture(scope="module")
+def model(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("drain") / "model")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I", CSRC, os.path.join(ROOT, "tests", "ffn_drain.cpp"), "-o", exe],
+                   check=True)
+
+    def run(rule):
+        out = subprocess.run([exe, str(rule)], capture_output=True, text=True, check=True).stdout
+        return [int(v) for v in out.split()]
+    return run
+
+
+def test_an_aborted_pair_waits_for_what_it_asked_for(model):
+    assert model(1) == [0, 0]
+
+
+def test_the_model_finds_loads_that_nobody_waits_for(model):
+    """With each CTA's first thread waiting for the stages that it has loaded
+    itself, pairs leave with loads in flight, and wait for bytes that nobody
+    asked for."""
+    left, stuck = model(0)
+    assert left > 0 and stuck > 0
+
+
+def test_the_pair_drains_after_all_roles_have_ended():
+    """Behind the barrier at which both CTAs meet, whichever of them and
+    whatever role gave up; and neither leaves before the other has drained."""
+    text = open(os.path.join(CSRC, "gated_ffn.cu")).read()
+    end = text[text.index("if (*abort_flag) store_cluster("):]
+    end = end[:end.index("tcgen05.dealloc")]
+    first = end.index("cluster_sync_all()")
+    assert first < end.index("drain_loads<OP>(") < end.rindex("cluster_sync_all()")
+    assert first < end.index("commit_pair_local(") < end.rindex("cluster_sync_all()")
+    assert end.count("cluster_sync_all()") == 2
+    # each loading thread leaves its counts, whatever ended its loop
+    body = text[text.index("load_operand(const FfnLaunch& p"):text.index("drain_loads(uint8_t*")]
+    assert "return" not in body and body.index("= asked;") > body.rindex("load_box(")
