@@ -3,11 +3,13 @@
 // aborts through on the CPU.
 //
 // A step's boxes are asked for by two threads a CTA, and counted on one
-// barrier: the leader's of that stage for all four threads, or, where a step
-// is short, each CTA's own for its two.  The first of them arms the phase with
-// the bytes of all.  A pair that gives up may leave a stage that only some of
-// them have asked for: then the phase either expects bytes that never come, or
-// is not armed and its barrier says nothing about those under way.
+// barrier: the leader's of that stage for all four threads, or, where the step
+// is torn (its last 16 rows are not all the expert's), each CTA's own for its
+// two.  Then a warp a CTA asks for zeros over those rows, which count on another
+// barrier of the leader's.  The first of each set arms the phase with the bytes of
+// all.  A pair that gives up may leave a stage that only some of them have asked
+// for: then the phase either expects bytes that never come, or is not armed and
+// its barrier says nothing about those under way.
 #pragma once
 
 #include <cstdint>
@@ -23,56 +25,98 @@
 namespace muon {
 namespace ops {
 
-// What a loading thread has asked for.
+constexpr uint32_t DRAIN_BOX = 64 * 64 * 2;      // bytes of a box: 64 rows of 128
+
+// What a loading thread has asked for, or (steps alone) a clearing warp.
 struct Asked {
     uint32_t steps;          // so many steps, from the first one on
-    uint32_t tails, two;     // a bit a stage: its last step was a short one; had two boxes of B
-    uint32_t full, tail;     // a bit a stage: whole and short steps it has had, modulo 2
+    uint32_t gaps;           // four bits a stage: the rows to clear of its last step (0: it is not torn)
+    uint32_t two;            // a bit a stage: its last step has two boxes of B
+    uint32_t full, torn;     // a bit a stage: whole and torn steps it has had, modulo 2
 };
 
-// The last of `steps` steps that had the stage: false if none had.
-MUON_HD bool last_step(uint32_t steps, uint32_t stage, uint32_t stages, uint32_t* step) {
-    if (steps <= stage) return false;
-    *step = steps - 1 - (steps - 1 - stage) % stages;
-    return true;
+// One more step, in this stage.
+MUON_HD void ask(Asked& a, uint32_t stage, uint32_t gap, bool two) {
+    const uint32_t bit = 1u << stage;
+    a.gaps = (a.gaps & ~(15u << 4 * stage)) | gap << 4 * stage;
+    a.two = two ? a.two | bit : a.two & ~bit;
+    if (gap) a.torn ^= bit;
+    else a.full ^= bit;
+    ++a.steps;
 }
 
-// What makes the barrier's phase end when the last byte that was asked for is
+// Bytes that a step takes of a thread for A, for B, of a clearing warp.
+MUON_HD uint32_t a_bytes() { return 2 * DRAIN_BOX; }
+MUON_HD uint32_t b_bytes(bool two) { return two ? 2 * DRAIN_BOX : DRAIN_BOX; }
+MUON_HD uint32_t zero_bytes(uint32_t gap, bool two) { return gap * 128 * (two ? 4 : 3); }
+
+// The last step that any of n threads has asked for in a stage.  No other can
+// be in flight: a stage is loaded again when its products have run.
+struct Last {
+    bool any, two;
+    uint32_t step, gap, full, torn;      // the parities of its phases
+};
+MUON_HD Last last_of(const Asked* by, int n, uint32_t stage, uint32_t stages) {
+    Last l{false, false, 0, 0, 0, 0};
+    for (int i = 0; i < n; ++i) {
+        const Asked& a = by[i];
+        if (a.steps <= stage) continue;
+        const uint32_t step = a.steps - 1 - (a.steps - 1 - stage) % stages;
+        if (l.any && step <= l.step) continue;
+        l = {true, (a.two >> stage & 1) != 0, step, a.gaps >> 4 * stage & 15, (a.full >> stage & 1) ^ 1,
+             (a.torn >> stage & 1) ^ 1};
+    }
+    return l;
+}
+
+// What makes a barrier's phase end when the last byte that was asked for is
 // there: arm it with these bytes (nobody has), or take these off (they were
 // never asked for), and wait for the parity.
 struct Settle {
     uint32_t arm, cancel, parity;
     bool wait;
 };
-
-// Of one stage's barrier.  by: the threads that load for it, the first of
-// which arms it; bytes(i, two): what thread i asks for.  Only the last step
-// that any of them asked for can be in flight: a stage is loaded again when its
-// products have run.  tail: of the short steps' barrier.
-template <typename Bytes>
-MUON_HD Settle settle(const Asked* by, int n, uint32_t stage, uint32_t stages, bool tail, Bytes bytes) {
-    Settle s{0, 0, 0, false};
-    uint32_t step = 0;
-    int who = -1;
-    for (int i = 0; i < n; ++i) {
-        uint32_t at;
-        if (last_step(by[i].steps, stage, stages, &at) && (who < 0 || at > step)) {
-            step = at;
-            who = i;
-        }
+MUON_HD void add(Settle& s, bool asked, bool first, uint32_t bytes, bool& armed) {
+    if (first) armed = asked;
+    if (asked) {
+        s.arm += bytes;
+        s.wait = true;
+    } else {
+        s.cancel += bytes;
     }
-    if (who < 0 || (by[who].tails >> stage & 1) != (tail ? 1u : 0u)) return s;
-    const bool two = by[who].two >> stage & 1;
-    uint32_t asked = 0, all = 0;
-    for (int i = 0; i < n; ++i) {
-        all += bytes(i, two);
-        if (by[i].steps > step) asked += bytes(i, two);
-    }
-    if (by[0].steps > step) s.cancel = all - asked;
-    else s.arm = asked;
-    s.parity = ((tail ? by[who].tail : by[who].full) >> stage & 1) ^ 1;
-    s.wait = true;
+}
+MUON_HD Settle settled(Settle s, bool armed) {
+    if (armed) s.arm = 0;
+    else s.cancel = 0;
     return s;
+}
+
+// Of a stage's barriers: the leader's of whole steps (by: A and B of the
+// leader, then of the other CTA), a CTA's of torn ones (its own A and B), and the
+// leader's of the zeros (zeros: both CTAs').
+MUON_HD Settle settle_full(const Asked* by, uint32_t stage, uint32_t stages) {
+    const Last l = last_of(by, 4, stage, stages);
+    Settle s{0, 0, l.full, false};
+    bool armed = false;
+    if (l.any && !l.gap)
+        for (int i = 0; i < 4; ++i) add(s, by[i].steps > l.step, i == 0, i & 1 ? b_bytes(l.two) : a_bytes(), armed);
+    return settled(s, armed);
+}
+MUON_HD Settle settle_torn(const Asked* by, uint32_t stage, uint32_t stages) {
+    const Last l = last_of(by, 2, stage, stages);
+    Settle s{0, 0, l.torn, false};
+    bool armed = false;
+    if (l.any && l.gap)
+        for (int i = 0; i < 2; ++i) add(s, by[i].steps > l.step, i == 0, i & 1 ? b_bytes(l.two) : a_bytes(), armed);
+    return settled(s, armed);
+}
+MUON_HD Settle settle_zeros(const Asked* by, const Asked* zeros, uint32_t stage, uint32_t stages) {
+    const Last l = last_of(by, 4, stage, stages);
+    Settle s{0, 0, l.torn, false};
+    bool armed = false;
+    if (l.any && l.gap)
+        for (int i = 0; i < 2; ++i) add(s, zeros[i].steps > l.step, i == 0, zero_bytes(l.gap, l.two), armed);
+    return settled(s, armed);
 }
 
 }  // namespace ops

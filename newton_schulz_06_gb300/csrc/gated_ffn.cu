@@ -25,8 +25,8 @@
 //
 // Roles in a CTA: warps 0 and 11 load (TMA), warp 1 issues the products (the
 // pair's leader only), warps 2-9 are the epilogue, in two teams of four that
-// take a tile's columns in turn, warp 10 clears what DW loads past an expert's
-// last token, warp 12 finds the tiles.  Two accumulators, so that a tile is
+// take a tile's columns in turn, warp 10 lays zeros over what DW loads past an
+// expert's last token, warp 12 finds the tiles.  Two accumulators, so that a tile is
 // written out while the next one's products run.  Pairs walk the tiles in turn.
 //
 // What bounds it.  Long sums: the tensor cores, at the rate that the power
@@ -58,6 +58,7 @@ constexpr int F_K = 64;                            // of the sums, a step
 constexpr int F_BOX = 64 * 64 * 2;                 // a TMA box: 64 rows of 64 bf16
 constexpr int F_OP_BYTES = 2 * F_BOX;              // an operand's part of a CTA, a step
 constexpr int F_STAGE_BYTES = 2 * F_OP_BYTES;
+static_assert(F_BOX == DRAIN_BOX, "what the drain counts");
 constexpr int F_EXPERTS = 1024;
 constexpr int F_COLS = 16;                         // columns that are turned at a time in fp32
 constexpr int F_ROW = 132;                         // floats of a turned row: 128 and a gap
@@ -67,8 +68,8 @@ constexpr int F_TURN_BYTES = F_COLS16 * F_ROW16 * 2;
 static_assert(F_TURN_BYTES >= F_COLS * F_ROW * 4 && F_TURN_BYTES % 16 == 0, "a team's buffer");
 constexpr int F_KEPT_BYTES = 2 * 4 * 128 * 16;     // a team's g and u of 16 columns, twice (DHIDDEN)
 constexpr int F_EPI_WARPS = 8;
-constexpr int F_PATCH_WARP = 2 + F_EPI_WARPS;
-constexpr int F_LOAD_B_WARP = F_PATCH_WARP + 1;
+constexpr int F_CLEAR_WARP = 2 + F_EPI_WARPS;
+constexpr int F_LOAD_B_WARP = F_CLEAR_WARP + 1;
 constexpr int F_TILE_WARP = F_LOAD_B_WARP + 1;
 constexpr int F_THREADS = 32 * (F_TILE_WARP + 1);
 constexpr int F_ITEMS = 4;                         // tiles found ahead
@@ -96,14 +97,14 @@ template <int OP>
 struct Space {
     static constexpr int STAGES = OP == DHIDDEN ? 5 : 6;
     static constexpr int BARS = STAGES * F_STAGE_BYTES;
-    static constexpr int ASKED = BARS + 320;                 // by the loading threads, for an abort
+    static constexpr int ASKED = BARS + 320;                 // loads asked for, for an abort
     static constexpr int ITEMS = BARS + 384;                 // tiles handed out
     static constexpr int TURN = ITEMS + 256;
     static constexpr int KEPT = TURN + 2 * F_TURN_BYTES;     // two teams'
     static constexpr int TABLE = KEPT + (OP == DHIDDEN ? 2 * F_KEPT_BYTES : 0);
     static constexpr int BYTES = TABLE + 2 * (F_EXPERTS + 1) * 4 + 1024;
     static_assert(BYTES <= 232448, "shared memory per CTA");
-    static_assert(8 * (4 * STAGES + 5 + 2 * F_ITEMS) + 8 <= 320 && 2 * sizeof(Asked) <= 64, "barriers and counts");
+    static_assert(8 * (4 * STAGES + 5 + 2 * F_ITEMS) + 8 <= 320 && 3 * sizeof(Asked) <= 64, "barriers and counts");
 };
 
 // One output matrix (or as many as there are experts).
@@ -112,6 +113,9 @@ struct Out {
     int64_t ld, stride;
     int32_t vec;             // rows lie on 16 bytes
 };
+
+// Zeros come by maps of one row, from rows past it: nothing is read.
+constexpr int F_NO_ROW = 64;
 
 // One of the sums' operand pairs: a is M's side, b is N's (b64: in boxes of 64,
 // for the tiles that have no more a CTA).  wide_a, wide_b: a box has 128
@@ -123,6 +127,7 @@ struct Maps {
 
 struct FfnLaunch {
     Maps maps[3];            // UP: Wg with x, Wu; DX: Wg with dg, Wu with du; DW: its three products
+    CUtensorMap zeros[4];    // DW: boxes of 1, 2, 4 and 8 rows of 64
     Out out[3];              // UP: h, g, u; DHIDDEN: dg, du, h; DW: dWg, dWu, dWd
     const void *gate, *up;   // DHIDDEN reads them
     int64_t ld_kept;
@@ -179,6 +184,9 @@ struct alignas(16) Item {
     int32_t s0, split;       // from this one of the whole sum on; which part of it that is
     int32_t t0;              // DW: the first token
     int32_t tail;            // DW: tokens of the last step, if not 64
+    // DW: the rows of the last step's last product that are not this expert's
+    // (0: the step is not torn)
+    __device__ __forceinline__ uint32_t gap() const { return -tail & 15; }
     int32_t chunk;           // DW: which end of a long sum this is (FIRST, LAST)
 };
 constexpr int FIRST = 1, LAST = 2;
@@ -331,6 +339,14 @@ __device__ __forceinline__ void load_box(uint32_t dst, const void* tmap, uint32_
 __device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void read_cluster(void* to, uint32_t cluster_addr, uint32_t bytes) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < bytes / 4; ++i)
+        asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                     : "=r"(static_cast<uint32_t*>(to)[i])
+                     : "r"(cluster_addr + 4 * i)
+                     : "memory");
+}
 __device__ __forceinline__ void store_cluster(uint32_t cluster_addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
@@ -355,13 +371,6 @@ __device__ __forceinline__ void commit_pair_local(uint32_t bar) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
         : "memory");
-}
-// Arrive on a barrier of the pair's leader.  What the waiter's products read
-// are this CTA's own writes to its shared memory, ordered before the arrival
-// by the fence to the async proxy; a release over the whole cluster took 1500
-// cycles and more.
-__device__ __forceinline__ void arrive_leader(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // 16 fp32 columns of this warp's TMEM lanes.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
@@ -699,8 +708,8 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
                                              volatile int* abort_flag) {
     constexpr bool A_MN = OP == DHIDDEN || OP == DX || OP == DW, B_MN = OP == DW;
     constexpr int STAGES = Space<OP>::STAGES;
-    const uint32_t full = smem_u32(smem + Space<OP>::BARS), empty = full + 8 * STAGES, tail_bar = empty + 8 * STAGES;
-    const uint32_t full_leader = map_to_rank(full, 0), tail_own = map_to_rank(tail_bar, rank);
+    const uint32_t full = smem_u32(smem + Space<OP>::BARS), empty = full + 8 * STAGES, torn = empty + 8 * STAGES;
+    const uint32_t full_leader = map_to_rank(full, 0), torn_own = map_to_rank(torn, rank);
     const uint32_t stage0 = smem_u32(smem) + (A ? 0 : F_OP_BYTES);
     uint32_t slot = 0, parity = 1;
     Asked asked = {};
@@ -732,18 +741,14 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
                 const uint32_t ahead = slot + 1 == STAGES ? 0 : slot + 1;
                 free_next = is_over(empty + 8 * ahead, ahead ? parity : parity ^ 1);
                 uint32_t bar = full_leader + 8 * slot;
-                if (OP == DW && x.tail && s == stop - 1) {
-                    if (A) mbar_expect_tx(tail_bar + 8 * slot, bytes);
-                    asked.tails |= 1u << slot;
-                    asked.tail ^= 1u << slot;
-                    bar = tail_own + 8 * slot;
+                const uint32_t gap = OP == DW && s == stop - 1 ? x.gap() : 0;
+                if (OP == DW && gap) {
+                    if (A) mbar_expect_tx(torn + 8 * slot, bytes);
+                    bar = torn_own + 8 * slot;
                 } else {
                     if (A && rank == 0) mbar_expect_tx(full + 8 * slot, 2 * bytes);
-                    asked.tails &= ~(1u << slot);
-                    asked.full ^= 1u << slot;
                 }
-                asked.two = (asked.two & ~(1u << slot)) | (boxes > 1 ? 1u : 0u) << slot;
-                ++asked.steps;
+                ask(asked, slot, gap, boxes > 1);
                 const uint32_t to = stage0 + slot * F_STAGE_BYTES;
                 if constexpr (A) {
                     if constexpr (OP == UP) {
@@ -780,20 +785,20 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
 }
 
 // Waits, no longer than the limit for all of them, for the loads that a pair
-// which has given up still has in flight: this CTA's of short steps, and,
-// where the leader does it, both CTAs' of whole ones.  No thread asks for more.
+// which has given up still has in flight: this CTA's of torn steps, and, where
+// the leader does it, what else both CTAs asked for.  No thread asks for more.
 template <int OP>
 __device__ __forceinline__ void drain_loads(uint8_t* smem, uint32_t rank, uint64_t limit) {
     constexpr int STAGES = Space<OP>::STAGES;
-    const uint32_t full = smem_u32(smem + Space<OP>::BARS), tail_bar = full + 16 * STAGES;
-    const Asked* const own = reinterpret_cast<const Asked*>(smem + Space<OP>::ASKED);
-    Asked by[4] = {own[0], own[1]};
-    const uint32_t other = map_to_rank(smem_u32(own), rank ^ 1);
-    uint32_t* const words = reinterpret_cast<uint32_t*>(by + 2);
-#pragma unroll
-    for (uint32_t i = 0; i < 2 * sizeof(Asked) / 4; ++i)
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(words[i]) : "r"(other + 4 * i) : "memory");
-    const auto bytes = [](int i, bool two) -> uint32_t { return i & 1 ? F_BOX * (two ? 2 : 1) : F_OP_BYTES; };
+    const uint32_t full = smem_u32(smem + Space<OP>::BARS), torn = full + 16 * STAGES, zero = torn + 8 * STAGES;
+    const uint32_t own = smem_u32(smem + Space<OP>::ASKED);
+    Asked by[4], zeros[2];
+    for (uint32_t r = 0; r < 2; ++r) {
+        // (this CTA's first)
+        const uint32_t from = map_to_rank(own, rank ^ r);
+        read_cluster(&by[2 * r], from, 2 * sizeof(Asked));
+        read_cluster(&zeros[r], from + 2 * sizeof(Asked), sizeof(Asked));
+    }
     const uint64_t t0 = global_ns();
     const auto ends = [&](uint32_t bar, const Settle& s) {
         if (!s.wait) return true;
@@ -805,8 +810,10 @@ __device__ __forceinline__ void drain_loads(uint8_t* smem, uint32_t rank, uint64
     };
 #pragma unroll 1
     for (uint32_t i = 0; i < STAGES; ++i) {
-        if (OP == DW && !ends(tail_bar + 8 * i, settle(by, 2, i, STAGES, true, bytes))) return;
-        if (rank == 0 && !ends(full + 8 * i, settle(by, 4, i, STAGES, false, bytes))) return;
+        if (OP == DW && !ends(torn + 8 * i, settle_torn(by, i, STAGES))) return;
+        if (rank != 0) continue;
+        if (!ends(full + 8 * i, settle_full(by, i, STAGES))) return;
+        if (OP == DW && !ends(zero + 8 * i, settle_zeros(by, zeros, i, STAGES))) return;
     }
 }
 
@@ -820,9 +827,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     constexpr int STAGES = S::STAGES;
     uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + S::BARS);   // a step's loads (leader's)
     uint64_t* empty_bar = full_bar + STAGES;      // its products have run
-    uint64_t* tail_bar = empty_bar + STAGES;      // DW: this CTA's loads of a short step
-    uint64_t* patch_bar = tail_bar + STAGES;      // which both CTAs have cleared (leader's)
-    uint64_t* tfull_bar = patch_bar + STAGES;
+    uint64_t* torn_bar = empty_bar + STAGES;      // DW: this CTA's loads of a torn step
+    uint64_t* zero_bar = torn_bar + STAGES;       // and both CTAs' zeros over it (leader's)
+    uint64_t* tfull_bar = zero_bar + STAGES;
     uint64_t* tempty_bar = tfull_bar + 2;
     uint64_t* drain_bar = tempty_bar + 2;
     uint64_t* item_bar = drain_bar + 1;             // a tile is there; its place is free
@@ -841,8 +848,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&full_bar[s]), 1);
             mbar_init(smem_u32(&empty_bar[s]), 1);
-            mbar_init(smem_u32(&tail_bar[s]), 1);
-            mbar_init(smem_u32(&patch_bar[s]), 2);
+            mbar_init(smem_u32(&torn_bar[s]), 1);
+            mbar_init(smem_u32(&zero_bar[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&tfull_bar[a]), 1);
@@ -920,21 +927,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             }
         } else if (rank == 0) {
             uint32_t slot = 0;
-            uint32_t full_phase = 0, patch_phase = 0;       // a bit a stage
+            uint32_t full_phase = 0, zero_phase = 0;        // a bit a stage
             uint32_t uses[2] = {0, 0};
             uint32_t acc = 0;
             const uint64_t a_desc = smem_desc(smem_u32(smem), A_MN ? F_BOX : 16, 1024);
             const uint64_t b_desc = smem_desc(smem_u32(smem + F_OP_BYTES), B_MN ? F_BOX : 16, 1024);
             const uint32_t full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
             uint32_t idesc = 0, d_tmem = 0;
-            auto products = [&](uint32_t fresh) {
+            auto products = [&](uint32_t fresh, int count) {
                 const uint64_t ad = a_desc + (slot * F_STAGE_BYTES >> 4);
                 const uint64_t bd = b_desc + (slot * F_STAGE_BYTES >> 4);
                 if (elected()) {
 #pragma unroll
                     for (int kk = 0; kk < F_K / 16; ++kk)
-                        mma_pair(d_tmem, ad + uint64_t(kk * (A_MN ? 2048 : 32) >> 4),
-                                 bd + uint64_t(kk * (B_MN ? 2048 : 32) >> 4), idesc, kk ? 1u : fresh);
+                        if (kk < count)
+                            mma_pair(d_tmem, ad + uint64_t(kk * (A_MN ? 2048 : 32) >> 4),
+                                     bd + uint64_t(kk * (B_MN ? 2048 : 32) >> 4), idesc, kk ? 1u : fresh);
                     commit_pair_multicast(empty0 + 8 * slot);
                 }
                 __syncwarp();
@@ -978,19 +986,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     full_phase ^= 1u << slot;
                     const uint32_t next = slot + 1 == STAGES ? 0 : slot + 1;
                     there = is_over_warp(full0 + 8 * next, full_phase >> next & 1);
-                    products(fresh);
+                    products(fresh, F_K / 16);
                     fresh = 1;
                     slot = next;
                 }
                 if (!ok || !(ok = feed.next<true>(y, abort_flag, limit))) break;
-                // the last step, which DW's may be a short one
-                if (OP == DW && x.tail) {
-                    if (!wait(smem_u32(&patch_bar[slot]), patch_phase >> slot & 1)) {
+                // the last step, which DW's may be a short or a torn one: its
+                // products go no further than the expert's tokens
+                if (OP == DW && x.gap()) {
+                    if (!wait(smem_u32(&zero_bar[slot]), zero_phase >> slot & 1)) {
                         ok = false;
                         break;
                     }
-                    patch_phase ^= 1u << slot;
-                    tc_fence_after();
+                    zero_phase ^= 1u << slot;
                 } else {
                     if (!there && !wait(full0 + 8 * slot, full_phase >> slot & 1)) {
                         ok = false;
@@ -999,7 +1007,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     full_phase ^= 1u << slot;
                 }
                 free_acc = is_over_warp(smem_u32(&tempty_bar[acc ^ 1]), ((acc ? uses[0] : uses[1]) & 1) ^ 1);
-                products(fresh);
+                products(fresh, OP == DW && x.tail ? (x.tail + 15) / 16 : F_K / 16);
                 slot = slot + 1 == STAGES ? 0 : slot + 1;
                 if (elected()) commit_pair_multicast(smem_u32(&tfull_bar[acc]));
                 __syncwarp();
@@ -1047,32 +1055,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 if (x.e < 0) break;
             }
         }
-    } else if (warp == F_PATCH_WARP) {
-        // ---------------------------------------------------- short steps of DW
+    } else if (warp == F_CLEAR_WARP) {
+        // ----------------------------------------------------- torn steps of DW
         if constexpr (OP == DW) {
-            uint32_t step = 0, phase = 0;
-            const uint32_t patch_leader = map_to_rank(smem_u32(patch_bar), 0);
+            // Tokens of the next expert, or of none: 0 times a NaN of theirs would
+            // be a NaN here, so both operands' rows are cleared up to the next
+            // 16, which a product takes.  The zeros come as loads do, a box a lane,
+            // and like them count on the leader's barrier, so that the products
+            // read nothing that a thread of the other CTA has written: that
+            // took stores, a fence and a release to the whole cluster, with
+            // which 128 experts' DW takes 552 to 579 us, not 517 to 533.
+            Asked zeros = {};
+            uint32_t phase = 0;
+            const uint32_t leader = map_to_rank(smem_u32(zero_bar), 0);
+            const uint32_t box = lane >> 2, bit = lane & 3;
             for (Item x; feed.next<true>(x, abort_flag, limit) && x.e >= 0;) {
-                step += x.steps;
-                if (!x.steps || !x.tail) continue;
-                const uint32_t slot = (step - 1) % STAGES;
-                const bool got = wait_soon(smem_u32(&tail_bar[slot]), phase >> slot & 1, abort_flag,
-                                           &g_ffn_err, limit);
-                if (!__all_sync(0xffffffffu, got)) break;
-                phase ^= 1u << slot;
-                // tokens of the next expert, or of none: 0 times a NaN of
-                // theirs would be a NaN here, so both operands are cleared
-                uint8_t* const stage = smem + slot * F_STAGE_BYTES;
-                const int boxes = 2 + (x.n / 2 + 63) / 64;
-                for (int c = x.tail * 8 + lane; c < 64 * 8; c += 32)
-#pragma unroll
-                    for (int box = 0; box < 4; ++box)
-                        if (box < boxes)
-                            *reinterpret_cast<uint4*>(stage + box * F_BOX + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive_leader(patch_leader + 8 * slot);
+                const uint32_t step = zeros.steps + x.steps, gap = x.gap();
+                if (x.steps && gap) {
+                    const uint32_t slot = (step - 1) % STAGES;
+                    if (!wait_warp(smem_u32(&torn_bar[slot]), phase >> slot & 1, abort_flag, limit)) break;
+                    phase ^= 1u << slot;
+                    const bool two = x.n > 128;
+                    if (lane == 0 && rank == 0) mbar_expect_tx(smem_u32(&zero_bar[slot]), 2 * zero_bytes(gap, two));
+                    if (box < (two ? 4 : 3) && gap >> bit & 1)
+                        load_box(smem_u32(smem) + slot * F_STAGE_BYTES + box * F_BOX +
+                                     (x.tail + (gap & ((1u << bit) - 1))) * 128,
+                                 &p.zeros[bit], leader + 8 * slot, 0, F_NO_ROW, 0);
+                    __syncwarp();
+                }
+                zeros.steps = step;
             }
+            if (lane == 0) reinterpret_cast<Asked*>(smem + S::ASKED)[2] = zeros;
         }
     } else {
         // --------------------------------------------------------- write out
@@ -1383,7 +1396,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 bool encode(CUtensorMap* tm, const void* base, unsigned rank, const int64_t* dims, const int64_t* strides,
-            const unsigned* box) {
+            const unsigned* box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     if (!encoder()) return false;
     cuuint64_t d[4], st[3];
     cuuint32_t bx[4], el[4] = {1, 1, 1, 1};
@@ -1393,7 +1406,7 @@ bool encode(CUtensorMap* tm, const void* base, unsigned rank, const int64_t* dim
         if (i + 1 < rank) st[i] = cuuint64_t(strides[i]) * 2;
     }
     return encoder()(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, st, bx, el,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 int64_t row_stride(const Operand& o) { return o.rows > 1 ? o.ld : ceil_div(o.cols, 8) * 8; }
@@ -1418,6 +1431,13 @@ bool boxes_map(CUtensorMap* tm, const Operand& o, bool wide) {
 bool columns_map(CUtensorMap* tm, const Operand& o, int32_t* wide) {
     *wide = o.cols % 64 == 0;
     return boxes_map(tm, o, *wide != 0);
+}
+
+// Boxes of `high` rows of 64 zeros (from F_NO_ROW on), of an operand's memory.
+bool zeros_map(CUtensorMap* tm, const Operand& o, unsigned high) {
+    const int64_t dims[3] = {64, 1, 1}, strides[2] = {64, 64};
+    const unsigned box[3] = {64, high, 1};
+    return encode(tm, o.p, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // N's side, whose rows are the operand's.
@@ -1721,6 +1741,8 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
                        !boxes_map(&of.b64, *right[j], false)))
             return cudaErrorInvalidValue;
     }
+    for (int i = 0; a.rows && i < 4; ++i)
+        if (!zeros_map(&p.zeros[i], b.dy, 1u << i)) return cudaErrorInvalidValue;
     apply(p, b.cut_dw, base + b.part_at);
     return launch_op(DW, p, items, s);
 }

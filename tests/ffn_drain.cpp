@@ -43,65 +43,75 @@ struct Bar {
 };
 
 constexpr int STEPS = 60;
-constexpr int A_BYTES = 16384, BOX = 8192;
 
 struct Step {
-    bool tail, two;
+    uint32_t gap;
+    bool two;
 };
 struct Load {
     Bar* bar;
-    int bytes;
+    int64_t bytes;
 };
-
-// threads 0, 1: A and B of the leader; 2, 3: of the other CTA
-uint32_t part(int i, bool two) { return i % 2 == 0 ? A_BYTES : BOX * (two ? 2 : 1); }
 
 // bit 0: left with a load in flight; bit 1: a wait that would not end
 int plays(std::mt19937& rng, int rule) {
     const uint32_t stages = 5 + rng() % 2;
     std::vector<Step> steps(STEPS);
-    for (Step& s : steps) s = {rng() % 3 == 0, rng() % 3 != 0};
-    std::vector<Bar> full(stages), tail[2];
-    tail[0].resize(stages);
-    tail[1].resize(stages);
+    for (Step& s : steps) s = {rng() % 3 == 0 ? uint32_t(rng() % 16) : 0u, rng() % 3 != 0};
+    std::vector<Bar> full(stages), zero(stages), torn[2];
+    torn[0].resize(stages);
+    torn[1].resize(stages);
     std::vector<Load> flying;
-    Asked by[4] = {};
+    Asked by[4] = {}, zeros[2] = {};     // A and B of the leader, of the other CTA
     uint32_t products = 0;
-    const uint32_t moves = rng() % 600, lazy = rng() % 5;
+    const uint32_t moves = rng() % 700, lazy = rng() % 7;
     // (the parity of a step's phase goes by the steps of its kind that its stage had)
-    auto kind = [&](uint32_t step) {
+    auto parity = [&](uint32_t step) {
         uint32_t n = 0;
-        for (uint32_t i = step % stages; i < step; i += stages) n += steps[i].tail == steps[step].tail;
+        for (uint32_t i = step % stages; i < step; i += stages) n += !steps[i].gap == !steps[step].gap;
         return n & 1;
     };
+    auto parts = [&](Bar& bar, int64_t bytes) {
+        while (bytes) {
+            const int64_t n = bytes < 2048 ? bytes : 1 + int64_t(rng() % bytes);
+            flying.push_back({&bar, n});
+            bytes -= n;
+        }
+    };
     for (uint32_t m = 0; m < moves; ++m) {
-        const uint32_t what = rng() % 8;
+        const uint32_t what = rng() % 10;
+        if (what == lazy && rng() % 8) continue;
         if (what < 4) {
             Asked& me = by[what];
             const uint32_t i = me.steps, stage = i % stages, rank = what / 2;
-            if (i >= STEPS || (i >= stages && products < i - stages + 1) || (what == lazy && rng() % 8)) continue;
+            if (i >= STEPS || (i >= stages && products < i - stages + 1)) continue;
             const Step& s = steps[i];
-            Bar& bar = s.tail ? tail[rank][stage] : full[stage];
-            if (s.tail && what % 2 == 0) bar.arm(part(0, s.two) + part(1, s.two));
-            if (!s.tail && what == 0) bar.arm(2 * (part(0, s.two) + part(1, s.two)));
-            // the boxes, one by one
-            const int n = part(int(what), s.two) / BOX;
-            for (int k = 0; k < n; ++k) flying.push_back({&bar, BOX});
-            const uint32_t bit = 1u << stage;
-            me.tails = s.tail ? me.tails | bit : me.tails & ~bit;
-            me.two = s.two ? me.two | bit : me.two & ~bit;
-            (s.tail ? me.tail : me.full) ^= bit;
-            ++me.steps;
-        } else if (what < 7) {
+            Bar& bar = s.gap ? torn[rank][stage] : full[stage];
+            const int64_t cta = a_bytes() + b_bytes(s.two);
+            if (s.gap && what % 2 == 0) bar.arm(cta);
+            if (!s.gap && what == 0) bar.arm(2 * cta);
+            parts(bar, what % 2 ? b_bytes(s.two) : a_bytes());
+            ask(me, stage, s.gap, s.two);
+        } else if (what < 6) {
+            const uint32_t rank = what - 4, i = zeros[rank].steps, stage = i % stages;
+            if (i >= STEPS) continue;
+            const Step& s = steps[i];
+            // (the warp goes from torn step to torn step)
+            if (s.gap) {
+                if (by[2 * rank].steps <= i || by[2 * rank + 1].steps <= i || !torn[rank][stage].over(parity(i)))
+                    continue;
+                if (rank == 0) zero[stage].arm(2 * int64_t(zero_bytes(s.gap, s.two)));
+                parts(zero[stage], zero_bytes(s.gap, s.two));
+            }
+            ++zeros[rank].steps;
+        } else if (what < 9) {
             if (flying.empty() || rng() % 3 == 0) continue;
             const size_t at = rng() % flying.size();
             flying[at].bar->land(flying[at].bytes);
             flying.erase(flying.begin() + long(at));
         } else if (products < STEPS) {
-            const uint32_t stage = products % stages, parity = kind(products);
-            const bool there = steps[products].tail ? tail[0][stage].over(parity) && tail[1][stage].over(parity)
-                                                    : full[stage].over(parity);
-            if (there) ++products;
+            const uint32_t stage = products % stages;
+            if ((steps[products].gap ? zero : full)[stage].over(parity(products))) ++products;
         }
     }
     // The pair gives up here.
@@ -115,7 +125,7 @@ int plays(std::mt19937& rng, int rule) {
             for (int rank = 0; rank < 2; ++rank) {
                 const Asked& a = by[2 * rank];
                 if (a.steps <= s) continue;
-                if (a.tails >> s & 1) waits.push_back({&tail[rank][s], (a.tail >> s & 1) ^ 1});
+                if (a.gaps >> 4 * s & 15) waits.push_back({&torn[rank][s], (a.torn >> s & 1) ^ 1});
                 else if (rank == 0) waits.push_back({&full[s], (a.full >> s & 1) ^ 1});
             }
             continue;
@@ -126,9 +136,9 @@ int plays(std::mt19937& rng, int rule) {
             if (x.cancel) bar.land(x.cancel);
             waits.push_back({&bar, x.parity});
         };
-        for (int rank = 0; rank < 2; ++rank)
-            apply(tail[rank][s], settle(by + 2 * rank, 2, s, stages, true, part));
-        apply(full[s], settle(by, 4, s, stages, false, part));
+        for (int rank = 0; rank < 2; ++rank) apply(torn[rank][s], settle_torn(by + 2 * rank, s, stages));
+        apply(full[s], settle_full(by, s, stages));
+        apply(zero[s], settle_zeros(by, zeros, s, stages));
     }
     // The loads land in any order: when the last wait has ended, all have.
     while (true) {

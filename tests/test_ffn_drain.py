@@ -47,3 +47,15 @@ def test_the_pair_drains_after_all_roles_have_ended():
     # each loading thread leaves its counts, whatever ended its loop
     body = text[text.index("load_operand(const FfnLaunch& p"):text.index("drain_loads(uint8_t*")]
     assert "return" not in body and body.index("= asked;") > body.rindex("load_box(")
+
+
+def test_what_crosses_the_pair_is_released_to_it():
+    """A barrier of the other CTA is arrived at by the tensor cores, by loads, or
+    with the cluster's scope named; an arrival without one orders nothing
+    beyond its own CTA."""
+    text = open(os.path.join(CSRC, "gated_ffn.cu")).read() + open(os.path.join(CSRC, "tc_ptx.cuh")).read()
+    arrivals = [line for line in text.splitlines() if "mbarrier.arrive" in line and "shared::cluster" in line
+                and "tcgen05" not in line]
+    assert arrivals and all(".cluster.shared::cluster" in line for line in arrivals)
+    # the relaxed one only says that an accumulator has been read
+    assert text.count("mbar_arrive_cluster_relaxed(tempty_leader") == 1

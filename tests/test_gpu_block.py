@@ -864,3 +864,30 @@ def test_example_block(ns):
     block.muon.close()
     losses = ex.train(steps=3, tokens=128, hidden=64, inner=32, experts=4)
     assert len(losses) == 3 and all(math.isfinite(v) for v in losses)
+
+
+@pytest.mark.parametrize("hidden,inner", [(264, 96), (40, 200)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gated_ffn_every_last_step(ns, hidden, inner, dtype):
+    """Experts of 1 to 64 tokens and of 65 to 128, each beside one of a single
+    token whose rows are NaN: whatever a last step of 64 holds of them, their
+    gradients are those of their own tokens."""
+    counts = []
+    for n in range(1, 65):
+        counts += [n, 1, n + 64, 1]
+    offsets = bounds_of(counts)
+    t, experts = sum(counts), len(counts)
+    x, dy = rand(160, t, hidden, dtype=BF), rand(161, t, hidden, scale=0.1, dtype=BF)
+    w = [v[:1].expand(experts, -1, -1) for v in weights(162, hidden, inner, 1)]
+    _, saved = ns.gated_ffn(x, *w, offsets=offsets)
+    for e in range(1, experts, 2):
+        at = int(offsets[e])
+        x[at], dy[at] = math.nan, math.nan
+    got = ns.gated_ffn_backward(dy, x, saved, *w, offsets=offsets, dtype=dtype)
+    for e in range(0, experts, 2):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        s = [v[a:b] for v in saved]
+        want, bounds = O.ffn_grad(dy[a:b], x[a:b], *s, *[v[0] for v in w], None, "silu", dtype)
+        for i, what in ((1, "dw_gate"), (2, "dw_up"), (3, "dw_down")):
+            near(got[i][e], want[i], bounds[i], f"{what} of {b - a}")
+            assert bool(torch.isnan(got[i][e + 1]).any())
