@@ -458,6 +458,27 @@ __device__ __forceinline__ void team_sync(int team) {
 // to nearest, UP's write-out took 1550 cycles for 16 columns, not 600.)
 __device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
+// Phi(g) = erfc(-g / sqrt(2)) / 2, where e is exp(-g^2 / 2).  With z = |g| / sqrt(2),
+// erfc(z) / e is smooth: t P(t) of t = 1 / (1 + 0.43 z), where P, of degree 7, is
+// fitted to a relative error of 1e-7 over 0 <= z <= 10 (where e ends).  The lower
+// tail keeps all of its digits, of which (1 + erf) / 2 has lost 4 % at -5 and
+// everything below -5.6, and there is no second exponential: 128 experts with
+// GELU, kept and back, take 437 and 1027 us, by erff 436 and 1043, by erfcf 456
+// and 1085.
+__device__ __forceinline__ float normal_below(float g, float e) {
+    const float t = __fdividef(1.f, fmaf(0.30405592f, fabsf(g), 1.f));
+    float p = 0.036572915f;
+    p = fmaf(p, t, -0.154047829f);
+    p = fmaf(p, t, 0.189943648f);
+    p = fmaf(p, t, -0.0411521562f);
+    p = fmaf(p, t, 0.122540339f);
+    p = fmaf(p, t, 0.102736251f);
+    p = fmaf(p, t, 0.122146916f);
+    p = fmaf(p, t, 0.12125991f);
+    const float tail = p * t * e;
+    return g < 0.f ? tail : 1.f - tail;
+}
+
 // a = act(g) and d = act'(g), eight at a time.
 __device__ __forceinline__ void activate8(int act, const float (&g)[8], float (&a)[8], float (&d)[8]) {
     if (act == MUON_ACT_SILU) {
@@ -470,9 +491,9 @@ __device__ __forceinline__ void activate8(int act, const float (&g)[8], float (&
     } else if (act == MUON_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float c = fmaf(0.5f, erff(g[i] * 0.70710678f), 0.5f);
+            const float e = __expf(-0.5f * g[i] * g[i]), c = normal_below(g[i], e);
             a[i] = g[i] * c;
-            d[i] = fmaf(g[i] * 0.39894228f, __expf(-0.5f * g[i] * g[i]), c);
+            d[i] = fmaf(g[i] * 0.39894228f, e, c);
         }
     } else {
 #pragma unroll

@@ -891,3 +891,45 @@ def test_gated_ffn_every_last_step(ns, hidden, inner, dtype):
         for i, what in ((1, "dw_gate"), (2, "dw_up"), (3, "dw_down")):
             near(got[i][e], want[i], bounds[i], f"{what} of {b - a}")
             assert bool(torch.isnan(got[i][e + 1]).any())
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+def test_gated_ffn_small_activations_keep_their_digits(ns, name):
+    """Gates of -9 to -3, where act(g) falls to 1e-18 and less: h, dup and y are
+    off by a rounding of their own size, not of the gate's.
+
+    Relative errors of act(g), in units of 2^-23.  gelu: exp(-g^2 / 2), whose
+    argument is off by half a unit of itself, g^2 / 4, and which is itself off by 2 +
+    1.2 g^2 / 2; what it is multiplied by: the fit 1, the reciprocal 2, the sum and
+    the products 5.  The logistic function of z, for the others: the argument's
+    roundings 2 |z|, the exponential 2 + 1.2 |z|, the sum, the quotient and the
+    products 5."""
+    gates = -torch.linspace(3, 9, 256).to(BF)
+    n = gates.numel()
+    g64 = gates.to(D)
+    z = g64 if name == "silu" else 2 * math.sqrt(2 / math.pi) * (g64 + 0.044715 * g64 ** 3)
+    off = (0.85 * g64 * g64 + 10 if name == "gelu" else 3.2 * z.abs() + 7) * 2.0 ** -23
+    # (ndtr, even in 64 bits, is 0 below -8.3)
+    f64 = g64 / 2 * torch.special.erfc(-g64 / math.sqrt(2)) if name == "gelu" else O.act(name, g64)[0]
+    assert bool((f64.abs() > 1e-30).all())
+    bound = ((HALF[BF] + 1.01 * off) * f64.abs())[:, None].to(DEV)
+    want = f64[:, None].to(DEV)
+    # forward: rows whose gates are one of these, and whose u is 1
+    hidden = inner = 64
+    x = torch.zeros(n, hidden, dtype=BF, device=DEV)
+    x[:, 0], x[:, 1] = gates.to(DEV), 1.0
+    wg, wu = (torch.zeros(inner, hidden, dtype=BF, device=DEV) for _ in range(2))
+    wg[:, 0], wu[:, 1] = 1.0, 1.0
+    eye = torch.eye(hidden, dtype=BF, device=DEV)
+    y, saved = ns.gated_ffn(x, wg, wu, eye, activation=name)
+    assert torch.equal(saved[0], x[:, :1].expand(-1, inner)) and bool((saved[1] == 1).all())
+    near(y, want.expand(n, hidden), bound.expand(n, hidden), "y")
+    # backward, with dh = 1: dw_up = dup^T x and dw_down = dy^T h of one row each
+    one = torch.ones(1, hidden, dtype=BF, device=DEV)
+    wide = torch.ones(hidden, n, dtype=BF, device=DEV)
+    wide[1:] = 0
+    row = gates.to(DEV)[None]
+    dx, _, dup, ddown = ns.gated_ffn_backward(one, one, (row, torch.ones_like(row)), *[wide.t().contiguous()] * 2,
+                                              wide, activation=name, dtype=F32)
+    near(dup, want.expand(n, hidden), bound.expand(n, hidden), "dw_up")
+    near(ddown, want.t().expand(hidden, n), bound.t().expand(hidden, n), "dw_down")
