@@ -140,7 +140,7 @@ def gated_ffn_backward(dy: torch.Tensor, x: Union[torch.Tensor, Checkpoint8, Non
     grads: (dw_gate, dw_up, dw_down) to write, fp32 or bf16 tensors of the
     weights' shapes, e.g. those that a Muon set steps with (new ones of dtype
     otherwise); with accumulate the gradients are added to them.  Experts
-    without rows get zeros.  out: receives dx (it may not be dy)."""
+    without rows get zeros.  out: receives dx (it may not share memory with dy or x)."""
     rows, hidden, ld_dy, index = _rows("dy", dy)
     dev = dy.device
     act = _activation(activation)

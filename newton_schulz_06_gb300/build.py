@@ -36,7 +36,7 @@ SOURCES = ["ew_kernels.cu", "ns_kernels.cu", "ns2_kernels.cu", "muon_api.cpp",
 HEADERS = [os.path.join(CSRC, "muon_internal.h"), os.path.join(CSRC, "tc_ptx.cuh"),
            os.path.join(CSRC, "ops_internal.h"), os.path.join(CSRC, "tc_wait.cuh"),
            os.path.join(CSRC, "weight_grad_stages.h"), os.path.join(CSRC, "norm_ring.h"),
-           os.path.join(CSRC, "ffn_drain.h"),
+           os.path.join(CSRC, "ffn_drain.h"), os.path.join(CSRC, "overlap.h"),
            os.path.join(ROOT, "include", "muon.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -6,6 +6,7 @@
 #include <cstdio>
 
 #include "ops_internal.h"
+#include "overlap.h"
 
 using namespace muon;
 
@@ -155,6 +156,31 @@ int check_grads(const Err& err, const char* name, const void* p, int dtype, int6
     RETURN_IF(check_tensor(err, name, p, dtype, n, k, ld, false));
     if (experts > 1 && stride < (n > 1 ? (n - 1) * ld : 0) + k) return err.bad(name, "has too small a stride");
     return MUON_OK;
+}
+
+// Tensors of a call that may not share memory with what it still reads or with
+// each other.
+struct Named {
+    const char* name;
+    ops::Area area;
+    Named(const char* what, const void* p, int dtype, int64_t rows, int64_t cols, int64_t ld, int64_t matrices = 1,
+          int64_t stride = 0)
+        : name(what), area(p, cols * (dtype == MUON_F32 ? 4 : 2)) {
+        const int size = dtype == MUON_F32 ? 4 : 2;
+        area.axis(rows, ld * size).axis(matrices, stride * size);
+        there = p && rows > 0;
+    }
+    bool there;
+};
+int check_apart(const Err& err, const Named& a, const Named& b) {
+    if (a.there && b.there && ops::share(a.area, b.area))
+        return err.fail(MUON_ERR_INVALID_ARG, "%s and %s share memory", a.name, b.name);
+    return MUON_OK;
+}
+// The same, but for tensors of one address and one layout.
+int check_apart_or_same(const Err& err, const Named& a, const Named& b) {
+    const bool same = a.area.p == b.area.p && (a.area.axes == 0 || b.area.axes == 0 || a.area.stride[0] == b.area.stride[0]);
+    return same ? MUON_OK : check_apart(err, a, b);
 }
 
 int check_forward(const Err& err, const muon_gated_ffn_args* a) {
@@ -373,6 +399,21 @@ MUON_API int muon_gated_ffn(const muon_gated_ffn_args* a, void* ws, size_t bytes
         RETURN_IF(check_tensor(err, "up", a->up, MUON_BF16, a->rows, a->inner, a->ld_kept, false));
     }
     RETURN_IF(check_workspace(err, ws, bytes, ops::gated_ffn_workspace(*a)));
+    const Named x("x", a->x, MUON_BF16, a->rows, a->hidden, a->ld_x);
+    const Named y("y", a->y, MUON_BF16, a->rows, a->hidden, a->ld_y);
+    const Named gate("gate", a->gate, MUON_BF16, a->rows, a->inner, a->ld_kept);
+    const Named up("up", a->up, MUON_BF16, a->rows, a->inner, a->ld_kept);
+    const Named weights[3] = {
+        {"w_gate", a->w_gate, MUON_BF16, a->inner, a->hidden, a->ld_gate, a->experts, a->stride_gate},
+        {"w_up", a->w_up, MUON_BF16, a->inner, a->hidden, a->ld_up, a->experts, a->stride_up},
+        {"w_down", a->w_down, MUON_BF16, a->hidden, a->inner, a->ld_down, a->experts, a->stride_down}};
+    for (const Named* out : {&y, &gate, &up})
+        for (const Named& w : weights) RETURN_IF(check_apart(err, *out, w));
+    RETURN_IF(check_apart(err, gate, up));
+    for (const Named* kept : {&gate, &up}) {
+        RETURN_IF(check_apart(err, *kept, x));
+        RETURN_IF(check_apart(err, *kept, y));
+    }
     return err.done(ops::launch_gated_ffn(*a, ws, static_cast<cudaStream_t>(cuda_stream)));
 }
 
@@ -413,6 +454,43 @@ MUON_API int muon_gated_ffn_grad(const muon_gated_ffn_grad_args* a, void* ws, si
     for (const void* m : made)
         if (m) RETURN_IF(check_tensor(err, "dgate, dup or h", m, MUON_BF16, a->rows, a->inner, a->ld_d, false));
     RETURN_IF(check_workspace(err, ws, bytes, ops::gated_ffn_grad_workspace(*a)));
+    const int g = a->g_dtype;
+    const Named dy("dy", a->dy, MUON_BF16, a->rows, a->hidden, a->ld_dy);
+    const Named x("x", x_grads ? a->x : nullptr, MUON_BF16, a->rows, a->hidden, a->ld_x);
+    const Named dx("dx", a->dx, MUON_BF16, a->rows, a->hidden, a->ld_dx);
+    const Named kept[2] = {{"gate", a->gate, MUON_BF16, a->rows, a->inner, a->ld_kept},
+                           {"up", a->up, MUON_BF16, a->rows, a->inner, a->ld_kept}};
+    const Named on_way[3] = {{"dgate", a->dgate, MUON_BF16, a->rows, a->inner, a->ld_d},
+                             {"dup", a->dup, MUON_BF16, a->rows, a->inner, a->ld_d},
+                             {"h", a->h, MUON_BF16, a->rows, a->inner, a->ld_d}};
+    const Named weights[3] = {
+        {"w_gate", a->dx ? a->w_gate : nullptr, MUON_BF16, a->inner, a->hidden, a->ld_gate, a->experts, a->stride_gate},
+        {"w_up", a->dx ? a->w_up : nullptr, MUON_BF16, a->inner, a->hidden, a->ld_up, a->experts, a->stride_up},
+        {"w_down", a->w_down, MUON_BF16, a->hidden, a->inner, a->ld_down, a->experts, a->stride_down}};
+    const Named grads[3] = {
+        {"dw_gate", a->dw_gate, g, a->inner, a->hidden, a->ld_dw_gate, a->experts, a->stride_dw_gate},
+        {"dw_up", a->dw_up, g, a->inner, a->hidden, a->ld_dw_up, a->experts, a->stride_dw_up},
+        {"dw_down", a->dw_down, g, a->hidden, a->inner, a->ld_dw_down, a->experts, a->stride_dw_down}};
+    for (int i = 0; i < 3; ++i) {
+        // what DHIDDEN writes, each value in the place of its g or u at most
+        RETURN_IF(check_apart(err, on_way[i], dy));
+        for (const Named& k : kept) RETURN_IF(check_apart_or_same(err, on_way[i], k));
+        for (const Named& w : weights) RETURN_IF(check_apart(err, on_way[i], w));
+        RETURN_IF(check_apart(err, on_way[i], x));
+        RETURN_IF(check_apart(err, on_way[i], dx));
+        for (int j = 0; j < 3; ++j) {
+            if (j > i) RETURN_IF(check_apart(err, on_way[i], on_way[j]));
+            RETURN_IF(check_apart(err, on_way[i], grads[j]));
+        }
+        // what the weights' gradients read
+        if (a->dw_down) RETURN_IF(check_apart(err, grads[i], dy));
+        RETURN_IF(check_apart(err, grads[i], x));
+        RETURN_IF(check_apart(err, grads[i], dx));
+        for (int j = i + 1; j < 3; ++j) RETURN_IF(check_apart(err, grads[i], grads[j]));
+    }
+    for (int i = 0; i < 2; ++i) RETURN_IF(check_apart(err, dx, weights[i]));
+    if (a->dw_down) RETURN_IF(check_apart(err, dx, dy));
+    RETURN_IF(check_apart(err, dx, x));
     return err.done(ops::launch_gated_ffn_grad(*a, ws, static_cast<cudaStream_t>(cuda_stream)));
 }
 
