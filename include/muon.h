@@ -637,7 +637,8 @@ MUON_API int muon_gated_ffn_grad(const muon_gated_ffn_grad_args* args, void* wor
  * values of a head past 2 * pairs are copied (they stay where y is x).
  * q, k: tensors of batch x seq x heads x head values of x_dtype, each value
  * 1 element and batches, positions and heads the given strides apart; a
- * tensor of 0 heads is left out.  y may be x, with its strides.
+ * tensor of 0 heads is left out.  y may be x, with its strides; else no result may
+ * share memory with another, with an input or with itself.
  * positions: batch rows (stride_positions apart, 0 for one row) of seq values, 32-
  * or 64-bit (positions_64), in device memory; NULL: 0, 1, ... seq - 1.  offset
  * is added to each.  turns: host memory, read during the call: every pair's

@@ -324,7 +324,8 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], plan: RotaryPlan, *,
 
     q, k: seq x heads x head, or batch x seq x heads x head, fp32 or bf16; any
     strides but that a head is dense, so that views (a transposed batch, the
-    last values of longer heads) do.  out_q, out_k may be q and k themselves.
+    last values of longer heads) do.  out_q, out_k may be q and k themselves, and
+    otherwise share no memory with either.
     positions: int32 or int64, seq or batch x seq; None counts from 0.  offset
     is added to each."""
     return _turn(q, k, plan, positions, offset, out_q, out_k, False)

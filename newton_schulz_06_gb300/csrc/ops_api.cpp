@@ -210,6 +210,38 @@ int check_rotary_tensor(const Err& err, const char* name, const muon_rotary_tens
     return MUON_OK;
 }
 
+ops::Area rotary_area(const muon_rotary_args& a, const muon_rotary_tensor& t, bool written, int64_t values) {
+    const int64_t size = a.x_dtype == MUON_F32 ? 4 : 2;
+    ops::Area area(written ? t.y : t.x, values * size);
+    area.axis(t.heads, (written ? t.y_head : t.x_head) * size);
+    area.axis(a.seq, (written ? t.y_seq : t.x_seq) * size);
+    area.axis(a.batch, (written ? t.y_batch : t.x_batch) * size);
+    return area;
+}
+// Blocks read and write in any order: what one writes no other may read or
+// write.
+int check_rotary_areas(const Err& err, const muon_rotary_args& a) {
+    const muon_rotary_tensor* const t[2] = {&a.q, &a.k};
+    const char* const name[2] = {"q", "k"};
+    // what follows a head's pairs is copied for both tensors or stays for both
+    bool copy = false;
+    for (const muon_rotary_tensor* x : t) copy = copy || (x->heads && x->x != x->y);
+    const int64_t values = copy ? a.head : 2 * a.pairs;
+    for (int i = 0; i < 2; ++i) {
+        if (!t[i]->heads) continue;
+        const ops::Area y = rotary_area(a, *t[i], true, values);
+        if (y.folded()) return err.bad(name[i], "is written to places that share memory");
+        if (t[i]->x != t[i]->y && ops::share(y, rotary_area(a, *t[i], false, values)))
+            return err.bad(name[i], "is written to memory that it shares with its result");
+        const muon_rotary_tensor& other = *t[1 - i];
+        if (!other.heads) continue;
+        if (ops::share(y, rotary_area(a, other, false, values)) ||
+            (i == 0 && ops::share(y, rotary_area(a, other, true, values))))
+            return err.bad(name[i], "is written to memory that it shares with the other tensor");
+    }
+    return MUON_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -515,6 +547,7 @@ MUON_API int muon_rotary(const muon_rotary_args* a, void* cuda_stream, char* err
     }
     if ((a->q.heads + a->k.heads) * a->head > (int64_t(1) << 28)) return err.bad("heads out of range");
     if (a->batch * a->seq == 0 || a->q.heads + a->k.heads == 0) return MUON_OK;
+    RETURN_IF(check_rotary_areas(err, *a));
     return err.done(ops::launch_rotary(*a, static_cast<cudaStream_t>(cuda_stream)));
 }
 

@@ -78,6 +78,28 @@ def test_gated_ffn_grad_refuses_what_shares_memory(L, kw, names):
     assert "share memory" in msg and all(n in msg.split() for n in names.split()), msg
 
 
+TURNS = (ctypes.c_uint64 * 8)()
+# 2 batches of 3 positions of 2 heads of 16 bf16 values, dense: 384 bytes
+ROTARY = dict(turns=ctypes.addressof(TURNS), batch=2, seq=3, head=16, pairs=8, x_dtype=1, scale=1.0)
+HEADS = dict(heads=2, x_batch=96, x_seq=32, x_head=16, y_batch=96, y_seq=32, y_head=16)
+
+
+@pytest.mark.parametrize("q,k,word", [
+    (dict(y=1 * M + 32), {}, "q"), (dict(y=1 * M - 382), {}, "q"), ({}, dict(y=2 * M + 2), "k"),
+    (dict(y=2 * M), {}, "q"), ({}, dict(y=1 * M + 352), "k"), (dict(y=4 * M + 382), {}, "q"),
+    # the same tensor for both, in place
+    (dict(y=1 * M), dict(x=1 * M, y=1 * M), "q"),
+    # heads, positions and batches over one another
+    (dict(y_head=15), {}, "q"), ({}, dict(y_seq=31), "k"), ({}, dict(y_batch=95), "k"), (dict(y_seq=16), {}, "q"),
+    # columns of one row that have a head in common
+    (dict(x_seq=64, x_batch=192, y=1 * M + 32, y_seq=64, y_batch=192), {}, "q")])
+def test_rotary_refuses_what_shares_memory(L, q, k, word):
+    a = {**ROTARY, "q": L.RotaryTensor(**{**HEADS, "x": 1 * M, "y": 3 * M, **q}),
+         "k": L.RotaryTensor(**{**HEADS, "x": 2 * M, "y": 4 * M, **k})}
+    msg = refused(L, "muon_rotary", L.RotaryArgs, a)
+    assert msg.startswith(word + " is written to") and "share" in msg, msg
+
+
 # ------------------------------------------------------------- on the GPU
 
 @pytest.fixture(scope="module")
@@ -143,3 +165,27 @@ def test_gated_ffn_refuses_shifted_rows(ns):
     rows = rand(6, t + 1, hidden)
     want = ns.gated_ffn(rows[:-1].clone(), *w, keep=False)[0]
     assert torch.equal(ns.gated_ffn(rows[:-1], *w, keep=False, out=rows[1:])[0], want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_takes_views_that_interleave(ns, layout):
+    """Queries and keys beside each other in one row, in place and to another
+    part of it; heads of which only some values turn."""
+    plan = ns.RotaryPlan(32, layout=layout)
+    row = rand(1, 2, 21, 6 + 2 + 6, 48)
+    q, k, other = row.split([6, 2, 6], 2)
+    want_q, want_k = ns.rotary(q.clone(), k.clone(), plan, offset=5)
+    first = row.clone()
+    a, b, c = first.split([6, 2, 6], 2)
+    ns.rotary(a, b, plan, offset=5, out_q=c, out_k=b)
+    assert torch.equal(c, want_q) and torch.equal(b, want_k) and torch.equal(a, q)
+    ns.rotary(a, None, plan, offset=5, out_q=a)
+    assert torch.equal(a, want_q)
+    # batch x heads x seq x head, written to the other order
+    turned = torch.zeros(2, 6, 21, 48, dtype=BF, device="cuda").transpose(1, 2)
+    assert torch.equal(ns.rotary(q, None, plan, offset=5, out_q=turned)[0], want_q)
+    with pytest.raises(ns.MuonError, match="shares"):
+        ns.rotary(row[:, :, :6], None, plan, out_q=row[:, :, 1:7])
+    with pytest.raises(ns.MuonError, match="shares"):
+        ns.rotary(q, k, plan, out_q=row[:, :, 4:10])
