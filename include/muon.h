@@ -696,7 +696,7 @@ MUON_API int muon_rotary_frequencies(int64_t pairs, double base, int scaling, do
  * counter (optional): one value in device memory, read when the kernel runs,
  * so that a captured graph drops others in every replay.  A dropped element
  * is 0 whatever x holds.  x, residual, y: rows x cols of x_dtype; y may be x or
- * the residual.  0 <= rows < 2^31, 1 <= cols <= 1048576, 0 <= p <= 1. */
+ * the residual, with its leading dimension, and else shares no memory with them.  0 <= rows < 2^31, 1 <= cols <= 1048576, 0 <= p <= 1. */
 typedef struct {
     const void*    x;
     const void*    residual;

@@ -370,7 +370,8 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, *,
     alone, so that no mask is kept: :func:`dropout_backward` is given the same
     two.  Calls of one seed need offsets of their own.  p is taken to the
     nearest 2^-16.  counter: one int64 value on the device that is added to the
-    offset when the kernel runs (captured graphs).  out may be x or residual."""
+    offset when the kernel runs (captured graphs).  out may be x or residual, and
+    otherwise shares no memory with them."""
     return _drop("x", x, p, seed, offset, counter, residual, out)
 
 

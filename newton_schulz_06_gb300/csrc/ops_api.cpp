@@ -602,6 +602,9 @@ MUON_API int muon_dropout(const muon_dropout_args* a, void* cuda_stream, char* e
     if (a->rows > 1 && a->residual == a->y && a->ld_r != a->ld_y)
         return err.bad("y is residual with another leading dimension");
     if (a->rows == 0) return MUON_OK;
+    const Named y("y", a->y, a->x_dtype, a->rows, a->cols, a->ld_y);
+    RETURN_IF(check_apart_or_same(err, y, Named("x", a->x, a->x_dtype, a->rows, a->cols, a->ld_x)));
+    RETURN_IF(check_apart_or_same(err, y, Named("residual", a->residual, a->x_dtype, a->rows, a->cols, a->ld_r)));
     return err.done(ops::launch_dropout(*a, static_cast<cudaStream_t>(cuda_stream)));
 }
 

@@ -100,6 +100,18 @@ def test_rotary_refuses_what_shares_memory(L, q, k, word):
     assert msg.startswith(word + " is written to") and "share" in msg, msg
 
 
+DROP = dict(x=1 * M, residual=2 * M, y=3 * M, rows=4, cols=64, ld_x=64, ld_r=64, ld_y=64, p=0.1, x_dtype=1)
+
+
+@pytest.mark.parametrize("kw,names", [
+    (dict(y=1 * M + 2), "y x"), (dict(y=1 * M - 510), "y x"), (dict(y=2 * M + 128), "y residual"),
+    (dict(y=1 * M, residual=1 * M + 128), "y residual"), (dict(y=1 * M + 4, x_dtype=0), "y x"),
+    (dict(y=1 * M + 100, ld_x=100, ld_y=100), "y x")])
+def test_dropout_refuses_what_shares_memory(L, kw, names):
+    msg = refused(L, "muon_dropout", L.DropoutArgs, DROP, **kw)
+    assert "share memory" in msg and all(n in msg.split() for n in names.split()), msg
+
+
 # ------------------------------------------------------------- on the GPU
 
 @pytest.fixture(scope="module")
@@ -189,3 +201,20 @@ def test_rotary_takes_views_that_interleave(ns, layout):
         ns.rotary(row[:, :, :6], None, plan, out_q=row[:, :, 1:7])
     with pytest.raises(ns.MuonError, match="shares"):
         ns.rotary(q, k, plan, out_q=row[:, :, 4:10])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols", [64, 33])
+def test_dropout_takes_views_that_interleave(ns, cols):
+    buf = rand(1, 40, 3 * cols)
+    x, r, out = buf.split(cols, 1)
+    want = ns.dropout(x.clone(), 0.3, 1, 2, residual=r.clone())
+    assert torch.equal(ns.dropout(x, 0.3, 1, 2, residual=r, out=out), want)
+    assert torch.equal(ns.dropout(x, 0.3, 1, 2, residual=r, out=r), want)
+    row = buf[:1]
+    assert torch.equal(ns.dropout(row, 0.0, 1, 2, out=row), row)
+    for a, b in ((buf[:-1], buf[1:]), (buf[:, 1:], buf[:, :-1])):
+        with pytest.raises(ns.MuonError, match="share memory"):
+            ns.dropout(a, 0.3, 1, 2, out=b)
+        with pytest.raises(ns.MuonError, match="share memory"):
+            ns.dropout(torch.zeros_like(a), 0.3, 1, 2, residual=a, out=b)
