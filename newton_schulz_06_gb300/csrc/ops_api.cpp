@@ -179,7 +179,8 @@ int check_apart(const Err& err, const Named& a, const Named& b) {
 }
 // The same, but for tensors of one address and one layout.
 int check_apart_or_same(const Err& err, const Named& a, const Named& b) {
-    const bool same = a.area.p == b.area.p && (a.area.axes == 0 || b.area.axes == 0 || a.area.stride[0] == b.area.stride[0]);
+    const bool same = a.area.p == b.area.p && a.area.axes == b.area.axes &&
+                      (a.area.axes == 0 || a.area.stride[0] == b.area.stride[0]);
     return same ? MUON_OK : check_apart(err, a, b);
 }
 

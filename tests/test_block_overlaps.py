@@ -70,7 +70,7 @@ GRAD = dict(dy=1 * M, x=2 * M, gate=3 * M, up=4 * M, w_gate=5 * M, w_up=6 * M, w
     (dict(dw_up=9 * M + 4094), "dw_gate dw_up"), (dict(dw_down=10 * M), "dw_up dw_down"),
     (dict(dgate=1 * M), "dgate dy"), (dict(dup=3 * M + 2), "dup gate"), (dict(h=7 * M), "h w_down"),
     (dict(dgate=12 * M, dup=12 * M), "dgate dup"), (dict(dgate=8 * M), "dgate dx"), (dict(h=9 * M), "h dw_gate"),
-    (dict(dgate=2 * M), "dgate x"), (dict(dup=5 * M), "dup w_gate"),
+    (dict(dgate=3 * M, ld_kept=0), "dgate gate"), (dict(dgate=2 * M), "dgate x"), (dict(dup=5 * M), "dup w_gate"),
     (dict(offsets=64 * M, experts=3, stride_gate=2048, stride_up=2048, stride_down=2048, stride_dw_gate=4096,
           stride_dw_up=4096, stride_dw_down=4096, dw_gate=9 * M, dw_up=9 * M + 4094), "dw_gate dw_up")])
 def test_gated_ffn_grad_refuses_what_shares_memory(L, kw, names):
