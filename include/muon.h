@@ -641,7 +641,7 @@ MUON_API int muon_gated_ffn_grad(const muon_gated_ffn_grad_args* args, void* wor
  * share memory with another, with an input or with itself.
  * positions: batch rows (stride_positions apart, 0 for one row) of seq values, 32-
  * or 64-bit (positions_64), in device memory; NULL: 0, 1, ... seq - 1.  offset
- * is added to each.  turns: host memory, read during the call: every pair's
+ * is added to each, modulo 2^64.  turns: host memory, read during the call: every pair's
  * frequency in turns per position times 2^64 (muon_rotary_frequencies), so
  * that position * turns modulo 2^64 is the angle without whole turns: good to
  * 2^-53 of itself, whole turns included, and to 2^-64 turns a position.

@@ -287,6 +287,8 @@ def _turn(q, k, plan: RotaryPlan, positions, offset: int, out_q, out_k, inverse:
     shape, strides = _heads("q", q, index)
     batch, seq, _, head = shape
     dtype = _dtype("q", q)
+    if not -(1 << 63) <= offset < 1 << 63:
+        raise ValueError(f"offset must be a 64-bit whole number, got {offset}")
     if plan.dim > head:
         raise ValueError(f"heads of {head} values are shorter than the plan's {plan.dim}")
     first, out_q = _turned("q", q, out_q, shape, strides, index)

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(R_THREADS) rotary_kernel(const __grid_constant
             at = p.wide_pos ? static_cast<const int64_t*>(p.positions)[k]
                             : static_cast<const int32_t*>(p.positions)[k];
         }
-        const uint64_t angle = static_cast<uint64_t>(at + p.offset) * p.turns[i];
+        const uint64_t angle = (static_cast<uint64_t>(at) + static_cast<uint64_t>(p.offset)) * p.turns[i];
         // half turns in -1 .. 1
         float c, n;
         sincospif(__ll2float_rn(static_cast<int64_t>(angle)) * 1.0842021724855044e-19f, &n, &c);

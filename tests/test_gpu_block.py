@@ -933,3 +933,18 @@ def test_gated_ffn_small_activations_keep_their_digits(ns, name):
                                               wide, activation=name, dtype=F32)
     near(dup, want.expand(n, hidden), bound.expand(n, hidden), "dw_up")
     near(ddown, want.t().expand(hidden, n), bound.t().expand(hidden, n), "dw_down")
+
+
+def test_rotary_offset_of_64_bits(ns):
+    """Position and offset add up modulo 2^64, and an offset past 64 bits is
+    refused."""
+    plan, q = ns.RotaryPlan(32), rand(170, 3, 2, 32)
+    top = torch.full((3,), 2 ** 63 - 1, dtype=torch.int64, device=DEV)
+    low = torch.full((3,), -2 ** 63, dtype=torch.int64, device=DEV)
+    assert torch.equal(ns.rotary(q, None, plan, positions=top, offset=1)[0], ns.rotary(q, None, plan, positions=low)[0])
+    back = torch.zeros(3, dtype=torch.int64, device=DEV)
+    assert torch.equal(ns.rotary(q, None, plan, positions=low, offset=-2 ** 63)[0],
+                       ns.rotary(q, None, plan, positions=back)[0])
+    for offset in (2 ** 63, -2 ** 63 - 1, 10 ** 30):
+        with pytest.raises(ValueError, match="offset"):
+            ns.rotary(q, None, plan, offset=offset)
