@@ -721,6 +721,10 @@ MUON_API int muon_ops_sync(void* cuda_stream, char* err, size_t err_len);
  * muon_ops_sync then reports as MUON_ERR_TIMEOUT. */
 MUON_API int muon_debug_ops_wait_timeout(int limit_ms, void* cuda_stream, char* err,
                                          size_t err_len);
+/* The same for the gated feed-forward kernels, which have an error word of
+ * their own. */
+MUON_API int muon_debug_ffn_wait_timeout(int limit_ms, void* cuda_stream, char* err,
+                                         size_t err_len);
 
 #ifdef __cplusplus
 }

@@ -48,7 +48,8 @@ EXPORTS = ("muon_create", "muon_set_stream", "muon_register_params",
            "muon_gated_ffn_workspace", "muon_gated_ffn",
            "muon_gated_ffn_grad_workspace", "muon_gated_ffn_grad",
            "muon_rotary", "muon_rotary_frequencies", "muon_dropout",
-           "muon_ops_sync", "muon_debug_ops_wait_timeout")
+           "muon_ops_sync", "muon_debug_ops_wait_timeout",
+           "muon_debug_ffn_wait_timeout")
 
 
 class MuonParam(ctypes.Structure):
@@ -210,6 +211,7 @@ def lib() -> ctypes.CDLL:
         "muon_dropout": [vp, vp, vp, sz],
         "muon_ops_sync": [vp, vp, sz],
         "muon_debug_ops_wait_timeout": [i32, vp, vp, sz],
+        "muon_debug_ffn_wait_timeout": [i32, vp, vp, sz],
     }
     for name, args in sig.items():
         fn = getattr(L, name)

@@ -1353,6 +1353,18 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// A wait that nothing satisfies, as the roles wait.
+__global__ void __launch_bounds__(32) ffn_timeout_kernel(unsigned long long limit_ns) {
+    __shared__ uint64_t bar;
+    __shared__ volatile int abort_flag;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bar), 1);
+        abort_flag = 0;
+    }
+    __syncthreads();
+    wait_soon(smem_u32(&bar), 0, &abort_flag, &g_ffn_err, limit_ns);
+}
+
 // ------------------------------------------------------------------- host
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -1766,6 +1778,10 @@ cudaError_t launch_gated_ffn_grad(const muon_gated_ffn_grad_args& a, void* ws, c
         if (!zeros_map(&p.zeros[i], b.dy, 1u << i)) return cudaErrorInvalidValue;
     apply(p, b.cut_dw, base + b.part_at);
     return launch_op(DW, p, items, s);
+}
+
+cudaError_t launch_ffn_timeout(unsigned long long limit_ns, cudaStream_t s) {
+    return launch_kernel(ffn_timeout_kernel, dim3(1), dim3(32), 0, s, limit_ns);
 }
 
 cudaError_t ffn_error_word(void** word) { return cudaGetSymbolAddress(word, g_ffn_err); }

@@ -627,4 +627,12 @@ MUON_API int muon_debug_ops_wait_timeout(int limit_ms, void* cuda_stream, char* 
                                              static_cast<cudaStream_t>(cuda_stream)));
 }
 
+MUON_API int muon_debug_ffn_wait_timeout(int limit_ms, void* cuda_stream, char* err_buf,
+                                         size_t err_len) {
+    const Err err{err_buf, err_len};
+    if (limit_ms < 1 || limit_ms > 10000) return err.bad("need 1 <= limit_ms <= 10000");
+    return err.done(ops::launch_ffn_timeout(static_cast<unsigned long long>(limit_ms) * 1000000ull,
+                                            static_cast<cudaStream_t>(cuda_stream)));
+}
+
 }  // extern "C"

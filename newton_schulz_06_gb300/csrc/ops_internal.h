@@ -37,8 +37,9 @@ cudaError_t ops_status(cudaStream_t s, int* code);
 // Device addresses of the layer norm's and the feed-forward block's error words.
 cudaError_t norm_error_word(void** word);
 cudaError_t ffn_error_word(void** word);
-// A kernel whose wait nothing satisfies: it runs out after the limit.
+// Kernels whose wait nothing satisfies: it runs out after the limit.
 cudaError_t launch_ring_timeout(unsigned long long limit_ns, cudaStream_t s);
+cudaError_t launch_ffn_timeout(unsigned long long limit_ns, cudaStream_t s);
 // Limit of the kernels' waits (MUON_WAIT_LIMIT_MS, else two seconds).
 unsigned long long wait_limit_ns();
 

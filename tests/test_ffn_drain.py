@@ -5,6 +5,7 @@ import os
 import subprocess
 
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "newton_schulz_06_gb300", "csrc")
@@ -59,3 +60,27 @@ def test_what_crosses_the_pair_is_released_to_it():
     assert arrivals and all(".cluster.shared::cluster" in line for line in arrivals)
     # the relaxed one only says that an accumulator has been read
     assert text.count("mbar_arrive_cluster_relaxed(tempty_leader") == 1
+
+
+@pytest.mark.gpu
+def test_a_wait_that_runs_out_is_reported_once():
+    import ctypes
+
+    import newton_schulz_06_gb300 as ns
+    from newton_schulz_06_gb300 import _lib
+    buf = ctypes.create_string_buffer(128)
+    stream = torch.cuda.current_stream().cuda_stream
+    out_of_time = _lib.lib().muon_debug_ffn_wait_timeout
+    assert out_of_time(0, stream, buf, 128) == _lib.MUON_ERR_INVALID_ARG
+    ns.ops_sync()
+    assert out_of_time(100, stream, buf, 128) == 0
+    with pytest.raises(ns.MuonError) as e:
+        ns.ops_sync()
+    assert e.value.code == _lib.MUON_ERR_TIMEOUT
+    # the context is as usable as before, and the word has been cleared
+    ns.ops_sync()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, *w = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((300, 64), (96, 64), (96, 64), (64, 96)))
+    y, saved = ns.gated_ffn(x, *w)
+    ns.gated_ffn_backward(y, x, saved, *w)
+    ns.ops_sync()
