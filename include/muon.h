@@ -558,9 +558,10 @@ MUON_API int muon_route_grad(const muon_route_grad_args* args, void* cuda_stream
  * that one); rows of no expert are not written.
  * offsets = NULL: experts = 1, all rows.  y may be x or share memory with it; else no
  * output may share memory with another or with what is read (MUON_ERR_INVALID_ARG;
- * views that interleave, such as columns of one matrix, may).  The tensor cores cut their running sums off at the last place
- * (16384 terms of one sign lose 9e-5 of their sum at most); long sums of few rows are
- * added up in parts, so that a row's last bits may depend on the number of rows.
+ * views that interleave, such as columns of one matrix, may).  The tensor cores cut
+ * their running sums off at the last place (16384 terms of one sign lose 9e-5 of their
+ * sum at most, and others in proportion); long sums of few rows are added up in parts,
+ * so that a row's last bits may depend on the number of rows.
  * A stride of matrices may be 0 (one for all).  Operands whose rows do not all
  * start on 16 bytes are copied to the workspace first.  0 <= rows < 2^31 - 256,
  * 1 <= hidden, inner <= 262144, 1 <= experts <= 1024. */
@@ -597,7 +598,9 @@ MUON_API int muon_gated_ffn(const muon_gated_ffn_args* args, void* workspace, si
  * as their weights (leading dimensions ld_dgate ..., strides stride_dgate ...);
  * with accumulate they are added to what is there, in fp32, and rounded once.
  * Their sums over tokens are added up to nearest every 8192 tokens (bf16) or
- * 4096 (fp32) at most.  An expert without rows has zero gradients.  No output
+ * 4096 (fp32) at most; dh's over hidden and dx's over 2 * inner terms are cut off as
+ * the forward pass's are (dx of the widest inner, 262144: 2.9e-3 of a sum of one
+ * sign at most).  An expert without rows has zero gradients.  No output
  * may share memory with another or with what is read while or after it is
  * written: dx with dy only without dw_down, and with x only without dw_gate and
  * dw_up; dgate, dup and h may be gate or up, with their leading dimension.

@@ -948,3 +948,46 @@ def test_rotary_offset_of_64_bits(ns):
     for offset in (2 ** 63, -2 ** 63 - 1, 10 ** 30):
         with pytest.raises(ValueError, match="offset"):
             ns.rotary(q, None, plan, offset=offset)
+
+
+def test_gated_ffn_long_sums_added_to_bf16(ns):
+    """bf16 gradients over several chunks, added to what is there, of rows that
+    do not lie on 16 bytes: 8192 tokens in one running sum at most (512 products
+    of two cuts of 2^-23), the chunks' sums and the old value added up in fp32,
+    one rounding to bf16."""
+    size, tokens = 257, 30000
+    dy, x, saved, up, eye = one_sign(tokens, size, 5)
+    # (the tiles of an expert are not split into parts, whose sums end before a chunk does)
+    before = [rand(180 + i, 1, size, size).abs().to(BF) * 4096 for i in range(3)]
+    grads = [b.clone() for b in before]
+    ns.gated_ffn_backward(dy, x, saved, *[eye[None]] * 3, grads=grads, accumulate=True, offsets=bounds_of([tokens]))
+    bound = 512 * 2 * 2.0 ** -23 + 40 * U32
+    for got, want, old, name in zip(grads, one_sign_grads(dy, x, up, 0, tokens), before, ("gate", "up", "down")):
+        total = want + old[0].to(D)
+        near(got[0], total, bound * want + 4 * U32 * total + HALF[BF] * (1 + bound) * total, f"dw_{name}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gated_ffn_chunks_inside_parts(ns, dtype):
+    """Few tiles and many tokens: the sums are cut into parts (here 25), and a
+    part into chunks, of 10000 tokens two of bf16 (or three of fp32) results."""
+    size, tokens = 256, 250000
+    dy, x, saved, up, eye = one_sign(tokens, size, 6)
+    _, *grads = ns.gated_ffn_backward(dy, x, saved, eye, eye, eye, dtype=dtype)
+    bound = (512 if dtype == BF else 256) * 2 * 2.0 ** -23 + 100 * U32
+    for got, want, name in zip(grads, one_sign_grads(dy, x, up, 0, tokens), ("gate", "up", "down")):
+        near(got, want, (bound + HALF[dtype] * (1 + bound)) * want, f"dw_{name}")
+
+
+@pytest.mark.parametrize("tokens,hidden,inner", [(300, 264, 20000), (2500, 20000, 128)])
+def test_gated_ffn_long_sums_between_the_products(ns, tokens, hidden, inner):
+    """Sums of one sign over a wide inner (y, and dx, whose sum is twice as
+    long) or a wide hidden (g, u and dhidden): each product of 16 terms may cut
+    twice 2^-23 of the running sum (the oracle's sums())."""
+    g = torch.Generator().manual_seed(190)
+    x, dy = (torch.rand(tokens, hidden, generator=g).to(BF).to(DEV) for _ in range(2))
+    w = [(torch.rand(*s, generator=g) * 2 / s[1]).to(BF).to(DEV) for s in ((inner, hidden), (inner, hidden), (hidden, inner))]
+    y, saved = ns.gated_ffn(x, *w)
+    check_forward(x, w, y, saved)
+    check_backward(dy, x, saved, w, ns.gated_ffn_backward(dy, x, saved, *w))
+    ns.ops_sync()
