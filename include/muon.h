@@ -646,8 +646,8 @@ MUON_API int muon_gated_ffn_grad(const muon_gated_ffn_grad_args* args, void* wor
  * or 64-bit (positions_64), in device memory; NULL: 0, 1, ... seq - 1.  offset
  * is added to each, modulo 2^64.  turns: host memory, read during the call: every pair's
  * frequency in turns per position times 2^64 (muon_rotary_frequencies), so
- * that position * turns modulo 2^64 is the angle without whole turns: good to
- * 2^-53 of itself, whole turns included, and to 2^-64 turns a position.
+ * that position * turns modulo 2^64 is the angle without whole turns, good to
+ * what turns is: 2^-50 of the whole angle and 2^-64 turns a position.
  * 0 <= batch * seq < 2^31, 1 <= pairs <= 256, 2 * pairs <= head <= 65536, 0 <=
  * heads <= 65536 each, a position's values of both at most 2^28. */
 #define MUON_ROTARY_HALF 0

@@ -29,15 +29,18 @@
 // expert's last token, warp 12 finds the tiles.  Two accumulators, so that a tile is
 // written out while the next one's products run.  Pairs walk the tiles in turn.
 //
-// What bounds it.  Long sums: the tensor cores, at the rate that the power
-// limit leaves the library's product too (8192 tokens of 4096 x 11008: forward
-// 1245 us, 1.78 PFLOP/s; DX 846 us, 1.75; DW, both of whose operands have k as
-// rows, 1343 us, 1.65; DHIDDEN 496 us, 1.49, whose write-out reads two
-// and writes three values a sum).  128 experts of 2048 x 768 over 65536 rows:
-// forward 426 us and DX 290, the loads of tiles that are not full and the ends of
-// tiles of 12 to 32 steps; DHIDDEN 214, memory (5.5 TB/s); DW 510, tiles of
-// eight steps whose 1.2 GB of results leave meanwhile (442 us without storing
-// them).  Three teams that write out instead of two made no difference.
+// What bounds it (times in loops of 10 to 30 ms, over several boxes).  Long sums: the tensor
+// cores, at the rate that the power limit leaves the library's product too (8192
+// tokens of 4096 x 11008: forward 1219 to 1249 us, 1.79 PFLOP/s; DX 824 to 851,
+// 1.76; DW, both of whose operands have k as rows, 1278 to 1369, 1.68; DHIDDEN
+// 496 to 504, 1.48, whose write-out reads two and writes three values a sum).
+// 128 experts of 2048 x 768 over 65536 rows: forward 411 to 435 us and DX 287 to
+// 315, the loads of tiles that are not full and the ends of tiles of 12 to 32
+// steps; DHIDDEN 203 to 215, memory (5.6 TB/s); DW 491 to 533, tiles of eight
+// steps whose 1.2 GB of results leave meanwhile (442 us without storing them, where
+// it took 510).  In longer loops the power limit brings the clocks from 1.9 to 1.48
+// GHz, and that forward takes 480 to 495.  Three teams that write out instead of
+// two made no difference.
 //
 // Every wait is bounded; one that runs out raises g_ffn_err (muon_ops_sync).
 #include <algorithm>
@@ -453,8 +456,9 @@ __device__ __forceinline__ void team_sync(int team) {
     asm volatile("bar.sync %0, 128;" ::"r"(1 + team) : "memory");
 }
 
-// 1 / (1 + e^-v).  The exponential and the reciprocal are good to a few 2^-23,
-// a thousandth of the bf16 rounding behind them.  (With a reciprocal rounded
+// 1 / (1 + e^-v).  The exponential is off by 2 + 1.2 |v| units of 2^-23 and the
+// quotient by 2: 3e-6 at -20, where the bf16 rounding behind them is 4e-3; below
+// -87 it is 0.  (With a reciprocal rounded
 // to nearest, UP's write-out took 1550 cycles for 16 columns, not 600.)
 __device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 

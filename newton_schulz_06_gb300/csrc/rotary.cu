@@ -5,8 +5,10 @@
 //
 // Angles.  A pair's frequency is a 64-bit fraction of a turn per position, so
 // that position * frequency modulo 2^64 is the angle with whole turns already
-// gone: exact for every position, where the product in fp32 is off by 0.06
-// radians at a million.  No table of cosines is read: a block makes them for
+// gone, and the product is not rounded (in fp32 it is off by 0.06 radians at
+// position 10^6).  What is left is the frequency's own error, made in 64-bit
+// floating point: 2^-50 of the whole angle at most, 2e-6 radians at position
+// 2^31.  No table of cosines is read: a block makes them for
 // its tokens once, in shared memory, and all heads use them.
 //
 // What bounds it is memory: each value is read and written once (16384 tokens
