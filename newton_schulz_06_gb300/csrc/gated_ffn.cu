@@ -617,7 +617,8 @@ __device__ __forceinline__ void finish8(const FfnLaunch& p, int e, int j, int ro
         activate8(p.act, g, a, d);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            d[q] *= v[q] * w[q];
+            // (dh u may be past the largest number where act'(g) is 0)
+            d[q] = d[q] * w[q] * v[q];
             v[q] *= a[q];
             a[q] *= w[q];
         }

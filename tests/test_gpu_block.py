@@ -991,3 +991,20 @@ def test_gated_ffn_long_sums_between_the_products(ns, tokens, hidden, inner):
     check_forward(x, w, y, saved)
     check_backward(dy, x, saved, w, ns.gated_ffn_backward(dy, x, saved, *w))
     ns.ops_sync()
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+def test_gated_ffn_closed_gates_stay_closed(ns, name):
+    """Where act'(g) is 0, dg is 0 however large dh and u are; where it is 1, dg is
+    dh u.  (dh and du come through matrices of 0 and 1.)"""
+    hidden = inner = 64
+    gates = torch.tensor([-200.0, -200.0, 200.0, 200.0], device=DEV).to(BF)[:, None].expand(-1, inner).contiguous()
+    up = torch.tensor([1e20, -1e30, 1e10, 1e-20], device=DEV).to(BF)[:, None].expand(-1, inner).contiguous()
+    dy = torch.tensor([1e20, 1e30, 1e20, 1e20], device=DEV).to(BF)[:, None].expand(-1, hidden).contiguous()
+    eye = torch.eye(hidden, dtype=BF, device=DEV)
+    none = torch.zeros(inner, hidden, dtype=BF, device=DEV)
+    dx = ns.gated_ffn_backward(dy, None, (gates, up), eye, none, eye, activation=name)[0].to(D)
+    assert not dx[:2].any()
+    # dh is exact, dg and dx are rounded
+    want = dy[2:].to(D) * up[2:].to(D)
+    near(dx[2:], want, 2.1 * HALF[BF] * want, "dx")
