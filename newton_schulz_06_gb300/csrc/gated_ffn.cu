@@ -590,6 +590,11 @@ struct Units {
 };
 
 // Eight neighbours of an output row: v are their sums (UP: g's, and w u's).
+// What leaves is rounded once, from fp32, to bf16: h, dg, du and h again, because
+// the next product reads bf16 (a pass from given operands is then off by 2.3e-3 of
+// its norm, 1.7e-3 of which is its own result's rounding); g and u, because they
+// are what a block keeps for its backward pass, whose gradients are then off by
+// 3.5e-3. In fp32 they would take twice the memory and DHIDDEN's reads.
 // valid, start: as put8 has them; left: of the eight that are there.  All lanes
 // of a warp call this; WHOLE: all eight are there, on 16 bytes.
 template <int OP, bool WHOLE>
