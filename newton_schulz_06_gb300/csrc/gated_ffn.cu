@@ -26,13 +26,13 @@
 // Roles in a CTA: warps 0 and 11 load (TMA), warp 1 issues the products (the
 // pair's leader only), warps 2-9 are the epilogue, in two teams of four that
 // take a tile's columns in turn, warp 10 lays zeros over what DW loads past an
-// expert's last token, warp 12 finds the tiles.  Two accumulators, so that a tile is
-// written out while the next one's products run.  Pairs walk the tiles in turn.
+// expert's last token, warp 12 finds the tiles.  Two accumulators, so that a tile
+// is written out while the next one's products run.  Pairs walk the tiles in turn.
 //
-// What bounds it (times in loops of 10 to 30 ms, over several boxes).  Long sums: the tensor
-// cores, at the rate that the power limit leaves the library's product too (8192
-// tokens of 4096 x 11008: forward 1219 to 1249 us, 1.79 PFLOP/s; DX 824 to 851,
-// 1.76; DW, both of whose operands have k as rows, 1278 to 1369, 1.68; DHIDDEN
+// What bounds it (times in loops of 10 to 30 ms, over several boxes).  Long sums:
+// the tensor cores, at the rate that the power limit leaves the library's product
+// too (8192 tokens of 4096 x 11008: forward 1219 to 1249 us, 1.79 PFLOP/s; DX 824 to
+// 851, 1.76; DW, both of whose operands have k as rows, 1278 to 1369, 1.68; DHIDDEN
 // 496 to 504, 1.48, whose write-out reads two and writes three values a sum).
 // 128 experts of 2048 x 768 over 65536 rows: forward 411 to 435 us and DX 287 to
 // 315, the loads of tiles that are not full and the ends of tiles of 12 to 32
@@ -458,8 +458,8 @@ __device__ __forceinline__ void team_sync(int team) {
 
 // 1 / (1 + e^-v).  The exponential is off by 2 + 1.2 |v| units of 2^-23 and the
 // quotient by 2: 3e-6 at -20, where the bf16 rounding behind them is 4e-3; below
-// -87 it is 0.  (With a reciprocal rounded
-// to nearest, UP's write-out took 1550 cycles for 16 columns, not 600.)
+// -87 it is 0.  (With a reciprocal rounded to nearest, UP's write-out took 1550
+// cycles for 16 columns, not 600.)
 __device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
 // Phi(g) = erfc(-g / sqrt(2)) / 2, where e is exp(-g^2 / 2).  With z = |g| / sqrt(2),
@@ -594,7 +594,7 @@ struct Units {
 // the next product reads bf16 (a pass from given operands is then off by 2.3e-3 of
 // its norm, 1.7e-3 of which is its own result's rounding); g and u, because they
 // are what a block keeps for its backward pass, whose gradients are then off by
-// 3.5e-3. In fp32 they would take twice the memory and DHIDDEN's reads.
+// 3.5e-3.  In fp32 they would take twice the memory and DHIDDEN's reads.
 // valid, start: as put8 has them; left: of the eight that are there.  All lanes
 // of a warp call this; WHOLE: all eight are there, on 16 bytes.
 template <int OP, bool WHOLE>

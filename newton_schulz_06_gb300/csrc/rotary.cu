@@ -8,8 +8,8 @@
 // gone, and the product is not rounded (in fp32 it is off by 0.06 radians at
 // position 10^6).  What is left is the frequency's own error, made in 64-bit
 // floating point: 2^-50 of the whole angle at most, 2e-6 radians at position
-// 2^31.  No table of cosines is read: a block makes them for
-// its tokens once, in shared memory, and all heads use them.
+// 2^31.  No table of cosines is read: a block makes them for its tokens once, in
+// shared memory, and all heads use them.
 //
 // What bounds it is memory: each value is read and written once (16384 tokens
 // of 36 heads of 128 in bf16: 49 us, 6.1 TB/s; 8191 of 65 heads, of which 64 of 192
