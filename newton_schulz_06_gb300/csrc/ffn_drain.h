@@ -30,19 +30,26 @@ constexpr uint32_t DRAIN_BOX = 64 * 64 * 2;      // bytes of a box: 64 rows of 1
 // What a loading thread has asked for, or (steps alone) a clearing warp.
 struct Asked {
     uint32_t steps;          // so many steps, from the first one on
-    uint32_t gaps;           // four bits a stage: the rows to clear of its last step (0: it is not torn)
     uint32_t two;            // a bit a stage: its last step has two boxes of B
-    uint32_t full, torn;     // a bit a stage: whole and torn steps it has had, modulo 2
+    uint32_t torn;           // a bit a stage: its last step is torn,
+    uint32_t gaps;           // and has so many rows to clear (four bits a stage)
+    uint32_t times;          // a bit a stage: torn steps it has had, modulo 2
 };
 
-// One more step, in this stage.
-MUON_HD void ask(Asked& a, uint32_t stage, uint32_t gap, bool two) {
-    const uint32_t bit = 1u << stage;
-    a.gaps = (a.gaps & ~(15u << 4 * stage)) | gap << 4 * stage;
-    a.two = two ? a.two | bit : a.two & ~bit;
-    if (gap) a.torn ^= bit;
-    else a.full ^= bit;
-    ++a.steps;
+// n more steps of a tile, the first of them in this stage; gap: the last one's
+// (0: it is not torn, or was not asked for).
+MUON_HD void ask(Asked& a, uint32_t n, uint32_t stage, uint32_t stages, bool two, uint32_t gap) {
+    uint32_t m = n < stages ? ((1u << n) - 1) << stage : ~0u;
+    m |= m >> stages;
+    a.two = two ? a.two | m : a.two & ~m;
+    a.torn &= ~m;
+    a.steps += n;
+    if (gap) {
+        const uint32_t last = (stage + n - 1) % stages;
+        a.torn |= 1u << last;
+        a.times ^= 1u << last;
+        a.gaps = (a.gaps & ~(15u << 4 * last)) | gap << 4 * last;
+    }
 }
 
 // Bytes that a step takes of a thread for A, for B, of a clearing warp.
@@ -54,17 +61,19 @@ MUON_HD uint32_t zero_bytes(uint32_t gap, bool two) { return gap * 128 * (two ? 
 // be in flight: a stage is loaded again when its products have run.
 struct Last {
     bool any, two;
-    uint32_t step, gap, full, torn;      // the parities of its phases
+    uint32_t step, gap, phase;           // the parity of its phase
 };
 MUON_HD Last last_of(const Asked* by, int n, uint32_t stage, uint32_t stages) {
-    Last l{false, false, 0, 0, 0, 0};
+    Last l{false, false, 0, 0, 0};
     for (int i = 0; i < n; ++i) {
         const Asked& a = by[i];
         if (a.steps <= stage) continue;
-        const uint32_t step = a.steps - 1 - (a.steps - 1 - stage) % stages;
+        const uint32_t before = (a.steps - 1 - stage) / stages, step = before * stages + stage;
         if (l.any && step <= l.step) continue;
-        l = {true, (a.two >> stage & 1) != 0, step, a.gaps >> 4 * stage & 15, (a.full >> stage & 1) ^ 1,
-             (a.torn >> stage & 1) ^ 1};
+        // of its stage's steps before, those of its kind
+        const uint32_t torn = a.times >> stage & 1;
+        if (a.torn >> stage & 1) l = {true, (a.two >> stage & 1) != 0, step, a.gaps >> 4 * stage & 15, torn ^ 1};
+        else l = {true, (a.two >> stage & 1) != 0, step, 0, (before ^ torn) & 1};
     }
     return l;
 }
@@ -96,7 +105,7 @@ MUON_HD Settle settled(Settle s, bool armed) {
 // leader's of the zeros (zeros: both CTAs').
 MUON_HD Settle settle_full(const Asked* by, uint32_t stage, uint32_t stages) {
     const Last l = last_of(by, 4, stage, stages);
-    Settle s{0, 0, l.full, false};
+    Settle s{0, 0, l.phase, false};
     bool armed = false;
     if (l.any && !l.gap)
         for (int i = 0; i < 4; ++i) add(s, by[i].steps > l.step, i == 0, i & 1 ? b_bytes(l.two) : a_bytes(), armed);
@@ -104,7 +113,7 @@ MUON_HD Settle settle_full(const Asked* by, uint32_t stage, uint32_t stages) {
 }
 MUON_HD Settle settle_torn(const Asked* by, uint32_t stage, uint32_t stages) {
     const Last l = last_of(by, 2, stage, stages);
-    Settle s{0, 0, l.torn, false};
+    Settle s{0, 0, l.phase, false};
     bool armed = false;
     if (l.any && l.gap)
         for (int i = 0; i < 2; ++i) add(s, by[i].steps > l.step, i == 0, i & 1 ? b_bytes(l.two) : a_bytes(), armed);
@@ -112,7 +121,7 @@ MUON_HD Settle settle_torn(const Asked* by, uint32_t stage, uint32_t stages) {
 }
 MUON_HD Settle settle_zeros(const Asked* by, const Asked* zeros, uint32_t stage, uint32_t stages) {
     const Last l = last_of(by, 4, stage, stages);
-    Settle s{0, 0, l.torn, false};
+    Settle s{0, 0, l.phase, false};
     bool armed = false;
     if (l.any && l.gap)
         for (int i = 0; i < 2; ++i) add(s, zeros[i].steps > l.step, i == 0, zero_bytes(l.gap, l.two), armed);

@@ -298,31 +298,6 @@ struct Tiles {
     }
 };
 
-// The tiles as one warp finds them for all others: finding a tile takes 500 to
-// 1200 cycles, in which a role that did it itself kept the tensor cores waiting
-// (of 5000 a tile that has eight steps).
-struct Feed {
-    const Item* items;
-    uint32_t full, empty;
-    uint32_t n = 0;
-    __device__ __forceinline__ Feed(const void* at, uint32_t bars)
-        : items(static_cast<const Item*>(at)), full(bars), empty(bars + 8 * F_ITEMS) {}
-    // The next tile, for a thread or a whole warp: false where the wait ran
-    // out.
-    template <bool WARP>
-    __device__ __forceinline__ bool next(Item& x, volatile int* abort_flag, uint64_t limit) {
-        const uint32_t slot = n % F_ITEMS;
-        bool got = wait_soon(full + 8 * slot, n / F_ITEMS & 1, abort_flag, &g_ffn_err, limit);
-        if (WARP) got = __all_sync(0xffffffffu, got);
-        if (!got) return false;
-        x = items[slot];
-        if (WARP) __syncwarp();
-        if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * slot);
-        ++n;
-        return true;
-    }
-};
-
 __device__ __forceinline__ void load_box(uint32_t dst, const void* tmap, uint32_t cluster_bar, int x, int y,
                                          int z) {
     asm volatile(
@@ -414,6 +389,45 @@ __device__ __forceinline__ void store_turned(uint32_t to, const uint32_t (&r)[4]
                  "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
+// A wait that has gone on for a while.  Where it runs out, the other CTA of the
+// pair learns of it, too.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
+    if (wait_bounded(bar, parity, abort_flag, &g_ffn_err, limit)) return true;
+    store_cluster(map_to_rank(smem_u32(const_cast<int*>(abort_flag)), cluster_rank() ^ 1), 1u);
+    return false;
+}
+// As wait_soon, in a pair.
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return wait_long(bar, parity, abort_flag, limit);
+}
+// The tiles as one warp finds them for all others: finding a tile takes 500 to
+// 1200 cycles, in which a role that did it itself kept the tensor cores waiting
+// (of 5000 a tile that has eight steps).
+struct Feed {
+    const Item* items;
+    uint32_t full, empty;
+    uint32_t n = 0;
+    __device__ __forceinline__ Feed(const void* at, uint32_t bars)
+        : items(static_cast<const Item*>(at)), full(bars), empty(bars + 8 * F_ITEMS) {}
+    // The next tile, for a thread or a whole warp: false where the wait ran
+    // out.
+    template <bool WARP>
+    __device__ __forceinline__ bool next(Item& x, volatile int* abort_flag, uint64_t limit) {
+        const uint32_t slot = n % F_ITEMS;
+        bool got = wait_pair(full + 8 * slot, n / F_ITEMS & 1, abort_flag, limit);
+        if (WARP) got = __all_sync(0xffffffffu, got);
+        if (!got) return false;
+        x = items[slot];
+        if (WARP) __syncwarp();
+        if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * slot);
+        ++n;
+        return true;
+    }
+};
+
 // Whether a barrier's phase is over, without waiting.  Asked of the next step's
 // barrier before this step's work is issued, the answer's 220 cycles are hidden
 // behind it (the products' thread took 590 cycles a step otherwise, of 512 that
@@ -434,7 +448,7 @@ __device__ __forceinline__ bool is_over_warp(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, is_over(bar, parity));
 }
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
-    return __all_sync(0xffffffffu, wait_soon(bar, parity, abort_flag, &g_ffn_err, limit));
+    return __all_sync(0xffffffffu, wait_pair(bar, parity, abort_flag, limit));
 }
 // One lane of a whole warp.
 __device__ __forceinline__ bool elected() {
@@ -753,6 +767,7 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
         const int m0 = x.m0 + static_cast<int>(rank) * (OP == UP ? 64 : 128);
         const int n0 = x.n0 + static_cast<int>(rank) * (x.n / 2);
         int s = x.s0;
+        const uint32_t first = slot;
         const int stop = x.s0 + x.steps, half = (p.k + F_K - 1) / F_K;
         // DX has two sums' worth of steps, of one operand pair each
 #pragma unroll 1
@@ -765,21 +780,19 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
             int k0 = OP == DW ? x.t0 : (OP == DX ? s - part * half : s) * F_K;
 #pragma unroll 1
             for (; s < end; ++s, k0 += F_K) {
-                if (!free_next && !wait_soon(empty + 8 * slot, parity, abort_flag, &g_ffn_err, p.wait_limit_ns)) {
+                if (!free_next && !wait_pair(empty + 8 * slot, parity, abort_flag, p.wait_limit_ns)) {
                     ok = false;
                     break;
                 }
                 const uint32_t ahead = slot + 1 == STAGES ? 0 : slot + 1;
                 free_next = is_over(empty + 8 * ahead, ahead ? parity : parity ^ 1);
                 uint32_t bar = full_leader + 8 * slot;
-                const uint32_t gap = OP == DW && s == stop - 1 ? x.gap() : 0;
-                if (OP == DW && gap) {
+                if (OP == DW && s == stop - 1 && x.gap()) {
                     if (A) mbar_expect_tx(torn + 8 * slot, bytes);
                     bar = torn_own + 8 * slot;
                 } else {
                     if (A && rank == 0) mbar_expect_tx(full + 8 * slot, 2 * bytes);
                 }
-                ask(asked, slot, gap, boxes > 1);
                 const uint32_t to = stage0 + slot * F_STAGE_BYTES;
                 if constexpr (A) {
                     if constexpr (OP == UP) {
@@ -811,6 +824,7 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
                 }
             }
         }
+        ask(asked, s - x.s0, first, STAGES, boxes > 1, OP == DW && ok ? x.gap() : 0);
     }
     reinterpret_cast<Asked*>(smem + Space<OP>::ASKED)[A ? 0 : 1] = asked;
 }
@@ -819,13 +833,14 @@ __device__ __forceinline__ void load_operand(const FfnLaunch& p, Feed feed, uint
 // which has given up still has in flight: this CTA's of torn steps, and, where
 // the leader does it, what else both CTAs asked for.  No thread asks for more.
 template <int OP>
-__device__ __forceinline__ void drain_loads(uint8_t* smem, uint32_t rank, uint64_t limit) {
+__device__ void drain_loads(uint8_t* smem, uint32_t rank, uint64_t limit) {
     constexpr int STAGES = Space<OP>::STAGES;
     const uint32_t full = smem_u32(smem + Space<OP>::BARS), torn = full + 16 * STAGES, zero = torn + 8 * STAGES;
+    // both CTAs' counts, this one's first, where the write-out has ended
     const uint32_t own = smem_u32(smem + Space<OP>::ASKED);
-    Asked by[4], zeros[2];
+    Asked* const by = reinterpret_cast<Asked*>(smem + Space<OP>::TURN);
+    Asked* const zeros = by + 4;
     for (uint32_t r = 0; r < 2; ++r) {
-        // (this CTA's first)
         const uint32_t from = map_to_rank(own, rank ^ r);
         read_cluster(&by[2 * r], from, 2 * sizeof(Asked));
         read_cluster(&zeros[r], from + 2 * sizeof(Asked), sizeof(Asked));
@@ -846,6 +861,22 @@ __device__ __forceinline__ void drain_loads(uint8_t* smem, uint32_t rank, uint64
         if (!ends(full + 8 * i, settle_full(by, i, STAGES))) return;
         if (OP == DW && !ends(zero + 8 * i, settle_zeros(by, zeros, i, STAGES))) return;
     }
+}
+
+// What warps 0 and 1 of a pair that has given up do between the CTAs' meeting and
+// their end: the others have left.  issued: this warp has issued products.  (Out of
+// line, as what a wait that runs out does: at the kernels' ends the same code cost
+// every launch 0.1 to 0.45 us.)
+template <int OP>
+__device__ __noinline__ void give_up(uint8_t* smem, uint32_t drain_bar, bool issued, uint32_t rank, uint64_t limit) {
+    if (threadIdx.x == 0) drain_loads<OP>(smem, rank, limit);
+    // (the lane that issued the products: elections of one mask agree)
+    if (issued && elected()) {
+        commit_pair_local(drain_bar);
+        wait_quiet(drain_bar, 0, limit);
+    }
+    __syncwarp();
+    cluster_sync_all();
 }
 
 template <int OP>
@@ -1078,8 +1109,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     x.chunk |= left ? 0 : LAST;
                 }
                 const uint32_t slot = n % F_ITEMS;
-                if (!wait_soon(smem_u32(&item_bar[F_ITEMS + slot]), (n / F_ITEMS & 1) ^ 1, abort_flag, &g_ffn_err,
-                               limit))
+                if (!wait_pair(smem_u32(&item_bar[F_ITEMS + slot]), (n / F_ITEMS & 1) ^ 1, abort_flag, limit))
                     break;
                 items[slot] = x;
                 mbar_arrive(smem_u32(&item_bar[slot]));
@@ -1154,7 +1184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 if (OP == DW && !(x.chunk & FIRST)) held.fetch(p, team, tid);
                 if (x.steps) {
                     const uint32_t use = acc ? uses[1]++ : uses[0]++;
-                    got = wait_soon(smem_u32(&tfull_bar[acc]), use & 1, abort_flag, &g_ffn_err, limit);
+                    got = wait_pair(smem_u32(&tfull_bar[acc]), use & 1, abort_flag, limit);
                 }
             }
             // the team's barriers need all four warps: a wait that ran out for
@@ -1281,22 +1311,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         if (OP == DHIDDEN) copies_done();
     }
 
-    // A wait that ran out in one CTA is known to both before they meet, whatever
-    // of the pair had done its work by then.
-    if (*abort_flag) store_cluster(map_to_rank(smem_u32(tmem_slot + 1), rank ^ 1), 1u);
-    __syncwarp();
     tc_fence_before();
     cluster_sync_all();      // no CTA leaves while its pair may still touch it
-    if (*abort_flag) {
-        if (threadIdx.x == 0) drain_loads<OP>(smem, rank, limit);
-        // (the lane that issued the products: elections of one mask agree)
-        if (warp == 1 && any && elected()) {
-            commit_pair_local(smem_u32(drain_bar));
-            wait_quiet(smem_u32(drain_bar), 0, limit);
-        }
-        __syncwarp();
-        cluster_sync_all();
-    }
+    if (warp > 1) return;
+    // (a wait that ran out in one CTA is known to both by now, whatever of the
+    // pair had done its work before)
+    if (*abort_flag) give_up<OP>(smem, smem_u32(drain_bar), any, rank, limit);
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),

@@ -46,7 +46,7 @@ constexpr int STEPS = 60;
 
 struct Step {
     uint32_t gap;
-    bool two;
+    bool two, ends;          // its tile
 };
 struct Load {
     Bar* bar;
@@ -57,12 +57,21 @@ struct Load {
 int plays(std::mt19937& rng, int rule) {
     const uint32_t stages = 5 + rng() % 2;
     std::vector<Step> steps(STEPS);
-    for (Step& s : steps) s = {rng() % 3 == 0 ? uint32_t(rng() % 16) : 0u, rng() % 3 != 0};
+    for (int i = 0; i < STEPS;) {
+        // tiles of one width, of which the last step may be torn
+        const int n = 1 + int(rng() % (rng() % 3 ? 4 : 20));
+        const bool two = rng() % 3 != 0;
+        for (int k = 0; k < n && i < STEPS; ++k, ++i) {
+            const bool ends = k == n - 1 || i == STEPS - 1;
+            steps[i] = {ends && rng() % 2 ? uint32_t(rng() % 16) : 0u, two, ends};
+        }
+    }
     std::vector<Bar> full(stages), zero(stages), torn[2];
     torn[0].resize(stages);
     torn[1].resize(stages);
     std::vector<Load> flying;
     Asked by[4] = {}, zeros[2] = {};     // A and B of the leader, of the other CTA
+    uint32_t done[4] = {};               // steps of the tile that a thread is in
     uint32_t products = 0;
     const uint32_t moves = rng() % 700, lazy = rng() % 7;
     // (the parity of a step's phase goes by the steps of its kind that its stage had)
@@ -83,7 +92,7 @@ int plays(std::mt19937& rng, int rule) {
         if (what == lazy && rng() % 8) continue;
         if (what < 4) {
             Asked& me = by[what];
-            const uint32_t i = me.steps, stage = i % stages, rank = what / 2;
+            const uint32_t i = me.steps + done[what], stage = i % stages, rank = what / 2;
             if (i >= STEPS || (i >= stages && products < i - stages + 1)) continue;
             const Step& s = steps[i];
             Bar& bar = s.gap ? torn[rank][stage] : full[stage];
@@ -91,14 +100,19 @@ int plays(std::mt19937& rng, int rule) {
             if (s.gap && what % 2 == 0) bar.arm(cta);
             if (!s.gap && what == 0) bar.arm(2 * cta);
             parts(bar, what % 2 ? b_bytes(s.two) : a_bytes());
-            ask(me, stage, s.gap, s.two);
+            ++done[what];
+            if (s.ends) {
+                ask(me, done[what], me.steps % stages, stages, s.two, s.gap);
+                done[what] = 0;
+            }
         } else if (what < 6) {
             const uint32_t rank = what - 4, i = zeros[rank].steps, stage = i % stages;
             if (i >= STEPS) continue;
             const Step& s = steps[i];
             // (the warp goes from torn step to torn step)
             if (s.gap) {
-                if (by[2 * rank].steps <= i || by[2 * rank + 1].steps <= i || !torn[rank][stage].over(parity(i)))
+                const uint32_t a = 2 * rank, b = a + 1;
+                if (by[a].steps + done[a] <= i || by[b].steps + done[b] <= i || !torn[rank][stage].over(parity(i)))
                     continue;
                 if (rank == 0) zero[stage].arm(2 * int64_t(zero_bytes(s.gap, s.two)));
                 parts(zero[stage], zero_bytes(s.gap, s.two));
@@ -114,7 +128,9 @@ int plays(std::mt19937& rng, int rule) {
             if ((steps[products].gap ? zero : full)[stage].over(parity(products))) ++products;
         }
     }
-    // The pair gives up here.
+    // The pair gives up here, some threads within a tile.
+    for (int k = 0; k < 4; ++k)
+        if (done[k]) ask(by[k], done[k], by[k].steps % stages, stages, steps[by[k].steps].two, 0);
     struct Wait {
         Bar* bar;
         uint32_t parity;
@@ -124,9 +140,10 @@ int plays(std::mt19937& rng, int rule) {
         if (rule == 0) {
             for (int rank = 0; rank < 2; ++rank) {
                 const Asked& a = by[2 * rank];
-                if (a.steps <= s) continue;
-                if (a.gaps >> 4 * s & 15) waits.push_back({&torn[rank][s], (a.torn >> s & 1) ^ 1});
-                else if (rank == 0) waits.push_back({&full[s], (a.full >> s & 1) ^ 1});
+                const Last l = last_of(&a, 1, s, stages);
+                if (!l.any) continue;
+                if (l.gap) waits.push_back({&torn[rank][s], l.phase});
+                else if (rank == 0) waits.push_back({&full[s], l.phase});
             }
             continue;
         }

@@ -39,12 +39,17 @@ def test_the_pair_drains_after_all_roles_have_ended():
     """Behind the barrier at which both CTAs meet, whichever of them and
     whatever role gave up; and neither leaves before the other has drained."""
     text = open(os.path.join(CSRC, "gated_ffn.cu")).read()
-    end = text[text.index("if (*abort_flag) store_cluster("):]
+    end = text[text.index("        if (OP == DHIDDEN) copies_done();"):]
     end = end[:end.index("tcgen05.dealloc")]
-    first = end.index("cluster_sync_all()")
-    assert first < end.index("drain_loads<OP>(") < end.rindex("cluster_sync_all()")
-    assert first < end.index("commit_pair_local(") < end.rindex("cluster_sync_all()")
-    assert end.count("cluster_sync_all()") == 2
+    assert end.index("cluster_sync_all()") < end.index("if (*abort_flag) give_up<OP>(") and end.count("return;") == 1
+    last = text[text.index("void give_up("):]
+    last = last[:last.index("\n}\n")]
+    assert max(last.index("drain_loads<OP>("), last.index("commit_pair_local(")) < last.index("cluster_sync_all()")
+    # whichever wait runs out, the other CTA learns of it before it meets this one
+    body = text[text.index("bool wait_long("):]
+    body = body[:body.index("\n}\n")]
+    assert body.index("wait_bounded(") < body.index("store_cluster(")
+    assert text.count("wait_bounded(") == 1 and text.count("wait_soon(") == 1       # that of the timeout test
     # each loading thread leaves its counts, whatever ended its loop
     body = text[text.index("load_operand(const FfnLaunch& p"):text.index("drain_loads(uint8_t*")]
     assert "return" not in body and body.index("= asked;") > body.rindex("load_box(")
