@@ -168,12 +168,14 @@ struct Named {
         : name(what), area(p, cols * (dtype == MUON_F32 ? 4 : 2)) {
         const int size = dtype == MUON_F32 ? 4 : 2;
         area.axis(rows, ld * size).axis(matrices, stride * size);
+        end = area.p + area.span();
         there = p && rows > 0;
     }
+    __int128 end;
     bool there;
 };
 int check_apart(const Err& err, const Named& a, const Named& b) {
-    if (a.there && b.there && ops::share(a.area, b.area))
+    if (a.there && b.there && a.area.p < b.end && b.area.p < a.end && ops::share(a.area, b.area))
         return err.fail(MUON_ERR_INVALID_ARG, "%s and %s share memory", a.name, b.name);
     return MUON_OK;
 }
